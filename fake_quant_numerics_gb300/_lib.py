@@ -30,6 +30,8 @@ F32, BF16 = 0, 1
 SYMMETRIC, AFFINE = 0, 1
 PER_TENSOR, PER_ROW, PER_GROUP, PER_COLUMN = 0, 1, 2, 3
 E4M3, E5M2 = 0, 1
+W4_DOUBLE = 16
+SILU, GELU, RELU = 0, 1, 2
 
 _lib = None
 
@@ -49,6 +51,15 @@ class CalibOptions(ctypes.Structure):
     """qat_calib_options (include/qat.h)."""
     _fields_ = [("clip", ctypes.c_float), ("scale_fp16", ctypes.c_int)]
 
+
+class Weight4Struct(ctypes.Structure):
+    """qat_weight4 (include/qat.h)."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("zero_points", ctypes.c_void_p), ("super_scales", ctypes.c_void_p),
+                ("rows", _i64), ("cols", _i64), ("group", _i64), ("layout", _int)]
+
+
+_w4 = ctypes.POINTER(Weight4Struct)
 
 PROTOTYPES = {
     "qat_status_string": ([_int], ctypes.c_char_p),
@@ -74,6 +85,17 @@ PROTOTYPES = {
     "qat_ste_backward": ([_vp, _int, _i64, _vp, _vp, _vp], _int),
     "qat_quant4_double": ([_vp, _i64, _vp, _vp, _vp, _vp, _vp], _int),
     "qat_dequant4_double": ([_vp, _vp, _vp, _i64, _vp, _vp], _int),
+    "qat_linear4": ([_vp, _int, _i64, _w4, _vp, _int, _vp], _int),
+    "qat_gated4": ([_vp, _int, _i64, _w4, _w4, _int, _vp, _vp], _int),
+    "qat_gated_ffn_workspace_bytes": ([_int, _i64, _i64, _i64, _int], _sz),
+    "qat_gated_ffn": ([_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp, _vp,
+                       _sz, _vp], _int),
+    "qat_gated_ffn_backward": ([_vp, _vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _int, _vp, _vp,
+                                _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _int),
+    "qat_layer_norm": ([_vp, _int, _i64, _i64, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp], _int),
+    "qat_layer_norm_backward_workspace_bytes": ([_i64, _i64], _sz),
+    "qat_layer_norm_backward": ([_vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                 _sz, _vp], _int),
     "qat_kernel_launch_count": ([], ctypes.c_uint64),
     "qat_debug_set_wait_limit": ([_i64], None),
 }

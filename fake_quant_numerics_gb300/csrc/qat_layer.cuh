@@ -1,0 +1,48 @@
+// qat_layer.cuh -- device helpers shared by the layer operators' kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "qat_device.cuh"
+
+namespace qat {
+
+template <typename T>
+__device__ __forceinline__ float ld_elem(const void* p, int64_t i) {
+  return __uint_as_float(load_elem_bits<T>(p, i));
+}
+
+template <typename T>
+__device__ __forceinline__ void st_elem(void* p, int64_t i, float v);
+template <>
+__device__ __forceinline__ void st_elem<F32>(void* p, int64_t i, float v) {
+  static_cast<float*>(p)[i] = v;
+}
+template <>
+__device__ __forceinline__ void st_elem<BF16>(void* p, int64_t i, float v) {
+  static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// act(g) and act'(g): silu (0), gelu in the erf form (1), relu (2).  A NaN
+// stays NaN; relu'(0) = 0.
+__device__ __forceinline__ void act_grad(int act, float g, float& a, float& da) {
+  if (act == QAT_ACT_SILU) {
+    const float s = __frcp_rn(1.0f + expf(-g));
+    a = g * s;
+    da = s * fmaf(g, 1.0f - s, 1.0f);
+  } else if (act == QAT_ACT_GELU) {
+    const float phi = 0.5f * erfcf(g * -0.70710678118654752f);  // keeps the tail's digits
+    a = g * phi;
+    da = fmaf(g * 0.39894228040143268f, expf(-0.5f * g * g), phi);
+  } else {
+    a = g > 0.0f ? g : (g != g ? g : 0.0f);
+    da = g > 0.0f ? 1.0f : 0.0f;
+  }
+}
+__device__ __forceinline__ float act_value(int act, float g) {
+  float a, da;
+  act_grad(act, g, a, da);
+  return a;
+}
+
+}  // namespace qat

@@ -1,0 +1,332 @@
+"""Layer operators on quantized weights (include/qat.h, "Layer operators").
+
+Products of a few tokens with the 4-bit codes the library writes
+(:func:`linear4`), the gated feed-forward block with its backward pass
+(:func:`gated_ffn`, :func:`gated_ffn_backward`) and from 4-bit codes
+(:func:`gated_ffn4`), and layer norm with its backward pass
+(:func:`layer_norm`, :func:`layer_norm_backward`).  The ``qat_*`` functions
+mirror the C ABI; the named ones check shapes, allocate the outputs with torch
+and run on the current stream.  Every step of the computation runs in the
+library's kernels.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import _lib
+from ._lib import (GELU, PER_COLUMN, PER_GROUP, PER_ROW, PER_TENSOR, RELU, SILU, W4_DOUBLE, QatError)
+from .api import _GRAN, _dt, _nbytes, _p, _ready, _s, DoubleQuantized4Bit
+
+_ACT = {"silu": SILU, "gelu": GELU, "relu": RELU, SILU: SILU, GELU: GELU, RELU: RELU}
+
+
+def _mismatch(what: str) -> QatError:
+    return QatError(what, _lib.QAT_ERR_DIMENSION_MISMATCH)
+
+
+def _flat(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    return None if t is None else t.contiguous()
+
+
+def _of_type(like: torch.Tensor, *tensors: Optional[torch.Tensor]):
+    """Every tensor has like's dtype and device."""
+    for t in tensors:
+        if t is None:
+            continue
+        if t.dtype != like.dtype:
+            raise TypeError(f"{t.dtype} beside {like.dtype}: the call's tensors share one dtype")
+        if t.device != like.device:
+            raise ValueError(f"tensors on {t.device} and {like.device}")
+
+
+# ---------------------------------------------------------------------------
+# products with 4-bit weights
+# ---------------------------------------------------------------------------
+class Weight4(NamedTuple):
+    """A [rows, cols] weight as packed 4-bit codes (see :func:`weight4`)."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+    zero_point: Optional[torch.Tensor]
+    super_scales: Optional[torch.Tensor]
+    rows: int
+    cols: int
+    layout: int
+    group: int
+
+    def struct(self) -> "_lib.Weight4Struct":
+        """qat_weight4; it holds addresses only, so keep this Weight4 alive."""
+        for t in (self.codes, self.scale, self.zero_point, self.super_scales):
+            if t is not None and not t.is_cuda:
+                raise ValueError("libqat takes CUDA tensors only")
+        return _lib.Weight4Struct(
+            self.codes.data_ptr(), self.scale.data_ptr(),
+            None if self.zero_point is None else self.zero_point.data_ptr(),
+            None if self.super_scales is None else self.super_scales.data_ptr(),
+            self.rows, self.cols, self.group, self.layout)
+
+
+def weight4(codes: torch.Tensor, scale: torch.Tensor, rows: int, cols: int, granularity="group",
+            group: int = 128, zero_point: Optional[torch.Tensor] = None) -> Weight4:
+    """The [rows, cols] weight of fake_quant_int(bits=4)'s codes, scale and
+    zero_point (per tensor, row or group of the last dimension)."""
+    layout = _GRAN[granularity]
+    if layout == PER_COLUMN:
+        raise ValueError("4-bit products take scales per tensor, row or group")
+    if layout == PER_GROUP and (group <= 0 or cols % group):
+        raise ValueError(f"group {group} must divide the last dimension {cols}")
+    units = {PER_TENSOR: 1, PER_ROW: rows}.get(layout) if layout != PER_GROUP else rows * (cols // group)
+    if codes.dtype != torch.uint8 or scale.dtype != torch.float32:
+        raise TypeError("codes are uint8 (two per byte), scales float32")
+    if zero_point is not None and zero_point.dtype != torch.int32:
+        raise TypeError("zero points are int32")
+    if (codes.numel() != (rows * cols + 1) // 2 or scale.numel() != units
+            or (zero_point is not None and zero_point.numel() != units)):
+        raise _mismatch("weight4")
+    return Weight4(_ready(codes), scale.contiguous(), _flat(zero_point), None, rows, cols, layout,
+                   group if layout == PER_GROUP else 0)
+
+
+def weight4_double(dq: DoubleQuantized4Bit, rows: int, cols: int) -> Weight4:
+    """The [rows, cols] weight of quantize_4bit_double's result."""
+    if dq.len != rows * cols:
+        raise _mismatch("weight4_double")
+    return Weight4(_ready(dq.data), _ready(dq.quantized_scales), None, dq.super_scales.contiguous(),
+                   rows, cols, W4_DOUBLE, 0)
+
+
+def qat_linear4(x, tokens, w: Weight4, y, stream=None):
+    st = _lib.lib().qat_linear4(_p(x), _dt(x), tokens, w.struct(), _p(y), _dt(y), _s(stream))
+    _lib.check("qat_linear4", st)
+
+
+def qat_gated4(x, tokens, gate: Weight4, up: Weight4, act, h, stream=None):
+    st = _lib.lib().qat_gated4(_p(x), _dt(x), tokens, gate.struct(), up.struct(), _ACT[act], _p(h),
+                               _s(stream))
+    _lib.check("qat_gated4", st)
+
+
+def linear4(x: torch.Tensor, weight: Weight4) -> torch.Tensor:
+    """x [..., cols] times the weight's transpose: [..., rows] in x's dtype
+    (float32 or bfloat16).  For a few tokens (the weight is read once per 32)."""
+    if x.dim() == 0 or x.shape[-1] != weight.cols:
+        raise _mismatch("linear4")
+    x = x.contiguous()
+    lead = x.shape[:-1]
+    y = torch.empty(*lead, weight.rows, dtype=x.dtype, device=x.device)
+    qat_linear4(x, lead.numel(), weight, y)
+    return y
+
+
+def gated_ffn4(x: torch.Tensor, gate: Weight4, up: Weight4, down: Weight4,
+               activation="silu") -> torch.Tensor:
+    """The gated feed-forward block from 4-bit codes: (act(x gate^T) * (x up^T)) down^T,
+    the hidden values kept in float32."""
+    if x.dim() == 0 or x.shape[-1] != gate.cols or down.cols != gate.rows:
+        raise _mismatch("gated_ffn4")
+    x = x.contiguous()
+    lead = x.shape[:-1]
+    tokens = lead.numel()
+    h = torch.empty(tokens, gate.rows, dtype=torch.float32, device=x.device)
+    y = torch.empty(*lead, down.rows, dtype=x.dtype, device=x.device)
+    qat_gated4(x, tokens, gate, up, activation, h)
+    qat_linear4(h, tokens, down, y)
+    return y
+
+
+# ---------------------------------------------------------------------------
+# gated feed-forward block
+# ---------------------------------------------------------------------------
+class GatedFfn(NamedTuple):
+    y: torch.Tensor
+    h: torch.Tensor                    # act(g) * u, x's dtype
+    gate_pre: Optional[torch.Tensor]   # g, float32 (save=True)
+    up_pre: Optional[torch.Tensor]     # u, float32 (save=True)
+
+
+def qat_gated_ffn_workspace_bytes(dtype, tokens, dim, hidden, backward=False) -> int:
+    return int(_lib.lib().qat_gated_ffn_workspace_bytes(dtype, tokens, dim, hidden, int(backward)))
+
+
+def qat_gated_ffn(x, tokens, dim, hidden, w_gate, w_up, w_down, act, h, gate_pre, up_pre, y,
+                  workspace, stream=None):
+    st = _lib.lib().qat_gated_ffn(_p(x), _dt(x), tokens, dim, hidden, _p(w_gate), _p(w_up),
+                                  _p(w_down), _ACT[act], _p(h), _p(gate_pre), _p(up_pre), _p(y),
+                                  _p(workspace), _nbytes(workspace), _s(stream))
+    _lib.check("qat_gated_ffn", st)
+
+
+def qat_gated_ffn_backward(dy, x, tokens, dim, hidden, w_gate, w_up, w_down, act, h, gate_pre,
+                           up_pre, dx, dw_gate, dw_up, dw_down, workspace, stream=None):
+    st = _lib.lib().qat_gated_ffn_backward(
+        _p(dy), _p(x), _dt(x), tokens, dim, hidden, _p(w_gate), _p(w_up), _p(w_down), _ACT[act],
+        _p(h), _p(gate_pre), _p(up_pre), _p(dx), _p(dw_gate), _p(dw_up), _p(dw_down),
+        _p(workspace), _nbytes(workspace), _s(stream))
+    _lib.check("qat_gated_ffn_backward", st)
+
+
+def _ffn_sizes(what, x, w_gate, w_up, w_down):
+    if w_gate.dim() != 2 or x.dim() == 0:
+        raise _mismatch(what)
+    hidden, dim = w_gate.shape
+    if x.shape[-1] != dim or tuple(w_up.shape) != (hidden, dim) or tuple(w_down.shape) != (dim, hidden):
+        raise _mismatch(what)
+    _of_type(x, w_gate, w_up, w_down)
+    return x.shape[:-1].numel(), dim, hidden
+
+
+def _ffn_workspace(x, tokens, dim, hidden, backward):
+    n = qat_gated_ffn_workspace_bytes(_dt(x), tokens, dim, hidden, backward)
+    return torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+
+
+def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
+              activation="silu", save: bool = False) -> GatedFfn:
+    """y = (act(x w_gate^T) * (x w_up^T)) w_down^T for x [..., dim], w_gate and w_up
+    [hidden, dim], w_down [dim, hidden], one dtype (float32 or bfloat16).
+    save=True keeps the pre-activations for gated_ffn_backward."""
+    tokens, dim, hidden = _ffn_sizes("gated_ffn", x, w_gate, w_up, w_down)
+    x, w_gate, w_up, w_down = x.contiguous(), w_gate.contiguous(), w_up.contiguous(), w_down.contiguous()
+    h = torch.empty(tokens, hidden, dtype=x.dtype, device=x.device)
+    g = u = None
+    if save:
+        g = torch.empty(tokens, hidden, dtype=torch.float32, device=x.device)
+        u = torch.empty_like(g)
+    y = torch.empty_like(x)
+    qat_gated_ffn(x, tokens, dim, hidden, w_gate, w_up, w_down, activation, h, g, u, y,
+                  _ffn_workspace(x, tokens, dim, hidden, False))
+    return GatedFfn(y, h, g, u)
+
+
+def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                       w_down: torch.Tensor, saved: GatedFfn, activation="silu", want_dx: bool = True,
+                       want_dw: bool = True):
+    """(dx, dw_gate, dw_up, dw_down) of gated_ffn(..., save=True), in x's dtype; None
+    for what is not wanted."""
+    tokens, dim, hidden = _ffn_sizes("gated_ffn_backward", x, w_gate, w_up, w_down)
+    if saved.gate_pre is None or saved.up_pre is None:
+        raise ValueError("gated_ffn_backward needs the pre-activations of gated_ffn(save=True)")
+    if dy.shape != x.shape or any(tuple(t.shape) != (tokens, hidden)
+                                  for t in (saved.h, saved.gate_pre, saved.up_pre)):
+        raise _mismatch("gated_ffn_backward")
+    _of_type(x, dy, saved.h)
+    dy, x = dy.contiguous(), x.contiguous()
+    w_gate, w_up, w_down = w_gate.contiguous(), w_up.contiguous(), w_down.contiguous()
+    dx = torch.empty_like(x) if want_dx else None
+    dwg = dwu = dwd = None
+    if want_dw:
+        dwg, dwu, dwd = torch.empty_like(w_gate), torch.empty_like(w_up), torch.empty_like(w_down)
+    qat_gated_ffn_backward(dy, x, tokens, dim, hidden, w_gate, w_up, w_down, activation, saved.h,
+                           saved.gate_pre, saved.up_pre, dx, dwg, dwu, dwd,
+                           _ffn_workspace(x, tokens, dim, hidden, True))
+    return dx, dwg, dwu, dwd
+
+
+class GatedFfnFunction(torch.autograd.Function):
+    """gated_ffn with its backward pass."""
+
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, w_down, activation="silu"):
+        r = gated_ffn(x, w_gate, w_up, w_down, activation, save=True)
+        ctx.save_for_backward(x, w_gate, w_up, w_down, r.h, r.gate_pre, r.up_pre)
+        ctx.activation = activation
+        return r.y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, wg, wu, wd, h, g, u = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dg, du, dd = gated_ffn_backward(dy, x, wg, wu, wd, GatedFfn(None, h, g, u),
+                                            ctx.activation, want_dx=need[0], want_dw=any(need[1:4]))
+        return dx, dg, du, dd, None
+
+
+# ---------------------------------------------------------------------------
+# layer norm
+# ---------------------------------------------------------------------------
+class LayerNorm(NamedTuple):
+    y: torch.Tensor
+    mean: torch.Tensor   # float32, one per row
+    rstd: torch.Tensor
+
+
+def qat_layer_norm(x, rows, cols, weight, bias, eps, y, mean, rstd, stream=None):
+    st = _lib.lib().qat_layer_norm(_p(x), _dt(x), rows, cols, _p(weight), _p(bias), eps, _p(y),
+                                   _p(mean), _p(rstd), _s(stream))
+    _lib.check("qat_layer_norm", st)
+
+
+def qat_layer_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    return int(_lib.lib().qat_layer_norm_backward_workspace_bytes(rows, cols))
+
+
+def qat_layer_norm_backward(dy, x, rows, cols, weight, mean, rstd, dx, dweight, dbias, workspace,
+                            stream=None):
+    st = _lib.lib().qat_layer_norm_backward(_p(dy), _p(x), _dt(x), rows, cols, _p(weight), _p(mean),
+                                            _p(rstd), _p(dx), _p(dweight), _p(dbias), _p(workspace),
+                                            _nbytes(workspace), _s(stream))
+    _lib.check("qat_layer_norm_backward", st)
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+               bias: Optional[torch.Tensor] = None, eps: float = 1e-5) -> LayerNorm:
+    """Layer norm of x [..., cols] over its last dimension, with the rows' mean and
+    rstd (float32) for the backward pass."""
+    if x.dim() == 0:
+        raise _mismatch("layer_norm")
+    cols = x.shape[-1]
+    if any(t is not None and tuple(t.shape) != (cols,) for t in (weight, bias)):
+        raise _mismatch("layer_norm")
+    _of_type(x, weight, bias)
+    x, weight, bias = x.contiguous(), _flat(weight), _flat(bias)
+    lead = x.shape[:-1]
+    y = torch.empty_like(x)
+    mean = torch.empty(lead, dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
+    qat_layer_norm(x, lead.numel(), cols, weight, bias, eps, y, mean, rstd)
+    return LayerNorm(y, mean, rstd)
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor],
+                        mean: torch.Tensor, rstd: torch.Tensor, want_dx: bool = True,
+                        want_dw: bool = True):
+    """(dx, dweight, dbias) of layer_norm; None for what is not wanted."""
+    if x.dim() == 0 or dy.shape != x.shape:
+        raise _mismatch("layer_norm_backward")
+    cols, lead = x.shape[-1], x.shape[:-1]
+    rows = lead.numel()
+    if (weight is not None and tuple(weight.shape) != (cols,)) or mean.numel() != rows or rstd.numel() != rows:
+        raise _mismatch("layer_norm_backward")
+    _of_type(x, dy, weight)
+    if mean.dtype != torch.float32 or rstd.dtype != torch.float32:
+        raise TypeError("mean and rstd are float32")
+    dy, x, weight, mean, rstd = dy.contiguous(), x.contiguous(), _flat(weight), _flat(mean), _flat(rstd)
+    dx = torch.empty_like(x) if want_dx else None
+    dw = db = ws = None
+    if want_dw:
+        dw = torch.empty(cols, dtype=x.dtype, device=x.device)
+        db = torch.empty_like(dw)
+        n = qat_layer_norm_backward_workspace_bytes(rows, cols)
+        ws = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+    qat_layer_norm_backward(dy, x, rows, cols, weight, mean, rstd, dx, dw, db, ws)
+    return dx, dw, db
+
+
+class LayerNormFunction(torch.autograd.Function):
+    """layer_norm with its backward pass."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps=1e-5):
+        r = layer_norm(x, weight, bias, eps)
+        ctx.save_for_backward(x, weight, r.mean, r.rstd)
+        return r.y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dw, db = layer_norm_backward(dy, x, weight, mean, rstd, want_dx=need[0],
+                                         want_dw=need[1] or need[2])
+        return dx, dw if need[1] else None, db if need[2] else None, None

@@ -425,6 +425,127 @@ qat_status qat_fake_quant_fp8_noalloc(const void* x, qat_dtype dtype, int64_t n,
                                       void* y, uint8_t* codes, uint32_t* mask, int32_t* dev_flags,
                                       qat_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Layer operators: what a layer does with the weights the calls above
+ * quantize.  No counterpart on the source pages.  The conventions above hold
+ * (device pointers, stream order, caller-owned buffers and workspaces, no
+ * state between calls, synchronous errors) except that every tensor here is
+ * aligned to its element only: x, y, weights, gradients and their views may
+ * start anywhere a whole element does.  Sums, statistics and products are held
+ * in binary32; every output is rounded once to its type.
+ */
+
+/*
+ * A [rows, cols] weight held as packed 4-bit codes (the nibble order above,
+ * flat over rows * cols elements), read by the products below.
+ *   layout QAT_PER_TENSOR / QAT_PER_ROW / QAT_PER_GROUP: codes, float scales
+ *     and int32 zero points (NULL: symmetric) as qat_fake_quant_int writes
+ *     them; w = (q - zp) * scale.  A zero point outside [-8, 7] counts as the
+ *     nearer end.  `group` as in that call.
+ *   layout QAT_W4_DOUBLE: data, qscales and super_scales as
+ *     qat_quant4_double writes them for the flat weight; w = q * (qscale / 255
+ *     * super).  scales holds the uint8 qscales, zero_points is NULL.
+ * codes 16-byte aligned, the other arrays to their element.  rows * cols up
+ * to 2^50.
+ */
+#define QAT_W4_DOUBLE 16
+typedef struct {
+  const void* codes;
+  const void* scales;
+  const int32_t* zero_points;
+  const float* super_scales;
+  int64_t rows, cols, group;
+  int layout; /* qat_granularity (not QAT_PER_COLUMN) or QAT_W4_DOUBLE */
+} qat_weight4;
+
+typedef enum { QAT_ACT_SILU = 0, QAT_ACT_GELU = 1, QAT_ACT_RELU = 2 } qat_activation;
+
+/*
+ * y[t, n] = sum_k x[t, k] w[n, k] for a few tokens: x is x_dtype[tokens,
+ * cols], y y_dtype[tokens, rows].  Products of codes and x are summed in
+ * binary32 inside a unit, then scaled and summed over the units, so a scale
+ * that is not finite makes its outputs NaN whatever the codes.  Any number of
+ * tokens; the weight is read once per 32 of them.  tokens == 0 or rows == 0
+ * is a no-op; cols == 0 writes zeros.  QAT_ERR_INVALID_ARGUMENT: a NULL array,
+ * a negative size, a group that does not divide cols, zero points with
+ * QAT_W4_DOUBLE; QAT_ERR_UNSUPPORTED: an unknown dtype or layout;
+ * QAT_ERR_MISALIGNED.  One launch per 32 tokens.
+ */
+qat_status qat_linear4(const void* x, qat_dtype x_dtype, int64_t tokens, const qat_weight4* w,
+                       void* y, qat_dtype y_dtype, qat_stream_t stream);
+
+/*
+ * The first half of a gated feed-forward block from 4-bit codes:
+ * h[t, f] = act(sum_k x[t, k] gate[f, k]) * (sum_k x[t, k] up[f, k]), h
+ * float[tokens, rows], both products, the activation and the product in one
+ * kernel.  gate and up have the same rows, cols, layout and group
+ * (QAT_ERR_DIMENSION_MISMATCH otherwise) and either both zero points or
+ * neither.  The second half is qat_linear4 of h.  Otherwise as qat_linear4.
+ */
+qat_status qat_gated4(const void* x, qat_dtype x_dtype, int64_t tokens, const qat_weight4* gate,
+                      const qat_weight4* up, qat_activation act, float* h, qat_stream_t stream);
+
+/*
+ * Gated feed-forward block: g = x Wg^T, u = x Wu^T, h = act(g) * u (rounded
+ * to dtype), y = h Wd^T.  x, y: dtype[tokens, dim]; w_gate, w_up:
+ * dtype[hidden, dim]; w_down: dtype[dim, hidden]; h: dtype[tokens, hidden];
+ * gate_pre, up_pre (both or neither): float[tokens, hidden], g and u kept for
+ * the backward pass.  act: silu g * sigmoid(g), gelu g * Phi(g) (the erf
+ * form), relu max(g, 0).  Products and sums in binary32.  An empty sum
+ * (dim == 0 or hidden == 0) is zero.  workspace:
+ * qat_gated_ffn_workspace_bytes(dtype, tokens, dim, hidden, 0) bytes.
+ */
+size_t qat_gated_ffn_workspace_bytes(qat_dtype dtype, int64_t tokens, int64_t dim, int64_t hidden,
+                                     int backward);
+qat_status qat_gated_ffn(const void* x, qat_dtype dtype, int64_t tokens, int64_t dim,
+                         int64_t hidden, const void* w_gate, const void* w_up, const void* w_down,
+                         qat_activation act, void* h, float* gate_pre, float* up_pre, void* y,
+                         void* workspace, size_t workspace_bytes, qat_stream_t stream);
+
+/*
+ * Its backward pass from dy (dtype[tokens, dim]) and the forward call's x, h,
+ * gate_pre and up_pre: dh = dy Wd; dg = dh * u * act'(g) and du = dh * act(g),
+ * each rounded once to dtype; dx = dg Wg + du Wu; dw_gate = dg^T x;
+ * dw_up = du^T x; dw_down = dy^T h.  dx, dw_gate, dw_up and dw_down are each
+ * nullable (their products are then skipped).  relu'(0) = 0.  tokens == 0
+ * gives zero weight gradients.  workspace:
+ * qat_gated_ffn_workspace_bytes(dtype, tokens, dim, hidden, 1) bytes.
+ */
+qat_status qat_gated_ffn_backward(const void* dy, const void* x, qat_dtype dtype, int64_t tokens,
+                                  int64_t dim, int64_t hidden, const void* w_gate,
+                                  const void* w_up, const void* w_down, qat_activation act,
+                                  const void* h, const float* gate_pre, const float* up_pre,
+                                  void* dx, void* dw_gate, void* dw_up, void* dw_down,
+                                  void* workspace, size_t workspace_bytes, qat_stream_t stream);
+
+/*
+ * Layer norm over the last dimension: mean = sum x / cols, rstd =
+ * 1 / sqrt(sum (x - mean)^2 / cols + eps), y = (x - mean) * rstd * weight +
+ * bias.  x, y: dtype[rows, cols]; weight, bias (nullable: 1 and 0):
+ * dtype[cols]; mean, rstd (nullable): float[rows].  The deviations are summed
+ * around the mean, not from sum x^2.  eps finite and >= 0
+ * (QAT_ERR_INVALID_ARGUMENT).  rows * cols == 0 is a no-op.  One launch.
+ */
+qat_status qat_layer_norm(const void* x, qat_dtype dtype, int64_t rows, int64_t cols,
+                          const void* weight, const void* bias, float eps, void* y, float* mean,
+                          float* rstd, qat_stream_t stream);
+
+/*
+ * Its backward pass: with z = (x - mean) * rstd and p = dy * weight,
+ * dx = rstd * (p - mean(p) - z * mean(p * z)); dweight = sum over rows of
+ * dy * z; dbias = sum over rows of dy.  dx, dweight, dbias are each nullable;
+ * dweight and dbias are dtype[cols], summed in a fixed order (the same bits
+ * every call).  rows == 0 gives zero dweight and dbias.  workspace:
+ * qat_layer_norm_backward_workspace_bytes(rows, cols) bytes, 16-byte aligned,
+ * when dweight or dbias is asked for.
+ */
+size_t qat_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+qat_status qat_layer_norm_backward(const void* dy, const void* x, qat_dtype dtype, int64_t rows,
+                                   int64_t cols, const void* weight, const float* mean,
+                                   const float* rstd, void* dx, void* dweight, void* dbias,
+                                   void* workspace, size_t workspace_bytes, qat_stream_t stream);
+
 /* Number of kernels this library has launched in this process (diagnostic). */
 uint64_t qat_kernel_launch_count(void);
 
