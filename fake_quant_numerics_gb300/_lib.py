@@ -89,9 +89,9 @@ PROTOTYPES = {
     "qat_gated4": ([_vp, _int, _i64, _w4, _w4, _int, _vp, _vp], _int),
     "qat_gated_ffn_workspace_bytes": ([_int, _i64, _i64, _i64, _int], _sz),
     "qat_gated_ffn": ([_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp, _vp,
-                       _sz, _vp], _int),
+                       _vp, _sz, _vp], _int),
     "qat_gated_ffn_backward": ([_vp, _vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _int, _vp, _vp,
-                                _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _int),
+                                _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _int),
     "qat_layer_norm": ([_vp, _int, _i64, _i64, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp], _int),
     "qat_layer_norm_backward_workspace_bytes": ([_i64, _i64], _sz),
     "qat_layer_norm_backward": ([_vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,

@@ -1,0 +1,535 @@
+// kernels_dense.cu -- the dense products of the gated feed-forward block on the
+// fifth-generation tensor cores.
+//
+//   C[m, n] = sum over segments s of sum_k A_s(m, k) B_s(n, k)
+//
+// with the block's element-wise steps as epilogues.  An operand is read by
+// bulk tensor copies either along k (K-major) or along its own rows
+// (MN-major), so no transpose is ever written.
+//
+// A CTA stages 128 rows of A and 128 of B, 64 deep, per step (32 KB, six steps
+// in flight) in 128-byte swizzled rows.  One thread issues the copies, one the
+// MMAs; the sums stay in tensor memory, in two buffers, so that four warps
+// finish one tile while the next is multiplied.  CG = 2: two CTAs share a
+// 256 x 256 tile, each holding half of A and half of B, which halves the
+// shared-memory traffic per product (a single CTA's 128 x 128 tile reads its
+// operands faster than shared memory delivers them) - taken when such tiles
+// fill the GPU.  CG = 1: 128 x 128 tiles, and where those are few a cluster of
+// up to eight CTAs splits k and adds its sums through distributed shared
+// memory in rank order.
+#include "qat_dense.h"
+#include "qat_layer.cuh"
+#include "qat_tc.cuh"
+
+#include <atomic>
+
+namespace qat {
+
+constexpr int kBK = 64, kStages = 6;
+constexpr int kRows = 128;                      // rows of A and of B per CTA and stage
+constexpr uint32_t kOpBytes = kRows * kBK * 2;  // 16 KB
+constexpr uint32_t kStageBytes = 2 * kOpBytes;
+constexpr uint32_t kBarBytes = 256;
+constexpr uint32_t kDenseSmem = kStages * kStageBytes + kBarBytes + 1024;
+constexpr int kDenseThreads = 192;
+
+struct DenseArgs {
+  CUtensorMap a[2], b[2];
+  int64_t m, n;            // output size (gated: n = hidden)
+  int mt, nt, problems;    // tiles of the output; outputs that share B
+  int kt, segs, parts;     // k steps of a segment; segments; operand parts (1, or 3: fp32)
+  int split;               // CTAs of a cluster that share k (CG = 1)
+  int act;
+  void* c[2];
+  int64_t ld;
+  float* gp;
+  float* up;
+  void* dg;
+  void* du;
+  int32_t* flags;
+  uint32_t limit;
+};
+
+// 32 consecutive outputs of one row: full vectors where the row allows
+template <typename T>
+__device__ __forceinline__ void st_row32(void* p, int64_t at, int left, uint32_t align,
+                                         const float (&v)[32]) {
+  if (left >= 32 && align >= 16) {
+    constexpr int W = T::BYTES == 4 ? 32 : 16;  // words
+    uint32_t w[W];
+    if (T::BYTES == 4) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = __float_as_uint(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    }
+    char* q = static_cast<char*>(p) + at * T::BYTES;
+    if (align >= 32) {
+#pragma unroll
+      for (int i = 0; i < W; i += 8) {
+        V32 o;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o.w[j] = w[i + j];
+        st_v32(q + i * 4, o);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; i += 4)
+        *reinterpret_cast<uint4*>(q + i * 4) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < left) st_elem<T>(p, at + i, v[i]);
+  }
+}
+__device__ __forceinline__ void ld_row32(const float* p, int64_t at, int left, uint32_t align,
+                                         float (&v)[32]) {
+  if (left >= 32 && align >= 16) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(p + at + i);
+      v[i] = q.x;
+      v[i + 1] = q.y;
+      v[i + 2] = q.z;
+      v[i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = i < left ? p[at + i] : 0.0f;
+  }
+}
+// the largest of 32, 16 or 1 that divides the address and the row pitch
+__device__ __forceinline__ uint32_t row_align(const void* p, int64_t pitch_bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p) | (uint64_t)pitch_bytes;
+  return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : 1;
+}
+
+// One row's 32 columns from column c on (gated: v = g, u beside it).
+template <typename T, int EPI>
+__device__ __forceinline__ void finish32(const DenseArgs& p, int prob, int64_t row, int64_t c,
+                                         const float (&v)[32], const float (&u)[32]) {
+  const int64_t at = row * p.ld + c;
+  const int left = (int)min((int64_t)32, p.n - c);
+  if (EPI == kDenseStore) {
+    st_row32<T>(p.c[prob], at, left, row_align(p.c[prob], p.ld * T::BYTES), v);
+  } else if (EPI == kDenseGated) {
+    float h[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) h[i] = act_value(p.act, v[i]) * u[i];
+    st_row32<T>(p.c[0], at, left, row_align(p.c[0], p.ld * T::BYTES), h);
+    if (p.gp) {
+      st_row32<F32>(p.gp, at, left, row_align(p.gp, p.ld * 4), v);
+      st_row32<F32>(p.up, at, left, row_align(p.up, p.ld * 4), u);
+    }
+  } else {
+    float g[32], w[32], dg[32], du[32];
+    ld_row32(p.gp, at, left, row_align(p.gp, p.ld * 4), g);
+    ld_row32(p.up, at, left, row_align(p.up, p.ld * 4), w);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      float a, da;
+      act_grad(p.act, g[i], a, da);
+      dg[i] = v[i] * w[i] * da;
+      du[i] = v[i] * a;
+    }
+    st_row32<T>(p.dg, at, left, row_align(p.dg, p.ld * T::BYTES), dg);
+    st_row32<T>(p.du, at, left, row_align(p.du, p.ld * T::BYTES), du);
+  }
+}
+// The same for one element.
+template <typename T, int EPI>
+__device__ __forceinline__ void finish1(const DenseArgs& p, int prob, int64_t row, int64_t c,
+                                        float v, float u) {
+  const int64_t at = row * p.ld + c;
+  if (EPI == kDenseStore) {
+    st_elem<T>(p.c[prob], at, v);
+  } else if (EPI == kDenseGated) {
+    st_elem<T>(p.c[0], at, act_value(p.act, v) * u);
+    if (p.gp) {
+      p.gp[at] = v;
+      p.up[at] = u;
+    }
+  } else {
+    float a, da;
+    act_grad(p.act, p.gp[at], a, da);
+    st_elem<T>(p.dg, at, v * p.up[at] * da);
+    st_elem<T>(p.du, at, v * a);
+  }
+}
+
+struct Tile {
+  int prob;
+  int64_t m0, n0;  // first output row and column (of the CTA pair)
+};
+// Tiles in groups of 16 row tiles, columns outermost inside a group: the tiles
+// at work together then reread few operand rows, from L2.
+template <int CG, int EPI>
+__device__ __forceinline__ Tile tile_at(const DenseArgs& p, int64_t t) {
+  constexpr int BM = kRows * CG, BN = kRows * CG / (EPI == kDenseGated ? 2 : 1);
+  const int64_t per = (int64_t)p.mt * p.nt;
+  Tile r;
+  r.prob = (int)(t / per);
+  t -= r.prob * per;
+  constexpr int G = 16;
+  const int64_t g = t / ((int64_t)G * p.nt), in = t - g * G * p.nt;
+  const int rows = (int)min((int64_t)G, p.mt - g * G);
+  r.m0 = (g * G + in % rows) * BM;
+  r.n0 = (in / rows) * BN;
+  return r;
+}
+
+// fp32 operands are held as three bf16 parts (high, middle, low); the six
+// products that reach 2^-24 of the whole, smallest first
+__device__ __constant__ const uint8_t kPairA[6] = {2, 0, 1, 1, 0, 0};
+__device__ __constant__ const uint8_t kPairB[6] = {0, 2, 1, 0, 1, 0};
+
+template <typename T, int CG, int EPI, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constant__ DenseArgs p) {
+  extern __shared__ uint8_t raw[];
+  const uint32_t base = (tc::smem(raw) + 1023) & ~1023u;
+  const uint32_t bars = base + kStages * kStageBytes;
+  // full[6], empty[6], acc_full[2], acc_empty[2], drain; then the TMEM address
+  const auto full = [&](int s) { return bars + 8 * s; };
+  const auto empty = [&](int s) { return bars + 8 * (kStages + s); };
+  const auto acc_full = [&](int b) { return bars + 8 * (2 * kStages + b); };
+  const auto acc_empty = [&](int b) { return bars + 8 * (2 * kStages + 2 + b); };
+  const uint32_t drain = bars + 8 * (2 * kStages + 4);
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_rank();  // CG = 2: half of the tile; else k slice
+  const bool leader = CG == 1 || rank == 0;
+  constexpr int kAccCols = kRows * CG;  // TMEM columns of a buffer
+  constexpr int kTmemCols = 2 * kAccCols;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::bar_init(full(s), 1);
+      tc::bar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::bar_init(acc_full(b), 1);
+      tc::bar_init(acc_empty(b), 4 * CG);
+    }
+    tc::bar_init(drain, 1);
+    tc::bar_init_fence();
+    abort_flag = 0;
+    for (int i = 0; i < 2; ++i) {
+      tc::prefetch_map(&p.a[i]);
+      tc::prefetch_map(&p.b[i]);
+    }
+  }
+  if (warp == 1) tc::tmem_alloc<CG>(tc::smem(&tmem_slot), kTmemCols);
+  tc::fence_before();
+  __syncthreads();
+  if (CG == 2 || p.split > 1) tc::cluster_sync();
+  tc::fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  const int npairs = p.parts == 1 ? 1 : 6;
+  const int steps_all = p.segs * npairs * p.kt;
+  // this CTA's k steps
+  const int s0 = CG == 1 ? (int)((int64_t)steps_all * rank / p.split) : 0;
+  const int s1 = CG == 1 ? (int)((int64_t)steps_all * (rank + 1) / p.split) : steps_all;
+  const int64_t tiles = (int64_t)p.mt * p.nt * p.problems;
+  const int per_cluster = CG == 2 ? 2 : p.split;
+  const int64_t first = blockIdx.x / per_cluster, stride = gridDim.x / per_cluster;
+  bool ok = true;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 1;  // a fresh barrier passes the wait for "already empty"
+      int64_t issued = 0;
+      for (int64_t t = first; ok && t < tiles; t += stride) {
+        const Tile w = tile_at<CG, EPI>(p, t);
+        const int am = (int)(w.m0 + (CG == 2 ? (int64_t)rank * kRows : 0));
+        const int bn = (int)(w.n0 + (CG == 2 && EPI != kDenseGated ? (int64_t)rank * kRows : 0));
+        for (int s = s0; s < s1; ++s) {
+          ok = tc::bar_wait(empty(stage), phase, &abort_flag, p.limit);
+          if (!ok) break;
+          const int seg = s / (npairs * p.kt), r = s - seg * npairs * p.kt;
+          const int pr = r / p.kt, k0 = (r - pr * p.kt) * kBK;
+          const int pa = npairs == 1 ? 0 : kPairA[pr], pb = npairs == 1 ? 0 : kPairB[pr];
+          const uint32_t sa = base + stage * kStageBytes, sb = sa + kOpBytes;
+          uint32_t bar = full(stage);
+          if (leader) tc::bar_expect(bar, kStageBytes * CG);
+          if (CG == 2) bar = tc::map_rank(bar, 0);
+          const CUtensorMap* ma = &p.a[p.problems > 1 ? w.prob : seg];
+          if (A_MN) {
+            tc::load_box<CG == 2>(ma, sa, bar, am, k0, pa);
+            tc::load_box<CG == 2>(ma, sa + kOpBytes / 2, bar, am + 64, k0, pa);
+          } else {
+            tc::load_box<CG == 2>(ma, sa, bar, k0, am, pa);
+          }
+          if (EPI == kDenseGated) {
+            // gate rows then up rows; a pair's CTAs hold one each
+            if (CG == 2) {
+              tc::load_box<true>(&p.b[rank], sb, bar, k0, bn, pb);
+            } else {
+              tc::load_box<false>(&p.b[0], sb, bar, k0, bn, pb);
+              tc::load_box<false>(&p.b[1], sb + kOpBytes / 2, bar, k0, bn, pb);
+            }
+          } else if (B_MN) {
+            tc::load_box<CG == 2>(&p.b[seg], sb, bar, bn, k0, pb);
+            tc::load_box<CG == 2>(&p.b[seg], sb + kOpBytes / 2, bar, bn + 64, k0, pb);
+          } else {
+            tc::load_box<CG == 2>(&p.b[seg], sb, bar, k0, bn, pb);
+          }
+          ++issued;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok) {  // copies in flight land before the block ends
+        volatile int none = 0;
+        if (leader)
+          for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+            tc::bar_wait(full((int)(i % kStages)), (uint32_t)(i / kStages) & 1, &none, 1u << 16);
+        else  // they are counted in the other CTA: a millisecond is ample
+          for (int i = 0; i < 1024; ++i) __nanosleep(1000);
+      }
+    }
+  } else if (warp == 1) {
+    if (leader && lane == 0) {
+      constexpr uint32_t idesc = tc::idesc_bf16(kRows * CG, kRows * CG, A_MN, B_MN);
+      int stage = 0;
+      uint32_t phase = 0;
+      int64_t it = 0;
+      for (int64_t t = first; ok && t < tiles; t += stride, ++it) {
+        const int buf = (int)(it & 1);
+        ok = tc::bar_wait(acc_empty(buf), (uint32_t)(it >> 1 & 1) ^ 1, &abort_flag, p.limit);
+        tc::fence_after();
+        for (int s = s0; ok && s < s1; ++s) {
+          ok = tc::bar_wait(full(stage), phase, &abort_flag, p.limit);
+          if (!ok) break;
+          tc::fence_after();
+          const uint32_t sa = base + stage * kStageBytes, sb = sa + kOpBytes;
+          const uint64_t da = tc::desc_sw128(sa, A_MN ? kOpBytes / 2 : 16);
+          const uint64_t db = tc::desc_sw128(sb, B_MN ? kOpBytes / 2 : 16);
+#pragma unroll
+          for (int k = 0; k < kBK / 16; ++k)
+            tc::mma_bf16<CG>(tmem + buf * kAccCols, da + (A_MN ? 2048 : 32) / 16 * k,
+                             db + (B_MN ? 2048 : 32) / 16 * k, idesc, s > s0 || k > 0);
+          tc::mma_commit<CG>(empty(stage));
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (ok) tc::mma_commit<CG>(acc_full(buf));
+      }
+      if (!ok) {  // MMAs in flight end before tensor memory is freed
+        volatile int none = 0;
+        tc::mma_commit<CG>(drain);
+        tc::bar_wait(drain, 0, &none, 1u << 16);
+      }
+    }
+  } else {
+    const int quad = warp & 3;
+    int64_t it = 0;
+    for (int64_t t = first; t < tiles; t += stride, ++it) {
+      const Tile w = tile_at<CG, EPI>(p, t);
+      const int buf = (int)(it & 1);
+      if (ok) ok = tc::bar_wait(acc_full(buf), (uint32_t)(it >> 1 & 1), &abort_flag, p.limit);
+      ok = __all_sync(~0u, ok);
+      tc::fence_after();
+      const uint32_t acc = tmem + buf * kAccCols + ((uint32_t)(quad * 32) << 16);
+      constexpr int kOut = EPI == kDenseGated ? kAccCols / 2 : kAccCols;
+      if (CG == 1 && p.split > 1) {
+        // this CTA's sums to its own shared memory, [column][row]: every stage
+        // has been multiplied, so the buffers are free
+        float* sums = reinterpret_cast<float*>(raw + (base - tc::smem(raw)));
+#pragma unroll
+        for (int c = 0; c < kAccCols; c += 32) {
+          uint32_t r[32];
+          tc::tmem_ld32(acc + c, r);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            sums[(c + i) * kRows + quad * 32 + lane] = ok ? __uint_as_float(r[i]) : __int_as_float(0x7fc00000);
+        }
+        break;  // joined below
+      }
+      const int64_t row = w.m0 + (CG == 2 ? (int64_t)rank * kRows : 0) + quad * 32 + lane;
+#pragma unroll 1
+      for (int c = 0; c < kOut; c += 32) {
+        uint32_t r[32], q[32];
+        tc::tmem_ld32(acc + c, r);
+        if (EPI == kDenseGated) tc::tmem_ld32(acc + kOut + c, q);
+        tc::tmem_ld_wait();
+        if (c + 32 == kOut) {  // the buffer is read: the next tile's MMAs may use it
+          tc::fence_before();
+          if (lane == 0)
+            tc::bar_arrive_cluster(CG == 2 ? tc::map_rank(acc_empty(buf), 0) : tc::map_rank(acc_empty(buf), rank));
+        }
+        if (row < p.m && w.n0 + c < p.n) {
+          float v[32], u[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            v[i] = ok ? __uint_as_float(r[i]) : __int_as_float(0x7fc00000);
+            u[i] = EPI == kDenseGated ? __uint_as_float(q[i]) : 0.0f;
+          }
+          finish32<T, EPI>(p, w.prob, row, w.n0 + c, v, u);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (CG == 1 && p.split > 1) {
+    tc::cluster_sync();
+    // each CTA of the cluster finishes its share of the columns, adding the
+    // k slices in rank order
+    constexpr int kOut = EPI == kDenseGated ? kAccCols / 2 : kAccCols;
+    const Tile w = tile_at<CG, EPI>(p, first);
+    const int rows = (int)min((int64_t)kRows, p.m - w.m0);
+    const int c0 = kOut * (int)rank / p.split, c1 = kOut * ((int)rank + 1) / p.split;
+    const int width = c1 - c0;
+    for (int i = threadIdx.x; i < rows * width; i += kDenseThreads) {
+      const int c = c0 + i % width, r = i / width;
+      if (w.n0 + c >= p.n) continue;
+      float v = 0.0f, u = 0.0f;
+      for (int q = 0; q < p.split; ++q) {
+        const uint32_t peer = tc::map_rank(base, q);
+        v += tc::ld_cluster(peer + (c * kRows + r) * 4);
+        if (EPI == kDenseGated) u += tc::ld_cluster(peer + ((kOut + c) * kRows + r) * 4);
+      }
+      finish1<T, EPI>(p, w.prob, w.m0 + r, w.n0 + c, v, u);
+    }
+  }
+  if (CG == 2 || p.split > 1) tc::cluster_sync();  // peers have read this CTA's memory
+  if (threadIdx.x == 0 && abort_flag && p.flags) atomicOr(p.flags, QAT_FLAG_DEVICE_TIMEOUT);
+  if (warp == 1) tc::tmem_free<CG>(tmem, kTmemCols);
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+static EncodeTiled encoder() {
+  static std::atomic<EncodeTiled> fn{nullptr};
+  EncodeTiled f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    void* q = nullptr;
+    cudaDriverEntryPointQueryResult st;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault,
+                                         &st) != cudaSuccess ||
+        st != cudaDriverEntryPointSuccess)
+      return nullptr;
+    f = reinterpret_cast<EncodeTiled>(q);
+    fn.store(f, std::memory_order_release);
+  }
+  return f;
+}
+
+// Operand of `rows` m or n and `depth` k: boxes of `box` rows x 64 k (K-major)
+// or 64 rows x 64 k (MN-major).
+static bool encode(CUtensorMap* map, const DenseOp& o, int64_t rows, int64_t depth, int parts,
+                   int box) {
+  EncodeTiled f = encoder();
+  if (!f) return false;
+  const cuuint64_t inner = o.mn_major ? rows : depth, outer = o.mn_major ? depth : rows;
+  const cuuint64_t dims[3] = {inner, outer, (cuuint64_t)parts};
+  const cuuint64_t pitch = (cuuint64_t)o.pitch * 2;
+  const cuuint64_t strides[2] = {pitch, parts > 1 ? (cuuint64_t)o.part * 2 : pitch * outer};
+  const cuuint32_t boxes[3] = {64, (cuuint32_t)(o.mn_major ? 64 : box), 1};
+  const cuuint32_t unit[3] = {1, 1, 1};
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p), dims, strides, boxes,
+           unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int CG, int EPI, bool A_MN, bool B_MN>
+static qat_status launch(DenseArgs& p, cudaStream_t s) {
+  const auto kernel = k_dense<T, CG, EPI, A_MN, B_MN>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmem) !=
+      cudaSuccess) {
+    (void)cudaGetLastError();
+    return QAT_ERR_CUDA;
+  }
+  const int sms = device_info().sms;
+  const int64_t tiles = (int64_t)p.mt * p.nt * p.problems;
+  const int cluster = CG == 2 ? 2 : p.split;
+  int64_t most = sms / cluster;
+  const int64_t clusters = CG == 1 && p.split > 1 ? tiles : tiles < most ? tiles : most;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(clusters * cluster));
+  cfg.blockDim = dim3(kDenseThreads);
+  cfg.dynamicSmemBytes = kDenseSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return QAT_ERR_CUDA;
+  }
+  count_launch(1);
+  return QAT_OK;
+}
+
+template <typename T, int CG>
+static qat_status launch_majors(DenseArgs& p, int epi, bool a_mn, bool b_mn, cudaStream_t s) {
+  if (epi == kDenseGated) return launch<T, CG, kDenseGated, false, false>(p, s);
+  if (epi == kDenseGatedBwd) return launch<T, CG, kDenseGatedBwd, false, true>(p, s);
+  if (a_mn) return launch<T, CG, kDenseStore, true, true>(p, s);
+  if (b_mn) return launch<T, CG, kDenseStore, false, true>(p, s);
+  return launch<T, CG, kDenseStore, false, false>(p, s);
+}
+
+qat_status launch_dense(const Dense& d, cudaStream_t s) {
+  if (d.m == 0 || d.n == 0) return QAT_OK;
+  DenseArgs p = {};
+  const bool gated = d.epi == kDenseGated;
+  const int sms = device_info().sms;
+  const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  p.m = d.m;
+  p.n = d.n;
+  p.problems = d.problems;
+  p.segs = d.segs;
+  p.parts = d.parts;
+  p.kt = (int)up(d.k, kBK);
+  // pairs of CTAs once their tiles fill the GPU
+  const int64_t big = up(d.m, 256) * up(d.n, gated ? 128 : 256) * d.problems;
+  const bool pair = big >= sms / 2;
+  const int bm = pair ? 256 : 128, bn = gated ? bm / 2 : bm;
+  p.mt = (int)up(d.m, bm);
+  p.nt = (int)up(d.n, bn);
+  p.split = 1;
+  if (!pair) {
+    // k is split while there are SMs for it and four steps for each CTA
+    const int64_t tiles = (int64_t)p.mt * p.nt * p.problems;
+    const int64_t steps = (int64_t)p.segs * (p.parts == 1 ? 1 : 6) * p.kt;
+    while (p.split < 8 && tiles * p.split * 2 <= sms && steps >= p.split * 2 * 4) p.split *= 2;
+  }
+  const int nb = gated ? 2 : d.segs, na = d.problems > 1 ? d.problems : d.segs;
+  for (int i = 0; i < 2; ++i) {
+    if (!encode(&p.a[i], d.a[i < na ? i : 0], d.m, d.k, d.parts, 128)) return QAT_ERR_CUDA;
+    if (!encode(&p.b[i], d.b[i < nb ? i : 0], d.n, d.k, d.parts, gated && !pair ? 64 : 128))
+      return QAT_ERR_CUDA;
+  }
+  p.act = d.act;
+  p.c[0] = d.c[0];
+  p.c[1] = d.c[1];
+  p.ld = d.n;
+  p.gp = d.gp;
+  p.up = d.up;
+  p.dg = d.dg;
+  p.du = d.du;
+  p.flags = d.flags;
+  p.limit = device_wait_limit();
+  const bool a_mn = d.a[0].mn_major, b_mn = d.b[0].mn_major;
+  return pair ? launch_majors<BF16, 2>(p, d.epi, a_mn, b_mn, s)
+              : launch_majors<BF16, 1>(p, d.epi, a_mn, b_mn, s);
+}
+
+}  // namespace qat

@@ -5,6 +5,7 @@
 //   dx = dg Wg + du Wu; dWg = dg^T x, dWu = du^T x, dWd = dy^T h
 //
 // One tiled product kernel with the element-wise steps as its epilogues.
+#include "qat_dense.h"
 #include "qat_layer.cuh"
 #include "qat_layer.h"
 
@@ -118,6 +119,16 @@ size_t ffn_ws_bytes(qat_dtype dt, int64_t tokens, int64_t dim, int64_t hidden, b
   return backward ? 2 * r256((size_t)tokens * hidden * (dt == QAT_F32 ? 4 : 2)) : 0;
 }
 
+static bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// The tensor cores take bf16 rows of whole 16-byte vectors.
+static bool dense_ok(qat_dtype dt, int64_t d, int64_t f, const void* const* ps, int n) {
+  if (dt != QAT_BF16 || d % 8 || f % 8) return false;
+  for (int i = 0; i < n; ++i)
+    if (!on16(ps[i])) return false;
+  return true;
+}
+
 template <typename T>
 static qat_status fwd(const void* x, int64_t t, int64_t d, int64_t f, const void* wg,
                       const void* wu, const void* wd, int act, void* h, float* gp, float* up,
@@ -152,10 +163,111 @@ static qat_status bwd(const void* dy, const void* x, int64_t t, int64_t d, int64
   return launch_status();
 }
 
+static qat_status fwd_dense(const void* x, int64_t t, int64_t d, int64_t f, const void* wg,
+                            const void* wu, const void* wd, int act, void* h, float* gp, float* up,
+                            void* y, int32_t* flags, cudaStream_t s) {
+  Dense g = {};
+  g.epi = kDenseGated;
+  g.m = t;
+  g.n = f;
+  g.k = d;
+  g.a[0] = DenseOp{x, d, false, 0};
+  g.b[0] = DenseOp{wg, d, false, 0};
+  g.b[1] = DenseOp{wu, d, false, 0};
+  g.act = act;
+  g.c[0] = h;
+  g.gp = gp;
+  g.up = up;
+  g.flags = flags;
+  const qat_status st = launch_dense(g, s);
+  if (st) return st;
+  Dense o = {};
+  o.epi = kDenseStore;
+  o.m = t;
+  o.n = d;
+  o.k = f;
+  o.a[0] = DenseOp{h, f, false, 0};
+  o.b[0] = DenseOp{wd, f, false, 0};
+  o.c[0] = y;
+  o.flags = flags;
+  return launch_dense(o, s);
+}
+
+static qat_status bwd_dense(const void* dy, const void* x, int64_t t, int64_t d, int64_t f,
+                            const void* wg, const void* wu, const void* wd, int act, const void* h,
+                            const float* gp, const float* up, void* dx, void* dwg, void* dwu,
+                            void* dwd, int32_t* flags, void* ws, cudaStream_t s) {
+  char* dg = static_cast<char*>(ws);
+  char* du = dg + r256((size_t)t * f * 2);
+  qat_status st = QAT_OK;
+  if (dx || dwg || dwu) {
+    Dense q = {};
+    q.epi = kDenseGatedBwd;
+    q.m = t;
+    q.n = f;
+    q.k = d;
+    q.a[0] = DenseOp{dy, d, false, 0};
+    q.b[0] = DenseOp{wd, f, true, 0};
+    q.act = act;
+    q.gp = const_cast<float*>(gp);
+    q.up = const_cast<float*>(up);
+    q.dg = dg;
+    q.du = du;
+    q.flags = flags;
+    st = launch_dense(q, s);
+  }
+  if (!st && dx) {
+    Dense q = {};
+    q.epi = kDenseStore;
+    q.m = t;
+    q.n = d;
+    q.k = f;
+    q.segs = 2;
+    q.a[0] = DenseOp{dg, f, false, 0};
+    q.a[1] = DenseOp{du, f, false, 0};
+    q.b[0] = DenseOp{wg, d, true, 0};
+    q.b[1] = DenseOp{wu, d, true, 0};
+    q.c[0] = dx;
+    q.flags = flags;
+    st = launch_dense(q, s);
+  }
+  if (!st && (dwg || dwu)) {
+    Dense q = {};
+    q.epi = kDenseStore;
+    q.m = f;
+    q.n = d;
+    q.k = t;
+    q.problems = dwg && dwu ? 2 : 1;
+    q.a[0] = DenseOp{dwg ? dg : du, f, true, 0};
+    q.a[1] = DenseOp{du, f, true, 0};
+    q.b[0] = DenseOp{x, d, true, 0};
+    q.c[0] = dwg ? dwg : dwu;
+    q.c[1] = dwu;
+    q.flags = flags;
+    st = launch_dense(q, s);
+  }
+  if (!st && dwd) {
+    Dense q = {};
+    q.epi = kDenseStore;
+    q.m = d;
+    q.n = f;
+    q.k = t;
+    q.a[0] = DenseOp{dy, d, true, 0};
+    q.b[0] = DenseOp{h, f, true, 0};
+    q.c[0] = dwd;
+    q.flags = flags;
+    st = launch_dense(q, s);
+  }
+  return st;
+}
+
 qat_status launch_ffn_fwd(const void* x, qat_dtype dt, int64_t t, int64_t d, int64_t f,
                           const void* wg, const void* wu, const void* wd, int act, void* h,
-                          float* gp, float* up, void* y, void* ws, cudaStream_t s) {
+                          float* gp, float* up, void* y, int32_t* flags, void* ws, cudaStream_t s) {
   (void)ws;
+  const void* ps[] = {x, wg, wu, wd, h};
+  if (t > 0 && d > 0 && f > 0 && dense_ok(dt, d, f, ps, 5))
+    return fwd_dense(x, t, d, f, wg, wu, wd, act, h, gp, up, y, flags, s);
   return dt == QAT_F32 ? fwd<F32>(x, t, d, f, wg, wu, wd, act, h, gp, up, y, s)
                        : fwd<BF16>(x, t, d, f, wg, wu, wd, act, h, gp, up, y, s);
 }
@@ -163,7 +275,10 @@ qat_status launch_ffn_fwd(const void* x, qat_dtype dt, int64_t t, int64_t d, int
 qat_status launch_ffn_bwd(const void* dy, const void* x, qat_dtype dt, int64_t t, int64_t d,
                           int64_t f, const void* wg, const void* wu, const void* wd, int act,
                           const void* h, const float* gp, const float* up, void* dx, void* dwg,
-                          void* dwu, void* dwd, void* ws, cudaStream_t s) {
+                          void* dwu, void* dwd, int32_t* flags, void* ws, cudaStream_t s) {
+  const void* ps[] = {dy, x, wg, wu, wd, h};
+  if (t > 0 && d > 0 && f > 0 && dense_ok(dt, d, f, ps, 6))
+    return bwd_dense(dy, x, t, d, f, wg, wu, wd, act, h, gp, up, dx, dwg, dwu, dwd, flags, ws, s);
   return dt == QAT_F32
              ? bwd<F32>(dy, x, t, d, f, wg, wu, wd, act, h, gp, up, dx, dwg, dwu, dwd, ws, s)
              : bwd<BF16>(dy, x, t, d, f, wg, wu, wd, act, h, gp, up, dx, dwg, dwu, dwd, ws, s);

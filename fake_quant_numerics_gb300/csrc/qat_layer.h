@@ -27,10 +27,10 @@ qat_status launch_norm_bwd(const void* dy, const void* x, qat_dtype dt, int64_t 
 size_t ffn_ws_bytes(qat_dtype dt, int64_t tokens, int64_t dim, int64_t hidden, bool backward);
 qat_status launch_ffn_fwd(const void* x, qat_dtype dt, int64_t t, int64_t d, int64_t f,
                           const void* wg, const void* wu, const void* wd, int act, void* h,
-                          float* gp, float* up, void* y, void* ws, cudaStream_t s);
+                          float* gp, float* up, void* y, int32_t* flags, void* ws, cudaStream_t s);
 qat_status launch_ffn_bwd(const void* dy, const void* x, qat_dtype dt, int64_t t, int64_t d,
                           int64_t f, const void* wg, const void* wu, const void* wd, int act,
                           const void* h, const float* gp, const float* up, void* dx, void* dwg,
-                          void* dwu, void* dwd, void* ws, cudaStream_t s);
+                          void* dwu, void* dwd, int32_t* flags, void* ws, cudaStream_t s);
 
 }  // namespace qat

@@ -94,7 +94,7 @@ size_t qat_gated_ffn_workspace_bytes(qat_dtype dtype, int64_t tokens, int64_t di
 qat_status qat_gated_ffn(const void* x, qat_dtype dtype, int64_t tokens, int64_t dim,
                          int64_t hidden, const void* w_gate, const void* w_up, const void* w_down,
                          qat_activation act, void* h, float* gate_pre, float* up_pre, void* y,
-                         void* workspace, size_t workspace_bytes, qat_stream_t stream) {
+                         int32_t* dev_flags, void* workspace, size_t workspace_bytes, qat_stream_t stream) {
   qat::NvtxScope nvtx("qat_gated_ffn");
   if (!dtype_ok(dtype) || !act_ok(act)) return QAT_ERR_UNSUPPORTED;
   if (!ffn_sizes_ok(tokens, dim, hidden)) return QAT_ERR_INVALID_ARGUMENT;
@@ -106,13 +106,13 @@ qat_status qat_gated_ffn(const void* x, qat_dtype dtype, int64_t tokens, int64_t
     return QAT_ERR_INVALID_ARGUMENT;
   const uintptr_t e = esize(dtype);
   if (!on(x, e) || !on(w_gate, e) || !on(w_up, e) || !on(w_down, e) || !on(h, e) || !on(y, e) ||
-      !on(gate_pre, 4) || !on(up_pre, 4))
+      !on(gate_pre, 4) || !on(up_pre, 4) || !on(dev_flags, 4))
     return QAT_ERR_MISALIGNED;
   const size_t need = ffn_ws_bytes(dtype, tokens, dim, hidden, false);
   if (need && (!workspace || workspace_bytes < need)) return QAT_ERR_WORKSPACE;
   if (need && !on(workspace, 16)) return QAT_ERR_MISALIGNED;
   return launch_ffn_fwd(x, dtype, tokens, dim, hidden, w_gate, w_up, w_down, act, h, gate_pre,
-                        up_pre, y, workspace, reinterpret_cast<cudaStream_t>(stream));
+                        up_pre, y, dev_flags, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 qat_status qat_gated_ffn_backward(const void* dy, const void* x, qat_dtype dtype, int64_t tokens,
@@ -120,7 +120,7 @@ qat_status qat_gated_ffn_backward(const void* dy, const void* x, qat_dtype dtype
                                   const void* w_up, const void* w_down, qat_activation act,
                                   const void* h, const float* gate_pre, const float* up_pre,
                                   void* dx, void* dw_gate, void* dw_up, void* dw_down,
-                                  void* workspace, size_t workspace_bytes, qat_stream_t stream) {
+                                  int32_t* dev_flags, void* workspace, size_t workspace_bytes, qat_stream_t stream) {
   qat::NvtxScope nvtx("qat_gated_ffn_backward");
   if (!dtype_ok(dtype) || !act_ok(act)) return QAT_ERR_UNSUPPORTED;
   if (!ffn_sizes_ok(tokens, dim, hidden)) return QAT_ERR_INVALID_ARGUMENT;
@@ -131,13 +131,13 @@ qat_status qat_gated_ffn_backward(const void* dy, const void* x, qat_dtype dtype
   const uintptr_t e = esize(dtype);
   if (!on(dy, e) || !on(x, e) || !on(w_gate, e) || !on(w_up, e) || !on(w_down, e) || !on(h, e) ||
       !on(gate_pre, 4) || !on(up_pre, 4) || !on(dx, e) || !on(dw_gate, e) || !on(dw_up, e) ||
-      !on(dw_down, e))
+      !on(dw_down, e) || !on(dev_flags, 4))
     return QAT_ERR_MISALIGNED;
   const size_t need = ffn_ws_bytes(dtype, tokens, dim, hidden, true);
   if (need && (!workspace || workspace_bytes < need)) return QAT_ERR_WORKSPACE;
   if (need && !on(workspace, 16)) return QAT_ERR_MISALIGNED;
   return launch_ffn_bwd(dy, x, dtype, tokens, dim, hidden, w_gate, w_up, w_down, act, h, gate_pre,
-                        up_pre, dx, dw_gate, dw_up, dw_down, workspace,
+                        up_pre, dx, dw_gate, dw_up, dw_down, dev_flags, workspace,
                         reinterpret_cast<cudaStream_t>(stream));
 }
 

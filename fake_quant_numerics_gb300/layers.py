@@ -151,19 +151,19 @@ def qat_gated_ffn_workspace_bytes(dtype, tokens, dim, hidden, backward=False) ->
 
 
 def qat_gated_ffn(x, tokens, dim, hidden, w_gate, w_up, w_down, act, h, gate_pre, up_pre, y,
-                  workspace, stream=None):
+                  dev_flags, workspace, stream=None):
     st = _lib.lib().qat_gated_ffn(_p(x), _dt(x), tokens, dim, hidden, _p(w_gate), _p(w_up),
                                   _p(w_down), _ACT[act], _p(h), _p(gate_pre), _p(up_pre), _p(y),
-                                  _p(workspace), _nbytes(workspace), _s(stream))
+                                  _p(dev_flags), _p(workspace), _nbytes(workspace), _s(stream))
     _lib.check("qat_gated_ffn", st)
 
 
 def qat_gated_ffn_backward(dy, x, tokens, dim, hidden, w_gate, w_up, w_down, act, h, gate_pre,
-                           up_pre, dx, dw_gate, dw_up, dw_down, workspace, stream=None):
+                           up_pre, dx, dw_gate, dw_up, dw_down, dev_flags, workspace, stream=None):
     st = _lib.lib().qat_gated_ffn_backward(
         _p(dy), _p(x), _dt(x), tokens, dim, hidden, _p(w_gate), _p(w_up), _p(w_down), _ACT[act],
         _p(h), _p(gate_pre), _p(up_pre), _p(dx), _p(dw_gate), _p(dw_up), _p(dw_down),
-        _p(workspace), _nbytes(workspace), _s(stream))
+        _p(dev_flags), _p(workspace), _nbytes(workspace), _s(stream))
     _lib.check("qat_gated_ffn_backward", st)
 
 
@@ -195,7 +195,7 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
         g = torch.empty(tokens, hidden, dtype=torch.float32, device=x.device)
         u = torch.empty_like(g)
     y = torch.empty_like(x)
-    qat_gated_ffn(x, tokens, dim, hidden, w_gate, w_up, w_down, activation, h, g, u, y,
+    qat_gated_ffn(x, tokens, dim, hidden, w_gate, w_up, w_down, activation, h, g, u, y, None,
                   _ffn_workspace(x, tokens, dim, hidden, False))
     return GatedFfn(y, h, g, u)
 
@@ -219,7 +219,7 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
     if want_dw:
         dwg, dwu, dwd = torch.empty_like(w_gate), torch.empty_like(w_up), torch.empty_like(w_down)
     qat_gated_ffn_backward(dy, x, tokens, dim, hidden, w_gate, w_up, w_down, activation, saved.h,
-                           saved.gate_pre, saved.up_pre, dx, dwg, dwu, dwd,
+                           saved.gate_pre, saved.up_pre, dx, dwg, dwu, dwd, None,
                            _ffn_workspace(x, tokens, dim, hidden, True))
     return dx, dwg, dwu, dwd
 

@@ -494,14 +494,16 @@ qat_status qat_gated4(const void* x, qat_dtype x_dtype, int64_t tokens, const qa
  * the backward pass.  act: silu g * sigmoid(g), gelu g * Phi(g) (the erf
  * form), relu max(g, 0).  Products and sums in binary32.  An empty sum
  * (dim == 0 or hidden == 0) is zero.  workspace:
- * qat_gated_ffn_workspace_bytes(dtype, tokens, dim, hidden, 0) bytes.
+ * qat_gated_ffn_workspace_bytes(dtype, tokens, dim, hidden, 0) bytes, 16-byte
+ * aligned.  A bounded device wait that runs out sets QAT_FLAG_DEVICE_TIMEOUT in
+ * *dev_flags (nullable) and makes the outputs it did not reach NaN.
  */
 size_t qat_gated_ffn_workspace_bytes(qat_dtype dtype, int64_t tokens, int64_t dim, int64_t hidden,
                                      int backward);
 qat_status qat_gated_ffn(const void* x, qat_dtype dtype, int64_t tokens, int64_t dim,
                          int64_t hidden, const void* w_gate, const void* w_up, const void* w_down,
                          qat_activation act, void* h, float* gate_pre, float* up_pre, void* y,
-                         void* workspace, size_t workspace_bytes, qat_stream_t stream);
+                         int32_t* dev_flags, void* workspace, size_t workspace_bytes, qat_stream_t stream);
 
 /*
  * Its backward pass from dy (dtype[tokens, dim]) and the forward call's x, h,
@@ -517,7 +519,7 @@ qat_status qat_gated_ffn_backward(const void* dy, const void* x, qat_dtype dtype
                                   const void* w_up, const void* w_down, qat_activation act,
                                   const void* h, const float* gate_pre, const float* up_pre,
                                   void* dx, void* dw_gate, void* dw_up, void* dw_down,
-                                  void* workspace, size_t workspace_bytes, qat_stream_t stream);
+                                  int32_t* dev_flags, void* workspace, size_t workspace_bytes, qat_stream_t stream);
 
 /*
  * Layer norm over the last dimension: mean = sum x / cols, rstd =

@@ -66,7 +66,7 @@ def test_ffn_refusals(lib):
         a = dict(x=A, wg=A, wu=A, wd=A, h=A, g=None, u=None, y=A)
         a.update(kw)
         return lib.qat_gated_ffn(a["x"], dt, t, d, f, a["wg"], a["wu"], a["wd"], act, a["h"],
-                                 a["g"], a["u"], a["y"], A, 1 << 40, None)
+                                 a["g"], a["u"], a["y"], None, A, 1 << 40, None)
 
     inv, uns, mis = L.QAT_ERR_INVALID_ARGUMENT, L.QAT_ERR_UNSUPPORTED, L.QAT_ERR_MISALIGNED
     assert fwd(dt=9) == uns and fwd(act=3) == uns
@@ -81,7 +81,7 @@ def test_ffn_refusals(lib):
         a.update(kw)
         return lib.qat_gated_ffn_backward(a["dy"], a["x"], dt, 4, 16, 32, a["wg"], a["wu"], a["wd"],
                                           L.SILU, a["h"], a["g"], a["u"], a["dx"], a["dg"], a["du"],
-                                          a["dd"], ws, wsb, None)
+                                          a["dd"], None, ws, wsb, None)
 
     assert bwd(dt=9) == uns
     assert all(bwd(**{k: None}) == inv for k in ("dy", "x", "wg", "wu", "wd", "h", "g", "u"))
