@@ -6,6 +6,7 @@
 // (rows * cols / 2 bytes and the parameters) while the tokens are few.
 #include "qat_layer.cuh"
 #include "qat_layer.h"
+#include "qat_tc.cuh"
 
 namespace qat {
 
@@ -91,6 +92,387 @@ __global__ void __launch_bounds__(128) k_w4_generic(const void* __restrict__ x, 
   }
 }
 
+// ---------------------------------------------------------------------------
+// Rows of whole 8-code words whose units are whole runs of 32 codes.
+//
+// A warp multiplies 16 rows (of each of R row tiles and NW weights) by 8 NT
+// tokens with m16n8k16 tensor-core products: a code is exact in bf16 (128 + q
+// with the low mantissa bits, one logic operation for two codes, then an exact
+// subtraction of 136 + zero point), so is a bf16 x, and the sums are binary32.
+// Arithmetic per code is then about 1.4 instructions, which keeps reading the
+// codes the bound; scalar multiply-adds would need four.  A float x is split
+// into TERMS bf16 values (high, middle, low: 3 hold all its 24 bits, 2 hold 16,
+// enough under a bf16 output), one product each.
+//
+// k runs in blocks of 32 CH codes: lane t of a row's four takes 8 CH
+// consecutive codes (one load), so a load instruction covers 16 CH bytes of
+// each of 8 rows.  The order of k inside a block is the codes' bit order, the
+// same for both operands.  The block's 8 warps take blocks in turn, the CTAs of
+// a cluster split them once more where rows are few; partial sums are added in
+// shared memory, then over the cluster in rank order.
+// ---------------------------------------------------------------------------
+constexpr int kW4Warps = 8;
+
+struct W4Fast {
+  const uint8_t* codes;
+  const void* scales;
+  const int32_t* zp;
+  const float* super;
+};
+struct W4Args {
+  W4Fast w[2];
+  const void* x;
+  void* y;
+  int64_t rows, cols, tokens;
+  int64_t row_units;  // units from one row to the next
+  int64_t unit;       // codes of a unit
+  int dbl, act, y_bf16, split;
+};
+
+// two codes of a word (bits 0-3 and 16-19 after the shift) as bf16 q - zp
+__device__ __forceinline__ uint32_t w4_pair(uint32_t w, uint32_t bias) {
+  uint32_t v;
+  // (w & 0x000f000f) ^ 0x43084308: bf16 128 + (q + 8)
+  asm("lop3.b32 %0, %1, 0x000f000f, 0x43084308, 0x6a;" : "=r"(v) : "r"(w));
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(v), "r"(bias));
+  return v;
+}
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// x of 8 consecutive k as bf16 pairs in the codes' order (1,5) (0,4) (3,7) (2,6)
+__device__ __forceinline__ void pairs_bf16(const uint4& v, uint32_t (&b)[4]) {
+  b[0] = __byte_perm(v.x, v.z, 0x7632);
+  b[1] = __byte_perm(v.x, v.z, 0x5410);
+  b[2] = __byte_perm(v.y, v.w, 0x7632);
+  b[3] = __byte_perm(v.y, v.w, 0x5410);
+}
+// the bf16 terms of one float: truncations, so that none overflows; the
+// remainder of an infinity is 0 and a NaN keeps a mantissa bit
+template <int TERMS>
+__device__ __forceinline__ void split_f32(float x, uint32_t (&h)[TERMS]) {
+  const uint32_t u = __float_as_uint(x);
+  const bool special = (u & 0x7f800000u) == 0x7f800000u;
+  h[0] = u & 0xffff0000u;
+  if (special && (u & 0x007fffffu)) h[0] |= 0x00400000u;
+  float r = special ? 0.0f : x - __uint_as_float(h[0]);
+#pragma unroll
+  for (int i = 1; i < TERMS; ++i) {
+    h[i] = __float_as_uint(r) & 0xffff0000u;
+    r -= __uint_as_float(h[i]);
+  }
+}
+
+template <typename T, int CH>
+struct XWords {
+  uint32_t v[CH * (T::BYTES == 2 ? 4 : 8)];
+};
+// a lane's x of 8 CH consecutive k of one token (zeros where there is none)
+template <typename T, int CH>
+__device__ __forceinline__ void load_x(XWords<T, CH>& o, const void* x, int64_t at, int words,
+                                       bool vec) {
+  constexpr int W = T::BYTES == 2 ? 4 : 8;
+  const char* p = static_cast<const char*>(x) + at * T::BYTES;
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) o.v[j * W + i] = 0u;
+    if (j >= words) continue;
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(p + j * 8 * T::BYTES) + i / 4);
+        o.v[j * W + i] = q.x;
+        o.v[j * W + i + 1] = q.y;
+        o.v[j * W + i + 2] = q.z;
+        o.v[j * W + i + 3] = q.w;
+      }
+    } else if (T::BYTES == 4) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) o.v[j * W + i] = __ldg(reinterpret_cast<const uint32_t*>(p) + j * 8 + i);
+    } else {
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + j * 8;
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        o.v[j * W + i] = (uint32_t)__ldg(q + 2 * i) | (uint32_t)__ldg(q + 2 * i + 1) << 16;
+    }
+  }
+}
+// the B registers of word j, TERMS sets of four pairs
+template <typename T, int TERMS, int CH>
+__device__ __forceinline__ void x_pairs(const XWords<T, CH>& x, int j, uint32_t (&b)[TERMS][4]) {
+  if constexpr (T::BYTES == 2) {
+    pairs_bf16(make_uint4(x.v[j * 4], x.v[j * 4 + 1], x.v[j * 4 + 2], x.v[j * 4 + 3]), b[0]);
+  } else {
+    uint32_t h[8][TERMS];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) split_f32<TERMS>(__uint_as_float(x.v[j * 8 + i]), h[i]);
+    constexpr int lo[4] = {1, 0, 3, 2};
+#pragma unroll
+    for (int q = 0; q < TERMS; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[q][i] = __byte_perm(h[lo[i]][q], h[lo[i] + 4][q], 0x7632);
+  }
+}
+
+template <int CH>
+struct CodeWords {
+  uint32_t v[CH];
+};
+template <int CH>
+__device__ __forceinline__ void load_codes(CodeWords<CH>& o, const uint8_t* p, bool in) {
+  if constexpr (CH == 4) {
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (in) q = __ldcs(reinterpret_cast<const uint4*>(p));
+    o.v[0] = q.x, o.v[1] = q.y, o.v[2] = q.z, o.v[3] = q.w;
+  } else if constexpr (CH == 2) {
+    uint2 q = make_uint2(0, 0);
+    if (in) q = __ldcs(reinterpret_cast<const uint2*>(p));
+    o.v[0] = q.x, o.v[1] = q.y;
+  } else {
+    o.v[0] = in ? __ldcs(reinterpret_cast<const uint32_t*>(p)) : 0u;
+  }
+}
+
+__device__ __forceinline__ float w4_scale(const W4Args& p, const W4Fast& w, int64_t u) {
+  if (p.dbl)  // within an ulp of (q / 255) * super
+    return __fmul_rn((float)__ldg(static_cast<const uint8_t*>(w.scales) + u), 1.0f / 255.0f) *
+           __ldg(w.super + (u >> 8));
+  return __ldg(static_cast<const float*>(w.scales) + u);
+}
+// 136 + zp as a bf16 pair (exact)
+__device__ __forceinline__ uint32_t w4_bias(const W4Fast& w, int64_t u) {
+  if (!w.zp) return 0x43084308u;
+  const uint32_t h = 0x4308u + (uint32_t)min(max(__ldg(w.zp + u), -8), 7);
+  return h | h << 16;
+}
+
+template <typename T, int TERMS, int CH, int NT, int NW>
+__global__ void __launch_bounds__(kW4Warps * 32, NT == 1 && NW == 1 ? 2 : 1) k_w4(const W4Args p) {
+  constexpr int R = NW == 2 && NT == 4 ? 1 : 2;  // row tiles of each weight
+  constexpr int RT = R * NW, kRowsOut = 16 * R, kTok = 8 * NT;
+  __shared__ float red[kW4Warps][RT * 16][kTok];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int split = p.split;
+  const int rank = split > 1 ? (int)(blockIdx.x % split) : 0;
+  const int64_t n0 = (int64_t)(blockIdx.x / split) * kRowsOut;
+  const int64_t tok0 = (int64_t)blockIdx.y * kTok;
+  constexpr int KB = 32 * CH;
+  const int64_t blocks = (p.cols + KB - 1) / KB;
+  const int64_t per_unit = p.unit >= p.cols ? blocks : p.unit / KB;
+  const int64_t step = (int64_t)kW4Warps * split;
+  const bool vec_x = p.cols % 8 == 0 && (reinterpret_cast<uint64_t>(p.x) & 15) == 0;
+
+  // this lane's rows: g and g + 8 of each tile (rows past the end read row 0
+  // and are dropped at the end)
+  const uint8_t* cp[RT][2];
+  int64_t ru[R][2];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t n = n0 + r * 16 + h * 8 + g, m = n < p.rows ? n : 0;
+      ru[r][h] = m * p.row_units;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) cp[w * R + r][h] = p.w[w].codes + (m * p.cols) / 2;
+    }
+
+  float total[RT][NT][4] = {};
+  CodeWords<CH> next[RT][2];
+  const auto fetch = [&](int64_t kb) {
+    const int64_t k = kb * KB + t * 8 * CH;
+    const bool in = kb < blocks && k < p.cols;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) load_codes<CH>(next[i][h], cp[i][h] + k / 2, in);
+  };
+  int64_t kb = (int64_t)rank * kW4Warps + warp;
+  fetch(kb);
+  for (; kb < blocks; kb += step) {
+    CodeWords<CH> now[RT][2];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) now[i][h] = next[i][h];
+    const int64_t k = kb * KB + t * 8 * CH;
+    const int words = k < p.cols ? (int)min((int64_t)CH, (p.cols - k) / 8) : 0;
+    XWords<T, CH> xw[NT];
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+      const int64_t tok = tok0 + q * 8 + g;
+      load_x<T, CH>(xw[q], p.x, tok * p.cols + k, tok < p.tokens ? words : 0, vec_x);
+    }
+    fetch(kb + step);
+    const int64_t u = kb / per_unit;
+    float sc[RT][2];
+    uint32_t bias[RT][2];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        sc[i][h] = w4_scale(p, p.w[i / R], ru[i % R][h] + u);
+        bias[i][h] = w4_bias(p.w[i / R], ru[i % R][h] + u);
+      }
+    float part[RT][NT][4] = {};
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      uint32_t b[NT][TERMS][4];
+#pragma unroll
+      for (int q = 0; q < NT; ++q) x_pairs<T, TERMS, CH>(xw[q], j, b[q]);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        uint32_t a[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[h][e] = w4_pair(now[i][h].v[j] >> (4 * e), bias[i][h]);
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+#pragma unroll
+          for (int m = TERMS - 1; m >= 0; --m) {
+            mma_16816(part[i][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m][0], b[q][m][1]);
+            mma_16816(part[i][q], a[0][2], a[1][2], a[0][3], a[1][3], b[q][m][2], b[q][m][3]);
+          }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          total[i][q][e] = fmaf(part[i][q][e], sc[i][e >> 1], total[i][q][e]);
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2*>(&red[warp][i * 16 + h * 8 + g][q * 8 + 2 * t]) =
+            make_float2(total[i][q][2 * h], total[i][q][2 * h + 1]);
+  __syncthreads();
+  const int tokens = (int)min((int64_t)kTok, p.tokens - tok0);
+  // this CTA's sums over its warps, in red[0]
+  for (int i = threadIdx.x; i < RT * 16 * tokens; i += kW4Warps * 32) {
+    const int r = i % (RT * 16), c = i / (RT * 16);
+    float v = red[0][r][c];
+#pragma unroll
+    for (int w = 1; w < kW4Warps; ++w) v += red[w][r][c];
+    red[0][r][c] = v;
+  }
+  if (split > 1)
+    tc::cluster_sync();
+  else
+    __syncthreads();
+  for (int i = threadIdx.x + rank * kW4Warps * 32; i < kRowsOut * tokens;
+       i += kW4Warps * 32 * split) {
+    const int r = i % kRowsOut, c = i / kRowsOut;
+    if (n0 + r >= p.rows) continue;
+    float v = 0.0f, u = 0.0f;
+    if (split > 1) {
+      for (int q = 0; q < split; ++q) {
+        v += tc::ld_cluster(tc::map_rank(tc::smem(&red[0][r][c]), q));
+        if (NW == 2) u += tc::ld_cluster(tc::map_rank(tc::smem(&red[0][RT * 16 / 2 + r][c]), q));
+      }
+    } else {
+      v = red[0][r][c];
+      if (NW == 2) u = red[0][RT * 16 / 2 + r][c];
+    }
+    if (NW == 2) v = act_value(p.act, v) * u;
+    const int64_t at = (tok0 + c) * p.rows + n0 + r;
+    if (p.y_bf16)
+      st_elem<BF16>(p.y, at, v);
+    else
+      st_elem<F32>(p.y, at, v);
+  }
+  if (split > 1) tc::cluster_sync();  // the other CTAs have read red
+}
+
+template <typename T, int TERMS, int CH, int NT, int NW>
+static qat_status launch_fast(W4Args p, cudaStream_t s) {
+  constexpr int R = NW == 2 && NT == 4 ? 1 : 2;
+  const int64_t row_blocks = (p.rows + 16 * R - 1) / (16 * R);
+  const int64_t kblocks = (p.cols + 32 * CH - 1) / (32 * CH);
+  // a cluster splits k while two CTAs a SM are not reached and every warp keeps
+  // a block
+  p.split = 1;
+  const int64_t room = (int64_t)device_info().sms * 2;
+  while (p.split < 8 && row_blocks * p.split * 2 <= room && kblocks >= p.split * 2 * kW4Warps)
+    p.split *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(row_blocks * p.split), (unsigned)((p.tokens + 8 * NT - 1) / (8 * NT)));
+  cfg.blockDim = dim3(kW4Warps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, k_w4<T, TERMS, CH, NT, NW>, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return QAT_ERR_CUDA;
+  }
+  count_launch(1);
+  return QAT_OK;
+}
+template <typename T, int TERMS, int CH, int NW>
+static qat_status fast_tokens(const W4Args& p, cudaStream_t s) {
+  if (p.tokens <= 8) return launch_fast<T, TERMS, CH, 1, NW>(p, s);
+  if (p.tokens <= 16) return launch_fast<T, TERMS, CH, 2, NW>(p, s);
+  return launch_fast<T, TERMS, CH, 4, NW>(p, s);
+}
+template <typename T, int TERMS, int NW>
+static qat_status fast_chunk(const W4Args& p, int ch, cudaStream_t s) {
+  if (ch == 4) return fast_tokens<T, TERMS, 4, NW>(p, s);
+  if (ch == 2) return fast_tokens<T, TERMS, 2, NW>(p, s);
+  return fast_tokens<T, TERMS, 1, NW>(p, s);
+}
+
+// Words of 8 codes a lane takes at once: the widest load that rows, units and
+// blocks of k allow; 0 when the shape needs the generic kernel.
+static int w4_chunk(const qat_weight4& w) {
+  if (w.cols % 8) return 0;
+  if (w.layout == QAT_PER_TENSOR || w.layout == QAT_PER_ROW)
+    return w.cols % 32 == 0 ? 4 : w.cols % 16 == 0 ? 2 : 1;
+  const int64_t unit = w.layout == QAT_W4_DOUBLE ? 64 : w.group;
+  if (w.layout == QAT_W4_DOUBLE && w.cols % 64) return 0;
+  return unit % 128 == 0 ? 4 : unit % 64 == 0 ? 2 : unit % 32 == 0 ? 1 : 0;
+}
+
+static qat_status launch_w4_fast(const void* x, qat_dtype xdt, int64_t tokens,
+                                 const qat_weight4* w, int nw, int act, void* y, qat_dtype ydt,
+                                 int ch, cudaStream_t s) {
+  W4Args p = {};
+  for (int i = 0; i < nw; ++i)
+    p.w[i] = W4Fast{static_cast<const uint8_t*>(w[i].codes), w[i].scales, w[i].zero_points,
+                    w[i].super_scales};
+  p.x = x;
+  p.y = y;
+  p.rows = w->rows;
+  p.cols = w->cols;
+  p.tokens = tokens;
+  p.dbl = w->layout == QAT_W4_DOUBLE;
+  p.unit = w->layout == QAT_PER_GROUP ? w->group : p.dbl ? 64 : w->cols;
+  p.row_units = w->layout == QAT_PER_TENSOR ? 0 : w->cols / p.unit;
+  p.act = act;
+  p.y_bf16 = ydt == QAT_BF16;
+  if (xdt == QAT_BF16)
+    return nw == 2 ? fast_chunk<BF16, 1, 2>(p, ch, s) : fast_chunk<BF16, 1, 1>(p, ch, s);
+  if (nw == 2) return fast_chunk<F32, 3, 2>(p, ch, s);
+  return p.y_bf16 ? fast_chunk<F32, 2, 1>(p, ch, s) : fast_chunk<F32, 3, 1>(p, ch, s);
+}
+
 static W4 w4_of(const qat_weight4& w) {
   W4 r;
   r.codes = static_cast<const uint8_t*>(w.codes);
@@ -109,6 +491,8 @@ qat_status launch_w4(const void* x, qat_dtype xdt, int64_t tokens, const qat_wei
                      int act, void* y, qat_dtype ydt, cudaStream_t s) {
   const W4 a = w4_of(w[0]), b = w4_of(w[nw - 1]);
   const bool dbl = w->layout == QAT_W4_DOUBLE;
+  const int ch = w->cols > 0 && tokens <= 65535 * 8 ? w4_chunk(*w) : 0;
+  if (ch) return launch_w4_fast(x, xdt, tokens, w, nw, act, y, ydt, ch, s);
   // gridDim.y holds 65535 token tiles: longer inputs in several launches
   constexpr int64_t kMost = (int64_t)65535 * kGenTokens;
   for (int64_t t0 = 0; t0 < tokens; t0 += kMost) {
