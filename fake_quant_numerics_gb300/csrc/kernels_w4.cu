@@ -123,10 +123,12 @@ struct W4Args {
   W4Fast w[2];
   const void* x;
   void* y;
-  int64_t rows, cols, tokens;
+  int64_t rows, tokens;
   int64_t row_units;  // units from one row to the next
   int64_t unit;       // codes of a unit
-  int dbl, act, y_bf16, split;
+  int cols;
+  uint32_t unit_magic;
+  int dbl, act, y_bf16, vec_x, split;
 };
 
 // two codes of a word (bits 0-3 and 16-19 after the shift) as bf16 q - zp
@@ -145,6 +147,17 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// the same with no sum before it
+__device__ __forceinline__ void mma_16816_first(float (&c)[4], uint32_t a0, uint32_t a1,
+                                                uint32_t a2, uint32_t a3, uint32_t b0,
+                                                uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // x of 8 consecutive k as bf16 pairs in the codes' order (1,5) (0,4) (3,7) (2,6)
@@ -176,33 +189,25 @@ struct XWords {
 };
 // a lane's x of 8 CH consecutive k of one token (zeros where there is none)
 template <typename T, int CH>
-__device__ __forceinline__ void load_x(XWords<T, CH>& o, const void* x, int64_t at, int words,
-                                       bool vec) {
-  constexpr int W = T::BYTES == 2 ? 4 : 8;
-  const char* p = static_cast<const char*>(x) + at * T::BYTES;
+__device__ __forceinline__ void load_x(XWords<T, CH>& o, const char* p, bool in, bool vec) {
+  constexpr int W = CH * (T::BYTES == 2 ? 4 : 8);
 #pragma unroll
-  for (int j = 0; j < CH; ++j) {
+  for (int i = 0; i < W; ++i) o.v[i] = 0u;
+  if (!in) return;
+  if (vec) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) o.v[j * W + i] = 0u;
-    if (j >= words) continue;
-    if (vec) {
-#pragma unroll
-      for (int i = 0; i < W; i += 4) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(p + j * 8 * T::BYTES) + i / 4);
-        o.v[j * W + i] = q.x;
-        o.v[j * W + i + 1] = q.y;
-        o.v[j * W + i + 2] = q.z;
-        o.v[j * W + i + 3] = q.w;
-      }
-    } else if (T::BYTES == 4) {
-#pragma unroll
-      for (int i = 0; i < W; ++i) o.v[j * W + i] = __ldg(reinterpret_cast<const uint32_t*>(p) + j * 8 + i);
-    } else {
-      const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + j * 8;
-#pragma unroll
-      for (int i = 0; i < W; ++i)
-        o.v[j * W + i] = (uint32_t)__ldg(q + 2 * i) | (uint32_t)__ldg(q + 2 * i + 1) << 16;
+    for (int i = 0; i < W; i += 4) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+      o.v[i] = q.x, o.v[i + 1] = q.y, o.v[i + 2] = q.z, o.v[i + 3] = q.w;
     }
+  } else if (T::BYTES == 4) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) o.v[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+  } else {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      o.v[i] = (uint32_t)__ldg(q + 2 * i) | (uint32_t)__ldg(q + 2 * i + 1) << 16;
   }
 }
 // the B registers of word j, TERMS sets of four pairs
@@ -241,87 +246,102 @@ __device__ __forceinline__ void load_codes(CodeWords<CH>& o, const uint8_t* p, b
   }
 }
 
-__device__ __forceinline__ float w4_scale(const W4Args& p, const W4Fast& w, int64_t u) {
-  if (p.dbl)  // within an ulp of (q / 255) * super
-    return __fmul_rn((float)__ldg(static_cast<const uint8_t*>(w.scales) + u), 1.0f / 255.0f) *
-           __ldg(w.super + (u >> 8));
-  return __ldg(static_cast<const float*>(w.scales) + u);
-}
 // 136 + zp as a bf16 pair (exact)
-__device__ __forceinline__ uint32_t w4_bias(const W4Fast& w, int64_t u) {
-  if (!w.zp) return 0x43084308u;
-  const uint32_t h = 0x4308u + (uint32_t)min(max(__ldg(w.zp + u), -8), 7);
+__device__ __forceinline__ uint32_t w4_bias(int zp) {
+  const uint32_t h = 0x4308u + (uint32_t)min(max(zp, -8), 7);
   return h | h << 16;
 }
 
+// Row tiles of a warp and the warps that share a block of k: with more tokens
+// the warps of a CTA sit side by side along the rows, so that they read the
+// same x from L1.
+template <int NT, int NW>
+struct W4Shape {
+  static constexpr int R = NW == 2 && NT == 4 ? 1 : 2;  // row tiles of each weight
+  static constexpr int RT = R * NW;
+  static constexpr int WR = NT;              // warps along the rows
+  static constexpr int WK = kW4Warps / WR;   // warps along k
+  static constexpr int kRows = 16 * R * WR;  // output rows of a CTA
+};
+
 template <typename T, int TERMS, int CH, int NT, int NW>
-__global__ void __launch_bounds__(kW4Warps * 32, NT == 1 && NW == 1 ? 2 : 1) k_w4(const W4Args p) {
-  constexpr int R = NW == 2 && NT == 4 ? 1 : 2;  // row tiles of each weight
-  constexpr int RT = R * NW, kRowsOut = 16 * R, kTok = 8 * NT;
-  __shared__ float red[kW4Warps][RT * 16][kTok];
+__global__ void __launch_bounds__(kW4Warps * 32, NT == 1 && NW == 1 ? 2 : 1)
+    k_w4(const __grid_constant__ W4Args p) {
+  using S = W4Shape<NT, NW>;
+  constexpr int R = S::R, RT = S::RT, kTok = 8 * NT, KB = 32 * CH;
+  __shared__ float red[S::WK][NW][S::kRows][kTok];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int wr = warp % S::WR, wk = warp / S::WR;
   const int split = p.split;
   const int rank = split > 1 ? (int)(blockIdx.x % split) : 0;
-  const int64_t n0 = (int64_t)(blockIdx.x / split) * kRowsOut;
+  const int64_t n0 = (int64_t)(blockIdx.x / split) * S::kRows;
   const int64_t tok0 = (int64_t)blockIdx.y * kTok;
-  constexpr int KB = 32 * CH;
-  const int64_t blocks = (p.cols + KB - 1) / KB;
-  const int64_t per_unit = p.unit >= p.cols ? blocks : p.unit / KB;
-  const int64_t step = (int64_t)kW4Warps * split;
-  const bool vec_x = p.cols % 8 == 0 && (reinterpret_cast<uint64_t>(p.x) & 15) == 0;
+  const int cols = p.cols, blocks = (cols + KB - 1) / KB, step = S::WK * split;
+  const bool vec_x = p.vec_x;
 
   // this lane's rows: g and g + 8 of each tile (rows past the end read row 0
   // and are dropped at the end)
   const uint8_t* cp[RT][2];
-  int64_t ru[R][2];
+  uint32_t ru[R][2];
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t n = n0 + r * 16 + h * 8 + g, m = n < p.rows ? n : 0;
-      ru[r][h] = m * p.row_units;
+      const int64_t n = n0 + (wr * R + r) * 16 + h * 8 + g, m = n < p.rows ? n : 0;
+      ru[r][h] = (uint32_t)(m * p.row_units);
 #pragma unroll
-      for (int w = 0; w < NW; ++w) cp[w * R + r][h] = p.w[w].codes + (m * p.cols) / 2;
+      for (int w = 0; w < NW; ++w) cp[w * R + r][h] = p.w[w].codes + ((m * cols) >> 1) + t * 4 * CH;
     }
+  const char* xp[NT];
+  bool xin[NT];
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    const int64_t tok = tok0 + q * 8 + g;
+    xin[q] = tok < p.tokens;
+    xp[q] = static_cast<const char*>(p.x) + ((xin[q] ? tok : 0) * cols + t * 8 * CH) * T::BYTES;
+  }
 
   float total[RT][NT][4] = {};
   CodeWords<CH> next[RT][2];
-  const auto fetch = [&](int64_t kb) {
-    const int64_t k = kb * KB + t * 8 * CH;
-    const bool in = kb < blocks && k < p.cols;
+  const auto fetch = [&](int kb) {
+    const bool in = kb * KB + t * 8 * CH < cols;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) load_codes<CH>(next[i][h], cp[i][h] + k / 2, in);
+      for (int h = 0; h < 2; ++h) load_codes<CH>(next[i][h], cp[i][h] + kb * (KB / 2), in);
   };
-  int64_t kb = (int64_t)rank * kW4Warps + warp;
+  int kb = rank * S::WK + wk;
   fetch(kb);
+#pragma unroll 1
   for (; kb < blocks; kb += step) {
     CodeWords<CH> now[RT][2];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) now[i][h] = next[i][h];
-    const int64_t k = kb * KB + t * 8 * CH;
-    const int words = k < p.cols ? (int)min((int64_t)CH, (p.cols - k) / 8) : 0;
+    const bool in = kb * KB + t * 8 * CH < cols;
     XWords<T, CH> xw[NT];
 #pragma unroll
-    for (int q = 0; q < NT; ++q) {
-      const int64_t tok = tok0 + q * 8 + g;
-      load_x<T, CH>(xw[q], p.x, tok * p.cols + k, tok < p.tokens ? words : 0, vec_x);
-    }
+    for (int q = 0; q < NT; ++q)
+      load_x<T, CH>(xw[q], xp[q] + (int64_t)kb * (KB * T::BYTES), in && xin[q], vec_x);
     fetch(kb + step);
-    const int64_t u = kb / per_unit;
+    const uint32_t u = p.unit_magic ? __umulhi((uint32_t)kb, p.unit_magic) : 0u;
     float sc[RT][2];
     uint32_t bias[RT][2];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        sc[i][h] = w4_scale(p, p.w[i / R], ru[i % R][h] + u);
-        bias[i][h] = w4_bias(p.w[i / R], ru[i % R][h] + u);
+        const W4Fast& w = p.w[i / R];
+        const uint32_t at = ru[i % R][h] + (p.unit_magic == 1 ? (uint32_t)kb : u);
+        if (p.dbl)  // within an ulp of (q / 255) * super
+          sc[i][h] = (float)__ldg(static_cast<const uint8_t*>(w.scales) + at) * (1.0f / 255.0f) *
+                     __ldg(w.super + (at >> 8));
+        else
+          sc[i][h] = __ldg(static_cast<const float*>(w.scales) + at);
+        bias[i][h] = w.zp ? w4_bias(__ldg(w.zp + at)) : 0x43084308u;
       }
-    float part[RT][NT][4] = {};
+    float part[RT][NT][4];
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       uint32_t b[NT][TERMS][4];
@@ -338,7 +358,10 @@ __global__ void __launch_bounds__(kW4Warps * 32, NT == 1 && NW == 1 ? 2 : 1) k_w
         for (int q = 0; q < NT; ++q)
 #pragma unroll
           for (int m = TERMS - 1; m >= 0; --m) {
-            mma_16816(part[i][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m][0], b[q][m][1]);
+            if (j == 0 && m == TERMS - 1)
+              mma_16816_first(part[i][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m][0], b[q][m][1]);
+            else
+              mma_16816(part[i][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m][0], b[q][m][1]);
             mma_16816(part[i][q], a[0][2], a[1][2], a[0][3], a[1][3], b[q][m][2], b[q][m][3]);
           }
       }
@@ -357,35 +380,37 @@ __global__ void __launch_bounds__(kW4Warps * 32, NT == 1 && NW == 1 ? 2 : 1) k_w
     for (int q = 0; q < NT; ++q)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float2*>(&red[warp][i * 16 + h * 8 + g][q * 8 + 2 * t]) =
+        *reinterpret_cast<float2*>(
+            &red[wk][i / R][(wr * R + i % R) * 16 + h * 8 + g][q * 8 + 2 * t]) =
             make_float2(total[i][q][2 * h], total[i][q][2 * h + 1]);
   __syncthreads();
   const int tokens = (int)min((int64_t)kTok, p.tokens - tok0);
   // this CTA's sums over its warps, in red[0]
-  for (int i = threadIdx.x; i < RT * 16 * tokens; i += kW4Warps * 32) {
-    const int r = i % (RT * 16), c = i / (RT * 16);
-    float v = red[0][r][c];
+  for (int i = threadIdx.x; i < NW * S::kRows * tokens; i += kW4Warps * 32) {
+    const int r = i % (NW * S::kRows), c = i / (NW * S::kRows);
+    float* at = &red[0][0][r][c];
+    float v = *at;
 #pragma unroll
-    for (int w = 1; w < kW4Warps; ++w) v += red[w][r][c];
-    red[0][r][c] = v;
+    for (int w = 1; w < S::WK; ++w) v += at[w * NW * S::kRows * kTok];
+    *at = v;
   }
   if (split > 1)
     tc::cluster_sync();
   else
     __syncthreads();
-  for (int i = threadIdx.x + rank * kW4Warps * 32; i < kRowsOut * tokens;
+  for (int i = threadIdx.x + rank * kW4Warps * 32; i < S::kRows * tokens;
        i += kW4Warps * 32 * split) {
-    const int r = i % kRowsOut, c = i / kRowsOut;
+    const int r = i % S::kRows, c = i / S::kRows;
     if (n0 + r >= p.rows) continue;
     float v = 0.0f, u = 0.0f;
     if (split > 1) {
       for (int q = 0; q < split; ++q) {
-        v += tc::ld_cluster(tc::map_rank(tc::smem(&red[0][r][c]), q));
-        if (NW == 2) u += tc::ld_cluster(tc::map_rank(tc::smem(&red[0][RT * 16 / 2 + r][c]), q));
+        v += tc::ld_cluster(tc::map_rank(tc::smem(&red[0][0][r][c]), q));
+        if (NW == 2) u += tc::ld_cluster(tc::map_rank(tc::smem(&red[0][NW - 1][r][c]), q));
       }
     } else {
-      v = red[0][r][c];
-      if (NW == 2) u = red[0][RT * 16 / 2 + r][c];
+      v = red[0][0][r][c];
+      if (NW == 2) u = red[0][NW - 1][r][c];
     }
     if (NW == 2) v = act_value(p.act, v) * u;
     const int64_t at = (tok0 + c) * p.rows + n0 + r;
@@ -399,14 +424,20 @@ __global__ void __launch_bounds__(kW4Warps * 32, NT == 1 && NW == 1 ? 2 : 1) k_w
 
 template <typename T, int TERMS, int CH, int NT, int NW>
 static qat_status launch_fast(W4Args p, cudaStream_t s) {
-  constexpr int R = NW == 2 && NT == 4 ? 1 : 2;
-  const int64_t row_blocks = (p.rows + 16 * R - 1) / (16 * R);
-  const int64_t kblocks = (p.cols + 32 * CH - 1) / (32 * CH);
+  using S = W4Shape<NT, NW>;
+  const int64_t row_blocks = (p.rows + S::kRows - 1) / S::kRows;
+  const int kblocks = (p.cols + 32 * CH - 1) / (32 * CH);
+  // units of a row: none (whole rows), one a block, or kb / per_unit by
+  // multiplication (exact while blocks^2 < 2^32)
+  const int64_t per_unit = p.unit / (32 * CH);
+  p.unit_magic = p.unit >= p.cols ? 0u
+                 : per_unit == 1  ? 1u
+                                  : (uint32_t)((UINT64_C(1) << 32) / per_unit + 1);
   // a cluster splits k while two CTAs a SM are not reached and every warp keeps
   // a block
   p.split = 1;
   const int64_t room = (int64_t)device_info().sms * 2;
-  while (p.split < 8 && row_blocks * p.split * 2 <= room && kblocks >= p.split * 2 * kW4Warps)
+  while (p.split < 8 && row_blocks * p.split * 2 <= room && kblocks >= p.split * 2 * S::WK)
     p.split *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(row_blocks * p.split), (unsigned)((p.tokens + 8 * NT - 1) / (8 * NT)));
@@ -440,9 +471,12 @@ static qat_status fast_chunk(const W4Args& p, int ch, cudaStream_t s) {
 }
 
 // Words of 8 codes a lane takes at once: the widest load that rows, units and
-// blocks of k allow; 0 when the shape needs the generic kernel.
+// blocks of k allow; 0 when the shape needs the generic kernel (longer rows and
+// more units than the 32-bit indexes hold too).
 static int w4_chunk(const qat_weight4& w) {
-  if (w.cols % 8) return 0;
+  if (w.cols % 8 || w.cols > (1 << 20) || w.rows > (1 << 30)) return 0;
+  if (w.layout != QAT_PER_TENSOR && w.layout != QAT_PER_ROW && w.rows * w.cols >= (INT64_C(1) << 36))
+    return 0;
   if (w.layout == QAT_PER_TENSOR || w.layout == QAT_PER_ROW)
     return w.cols % 32 == 0 ? 4 : w.cols % 16 == 0 ? 2 : 1;
   const int64_t unit = w.layout == QAT_W4_DOUBLE ? 64 : w.group;
@@ -460,8 +494,9 @@ static qat_status launch_w4_fast(const void* x, qat_dtype xdt, int64_t tokens,
   p.x = x;
   p.y = y;
   p.rows = w->rows;
-  p.cols = w->cols;
+  p.cols = (int)w->cols;
   p.tokens = tokens;
+  p.vec_x = w->cols % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0;
   p.dbl = w->layout == QAT_W4_DOUBLE;
   p.unit = w->layout == QAT_PER_GROUP ? w->group : p.dbl ? 64 : w->cols;
   p.row_units = w->layout == QAT_PER_TENSOR ? 0 : w->cols / p.unit;
