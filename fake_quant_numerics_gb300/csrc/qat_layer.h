@@ -15,8 +15,12 @@ qat_status launch_w4(const void* x, qat_dtype xdt, int64_t tokens, const qat_wei
                      int act, void* y, qat_dtype ydt, cudaStream_t s);
 
 // Row partials of dweight / dbias that the layer norm's backward pass keeps in
-// its workspace: [2][parts][cols] floats, parts at most kNormMaxParts.
-constexpr int kNormMaxParts = 320;
+// its workspace: [2][parts][cols] floats.  Enough parts for every resident
+// block: eight 128-thread blocks a SM for short rows, four from there on.
+constexpr int norm_parts(int64_t rows, int64_t cols) {
+  const int most = cols <= 1024 ? 1216 : 608;
+  return rows < most ? (int)rows : most;
+}
 qat_status launch_norm_fwd(const void* x, qat_dtype dt, int64_t rows, int64_t cols, const void* w,
                            const void* b, float eps, void* y, float* mean, float* rstd,
                            cudaStream_t s);

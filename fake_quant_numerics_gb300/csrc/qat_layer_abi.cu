@@ -158,7 +158,7 @@ qat_status qat_layer_norm(const void* x, qat_dtype dtype, int64_t rows, int64_t 
 
 size_t qat_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
   if (!fits(rows, cols)) return 0;
-  return (size_t)(rows < kNormMaxParts ? rows : kNormMaxParts) * (size_t)cols * 8;
+  return (size_t)norm_parts(rows, cols) * (size_t)cols * 8;
 }
 
 qat_status qat_layer_norm_backward(const void* dy, const void* x, qat_dtype dtype, int64_t rows,

@@ -17,7 +17,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib
-from ._lib import (GELU, PER_COLUMN, PER_GROUP, PER_ROW, PER_TENSOR, RELU, SILU, W4_DOUBLE, QatError)
+from ._lib import (F32, GELU, PER_COLUMN, PER_GROUP, PER_ROW, PER_TENSOR, RELU, SILU, W4_DOUBLE, QatError)
 from .api import _GRAN, _dt, _nbytes, _p, _ready, _s, DoubleQuantized4Bit
 
 _ACT = {"silu": SILU, "gelu": GELU, "relu": RELU, SILU: SILU, GELU: GELU, RELU: RELU}
@@ -27,8 +27,21 @@ def _mismatch(what: str) -> QatError:
     return QatError(what, _lib.QAT_ERR_DIMENSION_MISMATCH)
 
 
-def _flat(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
-    return None if t is None else t.contiguous()
+def _ptr(t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError("libqat takes CUDA tensors only")
+    return t.data_ptr()
+
+
+def _here(t: torch.Tensor) -> int:
+    """The current stream of t's device (the raw handle: the calls here are short,
+    and a Stream object costs as much as the launch)."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _leading(t: torch.Tensor, shape) -> int:
+    """Rows of t seen as [rows, last dimension]."""
+    return t.numel() // shape[-1] if shape[-1] else shape[:-1].numel()
 
 
 def _of_type(like: torch.Tensor, *tensors: Optional[torch.Tensor]):
@@ -45,27 +58,19 @@ def _of_type(like: torch.Tensor, *tensors: Optional[torch.Tensor]):
 # ---------------------------------------------------------------------------
 # products with 4-bit weights
 # ---------------------------------------------------------------------------
-class Weight4(NamedTuple):
-    """A [rows, cols] weight as packed 4-bit codes (see :func:`weight4`)."""
-    codes: torch.Tensor
-    scale: torch.Tensor
-    zero_point: Optional[torch.Tensor]
-    super_scales: Optional[torch.Tensor]
-    rows: int
-    cols: int
-    layout: int
-    group: int
+class Weight4:
+    """A [rows, cols] weight as packed 4-bit codes (see :func:`weight4`).  It holds
+    its tensors and the qat_weight4 of their addresses: do not change them."""
 
-    def struct(self) -> "_lib.Weight4Struct":
-        """qat_weight4; it holds addresses only, so keep this Weight4 alive."""
-        for t in (self.codes, self.scale, self.zero_point, self.super_scales):
-            if t is not None and not t.is_cuda:
-                raise ValueError("libqat takes CUDA tensors only")
-        return _lib.Weight4Struct(
-            self.codes.data_ptr(), self.scale.data_ptr(),
-            None if self.zero_point is None else self.zero_point.data_ptr(),
-            None if self.super_scales is None else self.super_scales.data_ptr(),
-            self.rows, self.cols, self.group, self.layout)
+    __slots__ = ("codes", "scale", "zero_point", "super_scales", "rows", "cols", "layout", "group",
+                 "struct")
+
+    def __init__(self, codes, scale, zero_point, super_scales, rows, cols, layout, group):
+        self.codes, self.scale, self.zero_point, self.super_scales = codes, scale, zero_point, super_scales
+        self.rows, self.cols, self.layout, self.group = rows, cols, layout, group
+        self.struct = _lib.Weight4Struct(
+            codes.data_ptr(), scale.data_ptr(), None if zero_point is None else zero_point.data_ptr(),
+            None if super_scales is None else super_scales.data_ptr(), rows, cols, group, layout)
 
 
 def weight4(codes: torch.Tensor, scale: torch.Tensor, rows: int, cols: int, granularity="group",
@@ -85,8 +90,9 @@ def weight4(codes: torch.Tensor, scale: torch.Tensor, rows: int, cols: int, gran
     if (codes.numel() != (rows * cols + 1) // 2 or scale.numel() != units
             or (zero_point is not None and zero_point.numel() != units)):
         raise _mismatch("weight4")
-    return Weight4(_ready(codes), scale.contiguous(), _flat(zero_point), None, rows, cols, layout,
-                   group if layout == PER_GROUP else 0)
+    return Weight4(_ready(codes), scale.contiguous(),
+                   None if zero_point is None else zero_point.contiguous(), None, rows, cols,
+                   layout, group if layout == PER_GROUP else 0)
 
 
 def weight4_double(dq: DoubleQuantized4Bit, rows: int, cols: int) -> Weight4:
@@ -97,13 +103,19 @@ def weight4_double(dq: DoubleQuantized4Bit, rows: int, cols: int) -> Weight4:
                    rows, cols, W4_DOUBLE, 0)
 
 
+def _w4(w: Weight4):
+    if not w.codes.is_cuda:
+        raise ValueError("libqat takes CUDA tensors only")
+    return w.struct
+
+
 def qat_linear4(x, tokens, w: Weight4, y, stream=None):
-    st = _lib.lib().qat_linear4(_p(x), _dt(x), tokens, w.struct(), _p(y), _dt(y), _s(stream))
+    st = _lib.lib().qat_linear4(_p(x), _dt(x), tokens, _w4(w), _p(y), _dt(y), _s(stream))
     _lib.check("qat_linear4", st)
 
 
 def qat_gated4(x, tokens, gate: Weight4, up: Weight4, act, h, stream=None):
-    st = _lib.lib().qat_gated4(_p(x), _dt(x), tokens, gate.struct(), up.struct(), _ACT[act], _p(h),
+    st = _lib.lib().qat_gated4(_p(x), _dt(x), tokens, _w4(gate), _w4(up), _ACT[act], _p(h),
                                _s(stream))
     _lib.check("qat_gated4", st)
 
@@ -111,12 +123,15 @@ def qat_gated4(x, tokens, gate: Weight4, up: Weight4, act, h, stream=None):
 def linear4(x: torch.Tensor, weight: Weight4) -> torch.Tensor:
     """x [..., cols] times the weight's transpose: [..., rows] in x's dtype
     (float32 or bfloat16).  For a few tokens (the weight is read once per 32)."""
-    if x.dim() == 0 or x.shape[-1] != weight.cols:
+    shape, cols = x.shape, weight.cols
+    if not shape or shape[-1] != cols:
         raise _mismatch("linear4")
     x = x.contiguous()
-    lead = x.shape[:-1]
-    y = torch.empty(*lead, weight.rows, dtype=x.dtype, device=x.device)
-    qat_linear4(x, lead.numel(), weight, y)
+    y = x.new_empty((*shape[:-1], weight.rows))
+    dt = _dt(x)
+    st = _lib.lib().qat_linear4(_ptr(x), dt, _leading(x, shape), _w4(weight), y.data_ptr(), dt, _here(x))
+    if st:
+        _lib.check("qat_linear4", st)
     return y
 
 
@@ -124,15 +139,20 @@ def gated_ffn4(x: torch.Tensor, gate: Weight4, up: Weight4, down: Weight4,
                activation="silu") -> torch.Tensor:
     """The gated feed-forward block from 4-bit codes: (act(x gate^T) * (x up^T)) down^T,
     the hidden values kept in float32."""
-    if x.dim() == 0 or x.shape[-1] != gate.cols or down.cols != gate.rows:
+    shape = x.shape
+    if not shape or shape[-1] != gate.cols or down.cols != gate.rows:
         raise _mismatch("gated_ffn4")
     x = x.contiguous()
-    lead = x.shape[:-1]
-    tokens = lead.numel()
-    h = torch.empty(tokens, gate.rows, dtype=torch.float32, device=x.device)
-    y = torch.empty(*lead, down.rows, dtype=x.dtype, device=x.device)
-    qat_gated4(x, tokens, gate, up, activation, h)
-    qat_linear4(h, tokens, down, y)
+    tokens = _leading(x, shape)
+    h = x.new_empty((tokens, gate.rows), dtype=torch.float32)
+    y = x.new_empty((*shape[:-1], down.rows))
+    lib, dt, stream, hp = _lib.lib(), _dt(x), _here(x), h.data_ptr()
+    st = lib.qat_gated4(_ptr(x), dt, tokens, _w4(gate), _w4(up), _ACT[activation], hp, stream)
+    if st:
+        _lib.check("qat_gated4", st)
+    st = lib.qat_linear4(hp, F32, tokens, _w4(down), y.data_ptr(), dt, stream)
+    if st:
+        _lib.check("qat_linear4", st)
     return y
 
 
@@ -177,11 +197,6 @@ def _ffn_sizes(what, x, w_gate, w_up, w_down):
     return x.shape[:-1].numel(), dim, hidden
 
 
-def _ffn_workspace(x, tokens, dim, hidden, backward):
-    n = qat_gated_ffn_workspace_bytes(_dt(x), tokens, dim, hidden, backward)
-    return torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
-
-
 def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
               activation="silu", save: bool = False) -> GatedFfn:
     """y = (act(x w_gate^T) * (x w_up^T)) w_down^T for x [..., dim], w_gate and w_up
@@ -189,14 +204,21 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     save=True keeps the pre-activations for gated_ffn_backward."""
     tokens, dim, hidden = _ffn_sizes("gated_ffn", x, w_gate, w_up, w_down)
     x, w_gate, w_up, w_down = x.contiguous(), w_gate.contiguous(), w_up.contiguous(), w_down.contiguous()
-    h = torch.empty(tokens, hidden, dtype=x.dtype, device=x.device)
+    h = x.new_empty((tokens, hidden))
     g = u = None
     if save:
-        g = torch.empty(tokens, hidden, dtype=torch.float32, device=x.device)
+        g = x.new_empty((tokens, hidden), dtype=torch.float32)
         u = torch.empty_like(g)
     y = torch.empty_like(x)
-    qat_gated_ffn(x, tokens, dim, hidden, w_gate, w_up, w_down, activation, h, g, u, y, None,
-                  _ffn_workspace(x, tokens, dim, hidden, False))
+    lib, dt = _lib.lib(), _dt(x)
+    n = lib.qat_gated_ffn_workspace_bytes(dt, tokens, dim, hidden, 0)
+    ws = x.new_empty((n,), dtype=torch.uint8)
+    st = lib.qat_gated_ffn(_ptr(x), dt, tokens, dim, hidden, w_gate.data_ptr(), w_up.data_ptr(),
+                           w_down.data_ptr(), _ACT[activation], h.data_ptr(),
+                           g.data_ptr() if save else None, u.data_ptr() if save else None,
+                           y.data_ptr(), None, ws.data_ptr() if n else None, n, _here(x))
+    if st:
+        _lib.check("qat_gated_ffn", st)
     return GatedFfn(y, h, g, u)
 
 
@@ -206,21 +228,31 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
     """(dx, dw_gate, dw_up, dw_down) of gated_ffn(..., save=True), in x's dtype; None
     for what is not wanted."""
     tokens, dim, hidden = _ffn_sizes("gated_ffn_backward", x, w_gate, w_up, w_down)
-    if saved.gate_pre is None or saved.up_pre is None:
+    h, g, u = saved.h, saved.gate_pre, saved.up_pre
+    if g is None or u is None:
         raise ValueError("gated_ffn_backward needs the pre-activations of gated_ffn(save=True)")
-    if dy.shape != x.shape or any(tuple(t.shape) != (tokens, hidden)
-                                  for t in (saved.h, saved.gate_pre, saved.up_pre)):
+    if dy.shape != x.shape or any(t.shape != (tokens, hidden) for t in (h, g, u)):
         raise _mismatch("gated_ffn_backward")
-    _of_type(x, dy, saved.h)
-    dy, x = dy.contiguous(), x.contiguous()
+    _of_type(x, dy, h)
+    if g.dtype != torch.float32 or u.dtype != torch.float32:
+        raise TypeError("the saved pre-activations are float32")
+    dy, x, h, g, u = dy.contiguous(), x.contiguous(), h.contiguous(), g.contiguous(), u.contiguous()
     w_gate, w_up, w_down = w_gate.contiguous(), w_up.contiguous(), w_down.contiguous()
     dx = torch.empty_like(x) if want_dx else None
     dwg = dwu = dwd = None
     if want_dw:
         dwg, dwu, dwd = torch.empty_like(w_gate), torch.empty_like(w_up), torch.empty_like(w_down)
-    qat_gated_ffn_backward(dy, x, tokens, dim, hidden, w_gate, w_up, w_down, activation, saved.h,
-                           saved.gate_pre, saved.up_pre, dx, dwg, dwu, dwd, None,
-                           _ffn_workspace(x, tokens, dim, hidden, True))
+    lib, dt = _lib.lib(), _dt(x)
+    n = lib.qat_gated_ffn_workspace_bytes(dt, tokens, dim, hidden, 1)
+    ws = x.new_empty((n,), dtype=torch.uint8)
+    st = lib.qat_gated_ffn_backward(
+        _ptr(dy), _ptr(x), dt, tokens, dim, hidden, w_gate.data_ptr(), w_up.data_ptr(),
+        w_down.data_ptr(), _ACT[activation], h.data_ptr(), g.data_ptr(), u.data_ptr(),
+        dx.data_ptr() if want_dx else None, dwg.data_ptr() if want_dw else None,
+        dwu.data_ptr() if want_dw else None, dwd.data_ptr() if want_dw else None, None,
+        ws.data_ptr() if n else None, n, _here(x))
+    if st:
+        _lib.check("qat_gated_ffn_backward", st)
     return dx, dwg, dwu, dwd
 
 
@@ -274,43 +306,69 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
                bias: Optional[torch.Tensor] = None, eps: float = 1e-5) -> LayerNorm:
     """Layer norm of x [..., cols] over its last dimension, with the rows' mean and
     rstd (float32) for the backward pass."""
-    if x.dim() == 0:
+    shape = x.shape
+    if not shape:
         raise _mismatch("layer_norm")
-    cols = x.shape[-1]
-    if any(t is not None and tuple(t.shape) != (cols,) for t in (weight, bias)):
-        raise _mismatch("layer_norm")
-    _of_type(x, weight, bias)
-    x, weight, bias = x.contiguous(), _flat(weight), _flat(bias)
-    lead = x.shape[:-1]
+    x = x.contiguous()
+    wp = bp = None
+    if weight is not None:
+        weight = _vector("layer_norm", x, weight, shape[-1])
+        wp = weight.data_ptr()
+    if bias is not None:
+        bias = _vector("layer_norm", x, bias, shape[-1])
+        bp = bias.data_ptr()
     y = torch.empty_like(x)
-    mean = torch.empty(lead, dtype=torch.float32, device=x.device)
-    rstd = torch.empty_like(mean)
-    qat_layer_norm(x, lead.numel(), cols, weight, bias, eps, y, mean, rstd)
+    stats = x.new_empty((2, *shape[:-1]), dtype=torch.float32)
+    mean, rstd = stats.unbind()
+    st = _lib.lib().qat_layer_norm(_ptr(x), _dt(x), _leading(x, shape), shape[-1], wp, bp, eps,
+                                   y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _here(x))
+    if st:
+        _lib.check("qat_layer_norm", st)
     return LayerNorm(y, mean, rstd)
+
+
+def _vector(what, x, v, cols):
+    if v.shape != (cols,):
+        raise _mismatch(what)
+    if v.dtype != x.dtype or v.device != x.device:
+        _of_type(x, v)
+    return v.contiguous()
 
 
 def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor],
                         mean: torch.Tensor, rstd: torch.Tensor, want_dx: bool = True,
                         want_dw: bool = True):
     """(dx, dweight, dbias) of layer_norm; None for what is not wanted."""
-    if x.dim() == 0 or dy.shape != x.shape:
+    shape = x.shape
+    if not shape or dy.shape != shape:
         raise _mismatch("layer_norm_backward")
-    cols, lead = x.shape[-1], x.shape[:-1]
-    rows = lead.numel()
-    if (weight is not None and tuple(weight.shape) != (cols,)) or mean.numel() != rows or rstd.numel() != rows:
+    cols = shape[-1]
+    rows = _leading(x, shape)
+    if mean.numel() != rows or rstd.numel() != rows:
         raise _mismatch("layer_norm_backward")
-    _of_type(x, dy, weight)
+    if dy.dtype != x.dtype or dy.device != x.device:
+        _of_type(x, dy)
     if mean.dtype != torch.float32 or rstd.dtype != torch.float32:
         raise TypeError("mean and rstd are float32")
-    dy, x, weight, mean, rstd = dy.contiguous(), x.contiguous(), _flat(weight), _flat(mean), _flat(rstd)
+    dy, x, mean, rstd = dy.contiguous(), x.contiguous(), mean.contiguous(), rstd.contiguous()
+    wp = None
+    if weight is not None:
+        weight = _vector("layer_norm_backward", x, weight, cols)
+        wp = weight.data_ptr()
+    lib = _lib.lib()
     dx = torch.empty_like(x) if want_dx else None
     dw = db = ws = None
+    n = 0
     if want_dw:
-        dw = torch.empty(cols, dtype=x.dtype, device=x.device)
-        db = torch.empty_like(dw)
-        n = qat_layer_norm_backward_workspace_bytes(rows, cols)
-        ws = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
-    qat_layer_norm_backward(dy, x, rows, cols, weight, mean, rstd, dx, dw, db, ws)
+        dw, db = x.new_empty((cols,)), x.new_empty((cols,))
+        n = lib.qat_layer_norm_backward_workspace_bytes(rows, cols)
+        ws = x.new_empty((n,), dtype=torch.uint8)
+    st = lib.qat_layer_norm_backward(
+        _ptr(dy), _ptr(x), _dt(x), rows, cols, wp, _ptr(mean), _ptr(rstd),
+        dx.data_ptr() if want_dx else None, dw.data_ptr() if want_dw else None,
+        db.data_ptr() if want_dw else None, ws.data_ptr() if n else None, n, _here(x))
+    if st:
+        _lib.check("qat_layer_norm_backward", st)
     return dx, dw, db
 
 
