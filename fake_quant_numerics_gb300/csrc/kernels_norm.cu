@@ -137,54 +137,55 @@ template <typename T, bool VEC>
 __device__ __forceinline__ Pair pair(const Raw8<T, VEC>& v, int e) {
   return Pair{v.get(2 * e), v.get(2 * e + 1)};
 }
-// the columns of chunk r of thread i: eight from col, `step` apart
-template <int W, bool VEC>
+// The columns of chunk q of thread i, eight of them: with vectors runs of 16
+// bytes, side by side for neighbouring threads (a 32-byte run would be fetched
+// as two half sectors); else one element at a time.
+template <typename T, int W, bool VEC>
 struct Cols {
-  int col;
-  static constexpr int step = VEC ? 1 : 32 * W;
-  __device__ __forceinline__ Cols(int r, int i) : col(VEC ? (r * 32 * W + i) * 8 : r * 256 * W + i) {}
-  __device__ __forceinline__ bool has(int e, int cols) const {
-    return VEC ? col < cols : col + e * step < cols;
-  }
+  static constexpr int kRun = VEC ? 16 / T::BYTES : 1;  // elements of a run
+  static constexpr int kRuns = 8 / kRun;
+  int first;
+  __device__ __forceinline__ Cols(int q, int i) : first(q * 256 * W + i * kRun) {}
+  __device__ __forceinline__ int at(int e) const { return first + e / kRun * (32 * W * kRun) + e % kRun; }
+  __device__ __forceinline__ bool has(int e, int cols) const { return at(e / kRun * kRun) < cols; }
 };
 template <typename T, int W, bool VEC>
 __device__ __forceinline__ void ld_cols(Raw8<T, VEC>& v, const void* p, int64_t base,
-                                        const Cols<W, VEC>& c, int cols) {
-  if constexpr (VEC) {
-    constexpr int N = Raw8<T, VEC>::kPacked ? 4 : 8;
-    const bool in = c.has(0, cols);
-    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) +
-                                                    (base + c.col) * T::BYTES);
+                                        const Cols<T, W, VEC>& c, int cols) {
+  using C = Cols<T, W, VEC>;
 #pragma unroll
-    for (int k = 0; k < N; k += 4) {
+  for (int k = 0; k < C::kRuns; ++k) {
+    const int64_t at = base + c.at(k * C::kRun);
+    const bool in = c.has(k * C::kRun, cols);
+    if constexpr (VEC) {
       uint4 u = make_uint4(0, 0, 0, 0);
-      if (in) u = q[k / 4];
-      v.w[k] = u.x, v.w[k + 1] = u.y, v.w[k + 2] = u.z, v.w[k + 3] = u.w;
+      if (in) u = *reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * T::BYTES);
+      v.w[4 * k] = u.x, v.w[4 * k + 1] = u.y, v.w[4 * k + 2] = u.z, v.w[4 * k + 3] = u.w;
+    } else {
+      v.w[k] = in ? load_elem_bits<T>(p, at) : 0u;
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v.w[e] = c.has(e, cols) ? load_elem_bits<T>(p, base + c.col + e * c.step) : 0u;
   }
 }
 template <typename T, int W, bool VEC>
-__device__ __forceinline__ void st_cols(void* p, int64_t base, const Cols<W, VEC>& c, int cols,
+__device__ __forceinline__ void st_cols(void* p, int64_t base, const Cols<T, W, VEC>& c, int cols,
                                         const Pair (&v)[4]) {
-  if constexpr (VEC) {
-    if (!c.has(0, cols)) return;
-    uint4* q = reinterpret_cast<uint4*>(static_cast<char*>(p) + (base + c.col) * T::BYTES);
-    if constexpr (T::BYTES == 2) {
-      q[0] = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
-                        pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
-    } else {
-      float4* f = reinterpret_cast<float4*>(q);
-      f[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-      f[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
-    }
-  } else {
+  using C = Cols<T, W, VEC>;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c.has(e, cols)) st_elem<T>(p, base + c.col + e * c.step, e & 1 ? v[e / 2].y : v[e / 2].x);
+  for (int k = 0; k < C::kRuns; ++k) {
+    const int64_t at = base + c.at(k * C::kRun);
+    if (!c.has(k * C::kRun, cols)) continue;
+    if constexpr (VEC) {
+      uint4 u;
+      if constexpr (T::BYTES == 2)
+        u = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                       pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+      else
+        u = make_uint4(__float_as_uint(v[2 * k].x), __float_as_uint(v[2 * k].y),
+                       __float_as_uint(v[2 * k + 1].x), __float_as_uint(v[2 * k + 1].y));
+      *reinterpret_cast<uint4*>(static_cast<char*>(p) + at * T::BYTES) = u;
+    } else {
+      st_elem<T>(p, at, k & 1 ? v[k / 2].y : v[k / 2].x);
+    }
   }
 }
 // sums over the W warps of a row, to every thread; red holds 2 W floats that the
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, W == 1 ? 4 : 32 / W)
   const int64_t base = r * cols;
   Raw8<T, VEC> v[R];
 #pragma unroll
-  for (int q = 0; q < R; ++q) ld_cols<T>(v[q], x, base, Cols<W, VEC>(q, i), cols);
+  for (int q = 0; q < R; ++q) ld_cols<T>(v[q], x, base, Cols<T, W, VEC>(q, i), cols);
   Pair s = {0.0f, 0.0f};
 #pragma unroll
   for (int q = 0; q < R; ++q)
@@ -240,20 +241,19 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, W == 1 ? 4 : 32 / W)
   Pair d2 = {0.0f, 0.0f};
 #pragma unroll
   for (int q = 0; q < R; ++q) {
-    const Cols<W, VEC> c(q, i);
-    if (VEC && !c.has(0, cols)) continue;
+    const Cols<T, W, VEC> c(q, i);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       Pair d = pair(v[q], e) - both(m);
-      if (!VEC && !c.has(2 * e, cols)) d.x = 0.0f;
-      if (!VEC && !c.has(2 * e + 1, cols)) d.y = 0.0f;
+      if (!c.has(2 * e, cols)) d.x = 0.0f;
+      if (!c.has(2 * e + 1, cols)) d.y = 0.0f;
       d2 = fma(d, d, d2);
     }
   }
   const float rs = 1.0f / sqrtf(row_sum2<W>(d2.x + d2.y, 0.0f, red[1]).x / (float)cols + eps);
 #pragma unroll
   for (int q = 0; q < R; ++q) {
-    const Cols<W, VEC> c(q, i);
+    const Cols<T, W, VEC> c(q, i);
     Raw8<T, VEC> g, h;
     if (w) ld_cols<T>(g, w, 0, c, cols);
     if (b) ld_cols<T>(h, b, 0, c, cols);
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, W == 1 ? 2 : 16 / W)
   constexpr int ST = NormBwd<T, R, VEC>::kStages;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float red[2][2 * W];
-  __shared__ float join[G == 1 ? 1 : G][G == 1 ? 1 : 256 * R];
+  __shared__ __align__(16) float join[G == 1 ? 1 : G][G == 1 ? 1 : 256 * R];
   const int i = W == 1 ? threadIdx.x & 31 : threadIdx.x;
   const int64_t first = (int64_t)blockIdx.x * G + (G == 1 ? 0 : threadIdx.x >> 5);
   const int64_t step = (int64_t)gridDim.x * G;
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, W == 1 ? 2 : 16 / W)
   Raw8<T, VEC> wv[R];
   if (w)
 #pragma unroll
-    for (int q = 0; q < R; ++q) ld_cols<T>(wv[q], w, 0, Cols<W, VEC>(q, i), cols);
+    for (int q = 0; q < R; ++q) ld_cols<T>(wv[q], w, 0, Cols<T, W, VEC>(q, i), cols);
   const float inv = 1.0f / (float)cols;
 
   // 16-byte pieces of a thread's slots lie NT * 16 bytes apart (no conflicts)
@@ -313,18 +313,18 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, W == 1 ? 2 : 16 / W)
     if (r < rows) {
 #pragma unroll
       for (int q = 0; q < R; ++q) {
-        const Cols<W, VEC> c(q, i);
-        if (!c.has(0, cols)) continue;
-        const int64_t at = (r * cols + c.col) * T::BYTES;
+        const Cols<T, W, VEC> c(q, i);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
+          if (!c.has(k * c.kRun, cols)) continue;
+          const int64_t at = (r * cols + c.at(k * c.kRun)) * T::BYTES;
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                            (uint32_t)__cvta_generic_to_shared(ring + piece(st, 0, q, k))),
-                       "l"(static_cast<const char*>(x) + at + k * 16)
+                       "l"(static_cast<const char*>(x) + at)
                        : "memory");
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                            (uint32_t)__cvta_generic_to_shared(ring + piece(st, 1, q, k))),
-                       "l"(static_cast<const char*>(dy) + at + k * 16)
+                       "l"(static_cast<const char*>(dy) + at)
                        : "memory");
         }
       }
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, W == 1 ? 2 : 16 / W)
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       uint4 u = make_uint4(0, 0, 0, 0);
-      if (Cols<W, VEC>(q, i).has(0, cols))
+      if (Cols<T, W, VEC>(q, i).has(k * (16 / T::BYTES), cols))
         u = *reinterpret_cast<const uint4*>(ring + piece(st, which, q, k));
       v.w[4 * k] = u.x, v.w[4 * k + 1] = u.y, v.w[4 * k + 2] = u.z, v.w[4 * k + 3] = u.w;
     }
@@ -373,8 +373,8 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, W == 1 ? 2 : 16 / W)
     } else {
 #pragma unroll
       for (int q = 0; q < R; ++q) {
-        ld_cols<T>(xv[q], x, base, Cols<W, VEC>(q, i), cols);
-        ld_cols<T>(gv[q], dy, base, Cols<W, VEC>(q, i), cols);
+        ld_cols<T>(xv[q], x, base, Cols<T, W, VEC>(q, i), cols);
+        ld_cols<T>(gv[q], dy, base, Cols<T, W, VEC>(q, i), cols);
       }
     }
     Pair z[R][4], p[R][4], s1 = {0.0f, 0.0f}, s2 = {0.0f, 0.0f};
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, W == 1 ? 2 : 16 / W)
       Pair o[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = both(rs) * fma(z[q][e], c2, p[q][e] - c1);
-      st_cols<T>(dx, base, Cols<W, VEC>(q, i), cols, o);
+      st_cols<T>(dx, base, Cols<T, W, VEC>(q, i), cols, o);
     }
   }
   pdl_trigger();
@@ -408,28 +408,25 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, W == 1 ? 2 : 16 / W)
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     float* out = ws + ((int64_t)half * gridDim.x + blockIdx.x) * cols;
-    if (G == 1) {
+    if (G > 1) __syncthreads();
+    float* to = G == 1 ? out : join[threadIdx.x >> 5];
 #pragma unroll
-      for (int q = 0; q < R; ++q) {
-        const Cols<W, VEC> c(q, i);
+    for (int q = 0; q < R; ++q) {
+      const Cols<T, W, VEC> c(q, i);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (c.has(e, cols)) {
-            const Pair v = half ? ab[q][e / 2] : aw[q][e / 2];
-            out[c.col + e * c.step] = e & 1 ? v.y : v.x;
-          }
-      }
-    } else {
-      __syncthreads();
-#pragma unroll
-      for (int q = 0; q < R; ++q) {
-        const Cols<W, VEC> c(q, i);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const Pair v = half ? ab[q][e / 2] : aw[q][e / 2];
-          join[threadIdx.x >> 5][c.col + e * c.step] = e & 1 ? v.y : v.x;
+      for (int e = 0; e < 4; e += VEC ? 2 : 1) {  // pairs
+        const Pair v = half ? ab[q][e] : aw[q][e];
+        if (VEC) {
+          const Pair u = half ? ab[q][e + 1] : aw[q][e + 1];
+          if (G > 1 || c.has(2 * e, cols))
+            *reinterpret_cast<float4*>(to + c.at(2 * e)) = make_float4(v.x, v.y, u.x, u.y);
+        } else {
+          if (G > 1 || c.has(2 * e, cols)) to[c.at(2 * e)] = v.x;
+          if (G > 1 || c.has(2 * e + 1, cols)) to[c.at(2 * e + 1)] = v.y;
         }
       }
+    }
+    if (G > 1) {
       __syncthreads();
       for (int c = threadIdx.x; c < cols; c += 256) {
         float v = join[0][c];
@@ -516,16 +513,26 @@ static qat_status norm_fwd(const void* x, int64_t rows, int64_t cols, const void
     QAT_FWD(1, 1);
   } else if (cols <= 512) {
     QAT_FWD(1, 2);
-  } else if (cols <= 1024) {
-    QAT_FWD(4, 1);
-  } else if (cols <= 2048) {
-    QAT_FWD(4, 2);
-  } else if (cols <= 4096) {
-    QAT_FWD(8, 2);
-  } else if (cols <= 8192) {
-    QAT_FWD(16, 2);
+  } else if constexpr (T::BYTES == 2) {  // 64 bytes of a row a thread
+    if (cols <= 1024)
+      QAT_FWD(1, 4);
+    else if (cols <= 2048)
+      QAT_FWD(2, 4);
+    else if (cols <= 4096)
+      QAT_FWD(4, 4);
+    else if (cols <= 8192)
+      QAT_FWD(8, 4);
+    else
+      QAT_FWD(16, 4);
   } else {
-    QAT_FWD(16, 4);
+    if (cols <= 2048)
+      QAT_FWD(4, 2);
+    else if (cols <= 4096)
+      QAT_FWD(8, 2);
+    else if (cols <= 8192)
+      QAT_FWD(16, 2);
+    else
+      QAT_FWD(16, 4);
   }
 #undef QAT_FWD
   count_launch(1);

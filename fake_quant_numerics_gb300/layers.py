@@ -127,7 +127,7 @@ def linear4(x: torch.Tensor, weight: Weight4) -> torch.Tensor:
     if not shape or shape[-1] != cols:
         raise _mismatch("linear4")
     x = x.contiguous()
-    y = x.new_empty((*shape[:-1], weight.rows))
+    y = torch.empty((*shape[:-1], weight.rows), dtype=x.dtype, device=x.device)
     dt = _dt(x)
     st = _lib.lib().qat_linear4(_ptr(x), dt, _leading(x, shape), _w4(weight), y.data_ptr(), dt, _here(x))
     if st:
@@ -144,8 +144,8 @@ def gated_ffn4(x: torch.Tensor, gate: Weight4, up: Weight4, down: Weight4,
         raise _mismatch("gated_ffn4")
     x = x.contiguous()
     tokens = _leading(x, shape)
-    h = x.new_empty((tokens, gate.rows), dtype=torch.float32)
-    y = x.new_empty((*shape[:-1], down.rows))
+    h = torch.empty((tokens, gate.rows), dtype=torch.float32, device=x.device)
+    y = torch.empty((*shape[:-1], down.rows), dtype=x.dtype, device=x.device)
     lib, dt, stream, hp = _lib.lib(), _dt(x), _here(x), h.data_ptr()
     st = lib.qat_gated4(_ptr(x), dt, tokens, _w4(gate), _w4(up), _ACT[activation], hp, stream)
     if st:
@@ -204,15 +204,15 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     save=True keeps the pre-activations for gated_ffn_backward."""
     tokens, dim, hidden = _ffn_sizes("gated_ffn", x, w_gate, w_up, w_down)
     x, w_gate, w_up, w_down = x.contiguous(), w_gate.contiguous(), w_up.contiguous(), w_down.contiguous()
-    h = x.new_empty((tokens, hidden))
+    h = torch.empty((tokens, hidden), dtype=x.dtype, device=x.device)
     g = u = None
     if save:
-        g = x.new_empty((tokens, hidden), dtype=torch.float32)
+        g = torch.empty((tokens, hidden), dtype=torch.float32, device=x.device)
         u = torch.empty_like(g)
     y = torch.empty_like(x)
     lib, dt = _lib.lib(), _dt(x)
     n = lib.qat_gated_ffn_workspace_bytes(dt, tokens, dim, hidden, 0)
-    ws = x.new_empty((n,), dtype=torch.uint8)
+    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
     st = lib.qat_gated_ffn(_ptr(x), dt, tokens, dim, hidden, w_gate.data_ptr(), w_up.data_ptr(),
                            w_down.data_ptr(), _ACT[activation], h.data_ptr(),
                            g.data_ptr() if save else None, u.data_ptr() if save else None,
@@ -244,7 +244,7 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
         dwg, dwu, dwd = torch.empty_like(w_gate), torch.empty_like(w_up), torch.empty_like(w_down)
     lib, dt = _lib.lib(), _dt(x)
     n = lib.qat_gated_ffn_workspace_bytes(dt, tokens, dim, hidden, 1)
-    ws = x.new_empty((n,), dtype=torch.uint8)
+    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
     st = lib.qat_gated_ffn_backward(
         _ptr(dy), _ptr(x), dt, tokens, dim, hidden, w_gate.data_ptr(), w_up.data_ptr(),
         w_down.data_ptr(), _ACT[activation], h.data_ptr(), g.data_ptr(), u.data_ptr(),
@@ -318,8 +318,9 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
         bias = _vector("layer_norm", x, bias, shape[-1])
         bp = bias.data_ptr()
     y = torch.empty_like(x)
-    stats = x.new_empty((2, *shape[:-1]), dtype=torch.float32)
-    mean, rstd = stats.unbind()
+    lead = shape[:-1]
+    mean = torch.empty(lead, dtype=torch.float32, device=x.device)
+    rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
     st = _lib.lib().qat_layer_norm(_ptr(x), _dt(x), _leading(x, shape), shape[-1], wp, bp, eps,
                                    y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _here(x))
     if st:
@@ -360,9 +361,10 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
     dw = db = ws = None
     n = 0
     if want_dw:
-        dw, db = x.new_empty((cols,)), x.new_empty((cols,))
+        dw = torch.empty(cols, dtype=x.dtype, device=x.device)
+        db = torch.empty(cols, dtype=x.dtype, device=x.device)
         n = lib.qat_layer_norm_backward_workspace_bytes(rows, cols)
-        ws = x.new_empty((n,), dtype=torch.uint8)
+        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
     st = lib.qat_layer_norm_backward(
         _ptr(dy), _ptr(x), _dt(x), rows, cols, wp, _ptr(mean), _ptr(rstd),
         dx.data_ptr() if want_dx else None, dw.data_ptr() if want_dw else None,
