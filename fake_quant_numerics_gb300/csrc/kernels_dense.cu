@@ -37,15 +37,14 @@ struct DenseArgs {
   CUtensorMap a[2], b[2];
   int64_t m, n;            // output size (gated: n = hidden)
   int mt, nt, problems;    // tiles of the output; outputs that share B
-  int kt, segs, parts;     // k steps of a segment; segments; operand parts (1, or 3: fp32)
+  int kt, segs;            // k steps of a segment; segments
   int split;               // CTAs of a cluster that share k (CG = 1)
   int act;
-  void* c[2];
-  int64_t ld;
+  void* c[2];              // outputs (gated: c[0] = h), rows of n
   float* gp;
   float* up;
-  void* dg;
-  void* du;
+  void* q[2];              // outputs kept as operands (bf16 parts): gated h
+  int64_t q_pitch, q_part;  // (nullable), gated backward dg and du
   int32_t* flags;
   uint32_t limit;
 };
@@ -100,6 +99,37 @@ __device__ __forceinline__ void ld_row32(const float* p, int64_t at, int left, u
     for (int i = 0; i < 32; ++i) v[i] = i < left ? p[at + i] : 0.0f;
   }
 }
+// 32 consecutive outputs as an operand of a later product
+template <typename T>
+__device__ __forceinline__ void st_parts32(const DenseArgs& p, int which, int64_t row, int64_t c,
+                                           int left, const float (&v)[32]) {
+  const int64_t at = row * p.q_pitch + c;
+  if constexpr (T::BYTES == 2) {
+    st_row32<BF16>(p.q[which], at, left, 16, v);
+  } else {
+    float r[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = v[i];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      float h[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) h[i] = take_bf16(r[i]);
+      st_row32<BF16>(p.q[which], at + k * p.q_part, left, 16, h);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void st_parts1(const DenseArgs& p, int which, int64_t row, int64_t c,
+                                          float v) {
+  const int64_t at = row * p.q_pitch + c;
+  if constexpr (T::BYTES == 2) {
+    st_elem<BF16>(p.q[which], at, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) st_elem<BF16>(p.q[which], at + k * p.q_part, take_bf16(v));
+  }
+}
 // the largest of 32, 16 or 1 that divides the address and the row pitch
 __device__ __forceinline__ uint32_t row_align(const void* p, int64_t pitch_bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(p) | (uint64_t)pitch_bytes;
@@ -110,23 +140,24 @@ __device__ __forceinline__ uint32_t row_align(const void* p, int64_t pitch_bytes
 template <typename T, int EPI>
 __device__ __forceinline__ void finish32(const DenseArgs& p, int prob, int64_t row, int64_t c,
                                          const float (&v)[32], const float (&u)[32]) {
-  const int64_t at = row * p.ld + c;
+  const int64_t at = row * p.n + c;
   const int left = (int)min((int64_t)32, p.n - c);
   if (EPI == kDenseStore) {
-    st_row32<T>(p.c[prob], at, left, row_align(p.c[prob], p.ld * T::BYTES), v);
+    st_row32<T>(p.c[prob], at, left, row_align(p.c[prob], p.n * T::BYTES), v);
   } else if (EPI == kDenseGated) {
     float h[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) h[i] = act_value(p.act, v[i]) * u[i];
-    st_row32<T>(p.c[0], at, left, row_align(p.c[0], p.ld * T::BYTES), h);
+    st_row32<T>(p.c[0], at, left, row_align(p.c[0], p.n * T::BYTES), h);
+    if (p.q[0]) st_parts32<T>(p, 0, row, c, left, h);
     if (p.gp) {
-      st_row32<F32>(p.gp, at, left, row_align(p.gp, p.ld * 4), v);
-      st_row32<F32>(p.up, at, left, row_align(p.up, p.ld * 4), u);
+      st_row32<F32>(p.gp, at, left, row_align(p.gp, p.n * 4), v);
+      st_row32<F32>(p.up, at, left, row_align(p.up, p.n * 4), u);
     }
   } else {
     float g[32], w[32], dg[32], du[32];
-    ld_row32(p.gp, at, left, row_align(p.gp, p.ld * 4), g);
-    ld_row32(p.up, at, left, row_align(p.up, p.ld * 4), w);
+    ld_row32(p.gp, at, left, row_align(p.gp, p.n * 4), g);
+    ld_row32(p.up, at, left, row_align(p.up, p.n * 4), w);
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       float a, da;
@@ -134,19 +165,21 @@ __device__ __forceinline__ void finish32(const DenseArgs& p, int prob, int64_t r
       dg[i] = v[i] * w[i] * da;
       du[i] = v[i] * a;
     }
-    st_row32<T>(p.dg, at, left, row_align(p.dg, p.ld * T::BYTES), dg);
-    st_row32<T>(p.du, at, left, row_align(p.du, p.ld * T::BYTES), du);
+    st_parts32<T>(p, 0, row, c, left, dg);
+    st_parts32<T>(p, 1, row, c, left, du);
   }
 }
 // The same for one element.
 template <typename T, int EPI>
 __device__ __forceinline__ void finish1(const DenseArgs& p, int prob, int64_t row, int64_t c,
                                         float v, float u) {
-  const int64_t at = row * p.ld + c;
+  const int64_t at = row * p.n + c;
   if (EPI == kDenseStore) {
     st_elem<T>(p.c[prob], at, v);
   } else if (EPI == kDenseGated) {
-    st_elem<T>(p.c[0], at, act_value(p.act, v) * u);
+    const float h = act_value(p.act, v) * u;
+    st_elem<T>(p.c[0], at, h);
+    if (p.q[0]) st_parts1<T>(p, 0, row, c, h);
     if (p.gp) {
       p.gp[at] = v;
       p.up[at] = u;
@@ -154,8 +187,8 @@ __device__ __forceinline__ void finish1(const DenseArgs& p, int prob, int64_t ro
   } else {
     float a, da;
     act_grad(p.act, p.gp[at], a, da);
-    st_elem<T>(p.dg, at, v * p.up[at] * da);
-    st_elem<T>(p.du, at, v * a);
+    st_parts1<T>(p, 0, row, c, v * p.up[at] * da);
+    st_parts1<T>(p, 1, row, c, v * a);
   }
 }
 
@@ -180,10 +213,25 @@ __device__ __forceinline__ Tile tile_at(const DenseArgs& p, int64_t t) {
   return r;
 }
 
-// fp32 operands are held as three bf16 parts (high, middle, low); the six
-// products that reach 2^-24 of the whole, smallest first
+// fp32 operands are held as three bf16 parts (high, middle, low: all 24 bits);
+// the six products that reach 2^-24 of the whole, smallest first.  The tensor
+// cores round their binary32 sums toward zero, which would cost a few digits
+// over a long k, so fp32 products are summed there over 256 k only and then in
+// registers.
 __device__ __constant__ const uint8_t kPairA[6] = {2, 0, 1, 1, 0, 0};
 __device__ __constant__ const uint8_t kPairB[6] = {0, 2, 1, 0, 1, 0};
+constexpr int kChunk = 4;  // k steps of such a sum
+
+// The k work of a segment in units: one step, or for fp32 one chunk of up to
+// four steps for each of the six pairs.
+template <typename T>
+struct Units {
+  static constexpr bool kParts = T::BYTES == 4;
+  __host__ __device__ static int per_segment(int kt) { return kParts ? (kt + kChunk - 1) / kChunk : kt; }
+  __device__ static int steps(int kt, int in_seg) {
+    return kParts ? 6 * min(kChunk, kt - in_seg * kChunk) : 1;
+  }
+};
 
 template <typename T, int CG, int EPI, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constant__ DenseArgs p) {
@@ -229,11 +277,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
   tc::fence_after();
   const uint32_t tmem = tmem_slot;
 
-  const int npairs = p.parts == 1 ? 1 : 6;
-  const int steps_all = p.segs * npairs * p.kt;
-  // this CTA's k steps
-  const int s0 = CG == 1 ? (int)((int64_t)steps_all * rank / p.split) : 0;
-  const int s1 = CG == 1 ? (int)((int64_t)steps_all * (rank + 1) / p.split) : steps_all;
+  using U = Units<T>;
+  const int per_seg = U::per_segment(p.kt), units = p.segs * per_seg;
+  // this CTA's share of them
+  const int u0 = CG == 1 ? (int)((int64_t)units * rank / p.split) : 0;
+  const int u1 = CG == 1 ? (int)((int64_t)units * (rank + 1) / p.split) : units;
   const int64_t tiles = (int64_t)p.mt * p.nt * p.problems;
   const int per_cluster = CG == 2 ? 2 : p.split;
   const int64_t first = blockIdx.x / per_cluster, stride = gridDim.x / per_cluster;
@@ -248,41 +296,46 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
         const Tile w = tile_at<CG, EPI>(p, t);
         const int am = (int)(w.m0 + (CG == 2 ? (int64_t)rank * kRows : 0));
         const int bn = (int)(w.n0 + (CG == 2 && EPI != kDenseGated ? (int64_t)rank * kRows : 0));
-        for (int s = s0; s < s1; ++s) {
-          ok = tc::bar_wait(empty(stage), phase, &abort_flag, p.limit);
-          if (!ok) break;
-          const int seg = s / (npairs * p.kt), r = s - seg * npairs * p.kt;
-          const int pr = r / p.kt, k0 = (r - pr * p.kt) * kBK;
-          const int pa = npairs == 1 ? 0 : kPairA[pr], pb = npairs == 1 ? 0 : kPairB[pr];
-          const uint32_t sa = base + stage * kStageBytes, sb = sa + kOpBytes;
-          uint32_t bar = full(stage);
-          if (leader) tc::bar_expect(bar, kStageBytes * CG);
-          if (CG == 2) bar = tc::map_rank(bar, 0);
-          const CUtensorMap* ma = &p.a[p.problems > 1 ? w.prob : seg];
-          if (A_MN) {
-            tc::load_box<CG == 2>(ma, sa, bar, am, k0, pa);
-            tc::load_box<CG == 2>(ma, sa + kOpBytes / 2, bar, am + 64, k0, pa);
-          } else {
-            tc::load_box<CG == 2>(ma, sa, bar, k0, am, pa);
-          }
-          if (EPI == kDenseGated) {
-            // gate rows then up rows; a pair's CTAs hold one each
-            if (CG == 2) {
-              tc::load_box<true>(&p.b[rank], sb, bar, k0, bn, pb);
+        for (int un = u0; ok && un < u1; ++un) {
+          const int seg = un / per_seg, in_seg = un - seg * per_seg;
+          const int steps = U::steps(p.kt, in_seg);
+          for (int st = 0; st < steps; ++st) {
+            ok = tc::bar_wait(empty(stage), phase, &abort_flag, p.limit);
+            if (!ok) break;
+            const int nk = steps / 6;
+            const int pr = U::kParts ? st / nk : 0;
+            const int k0 = (U::kParts ? in_seg * kChunk + st - pr * nk : in_seg) * kBK;
+            const int pa = U::kParts ? kPairA[pr] : 0, pb = U::kParts ? kPairB[pr] : 0;
+            const uint32_t sa = base + stage * kStageBytes, sb = sa + kOpBytes;
+            uint32_t bar = full(stage);
+            if (leader) tc::bar_expect(bar, kStageBytes * CG);
+            if (CG == 2) bar = tc::map_rank(bar, 0);
+            const CUtensorMap* ma = &p.a[p.problems > 1 ? w.prob : seg];
+            if (A_MN) {
+              tc::load_box<CG == 2>(ma, sa, bar, am, k0, pa);
+              tc::load_box<CG == 2>(ma, sa + kOpBytes / 2, bar, am + 64, k0, pa);
             } else {
-              tc::load_box<false>(&p.b[0], sb, bar, k0, bn, pb);
-              tc::load_box<false>(&p.b[1], sb + kOpBytes / 2, bar, k0, bn, pb);
+              tc::load_box<CG == 2>(ma, sa, bar, k0, am, pa);
             }
-          } else if (B_MN) {
-            tc::load_box<CG == 2>(&p.b[seg], sb, bar, bn, k0, pb);
-            tc::load_box<CG == 2>(&p.b[seg], sb + kOpBytes / 2, bar, bn + 64, k0, pb);
-          } else {
-            tc::load_box<CG == 2>(&p.b[seg], sb, bar, k0, bn, pb);
-          }
-          ++issued;
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
+            if (EPI == kDenseGated) {
+              // gate rows then up rows; a pair's CTAs hold one each
+              if (CG == 2) {
+                tc::load_box<true>(&p.b[rank], sb, bar, k0, bn, pb);
+              } else {
+                tc::load_box<false>(&p.b[0], sb, bar, k0, bn, pb);
+                tc::load_box<false>(&p.b[1], sb + kOpBytes / 2, bar, k0, bn, pb);
+              }
+            } else if (B_MN) {
+              tc::load_box<CG == 2>(&p.b[seg], sb, bar, bn, k0, pb);
+              tc::load_box<CG == 2>(&p.b[seg], sb + kOpBytes / 2, bar, bn + 64, k0, pb);
+            } else {
+              tc::load_box<CG == 2>(&p.b[seg], sb, bar, k0, bn, pb);
+            }
+            ++issued;
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
         }
       }
@@ -300,29 +353,39 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
       constexpr uint32_t idesc = tc::idesc_bf16(kRows * CG, kRows * CG, A_MN, B_MN);
       int stage = 0;
       uint32_t phase = 0;
-      int64_t it = 0;
-      for (int64_t t = first; ok && t < tiles; t += stride, ++it) {
-        const int buf = (int)(it & 1);
-        ok = tc::bar_wait(acc_empty(buf), (uint32_t)(it >> 1 & 1) ^ 1, &abort_flag, p.limit);
-        tc::fence_after();
-        for (int s = s0; ok && s < s1; ++s) {
-          ok = tc::bar_wait(full(stage), phase, &abort_flag, p.limit);
-          if (!ok) break;
-          tc::fence_after();
-          const uint32_t sa = base + stage * kStageBytes, sb = sa + kOpBytes;
-          const uint64_t da = tc::desc_sw128(sa, A_MN ? kOpBytes / 2 : 16);
-          const uint64_t db = tc::desc_sw128(sb, B_MN ? kOpBytes / 2 : 16);
+      int64_t run = 0;  // sums begun: the accumulators alternate
+      for (int64_t t = first; ok && t < tiles; t += stride) {
+        for (int un = u0; ok && un < u1; ++un) {
+          const uint32_t acc = tmem + (uint32_t)(run & 1) * kAccCols;
+          const bool begin = U::kParts || un == u0, end = U::kParts || un + 1 == u1;
+          if (begin) {
+            ok = tc::bar_wait(acc_empty((int)(run & 1)), (uint32_t)(run >> 1 & 1) ^ 1, &abort_flag,
+                              p.limit);
+            tc::fence_after();
+          }
+          const int steps = U::steps(p.kt, U::kParts ? un % per_seg : 0);
+          for (int st = 0; ok && st < steps; ++st) {
+            ok = tc::bar_wait(full(stage), phase, &abort_flag, p.limit);
+            if (!ok) break;
+            tc::fence_after();
+            const uint32_t sa = base + stage * kStageBytes, sb = sa + kOpBytes;
+            const uint64_t da = tc::desc_sw128(sa, A_MN ? kOpBytes / 2 : 16);
+            const uint64_t db = tc::desc_sw128(sb, B_MN ? kOpBytes / 2 : 16);
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k)
-            tc::mma_bf16<CG>(tmem + buf * kAccCols, da + (A_MN ? 2048 : 32) / 16 * k,
-                             db + (B_MN ? 2048 : 32) / 16 * k, idesc, s > s0 || k > 0);
-          tc::mma_commit<CG>(empty(stage));
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
+            for (int k = 0; k < kBK / 16; ++k)
+              tc::mma_bf16<CG>(acc, da + (A_MN ? 2048 : 32) / 16 * k,
+                               db + (B_MN ? 2048 : 32) / 16 * k, idesc, !begin || st > 0 || k > 0);
+            tc::mma_commit<CG>(empty(stage));
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+          if (ok && end) {
+            tc::mma_commit<CG>(acc_full((int)(run & 1)));
+            ++run;
           }
         }
-        if (ok) tc::mma_commit<CG>(acc_full(buf));
       }
       if (!ok) {  // MMAs in flight end before tensor memory is freed
         volatile int none = 0;
@@ -332,50 +395,93 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
     }
   } else {
     const int quad = warp & 3;
-    int64_t it = 0;
-    for (int64_t t = first; t < tiles; t += stride, ++it) {
-      const Tile w = tile_at<CG, EPI>(p, t);
-      const int buf = (int)(it & 1);
-      if (ok) ok = tc::bar_wait(acc_full(buf), (uint32_t)(it >> 1 & 1), &abort_flag, p.limit);
+    constexpr int kOut = EPI == kDenseGated ? kAccCols / 2 : kAccCols;
+    constexpr float kBad = __builtin_nanf("");
+    int64_t run = 0;
+    // waits for the next sum; the address of this warp's lanes of it
+    const auto next_sum = [&]() {
+      const int buf = (int)(run & 1);
+      if (ok) ok = tc::bar_wait(acc_full(buf), (uint32_t)(run >> 1 & 1), &abort_flag, p.limit);
       ok = __all_sync(~0u, ok);
       tc::fence_after();
-      const uint32_t acc = tmem + buf * kAccCols + ((uint32_t)(quad * 32) << 16);
-      constexpr int kOut = EPI == kDenseGated ? kAccCols / 2 : kAccCols;
-      if (CG == 1 && p.split > 1) {
-        // this CTA's sums to its own shared memory, [column][row]: every stage
-        // has been multiplied, so the buffers are free
-        float* sums = reinterpret_cast<float*>(raw + (base - tc::smem(raw)));
-#pragma unroll
-        for (int c = 0; c < kAccCols; c += 32) {
-          uint32_t r[32];
-          tc::tmem_ld32(acc + c, r);
-          tc::tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            sums[(c + i) * kRows + quad * 32 + lane] = ok ? __uint_as_float(r[i]) : __int_as_float(0x7fc00000);
-        }
-        break;  // joined below
-      }
+      return tmem + buf * kAccCols + ((uint32_t)(quad * 32) << 16);
+    };
+    // the sum is read: MMAs may use its buffer again
+    const auto sum_read = [&]() {
+      tc::fence_before();
+      if (lane == 0) tc::bar_arrive_cluster(tc::map_rank(acc_empty((int)(run & 1)), CG == 2 ? 0 : rank));
+      ++run;
+    };
+    for (int64_t t = first; t < tiles; t += stride) {
+      const Tile w = tile_at<CG, EPI>(p, t);
       const int64_t row = w.m0 + (CG == 2 ? (int64_t)rank * kRows : 0) + quad * 32 + lane;
-#pragma unroll 1
-      for (int c = 0; c < kOut; c += 32) {
-        uint32_t r[32], q[32];
-        tc::tmem_ld32(acc + c, r);
-        if (EPI == kDenseGated) tc::tmem_ld32(acc + kOut + c, q);
-        tc::tmem_ld_wait();
-        if (c + 32 == kOut) {  // the buffer is read: the next tile's MMAs may use it
-          tc::fence_before();
-          if (lane == 0)
-            tc::bar_arrive_cluster(CG == 2 ? tc::map_rank(acc_empty(buf), 0) : tc::map_rank(acc_empty(buf), rank));
-        }
-        if (row < p.m && w.n0 + c < p.n) {
-          float v[32], u[32];
+      float* sums = reinterpret_cast<float*>(raw + (base - tc::smem(raw)));
+      if constexpr (U::kParts) {
+        float sum[kAccCols];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            v[i] = ok ? __uint_as_float(r[i]) : __int_as_float(0x7fc00000);
-            u[i] = EPI == kDenseGated ? __uint_as_float(q[i]) : 0.0f;
+        for (int i = 0; i < kAccCols; ++i) sum[i] = 0.0f;
+        for (int un = u0; un < u1; ++un) {
+          const uint32_t acc = next_sum();
+#pragma unroll
+          for (int c = 0; c < kAccCols; c += 32) {
+            uint32_t r[32];
+            tc::tmem_ld32(acc + c, r);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[c + i] += ok ? __uint_as_float(r[i]) : kBad;
           }
-          finish32<T, EPI>(p, w.prob, row, w.n0 + c, v, u);
+          sum_read();
+        }
+        if (p.split > 1) {
+#pragma unroll
+          for (int c = 0; c < kAccCols; ++c) sums[c * kRows + quad * 32 + lane] = sum[c];
+          break;  // joined below
+        }
+        if (row < p.m) {
+#pragma unroll
+          for (int c = 0; c < kOut; c += 32) {
+            if (w.n0 + c >= p.n) break;
+            float v[32], u[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              v[i] = sum[c + i];
+              u[i] = EPI == kDenseGated ? sum[kOut + c + i] : 0.0f;
+            }
+            finish32<T, EPI>(p, w.prob, row, w.n0 + c, v, u);
+          }
+        }
+      } else {
+        const uint32_t acc = next_sum();
+        if (CG == 1 && p.split > 1) {
+          // this CTA's sums to its own shared memory, [column][row]: every
+          // stage has been multiplied, so the buffers are free
+#pragma unroll
+          for (int c = 0; c < kAccCols; c += 32) {
+            uint32_t r[32];
+            tc::tmem_ld32(acc + c, r);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              sums[(c + i) * kRows + quad * 32 + lane] = ok ? __uint_as_float(r[i]) : kBad;
+          }
+          break;  // joined below
+        }
+#pragma unroll 1
+        for (int c = 0; c < kOut; c += 32) {
+          uint32_t r[32], q[32];
+          tc::tmem_ld32(acc + c, r);
+          if (EPI == kDenseGated) tc::tmem_ld32(acc + kOut + c, q);
+          tc::tmem_ld_wait();
+          if (c + 32 == kOut) sum_read();
+          if (row < p.m && w.n0 + c < p.n) {
+            float v[32], u[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              v[i] = ok ? __uint_as_float(r[i]) : kBad;
+              u[i] = EPI == kDenseGated ? __uint_as_float(q[i]) : 0.0f;
+            }
+            finish32<T, EPI>(p, w.prob, row, w.n0 + c, v, u);
+          }
         }
       }
     }
@@ -489,47 +595,106 @@ static qat_status launch_majors(DenseArgs& p, int epi, bool a_mn, bool b_mn, cud
 qat_status launch_dense(const Dense& d, cudaStream_t s) {
   if (d.m == 0 || d.n == 0) return QAT_OK;
   DenseArgs p = {};
-  const bool gated = d.epi == kDenseGated;
-  const int sms = device_info().sms;
+  const bool gated = d.epi == kDenseGated, f32 = d.dtype == QAT_F32;
+  const int sms = device_info().sms, parts = f32 ? 3 : 1;
   const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
   p.m = d.m;
   p.n = d.n;
   p.problems = d.problems;
   p.segs = d.segs;
-  p.parts = d.parts;
   p.kt = (int)up(d.k, kBK);
-  // pairs of CTAs once their tiles fill the GPU
+  // pairs of CTAs once their tiles fill the GPU; the fp32 sums need a tile of
+  // 128 columns, which is what a thread's registers hold
   const int64_t big = up(d.m, 256) * up(d.n, gated ? 128 : 256) * d.problems;
-  const bool pair = big >= sms / 2;
+  const bool pair = !f32 && big >= sms / 2;
   const int bm = pair ? 256 : 128, bn = gated ? bm / 2 : bm;
   p.mt = (int)up(d.m, bm);
   p.nt = (int)up(d.n, bn);
   p.split = 1;
   if (!pair) {
-    // k is split while there are SMs for it and four steps for each CTA
+    // k is split while there are SMs for it and work for each CTA
     const int64_t tiles = (int64_t)p.mt * p.nt * p.problems;
-    const int64_t steps = (int64_t)p.segs * (p.parts == 1 ? 1 : 6) * p.kt;
-    while (p.split < 8 && tiles * p.split * 2 <= sms && steps >= p.split * 2 * 4) p.split *= 2;
+    const int64_t units = (int64_t)p.segs * (f32 ? Units<F32>::per_segment(p.kt) : p.kt);
+    const int least = f32 ? 1 : 4;
+    while (p.split < 8 && tiles * p.split * 2 <= sms && units >= p.split * 2 * least) p.split *= 2;
   }
   const int nb = gated ? 2 : d.segs, na = d.problems > 1 ? d.problems : d.segs;
   for (int i = 0; i < 2; ++i) {
-    if (!encode(&p.a[i], d.a[i < na ? i : 0], d.m, d.k, d.parts, 128)) return QAT_ERR_CUDA;
-    if (!encode(&p.b[i], d.b[i < nb ? i : 0], d.n, d.k, d.parts, gated && !pair ? 64 : 128))
+    if (!encode(&p.a[i], d.a[i < na ? i : 0], d.m, d.k, parts, 128)) return QAT_ERR_CUDA;
+    if (!encode(&p.b[i], d.b[i < nb ? i : 0], d.n, d.k, parts, gated && !pair ? 64 : 128))
       return QAT_ERR_CUDA;
   }
   p.act = d.act;
-  p.c[0] = d.c[0];
-  p.c[1] = d.c[1];
-  p.ld = d.n;
+  for (int i = 0; i < 2; ++i) {
+    p.c[i] = d.c[i];
+    p.q[i] = d.q[i];
+  }
+  p.q_pitch = d.q_pitch;
+  p.q_part = d.q_part;
   p.gp = d.gp;
   p.up = d.up;
-  p.dg = d.dg;
-  p.du = d.du;
   p.flags = d.flags;
   p.limit = device_wait_limit();
   const bool a_mn = d.a[0].mn_major, b_mn = d.b[0].mn_major;
+  if (f32) return launch_majors<F32, 1>(p, d.epi, a_mn, b_mn, s);
   return pair ? launch_majors<BF16, 2>(p, d.epi, a_mn, b_mn, s)
               : launch_majors<BF16, 1>(p, d.epi, a_mn, b_mn, s);
+}
+
+// ---------------------------------------------------------------------------
+// Operands the copies cannot read in place (rows that are not whole 16-byte
+// vectors, fp32) as bf16 parts with padded rows.  One launch for up to six
+// tensors; a thread takes eight elements of a row.
+// ---------------------------------------------------------------------------
+struct PackArgs {
+  DensePack t[6];
+};
+template <typename T>
+__global__ void __launch_bounds__(256) k_dense_pack(const __grid_constant__ PackArgs p) {
+  const DensePack& t = p.t[blockIdx.y];
+  const int64_t wide = t.pitch / 8, total = t.rows * wide;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / wide, c = (i - r * wide) * 8;
+    float v[8];
+    const int64_t at = r * t.cols + c;
+    if (T::BYTES == 4 && t.cols % 4 == 0 && c + 8 <= t.cols) {
+      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(t.src) + at);
+      const float4 a = q[0], b = q[1];
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = c + e < t.cols ? ld_elem<T>(t.src, at + e) : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < (T::BYTES == 4 ? 3 : 1); ++k) {
+      float h[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = T::BYTES == 4 ? take_bf16(v[e]) : v[e];
+      *reinterpret_cast<uint4*>(static_cast<char*>(t.dst) + (k * t.part + r * t.pitch + c) * 2) =
+          make_uint4(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]), pack_bf16x2(h[4], h[5]),
+                     pack_bf16x2(h[6], h[7]));
+    }
+  }
+}
+
+qat_status launch_dense_pack(qat_dtype dt, const DensePack* list, int n, cudaStream_t s) {
+  if (n == 0) return QAT_OK;
+  PackArgs p = {};
+  int64_t most = 0;
+  for (int i = 0; i < n; ++i) {
+    p.t[i] = list[i];
+    const int64_t b = (list[i].rows * (list[i].pitch / 8) + 255) / 256;
+    most = b > most ? b : most;
+  }
+  const int64_t room = (int64_t)device_info().sms * 16;
+  const dim3 grid((unsigned)(most < room ? most : room), (unsigned)n);
+  if (dt == QAT_F32)
+    k_dense_pack<F32><<<grid, 256, 0, s>>>(p);
+  else
+    k_dense_pack<BF16><<<grid, 256, 0, s>>>(p);
+  count_launch(1);
+  return launch_status();
 }
 
 }  // namespace qat

@@ -167,20 +167,11 @@ __device__ __forceinline__ void pairs_bf16(const uint4& v, uint32_t (&b)[4]) {
   b[2] = __byte_perm(v.y, v.w, 0x7632);
   b[3] = __byte_perm(v.y, v.w, 0x5410);
 }
-// the bf16 terms of one float: truncations, so that none overflows; the
-// remainder of an infinity is 0 and a NaN keeps a mantissa bit
+// the bf16 terms of one float, in the high halves
 template <int TERMS>
 __device__ __forceinline__ void split_f32(float x, uint32_t (&h)[TERMS]) {
-  const uint32_t u = __float_as_uint(x);
-  const bool special = (u & 0x7f800000u) == 0x7f800000u;
-  h[0] = u & 0xffff0000u;
-  if (special && (u & 0x007fffffu)) h[0] |= 0x00400000u;
-  float r = special ? 0.0f : x - __uint_as_float(h[0]);
 #pragma unroll
-  for (int i = 1; i < TERMS; ++i) {
-    h[i] = __float_as_uint(r) & 0xffff0000u;
-    r -= __uint_as_float(h[i]);
-  }
+  for (int i = 0; i < TERMS; ++i) h[i] = __float_as_uint(take_bf16(x));
 }
 
 template <typename T, int CH>

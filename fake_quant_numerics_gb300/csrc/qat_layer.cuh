@@ -23,6 +23,18 @@ __device__ __forceinline__ void st_elem<BF16>(void* p, int64_t i, float v) {
   static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
+// The next bf16 part of a float, which keeps the remainder: three calls take all
+// 24 bits.  Truncation, so that no part overflows; an infinity leaves nothing
+// and a NaN keeps a mantissa bit.
+__device__ __forceinline__ float take_bf16(float& x) {
+  const uint32_t u = __float_as_uint(x);
+  const bool special = (u & 0x7f800000u) == 0x7f800000u;
+  uint32_t h = u & 0xffff0000u;
+  if (special && (u & 0x007fffffu)) h |= 0x00400000u;
+  x = special ? 0.0f : x - __uint_as_float(h);
+  return __uint_as_float(h);
+}
+
 // act(g) and act'(g): silu (0), gelu in the erf form (1), relu (2).  A NaN
 // stays NaN; relu'(0) = 0.
 __device__ __forceinline__ void act_grad(int act, float g, float& a, float& da) {

@@ -51,7 +51,9 @@ qat_status check_w4_call(const void* x, qat_dtype xdt, int64_t tokens, const qat
 }
 
 bool ffn_sizes_ok(int64_t t, int64_t d, int64_t f) {
-  return fits(t, d) && fits(t, f) && fits(d, f);
+  // coordinates of the tensor copies are 32-bit
+  constexpr int64_t most = INT32_MAX - 4096;
+  return t <= most && d <= most && f <= most && fits(t, d) && fits(t, f) && fits(d, f);
 }
 
 }  // namespace
@@ -105,8 +107,8 @@ qat_status qat_gated_ffn(const void* x, qat_dtype dtype, int64_t tokens, int64_t
       (weights && (!w_gate || !w_up || !w_down)))
     return QAT_ERR_INVALID_ARGUMENT;
   const uintptr_t e = esize(dtype);
-  if (!on(x, e) || !on(w_gate, e) || !on(w_up, e) || !on(w_down, e) || !on(h, e) || !on(y, e) ||
-      !on(gate_pre, 4) || !on(up_pre, 4) || !on(dev_flags, 4))
+  if (!on(x, 16) || !on(w_gate, 16) || !on(w_up, 16) || !on(w_down, 16) || !on(h, 16) ||
+      !on(y, e) || !on(gate_pre, 4) || !on(up_pre, 4) || !on(dev_flags, 4))
     return QAT_ERR_MISALIGNED;
   const size_t need = ffn_ws_bytes(dtype, tokens, dim, hidden, false);
   if (need && (!workspace || workspace_bytes < need)) return QAT_ERR_WORKSPACE;
@@ -129,8 +131,8 @@ qat_status qat_gated_ffn_backward(const void* dy, const void* x, qat_dtype dtype
       (tokens > 0 && hidden > 0 && (!h || !gate_pre || !up_pre)))
     return QAT_ERR_INVALID_ARGUMENT;
   const uintptr_t e = esize(dtype);
-  if (!on(dy, e) || !on(x, e) || !on(w_gate, e) || !on(w_up, e) || !on(w_down, e) || !on(h, e) ||
-      !on(gate_pre, 4) || !on(up_pre, 4) || !on(dx, e) || !on(dw_gate, e) || !on(dw_up, e) ||
+  if (!on(dy, 16) || !on(x, 16) || !on(w_gate, 16) || !on(w_up, 16) || !on(w_down, 16) ||
+      !on(h, 16) || !on(gate_pre, 4) || !on(up_pre, 4) || !on(dx, e) || !on(dw_gate, e) || !on(dw_up, e) ||
       !on(dw_down, e) || !on(dev_flags, 4))
     return QAT_ERR_MISALIGNED;
   const size_t need = ffn_ws_bytes(dtype, tokens, dim, hidden, true);

@@ -39,6 +39,12 @@ def _here(t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
+def _aligned(t: torch.Tensor) -> torch.Tensor:
+    """Contiguous and 16-byte aligned (a fresh copy when it is not)."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 def _leading(t: torch.Tensor, shape) -> int:
     """Rows of t seen as [rows, last dimension]."""
     return t.numel() // shape[-1] if shape[-1] else shape[:-1].numel()
@@ -203,7 +209,7 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     [hidden, dim], w_down [dim, hidden], one dtype (float32 or bfloat16).
     save=True keeps the pre-activations for gated_ffn_backward."""
     tokens, dim, hidden = _ffn_sizes("gated_ffn", x, w_gate, w_up, w_down)
-    x, w_gate, w_up, w_down = x.contiguous(), w_gate.contiguous(), w_up.contiguous(), w_down.contiguous()
+    x, w_gate, w_up, w_down = _aligned(x), _aligned(w_gate), _aligned(w_up), _aligned(w_down)
     h = torch.empty((tokens, hidden), dtype=x.dtype, device=x.device)
     g = u = None
     if save:
@@ -236,8 +242,8 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
     _of_type(x, dy, h)
     if g.dtype != torch.float32 or u.dtype != torch.float32:
         raise TypeError("the saved pre-activations are float32")
-    dy, x, h, g, u = dy.contiguous(), x.contiguous(), h.contiguous(), g.contiguous(), u.contiguous()
-    w_gate, w_up, w_down = w_gate.contiguous(), w_up.contiguous(), w_down.contiguous()
+    dy, x, h, g, u = _aligned(dy), _aligned(x), _aligned(h), g.contiguous(), u.contiguous()
+    w_gate, w_up, w_down = _aligned(w_gate), _aligned(w_up), _aligned(w_down)
     dx = torch.empty_like(x) if want_dx else None
     dwg = dwu = dwd = None
     if want_dw:

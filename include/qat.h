@@ -430,10 +430,10 @@ qat_status qat_fake_quant_fp8_noalloc(const void* x, qat_dtype dtype, int64_t n,
  * Layer operators: what a layer does with the weights the calls above
  * quantize.  No counterpart on the source pages.  The conventions above hold
  * (device pointers, stream order, caller-owned buffers and workspaces, no
- * state between calls, synchronous errors) except that every tensor here is
- * aligned to its element only: x, y, weights, gradients and their views may
- * start anywhere a whole element does.  Sums, statistics and products are held
- * in binary32; every output is rounded once to its type.
+ * state between calls, synchronous errors) except that tensors here are aligned
+ * to their element only (views may start anywhere a whole element does) where
+ * nothing else is said.  Sums, statistics and products are held in binary32;
+ * every output is rounded once to its type.
  */
 
 /*
@@ -465,7 +465,10 @@ typedef enum { QAT_ACT_SILU = 0, QAT_ACT_GELU = 1, QAT_ACT_RELU = 2 } qat_activa
  * y[t, n] = sum_k x[t, k] w[n, k] for a few tokens: x is x_dtype[tokens,
  * cols], y y_dtype[tokens, rows].  Products of codes and x are summed in
  * binary32 inside a unit, then scaled and summed over the units, so a scale
- * that is not finite makes its outputs NaN whatever the codes.  Any number of
+ * that is not finite makes its outputs NaN whatever the codes, and |x| up to
+ * 2^-10 of the binary32 range is safe from overflow.  A float x is taken as
+ * bf16 parts: three (all 24 bits), or two (16 bits) under a bf16 y; parts below
+ * 2^-133 are lost.  Any number of
  * tokens; the weight is read once per 32 of them.  tokens == 0 or rows == 0
  * is a no-op; cols == 0 writes zeros.  QAT_ERR_INVALID_ARGUMENT: a NULL array,
  * a negative size, a group that does not divide cols, zero points with
@@ -492,8 +495,13 @@ qat_status qat_gated4(const void* x, qat_dtype x_dtype, int64_t tokens, const qa
  * dtype[hidden, dim]; w_down: dtype[dim, hidden]; h: dtype[tokens, hidden];
  * gate_pre, up_pre (both or neither): float[tokens, hidden], g and u kept for
  * the backward pass.  act: silu g * sigmoid(g), gelu g * Phi(g) (the erf
- * form), relu max(g, 0).  Products and sums in binary32.  An empty sum
- * (dim == 0 or hidden == 0) is zero.  workspace:
+ * form), relu max(g, 0).  bf16 products are exact and their sums binary32;
+ * fp32 operands are taken as three bf16 parts that hold all 24 bits (an
+ * infinite operand may give NaN where binary32 gives an infinity, and the last
+ * digits of operands below 2^-100 are lost).  An empty sum (dim == 0 or hidden
+ * == 0) is zero.  x, w_gate, w_up, w_down and h are 16-byte aligned; sizes are
+ * below 2^31 - 4096.  workspace (operand copies where rows are not whole
+ * 16-byte vectors of bf16, else none):
  * qat_gated_ffn_workspace_bytes(dtype, tokens, dim, hidden, 0) bytes, 16-byte
  * aligned.  A bounded device wait that runs out sets QAT_FLAG_DEVICE_TIMEOUT in
  * *dev_flags (nullable) and makes the outputs it did not reach NaN.
@@ -511,8 +519,9 @@ qat_status qat_gated_ffn(const void* x, qat_dtype dtype, int64_t tokens, int64_t
  * each rounded once to dtype; dx = dg Wg + du Wu; dw_gate = dg^T x;
  * dw_up = du^T x; dw_down = dy^T h.  dx, dw_gate, dw_up and dw_down are each
  * nullable (their products are then skipped).  relu'(0) = 0.  tokens == 0
- * gives zero weight gradients.  workspace:
- * qat_gated_ffn_workspace_bytes(dtype, tokens, dim, hidden, 1) bytes.
+ * gives zero weight gradients.  dy, x, the weights and h are 16-byte aligned.
+ * workspace: qat_gated_ffn_workspace_bytes(dtype, tokens, dim, hidden, 1)
+ * bytes, 16-byte aligned.  dev_flags as above.
  */
 qat_status qat_gated_ffn_backward(const void* dy, const void* x, qat_dtype dtype, int64_t tokens,
                                   int64_t dim, int64_t hidden, const void* w_gate,
