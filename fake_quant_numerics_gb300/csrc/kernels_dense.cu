@@ -9,7 +9,7 @@
 //
 // A CTA stages 128 rows of A and 128 of B, 64 deep, per step (32 KB, six steps
 // in flight) in 128-byte swizzled rows.  One thread issues the copies, one the
-// MMAs; the sums stay in tensor memory, in two buffers, so that four warps
+// MMAs; the sums stay in tensor memory, in two buffers, so that eight warps
 // finish one tile while the next is multiplied.  CG = 2: two CTAs share a
 // 256 x 256 tile, each holding half of A and half of B, which halves the
 // shared-memory traffic per product (a single CTA's 128 x 128 tile reads its
@@ -31,7 +31,8 @@ constexpr uint32_t kOpBytes = kRows * kBK * 2;  // 16 KB
 constexpr uint32_t kStageBytes = 2 * kOpBytes;
 constexpr uint32_t kBarBytes = 256;
 constexpr uint32_t kDenseSmem = kStages * kStageBytes + kBarBytes + 1024;
-constexpr int kDenseThreads = 192;
+constexpr int kFinishWarps = 8;  // two for each quarter of the tile's rows
+constexpr int kDenseThreads = 64 + 32 * kFinishWarps;
 
 struct DenseArgs {
   CUtensorMap a[2], b[2];
@@ -192,6 +193,10 @@ __device__ __forceinline__ void finish1(const DenseArgs& p, int prob, int64_t ro
   }
 }
 
+__device__ __forceinline__ void add4(float4& a, const float4& b) {
+  a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+}
+
 struct Tile {
   int prob;
   int64_t m0, n0;  // first output row and column (of the CTA pair)
@@ -260,7 +265,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
     }
     for (int b = 0; b < 2; ++b) {
       tc::bar_init(acc_full(b), 1);
-      tc::bar_init(acc_empty(b), 4 * CG);
+      tc::bar_init(acc_empty(b), kFinishWarps * CG);
     }
     tc::bar_init(drain, 1);
     tc::bar_init_fence();
@@ -276,6 +281,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
   if (CG == 2 || p.split > 1) tc::cluster_sync();
   tc::fence_after();
   const uint32_t tmem = tmem_slot;
+  pdl_trigger();  // the call's next kernel may take each SM as this one leaves it
+  pdl_wait();     // and this one's set-up overlapped the previous kernel's end
 
   using U = Units<T>;
   const int per_seg = U::per_segment(p.kt), units = p.segs * per_seg;
@@ -396,6 +403,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
   } else {
     const int quad = warp & 3;
     constexpr int kOut = EPI == kDenseGated ? kAccCols / 2 : kAccCols;
+    constexpr int kHalf = kOut / 2;
+    const int c_first = (warp - 2) / 4 * kHalf;  // this warp's columns
     constexpr float kBad = __builtin_nanf("");
     int64_t run = 0;
     // waits for the next sum; the address of this warp's lanes of it
@@ -404,7 +413,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
       if (ok) ok = tc::bar_wait(acc_full(buf), (uint32_t)(run >> 1 & 1), &abort_flag, p.limit);
       ok = __all_sync(~0u, ok);
       tc::fence_after();
-      return tmem + buf * kAccCols + ((uint32_t)(quad * 32) << 16);
+      return tmem + buf * kAccCols + ((uint32_t)(quad * 32) << 16) + c_first;
     };
     // the sum is read: MMAs may use its buffer again
     const auto sum_read = [&]() {
@@ -415,74 +424,82 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
     for (int64_t t = first; t < tiles; t += stride) {
       const Tile w = tile_at<CG, EPI>(p, t);
       const int64_t row = w.m0 + (CG == 2 ? (int64_t)rank * kRows : 0) + quad * 32 + lane;
-      float* sums = reinterpret_cast<float*>(raw + (base - tc::smem(raw)));
+      const int64_t col = w.n0 + c_first;
+      // where k is split: this CTA's sums, [column][row], in the stage buffers
+      // (every stage has been multiplied by then)
+      float* sums = reinterpret_cast<float*>(raw + (base - tc::smem(raw))) + quad * 32 + lane;
       if constexpr (U::kParts) {
-        float sum[kAccCols];
+        constexpr int kU = EPI == kDenseGated ? kHalf : 1;
+        float sv[kHalf], su[kU];
 #pragma unroll
-        for (int i = 0; i < kAccCols; ++i) sum[i] = 0.0f;
+        for (int i = 0; i < kHalf; ++i) sv[i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kU; ++i) su[i] = 0.0f;
         for (int un = u0; un < u1; ++un) {
           const uint32_t acc = next_sum();
 #pragma unroll
-          for (int c = 0; c < kAccCols; c += 32) {
+          for (int c = 0; c < kHalf; c += 32) {
             uint32_t r[32];
             tc::tmem_ld32(acc + c, r);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sum[c + i] += ok ? __uint_as_float(r[i]) : kBad;
+            for (int i = 0; i < 32; ++i) sv[c + i] += ok ? __uint_as_float(r[i]) : kBad;
+            if constexpr (EPI == kDenseGated) {
+              tc::tmem_ld32(acc + kOut + c, r);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) su[c + i] += __uint_as_float(r[i]);
+            }
           }
           sum_read();
         }
-        if (p.split > 1) {
+        if (CG == 1 && p.split > 1) {
 #pragma unroll
-          for (int c = 0; c < kAccCols; ++c) sums[c * kRows + quad * 32 + lane] = sum[c];
+          for (int c = 0; c < kHalf; ++c) {
+            sums[(c_first + c) * kRows] = sv[c];
+            if (EPI == kDenseGated) sums[(kOut + c_first + c) * kRows] = su[c % kU];
+          }
           break;  // joined below
         }
         if (row < p.m) {
 #pragma unroll
-          for (int c = 0; c < kOut; c += 32) {
-            if (w.n0 + c >= p.n) break;
+          for (int c = 0; c < kHalf; c += 32) {
+            if (col + c >= p.n) break;
             float v[32], u[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              v[i] = sum[c + i];
-              u[i] = EPI == kDenseGated ? sum[kOut + c + i] : 0.0f;
+              v[i] = sv[c + i];
+              u[i] = su[(c + i) % kU];
             }
-            finish32<T, EPI>(p, w.prob, row, w.n0 + c, v, u);
+            finish32<T, EPI>(p, w.prob, row, col + c, v, u);
           }
         }
       } else {
         const uint32_t acc = next_sum();
-        if (CG == 1 && p.split > 1) {
-          // this CTA's sums to its own shared memory, [column][row]: every
-          // stage has been multiplied, so the buffers are free
-#pragma unroll
-          for (int c = 0; c < kAccCols; c += 32) {
-            uint32_t r[32];
-            tc::tmem_ld32(acc + c, r);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              sums[(c + i) * kRows + quad * 32 + lane] = ok ? __uint_as_float(r[i]) : kBad;
-          }
-          break;  // joined below
-        }
 #pragma unroll 1
-        for (int c = 0; c < kOut; c += 32) {
+        for (int c = 0; c < kHalf; c += 32) {
           uint32_t r[32], q[32];
           tc::tmem_ld32(acc + c, r);
           if (EPI == kDenseGated) tc::tmem_ld32(acc + kOut + c, q);
           tc::tmem_ld_wait();
-          if (c + 32 == kOut) sum_read();
-          if (row < p.m && w.n0 + c < p.n) {
-            float v[32], u[32];
+          if (c + 32 == kHalf) sum_read();
+          float v[32], u[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            v[i] = ok ? __uint_as_float(r[i]) : kBad;
+            u[i] = EPI == kDenseGated ? __uint_as_float(q[i]) : 0.0f;
+          }
+          if (CG == 1 && p.split > 1) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              v[i] = ok ? __uint_as_float(r[i]) : kBad;
-              u[i] = EPI == kDenseGated ? __uint_as_float(q[i]) : 0.0f;
+              sums[(c_first + c + i) * kRows] = v[i];
+              if (EPI == kDenseGated) sums[(kOut + c_first + c + i) * kRows] = u[i];
             }
-            finish32<T, EPI>(p, w.prob, row, w.n0 + c, v, u);
+          } else if (row < p.m && col + c < p.n) {
+            finish32<T, EPI>(p, w.prob, row, col + c, v, u);
           }
         }
+        if (CG == 1 && p.split > 1) break;  // joined below
       }
     }
   }
@@ -490,22 +507,27 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
   if (CG == 1 && p.split > 1) {
     tc::cluster_sync();
     // each CTA of the cluster finishes its share of the columns, adding the
-    // k slices in rank order
+    // k slices in rank order: four rows of a column a thread, every slice's
+    // load in flight at once
     constexpr int kOut = EPI == kDenseGated ? kAccCols / 2 : kAccCols;
     const Tile w = tile_at<CG, EPI>(p, first);
-    const int rows = (int)min((int64_t)kRows, p.m - w.m0);
-    const int c0 = kOut * (int)rank / p.split, c1 = kOut * ((int)rank + 1) / p.split;
-    const int width = c1 - c0;
-    for (int i = threadIdx.x; i < rows * width; i += kDenseThreads) {
-      const int c = c0 + i % width, r = i / width;
+    const int rows = (int)min((int64_t)kRows, p.m - w.m0), groups = (rows + 3) / 4;
+    const int c0 = kOut * (int)rank / p.split, width = kOut / p.split;
+    for (int i = threadIdx.x; i < groups * width; i += kDenseThreads) {
+      const int c = c0 + i / groups, r = i % groups * 4;
       if (w.n0 + c >= p.n) continue;
-      float v = 0.0f, u = 0.0f;
-      for (int q = 0; q < p.split; ++q) {
+      float4 v = make_float4(0, 0, 0, 0), u = v;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        if (q >= p.split) break;
         const uint32_t peer = tc::map_rank(base, q);
-        v += tc::ld_cluster(peer + (c * kRows + r) * 4);
-        if (EPI == kDenseGated) u += tc::ld_cluster(peer + ((kOut + c) * kRows + r) * 4);
+        add4(v, tc::ld_cluster4(peer + (c * kRows + r) * 4));
+        if (EPI == kDenseGated) add4(u, tc::ld_cluster4(peer + ((kOut + c) * kRows + r) * 4));
       }
-      finish1<T, EPI>(p, w.prob, w.m0 + r, w.n0 + c, v, u);
+      const float vs[4] = {v.x, v.y, v.z, v.w}, us[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (r + e < rows) finish1<T, EPI>(p, w.prob, w.m0 + r + e, w.n0 + c, vs[e], us[e]);
     }
   }
   if (CG == 2 || p.split > 1) tc::cluster_sync();  // peers have read this CTA's memory
@@ -551,7 +573,7 @@ static bool encode(CUtensorMap* map, const DenseOp& o, int64_t rows, int64_t dep
 }
 
 template <typename T, int CG, int EPI, bool A_MN, bool B_MN>
-static qat_status launch(DenseArgs& p, cudaStream_t s) {
+static qat_status launch(DenseArgs& p, bool pdl, cudaStream_t s) {
   const auto kernel = k_dense<T, CG, EPI, A_MN, B_MN>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmem) !=
       cudaSuccess) {
@@ -568,13 +590,15 @@ static qat_status launch(DenseArgs& p, cudaStream_t s) {
   cfg.blockDim = dim3(kDenseThreads);
   cfg.dynamicSmemBytes = kDenseSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = pdl ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return QAT_ERR_CUDA;
@@ -584,12 +608,13 @@ static qat_status launch(DenseArgs& p, cudaStream_t s) {
 }
 
 template <typename T, int CG>
-static qat_status launch_majors(DenseArgs& p, int epi, bool a_mn, bool b_mn, cudaStream_t s) {
-  if (epi == kDenseGated) return launch<T, CG, kDenseGated, false, false>(p, s);
-  if (epi == kDenseGatedBwd) return launch<T, CG, kDenseGatedBwd, false, true>(p, s);
-  if (a_mn) return launch<T, CG, kDenseStore, true, true>(p, s);
-  if (b_mn) return launch<T, CG, kDenseStore, false, true>(p, s);
-  return launch<T, CG, kDenseStore, false, false>(p, s);
+static qat_status launch_majors(DenseArgs& p, const Dense& d, cudaStream_t s) {
+  const bool a_mn = d.a[0].mn_major, b_mn = d.b[0].mn_major;
+  if (d.epi == kDenseGated) return launch<T, CG, kDenseGated, false, false>(p, d.pdl, s);
+  if (d.epi == kDenseGatedBwd) return launch<T, CG, kDenseGatedBwd, false, true>(p, d.pdl, s);
+  if (a_mn) return launch<T, CG, kDenseStore, true, true>(p, d.pdl, s);
+  if (b_mn) return launch<T, CG, kDenseStore, false, true>(p, d.pdl, s);
+  return launch<T, CG, kDenseStore, false, false>(p, d.pdl, s);
 }
 
 qat_status launch_dense(const Dense& d, cudaStream_t s) {
@@ -603,10 +628,9 @@ qat_status launch_dense(const Dense& d, cudaStream_t s) {
   p.problems = d.problems;
   p.segs = d.segs;
   p.kt = (int)up(d.k, kBK);
-  // pairs of CTAs once their tiles fill the GPU; the fp32 sums need a tile of
-  // 128 columns, which is what a thread's registers hold
+  // pairs of CTAs once their tiles fill the GPU
   const int64_t big = up(d.m, 256) * up(d.n, gated ? 128 : 256) * d.problems;
-  const bool pair = !f32 && big >= sms / 2;
+  const bool pair = big >= sms / 2;
   const int bm = pair ? 256 : 128, bn = gated ? bm / 2 : bm;
   p.mt = (int)up(d.m, bm);
   p.nt = (int)up(d.n, bn);
@@ -635,10 +659,8 @@ qat_status launch_dense(const Dense& d, cudaStream_t s) {
   p.up = d.up;
   p.flags = d.flags;
   p.limit = device_wait_limit();
-  const bool a_mn = d.a[0].mn_major, b_mn = d.b[0].mn_major;
-  if (f32) return launch_majors<F32, 1>(p, d.epi, a_mn, b_mn, s);
-  return pair ? launch_majors<BF16, 2>(p, d.epi, a_mn, b_mn, s)
-              : launch_majors<BF16, 1>(p, d.epi, a_mn, b_mn, s);
+  if (f32) return pair ? launch_majors<F32, 2>(p, d, s) : launch_majors<F32, 1>(p, d, s);
+  return pair ? launch_majors<BF16, 2>(p, d, s) : launch_majors<BF16, 1>(p, d, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -652,6 +674,7 @@ struct PackArgs {
 template <typename T>
 __global__ void __launch_bounds__(256) k_dense_pack(const __grid_constant__ PackArgs p) {
   const DensePack& t = p.t[blockIdx.y];
+  pdl_trigger();
   const int64_t wide = t.pitch / 8, total = t.rows * wide;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / wide, c = (i - r * wide) * 8;

@@ -46,6 +46,13 @@ struct Packer {
     return DenseOp{k.dst, k.pitch, false, k.part};
   }
   qat_status go(cudaStream_t s) { return launch_dense_pack(dt, list, n, s); }
+  // whether a kernel of this call has been launched before
+  bool launched = false;
+  bool next() {
+    const bool was = launched || n > 0;
+    launched = true;
+    return was;
+  }
 };
 // the same matrix read along its rows
 static DenseOp turned(DenseOp o) {
@@ -136,6 +143,7 @@ qat_status launch_ffn_fwd(const void* x, qat_dtype dt, int64_t t, int64_t d, int
   q.gp = gp;
   q.up = up;
   q.flags = flags;
+  q.pdl = w.next();
   st = launch_dense(q, s);
   if (st) return st;
   q = {};
@@ -148,6 +156,7 @@ qat_status launch_ffn_fwd(const void* x, qat_dtype dt, int64_t t, int64_t d, int
   q.b[0] = o.wd;
   q.c[0] = y;
   q.flags = flags;
+  q.pdl = w.next();
   return launch_dense(q, s);
 }
 
@@ -181,6 +190,7 @@ qat_status launch_ffn_bwd(const void* dy, const void* x, qat_dtype dt, int64_t t
     q.q_pitch = o.dg.pitch;
     q.q_part = o.dg.part;
     q.flags = flags;
+    q.pdl = w.next();
     st = launch_dense(q, s);
   }
   if (!st && dx) {
@@ -197,6 +207,7 @@ qat_status launch_ffn_bwd(const void* dy, const void* x, qat_dtype dt, int64_t t
     q.b[1] = turned(o.wu);
     q.c[0] = dx;
     q.flags = flags;
+    q.pdl = w.next();
     st = launch_dense(q, s);
   }
   if (!st && (dwg || dwu)) {
@@ -213,6 +224,7 @@ qat_status launch_ffn_bwd(const void* dy, const void* x, qat_dtype dt, int64_t t
     q.c[0] = dwg ? dwg : dwu;
     q.c[1] = dwu;
     q.flags = flags;
+    q.pdl = w.next();
     st = launch_dense(q, s);
   }
   if (!st && dwd) {
@@ -226,6 +238,7 @@ qat_status launch_ffn_bwd(const void* dy, const void* x, qat_dtype dt, int64_t t
     q.b[0] = turned(o.h);
     q.c[0] = dwd;
     q.flags = flags;
+    q.pdl = w.next();
     st = launch_dense(q, s);
   }
   return st;

@@ -41,6 +41,7 @@ struct Dense {
   float* gp = nullptr;
   float* up = nullptr;
   int32_t* flags = nullptr;
+  bool pdl = false;  // the call's previous kernel may still be running
 };
 qat_status launch_dense(const Dense& d, cudaStream_t s);
 
