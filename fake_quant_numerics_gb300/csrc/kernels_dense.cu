@@ -120,17 +120,6 @@ __device__ __forceinline__ void st_parts32(const DenseArgs& p, int which, int64_
     }
   }
 }
-template <typename T>
-__device__ __forceinline__ void st_parts1(const DenseArgs& p, int which, int64_t row, int64_t c,
-                                          float v) {
-  const int64_t at = row * p.q_pitch + c;
-  if constexpr (T::BYTES == 2) {
-    st_elem<BF16>(p.q[which], at, v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 3; ++k) st_elem<BF16>(p.q[which], at + k * p.q_part, take_bf16(v));
-  }
-}
 // the largest of 32, 16 or 1 that divides the address and the row pitch
 __device__ __forceinline__ uint32_t row_align(const void* p, int64_t pitch_bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(p) | (uint64_t)pitch_bytes;
@@ -170,29 +159,83 @@ __device__ __forceinline__ void finish32(const DenseArgs& p, int prob, int64_t r
     st_parts32<T>(p, 1, row, c, left, du);
   }
 }
-// The same for one element.
-template <typename T, int EPI>
-__device__ __forceinline__ void finish1(const DenseArgs& p, int prob, int64_t row, int64_t c,
-                                        float v, float u) {
-  const int64_t at = row * p.n + c;
-  if (EPI == kDenseStore) {
-    st_elem<T>(p.c[prob], at, v);
-  } else if (EPI == kDenseGated) {
-    const float h = act_value(p.act, v) * u;
-    st_elem<T>(p.c[0], at, h);
-    if (p.q[0]) st_parts1<T>(p, 0, row, c, h);
-    if (p.gp) {
-      p.gp[at] = v;
-      p.up[at] = u;
-    }
+// The same for four columns.
+template <typename T>
+__device__ __forceinline__ void st_row4(void* p, int64_t at, int left, bool vec, const float (&v)[4]) {
+  if (vec && left >= 4) {
+    if constexpr (T::BYTES == 4)
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + at) =
+          make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < left) st_elem<T>(p, at + i, v[i]);
+}
+template <typename T>
+__device__ __forceinline__ void st_parts4(const DenseArgs& p, int which, int64_t row, int64_t c,
+                                          int left, const float (&v)[4]) {
+  const int64_t at = row * p.q_pitch + c;
+  if constexpr (T::BYTES == 2) {
+    st_row4<BF16>(p.q[which], at, left, true, v);
   } else {
-    float a, da;
-    act_grad(p.act, p.gp[at], a, da);
-    st_parts1<T>(p, 0, row, c, v * p.up[at] * da);
-    st_parts1<T>(p, 1, row, c, v * a);
+    float r[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      float h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = take_bf16(r[i]);
+      st_row4<BF16>(p.q[which], at + k * p.q_part, left, true, h);
+    }
   }
 }
-
+template <typename T, int EPI>
+__device__ __forceinline__ void finish4(const DenseArgs& p, int prob, int64_t row, int64_t c,
+                                        const float (&v)[4], const float (&u)[4]) {
+  const int64_t at = row * p.n + c;
+  const int left = (int)min((int64_t)4, p.n - c);
+  const bool whole = p.n % 4 == 0;
+  const auto vec = [&](const void* q, int bytes) {
+    return whole && reinterpret_cast<uint64_t>(q) % (4 * bytes) == 0;
+  };
+  if (EPI == kDenseStore) {
+    st_row4<T>(p.c[prob], at, left, vec(p.c[prob], T::BYTES), v);
+  } else if (EPI == kDenseGated) {
+    float h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = act_value(p.act, v[i]) * u[i];
+    st_row4<T>(p.c[0], at, left, vec(p.c[0], T::BYTES), h);
+    if (p.q[0]) st_parts4<T>(p, 0, row, c, left, h);
+    if (p.gp) {
+      st_row4<F32>(p.gp, at, left, vec(p.gp, 4), v);
+      st_row4<F32>(p.up, at, left, vec(p.up, 4), u);
+    }
+  } else {
+    float g[4], w[4], dg[4], du[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      g[i] = i < left ? p.gp[at + i] : 0.0f;
+      w[i] = i < left ? p.up[at + i] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, da;
+      act_grad(p.act, g[i], a, da);
+      dg[i] = v[i] * w[i] * da;
+      du[i] = v[i] * a;
+    }
+    st_parts4<T>(p, 0, row, c, left, dg);
+    st_parts4<T>(p, 1, row, c, left, du);
+  }
+}
+// floats from one row of a tile's joined sums to the next: 16-byte accesses by
+// neighbouring rows then fall into different banks
+constexpr int kJoinPitch = kRows + 4;
+__device__ __forceinline__ void put4(float* p, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
 __device__ __forceinline__ void add4(float4& a, const float4& b) {
   a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
 }
@@ -425,9 +468,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
       const Tile w = tile_at<CG, EPI>(p, t);
       const int64_t row = w.m0 + (CG == 2 ? (int64_t)rank * kRows : 0) + quad * 32 + lane;
       const int64_t col = w.n0 + c_first;
-      // where k is split: this CTA's sums, [column][row], in the stage buffers
-      // (every stage has been multiplied by then)
-      float* sums = reinterpret_cast<float*>(raw + (base - tc::smem(raw))) + quad * 32 + lane;
+      // where k is split: this row of the CTA's sums, in the stage buffers (every
+      // stage has been multiplied by then)
+      float* sums = reinterpret_cast<float*>(raw + (base - tc::smem(raw))) +
+                    (quad * 32 + lane) * kJoinPitch + c_first;
       if constexpr (U::kParts) {
         constexpr int kU = EPI == kDenseGated ? kHalf : 1;
         float sv[kHalf], su[kU];
@@ -455,9 +499,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
         }
         if (CG == 1 && p.split > 1) {
 #pragma unroll
-          for (int c = 0; c < kHalf; ++c) {
-            sums[(c_first + c) * kRows] = sv[c];
-            if (EPI == kDenseGated) sums[(kOut + c_first + c) * kRows] = su[c % kU];
+          for (int c = 0; c < kHalf; c += 4) {
+            put4(sums + c, sv[c], sv[c + 1], sv[c + 2], sv[c + 3]);
+            if constexpr (EPI == kDenseGated)
+              put4(sums + kOut + c, su[c], su[c + 1], su[c + 2], su[c + 3]);
           }
           break;  // joined below
         }
@@ -491,9 +536,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
           }
           if (CG == 1 && p.split > 1) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              sums[(c_first + c + i) * kRows] = v[i];
-              if (EPI == kDenseGated) sums[(kOut + c_first + c + i) * kRows] = u[i];
+            for (int i = 0; i < 32; i += 4) {
+              put4(sums + c + i, v[i], v[i + 1], v[i + 2], v[i + 3]);
+              if (EPI == kDenseGated) put4(sums + kOut + c + i, u[i], u[i + 1], u[i + 2], u[i + 3]);
             }
           } else if (row < p.m && col + c < p.n) {
             finish32<T, EPI>(p, w.prob, row, col + c, v, u);
@@ -506,28 +551,26 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
   __syncthreads();
   if (CG == 1 && p.split > 1) {
     tc::cluster_sync();
-    // each CTA of the cluster finishes its share of the columns, adding the
-    // k slices in rank order: four rows of a column a thread, every slice's
-    // load in flight at once
+    // the cluster's CTAs finish the tile together, four columns of a row a
+    // thread, adding the k slices in rank order with every slice's load in flight
     constexpr int kOut = EPI == kDenseGated ? kAccCols / 2 : kAccCols;
     const Tile w = tile_at<CG, EPI>(p, first);
-    const int rows = (int)min((int64_t)kRows, p.m - w.m0), groups = (rows + 3) / 4;
-    const int c0 = kOut * (int)rank / p.split, width = kOut / p.split;
-    for (int i = threadIdx.x; i < groups * width; i += kDenseThreads) {
-      const int c = c0 + i / groups, r = i % groups * 4;
+    const int rows = (int)min((int64_t)kRows, p.m - w.m0);
+    for (int i = (int)rank * kDenseThreads + threadIdx.x; i < rows * (kOut / 4);
+         i += kDenseThreads * p.split) {
+      const int r = i / (kOut / 4), c = i % (kOut / 4) * 4;
       if (w.n0 + c >= p.n) continue;
       float4 v = make_float4(0, 0, 0, 0), u = v;
+      const uint32_t at = base + (r * kJoinPitch + c) * 4;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         if (q >= p.split) break;
-        const uint32_t peer = tc::map_rank(base, q);
-        add4(v, tc::ld_cluster4(peer + (c * kRows + r) * 4));
-        if (EPI == kDenseGated) add4(u, tc::ld_cluster4(peer + ((kOut + c) * kRows + r) * 4));
+        const uint32_t peer = tc::map_rank(at, q);
+        add4(v, tc::ld_cluster4(peer));
+        if (EPI == kDenseGated) add4(u, tc::ld_cluster4(peer + kOut * 4));
       }
       const float vs[4] = {v.x, v.y, v.z, v.w}, us[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (r + e < rows) finish1<T, EPI>(p, w.prob, w.m0 + r + e, w.n0 + c, vs[e], us[e]);
+      finish4<T, EPI>(p, w.prob, w.m0 + r, w.n0 + c, vs, us);
     }
   }
   if (CG == 2 || p.split > 1) tc::cluster_sync();  // peers have read this CTA's memory
