@@ -24,6 +24,6 @@ from .api import (DoubleQuantized4Bit, FakeQuantBlock, FakeQuantFp8, FakeQuantIn
                   raise_on_flags)
 from .layers import (GatedFfn, GatedFfnFunction, LayerNorm, LayerNormFunction, Weight4,  # noqa: F401
                      gated_ffn, gated_ffn4, gated_ffn_backward, layer_norm, layer_norm_backward,
-                     linear4, qat_gated4, qat_gated_ffn, qat_gated_ffn_backward,
-                     qat_gated_ffn_workspace_bytes, qat_layer_norm, qat_layer_norm_backward,
-                     qat_layer_norm_backward_workspace_bytes, qat_linear4, weight4, weight4_double)
+                     linear4, qat_gated_ffn, qat_gated_ffn_backward,
+                     qat_gated_ffn4, qat_gated_ffn4_workspace_bytes, qat_gated_ffn_workspace_bytes, qat_layer_norm, qat_layer_norm_backward,
+                     qat_layer_norm_backward_workspace_bytes, qat_linear4, qat_linear4_workspace_bytes, weight4, weight4_double)

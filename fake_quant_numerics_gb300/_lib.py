@@ -85,8 +85,10 @@ PROTOTYPES = {
     "qat_ste_backward": ([_vp, _int, _i64, _vp, _vp, _vp], _int),
     "qat_quant4_double": ([_vp, _i64, _vp, _vp, _vp, _vp, _vp], _int),
     "qat_dequant4_double": ([_vp, _vp, _vp, _i64, _vp, _vp], _int),
-    "qat_linear4": ([_vp, _int, _i64, _w4, _vp, _int, _vp], _int),
-    "qat_gated4": ([_vp, _int, _i64, _w4, _w4, _int, _vp, _vp], _int),
+    "qat_linear4_workspace_bytes": ([_int, _i64, _i64], _sz),
+    "qat_linear4": ([_vp, _int, _i64, _w4, _vp, _vp, _sz, _vp], _int),
+    "qat_gated_ffn4_workspace_bytes": ([_int, _i64, _i64, _i64], _sz),
+    "qat_gated_ffn4": ([_vp, _int, _i64, _w4, _w4, _w4, _int, _vp, _vp, _sz, _vp], _int),
     "qat_gated_ffn_workspace_bytes": ([_int, _i64, _i64, _i64, _int], _sz),
     "qat_gated_ffn": ([_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp, _vp,
                        _vp, _sz, _vp], _int),

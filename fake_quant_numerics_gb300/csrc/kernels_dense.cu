@@ -660,6 +660,37 @@ static qat_status launch_majors(DenseArgs& p, const Dense& d, cudaStream_t s) {
   return launch<T, CG, kDenseStore, false, false>(p, d.pdl, s);
 }
 
+// Clusters of c CTAs that run at the same time (one CTA a SM; a cluster stays
+// inside a group of SMs, so eight times fifteen is all of 152).
+static int resident_clusters(int c) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> cache[kMaxDev][9];  // 0 = unknown
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
+  int n = cache[dev][c].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  const auto kernel = k_dense<BF16, 1, kDenseStore, false, false>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)c);
+  cfg.blockDim = dim3(kDenseThreads);
+  cfg.dynamicSmemBytes = kDenseSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmem) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  cache[dev][c].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 qat_status launch_dense(const Dense& d, cudaStream_t s) {
   if (d.m == 0 || d.n == 0) return QAT_OK;
   DenseArgs p = {};
@@ -683,7 +714,8 @@ qat_status launch_dense(const Dense& d, cudaStream_t s) {
     const int64_t tiles = (int64_t)p.mt * p.nt * p.problems;
     const int64_t units = (int64_t)p.segs * (f32 ? Units<F32>::per_segment(p.kt) : p.kt);
     const int least = f32 ? 1 : 4;
-    while (p.split < 8 && tiles * p.split * 2 <= sms && units >= p.split * 2 * least) p.split *= 2;
+    for (int c = 2; c <= 8; ++c)
+      if (tiles <= resident_clusters(c) && units >= c * least) p.split = c;
   }
   const int nb = gated ? 2 : d.segs, na = d.problems > 1 ? d.problems : d.segs;
   for (int i = 0; i < 2; ++i) {

@@ -72,6 +72,8 @@ template <typename T, bool DOUBLE, int NW>
 __global__ void __launch_bounds__(128) k_w4_generic(const void* __restrict__ x, int64_t tokens,
                                                     W4 wa, W4 wb, int64_t rows, int64_t cols,
                                                     int act, void* __restrict__ y, int y_bf16) {
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (n >= rows) return;
@@ -95,23 +97,26 @@ __global__ void __launch_bounds__(128) k_w4_generic(const void* __restrict__ x, 
 // ---------------------------------------------------------------------------
 // Rows of whole 8-code words whose units are whole runs of 32 codes.
 //
-// A warp multiplies 16 rows (of each of R row tiles and NW weights) by 8 NT
-// tokens with m16n8k16 tensor-core products: a code is exact in bf16 (128 + q
-// with the low mantissa bits, one logic operation for two codes, then an exact
-// subtraction of 136 + zero point), so is a bf16 x, and the sums are binary32.
-// Arithmetic per code is then about 1.4 instructions, which keeps reading the
-// codes the bound; scalar multiply-adds would need four.  A float x is split
-// into TERMS bf16 values (high, middle, low: 3 hold all its 24 bits, 2 hold 16,
-// enough under a bf16 output), one product each.
+// A warp multiplies 16 rows (of each of NW weights) by 8 NT tokens with
+// m16n8k16 tensor-core products: a code is exact in bf16 (128 + q with the low
+// mantissa bits, one logic operation for two codes, then an exact subtraction
+// of 136 + zero point), so is a bf16 x, and the sums are binary32.  That is about
+// 1.5 instructions a code, which keeps reading the codes the bound; scalar
+// multiply-adds would need four.  A float x comes as TERMS bf16 planes (high,
+// middle, low: three hold all its 24 bits, two hold 16, enough under a bf16
+// output), one product each.
 //
 // k runs in blocks of 32 CH codes: lane t of a row's four takes 8 CH
 // consecutive codes (one load), so a load instruction covers 16 CH bytes of
-// each of 8 rows.  The order of k inside a block is the codes' bit order, the
-// same for both operands.  The block's 8 warps take blocks in turn, the CTAs of
-// a cluster split them once more where rows are few; partial sums are added in
-// shared memory, then over the cluster in rank order.
+// each of 8 rows.  The order of k inside a word is the codes' bit order, the
+// same for both operands.  The warps of a block split k (and, with more tokens,
+// also the rows, so that they read the same x from L1) and walk over the
+// block's row tiles with the codes of the next blocks of k in flight across the
+// tiles.  Where rows are few a cluster splits k once more.  Partial sums are
+// added in shared memory, then over the cluster, in a fixed order.
 // ---------------------------------------------------------------------------
 constexpr int kW4Warps = 8;
+enum { kOutF32 = 0, kOutBf16 = 1, kOutPlanes = 2 };
 
 struct W4Fast {
   const uint8_t* codes;
@@ -121,14 +126,16 @@ struct W4Fast {
 };
 struct W4Args {
   W4Fast w[2];
-  const void* x;
+  const void* x;           // bf16 rows, or planes
+  int64_t x_pitch, x_plane;
   void* y;
+  int64_t y_pitch, y_plane;  // planes
   int64_t rows, tokens;
-  int64_t row_units;  // units from one row to the next
-  int64_t unit;       // codes of a unit
-  int cols;
+  int64_t row_units;       // units from one row to the next
+  int64_t unit;            // codes of a unit
+  int cols, tiles;
   uint32_t unit_magic;
-  int dbl, act, y_bf16, vec_x, split;
+  int dbl, act, out, y_terms, split;
 };
 
 // two codes of a word (bits 0-3 and 16-19 after the shift) as bf16 q - zp
@@ -139,6 +146,11 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t w, uint32_t bias) {
   asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(v), "r"(bias));
   return v;
 }
+// 136 + zp as a bf16 pair (exact)
+__device__ __forceinline__ uint32_t w4_bias(int zp) {
+  const uint32_t h = 0x4308u + (uint32_t)min(max(zp, -8), 7);
+  return h | h << 16;
+}
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -148,7 +160,6 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
 // the same with no sum before it
 __device__ __forceinline__ void mma_16816_first(float (&c)[4], uint32_t a0, uint32_t a1,
                                                 uint32_t a2, uint32_t a3, uint32_t b0,
@@ -160,62 +171,14 @@ __device__ __forceinline__ void mma_16816_first(float (&c)[4], uint32_t a0, uint
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// x of 8 consecutive k as bf16 pairs in the codes' order (1,5) (0,4) (3,7) (2,6)
-__device__ __forceinline__ void pairs_bf16(const uint4& v, uint32_t (&b)[4]) {
-  b[0] = __byte_perm(v.x, v.z, 0x7632);
-  b[1] = __byte_perm(v.x, v.z, 0x5410);
-  b[2] = __byte_perm(v.y, v.w, 0x7632);
-  b[3] = __byte_perm(v.y, v.w, 0x5410);
-}
-// the bf16 terms of one float, in the high halves
-template <int TERMS>
-__device__ __forceinline__ void split_f32(float x, uint32_t (&h)[TERMS]) {
-#pragma unroll
-  for (int i = 0; i < TERMS; ++i) h[i] = __float_as_uint(take_bf16(x));
-}
-
-template <typename T, int CH>
-struct XWords {
-  uint32_t v[CH * (T::BYTES == 2 ? 4 : 8)];
-};
-// a lane's x of 8 CH consecutive k of one token (zeros where there is none)
-template <typename T, int CH>
-__device__ __forceinline__ void load_x(XWords<T, CH>& o, const char* p, bool in, bool vec) {
-  constexpr int W = CH * (T::BYTES == 2 ? 4 : 8);
-#pragma unroll
-  for (int i = 0; i < W; ++i) o.v[i] = 0u;
-  if (!in) return;
-  if (vec) {
-#pragma unroll
-    for (int i = 0; i < W; i += 4) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
-      o.v[i] = q.x, o.v[i + 1] = q.y, o.v[i + 2] = q.z, o.v[i + 3] = q.w;
-    }
-  } else if (T::BYTES == 4) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) o.v[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
-  } else {
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-      o.v[i] = (uint32_t)__ldg(q + 2 * i) | (uint32_t)__ldg(q + 2 * i + 1) << 16;
-  }
-}
-// the B registers of word j, TERMS sets of four pairs
-template <typename T, int TERMS, int CH>
-__device__ __forceinline__ void x_pairs(const XWords<T, CH>& x, int j, uint32_t (&b)[TERMS][4]) {
-  if constexpr (T::BYTES == 2) {
-    pairs_bf16(make_uint4(x.v[j * 4], x.v[j * 4 + 1], x.v[j * 4 + 2], x.v[j * 4 + 3]), b[0]);
-  } else {
-    uint32_t h[8][TERMS];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) split_f32<TERMS>(__uint_as_float(x.v[j * 8 + i]), h[i]);
-    constexpr int lo[4] = {1, 0, 3, 2};
-#pragma unroll
-    for (int q = 0; q < TERMS; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) b[q][i] = __byte_perm(h[lo[i]][q], h[lo[i] + 4][q], 0x7632);
-  }
+// The place of element e of 8 in the codes' order, pairs (1,5) (0,4) (3,7) (2,6).
+__device__ __forceinline__ int w4_place(int e) { return (0x57134602 >> (4 * e)) & 7; }
+// x of 8 consecutive k in that order: as stored in planes, or a bf16 row's
+template <bool PLANES>
+__device__ __forceinline__ uint4 x_pairs(const uint4& v) {
+  if (PLANES) return v;
+  return make_uint4(__byte_perm(v.x, v.z, 0x7632), __byte_perm(v.x, v.z, 0x5410),
+                    __byte_perm(v.y, v.w, 0x7632), __byte_perm(v.y, v.w, 0x5410));
 }
 
 template <int CH>
@@ -237,186 +200,276 @@ __device__ __forceinline__ void load_codes(CodeWords<CH>& o, const uint8_t* p, b
   }
 }
 
-// 136 + zp as a bf16 pair (exact)
-__device__ __forceinline__ uint32_t w4_bias(int zp) {
-  const uint32_t h = 0x4308u + (uint32_t)min(max(zp, -8), 7);
-  return h | h << 16;
-}
-
-// Row tiles of a warp and the warps that share a block of k: with more tokens
-// the warps of a CTA sit side by side along the rows, so that they read the
-// same x from L1.
 template <int NT, int NW>
 struct W4Shape {
-  static constexpr int R = NW == 2 && NT == 4 ? 1 : 2;  // row tiles of each weight
-  static constexpr int RT = R * NW;
-  static constexpr int WR = NT;              // warps along the rows
-  static constexpr int WK = kW4Warps / WR;   // warps along k
-  static constexpr int kRows = 16 * R * WR;  // output rows of a CTA
+  static constexpr int WR = NT;                 // warps along the rows
+  static constexpr int WK = kW4Warps / WR;      // warps along k
+  static constexpr int kRows = 16 * WR;         // output rows of a tile
+  static constexpr int kTok = 8 * NT;
+  static constexpr int kDepth = 4 / NW;         // blocks of k in flight
+  static constexpr int kSlots = NT == 1 ? 4 : NT * NW >= 8 ? 1 : 2;  // tiles between joins
 };
 
-template <typename T, int TERMS, int CH, int NT, int NW>
-__global__ void __launch_bounds__(kW4Warps * 32, NT == 1 && NW == 1 ? 2 : 1)
+template <bool PLANES, int TERMS, int CH, int NT, int NW>
+__global__ void __launch_bounds__(kW4Warps * 32, NT == 4 ? 1 : 2)
     k_w4(const __grid_constant__ W4Args p) {
   using S = W4Shape<NT, NW>;
-  constexpr int R = S::R, RT = S::RT, kTok = 8 * NT, KB = 32 * CH;
-  __shared__ float red[S::WK][NW][S::kRows][kTok];
+  constexpr int KB = 32 * CH, D = S::kDepth;
+  __shared__ float red[S::kSlots][S::WK][NW][S::kRows][S::kTok];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int wr = warp % S::WR, wk = warp / S::WR;
-  const int split = p.split;
+  const int wr = warp % S::WR, wk = warp / S::WR, split = p.split;
   const int rank = split > 1 ? (int)(blockIdx.x % split) : 0;
-  const int64_t n0 = (int64_t)(blockIdx.x / split) * S::kRows;
-  const int64_t tok0 = (int64_t)blockIdx.y * kTok;
+  const int first = blockIdx.x / split, stride = gridDim.x / split;
+  const int mine = (p.tiles - first + stride - 1) / stride;  // tiles of this block
+  const int64_t tok0 = (int64_t)blockIdx.y * S::kTok;
+  const int tokens = (int)min((int64_t)S::kTok, p.tokens - tok0);
   const int cols = p.cols, blocks = (cols + KB - 1) / KB, step = S::WK * split;
-  const bool vec_x = p.vec_x;
+  const int start = rank * S::WK + wk;
+  const int per_tile = start < blocks ? (blocks - start + step - 1) / step : 0;
 
-  // this lane's rows: g and g + 8 of each tile (rows past the end read row 0
-  // and are dropped at the end)
-  const uint8_t* cp[RT][2];
-  uint32_t ru[R][2];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t n = n0 + (wr * R + r) * 16 + h * 8 + g, m = n < p.rows ? n : 0;
-      ru[r][h] = (uint32_t)(m * p.row_units);
-#pragma unroll
-      for (int w = 0; w < NW; ++w) cp[w * R + r][h] = p.w[w].codes + ((m * cols) >> 1) + t * 4 * CH;
-    }
-  const char* xp[NT];
+  const __nv_bfloat16* xp[NT];
   bool xin[NT];
 #pragma unroll
   for (int q = 0; q < NT; ++q) {
-    const int64_t tok = tok0 + q * 8 + g;
-    xin[q] = tok < p.tokens;
-    xp[q] = static_cast<const char*>(p.x) + ((xin[q] ? tok : 0) * cols + t * 8 * CH) * T::BYTES;
+    xin[q] = q * 8 + g < tokens;
+    xp[q] = static_cast<const __nv_bfloat16*>(p.x) + (xin[q] ? tok0 + q * 8 + g : 0) * p.x_pitch +
+            t * 8 * CH;
   }
 
-  float total[RT][NT][4] = {};
-  CodeWords<CH> next[RT][2];
-  const auto fetch = [&](int kb) {
-    const bool in = kb * KB + t * 8 * CH < cols;
+  // the loads in flight: codes, scales and zero points of D blocks of k
+  CodeWords<CH> code[D][NW][2];
+  float sc[D][NW][2];
+  uint32_t bias[D][NW][2];
+  const uint8_t* cp[NW][2];
+  int64_t ru[2];
+  int f_tile = 0, f_kb = start;
+  // this lane's rows of the tile being fetched: g and g + 8 (rows past the end
+  // read row 0 and are dropped at the end)
+  const auto rows_of = [&](int tile) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+    for (int h = 0; h < 2; ++h) {
+      const int64_t n = (int64_t)(first + tile * stride) * S::kRows + wr * 16 + h * 8 + g;
+      const int64_t m = n < p.rows ? n : 0;
+      ru[h] = m * p.row_units;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) load_codes<CH>(next[i][h], cp[i][h] + kb * (KB / 2), in);
+      for (int w = 0; w < NW; ++w) cp[w][h] = p.w[w].codes + ((m * cols) >> 1) + t * 4 * CH;
+    }
   };
-  int kb = rank * S::WK + wk;
-  fetch(kb);
-#pragma unroll 1
-  for (; kb < blocks; kb += step) {
-    CodeWords<CH> now[RT][2];
+  const auto fetch = [&](int d) {
+    const bool in = f_kb * KB + t * 8 * CH < cols;
+    const uint32_t u = p.unit_magic == 1 ? (uint32_t)f_kb : __umulhi((uint32_t)f_kb, p.unit_magic);
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) now[i][h] = next[i][h];
-    const bool in = kb * KB + t * 8 * CH < cols;
-    XWords<T, CH> xw[NT];
-#pragma unroll
-    for (int q = 0; q < NT; ++q)
-      load_x<T, CH>(xw[q], xp[q] + (int64_t)kb * (KB * T::BYTES), in && xin[q], vec_x);
-    fetch(kb + step);
-    const uint32_t u = p.unit_magic ? __umulhi((uint32_t)kb, p.unit_magic) : 0u;
-    float sc[RT][2];
-    uint32_t bias[RT][2];
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
+    for (int w = 0; w < NW; ++w)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const W4Fast& w = p.w[i / R];
-        const uint32_t at = ru[i % R][h] + (p.unit_magic == 1 ? (uint32_t)kb : u);
+        load_codes<CH>(code[d][w][h], cp[w][h] + f_kb * (KB / 2), in);
+        const int64_t at = ru[h] + u;
         if (p.dbl)  // within an ulp of (q / 255) * super
-          sc[i][h] = (float)__ldg(static_cast<const uint8_t*>(w.scales) + at) * (1.0f / 255.0f) *
-                     __ldg(w.super + (at >> 8));
+          sc[d][w][h] = (float)__ldg(static_cast<const uint8_t*>(p.w[w].scales) + at) *
+                        (1.0f / 255.0f) * __ldg(p.w[w].super + (at >> 8));
         else
-          sc[i][h] = __ldg(static_cast<const float*>(w.scales) + at);
-        bias[i][h] = w.zp ? w4_bias(__ldg(w.zp + at)) : 0x43084308u;
+          sc[d][w][h] = __ldg(static_cast<const float*>(p.w[w].scales) + at);
+        bias[d][w][h] = p.w[w].zp ? w4_bias(__ldg(p.w[w].zp + at)) : 0x43084308u;
       }
-    float part[RT][NT][4];
-#pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      uint32_t b[NT][TERMS][4];
-#pragma unroll
-      for (int q = 0; q < NT; ++q) x_pairs<T, TERMS, CH>(xw[q], j, b[q]);
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        uint32_t a[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) a[h][e] = w4_pair(now[i][h].v[j] >> (4 * e), bias[i][h]);
-#pragma unroll
-        for (int q = 0; q < NT; ++q)
-#pragma unroll
-          for (int m = TERMS - 1; m >= 0; --m) {
-            if (j == 0 && m == TERMS - 1)
-              mma_16816_first(part[i][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m][0], b[q][m][1]);
-            else
-              mma_16816(part[i][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m][0], b[q][m][1]);
-            mma_16816(part[i][q], a[0][2], a[1][2], a[0][3], a[1][3], b[q][m][2], b[q][m][3]);
-          }
-      }
+    f_kb += step;
+    if (f_kb >= blocks) {
+      f_kb = start;
+      if (++f_tile < mine) rows_of(f_tile);
     }
+  };
+
+  // Adds the partial sums of the tiles in the slots (the last one `last`).
+  const auto join = [&](int last, int used) {
+    __syncthreads();
+    for (int s = 0; s < used; ++s) {
+      const int64_t n0 = (int64_t)(first + (last - used + 1 + s) * stride) * S::kRows;
+      float* base = &red[s][0][0][0][0];
+      constexpr int kOne = NW * S::kRows * S::kTok;  // one warp's sums
+      if (split > 1) {
+        for (int i = threadIdx.x; i < NW * S::kRows * S::kTok; i += kW4Warps * 32) {
+          float v = base[i];
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+          for (int w = 1; w < S::WK; ++w) v += base[w * kOne + i];
+          base[i] = v;
+        }
+        tc::cluster_sync();
+      }
+      for (int i = threadIdx.x + rank * kW4Warps * 32; i < S::kRows * tokens;
+           i += kW4Warps * 32 * split) {
+        const int r = i % S::kRows, c = i / S::kRows, at = r * S::kTok + c;
+        const int64_t n = n0 + r;
+        if (n >= p.rows) continue;
+        float v = 0.0f, u = 0.0f;
+        if (split > 1) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            if (q >= split) break;
+            v += tc::ld_cluster(tc::map_rank(tc::smem(base + at), q));
+            if (NW == 2) u += tc::ld_cluster(tc::map_rank(tc::smem(base + kOne / 2 + at), q));
+          }
+        } else {
+#pragma unroll
+          for (int w = 0; w < S::WK; ++w) {
+            v += base[w * kOne + at];
+            if (NW == 2) u += base[w * kOne + kOne / 2 + at];
+          }
+        }
+        if (NW == 2) v = act_value(p.act, v) * u;
+        const int64_t tok = tok0 + c;
+        if (p.out == kOutBf16) {
+          st_elem<BF16>(p.y, tok * p.rows + n, v);
+        } else if (p.out == kOutF32) {
+          st_elem<F32>(p.y, tok * p.rows + n, v);
+        } else {
+          const int64_t o = tok * p.y_pitch + (n & ~INT64_C(7)) + w4_place((int)(n & 7));
+          for (int q = 0; q < p.y_terms; ++q) st_elem<BF16>(p.y, o + q * p.y_plane, take_bf16(v));
+        }
+      }
+      if (split > 1) tc::cluster_sync();  // the other CTAs have read these sums
+    }
+    __syncthreads();
+  };
+
+  float total[NW][NT][4] = {};
+  int tile = 0, left = per_tile, slot = 0;
+  const auto flush = [&]() {
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
 #pragma unroll
       for (int q = 0; q < NT; ++q)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          total[i][q][e] = fmaf(part[i][q][e], sc[i][e >> 1], total[i][q][e]);
-  }
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int q = 0; q < NT; ++q)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float2*>(
-            &red[wk][i / R][(wr * R + i % R) * 16 + h * 8 + g][q * 8 + 2 * t]) =
-            make_float2(total[i][q][2 * h], total[i][q][2 * h + 1]);
-  __syncthreads();
-  const int tokens = (int)min((int64_t)kTok, p.tokens - tok0);
-  // this CTA's sums over its warps, in red[0]
-  for (int i = threadIdx.x; i < NW * S::kRows * tokens; i += kW4Warps * 32) {
-    const int r = i % (NW * S::kRows), c = i / (NW * S::kRows);
-    float* at = &red[0][0][r][c];
-    float v = *at;
-#pragma unroll
-    for (int w = 1; w < S::WK; ++w) v += at[w * NW * S::kRows * kTok];
-    *at = v;
-  }
-  if (split > 1)
-    tc::cluster_sync();
-  else
-    __syncthreads();
-  for (int i = threadIdx.x + rank * kW4Warps * 32; i < S::kRows * tokens;
-       i += kW4Warps * 32 * split) {
-    const int r = i % S::kRows, c = i / S::kRows;
-    if (n0 + r >= p.rows) continue;
-    float v = 0.0f, u = 0.0f;
-    if (split > 1) {
-      for (int q = 0; q < split; ++q) {
-        v += tc::ld_cluster(tc::map_rank(tc::smem(&red[0][0][r][c]), q));
-        if (NW == 2) u += tc::ld_cluster(tc::map_rank(tc::smem(&red[0][NW - 1][r][c]), q));
-      }
-    } else {
-      v = red[0][0][r][c];
-      if (NW == 2) u = red[0][NW - 1][r][c];
+        for (int h = 0; h < 2; ++h) {
+          *reinterpret_cast<float2*>(&red[slot][wk][w][wr * 16 + h * 8 + g][q * 8 + 2 * t]) =
+              make_float2(total[w][q][2 * h], total[w][q][2 * h + 1]);
+          total[w][q][2 * h] = total[w][q][2 * h + 1] = 0.0f;
+        }
+    if (++slot == S::kSlots || tile + 1 == mine) {
+      join(tile, slot);
+      slot = 0;
     }
-    if (NW == 2) v = act_value(p.act, v) * u;
-    const int64_t at = (tok0 + c) * p.rows + n0 + r;
-    if (p.y_bf16)
-      st_elem<BF16>(p.y, at, v);
-    else
-      st_elem<F32>(p.y, at, v);
+    ++tile;
+    left = per_tile;
+  };
+
+  const int work = per_tile * mine;
+  if (work) rows_of(0);
+  pdl_trigger();
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (d < work) fetch(d);
+  pdl_wait();  // x may be the previous kernel's output; the weights are not
+  int kb = start;
+  for (int it = 0; it < work; it += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (it + d >= work) break;
+      const bool in = kb * KB + t * 8 * CH < cols;
+      float part[NW][NT][4];
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        uint4 b[NT][TERMS];
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+#pragma unroll
+          for (int m = 0; m < TERMS; ++m) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (in && xin[q])
+              v = __ldg(reinterpret_cast<const uint4*>(xp[q] + m * p.x_plane + kb * KB) + j);
+            b[q][m] = x_pairs<PLANES>(v);
+          }
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          uint32_t a[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              a[h][e] = w4_pair(code[d][w][h].v[j] >> (4 * e), bias[d][w][h]);
+#pragma unroll
+          for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int m = TERMS - 1; m >= 0; --m) {
+              if (j == 0 && m == TERMS - 1)
+                mma_16816_first(part[w][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m].x, b[q][m].y);
+              else
+                mma_16816(part[w][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m].x, b[q][m].y);
+              mma_16816(part[w][q], a[0][2], a[1][2], a[0][3], a[1][3], b[q][m].z, b[q][m].w);
+            }
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            total[w][q][e] = fmaf(part[w][q][e], sc[d][w][e >> 1], total[w][q][e]);
+      if (it + d + D < work) fetch(d);
+      kb += step;
+      if (--left == 0) {
+        kb = start;
+        flush();
+      }
+    }
   }
-  if (split > 1) tc::cluster_sync();  // the other CTAs have read red
+  if (!work)  // more warps than blocks of k: nothing to add, but the joins to make
+    while (tile < mine) flush();
 }
 
-template <typename T, int TERMS, int CH, int NT, int NW>
-static qat_status launch_fast(W4Args p, cudaStream_t s) {
+// x [tokens, cols] as planes (cols a multiple of 8): a thread takes 8 elements.
+template <typename T>
+__global__ void __launch_bounds__(256) k_w4_planes(const void* __restrict__ x, int64_t total,
+                                                   int terms, int64_t plane,
+                                                   __nv_bfloat16* __restrict__ out) {
+  pdl_trigger();
+  pdl_wait();
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i >= total) return;
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = ld_elem<T>(x, i + e);
+  for (int q = 0; q < terms; ++q) {
+    float h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = take_bf16(v[e]);
+    *reinterpret_cast<uint4*>(out + q * plane + i) =
+        make_uint4(pack_bf16x2(h[1], h[5]), pack_bf16x2(h[0], h[4]), pack_bf16x2(h[3], h[7]),
+                   pack_bf16x2(h[2], h[6]));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+static cudaError_t launch_w4_kernel(void (*k)(W4Args), dim3 grid, int cluster, bool pdl,
+                                    const W4Args& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kW4Warps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, p);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e;
+}
+
+template <bool PLANES, int TERMS, int CH, int NT, int NW>
+static qat_status launch_fast(W4Args p, bool pdl, cudaStream_t s) {
   using S = W4Shape<NT, NW>;
-  const int64_t row_blocks = (p.rows + S::kRows - 1) / S::kRows;
+  p.tiles = (int)((p.rows + S::kRows - 1) / S::kRows);
   const int kblocks = (p.cols + 32 * CH - 1) / (32 * CH);
   // units of a row: none (whole rows), one a block, or kb / per_unit by
   // multiplication (exact while blocks^2 < 2^32)
@@ -424,50 +477,36 @@ static qat_status launch_fast(W4Args p, cudaStream_t s) {
   p.unit_magic = p.unit >= p.cols ? 0u
                  : per_unit == 1  ? 1u
                                   : (uint32_t)((UINT64_C(1) << 32) / per_unit + 1);
-  // a cluster splits k while two CTAs a SM are not reached and every warp keeps
-  // a block
+  const int room = device_info().sms * (NT == 4 ? 1 : 2);
+  // a cluster splits k while the GPU has room and every warp keeps a block
   p.split = 1;
-  const int64_t room = (int64_t)device_info().sms * 2;
-  while (p.split < 8 && row_blocks * p.split * 2 <= room && kblocks >= p.split * 2 * S::WK)
+  while (p.split < 8 && p.tiles * p.split * 2 <= room && kblocks >= p.split * 2 * S::WK)
     p.split *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(row_blocks * p.split), (unsigned)((p.tokens + 8 * NT - 1) / (8 * NT)));
-  cfg.blockDim = dim3(kW4Warps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, k_w4<T, TERMS, CH, NT, NW>, p) != cudaSuccess) {
-    (void)cudaGetLastError();
+  const unsigned blocks = (unsigned)(p.split > 1 ? p.tiles * p.split : p.tiles < room ? p.tiles : room);
+  const dim3 grid(blocks, (unsigned)((p.tokens + S::kTok - 1) / S::kTok));
+  if (launch_w4_kernel(k_w4<PLANES, TERMS, CH, NT, NW>, grid, p.split, pdl, p, s) != cudaSuccess)
     return QAT_ERR_CUDA;
-  }
   count_launch(1);
   return QAT_OK;
 }
-template <typename T, int TERMS, int CH, int NW>
-static qat_status fast_tokens(const W4Args& p, cudaStream_t s) {
-  if (p.tokens <= 8) return launch_fast<T, TERMS, CH, 1, NW>(p, s);
-  if (p.tokens <= 16) return launch_fast<T, TERMS, CH, 2, NW>(p, s);
-  return launch_fast<T, TERMS, CH, 4, NW>(p, s);
+template <bool PLANES, int TERMS, int CH, int NW>
+static qat_status fast_tokens(const W4Args& p, bool pdl, cudaStream_t s) {
+  if (p.tokens <= 8) return launch_fast<PLANES, TERMS, CH, 1, NW>(p, pdl, s);
+  if (p.tokens <= 16) return launch_fast<PLANES, TERMS, CH, 2, NW>(p, pdl, s);
+  return launch_fast<PLANES, TERMS, CH, 4, NW>(p, pdl, s);
 }
-template <typename T, int TERMS, int NW>
-static qat_status fast_chunk(const W4Args& p, int ch, cudaStream_t s) {
-  if (ch == 4) return fast_tokens<T, TERMS, 4, NW>(p, s);
-  if (ch == 2) return fast_tokens<T, TERMS, 2, NW>(p, s);
-  return fast_tokens<T, TERMS, 1, NW>(p, s);
+template <bool PLANES, int TERMS, int NW>
+static qat_status fast_chunk(const W4Args& p, int ch, bool pdl, cudaStream_t s) {
+  if (ch == 4) return fast_tokens<PLANES, TERMS, 4, NW>(p, pdl, s);
+  if (ch == 2) return fast_tokens<PLANES, TERMS, 2, NW>(p, pdl, s);
+  return fast_tokens<PLANES, TERMS, 1, NW>(p, pdl, s);
 }
 
 // Words of 8 codes a lane takes at once: the widest load that rows, units and
 // blocks of k allow; 0 when the shape needs the generic kernel (longer rows and
-// more units than the 32-bit indexes hold too).
+// more rows than the 32-bit indexes hold too).
 static int w4_chunk(const qat_weight4& w) {
-  if (w.cols % 8 || w.cols > (1 << 20) || w.rows > (1 << 30)) return 0;
-  if (w.layout != QAT_PER_TENSOR && w.layout != QAT_PER_ROW && w.rows * w.cols >= (INT64_C(1) << 36))
-    return 0;
+  if (w.cols <= 0 || w.cols % 8 || w.cols > (1 << 20) || w.rows > (1 << 28)) return 0;
   if (w.layout == QAT_PER_TENSOR || w.layout == QAT_PER_ROW)
     return w.cols % 32 == 0 ? 4 : w.cols % 16 == 0 ? 2 : 1;
   const int64_t unit = w.layout == QAT_W4_DOUBLE ? 64 : w.group;
@@ -475,28 +514,50 @@ static int w4_chunk(const qat_weight4& w) {
   return unit % 128 == 0 ? 4 : unit % 64 == 0 ? 2 : unit % 32 == 0 ? 1 : 0;
 }
 
-static qat_status launch_w4_fast(const void* x, qat_dtype xdt, int64_t tokens,
-                                 const qat_weight4* w, int nw, int act, void* y, qat_dtype ydt,
-                                 int ch, cudaStream_t s) {
+// A product's x: its type's rows, or planes of `terms` parts.
+struct X4 {
+  const void* p;
+  qat_dtype dt;
+  int terms;  // 0: rows
+  int64_t pitch, plane;
+};
+// Its y, likewise (planes only from the gated pair).
+struct Y4 {
+  void* p;
+  qat_dtype dt;
+  int terms;
+  int64_t pitch, plane;
+};
+
+static qat_status run_fast(const X4& x, int64_t tokens, const qat_weight4* w, int nw, int act,
+                           const Y4& y, int ch, bool pdl, cudaStream_t s) {
   W4Args p = {};
   for (int i = 0; i < nw; ++i)
     p.w[i] = W4Fast{static_cast<const uint8_t*>(w[i].codes), w[i].scales, w[i].zero_points,
                     w[i].super_scales};
-  p.x = x;
-  p.y = y;
+  p.x = x.p;
+  p.x_pitch = x.terms ? x.pitch : w->cols;
+  p.x_plane = x.plane;
+  p.y = y.p;
+  p.y_pitch = y.pitch;
+  p.y_plane = y.plane;
+  p.y_terms = y.terms;
+  p.out = y.terms ? kOutPlanes : y.dt == QAT_BF16 ? kOutBf16 : kOutF32;
   p.rows = w->rows;
   p.cols = (int)w->cols;
   p.tokens = tokens;
-  p.vec_x = w->cols % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0;
   p.dbl = w->layout == QAT_W4_DOUBLE;
   p.unit = w->layout == QAT_PER_GROUP ? w->group : p.dbl ? 64 : w->cols;
   p.row_units = w->layout == QAT_PER_TENSOR ? 0 : w->cols / p.unit;
   p.act = act;
-  p.y_bf16 = ydt == QAT_BF16;
-  if (xdt == QAT_BF16)
-    return nw == 2 ? fast_chunk<BF16, 1, 2>(p, ch, s) : fast_chunk<BF16, 1, 1>(p, ch, s);
-  if (nw == 2) return fast_chunk<F32, 3, 2>(p, ch, s);
-  return p.y_bf16 ? fast_chunk<F32, 2, 1>(p, ch, s) : fast_chunk<F32, 3, 1>(p, ch, s);
+  if (nw == 2)
+    return x.terms == 0   ? fast_chunk<false, 1, 2>(p, ch, pdl, s)
+           : x.terms == 1 ? fast_chunk<true, 1, 2>(p, ch, pdl, s)
+                          : fast_chunk<true, 3, 2>(p, ch, pdl, s);
+  return x.terms == 0   ? fast_chunk<false, 1, 1>(p, ch, pdl, s)
+         : x.terms == 1 ? fast_chunk<true, 1, 1>(p, ch, pdl, s)
+         : x.terms == 2 ? fast_chunk<true, 2, 1>(p, ch, pdl, s)
+                        : fast_chunk<true, 3, 1>(p, ch, pdl, s);
 }
 
 static W4 w4_of(const qat_weight4& w) {
@@ -513,33 +574,131 @@ static W4 w4_of(const qat_weight4& w) {
   return r;
 }
 
-qat_status launch_w4(const void* x, qat_dtype xdt, int64_t tokens, const qat_weight4* w, int nw,
-                     int act, void* y, qat_dtype ydt, cudaStream_t s) {
+static qat_status run_generic(const void* x, qat_dtype xdt, int64_t tokens, const qat_weight4* w,
+                              int nw, int act, void* y, qat_dtype ydt, bool pdl, cudaStream_t s) {
   const W4 a = w4_of(w[0]), b = w4_of(w[nw - 1]);
   const bool dbl = w->layout == QAT_W4_DOUBLE;
-  const int ch = w->cols > 0 && tokens <= 65535 * 8 ? w4_chunk(*w) : 0;
-  if (ch) return launch_w4_fast(x, xdt, tokens, w, nw, act, y, ydt, ch, s);
   // gridDim.y holds 65535 token tiles: longer inputs in several launches
   constexpr int64_t kMost = (int64_t)65535 * kGenTokens;
   for (int64_t t0 = 0; t0 < tokens; t0 += kMost) {
     const int64_t nt = tokens - t0 < kMost ? tokens - t0 : kMost;
     const dim3 grid((unsigned)((w->rows + 3) / 4), (unsigned)((nt + kGenTokens - 1) / kGenTokens));
-    const char* xp = static_cast<const char*>(x) + t0 * w->cols * (xdt == QAT_F32 ? 4 : 2);
-    char* yp = static_cast<char*>(y) + t0 * w->rows * (ydt == QAT_F32 ? 4 : 2);
+    const void* xp = static_cast<const char*>(x) + t0 * w->cols * (xdt == QAT_F32 ? 4 : 2);
+    void* yp = static_cast<char*>(y) + t0 * w->rows * (ydt == QAT_F32 ? 4 : 2);
     const int yb = ydt == QAT_BF16;
-#define QAT_W4_GO(T, D, N) \
-  k_w4_generic<T, D, N><<<grid, 128, 0, s>>>(xp, nt, a, b, w->rows, w->cols, act, yp, yb)
-#define QAT_W4_D(T, D) (nw == 2 ? QAT_W4_GO(T, D, 2) : QAT_W4_GO(T, D, 1))
-    if (xdt == QAT_F32) {
-      if (dbl) QAT_W4_D(F32, true); else QAT_W4_D(F32, false);
-    } else {
-      if (dbl) QAT_W4_D(BF16, true); else QAT_W4_D(BF16, false);
+    const auto go = [&](auto kernel) {
+      return launch_kernel(kernel, grid, dim3(128), 0, s, pdl || t0 > 0, xp, nt, a, b, w->rows,
+                           w->cols, act, yp, yb);
+    };
+    cudaError_t e;
+    if (xdt == QAT_F32)
+      e = nw == 2 ? (dbl ? go(k_w4_generic<F32, true, 2>) : go(k_w4_generic<F32, false, 2>))
+                  : (dbl ? go(k_w4_generic<F32, true, 1>) : go(k_w4_generic<F32, false, 1>));
+    else
+      e = nw == 2 ? (dbl ? go(k_w4_generic<BF16, true, 2>) : go(k_w4_generic<BF16, false, 2>))
+                  : (dbl ? go(k_w4_generic<BF16, true, 1>) : go(k_w4_generic<BF16, false, 1>));
+    if (e != cudaSuccess) {
+      (void)cudaGetLastError();
+      return QAT_ERR_CUDA;
     }
-#undef QAT_W4_D
-#undef QAT_W4_GO
     count_launch(1);
   }
-  return launch_status();
+  return QAT_OK;
+}
+
+// Tokens of a launch of the fast kernel at most (gridDim.y).
+constexpr int64_t kFastTokens = (int64_t)65535 * 8;
+static bool fast_ok(const qat_weight4& w, int64_t tokens) {
+  return w4_chunk(w) != 0 && tokens <= kFastTokens;
+}
+
+// bf16 rows that can be read as they are need no planes
+static int x_terms(const void* x, qat_dtype dt, qat_dtype ydt) {
+  if (dt == QAT_BF16) return reinterpret_cast<uintptr_t>(x) % 16 == 0 ? 0 : 1;
+  return ydt == QAT_BF16 ? 2 : 3;
+}
+static int64_t plane_of(int64_t tokens, int64_t pitch) { return (tokens * pitch + 7) / 8 * 8; }
+
+static qat_status make_planes(const void* x, qat_dtype dt, int64_t tokens, int64_t cols, int terms,
+                              void* out, bool pdl, X4* r, cudaStream_t s) {
+  *r = X4{out, QAT_BF16, terms, cols, plane_of(tokens, cols)};
+  const int64_t total = tokens * cols;
+  const dim3 grid((unsigned)((total / 8 + 255) / 256));
+  auto* o = static_cast<__nv_bfloat16*>(out);
+  const cudaError_t e =
+      dt == QAT_F32
+          ? launch_kernel(k_w4_planes<F32>, grid, dim3(256), 0, s, pdl, x, total, terms, r->plane, o)
+          : launch_kernel(k_w4_planes<BF16>, grid, dim3(256), 0, s, pdl, x, total, terms, r->plane, o);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return QAT_ERR_CUDA;
+  }
+  count_launch(1);
+  return QAT_OK;
+}
+
+// y = act(x W0^T) * (x W1^T) (nw = 2) or x W^T; `planes` is room for x's planes.
+// *launched: a kernel of this call ran before.
+static qat_status product(const void* x, qat_dtype dt, int64_t tokens, const qat_weight4* w, int nw,
+                          int act, const Y4& y, void* planes, bool* launched, cudaStream_t s) {
+  const int ch = w4_chunk(*w);
+  if (!fast_ok(*w, tokens)) {
+    const bool pdl = *launched;
+    *launched = true;
+    return run_generic(x, dt, tokens, w, nw, act, y.p, y.dt, pdl, s);
+  }
+  // the gated pair's sums go through act, and its planes hold what y needs
+  const int terms = x_terms(x, dt, nw == 2 ? QAT_F32 : y.dt);
+  X4 xv = {x, dt, 0, 0, 0};
+  if (terms) {
+    const qat_status st = make_planes(x, dt, tokens, w->cols, terms, planes, *launched, &xv, s);
+    if (st) return st;
+    *launched = true;
+  }
+  const bool pdl = *launched;
+  *launched = true;
+  return run_fast(xv, tokens, w, nw, act, y, ch, pdl, s);
+}
+
+static size_t r256(size_t b) { return (b + 255) / 256 * 256; }
+static size_t planes_bytes(int64_t tokens, int64_t cols, int terms) {
+  return r256((size_t)plane_of(tokens, (cols + 7) / 8 * 8) * terms * 2);
+}
+
+size_t linear4_ws_bytes(qat_dtype dt, int64_t tokens, int64_t cols) {
+  return planes_bytes(tokens, cols, dt == QAT_F32 ? 3 : 1);
+}
+qat_status launch_linear4(const void* x, qat_dtype dt, int64_t tokens, const qat_weight4& w, void* y,
+                          void* ws, cudaStream_t s) {
+  bool launched = false;
+  return product(x, dt, tokens, &w, 1, 0, Y4{y, dt, 0, 0, 0}, ws, &launched, s);
+}
+
+// workspace: x's planes, then h (float, or its planes), then planes of a float h
+size_t gated4_ws_bytes(qat_dtype dt, int64_t tokens, int64_t dim, int64_t hidden) {
+  return planes_bytes(tokens, dim, dt == QAT_F32 ? 3 : 1) +
+         r256((size_t)tokens * hidden * 4) + planes_bytes(tokens, hidden, 3);
+}
+qat_status launch_gated4(const void* x, qat_dtype dt, int64_t tokens, const qat_weight4* gate_up,
+                         const qat_weight4& down, int act, void* y, void* ws, cudaStream_t s) {
+  const int64_t dim = gate_up->cols, hidden = gate_up->rows;
+  char* base = static_cast<char*>(ws);
+  char* h = base + planes_bytes(tokens, dim, dt == QAT_F32 ? 3 : 1);
+  char* h_planes = h + r256((size_t)tokens * hidden * 4);
+  bool launched = false;
+  if (fast_ok(*gate_up, tokens) && fast_ok(down, tokens)) {
+    // h straight as the second product's planes
+    const int terms = dt == QAT_BF16 ? 2 : 3;
+    const Y4 hy = {h_planes, QAT_F32, terms, hidden, plane_of(tokens, hidden)};
+    const qat_status st = product(x, dt, tokens, gate_up, 2, act, hy, base, &launched, s);
+    if (st) return st;
+    return run_fast(X4{h_planes, QAT_BF16, terms, hy.pitch, hy.plane}, tokens, &down, 1, 0,
+                    Y4{y, dt, 0, 0, 0}, w4_chunk(down), true, s);
+  }
+  const qat_status st =
+      product(x, dt, tokens, gate_up, 2, act, Y4{h, QAT_F32, 0, 0, 0}, base, &launched, s);
+  if (st) return st;
+  return product(h, QAT_F32, tokens, &down, 1, 0, Y4{y, dt, 0, 0, 0}, h_planes, &launched, s);
 }
 
 }  // namespace qat

@@ -10,9 +10,13 @@
 
 namespace qat {
 
-// Products with 4-bit weights; nw = 2: the gated pair (h float, act applied).
-qat_status launch_w4(const void* x, qat_dtype xdt, int64_t tokens, const qat_weight4* w, int nw,
-                     int act, void* y, qat_dtype ydt, cudaStream_t s);
+// Products with 4-bit weights (y in x's dtype) and the gated block from codes.
+size_t linear4_ws_bytes(qat_dtype dt, int64_t tokens, int64_t cols);
+qat_status launch_linear4(const void* x, qat_dtype dt, int64_t tokens, const qat_weight4& w, void* y,
+                          void* ws, cudaStream_t s);
+size_t gated4_ws_bytes(qat_dtype dt, int64_t tokens, int64_t dim, int64_t hidden);
+qat_status launch_gated4(const void* x, qat_dtype dt, int64_t tokens, const qat_weight4* gate_up,
+                         const qat_weight4& down, int act, void* y, void* ws, cudaStream_t s);
 
 // Row partials of dweight / dbias that the layer norm's backward pass keeps in
 // its workspace: [2][parts][cols] floats.  Enough parts for every resident

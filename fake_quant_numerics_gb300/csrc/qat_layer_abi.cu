@@ -38,18 +38,6 @@ qat_status check_w4(const qat_weight4* w) {
   return QAT_OK;
 }
 
-qat_status check_w4_call(const void* x, qat_dtype xdt, int64_t tokens, const qat_weight4* w,
-                         const void* y, qat_dtype ydt) {
-  if (!dtype_ok(xdt) || !dtype_ok(ydt)) return QAT_ERR_UNSUPPORTED;
-  const qat_status st = check_w4(w);
-  if (st) return st;
-  if (!fits(tokens, w->cols) || !fits(tokens, w->rows)) return QAT_ERR_INVALID_ARGUMENT;
-  if (tokens == 0 || w->rows == 0) return QAT_OK;
-  if ((!x && w->cols > 0) || !y) return QAT_ERR_INVALID_ARGUMENT;
-  if (!on(x, esize(xdt)) || !on(y, esize(ydt))) return QAT_ERR_MISALIGNED;
-  return QAT_OK;
-}
-
 bool ffn_sizes_ok(int64_t t, int64_t d, int64_t f) {
   // coordinates of the tensor copies are 32-bit
   constexpr int64_t most = INT32_MAX - 4096;
@@ -60,31 +48,57 @@ bool ffn_sizes_ok(int64_t t, int64_t d, int64_t f) {
 
 extern "C" {
 
-qat_status qat_linear4(const void* x, qat_dtype x_dtype, int64_t tokens, const qat_weight4* w,
-                       void* y, qat_dtype y_dtype, qat_stream_t stream) {
-  qat::NvtxScope nvtx("qat_linear4");
-  const qat_status st = check_w4_call(x, x_dtype, tokens, w, y, y_dtype);
-  if (st) return st;
-  if (tokens == 0 || w->rows == 0) return QAT_OK;
-  return launch_w4(x, x_dtype, tokens, w, 1, 0, y, y_dtype, reinterpret_cast<cudaStream_t>(stream));
+size_t qat_linear4_workspace_bytes(qat_dtype dtype, int64_t tokens, int64_t cols) {
+  if (!dtype_ok(dtype) || !fits(tokens, cols)) return 0;
+  return linear4_ws_bytes(dtype, tokens, cols);
 }
 
-qat_status qat_gated4(const void* x, qat_dtype x_dtype, int64_t tokens, const qat_weight4* gate,
-                      const qat_weight4* up, qat_activation act, float* h, qat_stream_t stream) {
-  qat::NvtxScope nvtx("qat_gated4");
-  if (!act_ok(act)) return QAT_ERR_UNSUPPORTED;
-  qat_status st = check_w4_call(x, x_dtype, tokens, gate, h, QAT_F32);
+qat_status qat_linear4(const void* x, qat_dtype dtype, int64_t tokens, const qat_weight4* w, void* y,
+                       void* workspace, size_t workspace_bytes, qat_stream_t stream) {
+  qat::NvtxScope nvtx("qat_linear4");
+  if (!dtype_ok(dtype)) return QAT_ERR_UNSUPPORTED;
+  const qat_status st = check_w4(w);
   if (st) return st;
-  st = check_w4(up);
-  if (st) return st;
+  if (!fits(tokens, w->cols) || !fits(tokens, w->rows)) return QAT_ERR_INVALID_ARGUMENT;
+  if (tokens == 0 || w->rows == 0) return QAT_OK;
+  if ((!x && w->cols > 0) || !y) return QAT_ERR_INVALID_ARGUMENT;
+  if (!on(x, esize(dtype)) || !on(y, esize(dtype))) return QAT_ERR_MISALIGNED;
+  const size_t need = linear4_ws_bytes(dtype, tokens, w->cols);
+  if (need && (!workspace || workspace_bytes < need)) return QAT_ERR_WORKSPACE;
+  if (need && !on(workspace, 16)) return QAT_ERR_MISALIGNED;
+  return launch_linear4(x, dtype, tokens, *w, y, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t qat_gated_ffn4_workspace_bytes(qat_dtype dtype, int64_t tokens, int64_t dim,
+                                      int64_t hidden) {
+  if (!dtype_ok(dtype) || !fits(tokens, dim) || !fits(tokens, hidden)) return 0;
+  return gated4_ws_bytes(dtype, tokens, dim, hidden);
+}
+
+qat_status qat_gated_ffn4(const void* x, qat_dtype dtype, int64_t tokens, const qat_weight4* gate,
+                          const qat_weight4* up, const qat_weight4* down, qat_activation act,
+                          void* y, void* workspace, size_t workspace_bytes, qat_stream_t stream) {
+  qat::NvtxScope nvtx("qat_gated_ffn4");
+  if (!dtype_ok(dtype) || !act_ok(act)) return QAT_ERR_UNSUPPORTED;
+  for (const qat_weight4* w : {gate, up, down}) {
+    const qat_status st = check_w4(w);
+    if (st) return st;
+  }
   if (gate->rows != up->rows || gate->cols != up->cols || gate->layout != up->layout ||
       (gate->layout == QAT_PER_GROUP && gate->group != up->group) ||
-      !gate->zero_points != !up->zero_points)
+      !gate->zero_points != !up->zero_points || down->cols != gate->rows)
     return QAT_ERR_DIMENSION_MISMATCH;
-  if (tokens == 0 || gate->rows == 0) return QAT_OK;
+  if (!fits(tokens, gate->cols) || !fits(tokens, gate->rows) || !fits(tokens, down->rows))
+    return QAT_ERR_INVALID_ARGUMENT;
+  if (tokens == 0 || down->rows == 0) return QAT_OK;
+  if ((!x && gate->cols > 0) || !y) return QAT_ERR_INVALID_ARGUMENT;
+  if (!on(x, esize(dtype)) || !on(y, esize(dtype))) return QAT_ERR_MISALIGNED;
+  const size_t need = gated4_ws_bytes(dtype, tokens, gate->cols, gate->rows);
+  if (need && (!workspace || workspace_bytes < need)) return QAT_ERR_WORKSPACE;
+  if (need && !on(workspace, 16)) return QAT_ERR_MISALIGNED;
   const qat_weight4 both[2] = {*gate, *up};
-  return launch_w4(x, x_dtype, tokens, both, 2, act, h, QAT_F32,
-                   reinterpret_cast<cudaStream_t>(stream));
+  return launch_gated4(x, dtype, tokens, both, *down, act, y, workspace,
+                       reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t qat_gated_ffn_workspace_bytes(qat_dtype dtype, int64_t tokens, int64_t dim, int64_t hidden,

@@ -17,7 +17,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib
-from ._lib import (F32, GELU, PER_COLUMN, PER_GROUP, PER_ROW, PER_TENSOR, RELU, SILU, W4_DOUBLE, QatError)
+from ._lib import (GELU, PER_COLUMN, PER_GROUP, PER_ROW, PER_TENSOR, RELU, SILU, W4_DOUBLE, QatError)
 from .api import _GRAN, _dt, _nbytes, _p, _ready, _s, DoubleQuantized4Bit
 
 _ACT = {"silu": SILU, "gelu": GELU, "relu": RELU, SILU: SILU, GELU: GELU, RELU: RELU}
@@ -115,15 +115,25 @@ def _w4(w: Weight4):
     return w.struct
 
 
-def qat_linear4(x, tokens, w: Weight4, y, stream=None):
-    st = _lib.lib().qat_linear4(_p(x), _dt(x), tokens, _w4(w), _p(y), _dt(y), _s(stream))
+def qat_linear4_workspace_bytes(dtype, tokens: int, cols: int) -> int:
+    return int(_lib.lib().qat_linear4_workspace_bytes(dtype, tokens, cols))
+
+
+def qat_linear4(x, tokens, w: Weight4, y, workspace, stream=None):
+    st = _lib.lib().qat_linear4(_p(x), _dt(x), tokens, _w4(w), _p(y), _p(workspace),
+                                _nbytes(workspace), _s(stream))
     _lib.check("qat_linear4", st)
 
 
-def qat_gated4(x, tokens, gate: Weight4, up: Weight4, act, h, stream=None):
-    st = _lib.lib().qat_gated4(_p(x), _dt(x), tokens, _w4(gate), _w4(up), _ACT[act], _p(h),
-                               _s(stream))
-    _lib.check("qat_gated4", st)
+def qat_gated_ffn4_workspace_bytes(dtype, tokens: int, dim: int, hidden: int) -> int:
+    return int(_lib.lib().qat_gated_ffn4_workspace_bytes(dtype, tokens, dim, hidden))
+
+
+def qat_gated_ffn4(x, tokens, gate: Weight4, up: Weight4, down: Weight4, act, y, workspace,
+                   stream=None):
+    st = _lib.lib().qat_gated_ffn4(_p(x), _dt(x), tokens, _w4(gate), _w4(up), _w4(down), _ACT[act],
+                                   _p(y), _p(workspace), _nbytes(workspace), _s(stream))
+    _lib.check("qat_gated_ffn4", st)
 
 
 def linear4(x: torch.Tensor, weight: Weight4) -> torch.Tensor:
@@ -133,9 +143,11 @@ def linear4(x: torch.Tensor, weight: Weight4) -> torch.Tensor:
     if not shape or shape[-1] != cols:
         raise _mismatch("linear4")
     x = x.contiguous()
+    tokens, dt, lib = _leading(x, shape), _dt(x), _lib.lib()
     y = torch.empty((*shape[:-1], weight.rows), dtype=x.dtype, device=x.device)
-    dt = _dt(x)
-    st = _lib.lib().qat_linear4(_ptr(x), dt, _leading(x, shape), _w4(weight), y.data_ptr(), dt, _here(x))
+    n = lib.qat_linear4_workspace_bytes(dt, tokens, cols)
+    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    st = lib.qat_linear4(_ptr(x), dt, tokens, _w4(weight), y.data_ptr(), ws.data_ptr(), n, _here(x))
     if st:
         _lib.check("qat_linear4", st)
     return y
@@ -149,16 +161,14 @@ def gated_ffn4(x: torch.Tensor, gate: Weight4, up: Weight4, down: Weight4,
     if not shape or shape[-1] != gate.cols or down.cols != gate.rows:
         raise _mismatch("gated_ffn4")
     x = x.contiguous()
-    tokens = _leading(x, shape)
-    h = torch.empty((tokens, gate.rows), dtype=torch.float32, device=x.device)
+    tokens, dt, lib = _leading(x, shape), _dt(x), _lib.lib()
     y = torch.empty((*shape[:-1], down.rows), dtype=x.dtype, device=x.device)
-    lib, dt, stream, hp = _lib.lib(), _dt(x), _here(x), h.data_ptr()
-    st = lib.qat_gated4(_ptr(x), dt, tokens, _w4(gate), _w4(up), _ACT[activation], hp, stream)
+    n = lib.qat_gated_ffn4_workspace_bytes(dt, tokens, gate.cols, gate.rows)
+    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    st = lib.qat_gated_ffn4(_ptr(x), dt, tokens, _w4(gate), _w4(up), _w4(down), _ACT[activation],
+                            y.data_ptr(), ws.data_ptr(), n, _here(x))
     if st:
-        _lib.check("qat_gated4", st)
-    st = lib.qat_linear4(hp, F32, tokens, _w4(down), y.data_ptr(), dt, stream)
-    if st:
-        _lib.check("qat_linear4", st)
+        _lib.check("qat_gated_ffn4", st)
     return y
 
 

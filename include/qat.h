@@ -462,32 +462,39 @@ typedef struct {
 typedef enum { QAT_ACT_SILU = 0, QAT_ACT_GELU = 1, QAT_ACT_RELU = 2 } qat_activation;
 
 /*
- * y[t, n] = sum_k x[t, k] w[n, k] for a few tokens: x is x_dtype[tokens,
- * cols], y y_dtype[tokens, rows].  Products of codes and x are summed in
- * binary32 inside a unit, then scaled and summed over the units, so a scale
- * that is not finite makes its outputs NaN whatever the codes, and |x| up to
- * 2^-10 of the binary32 range is safe from overflow.  A float x is taken as
- * bf16 parts: three (all 24 bits), or two (16 bits) under a bf16 y; parts below
- * 2^-133 are lost.  Any number of
- * tokens; the weight is read once per 32 of them.  tokens == 0 or rows == 0
- * is a no-op; cols == 0 writes zeros.  QAT_ERR_INVALID_ARGUMENT: a NULL array,
- * a negative size, a group that does not divide cols, zero points with
- * QAT_W4_DOUBLE; QAT_ERR_UNSUPPORTED: an unknown dtype or layout;
- * QAT_ERR_MISALIGNED.  One launch per 32 tokens.
+ * y[t, n] = sum_k x[t, k] w[n, k] for a few tokens: x is dtype[tokens, cols], y
+ * dtype[tokens, rows].  Products of codes and x are summed in binary32 inside a
+ * unit, then scaled and summed over the units, so a scale that is not finite
+ * makes its outputs NaN whatever the codes, and |x| up to 2^-10 of the binary32
+ * range is safe from overflow.  A float x is taken as three bf16 parts that
+ * hold all 24 bits (parts below 2^-133 are lost).  Any number of tokens; the
+ * weight is read once per 32 of them.  tokens == 0 or rows == 0 is a no-op;
+ * cols == 0 writes zeros.  QAT_ERR_INVALID_ARGUMENT: a NULL array, a negative
+ * size, a group that does not divide cols, zero points with QAT_W4_DOUBLE;
+ * QAT_ERR_UNSUPPORTED: an unknown dtype or layout; QAT_ERR_MISALIGNED.
+ * workspace: qat_linear4_workspace_bytes(dtype, tokens, cols) bytes, 16-byte
+ * aligned (x's parts).  One or two launches.
  */
-qat_status qat_linear4(const void* x, qat_dtype x_dtype, int64_t tokens, const qat_weight4* w,
-                       void* y, qat_dtype y_dtype, qat_stream_t stream);
+size_t qat_linear4_workspace_bytes(qat_dtype dtype, int64_t tokens, int64_t cols);
+qat_status qat_linear4(const void* x, qat_dtype dtype, int64_t tokens, const qat_weight4* w, void* y,
+                       void* workspace, size_t workspace_bytes, qat_stream_t stream);
 
 /*
- * The first half of a gated feed-forward block from 4-bit codes:
- * h[t, f] = act(sum_k x[t, k] gate[f, k]) * (sum_k x[t, k] up[f, k]), h
- * float[tokens, rows], both products, the activation and the product in one
- * kernel.  gate and up have the same rows, cols, layout and group
- * (QAT_ERR_DIMENSION_MISMATCH otherwise) and either both zero points or
- * neither.  The second half is qat_linear4 of h.  Otherwise as qat_linear4.
+ * The gated feed-forward block from 4-bit codes: h = act(x gate^T) * (x up^T)
+ * (both products, the activation and the product in one kernel), y = h down^T.
+ * x: dtype[tokens, gate.cols]; y: dtype[tokens, down.rows].  h stays in
+ * binary32, of which the second product takes 16 bits under a bf16 y and all 24
+ * under a float one.  gate and up have the same rows, cols, layout and group
+ * and either both zero points or neither, down.cols == gate.rows
+ * (QAT_ERR_DIMENSION_MISMATCH otherwise).  workspace:
+ * qat_gated_ffn4_workspace_bytes(dtype, tokens, gate.cols, gate.rows) bytes,
+ * 16-byte aligned.  Otherwise as qat_linear4.
  */
-qat_status qat_gated4(const void* x, qat_dtype x_dtype, int64_t tokens, const qat_weight4* gate,
-                      const qat_weight4* up, qat_activation act, float* h, qat_stream_t stream);
+size_t qat_gated_ffn4_workspace_bytes(qat_dtype dtype, int64_t tokens, int64_t dim,
+                                      int64_t hidden);
+qat_status qat_gated_ffn4(const void* x, qat_dtype dtype, int64_t tokens, const qat_weight4* gate,
+                          const qat_weight4* up, const qat_weight4* down, qat_activation act,
+                          void* y, void* workspace, size_t workspace_bytes, qat_stream_t stream);
 
 /*
  * Gated feed-forward block: g = x Wg^T, u = x Wu^T, h = act(g) * u (rounded

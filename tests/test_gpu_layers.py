@@ -78,7 +78,8 @@ def test_linear4_views_and_strides():
     wide[..., ::2] = x
     assert torch.equal(fq.linear4(wide[..., ::2], w), y)
     out = off_grid(torch.zeros(6, 96, device="cuda"))
-    fq.qat_linear4(x, 6, w, out)
+    ws = torch.empty(fq.qat_linear4_workspace_bytes(0, 6, 256), dtype=torch.uint8, device="cuda")
+    fq.qat_linear4(x.float().contiguous(), 6, w, out, ws)
     assert torch.equal(out.to(torch.bfloat16).view(2, 3, 96), y)
 
 

@@ -27,14 +27,14 @@ def w4(**kw):
     return L.Weight4Struct(**a)
 
 
-def lin(lib, x=A, xdt=L.F32, tokens=2, y=A, ydt=L.F32, w=None, **kw):
-    return lib.qat_linear4(x, xdt, tokens, ctypes.byref(w4(**kw)) if w is None else w, y, ydt, None)
+def lin(lib, x=A, dt=L.F32, tokens=2, y=A, ws=A, wsb=1 << 30, **kw):
+    return lib.qat_linear4(x, dt, tokens, ctypes.byref(w4(**kw)), y, ws, wsb, None)
 
 
 def test_linear4_refusals(lib):
     inv, uns, mis = L.QAT_ERR_INVALID_ARGUMENT, L.QAT_ERR_UNSUPPORTED, L.QAT_ERR_MISALIGNED
-    assert lib.qat_linear4(A, L.F32, 2, None, A, L.F32, None) == inv
-    assert lin(lib, xdt=5) == uns and lin(lib, ydt=5) == uns
+    assert lib.qat_linear4(A, L.F32, 2, None, A, A, 1 << 30, None) == inv
+    assert lin(lib, dt=5) == uns
     assert lin(lib, layout=L.PER_COLUMN) == uns and lin(lib, layout=9) == uns
     assert lin(lib, tokens=-1) == inv and lin(lib, rows=-1) == inv and lin(lib, cols=-64) == inv
     assert lin(lib, group=48) == inv and lin(lib, group=0) == inv
@@ -45,20 +45,31 @@ def test_linear4_refusals(lib):
     assert lin(lib, rows=1 << 40, cols=1 << 20) == inv               # past the element limit
     assert lin(lib, codes=0x10004) == mis and lin(lib, scales=0x10002) == mis
     assert lin(lib, zero_points=0x10002) == mis and lin(lib, x=ODD) == mis and lin(lib, y=ODD) == mis
+    need = lib.qat_linear4_workspace_bytes(L.F32, 2, 128)
+    assert need >= 3 * 2 * 128 * 2
+    assert lin(lib, ws=None) == L.QAT_ERR_WORKSPACE and lin(lib, wsb=need - 1) == L.QAT_ERR_WORKSPACE
+    assert lin(lib, ws=ODD) == mis
     assert lin(lib, tokens=0, x=None, y=None) == L.QAT_OK
     assert lin(lib, rows=0, codes=None, scales=None, y=None) == L.QAT_OK
 
 
 def test_gated4_refusals(lib):
-    def call(act=L.SILU, h=A, up=None, **kw):
+    def call(act=L.SILU, y=A, up=None, down=None, ws=A, wsb=1 << 30, **kw):
         g, u = w4(**kw), up or w4(**kw)
-        return lib.qat_gated4(A, L.F32, 2, ctypes.byref(g), ctypes.byref(u), act, h, None)
+        d = down or w4(rows=128, cols=32, layout=L.PER_ROW)
+        return lib.qat_gated_ffn4(A, L.F32, 2, ctypes.byref(g), ctypes.byref(u), ctypes.byref(d), act,
+                                  y, ws, wsb, None)
 
     assert call(act=7) == L.QAT_ERR_UNSUPPORTED
-    assert call(h=None) == L.QAT_ERR_INVALID_ARGUMENT
+    assert call(y=None) == L.QAT_ERR_INVALID_ARGUMENT
+    assert call(y=ODD) == L.QAT_ERR_MISALIGNED
+    assert call(ws=None) == L.QAT_ERR_WORKSPACE
+    need = lib.qat_gated_ffn4_workspace_bytes(L.F32, 2, 128, 32)
+    assert call(wsb=need - 1) == L.QAT_ERR_WORKSPACE
     for other in (dict(rows=64), dict(cols=64), dict(group=32), dict(layout=L.PER_ROW),
                   dict(zero_points=0x10000)):
         assert call(up=w4(**other)) == L.QAT_ERR_DIMENSION_MISMATCH, other
+    assert call(down=w4(rows=128, cols=64, layout=L.PER_ROW)) == L.QAT_ERR_DIMENSION_MISMATCH
 
 
 def test_ffn_refusals(lib):
