@@ -28,7 +28,7 @@ __device__ __forceinline__ void w4_params(const W4& w, int64_t u, float& s, floa
     z = 0.0f;
   } else {
     s = static_cast<const float*>(w.scales)[u];
-    z = w.zp ? (float)min(max(w.zp[u], -8), 7) : 0.0f;
+    z = w.zp ? (float)w.zp[u] : 0.0f;
   }
 }
 
@@ -147,10 +147,9 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t w, uint32_t bias) {
   return v;
 }
 // 136 + zp as a bf16 pair (exact)
-__device__ __forceinline__ uint32_t w4_bias(int zp) {
-  const uint32_t h = 0x4308u + (uint32_t)min(max(zp, -8), 7);
-  return h | h << 16;
-}
+__device__ __forceinline__ uint32_t w4_bias(int zp) { return (uint32_t)(0x4308 + zp) * 0x10001u; }
+// what a lane past the end of a row takes for x
+__device__ const uint4 kZeros[4] = {};
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -186,17 +185,15 @@ struct CodeWords {
   uint32_t v[CH];
 };
 template <int CH>
-__device__ __forceinline__ void load_codes(CodeWords<CH>& o, const uint8_t* p, bool in) {
+__device__ __forceinline__ void load_codes(CodeWords<CH>& o, const uint8_t* p) {
   if constexpr (CH == 4) {
-    uint4 q = make_uint4(0, 0, 0, 0);
-    if (in) q = __ldcs(reinterpret_cast<const uint4*>(p));
+    const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p));
     o.v[0] = q.x, o.v[1] = q.y, o.v[2] = q.z, o.v[3] = q.w;
   } else if constexpr (CH == 2) {
-    uint2 q = make_uint2(0, 0);
-    if (in) q = __ldcs(reinterpret_cast<const uint2*>(p));
+    const uint2 q = __ldcs(reinterpret_cast<const uint2*>(p));
     o.v[0] = q.x, o.v[1] = q.y;
   } else {
-    o.v[0] = in ? __ldcs(reinterpret_cast<const uint32_t*>(p)) : 0u;
+    o.v[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
   }
 }
 
@@ -210,11 +207,13 @@ struct W4Shape {
   static constexpr int kSlots = NT == 1 ? 4 : NT * NW >= 8 ? 1 : 2;  // tiles between joins
 };
 
-template <bool PLANES, int TERMS, int CH, int NT, int NW>
+// TERMS 0: x is bf16 rows; else that many planes.  CH 2 with DBL: the two-level
+// scales.
+template <int TERMS, int CH, bool DBL, int NT, int NW>
 __global__ void __launch_bounds__(kW4Warps * 32, NT == 4 ? 1 : 2)
     k_w4(const __grid_constant__ W4Args p) {
   using S = W4Shape<NT, NW>;
-  constexpr int KB = 32 * CH, D = S::kDepth;
+  constexpr int KB = 32 * CH, D = S::kDepth, kTerms = TERMS ? TERMS : 1;
   __shared__ float red[S::kSlots][S::WK][NW][S::kRows][S::kTok];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int wr = warp % S::WR, wk = warp / S::WR, split = p.split;
@@ -227,105 +226,122 @@ __global__ void __launch_bounds__(kW4Warps * 32, NT == 4 ? 1 : 2)
   const int start = rank * S::WK + wk;
   const int per_tile = start < blocks ? (blocks - start + step - 1) / step : 0;
 
+  // tokens past the end read the first one's x: their columns are not used
   const __nv_bfloat16* xp[NT];
-  bool xin[NT];
 #pragma unroll
-  for (int q = 0; q < NT; ++q) {
-    xin[q] = q * 8 + g < tokens;
-    xp[q] = static_cast<const __nv_bfloat16*>(p.x) + (xin[q] ? tok0 + q * 8 + g : 0) * p.x_pitch +
-            t * 8 * CH;
-  }
+  for (int q = 0; q < NT; ++q)
+    xp[q] = static_cast<const __nv_bfloat16*>(p.x) +
+            (q * 8 + g < tokens ? tok0 + q * 8 + g : 0) * p.x_pitch + t * 8 * CH;
 
-  // the loads in flight: codes, scales and zero points of D blocks of k
+  // The loads in flight, as loaded: codes, scales and zero points of D blocks of
+  // k.  Offsets are 32-bit and the same for both weights.
   CodeWords<CH> code[D][NW][2];
-  float sc[D][NW][2];
-  uint32_t bias[D][NW][2];
-  const uint8_t* cp[NW][2];
-  int64_t ru[2];
+  uint32_t sc[D][NW][2];
+  float sup[D][NW][2];
+  int zp[D][NW][2];
+  uint32_t co[2], so[2];  // this lane's rows g and g + 8: codes, units
   int f_tile = 0, f_kb = start;
-  // this lane's rows of the tile being fetched: g and g + 8 (rows past the end
-  // read row 0 and are dropped at the end)
+  // rows past the end read row 0 and are dropped at the end
   const auto rows_of = [&](int tile) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t n = (int64_t)(first + tile * stride) * S::kRows + wr * 16 + h * 8 + g;
-      const int64_t m = n < p.rows ? n : 0;
-      ru[h] = m * p.row_units;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) cp[w][h] = p.w[w].codes + ((m * cols) >> 1) + t * 4 * CH;
+      const uint32_t n = (uint32_t)(first + tile * stride) * S::kRows + wr * 16 + h * 8 + g;
+      const uint32_t m = n < p.rows ? n : 0;
+      co[h] = (uint32_t)(((uint64_t)m * cols) >> 1) + t * 4 * CH;
+      so[h] = m * (uint32_t)p.row_units;
     }
   };
+  const uint32_t co_step = (uint32_t)(((uint64_t)stride * S::kRows * cols) >> 1);
+  const uint32_t so_step = (uint32_t)(stride * S::kRows) * (uint32_t)p.row_units;
+  const bool affine = p.w[0].zp != nullptr;
   const auto fetch = [&](int d) {
-    const bool in = f_kb * KB + t * 8 * CH < cols;
-    const uint32_t u = p.unit_magic == 1 ? (uint32_t)f_kb : __umulhi((uint32_t)f_kb, p.unit_magic);
+    // past the row's end (in its last block) the lane reads the row's first
+    // codes; x is zero there
+    const uint32_t off = f_kb * KB + t * 8 * CH < cols ? (uint32_t)f_kb * (KB / 2) : 0u - t * 4 * CH;
+    const uint32_t u = __umulhi(2u * f_kb + 1, p.unit_magic);
 #pragma unroll
     for (int w = 0; w < NW; ++w)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        load_codes<CH>(code[d][w][h], cp[w][h] + f_kb * (KB / 2), in);
-        const int64_t at = ru[h] + u;
-        if (p.dbl)  // within an ulp of (q / 255) * super
-          sc[d][w][h] = (float)__ldg(static_cast<const uint8_t*>(p.w[w].scales) + at) *
-                        (1.0f / 255.0f) * __ldg(p.w[w].super + (at >> 8));
-        else
-          sc[d][w][h] = __ldg(static_cast<const float*>(p.w[w].scales) + at);
-        bias[d][w][h] = p.w[w].zp ? w4_bias(__ldg(p.w[w].zp + at)) : 0x43084308u;
+        load_codes<CH>(code[d][w][h], p.w[w].codes + (co[h] + off));
+        const uint32_t at = so[h] + u;
+        if (DBL) {
+          sc[d][w][h] = __ldg(static_cast<const uint8_t*>(p.w[w].scales) + at);
+          sup[d][w][h] = __ldg(p.w[w].super + (at >> 8));
+        } else {
+          sc[d][w][h] = __ldg(static_cast<const uint32_t*>(p.w[w].scales) + at);
+          if (affine) zp[d][w][h] = __ldg(p.w[w].zp + at);
+        }
       }
     f_kb += step;
     if (f_kb >= blocks) {
       f_kb = start;
-      if (++f_tile < mine) rows_of(f_tile);
+      ++f_tile;
+      if ((int64_t)(first + f_tile * stride + 1) * S::kRows > p.rows) {
+        if (f_tile < mine) rows_of(f_tile);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          co[h] += co_step;
+          so[h] += so_step;
+        }
+      }
     }
   };
 
-  // Adds the partial sums of the tiles in the slots (the last one `last`).
+  // Adds the partial sums of the tiles in the first `used` slots, of which the
+  // last holds tile `last`: an output a thread.
+  constexpr int kOne = NW * S::kRows * S::kTok;  // one warp's sums of a tile
+  const auto put = [&](int r, int c, int64_t n0, float v, float u) {
+    const int64_t n = n0 + r, tok = tok0 + c;
+    if (n >= p.rows) return;
+    if (NW == 2) v = act_value(p.act, v) * u;
+    if (p.out == kOutBf16) {
+      st_elem<BF16>(p.y, tok * p.rows + n, v);
+    } else if (p.out == kOutF32) {
+      st_elem<F32>(p.y, tok * p.rows + n, v);
+    } else {
+      const int64_t o = tok * p.y_pitch + (n & ~INT64_C(7)) + w4_place((int)(n & 7));
+      for (int q = 0; q < p.y_terms; ++q) st_elem<BF16>(p.y, o + q * p.y_plane, take_bf16(v));
+    }
+  };
   const auto join = [&](int last, int used) {
     __syncthreads();
-    for (int s = 0; s < used; ++s) {
-      const int64_t n0 = (int64_t)(first + (last - used + 1 + s) * stride) * S::kRows;
-      float* base = &red[s][0][0][0][0];
-      constexpr int kOne = NW * S::kRows * S::kTok;  // one warp's sums
-      if (split > 1) {
-        for (int i = threadIdx.x; i < NW * S::kRows * S::kTok; i += kW4Warps * 32) {
-          float v = base[i];
+    if (split > 1) {  // one tile: the CTAs of the cluster add theirs, then share the outputs
+      float* base = &red[0][0][0][0][0];
+      for (int i = threadIdx.x; i < kOne; i += kW4Warps * 32) {
+        float v = base[i];
 #pragma unroll
-          for (int w = 1; w < S::WK; ++w) v += base[w * kOne + i];
-          base[i] = v;
-        }
-        tc::cluster_sync();
+        for (int w = 1; w < S::WK; ++w) v += base[w * kOne + i];
+        base[i] = v;
       }
+      tc::cluster_sync();
       for (int i = threadIdx.x + rank * kW4Warps * 32; i < S::kRows * tokens;
            i += kW4Warps * 32 * split) {
         const int r = i % S::kRows, c = i / S::kRows, at = r * S::kTok + c;
-        const int64_t n = n0 + r;
-        if (n >= p.rows) continue;
         float v = 0.0f, u = 0.0f;
-        if (split > 1) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            if (q >= split) break;
-            v += tc::ld_cluster(tc::map_rank(tc::smem(base + at), q));
-            if (NW == 2) u += tc::ld_cluster(tc::map_rank(tc::smem(base + kOne / 2 + at), q));
-          }
-        } else {
-#pragma unroll
-          for (int w = 0; w < S::WK; ++w) {
-            v += base[w * kOne + at];
-            if (NW == 2) u += base[w * kOne + kOne / 2 + at];
-          }
+        for (int q = 0; q < 8; ++q) {
+          if (q >= split) break;
+          v += tc::ld_cluster(tc::map_rank(tc::smem(base + at), q));
+          if (NW == 2) u += tc::ld_cluster(tc::map_rank(tc::smem(base + kOne / 2 + at), q));
         }
-        if (NW == 2) v = act_value(p.act, v) * u;
-        const int64_t tok = tok0 + c;
-        if (p.out == kOutBf16) {
-          st_elem<BF16>(p.y, tok * p.rows + n, v);
-        } else if (p.out == kOutF32) {
-          st_elem<F32>(p.y, tok * p.rows + n, v);
-        } else {
-          const int64_t o = tok * p.y_pitch + (n & ~INT64_C(7)) + w4_place((int)(n & 7));
-          for (int q = 0; q < p.y_terms; ++q) st_elem<BF16>(p.y, o + q * p.y_plane, take_bf16(v));
-        }
+        put(r, c, (int64_t)first * S::kRows, v, u);
       }
-      if (split > 1) tc::cluster_sync();  // the other CTAs have read these sums
+      tc::cluster_sync();  // the other CTAs have read these sums
+      return;
+    }
+    const int each = S::kRows * tokens;
+    for (int i = threadIdx.x; i < used * each; i += kW4Warps * 32) {
+      const int s = i / each, j = i - s * each, r = j % S::kRows, c = j / S::kRows;
+      const float* at = &red[s][0][0][r][c];
+      float v = 0.0f, u = 0.0f;
+#pragma unroll
+      for (int w = 0; w < S::WK; ++w) {
+        v += at[w * kOne];
+        if (NW == 2) u += at[w * kOne + kOne / 2];
+      }
+      put(r, c, (int64_t)(first + (last - used + 1 + s) * stride) * S::kRows, v, u);
     }
     __syncthreads();
   };
@@ -364,19 +380,25 @@ __global__ void __launch_bounds__(kW4Warps * 32, NT == 4 ? 1 : 2)
     for (int d = 0; d < D; ++d) {
       if (it + d >= work) break;
       const bool in = kb * KB + t * 8 * CH < cols;
+      uint32_t bias[NW][2];
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) bias[w][h] = !DBL && affine ? w4_bias(zp[d][w][h]) : 0x43084308u;
+      const uint4* xs[NT][kTerms];
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int m = 0; m < kTerms; ++m)
+          xs[q][m] = in ? reinterpret_cast<const uint4*>(xp[q] + m * p.x_plane + kb * KB) : kZeros;
       float part[NW][NT][4];
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
-        uint4 b[NT][TERMS];
+        uint4 b[NT][kTerms];
 #pragma unroll
         for (int q = 0; q < NT; ++q)
 #pragma unroll
-          for (int m = 0; m < TERMS; ++m) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (in && xin[q])
-              v = __ldg(reinterpret_cast<const uint4*>(xp[q] + m * p.x_plane + kb * KB) + j);
-            b[q][m] = x_pairs<PLANES>(v);
-          }
+          for (int m = 0; m < kTerms; ++m) b[q][m] = x_pairs<TERMS != 0>(__ldg(xs[q][m] + j));
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
           uint32_t a[2][4];
@@ -384,12 +406,12 @@ __global__ void __launch_bounds__(kW4Warps * 32, NT == 4 ? 1 : 2)
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              a[h][e] = w4_pair(code[d][w][h].v[j] >> (4 * e), bias[d][w][h]);
+              a[h][e] = w4_pair(code[d][w][h].v[j] >> (4 * e), bias[w][h]);
 #pragma unroll
           for (int q = 0; q < NT; ++q)
 #pragma unroll
-            for (int m = TERMS - 1; m >= 0; --m) {
-              if (j == 0 && m == TERMS - 1)
+            for (int m = kTerms - 1; m >= 0; --m) {
+              if (j == 0 && m == kTerms - 1)
                 mma_16816_first(part[w][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m].x, b[q][m].y);
               else
                 mma_16816(part[w][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m].x, b[q][m].y);
@@ -400,10 +422,16 @@ __global__ void __launch_bounds__(kW4Warps * 32, NT == 4 ? 1 : 2)
 #pragma unroll
       for (int w = 0; w < NW; ++w)
 #pragma unroll
-        for (int q = 0; q < NT; ++q)
+        for (int h = 0; h < 2; ++h) {
+          // two-level: within an ulp of (q / 255) * super
+          const float s = DBL ? (float)sc[d][w][h] * (1.0f / 255.0f) * sup[d][w][h]
+                              : __uint_as_float(sc[d][w][h]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            total[w][q][e] = fmaf(part[w][q][e], sc[d][w][e >> 1], total[w][q][e]);
+          for (int q = 0; q < NT; ++q) {
+            total[w][q][2 * h] = fmaf(part[w][q][2 * h], s, total[w][q][2 * h]);
+            total[w][q][2 * h + 1] = fmaf(part[w][q][2 * h + 1], s, total[w][q][2 * h + 1]);
+          }
+        }
       if (it + d + D < work) fetch(d);
       kb += step;
       if (--left == 0) {
@@ -466,17 +494,15 @@ static cudaError_t launch_w4_kernel(void (*k)(W4Args), dim3 grid, int cluster, b
   return e;
 }
 
-template <bool PLANES, int TERMS, int CH, int NT, int NW>
+template <int TERMS, int CH, bool DBL, int NT, int NW>
 static qat_status launch_fast(W4Args p, bool pdl, cudaStream_t s) {
   using S = W4Shape<NT, NW>;
   p.tiles = (int)((p.rows + S::kRows - 1) / S::kRows);
   const int kblocks = (p.cols + 32 * CH - 1) / (32 * CH);
-  // units of a row: none (whole rows), one a block, or kb / per_unit by
-  // multiplication (exact while blocks^2 < 2^32)
-  const int64_t per_unit = p.unit / (32 * CH);
-  p.unit_magic = p.unit >= p.cols ? 0u
-                 : per_unit == 1  ? 1u
-                                  : (uint32_t)((UINT64_C(1) << 32) / per_unit + 1);
+  // the unit of block kb in its row is kb / d, as (2 kb + 1) ceil(2^31 / d) >> 32
+  // (exact while 2 kb d < 2^31); rows that are one unit: 0
+  const int64_t d = p.unit / (32 * CH);
+  p.unit_magic = p.unit >= p.cols ? 0u : (uint32_t)(((INT64_C(1) << 31) + d - 1) / d);
   const int room = device_info().sms * (NT == 4 ? 1 : 2);
   // a cluster splits k while the GPU has room and every warp keeps a block
   p.split = 1;
@@ -484,29 +510,32 @@ static qat_status launch_fast(W4Args p, bool pdl, cudaStream_t s) {
     p.split *= 2;
   const unsigned blocks = (unsigned)(p.split > 1 ? p.tiles * p.split : p.tiles < room ? p.tiles : room);
   const dim3 grid(blocks, (unsigned)((p.tokens + S::kTok - 1) / S::kTok));
-  if (launch_w4_kernel(k_w4<PLANES, TERMS, CH, NT, NW>, grid, p.split, pdl, p, s) != cudaSuccess)
+  if (launch_w4_kernel(k_w4<TERMS, CH, DBL, NT, NW>, grid, p.split, pdl, p, s) != cudaSuccess)
     return QAT_ERR_CUDA;
   count_launch(1);
   return QAT_OK;
 }
-template <bool PLANES, int TERMS, int CH, int NW>
+template <int TERMS, int CH, bool DBL, int NW>
 static qat_status fast_tokens(const W4Args& p, bool pdl, cudaStream_t s) {
-  if (p.tokens <= 8) return launch_fast<PLANES, TERMS, CH, 1, NW>(p, pdl, s);
-  if (p.tokens <= 16) return launch_fast<PLANES, TERMS, CH, 2, NW>(p, pdl, s);
-  return launch_fast<PLANES, TERMS, CH, 4, NW>(p, pdl, s);
+  if (p.tokens <= 8) return launch_fast<TERMS, CH, DBL, 1, NW>(p, pdl, s);
+  if (p.tokens <= 16) return launch_fast<TERMS, CH, DBL, 2, NW>(p, pdl, s);
+  return launch_fast<TERMS, CH, DBL, 4, NW>(p, pdl, s);
 }
-template <bool PLANES, int TERMS, int NW>
+template <int TERMS, int NW>
 static qat_status fast_chunk(const W4Args& p, int ch, bool pdl, cudaStream_t s) {
-  if (ch == 4) return fast_tokens<PLANES, TERMS, 4, NW>(p, pdl, s);
-  if (ch == 2) return fast_tokens<PLANES, TERMS, 2, NW>(p, pdl, s);
-  return fast_tokens<PLANES, TERMS, 1, NW>(p, pdl, s);
+  if (p.dbl) return fast_tokens<TERMS, 2, true, NW>(p, pdl, s);
+  if (ch == 4) return fast_tokens<TERMS, 4, false, NW>(p, pdl, s);
+  if (ch == 2) return fast_tokens<TERMS, 2, false, NW>(p, pdl, s);
+  return fast_tokens<TERMS, 1, false, NW>(p, pdl, s);
 }
 
 // Words of 8 codes a lane takes at once: the widest load that rows, units and
-// blocks of k allow; 0 when the shape needs the generic kernel (longer rows and
-// more rows than the 32-bit indexes hold too).
+// blocks of k allow; 0 when the shape needs the generic kernel (rows longer and
+// weights larger than the 32-bit offsets reach too).
 static int w4_chunk(const qat_weight4& w) {
-  if (w.cols <= 0 || w.cols % 8 || w.cols > (1 << 20) || w.rows > (1 << 28)) return 0;
+  if (w.cols <= 0 || w.cols % 8 || w.cols > (1 << 19) || w.rows > (1 << 28) ||
+      w.rows * w.cols >= (INT64_C(1) << 32))
+    return 0;
   if (w.layout == QAT_PER_TENSOR || w.layout == QAT_PER_ROW)
     return w.cols % 32 == 0 ? 4 : w.cols % 16 == 0 ? 2 : 1;
   const int64_t unit = w.layout == QAT_W4_DOUBLE ? 64 : w.group;
@@ -551,13 +580,10 @@ static qat_status run_fast(const X4& x, int64_t tokens, const qat_weight4* w, in
   p.row_units = w->layout == QAT_PER_TENSOR ? 0 : w->cols / p.unit;
   p.act = act;
   if (nw == 2)
-    return x.terms == 0   ? fast_chunk<false, 1, 2>(p, ch, pdl, s)
-           : x.terms == 1 ? fast_chunk<true, 1, 2>(p, ch, pdl, s)
-                          : fast_chunk<true, 3, 2>(p, ch, pdl, s);
-  return x.terms == 0   ? fast_chunk<false, 1, 1>(p, ch, pdl, s)
-         : x.terms == 1 ? fast_chunk<true, 1, 1>(p, ch, pdl, s)
-         : x.terms == 2 ? fast_chunk<true, 2, 1>(p, ch, pdl, s)
-                        : fast_chunk<true, 3, 1>(p, ch, pdl, s);
+    return x.terms == 0 ? fast_chunk<0, 2>(p, ch, pdl, s) : fast_chunk<3, 2>(p, ch, pdl, s);
+  return x.terms == 0   ? fast_chunk<0, 1>(p, ch, pdl, s)
+         : x.terms == 2 ? fast_chunk<2, 1>(p, ch, pdl, s)
+                        : fast_chunk<3, 1>(p, ch, pdl, s);
 }
 
 static W4 w4_of(const qat_weight4& w) {
@@ -612,9 +638,10 @@ static bool fast_ok(const qat_weight4& w, int64_t tokens) {
   return w4_chunk(w) != 0 && tokens <= kFastTokens;
 }
 
-// bf16 rows that can be read as they are need no planes
+// Planes x is taken as: none where bf16 rows can be read as they are (others
+// come as three of which two are zero: one kernel less for a rare case)
 static int x_terms(const void* x, qat_dtype dt, qat_dtype ydt) {
-  if (dt == QAT_BF16) return reinterpret_cast<uintptr_t>(x) % 16 == 0 ? 0 : 1;
+  if (dt == QAT_BF16) return reinterpret_cast<uintptr_t>(x) % 16 == 0 ? 0 : 3;
   return ydt == QAT_BF16 ? 2 : 3;
 }
 static int64_t plane_of(int64_t tokens, int64_t pitch) { return (tokens * pitch + 7) / 8 * 8; }
@@ -665,8 +692,8 @@ static size_t planes_bytes(int64_t tokens, int64_t cols, int terms) {
   return r256((size_t)plane_of(tokens, (cols + 7) / 8 * 8) * terms * 2);
 }
 
-size_t linear4_ws_bytes(qat_dtype dt, int64_t tokens, int64_t cols) {
-  return planes_bytes(tokens, cols, dt == QAT_F32 ? 3 : 1);
+size_t linear4_ws_bytes(int64_t tokens, int64_t cols) {
+  return planes_bytes(tokens, cols, 3);
 }
 qat_status launch_linear4(const void* x, qat_dtype dt, int64_t tokens, const qat_weight4& w, void* y,
                           void* ws, cudaStream_t s) {
@@ -675,15 +702,15 @@ qat_status launch_linear4(const void* x, qat_dtype dt, int64_t tokens, const qat
 }
 
 // workspace: x's planes, then h (float, or its planes), then planes of a float h
-size_t gated4_ws_bytes(qat_dtype dt, int64_t tokens, int64_t dim, int64_t hidden) {
-  return planes_bytes(tokens, dim, dt == QAT_F32 ? 3 : 1) +
+size_t gated4_ws_bytes(int64_t tokens, int64_t dim, int64_t hidden) {
+  return planes_bytes(tokens, dim, 3) +
          r256((size_t)tokens * hidden * 4) + planes_bytes(tokens, hidden, 3);
 }
 qat_status launch_gated4(const void* x, qat_dtype dt, int64_t tokens, const qat_weight4* gate_up,
                          const qat_weight4& down, int act, void* y, void* ws, cudaStream_t s) {
   const int64_t dim = gate_up->cols, hidden = gate_up->rows;
   char* base = static_cast<char*>(ws);
-  char* h = base + planes_bytes(tokens, dim, dt == QAT_F32 ? 3 : 1);
+  char* h = base + planes_bytes(tokens, dim, 3);
   char* h_planes = h + r256((size_t)tokens * hidden * 4);
   bool launched = false;
   if (fast_ok(*gate_up, tokens) && fast_ok(down, tokens)) {

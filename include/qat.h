@@ -441,8 +441,8 @@ qat_status qat_fake_quant_fp8_noalloc(const void* x, qat_dtype dtype, int64_t n,
  * flat over rows * cols elements), read by the products below.
  *   layout QAT_PER_TENSOR / QAT_PER_ROW / QAT_PER_GROUP: codes, float scales
  *     and int32 zero points (NULL: symmetric) as qat_fake_quant_int writes
- *     them; w = (q - zp) * scale.  A zero point outside [-8, 7] counts as the
- *     nearer end.  `group` as in that call.
+ *     them; w = (q - zp) * scale.  Zero points lie in [-8, 7] (products with
+ *     others are wrong).  `group` as in that call.
  *   layout QAT_W4_DOUBLE: data, qscales and super_scales as
  *     qat_quant4_double writes them for the flat weight; w = q * (qscale / 255
  *     * super).  scales holds the uint8 qscales, zero_points is NULL.
