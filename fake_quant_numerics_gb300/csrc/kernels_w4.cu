@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(128) k_w4_generic(const void* __restrict__ x, 
 // ---------------------------------------------------------------------------
 // Rows of whole 8-code words whose units are whole runs of 32 codes.
 //
-// A warp multiplies 16 rows (of each of NW weights) by 8 NT tokens with
-// m16n8k16 tensor-core products: a code is exact in bf16 (128 + q with the low
+// A warp multiplies two tiles of 16 rows (two of one weight, or one of each of
+// the gated pair) by 8 NT tokens with m16n8k16 tensor-core products: a code is exact in bf16 (128 + q with the low
 // mantissa bits, one logic operation for two codes, then an exact subtraction
 // of 136 + zero point), so is a bf16 x, and the sums are binary32.  That is about
 // 1.5 instructions a code, which keeps reading the codes the bound; scalar
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(128) k_w4_generic(const void* __restrict__ x, 
 // tiles.  Where rows are few a cluster splits k once more.  Partial sums are
 // added in shared memory, then over the cluster, in a fixed order.
 // ---------------------------------------------------------------------------
-constexpr int kW4Warps = 8;
+constexpr int kW4Warps = 16;
 enum { kOutF32 = 0, kOutBf16 = 1, kOutPlanes = 2 };
 
 struct W4Fast {
@@ -199,22 +199,24 @@ __device__ __forceinline__ void load_codes(CodeWords<CH>& o, const uint8_t* p) {
 
 template <int NT, int NW>
 struct W4Shape {
+  static constexpr int R = 2 / NW;              // row tiles of each weight
   static constexpr int WR = NT;                 // warps along the rows
   static constexpr int WK = kW4Warps / WR;      // warps along k
-  static constexpr int kRows = 16 * WR;         // output rows of a tile
+  static constexpr int kRows = 16 * R * WR;     // output rows of a block's tile
   static constexpr int kTok = 8 * NT;
-  static constexpr int kDepth = 4 / NW;         // blocks of k in flight
-  static constexpr int kSlots = NT == 1 ? 4 : NT * NW >= 8 ? 1 : 2;  // tiles between joins
+  static constexpr int kDepth = NT == 4 ? 1 : 2;  // blocks of k in flight
+  static constexpr int kSlots = NT == 1 ? 2 : 1;  // tiles between joins
+  static constexpr int kOne = NW * kRows * kTok;  // one k slice's sums of a tile
+  static constexpr int kSmem = kSlots * WK * kOne * 4;
 };
 
 // TERMS 0: x is bf16 rows; else that many planes.  CH 2 with DBL: the two-level
 // scales.
 template <int TERMS, int CH, bool DBL, int NT, int NW>
-__global__ void __launch_bounds__(kW4Warps * 32, NT == 4 ? 1 : 2)
-    k_w4(const __grid_constant__ W4Args p) {
+__global__ void __launch_bounds__(kW4Warps * 32, 1) k_w4(const __grid_constant__ W4Args p) {
   using S = W4Shape<NT, NW>;
-  constexpr int KB = 32 * CH, D = S::kDepth, kTerms = TERMS ? TERMS : 1;
-  __shared__ float red[S::kSlots][S::WK][NW][S::kRows][S::kTok];
+  constexpr int KB = 32 * CH, D = S::kDepth, kTerms = TERMS ? TERMS : 1, R = S::R;
+  extern __shared__ __align__(16) float red[];  // [slot][k slice][weight][row][token]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int wr = warp % S::WR, wk = warp / S::WR, split = p.split;
   const int rank = split > 1 ? (int)(blockIdx.x % split) : 0;
@@ -234,22 +236,25 @@ __global__ void __launch_bounds__(kW4Warps * 32, NT == 4 ? 1 : 2)
             (q * 8 + g < tokens ? tok0 + q * 8 + g : 0) * p.x_pitch + t * 8 * CH;
 
   // The loads in flight, as loaded: codes, scales and zero points of D blocks of
-  // k.  Offsets are 32-bit and the same for both weights.
-  CodeWords<CH> code[D][NW][2];
-  uint32_t sc[D][NW][2];
-  float sup[D][NW][2];
-  int zp[D][NW][2];
-  uint32_t co[2], so[2];  // this lane's rows g and g + 8: codes, units
+  // k, for the rows g and g + 8 of the two row tiles.  Offsets are 32-bit and the
+  // same for both weights.
+  CodeWords<CH> code[D][2][2];
+  uint32_t sc[D][2][2];
+  float sup[D][2][2];
+  int zp[D][2][2];
+  uint32_t co[R][2], so[R][2];  // codes, units
   int f_tile = 0, f_kb = start;
   // rows past the end read row 0 and are dropped at the end
   const auto rows_of = [&](int tile) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t n = (uint32_t)(first + tile * stride) * S::kRows + wr * 16 + h * 8 + g;
-      const uint32_t m = n < p.rows ? n : 0;
-      co[h] = (uint32_t)(((uint64_t)m * cols) >> 1) + t * 4 * CH;
-      so[h] = m * (uint32_t)p.row_units;
-    }
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t n = (uint32_t)(first + tile * stride) * S::kRows + (wr * R + r) * 16 + h * 8 + g;
+        const uint32_t m = n < p.rows ? n : 0;
+        co[r][h] = (uint32_t)(((uint64_t)m * cols) >> 1) + t * 4 * CH;
+        so[r][h] = m * (uint32_t)p.row_units;
+      }
   };
   const uint32_t co_step = (uint32_t)(((uint64_t)stride * S::kRows * cols) >> 1);
   const uint32_t so_step = (uint32_t)(stride * S::kRows) * (uint32_t)p.row_units;
@@ -260,17 +265,18 @@ __global__ void __launch_bounds__(kW4Warps * 32, NT == 4 ? 1 : 2)
     const uint32_t off = f_kb * KB + t * 8 * CH < cols ? (uint32_t)f_kb * (KB / 2) : 0u - t * 4 * CH;
     const uint32_t u = __umulhi(2u * f_kb + 1, p.unit_magic);
 #pragma unroll
-    for (int w = 0; w < NW; ++w)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        load_codes<CH>(code[d][w][h], p.w[w].codes + (co[h] + off));
-        const uint32_t at = so[h] + u;
+        const W4Fast& w = p.w[i / R];
+        load_codes<CH>(code[d][i][h], w.codes + (co[i % R][h] + off));
+        const uint32_t at = so[i % R][h] + u;
         if (DBL) {
-          sc[d][w][h] = __ldg(static_cast<const uint8_t*>(p.w[w].scales) + at);
-          sup[d][w][h] = __ldg(p.w[w].super + (at >> 8));
+          sc[d][i][h] = __ldg(static_cast<const uint8_t*>(w.scales) + at);
+          sup[d][i][h] = __ldg(w.super + (at >> 8));
         } else {
-          sc[d][w][h] = __ldg(static_cast<const uint32_t*>(p.w[w].scales) + at);
-          if (affine) zp[d][w][h] = __ldg(p.w[w].zp + at);
+          sc[d][i][h] = __ldg(static_cast<const uint32_t*>(w.scales) + at);
+          if (affine) zp[d][i][h] = __ldg(w.zp + at);
         }
       }
     f_kb += step;
@@ -281,17 +287,19 @@ __global__ void __launch_bounds__(kW4Warps * 32, NT == 4 ? 1 : 2)
         if (f_tile < mine) rows_of(f_tile);
       } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          co[h] += co_step;
-          so[h] += so_step;
-        }
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            co[r][h] += co_step;
+            so[r][h] += so_step;
+          }
       }
     }
   };
 
   // Adds the partial sums of the tiles in the first `used` slots, of which the
   // last holds tile `last`: an output a thread.
-  constexpr int kOne = NW * S::kRows * S::kTok;  // one warp's sums of a tile
+  constexpr int kOne = S::kOne;
   const auto put = [&](int r, int c, int64_t n0, float v, float u) {
     const int64_t n = n0 + r, tok = tok0 + c;
     if (n >= p.rows) return;
@@ -308,7 +316,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, NT == 4 ? 1 : 2)
   const auto join = [&](int last, int used) {
     __syncthreads();
     if (split > 1) {  // one tile: the CTAs of the cluster add theirs, then share the outputs
-      float* base = &red[0][0][0][0][0];
+      float* base = red;
       for (int i = threadIdx.x; i < kOne; i += kW4Warps * 32) {
         float v = base[i];
 #pragma unroll
@@ -334,7 +342,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, NT == 4 ? 1 : 2)
     const int each = S::kRows * tokens;
     for (int i = threadIdx.x; i < used * each; i += kW4Warps * 32) {
       const int s = i / each, j = i - s * each, r = j % S::kRows, c = j / S::kRows;
-      const float* at = &red[s][0][0][r][c];
+      const float* at = red + s * S::WK * kOne + r * S::kTok + c;
       float v = 0.0f, u = 0.0f;
 #pragma unroll
       for (int w = 0; w < S::WK; ++w) {
@@ -346,18 +354,19 @@ __global__ void __launch_bounds__(kW4Warps * 32, NT == 4 ? 1 : 2)
     __syncthreads();
   };
 
-  float total[NW][NT][4] = {};
+  float total[2][NT][4] = {};
   int tile = 0, left = per_tile, slot = 0;
   const auto flush = [&]() {
 #pragma unroll
-    for (int w = 0; w < NW; ++w)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int q = 0; q < NT; ++q)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          *reinterpret_cast<float2*>(&red[slot][wk][w][wr * 16 + h * 8 + g][q * 8 + 2 * t]) =
-              make_float2(total[w][q][2 * h], total[w][q][2 * h + 1]);
-          total[w][q][2 * h] = total[w][q][2 * h + 1] = 0.0f;
+          const int row = (i / R) * S::kRows + (wr * R + i % R) * 16 + h * 8 + g;
+          *reinterpret_cast<float2*>(red + (slot * S::WK + wk) * kOne + row * S::kTok + q * 8 + 2 * t) =
+              make_float2(total[i][q][2 * h], total[i][q][2 * h + 1]);
+          total[i][q][2 * h] = total[i][q][2 * h + 1] = 0.0f;
         }
     if (++slot == S::kSlots || tile + 1 == mine) {
       join(tile, slot);
@@ -380,18 +389,18 @@ __global__ void __launch_bounds__(kW4Warps * 32, NT == 4 ? 1 : 2)
     for (int d = 0; d < D; ++d) {
       if (it + d >= work) break;
       const bool in = kb * KB + t * 8 * CH < cols;
-      uint32_t bias[NW][2];
+      uint32_t bias[2][2];
 #pragma unroll
-      for (int w = 0; w < NW; ++w)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) bias[w][h] = !DBL && affine ? w4_bias(zp[d][w][h]) : 0x43084308u;
+        for (int h = 0; h < 2; ++h) bias[i][h] = !DBL && affine ? w4_bias(zp[d][i][h]) : 0x43084308u;
       const uint4* xs[NT][kTerms];
 #pragma unroll
       for (int q = 0; q < NT; ++q)
 #pragma unroll
         for (int m = 0; m < kTerms; ++m)
           xs[q][m] = in ? reinterpret_cast<const uint4*>(xp[q] + m * p.x_plane + kb * KB) : kZeros;
-      float part[NW][NT][4];
+      float part[2][NT][4];
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
         uint4 b[NT][kTerms];
@@ -400,36 +409,36 @@ __global__ void __launch_bounds__(kW4Warps * 32, NT == 4 ? 1 : 2)
 #pragma unroll
           for (int m = 0; m < kTerms; ++m) b[q][m] = x_pairs<TERMS != 0>(__ldg(xs[q][m] + j));
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
+        for (int i = 0; i < 2; ++i) {
           uint32_t a[2][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              a[h][e] = w4_pair(code[d][w][h].v[j] >> (4 * e), bias[w][h]);
+              a[h][e] = w4_pair(code[d][i][h].v[j] >> (4 * e), bias[i][h]);
 #pragma unroll
           for (int q = 0; q < NT; ++q)
 #pragma unroll
             for (int m = kTerms - 1; m >= 0; --m) {
               if (j == 0 && m == kTerms - 1)
-                mma_16816_first(part[w][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m].x, b[q][m].y);
+                mma_16816_first(part[i][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m].x, b[q][m].y);
               else
-                mma_16816(part[w][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m].x, b[q][m].y);
-              mma_16816(part[w][q], a[0][2], a[1][2], a[0][3], a[1][3], b[q][m].z, b[q][m].w);
+                mma_16816(part[i][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m].x, b[q][m].y);
+              mma_16816(part[i][q], a[0][2], a[1][2], a[0][3], a[1][3], b[q][m].z, b[q][m].w);
             }
         }
       }
 #pragma unroll
-      for (int w = 0; w < NW; ++w)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           // two-level: within an ulp of (q / 255) * super
-          const float s = DBL ? (float)sc[d][w][h] * (1.0f / 255.0f) * sup[d][w][h]
-                              : __uint_as_float(sc[d][w][h]);
+          const float s = DBL ? (float)sc[d][i][h] * (1.0f / 255.0f) * sup[d][i][h]
+                              : __uint_as_float(sc[d][i][h]);
 #pragma unroll
           for (int q = 0; q < NT; ++q) {
-            total[w][q][2 * h] = fmaf(part[w][q][2 * h], s, total[w][q][2 * h]);
-            total[w][q][2 * h + 1] = fmaf(part[w][q][2 * h + 1], s, total[w][q][2 * h + 1]);
+            total[i][q][2 * h] = fmaf(part[i][q][2 * h], s, total[i][q][2 * h]);
+            total[i][q][2 * h + 1] = fmaf(part[i][q][2 * h + 1], s, total[i][q][2 * h + 1]);
           }
         }
       if (it + d + D < work) fetch(d);
@@ -469,9 +478,17 @@ __global__ void __launch_bounds__(256) k_w4_planes(const void* __restrict__ x, i
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-static cudaError_t launch_w4_kernel(void (*k)(W4Args), dim3 grid, int cluster, bool pdl,
+static cudaError_t launch_w4_kernel(void (*k)(W4Args), dim3 grid, int smem, int cluster, bool pdl,
                                     const W4Args& p, cudaStream_t s) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) {
+      (void)cudaGetLastError();
+      return e;
+    }
+  }
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = smem;
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kW4Warps * 32);
   cfg.stream = s;
@@ -503,14 +520,14 @@ static qat_status launch_fast(W4Args p, bool pdl, cudaStream_t s) {
   // (exact while 2 kb d < 2^31); rows that are one unit: 0
   const int64_t d = p.unit / (32 * CH);
   p.unit_magic = p.unit >= p.cols ? 0u : (uint32_t)(((INT64_C(1) << 31) + d - 1) / d);
-  const int room = device_info().sms * (NT == 4 ? 1 : 2);
+  const int room = device_info().sms;
   // a cluster splits k while the GPU has room and every warp keeps a block
   p.split = 1;
   while (p.split < 8 && p.tiles * p.split * 2 <= room && kblocks >= p.split * 2 * S::WK)
     p.split *= 2;
   const unsigned blocks = (unsigned)(p.split > 1 ? p.tiles * p.split : p.tiles < room ? p.tiles : room);
   const dim3 grid(blocks, (unsigned)((p.tokens + S::kTok - 1) / S::kTok));
-  if (launch_w4_kernel(k_w4<TERMS, CH, DBL, NT, NW>, grid, p.split, pdl, p, s) != cudaSuccess)
+  if (launch_w4_kernel(k_w4<TERMS, CH, DBL, NT, NW>, grid, S::kSmem, p.split, pdl, p, s) != cudaSuccess)
     return QAT_ERR_CUDA;
   count_launch(1);
   return QAT_OK;
