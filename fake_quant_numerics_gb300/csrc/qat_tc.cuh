@@ -103,27 +103,29 @@ __device__ __forceinline__ void load_box(const CUtensorMap* map, uint32_t dst, u
         : "memory");
 }
 
-// Tensor memory.  CG is the number of CTAs that share an MMA (1 or 2).
+// Tensor memory.  CG is the number of CTAs that share an MMA (1 or 2).  The
+// permit to allocate goes back at once, so that blocks that share an SM start
+// together.
 template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t cols) {
-  if (CG == 2)
+  if (CG == 2) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
                  "r"(cols)
                  : "memory");
-  else
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  } else {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
                  "r"(cols)
                  : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
 }
 template <int CG>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-  if (CG == 2) {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  if (CG == 2)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
-  } else {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  else
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
-  }
 }
 __device__ __forceinline__ void fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
