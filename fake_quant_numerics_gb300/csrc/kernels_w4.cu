@@ -709,7 +709,8 @@ static size_t planes_bytes(int64_t tokens, int64_t cols, int terms) {
   return r256((size_t)plane_of(tokens, (cols + 7) / 8 * 8) * terms * 2);
 }
 
-size_t linear4_ws_bytes(int64_t tokens, int64_t cols) {
+size_t linear4_ws_bytes(const void* x, qat_dtype dt, int64_t tokens, int64_t cols) {
+  if (x && x_terms(x, dt, dt) == 0) return 0;
   return planes_bytes(tokens, cols, 3);
 }
 qat_status launch_linear4(const void* x, qat_dtype dt, int64_t tokens, const qat_weight4& w, void* y,

@@ -11,7 +11,8 @@
 namespace qat {
 
 // Products with 4-bit weights (y in x's dtype) and the gated block from codes.
-size_t linear4_ws_bytes(int64_t tokens, int64_t cols);
+// (none for a 16-byte aligned bf16 x)
+size_t linear4_ws_bytes(const void* x, qat_dtype dt, int64_t tokens, int64_t cols);
 qat_status launch_linear4(const void* x, qat_dtype dt, int64_t tokens, const qat_weight4& w, void* y,
                           void* ws, cudaStream_t s);
 size_t gated4_ws_bytes(int64_t tokens, int64_t dim, int64_t hidden);

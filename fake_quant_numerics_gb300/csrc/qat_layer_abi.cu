@@ -50,7 +50,7 @@ extern "C" {
 
 size_t qat_linear4_workspace_bytes(qat_dtype dtype, int64_t tokens, int64_t cols) {
   if (!dtype_ok(dtype) || !fits(tokens, cols)) return 0;
-  return linear4_ws_bytes(tokens, cols);
+  return linear4_ws_bytes(nullptr, dtype, tokens, cols);
 }
 
 qat_status qat_linear4(const void* x, qat_dtype dtype, int64_t tokens, const qat_weight4* w, void* y,
@@ -63,7 +63,7 @@ qat_status qat_linear4(const void* x, qat_dtype dtype, int64_t tokens, const qat
   if (tokens == 0 || w->rows == 0) return QAT_OK;
   if ((!x && w->cols > 0) || !y) return QAT_ERR_INVALID_ARGUMENT;
   if (!on(x, esize(dtype)) || !on(y, esize(dtype))) return QAT_ERR_MISALIGNED;
-  const size_t need = linear4_ws_bytes(tokens, w->cols);
+  const size_t need = linear4_ws_bytes(x, dtype, tokens, w->cols);
   if (need && (!workspace || workspace_bytes < need)) return QAT_ERR_WORKSPACE;
   if (need && !on(workspace, 16)) return QAT_ERR_MISALIGNED;
   return launch_linear4(x, dtype, tokens, *w, y, workspace, reinterpret_cast<cudaStream_t>(stream));

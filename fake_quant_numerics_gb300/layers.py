@@ -17,7 +17,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib
-from ._lib import (GELU, PER_COLUMN, PER_GROUP, PER_ROW, PER_TENSOR, RELU, SILU, W4_DOUBLE, QatError)
+from ._lib import (BF16, GELU, PER_COLUMN, PER_GROUP, PER_ROW, PER_TENSOR, RELU, SILU, W4_DOUBLE, QatError)
 from .api import _GRAN, _dt, _nbytes, _p, _ready, _s, DoubleQuantized4Bit
 
 _ACT = {"silu": SILU, "gelu": GELU, "relu": RELU, SILU: SILU, GELU: GELU, RELU: RELU}
@@ -145,9 +145,12 @@ def linear4(x: torch.Tensor, weight: Weight4) -> torch.Tensor:
     x = x.contiguous()
     tokens, dt, lib = _leading(x, shape), _dt(x), _lib.lib()
     y = torch.empty((*shape[:-1], weight.rows), dtype=x.dtype, device=x.device)
-    n = lib.qat_linear4_workspace_bytes(dt, tokens, cols)
-    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-    st = lib.qat_linear4(_ptr(x), dt, tokens, _w4(weight), y.data_ptr(), ws.data_ptr(), n, _here(x))
+    xp, ws, n = _ptr(x), None, 0
+    if dt != BF16 or xp % 16:
+        n = lib.qat_linear4_workspace_bytes(dt, tokens, cols)
+        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    st = lib.qat_linear4(xp, dt, tokens, _w4(weight), y.data_ptr(), ws.data_ptr() if n else None, n,
+                         _here(x))
     if st:
         _lib.check("qat_linear4", st)
     return y

@@ -473,7 +473,8 @@ typedef enum { QAT_ACT_SILU = 0, QAT_ACT_GELU = 1, QAT_ACT_RELU = 2 } qat_activa
  * size, a group that does not divide cols, zero points with QAT_W4_DOUBLE;
  * QAT_ERR_UNSUPPORTED: an unknown dtype or layout; QAT_ERR_MISALIGNED.
  * workspace: qat_linear4_workspace_bytes(dtype, tokens, cols) bytes, 16-byte
- * aligned (x's parts).  One or two launches.
+ * aligned (x's parts), or none for a 16-byte aligned bf16 x.  One or two
+ * launches.
  */
 size_t qat_linear4_workspace_bytes(qat_dtype dtype, int64_t tokens, int64_t cols);
 qat_status qat_linear4(const void* x, qat_dtype dtype, int64_t tokens, const qat_weight4* w, void* y,
