@@ -702,21 +702,34 @@ qat_status launch_dense(const Dense& d, cudaStream_t s) {
   p.problems = d.problems;
   p.segs = d.segs;
   p.kt = (int)up(d.k, kBK);
-  // pairs of CTAs once their tiles fill the GPU
-  const int64_t big = up(d.m, 256) * up(d.n, gated ? 128 : 256) * d.problems;
-  const bool pair = big >= sms / 2;
+  // Pairs of CTAs, single CTAs, or clusters that split k, whichever should end
+  // first: waves of tiles times k steps, and the end of a tile.  Measured cycles
+  // of a step: 620 of a pair's (256 x 256 x 64), 680 of a single CTA's (128 x 128
+  // x 64); a pair's tile ends in about 6000, a split one is joined in as many, a
+  // single one ends in 2500.  With 128 rows or fewer half a pair would idle.  At 1001 x 4096, k = 14336, pairs take 84 us and
+  // single CTAs 158; at 128 x 4096 it is 150 and 31 (split).
+  const auto tiles_of = [&](int side) {
+    return up(d.m, side) * up(d.n, gated ? side / 2 : side) * d.problems;
+  };
+  const int64_t units = (int64_t)p.segs * (f32 ? Units<F32>::per_segment(p.kt) : p.kt);
+  const int64_t steps = f32 ? (int64_t)p.segs * p.kt * 6 : units;
+  const int64_t pair_cost = up(tiles_of(256), sms / 2) * steps * 620 + 6000;
+  int64_t best = up(tiles_of(128), sms) * steps * 680 + 2500;
+  p.split = 1;
+  const int least = f32 ? 1 : 4;
+  for (int c = 2; c <= 8; ++c) {
+    if (units < c * least || tiles_of(128) > resident_clusters(c)) break;
+    const int64_t cost = up(steps, c) * 680 + 6000;
+    if (cost < best) {
+      best = cost;
+      p.split = c;
+    }
+  }
+  const bool pair = d.m > 128 && pair_cost <= best;
+  if (pair) p.split = 1;
   const int bm = pair ? 256 : 128, bn = gated ? bm / 2 : bm;
   p.mt = (int)up(d.m, bm);
   p.nt = (int)up(d.n, bn);
-  p.split = 1;
-  if (!pair) {
-    // k is split while there are SMs for it and work for each CTA
-    const int64_t tiles = (int64_t)p.mt * p.nt * p.problems;
-    const int64_t units = (int64_t)p.segs * (f32 ? Units<F32>::per_segment(p.kt) : p.kt);
-    const int least = f32 ? 1 : 4;
-    for (int c = 2; c <= 8; ++c)
-      if (tiles <= resident_clusters(c) && units >= c * least) p.split = c;
-  }
   const int nb = gated ? 2 : d.segs, na = d.problems > 1 ? d.problems : d.segs;
   for (int i = 0; i < 2; ++i) {
     if (!encode(&p.a[i], d.a[i < na ? i : 0], d.m, d.k, parts, 128)) return QAT_ERR_CUDA;
