@@ -7,16 +7,15 @@
 // bulk tensor copies either along k (K-major) or along its own rows
 // (MN-major), so no transpose is ever written.
 //
-// A CTA stages 128 rows of A and 128 of B, 64 deep, per step (32 KB, six steps
-// in flight) in 128-byte swizzled rows.  One thread issues the copies, one the
+// A CTA stages 128 rows of A and 128 of B, 64 deep, per step (32 KB, six or five
+// steps in flight) in 128-byte swizzled rows.  One thread issues the copies, one the
 // MMAs; the sums stay in tensor memory, in two buffers, so that eight warps
 // finish one tile while the next is multiplied.  CG = 2: two CTAs share a
 // 256 x 256 tile, each holding half of A and half of B, which halves the
 // shared-memory traffic per product (a single CTA's 128 x 128 tile reads its
-// operands faster than shared memory delivers them) - taken when such tiles
-// fill the GPU.  CG = 1: 128 x 128 tiles, and where those are few a cluster of
-// up to eight CTAs splits k and adds its sums through distributed shared
-// memory in rank order.
+// operands faster than shared memory delivers them).  CG = 1: 128 x 128 tiles,
+// and where those are few a cluster of up to eight CTAs splits k and adds its
+// sums through distributed shared memory in rank order.
 #include "qat_dense.h"
 #include "qat_layer.cuh"
 #include "qat_tc.cuh"
@@ -25,13 +24,20 @@
 
 namespace qat {
 
-constexpr int kBK = 64, kStages = 6;
+constexpr int kBK = 64;
 constexpr int kRows = 128;                      // rows of A and of B per CTA and stage
 constexpr uint32_t kOpBytes = kRows * kBK * 2;  // 16 KB
 constexpr uint32_t kStageBytes = 2 * kOpBytes;
 constexpr uint32_t kBarBytes = 256;
-constexpr uint32_t kDenseSmem = kStages * kStageBytes + kBarBytes + 1024;
 constexpr int kFinishWarps = 8;  // two for each quarter of the tile's rows
+// The backward epilogue reads g and u: each finishing warp has 32 x 32 floats of
+// both in shared memory, in the place of one stage.
+constexpr uint32_t kSideBytes = 2 * 32 * 32 * 4;
+__host__ __device__ constexpr int stages_of(int epi) { return epi == kDenseGatedBwd ? 5 : 6; }
+__host__ __device__ constexpr uint32_t dense_smem(int epi) {
+  return stages_of(epi) * kStageBytes + kBarBytes + 1024 +
+         (epi == kDenseGatedBwd ? kFinishWarps * kSideBytes : 0);
+}
 constexpr int kDenseThreads = 64 + 32 * kFinishWarps;
 
 struct DenseArgs {
@@ -126,10 +132,12 @@ __device__ __forceinline__ uint32_t row_align(const void* p, int64_t pitch_bytes
   return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : 1;
 }
 
-// One row's 32 columns from column c on (gated: v = g, u beside it).
+// One row's 32 columns from column c on
+// (gated: v = g, u beside it; backward: v = dh, g and w = u as kept)
 template <typename T, int EPI>
 __device__ __forceinline__ void finish32(const DenseArgs& p, int prob, int64_t row, int64_t c,
-                                         const float (&v)[32], const float (&u)[32]) {
+                                         const float (&v)[32], const float (&u)[32],
+                                         const float (&g)[32], const float (&w)[32]) {
   const int64_t at = row * p.n + c;
   const int left = (int)min((int64_t)32, p.n - c);
   if (EPI == kDenseStore) {
@@ -137,7 +145,7 @@ __device__ __forceinline__ void finish32(const DenseArgs& p, int prob, int64_t r
   } else if (EPI == kDenseGated) {
     float h[32];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) h[i] = act_value(p.act, v[i]) * u[i];
+    for (int i = 0; i < 32; ++i) h[i] = act_value<T::BYTES == 2>(p.act, v[i]) * u[i];
     st_row32<T>(p.c[0], at, left, row_align(p.c[0], p.n * T::BYTES), h);
     if (p.q[0]) st_parts32<T>(p, 0, row, c, left, h);
     if (p.gp) {
@@ -145,13 +153,11 @@ __device__ __forceinline__ void finish32(const DenseArgs& p, int prob, int64_t r
       st_row32<F32>(p.up, at, left, row_align(p.up, p.n * 4), u);
     }
   } else {
-    float g[32], w[32], dg[32], du[32];
-    ld_row32(p.gp, at, left, row_align(p.gp, p.n * 4), g);
-    ld_row32(p.up, at, left, row_align(p.up, p.n * 4), w);
+    float dg[32], du[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       float a, da;
-      act_grad(p.act, g[i], a, da);
+      act_grad<T::BYTES == 2>(p.act, g[i], a, da);
       dg[i] = v[i] * w[i] * da;
       du[i] = v[i] * a;
     }
@@ -205,7 +211,7 @@ __device__ __forceinline__ void finish4(const DenseArgs& p, int prob, int64_t ro
   } else if (EPI == kDenseGated) {
     float h[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = act_value(p.act, v[i]) * u[i];
+    for (int i = 0; i < 4; ++i) h[i] = act_value<T::BYTES == 2>(p.act, v[i]) * u[i];
     st_row4<T>(p.c[0], at, left, vec(p.c[0], T::BYTES), h);
     if (p.q[0]) st_parts4<T>(p, 0, row, c, left, h);
     if (p.gp) {
@@ -222,7 +228,7 @@ __device__ __forceinline__ void finish4(const DenseArgs& p, int prob, int64_t ro
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float a, da;
-      act_grad(p.act, g[i], a, da);
+      act_grad<T::BYTES == 2>(p.act, g[i], a, da);
       dg[i] = v[i] * w[i] * da;
       du[i] = v[i] * a;
     }
@@ -283,10 +289,11 @@ struct Units {
 
 template <typename T, int CG, int EPI, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constant__ DenseArgs p) {
+  constexpr int kStages = stages_of(EPI);
   extern __shared__ uint8_t raw[];
   const uint32_t base = (tc::smem(raw) + 1023) & ~1023u;
   const uint32_t bars = base + kStages * kStageBytes;
-  // full[6], empty[6], acc_full[2], acc_empty[2], drain; then the TMEM address
+  // full[stages], empty[stages], acc_full[2], acc_empty[2], drain
   const auto full = [&](int s) { return bars + 8 * s; };
   const auto empty = [&](int s) { return bars + 8 * (kStages + s); };
   const auto acc_full = [&](int b) { return bars + 8 * (2 * kStages + b); };
@@ -464,10 +471,57 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
       if (lane == 0) tc::bar_arrive_cluster(tc::map_rank(acc_empty((int)(run & 1)), CG == 2 ? 0 : rank));
       ++run;
     };
+    // Backward: g and u of 32 rows x 32 columns come in by rows of 128 bytes,
+    // asynchronously, and are taken back a row a thread; the 16-byte pieces of a
+    // row are permuted by it so that both ways are free of bank conflicts.
+    const bool side = EPI == kDenseGatedBwd && p.n % 4 == 0 &&
+                      ((reinterpret_cast<uint64_t>(p.gp) | reinterpret_cast<uint64_t>(p.up)) & 15) == 0;
+    const uint32_t side_at = bars + kBarBytes + (warp - 2) * kSideBytes;
+    const auto side_load = [&](int64_t row0, int64_t c) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + lane / 8, k = lane % 8;
+        if (row0 + r < p.m && c + k * 4 < p.n) {
+          const int64_t at = (row0 + r) * p.n + c + k * 4;
+          const uint32_t to = side_at + r * 128 + ((k ^ (r & 7)) * 16);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p.gp + at) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 4096), "l"(p.up + at)
+                       : "memory");
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const auto side_take = [&](float (&g)[32], float (&u)[32]) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncwarp();
+      const uint8_t* at = raw + (side_at - tc::smem(raw)) + lane * 128;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float4 a = *reinterpret_cast<const float4*>(at + ((k ^ (lane & 7)) * 16));
+        const float4 b = *reinterpret_cast<const float4*>(at + 4096 + ((k ^ (lane & 7)) * 16));
+        g[4 * k] = a.x, g[4 * k + 1] = a.y, g[4 * k + 2] = a.z, g[4 * k + 3] = a.w;
+        u[4 * k] = b.x, u[4 * k + 1] = b.y, u[4 * k + 2] = b.z, u[4 * k + 3] = b.w;
+      }
+      __syncwarp();  // taken: the next columns may come in
+    };
+    // g and u of this thread's row, columns c on; starts the next 32 columns
+    const auto kept = [&](float (&g)[32], float (&u)[32], int64_t row, int64_t c, bool more) {
+      if constexpr (EPI == kDenseGatedBwd) {
+        if (side) {
+          side_take(g, u);
+          if (more) side_load(row - lane, c + 32);
+        } else if (row < p.m && c < p.n) {
+          const int left = (int)min((int64_t)32, p.n - c);
+          ld_row32(p.gp, row * p.n + c, left, row_align(p.gp, p.n * 4), g);
+          ld_row32(p.up, row * p.n + c, left, row_align(p.up, p.n * 4), u);
+        }
+      }
+    };
     for (int64_t t = first; t < tiles; t += stride) {
       const Tile w = tile_at<CG, EPI>(p, t);
       const int64_t row = w.m0 + (CG == 2 ? (int64_t)rank * kRows : 0) + quad * 32 + lane;
       const int64_t col = w.n0 + c_first;
+      if (side && (CG == 2 || p.split == 1)) side_load(row - lane, col);
       // where k is split: this row of the CTA's sums, in the stage buffers (every
       // stage has been multiplied by then)
       float* sums = reinterpret_cast<float*>(raw + (base - tc::smem(raw))) +
@@ -506,18 +560,16 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
           }
           break;  // joined below
         }
-        if (row < p.m) {
 #pragma unroll
-          for (int c = 0; c < kHalf; c += 32) {
-            if (col + c >= p.n) break;
-            float v[32], u[32];
+        for (int c = 0; c < kHalf; c += 32) {
+          float v[32], u[32], g[32], k[32];
+          kept(g, k, row, col + c, c + 32 < kHalf);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              v[i] = sv[c + i];
-              u[i] = su[(c + i) % kU];
-            }
-            finish32<T, EPI>(p, w.prob, row, col + c, v, u);
+          for (int i = 0; i < 32; ++i) {
+            v[i] = sv[c + i];
+            u[i] = su[(c + i) % kU];
           }
+          if (row < p.m && col + c < p.n) finish32<T, EPI>(p, w.prob, row, col + c, v, u, g, k);
         }
       } else {
         const uint32_t acc = next_sum();
@@ -540,8 +592,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
               put4(sums + c + i, v[i], v[i + 1], v[i + 2], v[i + 3]);
               if (EPI == kDenseGated) put4(sums + kOut + c + i, u[i], u[i + 1], u[i + 2], u[i + 3]);
             }
-          } else if (row < p.m && col + c < p.n) {
-            finish32<T, EPI>(p, w.prob, row, col + c, v, u);
+          } else {
+            float g[32], k[32];
+            kept(g, k, row, col + c, c + 32 < kHalf);
+            if (row < p.m && col + c < p.n) finish32<T, EPI>(p, w.prob, row, col + c, v, u, g, k);
           }
         }
         if (CG == 1 && p.split > 1) break;  // joined below
@@ -618,8 +672,8 @@ static bool encode(CUtensorMap* map, const DenseOp& o, int64_t rows, int64_t dep
 template <typename T, int CG, int EPI, bool A_MN, bool B_MN>
 static qat_status launch(DenseArgs& p, bool pdl, cudaStream_t s) {
   const auto kernel = k_dense<T, CG, EPI, A_MN, B_MN>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmem) !=
-      cudaSuccess) {
+  constexpr uint32_t smem = dense_smem(EPI);
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
     (void)cudaGetLastError();
     return QAT_ERR_CUDA;
   }
@@ -631,7 +685,7 @@ static qat_status launch(DenseArgs& p, bool pdl, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * cluster));
   cfg.blockDim = dim3(kDenseThreads);
-  cfg.dynamicSmemBytes = kDenseSmem;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -673,7 +727,8 @@ static int resident_clusters(int c) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)c);
   cfg.blockDim = dim3(kDenseThreads);
-  cfg.dynamicSmemBytes = kDenseSmem;
+  constexpr uint32_t smem = dense_smem(kDenseStore);
+  cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = c;
@@ -681,8 +736,7 @@ static int resident_clusters(int c) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmem) !=
-          cudaSuccess ||
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
     (void)cudaGetLastError();
     return 0;

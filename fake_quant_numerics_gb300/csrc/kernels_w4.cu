@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(128) k_w4_generic(const void* __restrict__ x, 
 #pragma unroll
   for (int t = 0; t < kGenTokens; ++t) {
     if (t >= nt) break;
-    const float v = NW == 2 ? act_value(act, a[t]) * b[t] : a[t];
+    const float v = NW == 2 ? act_value<false>(act, a[t]) * b[t] : a[t];
     if (y_bf16)
       st_elem<BF16>(y, (t0 + t) * rows + n, v);
     else
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) k_w4(const __grid_constant__
   const auto put = [&](int r, int c, int64_t n0, float v, float u) {
     const int64_t n = n0 + r, tok = tok0 + c;
     if (n >= p.rows) return;
-    if (NW == 2) v = act_value(p.act, v) * u;
+    if (NW == 2) v = act_value<false>(p.act, v) * u;
     if (p.out == kOutBf16) {
       st_elem<BF16>(p.y, tok * p.rows + n, v);
     } else if (p.out == kOutF32) {

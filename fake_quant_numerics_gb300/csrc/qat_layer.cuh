@@ -36,10 +36,13 @@ __device__ __forceinline__ float take_bf16(float& x) {
 }
 
 // act(g) and act'(g): silu (0), gelu in the erf form (1), relu (2).  A NaN
-// stays NaN; relu'(0) = 0.
+// stays NaN; relu'(0) = 0.  FAST takes the hardware's exponential and reciprocal
+// for the sigmoid (within 2^-20 for |g| < 20, where it matters): enough under a
+// bf16 result, at a third of the instructions.
+template <bool FAST>
 __device__ __forceinline__ void act_grad(int act, float g, float& a, float& da) {
   if (act == QAT_ACT_SILU) {
-    const float s = __frcp_rn(1.0f + expf(-g));
+    const float s = FAST ? __fdividef(1.0f, 1.0f + __expf(-g)) : __frcp_rn(1.0f + expf(-g));
     a = g * s;
     da = s * fmaf(g, 1.0f - s, 1.0f);
   } else if (act == QAT_ACT_GELU) {
@@ -51,9 +54,10 @@ __device__ __forceinline__ void act_grad(int act, float g, float& a, float& da) 
     da = g > 0.0f ? 1.0f : 0.0f;
   }
 }
+template <bool FAST>
 __device__ __forceinline__ float act_value(int act, float g) {
   float a, da;
-  act_grad(act, g, a, da);
+  act_grad<FAST>(act, g, a, da);
   return a;
 }
 
