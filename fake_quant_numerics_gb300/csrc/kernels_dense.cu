@@ -46,6 +46,7 @@ struct DenseArgs {
   int mt, nt, problems;    // tiles of the output; outputs that share B
   int kt, segs;            // k steps of a segment; segments
   int split;               // CTAs of a cluster that share k (CG = 1)
+  int bn;                  // columns of a pair's tile (store)
   int act;
   void* c[2];              // outputs (gated: c[0] = h), rows of n
   float* gp;
@@ -254,7 +255,8 @@ struct Tile {
 // at work together then reread few operand rows, from L2.
 template <int CG, int EPI>
 __device__ __forceinline__ Tile tile_at(const DenseArgs& p, int64_t t) {
-  constexpr int BM = kRows * CG, BN = kRows * CG / (EPI == kDenseGated ? 2 : 1);
+  constexpr int BM = kRows * CG;
+  const int BN = EPI == kDenseGated ? kRows * CG / 2 : CG == 2 && EPI == kDenseStore ? p.bn : kRows * CG;
   const int64_t per = (int64_t)p.mt * p.nt;
   Tile r;
   r.prob = (int)(t / per);
@@ -334,6 +336,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
   pdl_trigger();  // the call's next kernel may take each SM as this one leaves it
   pdl_wait();     // and this one's set-up overlapped the previous kernel's end
 
+  // columns of the tile's sums, and the bytes of a stage of B
+  const int tile_cols = CG == 2 && EPI == kDenseStore ? p.bn : kAccCols;
+  const uint32_t b_bytes = CG == 2 && !B_MN ? (uint32_t)tile_cols / 2 * kBK * 2 : kOpBytes;
   using U = Units<T>;
   const int per_seg = U::per_segment(p.kt), units = p.segs * per_seg;
   // this CTA's share of them
@@ -352,7 +357,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
       for (int64_t t = first; ok && t < tiles; t += stride) {
         const Tile w = tile_at<CG, EPI>(p, t);
         const int am = (int)(w.m0 + (CG == 2 ? (int64_t)rank * kRows : 0));
-        const int bn = (int)(w.n0 + (CG == 2 && EPI != kDenseGated ? (int64_t)rank * kRows : 0));
+        const int bn = (int)(w.n0 + (CG == 2 && EPI != kDenseGated ? (int64_t)rank * (tile_cols / 2) : 0));
         for (int un = u0; ok && un < u1; ++un) {
           const int seg = un / per_seg, in_seg = un - seg * per_seg;
           const int steps = U::steps(p.kt, in_seg);
@@ -365,7 +370,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
             const int pa = U::kParts ? kPairA[pr] : 0, pb = U::kParts ? kPairB[pr] : 0;
             const uint32_t sa = base + stage * kStageBytes, sb = sa + kOpBytes;
             uint32_t bar = full(stage);
-            if (leader) tc::bar_expect(bar, kStageBytes * CG);
+            if (leader) tc::bar_expect(bar, (kOpBytes + b_bytes) * CG);
             if (CG == 2) bar = tc::map_rank(bar, 0);
             const CUtensorMap* ma = &p.a[p.problems > 1 ? w.prob : seg];
             if (A_MN) {
@@ -407,7 +412,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
     }
   } else if (warp == 1) {
     if (leader && lane == 0) {
-      constexpr uint32_t idesc = tc::idesc_bf16(kRows * CG, kRows * CG, A_MN, B_MN);
+      const uint32_t idesc = tc::idesc_bf16(kRows * CG, tile_cols, A_MN, B_MN);
       int stage = 0;
       uint32_t phase = 0;
       int64_t run = 0;  // sums begun: the accumulators alternate
@@ -455,6 +460,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
     constexpr int kOut = EPI == kDenseGated ? kAccCols / 2 : kAccCols;
     constexpr int kHalf = kOut / 2;
     const int c_first = (warp - 2) / 4 * kHalf;  // this warp's columns
+    const int c_count = EPI == kDenseGated ? kHalf : min(kHalf, tile_cols - c_first);
     constexpr float kBad = __builtin_nanf("");
     int64_t run = 0;
     // waits for the next sum; the address of this warp's lanes of it
@@ -563,6 +569,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
 #pragma unroll
         for (int c = 0; c < kHalf; c += 32) {
           float v[32], u[32], g[32], k[32];
+          if (c >= c_count) break;
           kept(g, k, row, col + c, c + 32 < kHalf);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
@@ -574,12 +581,12 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
       } else {
         const uint32_t acc = next_sum();
 #pragma unroll 1
-        for (int c = 0; c < kHalf; c += 32) {
+        for (int c = 0; c < c_count; c += 32) {
           uint32_t r[32], q[32];
           tc::tmem_ld32(acc + c, r);
           if (EPI == kDenseGated) tc::tmem_ld32(acc + kOut + c, q);
           tc::tmem_ld_wait();
-          if (c + 32 == kHalf) sum_read();
+          if (c + 32 >= c_count) sum_read();
           float v[32], u[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
@@ -767,7 +774,19 @@ qat_status launch_dense(const Dense& d, cudaStream_t s) {
   };
   const int64_t units = (int64_t)p.segs * (f32 ? Units<F32>::per_segment(p.kt) : p.kt);
   const int64_t steps = f32 ? (int64_t)p.segs * p.kt * 6 : units;
-  const int64_t pair_cost = up(tiles_of(256), sms / 2) * steps * 620 + 6000;
+  // A pair's tile has 256 columns, or 224 where that fills its last wave (560
+  // cycles a step): 4096 x 4096 is 256 tiles of 256 on 76 pairs, four waves, and
+  // 304 of 224, four waves too.
+  p.bn = 256;
+  int64_t pair_cost = up(tiles_of(256), sms / 2) * steps * 620 + 6000;
+  if (d.epi == kDenseStore) {
+    const int64_t narrow = up(d.m, 256) * up(d.n, 224) * d.problems;
+    const int64_t cost = up(narrow, sms / 2) * steps * 560 + 6000;
+    if (cost < pair_cost) {
+      p.bn = 224;
+      pair_cost = cost;
+    }
+  }
   int64_t best = up(tiles_of(128), sms) * steps * 680 + 2500;
   p.split = 1;
   const int least = f32 ? 1 : 4;
@@ -781,13 +800,13 @@ qat_status launch_dense(const Dense& d, cudaStream_t s) {
   }
   const bool pair = d.m > 128 && pair_cost <= best;
   if (pair) p.split = 1;
-  const int bm = pair ? 256 : 128, bn = gated ? bm / 2 : bm;
+  const int bm = pair ? 256 : 128, bn = gated ? bm / 2 : pair ? p.bn : bm;
   p.mt = (int)up(d.m, bm);
   p.nt = (int)up(d.n, bn);
   const int nb = gated ? 2 : d.segs, na = d.problems > 1 ? d.problems : d.segs;
   for (int i = 0; i < 2; ++i) {
     if (!encode(&p.a[i], d.a[i < na ? i : 0], d.m, d.k, parts, 128)) return QAT_ERR_CUDA;
-    if (!encode(&p.b[i], d.b[i < nb ? i : 0], d.n, d.k, parts, gated && !pair ? 64 : 128))
+    if (!encode(&p.b[i], d.b[i < nb ? i : 0], d.n, d.k, parts, gated ? bn : pair ? bn / 2 : 128))
       return QAT_ERR_CUDA;
   }
   p.act = d.act;
