@@ -398,3 +398,33 @@ def test_side_stream_and_graph_replay():
         graph.replay()
         for a, b in zip(outs, step()):
             assert torch.equal(a, b)
+
+
+# --- failure detection ---------------------------------------------------------
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,dim,hidden", [(5, 1024, 256), (200, 128, 128), (2600, 256, 2048)])
+def test_ffn_wait_that_runs_out_is_reported(dtype, tokens, dim, hidden):
+    """With no polls allowed every bounded wait of the products gives up at once:
+    the call returns, flags the time-out and leaves NaN, and the next call (with
+    the default limit) is whole again."""
+    x = rnd(1, tokens, dim, dtype=dtype)
+    w = [rnd(s, hidden, dim, dtype=dtype, scale=0.1) for s in (2, 3)]
+    wd = rnd(4, dim, hidden, dtype=dtype, scale=0.1)
+    want = fq.gated_ffn(x, *w, wd)
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    h, y = torch.zeros_like(want.h), torch.zeros_like(want.y)
+    dt = 0 if dtype == torch.float32 else 1
+    n = fq.qat_gated_ffn_workspace_bytes(dt, tokens, dim, hidden)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    lib = fq.load()
+    try:
+        lib.qat_debug_set_wait_limit(0)
+        fq.qat_gated_ffn(x, tokens, dim, hidden, *w, wd, "silu", h, None, None, y, flags, ws)
+        torch.cuda.synchronize()
+    finally:
+        lib.qat_debug_set_wait_limit(-1)
+    assert int(flags.item()) & 16                      # QAT_FLAG_DEVICE_TIMEOUT
+    assert torch.isnan(y).all() and torch.isnan(h).all()
+    flags.zero_()
+    fq.qat_gated_ffn(x, tokens, dim, hidden, *w, wd, "silu", h, None, None, y, flags, ws)
+    assert int(flags.item()) == 0 and torch.equal(y, want.y) and torch.equal(h, want.h)
