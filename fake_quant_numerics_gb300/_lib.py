@@ -59,7 +59,7 @@ class Weight4Struct(ctypes.Structure):
                 ("rows", _i64), ("cols", _i64), ("group", _i64), ("layout", _int)]
 
 
-_w4 = ctypes.POINTER(Weight4Struct)
+_w4 = ctypes.c_void_p  # the address of a Weight4Struct (a pointer type would wrap it on every call)
 
 PROTOTYPES = {
     "qat_status_string": ([_int], ctypes.c_char_p),

@@ -33,10 +33,14 @@ def _ptr(t: torch.Tensor) -> int:
     return t.data_ptr()
 
 
+# The current stream of a device as a raw handle (the calls here are short, and a
+# Stream object costs as much as a launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _here(t: torch.Tensor) -> int:
-    """The current stream of t's device (the raw handle: the calls here are short,
-    and a Stream object costs as much as the launch)."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return _raw_stream(t.device.index)
 
 
 def _aligned(t: torch.Tensor) -> torch.Tensor:
@@ -47,6 +51,8 @@ def _aligned(t: torch.Tensor) -> torch.Tensor:
 
 def _leading(t: torch.Tensor, shape) -> int:
     """Rows of t seen as [rows, last dimension]."""
+    if len(shape) == 2:
+        return shape[0]
     return t.numel() // shape[-1] if shape[-1] else shape[:-1].numel()
 
 
@@ -69,7 +75,7 @@ class Weight4:
     its tensors and the qat_weight4 of their addresses: do not change them."""
 
     __slots__ = ("codes", "scale", "zero_point", "super_scales", "rows", "cols", "layout", "group",
-                 "struct")
+                 "struct", "address")
 
     def __init__(self, codes, scale, zero_point, super_scales, rows, cols, layout, group):
         self.codes, self.scale, self.zero_point, self.super_scales = codes, scale, zero_point, super_scales
@@ -77,6 +83,7 @@ class Weight4:
         self.struct = _lib.Weight4Struct(
             codes.data_ptr(), scale.data_ptr(), None if zero_point is None else zero_point.data_ptr(),
             None if super_scales is None else super_scales.data_ptr(), rows, cols, group, layout)
+        self.address = ctypes.addressof(self.struct)
 
 
 def weight4(codes: torch.Tensor, scale: torch.Tensor, rows: int, cols: int, granularity="group",
@@ -112,7 +119,7 @@ def weight4_double(dq: DoubleQuantized4Bit, rows: int, cols: int) -> Weight4:
 def _w4(w: Weight4):
     if not w.codes.is_cuda:
         raise ValueError("libqat takes CUDA tensors only")
-    return w.struct
+    return w.address
 
 
 def qat_linear4_workspace_bytes(dtype, tokens: int, cols: int) -> int:
@@ -143,14 +150,14 @@ def linear4(x: torch.Tensor, weight: Weight4) -> torch.Tensor:
     if not shape or shape[-1] != cols:
         raise _mismatch("linear4")
     x = x.contiguous()
-    tokens, dt, lib = _leading(x, shape), _dt(x), _lib.lib()
-    y = torch.empty((*shape[:-1], weight.rows), dtype=x.dtype, device=x.device)
+    tokens, dt, dev, lib = _leading(x, shape), _dt(x), x.device, _lib.lib()
+    y = torch.empty(shape[:-1] + (weight.rows,), dtype=x.dtype, device=dev)
     xp, ws, n = _ptr(x), None, 0
     if dt != BF16 or xp % 16:
         n = lib.qat_linear4_workspace_bytes(dt, tokens, cols)
-        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
     st = lib.qat_linear4(xp, dt, tokens, _w4(weight), y.data_ptr(), ws.data_ptr() if n else None, n,
-                         _here(x))
+                         _raw_stream(dev.index))
     if st:
         _lib.check("qat_linear4", st)
     return y
@@ -164,12 +171,12 @@ def gated_ffn4(x: torch.Tensor, gate: Weight4, up: Weight4, down: Weight4,
     if not shape or shape[-1] != gate.cols or down.cols != gate.rows:
         raise _mismatch("gated_ffn4")
     x = x.contiguous()
-    tokens, dt, lib = _leading(x, shape), _dt(x), _lib.lib()
-    y = torch.empty((*shape[:-1], down.rows), dtype=x.dtype, device=x.device)
+    tokens, dt, dev, lib = _leading(x, shape), _dt(x), x.device, _lib.lib()
+    y = torch.empty(shape[:-1] + (down.rows,), dtype=x.dtype, device=dev)
     n = lib.qat_gated_ffn4_workspace_bytes(dt, tokens, gate.cols, gate.rows)
-    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
     st = lib.qat_gated_ffn4(_ptr(x), dt, tokens, _w4(gate), _w4(up), _w4(down), _ACT[activation],
-                            y.data_ptr(), ws.data_ptr(), n, _here(x))
+                            y.data_ptr(), ws.data_ptr(), n, _raw_stream(dev.index))
     if st:
         _lib.check("qat_gated_ffn4", st)
     return y
@@ -329,26 +336,27 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     if not shape:
         raise _mismatch("layer_norm")
     x = x.contiguous()
+    lead, cols, dev, f32 = shape[:-1], shape[-1], x.device, torch.float32
     wp = bp = None
     if weight is not None:
-        weight = _vector("layer_norm", x, weight, shape[-1])
+        weight = _vector("layer_norm", x, weight, cols)
         wp = weight.data_ptr()
     if bias is not None:
-        bias = _vector("layer_norm", x, bias, shape[-1])
+        bias = _vector("layer_norm", x, bias, cols)
         bp = bias.data_ptr()
     y = torch.empty_like(x)
-    lead = shape[:-1]
-    mean = torch.empty(lead, dtype=torch.float32, device=x.device)
-    rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
-    st = _lib.lib().qat_layer_norm(_ptr(x), _dt(x), _leading(x, shape), shape[-1], wp, bp, eps,
-                                   y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _here(x))
+    mean = torch.empty(lead, dtype=f32, device=dev)
+    rstd = torch.empty(lead, dtype=f32, device=dev)
+    st = _lib.lib().qat_layer_norm(_ptr(x), _dt(x), _leading(x, shape), cols, wp, bp, eps,
+                                   y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                   _raw_stream(dev.index))
     if st:
         _lib.check("qat_layer_norm", st)
     return LayerNorm(y, mean, rstd)
 
 
 def _vector(what, x, v, cols):
-    if v.shape != (cols,):
+    if v.dim() != 1 or v.numel() != cols:
         raise _mismatch(what)
     if v.dtype != x.dtype or v.device != x.device:
         _of_type(x, v)
