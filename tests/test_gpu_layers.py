@@ -428,3 +428,18 @@ def test_ffn_wait_that_runs_out_is_reported(dtype, tokens, dim, hidden):
     flags.zero_()
     fq.qat_gated_ffn(x, tokens, dim, hidden, *w, wd, "silu", h, None, None, y, flags, ws)
     assert int(flags.item()) == 0 and torch.equal(y, want.y) and torch.equal(h, want.h)
+
+
+def test_example_trains_and_serves():
+    """The example layer learns (the loss falls by half at least) and its 4-bit
+    form stays near it: codes of 15 levels are off by 1/14 of a group's largest
+    weight at most, about a tenth of the block's output, which is a part of y."""
+    import os
+    import sys
+
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import qat_ffn_layer
+
+    losses, off = qat_ffn_layer.main(steps=60)
+    assert losses[-1] < 0.5 * losses[0]
+    assert off < 0.15
