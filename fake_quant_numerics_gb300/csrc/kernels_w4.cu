@@ -106,9 +106,9 @@ __global__ void __launch_bounds__(128) k_w4_generic(const void* __restrict__ x, 
 // middle, low: three hold all its 24 bits, two hold 16, enough under a bf16
 // output), one product each.
 //
-// k runs in blocks of 32 CH codes: lane t of a row's four takes 8 CH
-// consecutive codes (one load), so a load instruction covers 16 CH bytes of
-// each of 8 rows.  The order of k inside a word is the codes' bit order, the
+// k runs in blocks of 128 codes, in parts of 32 CH: lane t of a row's four takes
+// 8 CH consecutive codes of each part (one load), so that a part's codes share a
+// unit; lane t brings the scale of part t.  The order of k inside a word is the codes' bit order, the
 // same for both operands.  The warps of a block split k (and, with more tokens,
 // also the rows, so that they read the same x from L1) and walk over the
 // block's row tiles with the codes of the next blocks of k in flight across the
@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(128) k_w4_generic(const void* __restrict__ x, 
 // added in shared memory, then over the cluster, in a fixed order.
 // ---------------------------------------------------------------------------
 constexpr int kW4Warps = 16;
+constexpr int kW4Block = 128;  // codes of a row in a block of k
 enum { kOutF32 = 0, kOutBf16 = 1, kOutPlanes = 2 };
 
 struct W4Fast {
@@ -180,20 +181,21 @@ __device__ __forceinline__ uint4 x_pairs(const uint4& v) {
                     __byte_perm(v.y, v.w, 0x7632), __byte_perm(v.y, v.w, 0x5410));
 }
 
-template <int CH>
+// a lane's 4 words of a block of 128 codes of a row: 16 bytes at once, or 8 of
+// each half, or 4 of each quarter
 struct CodeWords {
-  uint32_t v[CH];
+  uint32_t v[4];
 };
 template <int CH>
-__device__ __forceinline__ void load_codes(CodeWords<CH>& o, const uint8_t* p) {
+__device__ __forceinline__ void load_codes(uint32_t* v, const uint8_t* p) {
   if constexpr (CH == 4) {
     const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p));
-    o.v[0] = q.x, o.v[1] = q.y, o.v[2] = q.z, o.v[3] = q.w;
+    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
   } else if constexpr (CH == 2) {
     const uint2 q = __ldcs(reinterpret_cast<const uint2*>(p));
-    o.v[0] = q.x, o.v[1] = q.y;
+    v[0] = q.x, v[1] = q.y;
   } else {
-    o.v[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
+    v[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
   }
 }
 
@@ -215,7 +217,7 @@ struct W4Shape {
 template <int TERMS, int CH, bool DBL, int NT, int NW>
 __global__ void __launch_bounds__(kW4Warps * 32, 1) k_w4(const __grid_constant__ W4Args p) {
   using S = W4Shape<NT, NW>;
-  constexpr int KB = 32 * CH, D = S::kDepth, kTerms = TERMS ? TERMS : 1, R = S::R;
+  constexpr int KB = kW4Block, SUB = 4 / CH, D = S::kDepth, kTerms = TERMS ? TERMS : 1, R = S::R;
   extern __shared__ __align__(16) float red[];  // [slot][k slice][weight][row][token]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int wr = warp % S::WR, wk = warp / S::WR, split = p.split;
@@ -238,12 +240,14 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) k_w4(const __grid_constant__
   // The loads in flight, as loaded: codes, scales and zero points of D blocks of
   // k, for the rows g and g + 8 of the two row tiles.  Offsets are 32-bit and the
   // same for both weights.
-  CodeWords<CH> code[D][2][2];
+  CodeWords code[D][2][2];
   uint32_t sc[D][2][2];
   float sup[D][2][2];
   int zp[D][2][2];
   uint32_t co[R][2], so[R][2];  // codes, units
   int f_tile = 0, f_kb = start;
+  const int part_t = t & (SUB - 1);                // the part whose scale this lane brings
+  const int parts = (cols + 32 * CH - 1) / (32 * CH);  // parts of a row
   // rows past the end read row 0 and are dropped at the end
   const auto rows_of = [&](int tile) {
 #pragma unroll
@@ -260,16 +264,23 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) k_w4(const __grid_constant__
   const uint32_t so_step = (uint32_t)(stride * S::kRows) * (uint32_t)p.row_units;
   const bool affine = p.w[0].zp != nullptr;
   const auto fetch = [&](int d) {
+    const uint32_t run = (uint32_t)min(f_kb * SUB + part_t, parts - 1);
+    const uint32_t u = __umulhi(2 * run + 1, p.unit_magic);
+    uint32_t off[SUB];
     // past the row's end (in its last block) the lane reads the row's first
     // codes; x is zero there
-    const uint32_t off = f_kb * KB + t * 8 * CH < cols ? (uint32_t)f_kb * (KB / 2) : 0u - t * 4 * CH;
-    const uint32_t u = __umulhi(2u * f_kb + 1, p.unit_magic);
+#pragma unroll
+    for (int s = 0; s < SUB; ++s)
+      off[s] = f_kb * KB + s * 32 * CH + t * 8 * CH < cols
+                   ? (uint32_t)f_kb * (KB / 2) + s * 16 * CH : 0u - t * 4 * CH;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const W4Fast& w = p.w[i / R];
-        load_codes<CH>(code[d][i][h], w.codes + (co[i % R][h] + off));
+#pragma unroll
+        for (int s = 0; s < SUB; ++s)
+          load_codes<CH>(code[d][i][h].v + s * CH, w.codes + (co[i % R][h] + off[s]));
         const uint32_t at = so[i % R][h] + u;
         if (DBL) {
           sc[d][i][h] = __ldg(static_cast<const uint8_t*>(w.scales) + at);
@@ -388,59 +399,77 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) k_w4(const __grid_constant__
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       if (it + d >= work) break;
-      const bool in = kb * KB + t * 8 * CH < cols;
       uint32_t bias[2][2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) bias[i][h] = !DBL && affine ? w4_bias(zp[d][i][h]) : 0x43084308u;
-      const uint4* xs[NT][kTerms];
-#pragma unroll
-      for (int q = 0; q < NT; ++q)
-#pragma unroll
-        for (int m = 0; m < kTerms; ++m)
-          xs[q][m] = in ? reinterpret_cast<const uint4*>(xp[q] + m * p.x_plane + kb * KB) : kZeros;
-      float part[2][NT][4];
-#pragma unroll
-      for (int j = 0; j < CH; ++j) {
-        uint4 b[NT][kTerms];
-#pragma unroll
-        for (int q = 0; q < NT; ++q)
-#pragma unroll
-          for (int m = 0; m < kTerms; ++m) b[q][m] = x_pairs<TERMS != 0>(__ldg(xs[q][m] + j));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t a[2][4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              a[h][e] = w4_pair(code[d][i][h].v[j] >> (4 * e), bias[i][h]);
-#pragma unroll
-          for (int q = 0; q < NT; ++q)
-#pragma unroll
-            for (int m = kTerms - 1; m >= 0; --m) {
-              if (j == 0 && m == kTerms - 1)
-                mma_16816_first(part[i][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m].x, b[q][m].y);
-              else
-                mma_16816(part[i][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m].x, b[q][m].y);
-              mma_16816(part[i][q], a[0][2], a[1][2], a[0][3], a[1][3], b[q][m].z, b[q][m].w);
-            }
-        }
-      }
+      float scale[2][2];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          bias[i][h] = !DBL && affine ? w4_bias(zp[d][i][h]) : 0x43084308u;
           // two-level: within an ulp of (q / 255) * super
-          const float s = DBL ? (float)sc[d][i][h] * (1.0f / 255.0f) * sup[d][i][h]
-                              : __uint_as_float(sc[d][i][h]);
+          scale[i][h] = DBL ? (float)sc[d][i][h] * (1.0f / 255.0f) * sup[d][i][h]
+                            : __uint_as_float(sc[d][i][h]);
+        }
 #pragma unroll
-          for (int q = 0; q < NT; ++q) {
-            total[i][q][2 * h] = fmaf(part[i][q][2 * h], s, total[i][q][2 * h]);
-            total[i][q][2 * h + 1] = fmaf(part[i][q][2 * h + 1], s, total[i][q][2 * h + 1]);
+      for (int s = 0; s < SUB; ++s) {
+        const int k = kb * KB + s * 32 * CH;
+        const bool in = k + t * 8 * CH < cols;
+        const uint4* xs[NT][kTerms];
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+#pragma unroll
+          for (int m = 0; m < kTerms; ++m)
+            xs[q][m] = in ? reinterpret_cast<const uint4*>(xp[q] + m * p.x_plane + k) : kZeros;
+        // this part's parameters, from the lane that has them
+        uint32_t bs[2][2];
+        float ss[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            bs[i][h] = bias[i][h];
+            ss[i][h] = scale[i][h];
+            if (SUB > 1) {
+              ss[i][h] = __shfl_sync(~0u, ss[i][h], s, 4);
+              if (!DBL && affine) bs[i][h] = __shfl_sync(~0u, bs[i][h], s, 4);
+            }
+          }
+        float part[2][NT][4];
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+          uint4 b[NT][kTerms];
+#pragma unroll
+          for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int m = 0; m < kTerms; ++m) b[q][m] = x_pairs<TERMS != 0>(__ldg(xs[q][m] + j));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t a[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                a[h][e] = w4_pair(code[d][i][h].v[s * CH + j] >> (4 * e), bs[i][h]);
+#pragma unroll
+            for (int q = 0; q < NT; ++q)
+#pragma unroll
+              for (int m = kTerms - 1; m >= 0; --m) {
+                if (j == 0 && m == kTerms - 1)
+                  mma_16816_first(part[i][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m].x, b[q][m].y);
+                else
+                  mma_16816(part[i][q], a[0][0], a[1][0], a[0][1], a[1][1], b[q][m].x, b[q][m].y);
+                mma_16816(part[i][q], a[0][2], a[1][2], a[0][3], a[1][3], b[q][m].z, b[q][m].w);
+              }
           }
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              total[i][q][e] = fmaf(part[i][q][e], ss[i][e >> 1], total[i][q][e]);
+      }
       if (it + d + D < work) fetch(d);
       kb += step;
       if (--left == 0) {
@@ -515,9 +544,9 @@ template <int TERMS, int CH, bool DBL, int NT, int NW>
 static qat_status launch_fast(W4Args p, bool pdl, cudaStream_t s) {
   using S = W4Shape<NT, NW>;
   p.tiles = (int)((p.rows + S::kRows - 1) / S::kRows);
-  const int kblocks = (p.cols + 32 * CH - 1) / (32 * CH);
-  // the unit of block kb in its row is kb / d, as (2 kb + 1) ceil(2^31 / d) >> 32
-  // (exact while 2 kb d < 2^31); rows that are one unit: 0
+  const int kblocks = (p.cols + kW4Block - 1) / kW4Block;
+  // the unit of part j of a row is j / d, as (2 j + 1) ceil(2^31 / d) >> 32 (exact
+  // while 2 j d < 2^31); rows that are one unit: 0
   const int64_t d = p.unit / (32 * CH);
   p.unit_magic = p.unit >= p.cols ? 0u : (uint32_t)(((INT64_C(1) << 31) + d - 1) / d);
   const int room = device_info().sms;
