@@ -513,26 +513,16 @@ static qat_status norm_fwd(const void* x, int64_t rows, int64_t cols, const void
     QAT_FWD(1, 1);
   } else if (cols <= 512) {
     QAT_FWD(1, 2);
-  } else if constexpr (T::BYTES == 2) {  // 64 bytes of a row a thread
-    if (cols <= 1024)
-      QAT_FWD(1, 4);
-    else if (cols <= 2048)
-      QAT_FWD(2, 4);
-    else if (cols <= 4096)
-      QAT_FWD(4, 4);
-    else if (cols <= 8192)
-      QAT_FWD(8, 4);
-    else
-      QAT_FWD(16, 4);
+  } else if (cols <= 1024) {  // 32 elements a thread: enough bytes in flight
+    QAT_FWD(1, 4);
+  } else if (cols <= 2048) {
+    QAT_FWD(2, 4);
+  } else if (cols <= 4096) {
+    QAT_FWD(4, 4);
+  } else if (cols <= 8192) {
+    QAT_FWD(8, 4);
   } else {
-    if (cols <= 2048)
-      QAT_FWD(4, 2);
-    else if (cols <= 4096)
-      QAT_FWD(8, 2);
-    else if (cols <= 8192)
-      QAT_FWD(16, 2);
-    else
-      QAT_FWD(16, 4);
+    QAT_FWD(16, 4);
   }
 #undef QAT_FWD
   count_launch(1);
