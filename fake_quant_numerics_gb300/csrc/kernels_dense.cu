@@ -16,6 +16,16 @@
 // operands faster than shared memory delivers them).  CG = 1: 128 x 128 tiles,
 // and where those are few a cluster of up to eight CTAs splits k and adds its
 // sums through distributed shared memory in rank order.
+//
+// Measured at 4096 x 4096 x 14336 (tokens, dim, hidden; repeated calls, power
+// capped): the gated product 585 us (1644 TFLOP/s), the one back 335 (1435, its
+// tiles fill 3.4 waves of 76 pairs), dh 362 (1328, the epilogue reads and writes
+// 12 bytes an element), dx 650 (1480), the three weight gradients 938 (1539);
+// cuBLAS runs plain products at 1708 under the same cap.  fp32 at 2048 x 4096 x
+// 14336: 239 TFLOP/s forward, six bf16 products each.  With one token the weights
+// are read at 3.8 to 4.3 TB/s: half of each stage holds rows of x that do not
+// exist, so too few bytes are in flight.
+
 #include "qat_dense.h"
 #include "qat_layer.cuh"
 #include "qat_tc.cuh"

@@ -4,8 +4,15 @@
 //   p = dy * w;  dx = rstd * (p - mean(p) - z * mean(p * z))
 //   dw = sum_rows dy * z,  db = sum_rows dy
 //
-// Every kernel is bound by reading its rows.  Sums are binary32 trees around
-// the mean; dw and db are added over the rows in a fixed order.
+// The floor is reading the rows once and writing as many.  Sums are binary32
+// trees around the mean; dw and db are added over the rows in a fixed order.
+//
+// Measured, bytes that have to move over the copy rate: bf16 16384 x 4096 forward
+// 48 us (82%), backward 72 us (83%, its second kernel, which joins the column
+// sums, 7 us of it); fp32 8192 x 4096 forward 43 us (93%), backward 65 us (92%);
+// bf16 is held back by instruction issue (56% and 46% of the slots) as much as
+// by memory.  fp32 2053 x 5003, whose rows are not whole vectors: 20 and 38 us
+// (60% and 47%), one element a load.  4 x 4096: 3.2 and 4.4 us.
 #include "qat_layer.cuh"
 #include "qat_layer.h"
 
