@@ -13,6 +13,7 @@
 // dg and du likewise; g and u are kept in binary32 for the backward pass (a bf16
 // copy would double the error of dg).
 #include "qat_dense.h"
+#include "qat_few.h"
 #include "qat_layer.h"
 
 namespace qat {
@@ -77,6 +78,31 @@ static FwdOps fwd_ops(Packer& w, int64_t t, int64_t d, int64_t f, const void* x,
   return o;
 }
 
+// fp32 layers of a few tokens read their weights as they are.
+static bool few(qat_dtype dt, int64_t t) { return dt == QAT_F32 && t <= kFewTokens; }
+
+// The backward pass of a few fp32 tokens: dg and du in binary32, then they and
+// the tokens as operands of the weight gradients (t is short there, the weights
+// are outputs).
+struct FewOps {
+  float *dg32, *du32;
+  DenseOp dy, x, h, dg, du;
+};
+static FewOps few_ops(Packer& w, int64_t t, int64_t d, int64_t f, const void* dy, const void* x,
+                      const void* h) {
+  FewOps o;
+  const size_t bytes = r256((size_t)t * f * 4);
+  o.dg32 = reinterpret_cast<float*>(w.base + w.used);
+  o.du32 = reinterpret_cast<float*>(w.base + w.used + bytes);
+  w.used += 2 * bytes;
+  o.dy = w.operand(dy, t, d);
+  o.x = w.operand(x, t, d);
+  o.h = w.operand(h, t, f);
+  o.dg = w.operand(o.dg32, t, f);
+  o.du = w.operand(o.du32, t, f);
+  return o;
+}
+
 struct BwdOps {
   DenseOp dy, x, wg, wu, wd, h, dg, du;
 };
@@ -97,6 +123,10 @@ static BwdOps bwd_ops(Packer& w, int64_t t, int64_t d, int64_t f, const void* dy
 
 size_t ffn_ws_bytes(qat_dtype dt, int64_t t, int64_t d, int64_t f, bool backward) {
   Packer w = {dt, 0};
+  if (few(dt, t)) {
+    if (backward) few_ops(w, t, d, f, nullptr, nullptr, nullptr);
+    return w.used;
+  }
   if (backward)
     bwd_ops(w, t, d, f, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
   else
@@ -119,6 +149,12 @@ qat_status launch_ffn_fwd(const void* x, qat_dtype dt, int64_t t, int64_t d, int
     if (!st) st = zero(h, t * f, dt, s);
     if (!st) st = zero(gp, t * f, QAT_F32, s);
     return st ? st : zero(up, t * f, QAT_F32, s);
+  }
+  if (few(dt, t)) {
+    const auto f32 = [](const void* p) { return static_cast<const float*>(p); };
+    const qat_status st = launch_few_gated(f32(x), t, d, f, f32(wg), f32(wu), act,
+                                           static_cast<float*>(h), gp, up, false, s);
+    return st ? st : launch_few_rows(f32(h), t, f, d, f32(wd), static_cast<float*>(y), true, s);
   }
   Packer w = {dt, reinterpret_cast<uintptr_t>(ws)};
   const FwdOps o = fwd_ops(w, t, d, f, x, wg, wu, wd, h);
@@ -171,44 +207,64 @@ qat_status launch_ffn_bwd(const void* dy, const void* x, qat_dtype dt, int64_t t
     return st ? st : zero(dwd, d * f, dt, s);
   }
   Packer w = {dt, reinterpret_cast<uintptr_t>(ws)};
-  const BwdOps o = bwd_ops(w, t, d, f, dy, x, wg, wu, wd, h);
-  qat_status st = w.go(s);
-  if (!st && (dx || dwg || dwu)) {
-    Dense q = {};
-    q.epi = kDenseGatedBwd;
-    q.dtype = dt;
-    q.m = t;
-    q.n = f;
-    q.k = d;
-    q.a[0] = o.dy;
-    q.b[0] = turned(o.wd);
-    q.act = act;
-    q.gp = const_cast<float*>(gp);
-    q.up = const_cast<float*>(up);
-    q.q[0] = const_cast<void*>(o.dg.p);
-    q.q[1] = const_cast<void*>(o.du.p);
-    q.q_pitch = o.dg.pitch;
-    q.q_part = o.dg.part;
-    q.flags = flags;
-    q.pdl = w.next();
-    st = launch_dense(q, s);
-  }
-  if (!st && dx) {
-    Dense q = {};
-    q.epi = kDenseStore;
-    q.dtype = dt;
-    q.m = t;
-    q.n = d;
-    q.k = f;
-    q.segs = 2;
-    q.a[0] = o.dg;
-    q.a[1] = o.du;
-    q.b[0] = turned(o.wg);
-    q.b[1] = turned(o.wu);
-    q.c[0] = dx;
-    q.flags = flags;
-    q.pdl = w.next();
-    st = launch_dense(q, s);
+  DenseOp dy_op, x_op, h_op, dg_op, du_op;
+  qat_status st = QAT_OK;
+  if (few(dt, t)) {
+    const auto f32 = [](const void* p) { return static_cast<const float*>(p); };
+    const FewOps o = few_ops(w, t, d, f, dy, x, h);
+    if (dx || dwg || dwu) {
+      st = launch_few_gated_bwd(f32(dy), t, d, f, f32(wd), act, gp, up, o.dg32, o.du32, false, s);
+      w.launched = true;
+    }
+    if (!st && dx)
+      st = launch_few_cols2(o.dg32, o.du32, t, f, d, f32(wg), f32(wu), static_cast<float*>(dx), true, s);
+    if (!st && (dwg || dwu || dwd)) {
+      // without dg and du only dy, x and h are packed
+      if (!(dwg || dwu)) w.n = 3;
+      st = w.go(s);
+    }
+    dy_op = o.dy, x_op = o.x, h_op = o.h, dg_op = o.dg, du_op = o.du;
+  } else {
+    const BwdOps o = bwd_ops(w, t, d, f, dy, x, wg, wu, wd, h);
+    dy_op = o.dy, x_op = o.x, h_op = o.h, dg_op = o.dg, du_op = o.du;
+    st = w.go(s);
+    if (!st && (dx || dwg || dwu)) {
+      Dense q = {};
+      q.epi = kDenseGatedBwd;
+      q.dtype = dt;
+      q.m = t;
+      q.n = f;
+      q.k = d;
+      q.a[0] = o.dy;
+      q.b[0] = turned(o.wd);
+      q.act = act;
+      q.gp = const_cast<float*>(gp);
+      q.up = const_cast<float*>(up);
+      q.q[0] = const_cast<void*>(o.dg.p);
+      q.q[1] = const_cast<void*>(o.du.p);
+      q.q_pitch = o.dg.pitch;
+      q.q_part = o.dg.part;
+      q.flags = flags;
+      q.pdl = w.next();
+      st = launch_dense(q, s);
+    }
+    if (!st && dx) {
+      Dense q = {};
+      q.epi = kDenseStore;
+      q.dtype = dt;
+      q.m = t;
+      q.n = d;
+      q.k = f;
+      q.segs = 2;
+      q.a[0] = o.dg;
+      q.a[1] = o.du;
+      q.b[0] = turned(o.wg);
+      q.b[1] = turned(o.wu);
+      q.c[0] = dx;
+      q.flags = flags;
+      q.pdl = w.next();
+      st = launch_dense(q, s);
+    }
   }
   if (!st && (dwg || dwu)) {
     Dense q = {};
@@ -218,9 +274,9 @@ qat_status launch_ffn_bwd(const void* dy, const void* x, qat_dtype dt, int64_t t
     q.n = d;
     q.k = t;
     q.problems = dwg && dwu ? 2 : 1;
-    q.a[0] = turned(dwg ? o.dg : o.du);
-    q.a[1] = turned(o.du);
-    q.b[0] = turned(o.x);
+    q.a[0] = turned(dwg ? dg_op : du_op);
+    q.a[1] = turned(du_op);
+    q.b[0] = turned(x_op);
     q.c[0] = dwg ? dwg : dwu;
     q.c[1] = dwu;
     q.flags = flags;
@@ -234,8 +290,8 @@ qat_status launch_ffn_bwd(const void* dy, const void* x, qat_dtype dt, int64_t t
     q.m = d;
     q.n = f;
     q.k = t;
-    q.a[0] = turned(o.dy);
-    q.b[0] = turned(o.h);
+    q.a[0] = turned(dy_op);
+    q.b[0] = turned(h_op);
     q.c[0] = dwd;
     q.flags = flags;
     q.pdl = w.next();

@@ -402,7 +402,7 @@ def test_side_stream_and_graph_replay():
 
 # --- failure detection ---------------------------------------------------------
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("tokens,dim,hidden", [(5, 1024, 256), (200, 128, 128), (2600, 256, 2048)])
+@pytest.mark.parametrize("tokens,dim,hidden", [(70, 1024, 256), (200, 128, 128), (2600, 256, 2048)])
 def test_ffn_wait_that_runs_out_is_reported(dtype, tokens, dim, hidden):
     """With no polls allowed every bounded wait of the products gives up at once:
     the call returns, flags the time-out and leaves NaN, and the next call (with
