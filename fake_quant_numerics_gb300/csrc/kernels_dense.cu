@@ -117,25 +117,10 @@ __device__ __forceinline__ void ld_row32(const float* p, int64_t at, int left, u
     for (int i = 0; i < 32; ++i) v[i] = i < left ? p[at + i] : 0.0f;
   }
 }
-// 32 consecutive outputs as an operand of a later product
-template <typename T>
+// 32 consecutive bf16 outputs as an operand of a later product
 __device__ __forceinline__ void st_parts32(const DenseArgs& p, int which, int64_t row, int64_t c,
                                            int left, const float (&v)[32]) {
-  const int64_t at = row * p.q_pitch + c;
-  if constexpr (T::BYTES == 2) {
-    st_row32<BF16>(p.q[which], at, left, 16, v);
-  } else {
-    float r[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) r[i] = v[i];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      float h[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) h[i] = take_bf16(r[i]);
-      st_row32<BF16>(p.q[which], at + k * p.q_part, left, 16, h);
-    }
-  }
+  st_row32<BF16>(p.q[which], row * p.q_pitch + c, left, 16, v);
 }
 // the largest of 32, 16 or 1 that divides the address and the row pitch
 __device__ __forceinline__ uint32_t row_align(const void* p, int64_t pitch_bytes) {
@@ -143,22 +128,22 @@ __device__ __forceinline__ uint32_t row_align(const void* p, int64_t pitch_bytes
   return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : 1;
 }
 
-// One row's 32 columns from column c on
+// One row's 32 columns of a bf16 layer from column c on
 // (gated: v = g, u beside it; backward: v = dh, g and w = u as kept)
-template <typename T, int EPI>
+template <int EPI>
 __device__ __forceinline__ void finish32(const DenseArgs& p, int prob, int64_t row, int64_t c,
                                          const float (&v)[32], const float (&u)[32],
                                          const float (&g)[32], const float (&w)[32]) {
   const int64_t at = row * p.n + c;
   const int left = (int)min((int64_t)32, p.n - c);
   if (EPI == kDenseStore) {
-    st_row32<T>(p.c[prob], at, left, row_align(p.c[prob], p.n * T::BYTES), v);
+    st_row32<BF16>(p.c[prob], at, left, row_align(p.c[prob], p.n * 2), v);
   } else if (EPI == kDenseGated) {
     float h[32];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) h[i] = act_value<T::BYTES == 2>(p.act, v[i]) * u[i];
-    st_row32<T>(p.c[0], at, left, row_align(p.c[0], p.n * T::BYTES), h);
-    if (p.q[0]) st_parts32<T>(p, 0, row, c, left, h);
+    for (int i = 0; i < 32; ++i) h[i] = act_value<true>(p.act, v[i]) * u[i];
+    st_row32<BF16>(p.c[0], at, left, row_align(p.c[0], p.n * 2), h);
+    if (p.q[0]) st_parts32(p, 0, row, c, left, h);
     if (p.gp) {
       st_row32<F32>(p.gp, at, left, row_align(p.gp, p.n * 4), v);
       st_row32<F32>(p.up, at, left, row_align(p.up, p.n * 4), u);
@@ -168,12 +153,75 @@ __device__ __forceinline__ void finish32(const DenseArgs& p, int prob, int64_t r
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       float a, da;
-      act_grad<T::BYTES == 2>(p.act, g[i], a, da);
+      act_grad<true>(p.act, g[i], a, da);
       dg[i] = v[i] * w[i] * da;
       du[i] = v[i] * a;
     }
-    st_parts32<T>(p, 0, row, c, left, dg);
-    st_parts32<T>(p, 1, row, c, left, du);
+    st_parts32(p, 0, row, c, left, dg);
+    st_parts32(p, 1, row, c, left, du);
+  }
+}
+// The same for eight columns of a fp32 layer, whose sums leave fewer registers.
+__device__ __forceinline__ void st_row8(float* p, int64_t at, int left, bool vec, const float (&v)[8]) {
+  if (vec && left >= 8) {
+    float4* q = reinterpret_cast<float4*>(p + at);
+    q[0] = make_float4(v[0], v[1], v[2], v[3]);
+    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) p[at + i] = v[i];
+  }
+}
+__device__ __forceinline__ void st_parts8(const DenseArgs& p, int which, int64_t row, int64_t c,
+                                          int left, const float (&v)[8]) {
+  const int64_t at = row * p.q_pitch + c;
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = v[i];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    float h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = take_bf16(r[i]);
+    // pitch, part and c are multiples of 8; the padding of a row may be written
+    __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p.q[which]) + at + k * p.q_part;
+    if (left > 0)
+      *reinterpret_cast<uint4*>(q) = make_uint4(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]),
+                                                pack_bf16x2(h[4], h[5]), pack_bf16x2(h[6], h[7]));
+  }
+}
+template <int EPI>
+__device__ __forceinline__ void finish8(const DenseArgs& p, int prob, int64_t row, int64_t c,
+                                        const float (&v)[8], const float (&u)[8],
+                                        const float (&g)[8], const float (&w)[8]) {
+  const int64_t at = row * p.n + c;
+  const int left = (int)min((int64_t)8, p.n - c);
+  const bool whole = p.n % 4 == 0;
+  const auto vec = [&](const void* q) { return whole && reinterpret_cast<uint64_t>(q) % 16 == 0; };
+  if (EPI == kDenseStore) {
+    st_row8(static_cast<float*>(p.c[prob]), at, left, vec(p.c[prob]), v);
+  } else if (EPI == kDenseGated) {
+    float h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = act_value<false>(p.act, v[i]) * u[i];
+    st_row8(static_cast<float*>(p.c[0]), at, left, vec(p.c[0]), h);
+    st_parts8(p, 0, row, c, left, h);
+    if (p.gp) {
+      st_row8(p.gp, at, left, vec(p.gp), v);
+      st_row8(p.up, at, left, vec(p.up), u);
+    }
+  } else {
+    float dg[8], du[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float a, da;
+      act_grad<false>(p.act, g[i], a, da);
+      dg[i] = v[i] * w[i] * da;
+      du[i] = v[i] * a;
+    }
+    st_parts8(p, 0, row, c, left, dg);
+    st_parts8(p, 1, row, c, left, du);
   }
 }
 // The same for four columns.
@@ -507,25 +555,34 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    const auto side_take = [&](float (&g)[32], float (&u)[32]) {
+    const auto side_wait = [&]() {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncwarp();
-      const uint8_t* at = raw + (side_at - tc::smem(raw)) + lane * 128;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float4 a = *reinterpret_cast<const float4*>(at + ((k ^ (lane & 7)) * 16));
-        const float4 b = *reinterpret_cast<const float4*>(at + 4096 + ((k ^ (lane & 7)) * 16));
-        g[4 * k] = a.x, g[4 * k + 1] = a.y, g[4 * k + 2] = a.z, g[4 * k + 3] = a.w;
-        u[4 * k] = b.x, u[4 * k + 1] = b.y, u[4 * k + 2] = b.z, u[4 * k + 3] = b.w;
-      }
-      __syncwarp();  // taken: the next columns may come in
     };
-    // g and u of this thread's row, columns c on; starts the next 32 columns
+    // g and u of four columns of this thread's row
+    const auto side_get = [&](int k, float4& g, float4& u) {
+      const uint8_t* at = raw + (side_at - tc::smem(raw)) + lane * 128 + ((k ^ (lane & 7)) * 16);
+      g = *reinterpret_cast<const float4*>(at);
+      u = *reinterpret_cast<const float4*>(at + 4096);
+    };
+    // taken: the next 32 columns may come in
+    const auto side_next = [&](int64_t row, int64_t c, bool more) {
+      __syncwarp();
+      if (more) side_load(row - lane, c);
+    };
+    // g and u of this thread's row, 32 columns from c on
     const auto kept = [&](float (&g)[32], float (&u)[32], int64_t row, int64_t c, bool more) {
       if constexpr (EPI == kDenseGatedBwd) {
         if (side) {
-          side_take(g, u);
-          if (more) side_load(row - lane, c + 32);
+          side_wait();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float4 a, b;
+            side_get(k, a, b);
+            g[4 * k] = a.x, g[4 * k + 1] = a.y, g[4 * k + 2] = a.z, g[4 * k + 3] = a.w;
+            u[4 * k] = b.x, u[4 * k + 1] = b.y, u[4 * k + 2] = b.z, u[4 * k + 3] = b.w;
+          }
+          side_next(row, c + 32, more);
         } else if (row < p.m && c < p.n) {
           const int left = (int)min((int64_t)32, p.n - c);
           ld_row32(p.gp, row * p.n + c, left, row_align(p.gp, p.n * 4), g);
@@ -578,15 +635,38 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
         }
 #pragma unroll
         for (int c = 0; c < kHalf; c += 32) {
-          float v[32], u[32], g[32], k[32];
           if (c >= c_count) break;
-          kept(g, k, row, col + c, c + 32 < kHalf);
+          if (side) side_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            v[i] = sv[c + i];
-            u[i] = su[(c + i) % kU];
+          for (int e = 0; e < 32; e += 8) {
+            float v[8], u[8], g[8], k[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              v[i] = sv[c + e + i];
+              u[i] = su[(c + e + i) % kU];
+            }
+            const int64_t at = col + c + e;
+            if constexpr (EPI == kDenseGatedBwd) {
+              if (side) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 4) {
+                  float4 a, b;
+                  side_get((e + i) / 4, a, b);
+                  g[i] = a.x, g[i + 1] = a.y, g[i + 2] = a.z, g[i + 3] = a.w;
+                  k[i] = b.x, k[i + 1] = b.y, k[i + 2] = b.z, k[i + 3] = b.w;
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const bool in = row < p.m && at + i < p.n;
+                  g[i] = in ? p.gp[row * p.n + at + i] : 0.0f;
+                  k[i] = in ? p.up[row * p.n + at + i] : 0.0f;
+                }
+              }
+            }
+            if (row < p.m && at < p.n) finish8<EPI>(p, w.prob, row, at, v, u, g, k);
           }
-          if (row < p.m && col + c < p.n) finish32<T, EPI>(p, w.prob, row, col + c, v, u, g, k);
+          if (side) side_next(row, col + c + 32, c + 32 < c_count);
         }
       } else {
         const uint32_t acc = next_sum();
@@ -612,7 +692,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
           } else {
             float g[32], k[32];
             kept(g, k, row, col + c, c + 32 < kHalf);
-            if (row < p.m && col + c < p.n) finish32<T, EPI>(p, w.prob, row, col + c, v, u, g, k);
+            if (row < p.m && col + c < p.n) finish32<EPI>(p, w.prob, row, col + c, v, u, g, k);
           }
         }
         if (CG == 1 && p.split > 1) break;  // joined below
