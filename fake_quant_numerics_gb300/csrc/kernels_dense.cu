@@ -606,8 +606,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
         for (int i = 0; i < kHalf; ++i) sv[i] = 0.0f;
 #pragma unroll
         for (int i = 0; i < kU; ++i) su[i] = 0.0f;
+        uint32_t acc = 0;
         for (int un = u0; un < u1; ++un) {
-          const uint32_t acc = next_sum();
+          acc = next_sum();
 #pragma unroll
           for (int c = 0; c < kHalf; c += 32) {
             uint32_t r[32];
@@ -622,7 +623,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
               for (int i = 0; i < 32; ++i) su[c + i] += __uint_as_float(r[i]);
             }
           }
-          sum_read();
+          if (un + 1 < u1) sum_read();
         }
         if (CG == 1 && p.split > 1) {
 #pragma unroll
@@ -633,40 +634,50 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
           }
           break;  // joined below
         }
+        // the whole sums go back to their place in tensor memory, from where a
+        // short loop takes them: the code for all columns at once, unrolled for
+        // the registers, would not fit the instruction cache
 #pragma unroll
         for (int c = 0; c < kHalf; c += 32) {
-          if (c >= c_count) break;
-          if (side) side_wait();
+          tc::tmem_st32(acc + c, sv + c);
+          if constexpr (EPI == kDenseGated) tc::tmem_st32(acc + kOut + c, su + c);
+        }
+        tc::tmem_st_wait();
+#pragma unroll 1
+        for (int c = 0; c < c_count; c += 8) {
+          uint32_t r[8], q[8];
+          tc::tmem_ld8(acc + c, r);
+          if (EPI == kDenseGated) tc::tmem_ld8(acc + kOut + c, q);
+          tc::tmem_ld_wait();
+          if (c + 8 >= c_count) sum_read();
+          float v[8], u[8], g[8], k[8];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            float v[8], u[8], g[8], k[8];
+          for (int i = 0; i < 8; ++i) {
+            v[i] = __uint_as_float(r[i]);
+            u[i] = EPI == kDenseGated ? __uint_as_float(q[i]) : 0.0f;
+          }
+          const int64_t at = col + c;
+          if constexpr (EPI == kDenseGatedBwd) {
+            if (side) {
+              if (c % 32 == 0) side_wait();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              v[i] = sv[c + e + i];
-              u[i] = su[(c + e + i) % kU];
-            }
-            const int64_t at = col + c + e;
-            if constexpr (EPI == kDenseGatedBwd) {
-              if (side) {
+              for (int i = 0; i < 8; i += 4) {
+                float4 a, b;
+                side_get((c % 32 + i) / 4, a, b);
+                g[i] = a.x, g[i + 1] = a.y, g[i + 2] = a.z, g[i + 3] = a.w;
+                k[i] = b.x, k[i + 1] = b.y, k[i + 2] = b.z, k[i + 3] = b.w;
+              }
+              if (c % 32 == 24) side_next(row, at + 8, c + 8 < c_count);
+            } else {
 #pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                  float4 a, b;
-                  side_get((e + i) / 4, a, b);
-                  g[i] = a.x, g[i + 1] = a.y, g[i + 2] = a.z, g[i + 3] = a.w;
-                  k[i] = b.x, k[i + 1] = b.y, k[i + 2] = b.z, k[i + 3] = b.w;
-                }
-              } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const bool in = row < p.m && at + i < p.n;
-                  g[i] = in ? p.gp[row * p.n + at + i] : 0.0f;
-                  k[i] = in ? p.up[row * p.n + at + i] : 0.0f;
-                }
+              for (int i = 0; i < 8; ++i) {
+                const bool in = row < p.m && at + i < p.n;
+                g[i] = in ? p.gp[row * p.n + at + i] : 0.0f;
+                k[i] = in ? p.up[row * p.n + at + i] : 0.0f;
               }
             }
-            if (row < p.m && at < p.n) finish8<EPI>(p, w.prob, row, at, v, u, g, k);
           }
-          if (side) side_next(row, col + c + 32, c + 32 < c_count);
+          if (row < p.m && at < p.n) finish8<EPI>(p, w.prob, row, at, v, u, g, k);
         }
       } else {
         const uint32_t acc = next_sum();
