@@ -67,12 +67,12 @@ struct DenseArgs {
   uint32_t limit;
 };
 
-// 32 consecutive outputs of one row: full vectors where the row allows
+// 16 consecutive outputs of one row: full vectors where the row allows
 template <typename T>
-__device__ __forceinline__ void st_row32(void* p, int64_t at, int left, uint32_t align,
-                                         const float (&v)[32]) {
-  if (left >= 32 && align >= 16) {
-    constexpr int W = T::BYTES == 4 ? 32 : 16;  // words
+__device__ __forceinline__ void st_row16(void* p, int64_t at, int left, uint32_t align,
+                                         const float (&v)[16]) {
+  if (left >= 16 && align >= 16) {
+    constexpr int W = T::BYTES == 4 ? 16 : 8;  // words
     uint32_t w[W];
     if (T::BYTES == 4) {
 #pragma unroll
@@ -97,15 +97,15 @@ __device__ __forceinline__ void st_row32(void* p, int64_t at, int left, uint32_t
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < 16; ++i)
       if (i < left) st_elem<T>(p, at + i, v[i]);
   }
 }
-__device__ __forceinline__ void ld_row32(const float* p, int64_t at, int left, uint32_t align,
-                                         float (&v)[32]) {
-  if (left >= 32 && align >= 16) {
+__device__ __forceinline__ void ld_row16(const float* p, int64_t at, int left, uint32_t align,
+                                         float (&v)[16]) {
+  if (left >= 16 && align >= 16) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
+    for (int i = 0; i < 16; i += 4) {
       const float4 q = *reinterpret_cast<const float4*>(p + at + i);
       v[i] = q.x;
       v[i + 1] = q.y;
@@ -114,13 +114,13 @@ __device__ __forceinline__ void ld_row32(const float* p, int64_t at, int left, u
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = i < left ? p[at + i] : 0.0f;
+    for (int i = 0; i < 16; ++i) v[i] = i < left ? p[at + i] : 0.0f;
   }
 }
-// 32 consecutive bf16 outputs as an operand of a later product
-__device__ __forceinline__ void st_parts32(const DenseArgs& p, int which, int64_t row, int64_t c,
-                                           int left, const float (&v)[32]) {
-  st_row32<BF16>(p.q[which], row * p.q_pitch + c, left, 16, v);
+// 16 consecutive bf16 outputs as an operand of a later product
+__device__ __forceinline__ void st_parts16(const DenseArgs& p, int which, int64_t row, int64_t c,
+                                           int left, const float (&v)[16]) {
+  st_row16<BF16>(p.q[which], row * p.q_pitch + c, left, 16, v);
 }
 // the largest of 32, 16 or 1 that divides the address and the row pitch
 __device__ __forceinline__ uint32_t row_align(const void* p, int64_t pitch_bytes) {
@@ -128,37 +128,37 @@ __device__ __forceinline__ uint32_t row_align(const void* p, int64_t pitch_bytes
   return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : 1;
 }
 
-// One row's 32 columns of a bf16 layer from column c on
+// One row's 16 columns of a bf16 layer from column c on
 // (gated: v = g, u beside it; backward: v = dh, g and w = u as kept)
 template <int EPI>
-__device__ __forceinline__ void finish32(const DenseArgs& p, int prob, int64_t row, int64_t c,
-                                         const float (&v)[32], const float (&u)[32],
-                                         const float (&g)[32], const float (&w)[32]) {
+__device__ __forceinline__ void finish16(const DenseArgs& p, int prob, int64_t row, int64_t c,
+                                         const float (&v)[16], const float (&u)[16],
+                                         const float (&g)[16], const float (&w)[16]) {
   const int64_t at = row * p.n + c;
-  const int left = (int)min((int64_t)32, p.n - c);
+  const int left = (int)min((int64_t)16, p.n - c);
   if (EPI == kDenseStore) {
-    st_row32<BF16>(p.c[prob], at, left, row_align(p.c[prob], p.n * 2), v);
+    st_row16<BF16>(p.c[prob], at, left, row_align(p.c[prob], p.n * 2), v);
   } else if (EPI == kDenseGated) {
-    float h[32];
+    float h[16];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) h[i] = act_value<true>(p.act, v[i]) * u[i];
-    st_row32<BF16>(p.c[0], at, left, row_align(p.c[0], p.n * 2), h);
-    if (p.q[0]) st_parts32(p, 0, row, c, left, h);
+    for (int i = 0; i < 16; ++i) h[i] = act_value<true>(p.act, v[i]) * u[i];
+    st_row16<BF16>(p.c[0], at, left, row_align(p.c[0], p.n * 2), h);
+    if (p.q[0]) st_parts16(p, 0, row, c, left, h);
     if (p.gp) {
-      st_row32<F32>(p.gp, at, left, row_align(p.gp, p.n * 4), v);
-      st_row32<F32>(p.up, at, left, row_align(p.up, p.n * 4), u);
+      st_row16<F32>(p.gp, at, left, row_align(p.gp, p.n * 4), v);
+      st_row16<F32>(p.up, at, left, row_align(p.up, p.n * 4), u);
     }
   } else {
-    float dg[32], du[32];
+    float dg[16], du[16];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < 16; ++i) {
       float a, da;
       act_grad<true>(p.act, g[i], a, da);
       dg[i] = v[i] * w[i] * da;
       du[i] = v[i] * a;
     }
-    st_parts32(p, 0, row, c, left, dg);
-    st_parts32(p, 1, row, c, left, du);
+    st_parts16(p, 0, row, c, left, dg);
+    st_parts16(p, 1, row, c, left, du);
   }
 }
 // The same for eight columns of a fp32 layer, whose sums leave fewer registers.
@@ -570,23 +570,23 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
       __syncwarp();
       if (more) side_load(row - lane, c);
     };
-    // g and u of this thread's row, 32 columns from c on
-    const auto kept = [&](float (&g)[32], float (&u)[32], int64_t row, int64_t c, bool more) {
+    // g and u of this thread's row, 16 columns from c on (c = c32 within 32)
+    const auto kept = [&](float (&g)[16], float (&u)[16], int64_t row, int64_t c, int c32, bool more) {
       if constexpr (EPI == kDenseGatedBwd) {
         if (side) {
-          side_wait();
+          if (c32 == 0) side_wait();
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < 4; ++k) {
             float4 a, b;
-            side_get(k, a, b);
+            side_get(c32 / 4 + k, a, b);
             g[4 * k] = a.x, g[4 * k + 1] = a.y, g[4 * k + 2] = a.z, g[4 * k + 3] = a.w;
             u[4 * k] = b.x, u[4 * k + 1] = b.y, u[4 * k + 2] = b.z, u[4 * k + 3] = b.w;
           }
-          side_next(row, c + 32, more);
+          if (c32) side_next(row, c + 16, more);
         } else if (row < p.m && c < p.n) {
-          const int left = (int)min((int64_t)32, p.n - c);
-          ld_row32(p.gp, row * p.n + c, left, row_align(p.gp, p.n * 4), g);
-          ld_row32(p.up, row * p.n + c, left, row_align(p.up, p.n * 4), u);
+          const int left = (int)min((int64_t)16, p.n - c);
+          ld_row16(p.gp, row * p.n + c, left, row_align(p.gp, p.n * 4), g);
+          ld_row16(p.up, row * p.n + c, left, row_align(p.up, p.n * 4), u);
         }
       }
     };
@@ -682,28 +682,28 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
       } else {
         const uint32_t acc = next_sum();
 #pragma unroll 1
-        for (int c = 0; c < c_count; c += 32) {
-          uint32_t r[32], q[32];
-          tc::tmem_ld32(acc + c, r);
-          if (EPI == kDenseGated) tc::tmem_ld32(acc + kOut + c, q);
+        for (int c = 0; c < c_count; c += 16) {
+          uint32_t r[16], q[16];
+          tc::tmem_ld16(acc + c, r);
+          if (EPI == kDenseGated) tc::tmem_ld16(acc + kOut + c, q);
           tc::tmem_ld_wait();
-          if (c + 32 >= c_count) sum_read();
-          float v[32], u[32];
+          if (c + 16 >= c_count) sum_read();
+          float v[16], u[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
+          for (int i = 0; i < 16; ++i) {
             v[i] = ok ? __uint_as_float(r[i]) : kBad;
             u[i] = EPI == kDenseGated ? __uint_as_float(q[i]) : 0.0f;
           }
           if (CG == 1 && p.split > 1) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
+            for (int i = 0; i < 16; i += 4) {
               put4(sums + c + i, v[i], v[i + 1], v[i + 2], v[i + 3]);
               if (EPI == kDenseGated) put4(sums + kOut + c + i, u[i], u[i + 1], u[i + 2], u[i + 3]);
             }
           } else {
-            float g[32], k[32];
-            kept(g, k, row, col + c, c + 32 < kHalf);
-            if (row < p.m && col + c < p.n) finish32<EPI>(p, w.prob, row, col + c, v, u, g, k);
+            float g[16], k[16];
+            kept(g, k, row, col + c, c % 32, c + 16 < c_count);
+            if (row < p.m && col + c < p.n) finish16<EPI>(p, w.prob, row, col + c, v, u, g, k);
           }
         }
         if (CG == 1 && p.split > 1) break;  // joined below
