@@ -504,8 +504,9 @@ qat_status qat_gated_ffn4(const void* x, qat_dtype dtype, int64_t tokens, const 
  * gate_pre, up_pre (both or neither): float[tokens, hidden], g and u kept for
  * the backward pass.  act: silu g * sigmoid(g), gelu g * Phi(g) (the erf
  * form), relu max(g, 0).  bf16 products are exact and their sums binary32;
- * fp32 operands are taken as three bf16 parts that hold all 24 bits (an
- * infinite operand may give NaN where binary32 gives an infinity, and the last
+ * those of up to 32 fp32 tokens are binary32 multiply-adds, and above that fp32
+ * operands are taken as three bf16 parts that hold all 24 bits (an infinite
+ * operand may then give NaN where binary32 gives an infinity, and the last
  * digits of operands below 2^-100 are lost).  An empty sum (dim == 0 or hidden
  * == 0) is zero.  x, w_gate, w_up, w_down and h are 16-byte aligned; sizes are
  * below 2^31 - 4096.  workspace (operand copies where rows are not whole
