@@ -7,8 +7,8 @@
 // bulk tensor copies either along k (K-major) or along its own rows
 // (MN-major), so no transpose is ever written.
 //
-// A CTA stages 128 rows of A and 128 of B, 64 deep, per step (32 KB, six or five
-// steps in flight) in 128-byte swizzled rows.  One thread issues the copies, one the
+// A CTA stages up to 128 rows of A and of B, 64 deep, per step (32 KB, six or
+// five steps in flight) in 128-byte swizzled rows.  One thread issues the copies, one the
 // MMAs; the sums stay in tensor memory, in two buffers, so that eight warps
 // finish one tile while the next is multiplied.  CG = 2: two CTAs share a
 // 256 x 256 tile, each holding half of A and half of B, which halves the
@@ -17,14 +17,19 @@
 // and where those are few a cluster of up to eight CTAs splits k and adds its
 // sums through distributed shared memory in rank order.
 //
+// With few rows the weights are all that is read, and bytes in flight count: A
+// then holds 32 or 64 rows and more stages fit.  The MMA still reads 128 rows,
+// the others from whatever follows in the stage; they end in sums of rows that do
+// not exist.
+//
 // Measured at 4096 x 4096 x 14336 (tokens, dim, hidden; repeated calls, power
-// capped): the gated product 585 us (1644 TFLOP/s), the one back 335 (1435, its
-// tiles fill 3.4 waves of 76 pairs), dh 362 (1328, the epilogue reads and writes
-// 12 bytes an element), dx 650 (1480), the three weight gradients 938 (1539);
+// capped): the gated product 590 us (1631 TFLOP/s), the one back 340 (1415, its
+// tiles fill 3.4 waves of 76 pairs), dh 344 (1398, the epilogue reads and writes
+// 12 bytes an element), dx 655 (1469), the three weight gradients 937 (1540);
 // cuBLAS runs plain products at 1708 under the same cap.  fp32 at 2048 x 4096 x
-// 14336: 239 TFLOP/s forward, six bf16 products each.  With one token the weights
-// are read at 3.8 to 4.3 TB/s: half of each stage holds rows of x that do not
-// exist, so too few bytes are in flight.
+// 14336: 263 TFLOP/s forward, 233 backward, six bf16 products each.  With one
+// token the weights are read at 4.3 TB/s forward and for dx (128 rows of A in
+// every stage: 3.8).
 
 #include "qat_dense.h"
 #include "qat_layer.cuh"
@@ -43,9 +48,12 @@ constexpr int kFinishWarps = 8;  // two for each quarter of the tile's rows
 // The backward epilogue reads g and u: each finishing warp has 32 x 32 floats of
 // both in shared memory, in the place of one stage.
 constexpr uint32_t kSideBytes = 2 * 32 * 32 * 4;
-__host__ __device__ constexpr int stages_of(int epi) { return epi == kDenseGatedBwd ? 5 : 6; }
+__host__ __device__ constexpr uint32_t stage_room(int epi) {
+  return (epi == kDenseGatedBwd ? 5 : 6) * kStageBytes;
+}
+constexpr int kMaxStages = 12;
 __host__ __device__ constexpr uint32_t dense_smem(int epi) {
-  return stages_of(epi) * kStageBytes + kBarBytes + 1024 +
+  return stage_room(epi) + kBarBytes + 1024 +
          (epi == kDenseGatedBwd ? kFinishWarps * kSideBytes : 0);
 }
 constexpr int kDenseThreads = 64 + 32 * kFinishWarps;
@@ -56,7 +64,9 @@ struct DenseArgs {
   int mt, nt, problems;    // tiles of the output; outputs that share B
   int kt, segs;            // k steps of a segment; segments
   int split;               // CTAs of a cluster that share k (CG = 1)
-  int bn;                  // columns of a pair's tile (store)
+  int bn;                  // columns of a tile's sums (gated: of both)
+  int stages;
+  uint32_t a_bytes, stage_bytes;  // of a stage; A may hold fewer rows than the MMA reads
   int act;
   void* c[2];              // outputs (gated: c[0] = h), rows of n
   float* gp;
@@ -314,7 +324,8 @@ struct Tile {
 template <int CG, int EPI>
 __device__ __forceinline__ Tile tile_at(const DenseArgs& p, int64_t t) {
   constexpr int BM = kRows * CG;
-  const int BN = EPI == kDenseGated ? kRows * CG / 2 : CG == 2 && EPI == kDenseStore ? p.bn : kRows * CG;
+  const int cols = CG == 2 && EPI != kDenseStore ? kRows * CG : p.bn;
+  const int BN = EPI == kDenseGated ? cols / 2 : cols;
   const int64_t per = (int64_t)p.mt * p.nt;
   Tile r;
   r.prob = (int)(t / per);
@@ -349,16 +360,18 @@ struct Units {
 
 template <typename T, int CG, int EPI, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constant__ DenseArgs p) {
-  constexpr int kStages = stages_of(EPI);
   extern __shared__ uint8_t raw[];
   const uint32_t base = (tc::smem(raw) + 1023) & ~1023u;
-  const uint32_t bars = base + kStages * kStageBytes;
+  const uint32_t bars = base + stage_room(EPI);
+  const int stages = CG == 2 ? stage_room(EPI) / kStageBytes : p.stages;
+  const uint32_t a_bytes = CG == 2 ? kOpBytes : p.a_bytes;
+  const uint32_t stage_bytes = CG == 2 ? kStageBytes : p.stage_bytes;
   // full[stages], empty[stages], acc_full[2], acc_empty[2], drain
   const auto full = [&](int s) { return bars + 8 * s; };
-  const auto empty = [&](int s) { return bars + 8 * (kStages + s); };
-  const auto acc_full = [&](int b) { return bars + 8 * (2 * kStages + b); };
-  const auto acc_empty = [&](int b) { return bars + 8 * (2 * kStages + 2 + b); };
-  const uint32_t drain = bars + 8 * (2 * kStages + 4);
+  const auto empty = [&](int s) { return bars + 8 * (kMaxStages + s); };
+  const auto acc_full = [&](int b) { return bars + 8 * (2 * kMaxStages + b); };
+  const auto acc_empty = [&](int b) { return bars + 8 * (2 * kMaxStages + 2 + b); };
+  const uint32_t drain = bars + 8 * (2 * kMaxStages + 4);
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
 
@@ -369,7 +382,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
   constexpr int kTmemCols = 2 * kAccCols;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       tc::bar_init(full(s), 1);
       tc::bar_init(empty(s), 1);
     }
@@ -395,8 +408,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
   pdl_wait();     // and this one's set-up overlapped the previous kernel's end
 
   // columns of the tile's sums, and the bytes of a stage of B
-  const int tile_cols = CG == 2 && EPI == kDenseStore ? p.bn : kAccCols;
-  const uint32_t b_bytes = CG == 2 && !B_MN ? (uint32_t)tile_cols / 2 * kBK * 2 : kOpBytes;
+  const int tile_cols = CG == 2 && EPI != kDenseStore ? kAccCols : p.bn;
+  const uint32_t b_bytes = !B_MN ? (uint32_t)tile_cols / CG * kBK * 2 : kOpBytes;
   using U = Units<T>;
   const int per_seg = U::per_segment(p.kt), units = p.segs * per_seg;
   // this CTA's share of them
@@ -426,9 +439,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
             const int pr = U::kParts ? st / nk : 0;
             const int k0 = (U::kParts ? in_seg * kChunk + st - pr * nk : in_seg) * kBK;
             const int pa = U::kParts ? kPairA[pr] : 0, pb = U::kParts ? kPairB[pr] : 0;
-            const uint32_t sa = base + stage * kStageBytes, sb = sa + kOpBytes;
+            const uint32_t sa = base + stage * stage_bytes, sb = sa + a_bytes;
             uint32_t bar = full(stage);
-            if (leader) tc::bar_expect(bar, (kOpBytes + b_bytes) * CG);
+            if (leader) tc::bar_expect(bar, (a_bytes + b_bytes) * CG);
             if (CG == 2) bar = tc::map_rank(bar, 0);
             const CUtensorMap* ma = &p.a[p.problems > 1 ? w.prob : seg];
             if (A_MN) {
@@ -443,7 +456,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
                 tc::load_box<true>(&p.b[rank], sb, bar, k0, bn, pb);
               } else {
                 tc::load_box<false>(&p.b[0], sb, bar, k0, bn, pb);
-                tc::load_box<false>(&p.b[1], sb + kOpBytes / 2, bar, k0, bn, pb);
+                tc::load_box<false>(&p.b[1], sb + b_bytes / 2, bar, k0, bn, pb);
               }
             } else if (B_MN) {
               tc::load_box<CG == 2>(&p.b[seg], sb, bar, bn, k0, pb);
@@ -452,7 +465,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
               tc::load_box<CG == 2>(&p.b[seg], sb, bar, k0, bn, pb);
             }
             ++issued;
-            if (++stage == kStages) {
+            if (++stage == stages) {
               stage = 0;
               phase ^= 1;
             }
@@ -462,8 +475,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
       if (!ok) {  // copies in flight land before the block ends
         volatile int none = 0;
         if (leader)
-          for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-            tc::bar_wait(full((int)(i % kStages)), (uint32_t)(i / kStages) & 1, &none, 1u << 16);
+          for (int64_t i = issued > stages ? issued - stages : 0; i < issued; ++i)
+            tc::bar_wait(full((int)(i % stages)), (uint32_t)(i / stages) & 1, &none, 1u << 16);
         else  // they are counted in the other CTA: a millisecond is ample
           for (int i = 0; i < 1024; ++i) __nanosleep(1000);
       }
@@ -488,7 +501,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
             ok = tc::bar_wait(full(stage), phase, &abort_flag, p.limit);
             if (!ok) break;
             tc::fence_after();
-            const uint32_t sa = base + stage * kStageBytes, sb = sa + kOpBytes;
+            const uint32_t sa = base + stage * stage_bytes, sb = sa + a_bytes;
             const uint64_t da = tc::desc_sw128(sa, A_MN ? kOpBytes / 2 : 16);
             const uint64_t db = tc::desc_sw128(sb, B_MN ? kOpBytes / 2 : 16);
 #pragma unroll
@@ -496,7 +509,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
               tc::mma_bf16<CG>(acc, da + (A_MN ? 2048 : 32) / 16 * k,
                                db + (B_MN ? 2048 : 32) / 16 * k, idesc, !begin || st > 0 || k > 0);
             tc::mma_commit<CG>(empty(stage));
-            if (++stage == kStages) {
+            if (++stage == stages) {
               stage = 0;
               phase ^= 1;
             }
@@ -518,7 +531,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
     constexpr int kOut = EPI == kDenseGated ? kAccCols / 2 : kAccCols;
     constexpr int kHalf = kOut / 2;
     const int c_first = (warp - 2) / 4 * kHalf;  // this warp's columns
-    const int c_count = EPI == kDenseGated ? kHalf : min(kHalf, tile_cols - c_first);
+    const int u_at = tile_cols / 2;  // gated: u's columns begin
+    const int c_count = min(kHalf, (EPI == kDenseGated ? u_at : tile_cols) - c_first);
     constexpr float kBad = __builtin_nanf("");
     int64_t run = 0;
     // waits for the next sum; the address of this warp's lanes of it
@@ -617,7 +631,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
 #pragma unroll
             for (int i = 0; i < 32; ++i) sv[c + i] += ok ? __uint_as_float(r[i]) : kBad;
             if constexpr (EPI == kDenseGated) {
-              tc::tmem_ld32(acc + kOut + c, r);
+              tc::tmem_ld32(acc + u_at + c, r);
               tc::tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 32; ++i) su[c + i] += __uint_as_float(r[i]);
@@ -640,14 +654,14 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
 #pragma unroll
         for (int c = 0; c < kHalf; c += 32) {
           tc::tmem_st32(acc + c, sv + c);
-          if constexpr (EPI == kDenseGated) tc::tmem_st32(acc + kOut + c, su + c);
+          if constexpr (EPI == kDenseGated) tc::tmem_st32(acc + u_at + c, su + c);
         }
         tc::tmem_st_wait();
 #pragma unroll 1
         for (int c = 0; c < c_count; c += 8) {
           uint32_t r[8], q[8];
           tc::tmem_ld8(acc + c, r);
-          if (EPI == kDenseGated) tc::tmem_ld8(acc + kOut + c, q);
+          if (EPI == kDenseGated) tc::tmem_ld8(acc + u_at + c, q);
           tc::tmem_ld_wait();
           if (c + 8 >= c_count) sum_read();
           float v[8], u[8], g[8], k[8];
@@ -685,7 +699,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
         for (int c = 0; c < c_count; c += 16) {
           uint32_t r[16], q[16];
           tc::tmem_ld16(acc + c, r);
-          if (EPI == kDenseGated) tc::tmem_ld16(acc + kOut + c, q);
+          if (EPI == kDenseGated) tc::tmem_ld16(acc + u_at + c, q);
           tc::tmem_ld_wait();
           if (c + 16 >= c_count) sum_read();
           float v[16], u[16];
@@ -868,8 +882,9 @@ qat_status launch_dense(const Dense& d, cudaStream_t s) {
   // first: waves of tiles times k steps, and the end of a tile.  Measured cycles
   // of a step: 620 of a pair's (256 x 256 x 64), 680 of a single CTA's (128 x 128
   // x 64); a pair's tile ends in about 6000, a split one is joined in as many, a
-  // single one ends in 2500.  With 128 rows or fewer half a pair would idle.  At 1001 x 4096, k = 14336, pairs take 84 us and
-  // single CTAs 158; at 128 x 4096 it is 150 and 31 (split).
+  // single one ends in 2500.  With 128 rows or fewer half a pair would idle.  At
+  // 1001 x 4096, k = 14336, pairs take 84 us and single CTAs 158; at 128 x 4096 it
+  // is 150 and 31 (split).
   const auto tiles_of = [&](int side) {
     return up(d.m, side) * up(d.n, gated ? side / 2 : side) * d.problems;
   };
@@ -878,18 +893,32 @@ qat_status launch_dense(const Dense& d, cudaStream_t s) {
   // A pair's tile has 256 columns, or 224 where that fills its last wave (560
   // cycles a step): 4096 x 4096 is 256 tiles of 256 on 76 pairs, four waves, and
   // 304 of 224, four waves too.
-  p.bn = 256;
+  int pair_cols = 256;
   int64_t pair_cost = up(tiles_of(256), sms / 2) * steps * 620 + 6000;
   if (d.epi == kDenseStore) {
     const int64_t narrow = up(d.m, 256) * up(d.n, 224) * d.problems;
     const int64_t cost = up(narrow, sms / 2) * steps * 560 + 6000;
     if (cost < pair_cost) {
-      p.bn = 224;
+      pair_cols = 224;
       pair_cost = cost;
     }
   }
   int64_t best = up(tiles_of(128), sms) * steps * 680 + 2500;
+  // A single CTA's tile may have 96 columns (510 cycles a step) for the same
+  // reason: of a hidden layer of 14336, 48 columns of g and u each make 299 tiles
+  // for two waves of 152 where 64 make 224 (1 token x 4096 x 14336 forward 81 us
+  // against 93, the smaller stages of A included).  K-major B only, whose rows may
+  // be any multiple of eight, and one pass over the tile's sums.
+  int cols = 128;
   p.split = 1;
+  if (!f32 && !d.b[0].mn_major) {
+    const int64_t narrow = up(d.m, 128) * up(d.n, gated ? 48 : 96) * d.problems;
+    const int64_t cost = up(narrow, sms) * steps * 510 + 2500;
+    if (cost < best) {
+      best = cost;
+      cols = 96;
+    }
+  }
   const int least = f32 ? 1 : 4;
   for (int c = 2; c <= 8; ++c) {
     if (units < c * least || tiles_of(128) > resident_clusters(c)) break;
@@ -897,17 +926,24 @@ qat_status launch_dense(const Dense& d, cudaStream_t s) {
     if (cost < best) {
       best = cost;
       p.split = c;
+      cols = 128;
     }
   }
   const bool pair = d.m > 128 && pair_cost <= best;
   if (pair) p.split = 1;
-  const int bm = pair ? 256 : 128, bn = gated ? bm / 2 : pair ? p.bn : bm;
+  p.bn = pair ? pair_cols : cols;
+  const int bm = pair ? 256 : 128, bn = gated ? p.bn / 2 : p.bn;
   p.mt = (int)up(d.m, bm);
   p.nt = (int)up(d.n, bn);
+  const int a_rows = d.a[0].mn_major || d.m > 64 ? 128 : d.m > 32 ? 64 : 32;
+  p.a_bytes = (uint32_t)a_rows * kBK * 2;
+  p.stage_bytes = p.a_bytes + (pair ? kOpBytes : (uint32_t)p.bn * kBK * 2);
+  p.stages = (int)(stage_room(d.epi) / p.stage_bytes);
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
   const int nb = gated ? 2 : d.segs, na = d.problems > 1 ? d.problems : d.segs;
   for (int i = 0; i < 2; ++i) {
-    if (!encode(&p.a[i], d.a[i < na ? i : 0], d.m, d.k, parts, 128)) return QAT_ERR_CUDA;
-    if (!encode(&p.b[i], d.b[i < nb ? i : 0], d.n, d.k, parts, gated ? bn : pair ? bn / 2 : 128))
+    if (!encode(&p.a[i], d.a[i < na ? i : 0], d.m, d.k, parts, a_rows)) return QAT_ERR_CUDA;
+    if (!encode(&p.b[i], d.b[i < nb ? i : 0], d.n, d.k, parts, pair && !gated ? bn / 2 : bn))
       return QAT_ERR_CUDA;
   }
   p.act = d.act;
