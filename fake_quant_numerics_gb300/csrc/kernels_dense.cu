@@ -29,7 +29,8 @@
 // cuBLAS runs plain products at 1708 under the same cap.  fp32 at 2048 x 4096 x
 // 14336: 263 TFLOP/s forward, 233 backward, six bf16 products each.  With one
 // token the weights are read at 4.3 TB/s forward and for dx (128 rows of A in
-// every stage: 3.8).
+// every stage: 3.8; tiles of 96 columns, for fuller waves, moved nothing there and
+// cost 16% at 16 x 1024 x 4096).
 
 #include "qat_dense.h"
 #include "qat_layer.cuh"
@@ -51,7 +52,7 @@ constexpr uint32_t kSideBytes = 2 * 32 * 32 * 4;
 __host__ __device__ constexpr uint32_t stage_room(int epi) {
   return (epi == kDenseGatedBwd ? 5 : 6) * kStageBytes;
 }
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 9;
 __host__ __device__ constexpr uint32_t dense_smem(int epi) {
   return stage_room(epi) + kBarBytes + 1024 +
          (epi == kDenseGatedBwd ? kFinishWarps * kSideBytes : 0);
@@ -64,7 +65,7 @@ struct DenseArgs {
   int mt, nt, problems;    // tiles of the output; outputs that share B
   int kt, segs;            // k steps of a segment; segments
   int split;               // CTAs of a cluster that share k (CG = 1)
-  int bn;                  // columns of a tile's sums (gated: of both)
+  int bn;                  // columns of a pair's tile (store)
   int stages;
   uint32_t a_bytes, stage_bytes;  // of a stage; A may hold fewer rows than the MMA reads
   int act;
@@ -324,8 +325,7 @@ struct Tile {
 template <int CG, int EPI>
 __device__ __forceinline__ Tile tile_at(const DenseArgs& p, int64_t t) {
   constexpr int BM = kRows * CG;
-  const int cols = CG == 2 && EPI != kDenseStore ? kRows * CG : p.bn;
-  const int BN = EPI == kDenseGated ? cols / 2 : cols;
+  const int BN = EPI == kDenseGated ? kRows * CG / 2 : CG == 2 && EPI == kDenseStore ? p.bn : kRows * CG;
   const int64_t per = (int64_t)p.mt * p.nt;
   Tile r;
   r.prob = (int)(t / per);
@@ -408,8 +408,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
   pdl_wait();     // and this one's set-up overlapped the previous kernel's end
 
   // columns of the tile's sums, and the bytes of a stage of B
-  const int tile_cols = CG == 2 && EPI != kDenseStore ? kAccCols : p.bn;
-  const uint32_t b_bytes = !B_MN ? (uint32_t)tile_cols / CG * kBK * 2 : kOpBytes;
+  const int tile_cols = CG == 2 && EPI == kDenseStore ? p.bn : kAccCols;
+  const uint32_t b_bytes = CG == 2 && !B_MN ? (uint32_t)tile_cols / 2 * kBK * 2 : kOpBytes;
   using U = Units<T>;
   const int per_seg = U::per_segment(p.kt), units = p.segs * per_seg;
   // this CTA's share of them
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
                 tc::load_box<true>(&p.b[rank], sb, bar, k0, bn, pb);
               } else {
                 tc::load_box<false>(&p.b[0], sb, bar, k0, bn, pb);
-                tc::load_box<false>(&p.b[1], sb + b_bytes / 2, bar, k0, bn, pb);
+                tc::load_box<false>(&p.b[1], sb + kOpBytes / 2, bar, k0, bn, pb);
               }
             } else if (B_MN) {
               tc::load_box<CG == 2>(&p.b[seg], sb, bar, bn, k0, pb);
@@ -531,8 +531,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
     constexpr int kOut = EPI == kDenseGated ? kAccCols / 2 : kAccCols;
     constexpr int kHalf = kOut / 2;
     const int c_first = (warp - 2) / 4 * kHalf;  // this warp's columns
-    const int u_at = tile_cols / 2;  // gated: u's columns begin
-    const int c_count = min(kHalf, (EPI == kDenseGated ? u_at : tile_cols) - c_first);
+    const int c_count = EPI == kDenseGated ? kHalf : min(kHalf, tile_cols - c_first);
     constexpr float kBad = __builtin_nanf("");
     int64_t run = 0;
     // waits for the next sum; the address of this warp's lanes of it
@@ -631,7 +630,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
 #pragma unroll
             for (int i = 0; i < 32; ++i) sv[c + i] += ok ? __uint_as_float(r[i]) : kBad;
             if constexpr (EPI == kDenseGated) {
-              tc::tmem_ld32(acc + u_at + c, r);
+              tc::tmem_ld32(acc + kOut + c, r);
               tc::tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 32; ++i) su[c + i] += __uint_as_float(r[i]);
@@ -654,14 +653,14 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
 #pragma unroll
         for (int c = 0; c < kHalf; c += 32) {
           tc::tmem_st32(acc + c, sv + c);
-          if constexpr (EPI == kDenseGated) tc::tmem_st32(acc + u_at + c, su + c);
+          if constexpr (EPI == kDenseGated) tc::tmem_st32(acc + kOut + c, su + c);
         }
         tc::tmem_st_wait();
 #pragma unroll 1
         for (int c = 0; c < c_count; c += 8) {
           uint32_t r[8], q[8];
           tc::tmem_ld8(acc + c, r);
-          if (EPI == kDenseGated) tc::tmem_ld8(acc + u_at + c, q);
+          if (EPI == kDenseGated) tc::tmem_ld8(acc + kOut + c, q);
           tc::tmem_ld_wait();
           if (c + 8 >= c_count) sum_read();
           float v[8], u[8], g[8], k[8];
@@ -699,7 +698,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
         for (int c = 0; c < c_count; c += 16) {
           uint32_t r[16], q[16];
           tc::tmem_ld16(acc + c, r);
-          if (EPI == kDenseGated) tc::tmem_ld16(acc + u_at + c, q);
+          if (EPI == kDenseGated) tc::tmem_ld16(acc + kOut + c, q);
           tc::tmem_ld_wait();
           if (c + 16 >= c_count) sum_read();
           float v[16], u[16];
@@ -893,32 +892,18 @@ qat_status launch_dense(const Dense& d, cudaStream_t s) {
   // A pair's tile has 256 columns, or 224 where that fills its last wave (560
   // cycles a step): 4096 x 4096 is 256 tiles of 256 on 76 pairs, four waves, and
   // 304 of 224, four waves too.
-  int pair_cols = 256;
+  p.bn = 256;
   int64_t pair_cost = up(tiles_of(256), sms / 2) * steps * 620 + 6000;
   if (d.epi == kDenseStore) {
     const int64_t narrow = up(d.m, 256) * up(d.n, 224) * d.problems;
     const int64_t cost = up(narrow, sms / 2) * steps * 560 + 6000;
     if (cost < pair_cost) {
-      pair_cols = 224;
+      p.bn = 224;
       pair_cost = cost;
     }
   }
   int64_t best = up(tiles_of(128), sms) * steps * 680 + 2500;
-  // A single CTA's tile may have 96 columns (510 cycles a step) for the same
-  // reason: of a hidden layer of 14336, 48 columns of g and u each make 299 tiles
-  // for two waves of 152 where 64 make 224 (1 token x 4096 x 14336 forward 81 us
-  // against 93, the smaller stages of A included).  K-major B only, whose rows may
-  // be any multiple of eight, and one pass over the tile's sums.
-  int cols = 128;
   p.split = 1;
-  if (!f32 && !d.b[0].mn_major) {
-    const int64_t narrow = up(d.m, 128) * up(d.n, gated ? 48 : 96) * d.problems;
-    const int64_t cost = up(narrow, sms) * steps * 510 + 2500;
-    if (cost < best) {
-      best = cost;
-      cols = 96;
-    }
-  }
   const int least = f32 ? 1 : 4;
   for (int c = 2; c <= 8; ++c) {
     if (units < c * least || tiles_of(128) > resident_clusters(c)) break;
@@ -926,24 +911,23 @@ qat_status launch_dense(const Dense& d, cudaStream_t s) {
     if (cost < best) {
       best = cost;
       p.split = c;
-      cols = 128;
     }
   }
   const bool pair = d.m > 128 && pair_cost <= best;
   if (pair) p.split = 1;
-  p.bn = pair ? pair_cols : cols;
-  const int bm = pair ? 256 : 128, bn = gated ? p.bn / 2 : p.bn;
+  const int bm = pair ? 256 : 128, bn = gated ? bm / 2 : pair ? p.bn : bm;
   p.mt = (int)up(d.m, bm);
   p.nt = (int)up(d.n, bn);
+  // 32 rows of A leave room for nine stages (1 token x 4096 x 14336 forward 82 us,
+  // with six of 128 rows 93), 64 for eight
   const int a_rows = d.a[0].mn_major || d.m > 64 ? 128 : d.m > 32 ? 64 : 32;
   p.a_bytes = (uint32_t)a_rows * kBK * 2;
-  p.stage_bytes = p.a_bytes + (pair ? kOpBytes : (uint32_t)p.bn * kBK * 2);
+  p.stage_bytes = p.a_bytes + kOpBytes;
   p.stages = (int)(stage_room(d.epi) / p.stage_bytes);
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
   const int nb = gated ? 2 : d.segs, na = d.problems > 1 ? d.problems : d.segs;
   for (int i = 0; i < 2; ++i) {
     if (!encode(&p.a[i], d.a[i < na ? i : 0], d.m, d.k, parts, a_rows)) return QAT_ERR_CUDA;
-    if (!encode(&p.b[i], d.b[i < nb ? i : 0], d.n, d.k, parts, pair && !gated ? bn / 2 : bn))
+    if (!encode(&p.b[i], d.b[i < nb ? i : 0], d.n, d.k, parts, gated ? bn : pair ? bn / 2 : 128))
       return QAT_ERR_CUDA;
   }
   p.act = d.act;

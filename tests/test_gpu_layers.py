@@ -179,6 +179,32 @@ def test_ffn_sizes(dtype, tokens, dim, hidden):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,dim,hidden", [
+    (32, 640, 1032), (33, 648, 1032), (48, 1030, 320), (64, 1024, 520), (65, 640, 1032)])
+def test_ffn_few_rows(dtype, tokens, dim, hidden):
+    """Either side of the row counts at which a stage of the products changes size,
+    over more steps than the stages hold."""
+    ffn_case(tokens, dim, hidden, dtype, "gelu")
+
+
+def test_ffn_few_rows_do_not_depend_on_what_else_is_staged():
+    """The rows that a stage leaves out are read as whatever lies there: infinite
+    weights of one output stay in that output."""
+    x = rnd(1, 5, 1024, dtype=torch.bfloat16)
+    w = [rnd(s, 300, 1024, dtype=torch.bfloat16, scale=0.05) for s in (2, 3)]
+    wd = rnd(4, 1024, 300, dtype=torch.bfloat16, scale=0.05)
+    clean = fq.gated_ffn(x, *w, wd)
+    w[0][77] = float("inf")
+    wd[500] = float("nan")
+    r = fq.gated_ffn(x, *w, wd, save=True)
+    keep = [i for i in range(300) if i != 77]
+    assert torch.equal(r.h[:, keep], clean.h[:, keep])
+    assert not torch.isfinite(r.gate_pre[:, 77]).any()
+    assert torch.isfinite(r.gate_pre[:, keep]).all()
+    assert torch.isnan(r.y[:, 500]).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_ffn_views_off_the_vector_grid(dtype):
     ffn_case(70, 136, 264, dtype, "silu", place=off_grid)
 
@@ -428,6 +454,11 @@ def test_ffn_wait_that_runs_out_is_reported(dtype, tokens, dim, hidden):
     flags.zero_()
     fq.qat_gated_ffn(x, tokens, dim, hidden, *w, wd, "silu", h, None, None, y, flags, ws)
     assert int(flags.item()) == 0 and torch.equal(y, want.y) and torch.equal(h, want.h)
+
+
+@pytest.mark.parametrize("tokens,dim,hidden", [(5, 1024, 256), (40, 1024, 256)])
+def test_ffn_wait_that_runs_out_with_few_rows(tokens, dim, hidden):
+    test_ffn_wait_that_runs_out_is_reported(torch.bfloat16, tokens, dim, hidden)
 
 
 def test_example_trains_and_serves():
