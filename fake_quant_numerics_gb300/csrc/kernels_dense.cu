@@ -78,12 +78,12 @@ struct DenseArgs {
   uint32_t limit;
 };
 
-// 16 consecutive outputs of one row: full vectors where the row allows
-template <typename T>
-__device__ __forceinline__ void st_row16(void* p, int64_t at, int left, uint32_t align,
-                                         const float (&v)[16]) {
-  if (left >= 16 && align >= 16) {
-    constexpr int W = T::BYTES == 4 ? 16 : 8;  // words
+// N (8 or 16) consecutive outputs of one row: full vectors where the row allows
+template <typename T, int N>
+__device__ __forceinline__ void st_row(void* p, int64_t at, int left, uint32_t align,
+                                       const float (&v)[N]) {
+  if (left >= N && align >= 16) {
+    constexpr int W = N * T::BYTES / 4;  // words
     uint32_t w[W];
     if (T::BYTES == 4) {
 #pragma unroll
@@ -108,7 +108,7 @@ __device__ __forceinline__ void st_row16(void* p, int64_t at, int left, uint32_t
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < N; ++i)
       if (i < left) st_elem<T>(p, at + i, v[i]);
   }
 }
@@ -131,7 +131,7 @@ __device__ __forceinline__ void ld_row16(const float* p, int64_t at, int left, u
 // 16 consecutive bf16 outputs as an operand of a later product
 __device__ __forceinline__ void st_parts16(const DenseArgs& p, int which, int64_t row, int64_t c,
                                            int left, const float (&v)[16]) {
-  st_row16<BF16>(p.q[which], row * p.q_pitch + c, left, 16, v);
+  st_row<BF16>(p.q[which], row * p.q_pitch + c, left, 16, v);
 }
 // the largest of 32, 16 or 1 that divides the address and the row pitch
 __device__ __forceinline__ uint32_t row_align(const void* p, int64_t pitch_bytes) {
@@ -148,16 +148,16 @@ __device__ __forceinline__ void finish16(const DenseArgs& p, int prob, int64_t r
   const int64_t at = row * p.n + c;
   const int left = (int)min((int64_t)16, p.n - c);
   if (EPI == kDenseStore) {
-    st_row16<BF16>(p.c[prob], at, left, row_align(p.c[prob], p.n * 2), v);
+    st_row<BF16>(p.c[prob], at, left, row_align(p.c[prob], p.n * 2), v);
   } else if (EPI == kDenseGated) {
     float h[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) h[i] = act_value<true>(p.act, v[i]) * u[i];
-    st_row16<BF16>(p.c[0], at, left, row_align(p.c[0], p.n * 2), h);
+    st_row<BF16>(p.c[0], at, left, row_align(p.c[0], p.n * 2), h);
     if (p.q[0]) st_parts16(p, 0, row, c, left, h);
     if (p.gp) {
-      st_row16<F32>(p.gp, at, left, row_align(p.gp, p.n * 4), v);
-      st_row16<F32>(p.up, at, left, row_align(p.up, p.n * 4), u);
+      st_row<F32>(p.gp, at, left, row_align(p.gp, p.n * 4), v);
+      st_row<F32>(p.up, at, left, row_align(p.up, p.n * 4), u);
     }
   } else {
     float dg[16], du[16];
@@ -170,18 +170,6 @@ __device__ __forceinline__ void finish16(const DenseArgs& p, int prob, int64_t r
     }
     st_parts16(p, 0, row, c, left, dg);
     st_parts16(p, 1, row, c, left, du);
-  }
-}
-// The same for eight columns of a fp32 layer, whose sums leave fewer registers.
-__device__ __forceinline__ void st_row8(float* p, int64_t at, int left, bool vec, const float (&v)[8]) {
-  if (vec && left >= 8) {
-    float4* q = reinterpret_cast<float4*>(p + at);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left) p[at + i] = v[i];
   }
 }
 __device__ __forceinline__ void st_parts8(const DenseArgs& p, int which, int64_t row, int64_t c,
@@ -202,25 +190,25 @@ __device__ __forceinline__ void st_parts8(const DenseArgs& p, int which, int64_t
                                                 pack_bf16x2(h[4], h[5]), pack_bf16x2(h[6], h[7]));
   }
 }
+// The same for eight columns of a gated fp32 layer, whose sums leave fewer registers.
 template <int EPI>
-__device__ __forceinline__ void finish8(const DenseArgs& p, int prob, int64_t row, int64_t c,
+__device__ __forceinline__ void finish8(const DenseArgs& p, int64_t row, int64_t c,
                                         const float (&v)[8], const float (&u)[8],
                                         const float (&g)[8], const float (&w)[8]) {
   const int64_t at = row * p.n + c;
   const int left = (int)min((int64_t)8, p.n - c);
-  const bool whole = p.n % 4 == 0;
-  const auto vec = [&](const void* q) { return whole && reinterpret_cast<uint64_t>(q) % 16 == 0; };
-  if (EPI == kDenseStore) {
-    st_row8(static_cast<float*>(p.c[prob]), at, left, vec(p.c[prob]), v);
-  } else if (EPI == kDenseGated) {
+  const auto put = [&](void* q, const float (&o)[8]) {
+    st_row<F32>(q, at, left, row_align(q, p.n * 4), o);
+  };
+  if (EPI == kDenseGated) {
     float h[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = act_value<false>(p.act, v[i]) * u[i];
-    st_row8(static_cast<float*>(p.c[0]), at, left, vec(p.c[0]), h);
+    put(p.c[0], h);
     st_parts8(p, 0, row, c, left, h);
     if (p.gp) {
-      st_row8(p.gp, at, left, vec(p.gp), v);
-      st_row8(p.up, at, left, vec(p.up), u);
+      put(p.gp, v);
+      put(p.up, u);
     }
   } else {
     float dg[8], du[8];
@@ -656,41 +644,58 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
           if constexpr (EPI == kDenseGated) tc::tmem_st32(acc + kOut + c, su + c);
         }
         tc::tmem_st_wait();
+        if constexpr (EPI == kDenseStore) {
 #pragma unroll 1
-        for (int c = 0; c < c_count; c += 8) {
-          uint32_t r[8], q[8];
-          tc::tmem_ld8(acc + c, r);
-          if (EPI == kDenseGated) tc::tmem_ld8(acc + kOut + c, q);
-          tc::tmem_ld_wait();
-          if (c + 8 >= c_count) sum_read();
-          float v[8], u[8], g[8], k[8];
+          for (int c = 0; c < c_count; c += 16) {
+            uint32_t r[16];
+            tc::tmem_ld16(acc + c, r);
+            tc::tmem_ld_wait();
+            if (c + 16 >= c_count) sum_read();
+            float v[16];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            v[i] = __uint_as_float(r[i]);
-            u[i] = EPI == kDenseGated ? __uint_as_float(q[i]) : 0.0f;
+            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+            const int64_t at = col + c;
+            if (row < p.m && at < p.n)
+              st_row<F32>(p.c[w.prob], row * p.n + at, (int)min((int64_t)16, p.n - at),
+                          row_align(p.c[w.prob], p.n * 4), v);
           }
-          const int64_t at = col + c;
-          if constexpr (EPI == kDenseGatedBwd) {
-            if (side) {
-              if (c % 32 == 0) side_wait();
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < c_count; c += 8) {
+            uint32_t r[8], q[8];
+            tc::tmem_ld8(acc + c, r);
+            if (EPI == kDenseGated) tc::tmem_ld8(acc + kOut + c, q);
+            tc::tmem_ld_wait();
+            if (c + 8 >= c_count) sum_read();
+            float v[8], u[8], g[8], k[8];
 #pragma unroll
-              for (int i = 0; i < 8; i += 4) {
-                float4 a, b;
-                side_get((c % 32 + i) / 4, a, b);
-                g[i] = a.x, g[i + 1] = a.y, g[i + 2] = a.z, g[i + 3] = a.w;
-                k[i] = b.x, k[i + 1] = b.y, k[i + 2] = b.z, k[i + 3] = b.w;
-              }
-              if (c % 32 == 24) side_next(row, at + 8, c + 8 < c_count);
-            } else {
+            for (int i = 0; i < 8; ++i) {
+              v[i] = __uint_as_float(r[i]);
+              u[i] = EPI == kDenseGated ? __uint_as_float(q[i]) : 0.0f;
+            }
+            const int64_t at = col + c;
+            if constexpr (EPI == kDenseGatedBwd) {
+              if (side) {
+                if (c % 32 == 0) side_wait();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const bool in = row < p.m && at + i < p.n;
-                g[i] = in ? p.gp[row * p.n + at + i] : 0.0f;
-                k[i] = in ? p.up[row * p.n + at + i] : 0.0f;
+                for (int i = 0; i < 8; i += 4) {
+                  float4 a, b;
+                  side_get((c % 32 + i) / 4, a, b);
+                  g[i] = a.x, g[i + 1] = a.y, g[i + 2] = a.z, g[i + 3] = a.w;
+                  k[i] = b.x, k[i + 1] = b.y, k[i + 2] = b.z, k[i + 3] = b.w;
+                }
+                if (c % 32 == 24) side_next(row, at + 8, c + 8 < c_count);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const bool in = row < p.m && at + i < p.n;
+                  g[i] = in ? p.gp[row * p.n + at + i] : 0.0f;
+                  k[i] = in ? p.up[row * p.n + at + i] : 0.0f;
+                }
               }
             }
+            if (row < p.m && at < p.n) finish8<EPI>(p, row, at, v, u, g, k);
           }
-          if (row < p.m && at < p.n) finish8<EPI>(p, w.prob, row, at, v, u, g, k);
         }
       } else {
         const uint32_t acc = next_sum();
