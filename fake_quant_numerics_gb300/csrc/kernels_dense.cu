@@ -27,7 +27,7 @@
 // tiles fill 3.4 waves of 76 pairs), dh 344 (1398, the epilogue reads and writes
 // 12 bytes an element), dx 655 (1469), the three weight gradients 937 (1540);
 // cuBLAS runs plain products at 1708 under the same cap.  fp32 at 2048 x 4096 x
-// 14336: 263 TFLOP/s forward, 233 backward, six bf16 products each.  With one
+// 14336: 265 TFLOP/s forward, 236 backward, six bf16 products each.  With one
 // token the weights are read at 4.3 TB/s forward and for dx (128 rows of A in
 // every stage: 3.8; tiles of 96 columns, for fuller waves, moved nothing there and
 // cost 16% at 16 x 1024 x 4096).

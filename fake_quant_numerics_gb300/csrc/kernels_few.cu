@@ -11,10 +11,10 @@
 // bandwidth.  a is staged in shared memory; sums are binary32.
 //
 // Measured at dim 4096, hidden 14336 (us, here / on the tensor cores): forward of
-// 1 token 120 / 793 (reading the weights takes 104), 16 tokens 224 / 700, 32
-// tokens 437 / 690, 64 tokens 862 / 655; backward of 1 token 396 / 1000, 16
-// tokens 576 / 962, 32 tokens 908 / 955.  From 16 tokens on the multiply-adds
-// bound it.
+// 1 token 123 / 654 (reading the weights takes 104), 16 tokens 228 / 654, 32
+// tokens 442 / 655, 64 tokens 866 / 658; backward of 1 token 403 / 896, 16 tokens
+// 603 / 877, 32 tokens 924 / 879, 64 tokens 1595 / 885.  From 16 tokens on the
+// multiply-adds bound it.
 #include "qat_few.h"
 #include "qat_layer.cuh"
 #include "qat_tc.cuh"
