@@ -49,13 +49,17 @@ constexpr int kFinishWarps = 8;  // two for each quarter of the tile's rows
 // The backward epilogue reads g and u: each finishing warp has 32 x 32 floats of
 // both in shared memory, in the place of one stage.
 constexpr uint32_t kSideBytes = 2 * 32 * 32 * 4;
+// A plain output whose rows are off the vector grid leaves by pieces of rows: each
+// finishing warp turns 32 rows x 16 columns in shared memory.
+constexpr int kTurnPitch = 17;
+constexpr uint32_t kTurnBytes = 32 * kTurnPitch * 4;
 __host__ __device__ constexpr uint32_t stage_room(int epi) {
   return (epi == kDenseGatedBwd ? 5 : 6) * kStageBytes;
 }
 constexpr int kMaxStages = 9;
 __host__ __device__ constexpr uint32_t dense_smem(int epi) {
   return stage_room(epi) + kBarBytes + 1024 +
-         (epi == kDenseGatedBwd ? kFinishWarps * kSideBytes : 0);
+         kFinishWarps * (epi == kDenseGatedBwd ? kSideBytes : epi == kDenseStore ? kTurnBytes : 0);
 }
 constexpr int kDenseThreads = 64 + 32 * kFinishWarps;
 
@@ -591,8 +595,26 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
         }
       }
     };
+    // 16 columns of a row a thread, stored by 16 columns of two rows: a store of one
+    // element of 32 rows would take 32 sectors (dw_gate and dw_up of 300 tokens, 510
+    // x 1363, fp32: 49 us in place of 57)
+    float* turn = reinterpret_cast<float*>(raw + (bars + kBarBytes - tc::smem(raw)) + (warp - 2) * kTurnBytes);
+    const auto st_turned = [&](int prob, int64_t row0, int64_t c, const float (&v)[16]) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) turn[lane * kTurnPitch + i] = v[i];
+      __syncwarp();
+      const int64_t at = c + lane % 16;
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const int r = i + lane / 16;
+        if (row0 + r < p.m && at < p.n)
+          st_elem<T>(p.c[prob], (row0 + r) * p.n + at, turn[r * kTurnPitch + lane % 16]);
+      }
+    };
     for (int64_t t = first; t < tiles; t += stride) {
       const Tile w = tile_at<CG, EPI>(p, t);
+      const bool turned = EPI == kDenseStore && row_align(p.c[w.prob], p.n * T::BYTES) < 16;
       const int64_t row = w.m0 + (CG == 2 ? (int64_t)rank * kRows : 0) + quad * 32 + lane;
       const int64_t col = w.n0 + c_first;
       if (side && (CG == 2 || p.split == 1)) side_load(row - lane, col);
@@ -655,7 +677,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
             const int64_t at = col + c;
-            if (row < p.m && at < p.n)
+            if (turned)
+              st_turned(w.prob, row - lane, at, v);
+            else if (row < p.m && at < p.n)
               st_row<F32>(p.c[w.prob], row * p.n + at, (int)min((int64_t)16, p.n - at),
                           row_align(p.c[w.prob], p.n * 4), v);
           }
@@ -721,7 +745,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
           } else {
             float g[16], k[16];
             kept(g, k, row, col + c, c % 32, c + 16 < c_count);
-            if (row < p.m && col + c < p.n) finish16<EPI>(p, w.prob, row, col + c, v, u, g, k);
+            if (turned)
+              st_turned(w.prob, row - lane, col + c, v);
+            else if (row < p.m && col + c < p.n)
+              finish16<EPI>(p, w.prob, row, col + c, v, u, g, k);
           }
         }
         if (CG == 1 && p.split > 1) break;  // joined below
