@@ -49,17 +49,16 @@ constexpr int kFinishWarps = 8;  // two for each quarter of the tile's rows
 // The backward epilogue reads g and u: each finishing warp has 32 x 32 floats of
 // both in shared memory, in the place of one stage.
 constexpr uint32_t kSideBytes = 2 * 32 * 32 * 4;
-// A plain output whose rows are off the vector grid leaves by pieces of rows: each
+// Outputs whose rows are off the vector grid leave by pieces of rows: each
 // finishing warp turns 32 rows x 16 columns in shared memory.
-constexpr int kTurnPitch = 17;
-constexpr uint32_t kTurnBytes = 32 * kTurnPitch * 4;
+constexpr uint32_t kTurnBytes = 32 * 17 * 4;
 __host__ __device__ constexpr uint32_t stage_room(int epi) {
   return (epi == kDenseGatedBwd ? 5 : 6) * kStageBytes;
 }
 constexpr int kMaxStages = 9;
 __host__ __device__ constexpr uint32_t dense_smem(int epi) {
   return stage_room(epi) + kBarBytes + 1024 +
-         kFinishWarps * (epi == kDenseGatedBwd ? kSideBytes : epi == kDenseStore ? kTurnBytes : 0);
+         kFinishWarps * (epi == kDenseGatedBwd ? kSideBytes : kTurnBytes);
 }
 constexpr int kDenseThreads = 64 + 32 * kFinishWarps;
 
@@ -114,22 +113,6 @@ __device__ __forceinline__ void st_row(void* p, int64_t at, int left, uint32_t a
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (i < left) st_elem<T>(p, at + i, v[i]);
-  }
-}
-__device__ __forceinline__ void ld_row16(const float* p, int64_t at, int left, uint32_t align,
-                                         float (&v)[16]) {
-  if (left >= 16 && align >= 16) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const float4 q = *reinterpret_cast<const float4*>(p + at + i);
-      v[i] = q.x;
-      v[i + 1] = q.y;
-      v[i + 2] = q.z;
-      v[i + 3] = q.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = i < left ? p[at + i] : 0.0f;
   }
 }
 // 16 consecutive bf16 outputs as an operand of a later product
@@ -543,12 +526,24 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
     // Backward: g and u of 32 rows x 32 columns come in by rows of 128 bytes,
     // asynchronously, and are taken back a row a thread; the 16-byte pieces of a
     // row are permuted by it so that both ways are free of bank conflicts.
-    const bool side = EPI == kDenseGatedBwd && p.n % 4 == 0 &&
-                      ((reinterpret_cast<uint64_t>(p.gp) | reinterpret_cast<uint64_t>(p.up)) & 15) == 0;
+    // Rows off the vector grid come in an element a lane.
+    const bool pieces = p.n % 4 == 0 &&
+                        ((reinterpret_cast<uint64_t>(p.gp) | reinterpret_cast<uint64_t>(p.up)) & 15) == 0;
     const uint32_t side_at = bars + kBarBytes + (warp - 2) * kSideBytes;
     const auto side_load = [&](int64_t row0, int64_t c) {
+      if (!pieces) {
+        const int64_t from = row0 * p.n + c + lane;
+        const int rows = c + lane < p.n ? (int)max((int64_t)0, min((int64_t)32, p.m - row0)) : 0;
+#pragma unroll 4
+        for (int r = 0; r < rows; ++r) {
+          const uint32_t to = side_at + r * 128 + (((lane / 4) ^ (r & 7)) * 16) + lane % 4 * 4;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(p.gp + from + r * p.n) : "memory");
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 4096), "l"(p.up + from + r * p.n)
+                       : "memory");
+        }
+      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; pieces && i < 8; ++i) {
         const int r = i * 4 + lane / 8, k = lane % 8;
         if (row0 + r < p.m && c + k * 4 < p.n) {
           const int64_t at = (row0 + r) * p.n + c + k * 4;
@@ -578,46 +573,63 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
     // g and u of this thread's row, 16 columns from c on (c = c32 within 32)
     const auto kept = [&](float (&g)[16], float (&u)[16], int64_t row, int64_t c, int c32, bool more) {
       if constexpr (EPI == kDenseGatedBwd) {
-        if (side) {
-          if (c32 == 0) side_wait();
+        if (c32 == 0) side_wait();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float4 a, b;
-            side_get(c32 / 4 + k, a, b);
-            g[4 * k] = a.x, g[4 * k + 1] = a.y, g[4 * k + 2] = a.z, g[4 * k + 3] = a.w;
-            u[4 * k] = b.x, u[4 * k + 1] = b.y, u[4 * k + 2] = b.z, u[4 * k + 3] = b.w;
-          }
-          if (c32) side_next(row, c + 16, more);
-        } else if (row < p.m && c < p.n) {
-          const int left = (int)min((int64_t)16, p.n - c);
-          ld_row16(p.gp, row * p.n + c, left, row_align(p.gp, p.n * 4), g);
-          ld_row16(p.up, row * p.n + c, left, row_align(p.up, p.n * 4), u);
+        for (int k = 0; k < 4; ++k) {
+          float4 a, b;
+          side_get(c32 / 4 + k, a, b);
+          g[4 * k] = a.x, g[4 * k + 1] = a.y, g[4 * k + 2] = a.z, g[4 * k + 3] = a.w;
+          u[4 * k] = b.x, u[4 * k + 1] = b.y, u[4 * k + 2] = b.z, u[4 * k + 3] = b.w;
         }
+        if (c32) side_next(row, c + 16, more);
       }
     };
-    // 16 columns of a row a thread, stored by 16 columns of two rows: a store of one
-    // element of 32 rows would take 32 sectors (dw_gate and dw_up of 300 tokens, 510
-    // x 1363, fp32: 49 us in place of 57)
+    // N columns of a row a thread, stored by N columns of 32 / N rows: a store of
+    // one element of 32 rows would take 32 sectors (dw_gate and dw_up of 300 tokens,
+    // 510 x 1363, fp32: 49 us in place of 57)
     float* turn = reinterpret_cast<float*>(raw + (bars + kBarBytes - tc::smem(raw)) + (warp - 2) * kTurnBytes);
-    const auto st_turned = [&](int prob, int64_t row0, int64_t c, const float (&v)[16]) {
+    const auto st_turned = [&](auto type, void* to, int64_t row0, int64_t c, const auto& v) {
+      constexpr int N = sizeof(v) / 4, kPitch = N + 1;
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) turn[lane * kTurnPitch + i] = v[i];
+      for (int i = 0; i < N; ++i) turn[lane * kPitch + i] = v[i];
       __syncwarp();
-      const int64_t at = c + lane % 16;
+      const int64_t at = c + lane % N;
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const int r = i + lane / 16;
+      for (int i = 0; i < N; ++i) {
+        const int r = i * (32 / N) + lane / N;
         if (row0 + r < p.m && at < p.n)
-          st_elem<T>(p.c[prob], (row0 + r) * p.n + at, turn[r * kTurnPitch + lane % 16]);
+          st_elem<decltype(type)>(to, (row0 + r) * p.n + at, turn[r * kPitch + lane % N]);
+      }
+    };
+    const auto off_grid = [&](const void* q, int bytes) { return q && row_align(q, p.n * bytes) < 16; };
+    // the same of a gated layer's h, g and u
+    const auto gated_turned = [&](int64_t row, int64_t c, const auto& g, const auto& u) {
+      constexpr int N = sizeof(g) / 4;
+      float h[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) h[i] = act_value<T::BYTES == 2>(p.act, g[i]) * u[i];
+      st_turned(T{}, p.c[0], row - lane, c, h);
+      if (p.q[0] && row < p.m) {
+        const int left = (int)min((int64_t)N, p.n - c);
+        if constexpr (N == 8)
+          st_parts8(p, 0, row, c, left, h);
+        else
+          st_parts16(p, 0, row, c, left, h);
+      }
+      if (p.gp) {
+        st_turned(F32{}, p.gp, row - lane, c, g);
+        st_turned(F32{}, p.up, row - lane, c, u);
       }
     };
     for (int64_t t = first; t < tiles; t += stride) {
       const Tile w = tile_at<CG, EPI>(p, t);
-      const bool turned = EPI == kDenseStore && row_align(p.c[w.prob], p.n * T::BYTES) < 16;
+      const bool turned = EPI == kDenseStore ? off_grid(p.c[w.prob], T::BYTES)
+                          : EPI == kDenseGated ? off_grid(p.c[0], T::BYTES) || off_grid(p.gp, 4) || off_grid(p.up, 4)
+                                               : false;
       const int64_t row = w.m0 + (CG == 2 ? (int64_t)rank * kRows : 0) + quad * 32 + lane;
       const int64_t col = w.n0 + c_first;
-      if (side && (CG == 2 || p.split == 1)) side_load(row - lane, col);
+      if (EPI == kDenseGatedBwd && (CG == 2 || p.split == 1)) side_load(row - lane, col);
       // where k is split: this row of the CTA's sums, in the stage buffers (every
       // stage has been multiplied by then)
       float* sums = reinterpret_cast<float*>(raw + (base - tc::smem(raw))) +
@@ -678,7 +690,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
             for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
             const int64_t at = col + c;
             if (turned)
-              st_turned(w.prob, row - lane, at, v);
+              st_turned(F32{}, p.c[w.prob], row - lane, at, v);
             else if (row < p.m && at < p.n)
               st_row<F32>(p.c[w.prob], row * p.n + at, (int)min((int64_t)16, p.n - at),
                           row_align(p.c[w.prob], p.n * 4), v);
@@ -699,26 +711,20 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
             }
             const int64_t at = col + c;
             if constexpr (EPI == kDenseGatedBwd) {
-              if (side) {
-                if (c % 32 == 0) side_wait();
+              if (c % 32 == 0) side_wait();
 #pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                  float4 a, b;
-                  side_get((c % 32 + i) / 4, a, b);
-                  g[i] = a.x, g[i + 1] = a.y, g[i + 2] = a.z, g[i + 3] = a.w;
-                  k[i] = b.x, k[i + 1] = b.y, k[i + 2] = b.z, k[i + 3] = b.w;
-                }
-                if (c % 32 == 24) side_next(row, at + 8, c + 8 < c_count);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const bool in = row < p.m && at + i < p.n;
-                  g[i] = in ? p.gp[row * p.n + at + i] : 0.0f;
-                  k[i] = in ? p.up[row * p.n + at + i] : 0.0f;
-                }
+              for (int i = 0; i < 8; i += 4) {
+                float4 a, b;
+                side_get((c % 32 + i) / 4, a, b);
+                g[i] = a.x, g[i + 1] = a.y, g[i + 2] = a.z, g[i + 3] = a.w;
+                k[i] = b.x, k[i + 1] = b.y, k[i + 2] = b.z, k[i + 3] = b.w;
               }
+              if (c % 32 == 24) side_next(row, at + 8, c + 8 < c_count);
             }
-            if (row < p.m && at < p.n) finish8<EPI>(p, row, at, v, u, g, k);
+            if (EPI == kDenseGated && turned)
+              gated_turned(row, at, v, u);
+            else if (row < p.m && at < p.n)
+              finish8<EPI>(p, row, at, v, u, g, k);
           }
         }
       } else {
@@ -745,8 +751,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
           } else {
             float g[16], k[16];
             kept(g, k, row, col + c, c % 32, c + 16 < c_count);
-            if (turned)
-              st_turned(w.prob, row - lane, col + c, v);
+            if (EPI == kDenseStore && turned)
+              st_turned(T{}, p.c[w.prob], row - lane, col + c, v);
+            else if (EPI == kDenseGated && turned)
+              gated_turned(row, col + c, v, u);
             else if (row < p.m && col + c < p.n)
               finish16<EPI>(p, w.prob, row, col + c, v, u, g, k);
           }

@@ -187,6 +187,13 @@ def test_ffn_few_rows(dtype, tokens, dim, hidden):
     ffn_case(tokens, dim, hidden, dtype, "gelu")
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_ffn_odd_rows_in_many_tiles(dtype):
+    """More tiles than clusters that split k: every output leaves from a tile's own
+    sums, with rows off the vector grid."""
+    ffn_case(1100, 517, 2051, dtype, "silu")
+
+
 def test_ffn_few_rows_do_not_depend_on_what_else_is_staged():
     """The rows that a stage leaves out are read as whatever lies there: infinite
     weights of one output stay in that output."""
