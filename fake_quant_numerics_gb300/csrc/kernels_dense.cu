@@ -586,7 +586,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
     };
     // N columns of a row a thread, stored by N columns of 32 / N rows: a store of
     // one element of 32 rows would take 32 sectors (dw_gate and dw_up of 300 tokens,
-    // 510 x 1363, fp32: 49 us in place of 57)
+    // 510 x 1363, fp32: 49 us in place of 57; the gated product of bf16 layers of
+    // 4000 x 1001 x 4003 makes their forward 135 us in place of 243)
     float* turn = reinterpret_cast<float*>(raw + (bars + kBarBytes - tc::smem(raw)) + (warp - 2) * kTurnBytes);
     const auto st_turned = [&](auto type, void* to, int64_t row0, int64_t c, const auto& v) {
       constexpr int N = sizeof(v) / 4, kPitch = N + 1;
