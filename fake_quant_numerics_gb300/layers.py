@@ -63,8 +63,14 @@ def _of_type(like: torch.Tensor, *tensors: Optional[torch.Tensor]):
             continue
         if t.dtype != like.dtype:
             raise TypeError(f"{t.dtype} beside {like.dtype}: the call's tensors share one dtype")
-        if t.device != like.device:
-            raise ValueError(f"tensors on {t.device} and {like.device}")
+        _on_device(like.device, t)
+
+
+def _on_device(device, *tensors):
+    """Every tensor (or 4-bit weight) is on this device: the kernels take addresses."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {t.device} and {device}")
 
 
 # ---------------------------------------------------------------------------
@@ -75,9 +81,11 @@ class Weight4:
     its tensors and the qat_weight4 of their addresses: do not change them."""
 
     __slots__ = ("codes", "scale", "zero_point", "super_scales", "rows", "cols", "layout", "group",
-                 "struct", "address")
+                 "device", "struct", "address")
 
     def __init__(self, codes, scale, zero_point, super_scales, rows, cols, layout, group):
+        self.device = codes.device
+        _on_device(codes.device, scale, zero_point, super_scales)
         self.codes, self.scale, self.zero_point, self.super_scales = codes, scale, zero_point, super_scales
         self.rows, self.cols, self.layout, self.group = rows, cols, layout, group
         self.struct = _lib.Weight4Struct(
@@ -110,15 +118,21 @@ def weight4(codes: torch.Tensor, scale: torch.Tensor, rows: int, cols: int, gran
 
 def weight4_double(dq: DoubleQuantized4Bit, rows: int, cols: int) -> Weight4:
     """The [rows, cols] weight of quantize_4bit_double's result."""
-    if dq.len != rows * cols:
+    if (dq.data.dtype != torch.uint8 or dq.quantized_scales.dtype != torch.uint8
+            or dq.super_scales.dtype != torch.float32):
+        raise TypeError("codes and their scales are uint8, super scales float32")
+    blocks = (dq.len + 63) // 64
+    if (dq.len != rows * cols or dq.data.numel() < (dq.len + 1) // 2
+            or dq.quantized_scales.numel() < blocks or dq.super_scales.numel() < (blocks + 255) // 256):
         raise _mismatch("weight4_double")
     return Weight4(_ready(dq.data), _ready(dq.quantized_scales), None, dq.super_scales.contiguous(),
                    rows, cols, W4_DOUBLE, 0)
 
 
-def _w4(w: Weight4):
-    if not w.codes.is_cuda:
-        raise ValueError("libqat takes CUDA tensors only")
+def _w4(w: Weight4, x: torch.Tensor):
+    """The weight's address, for a call on x (itself refused off the GPU)."""
+    if w.device != x.device:
+        _on_device(x.device, w)
     return w.address
 
 
@@ -127,7 +141,7 @@ def qat_linear4_workspace_bytes(dtype, tokens: int, cols: int) -> int:
 
 
 def qat_linear4(x, tokens, w: Weight4, y, workspace, stream=None):
-    st = _lib.lib().qat_linear4(_p(x), _dt(x), tokens, _w4(w), _p(y), _p(workspace),
+    st = _lib.lib().qat_linear4(_p(x), _dt(x), tokens, _w4(w, x), _p(y), _p(workspace),
                                 _nbytes(workspace), _s(stream))
     _lib.check("qat_linear4", st)
 
@@ -138,8 +152,8 @@ def qat_gated_ffn4_workspace_bytes(dtype, tokens: int, dim: int, hidden: int) ->
 
 def qat_gated_ffn4(x, tokens, gate: Weight4, up: Weight4, down: Weight4, act, y, workspace,
                    stream=None):
-    st = _lib.lib().qat_gated_ffn4(_p(x), _dt(x), tokens, _w4(gate), _w4(up), _w4(down), _ACT[act],
-                                   _p(y), _p(workspace), _nbytes(workspace), _s(stream))
+    st = _lib.lib().qat_gated_ffn4(_p(x), _dt(x), tokens, _w4(gate, x), _w4(up, x), _w4(down, x),
+                                   _ACT[act], _p(y), _p(workspace), _nbytes(workspace), _s(stream))
     _lib.check("qat_gated_ffn4", st)
 
 
@@ -149,6 +163,7 @@ def linear4(x: torch.Tensor, weight: Weight4) -> torch.Tensor:
     shape, cols = x.shape, weight.cols
     if not shape or shape[-1] != cols:
         raise _mismatch("linear4")
+    w = _w4(weight, x)
     x = x.contiguous()
     tokens, dt, dev, lib = _leading(x, shape), _dt(x), x.device, _lib.lib()
     y = torch.empty(shape[:-1] + (weight.rows,), dtype=x.dtype, device=dev)
@@ -156,7 +171,7 @@ def linear4(x: torch.Tensor, weight: Weight4) -> torch.Tensor:
     if dt != BF16 or xp % 16:
         n = lib.qat_linear4_workspace_bytes(dt, tokens, cols)
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    st = lib.qat_linear4(xp, dt, tokens, _w4(weight), y.data_ptr(), ws.data_ptr() if n else None, n,
+    st = lib.qat_linear4(xp, dt, tokens, w, y.data_ptr(), ws.data_ptr() if n else None, n,
                          _raw_stream(dev.index))
     if st:
         _lib.check("qat_linear4", st)
@@ -170,12 +185,13 @@ def gated_ffn4(x: torch.Tensor, gate: Weight4, up: Weight4, down: Weight4,
     shape = x.shape
     if not shape or shape[-1] != gate.cols or down.cols != gate.rows:
         raise _mismatch("gated_ffn4")
+    w_gate, w_up, w_down = _w4(gate, x), _w4(up, x), _w4(down, x)
     x = x.contiguous()
     tokens, dt, dev, lib = _leading(x, shape), _dt(x), x.device, _lib.lib()
     y = torch.empty(shape[:-1] + (down.rows,), dtype=x.dtype, device=dev)
     n = lib.qat_gated_ffn4_workspace_bytes(dt, tokens, gate.cols, gate.rows)
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    st = lib.qat_gated_ffn4(_ptr(x), dt, tokens, _w4(gate), _w4(up), _w4(down), _ACT[activation],
+    st = lib.qat_gated_ffn4(_ptr(x), dt, tokens, w_gate, w_up, w_down, _ACT[activation],
                             y.data_ptr(), ws.data_ptr(), n, _raw_stream(dev.index))
     if st:
         _lib.check("qat_gated_ffn4", st)
@@ -262,6 +278,7 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
     _of_type(x, dy, h)
     if g.dtype != torch.float32 or u.dtype != torch.float32:
         raise TypeError("the saved pre-activations are float32")
+    _on_device(x.device, g, u)
     dy, x, h, g, u = _aligned(dy), _aligned(x), _aligned(h), g.contiguous(), u.contiguous()
     w_gate, w_up, w_down = _aligned(w_gate), _aligned(w_up), _aligned(w_down)
     dx = torch.empty_like(x) if want_dx else None
@@ -378,6 +395,8 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
         _of_type(x, dy)
     if mean.dtype != torch.float32 or rstd.dtype != torch.float32:
         raise TypeError("mean and rstd are float32")
+    if mean.device != x.device or rstd.device != x.device:
+        _on_device(x.device, mean, rstd)
     dy, x, mean, rstd = dy.contiguous(), x.contiguous(), mean.contiguous(), rstd.contiguous()
     wp = None
     if weight is not None:

@@ -1,0 +1,74 @@
+"""What the layer bindings refuse or set up before anything reaches a kernel
+(CPU; the meta device stands for another device)."""
+import pytest
+import torch
+
+import fake_quant_numerics_gb300 as fq
+from fake_quant_numerics_gb300 import _lib as L
+
+
+def meta(t):
+    return t.to("meta")
+
+
+CODES, SCALE, ZP = torch.zeros(32 * 64 // 2, dtype=torch.uint8), torch.ones(32), torch.zeros(32, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("build", [
+    lambda: fq.weight4(CODES, meta(SCALE), 32, 64, "row"),
+    lambda: fq.weight4(meta(CODES), SCALE, 32, 64, "row"),
+    lambda: fq.weight4(CODES, SCALE, 32, 64, "row", zero_point=meta(ZP)),
+    lambda: fq.weight4_double(double(super_scales=meta(torch.ones(1))), 32, 64),
+    lambda: fq.weight4_double(double(quantized_scales=meta(torch.zeros(32, dtype=torch.uint8))), 32, 64),
+])
+def test_weight_parts_share_a_device(build):
+    """The kernels take raw addresses: a scale in host memory beside codes on the
+    GPU must not reach them."""
+    with pytest.raises(ValueError, match="tensors on (cpu|meta)"):
+        build()
+
+
+def double(n=32 * 64, **kw):
+    blocks = -(-n // 64)
+    a = dict(data=torch.zeros(-(-n // 2), dtype=torch.uint8), quantized_scales=torch.zeros(blocks, dtype=torch.uint8),
+             super_scales=torch.ones(-(-blocks // 256)), len=n, y=None)
+    a.update(kw)
+    return fq.DoubleQuantized4Bit(**a)
+
+
+def test_two_level_weight_checks_its_parts():
+    assert fq.weight4_double(double(), 32, 64).rows == 32
+    assert fq.weight4_double(double(3 * 5501), 3, 5501).super_scales.numel() == 2
+    for short in (dict(data=torch.zeros(32 * 32 - 1, dtype=torch.uint8)),
+                  dict(quantized_scales=torch.zeros(31, dtype=torch.uint8)), dict(super_scales=torch.ones(0))):
+        with pytest.raises(fq.QatError) as e:
+            fq.weight4_double(double(**short), 32, 64)
+        assert e.value.status == L.QAT_ERR_DIMENSION_MISMATCH
+    for other in (dict(data=torch.zeros(32 * 32)), dict(quantized_scales=torch.zeros(32)),
+                  dict(super_scales=torch.ones(1).double())):
+        with pytest.raises(TypeError):
+            fq.weight4_double(double(**other), 32, 64)
+
+
+def test_weights_are_where_x_is():
+    w = fq.weight4(meta(CODES), meta(SCALE), 32, 64, "row")
+    here = fq.weight4(CODES, SCALE, 32, 64, "row")
+    down = fq.weight4(CODES, torch.ones(64), 64, 32, "row")
+    x = torch.zeros(3, 64)
+    for call in (lambda: fq.linear4(x, w), lambda: fq.gated_ffn4(x, w, here, down),
+                 lambda: fq.gated_ffn4(x, here, w, down),
+                 lambda: fq.gated_ffn4(x, here, here, fq.weight4(meta(CODES), meta(torch.ones(64)), 64, 32, "row"))):
+        with pytest.raises(ValueError, match="tensors on (cpu|meta)"):
+            call()
+
+
+def test_saved_tensors_are_where_x_is():
+    x, w, wd = torch.zeros(3, 64), torch.zeros(8, 64), torch.zeros(64, 8)
+    kept = torch.zeros(3, 8)
+    for g, u in ((meta(kept), kept), (kept, meta(kept))):
+        with pytest.raises(ValueError, match="tensors on (cpu|meta)"):
+            fq.gated_ffn_backward(x, x, w, w, wd, fq.GatedFfn(x, kept, g, u))
+    row = torch.zeros(3)
+    for mean, rstd in ((meta(row), row), (row, meta(row))):
+        with pytest.raises(ValueError, match="tensors on (cpu|meta)"):
+            fq.layer_norm_backward(x, x, None, mean, rstd)
