@@ -15,6 +15,7 @@ import ctypes
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._lib import (BF16, GELU, PER_COLUMN, PER_GROUP, PER_ROW, PER_TENSOR, RELU, SILU, W4_DOUBLE, QatError)
@@ -300,7 +301,7 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
 
 
 class GatedFfnFunction(torch.autograd.Function):
-    """gated_ffn with its backward pass."""
+    """gated_ffn with its backward pass (first derivatives; a second one is an error)."""
 
     @staticmethod
     def forward(ctx, x, w_gate, w_up, w_down, activation="silu"):
@@ -310,6 +311,7 @@ class GatedFfnFunction(torch.autograd.Function):
         return r.y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, wg, wu, wd, h, g, u = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -421,7 +423,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
 
 
 class LayerNormFunction(torch.autograd.Function):
-    """layer_norm with its backward pass."""
+    """layer_norm with its backward pass (first derivatives; a second one is an error)."""
 
     @staticmethod
     def forward(ctx, x, weight, bias, eps=1e-5):
@@ -430,6 +432,7 @@ class LayerNormFunction(torch.autograd.Function):
         return r.y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad

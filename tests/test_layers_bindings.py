@@ -72,3 +72,34 @@ def test_saved_tensors_are_where_x_is():
     for mean, rstd in ((meta(row), row), (row, meta(row))):
         with pytest.raises(ValueError, match="tensors on (cpu|meta)"):
             fq.layer_norm_backward(x, x, None, mean, rstd)
+
+
+# --- second derivatives --------------------------------------------------------
+def test_layer_functions_refuse_second_derivatives(monkeypatch):
+    """The backward passes fill tensors by address, so a gradient of a gradient
+    would lose its terms without a word; it is an error instead.  Plain products
+    stand for the kernels."""
+    from fake_quant_numerics_gb300 import layers
+
+    def norm(x, w, b, eps):
+        return layers.LayerNorm(x.detach() * w.detach(), torch.zeros(len(x)), torch.ones(len(x)))
+
+    def norm_back(dy, x, w, mean, rstd, want_dx, want_dw):
+        return (dy * w).detach(), (dy * x).sum(0).detach(), dy.sum(0).detach()
+
+    def ffn(x, wg, wu, wd, act, save):
+        h = (x @ wg.T).detach()
+        return layers.GatedFfn((h @ wd.T).detach(), h, h, h)
+
+    def ffn_back(dy, x, wg, wu, wd, saved, act, want_dx, want_dw):
+        return tuple(torch.ones_like(t) for t in (x, wg, wu, wd))
+
+    for name, f in (("layer_norm", norm), ("layer_norm_backward", norm_back), ("gated_ffn", ffn),
+                    ("gated_ffn_backward", ffn_back)):
+        monkeypatch.setattr(layers, name, f)
+    x, b = torch.randn(3, 4, requires_grad=True), torch.zeros(4, requires_grad=True)
+    w = [torch.randn(4, 4, requires_grad=True) for _ in range(3)]
+    for y in (fq.LayerNormFunction.apply(x, w[0][0], b, 1e-5), fq.GatedFfnFunction.apply(x, *w, "silu")):
+        (dx,) = torch.autograd.grad((y * y).sum(), x, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            ((dx * dx).sum() + x.sum()).backward()
