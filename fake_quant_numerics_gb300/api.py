@@ -555,6 +555,21 @@ def dequantize_4bit_double(dq: DoubleQuantized4Bit) -> torch.Tensor:
     return y
 
 
+class _SteBackward(torch.autograd.Function):
+    """fake_quant_backward as a function of the gradient: linear in it, so its own
+    backward pass is the same mask."""
+
+    @staticmethod
+    def forward(ctx, g, mask):
+        ctx.save_for_backward(mask)
+        return fake_quant_backward(g, mask)
+
+    @staticmethod
+    def backward(ctx, gg):
+        (mask,) = ctx.saved_tensors
+        return _SteBackward.apply(gg, mask), None
+
+
 class FakeQuantSTE(torch.autograd.Function):
     """Integer fake quant whose backward is the straight-through estimator."""
 
@@ -568,4 +583,4 @@ class FakeQuantSTE(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g):
         (mask,) = ctx.saved_tensors
-        return fake_quant_backward(g, mask).view(ctx.shape), None, None, None, None
+        return _SteBackward.apply(g, mask).view(ctx.shape), None, None, None, None

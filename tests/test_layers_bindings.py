@@ -103,3 +103,21 @@ def test_layer_functions_refuse_second_derivatives(monkeypatch):
         (dx,) = torch.autograd.grad((y * y).sum(), x, create_graph=True)
         with pytest.raises(RuntimeError, match="once_differentiable"):
             ((dx * dx).sum() + x.sum()).backward()
+
+
+def test_ste_second_derivative(monkeypatch):
+    """The estimator's backward pass is linear in the gradient: with a mask m,
+    y = x (forward value kept) and L = sum y^3, dL/dx = 3 m y^2 and the gradient of
+    sum (dL/dx) is 6 m y."""
+    from fake_quant_numerics_gb300 import api
+
+    m = torch.tensor([1.0, 0.0, 1.0])
+    monkeypatch.setattr(api, "fake_quant_int", lambda x, *a, **k: api.FakeQuantInt(x.detach().clone(), None, m, None,
+                                                                                 None, None))
+    monkeypatch.setattr(api, "fake_quant_backward", lambda g, mask: (g * mask).detach())
+    x = torch.tensor([2.0, 3.0, -1.0], requires_grad=True)
+    y = fq.FakeQuantSTE.apply(x)
+    (dx,) = torch.autograd.grad((y ** 3).sum(), x, create_graph=True)
+    assert torch.equal(dx.detach(), 3 * m * x.detach() ** 2)
+    (ddx,) = torch.autograd.grad(dx.sum(), x)
+    assert torch.equal(ddx, 6 * m * x.detach())
