@@ -6,7 +6,7 @@ Products of a few tokens with the 4-bit codes the library writes
 (:func:`gated_ffn4`), and layer norm with its backward pass
 (:func:`layer_norm`, :func:`layer_norm_backward`).  The ``qat_*`` functions
 mirror the C ABI; the named ones check shapes, allocate the outputs with torch
-and run on the current stream.  Every step of the computation runs in the
+and run on the current stream of the tensors' device.  Every step of the computation runs in the
 library's kernels.
 """
 from __future__ import annotations
@@ -40,8 +40,20 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _here(t: torch.Tensor) -> int:
-    return _raw_stream(t.device.index)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _call(name: str, device: torch.device, function, *args):
+    """The library's call on the device's current stream.  A launch goes to the
+    current device, so the device is made that for the call where it is not."""
+    index = device.index
+    if index == _current_device():
+        st = function(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            st = function(*args, _raw_stream(index))
+    if st:
+        _lib.check(name, st)
 
 
 def _aligned(t: torch.Tensor) -> torch.Tensor:
@@ -172,10 +184,8 @@ def linear4(x: torch.Tensor, weight: Weight4) -> torch.Tensor:
     if dt != BF16 or xp % 16:
         n = lib.qat_linear4_workspace_bytes(dt, tokens, cols)
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    st = lib.qat_linear4(xp, dt, tokens, w, y.data_ptr(), ws.data_ptr() if n else None, n,
-                         _raw_stream(dev.index))
-    if st:
-        _lib.check("qat_linear4", st)
+    _call("qat_linear4", dev, lib.qat_linear4, xp, dt, tokens, w, y.data_ptr(),
+          ws.data_ptr() if n else None, n)
     return y
 
 
@@ -192,10 +202,8 @@ def gated_ffn4(x: torch.Tensor, gate: Weight4, up: Weight4, down: Weight4,
     y = torch.empty(shape[:-1] + (down.rows,), dtype=x.dtype, device=dev)
     n = lib.qat_gated_ffn4_workspace_bytes(dt, tokens, gate.cols, gate.rows)
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    st = lib.qat_gated_ffn4(_ptr(x), dt, tokens, w_gate, w_up, w_down, _ACT[activation],
-                            y.data_ptr(), ws.data_ptr(), n, _raw_stream(dev.index))
-    if st:
-        _lib.check("qat_gated_ffn4", st)
+    _call("qat_gated_ffn4", dev, lib.qat_gated_ffn4, _ptr(x), dt, tokens, w_gate, w_up, w_down,
+          _ACT[activation], y.data_ptr(), ws.data_ptr(), n)
     return y
 
 
@@ -256,12 +264,10 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     lib, dt = _lib.lib(), _dt(x)
     n = lib.qat_gated_ffn_workspace_bytes(dt, tokens, dim, hidden, 0)
     ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-    st = lib.qat_gated_ffn(_ptr(x), dt, tokens, dim, hidden, w_gate.data_ptr(), w_up.data_ptr(),
-                           w_down.data_ptr(), _ACT[activation], h.data_ptr(),
-                           g.data_ptr() if save else None, u.data_ptr() if save else None,
-                           y.data_ptr(), None, ws.data_ptr() if n else None, n, _here(x))
-    if st:
-        _lib.check("qat_gated_ffn", st)
+    _call("qat_gated_ffn", x.device, lib.qat_gated_ffn, _ptr(x), dt, tokens, dim, hidden,
+          w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), _ACT[activation], h.data_ptr(),
+          g.data_ptr() if save else None, u.data_ptr() if save else None, y.data_ptr(), None,
+          ws.data_ptr() if n else None, n)
     return GatedFfn(y, h, g, u)
 
 
@@ -289,14 +295,11 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
     lib, dt = _lib.lib(), _dt(x)
     n = lib.qat_gated_ffn_workspace_bytes(dt, tokens, dim, hidden, 1)
     ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-    st = lib.qat_gated_ffn_backward(
-        _ptr(dy), _ptr(x), dt, tokens, dim, hidden, w_gate.data_ptr(), w_up.data_ptr(),
-        w_down.data_ptr(), _ACT[activation], h.data_ptr(), g.data_ptr(), u.data_ptr(),
-        dx.data_ptr() if want_dx else None, dwg.data_ptr() if want_dw else None,
-        dwu.data_ptr() if want_dw else None, dwd.data_ptr() if want_dw else None, None,
-        ws.data_ptr() if n else None, n, _here(x))
-    if st:
-        _lib.check("qat_gated_ffn_backward", st)
+    _call("qat_gated_ffn_backward", x.device, lib.qat_gated_ffn_backward, _ptr(dy), _ptr(x), dt, tokens,
+          dim, hidden, w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), _ACT[activation],
+          h.data_ptr(), g.data_ptr(), u.data_ptr(), dx.data_ptr() if want_dx else None,
+          dwg.data_ptr() if want_dw else None, dwu.data_ptr() if want_dw else None,
+          dwd.data_ptr() if want_dw else None, None, ws.data_ptr() if n else None, n)
     return dx, dwg, dwu, dwd
 
 
@@ -366,11 +369,8 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     y = torch.empty_like(x)
     mean = torch.empty(lead, dtype=f32, device=dev)
     rstd = torch.empty(lead, dtype=f32, device=dev)
-    st = _lib.lib().qat_layer_norm(_ptr(x), _dt(x), _leading(x, shape), cols, wp, bp, eps,
-                                   y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-                                   _raw_stream(dev.index))
-    if st:
-        _lib.check("qat_layer_norm", st)
+    _call("qat_layer_norm", dev, _lib.lib().qat_layer_norm, _ptr(x), _dt(x), _leading(x, shape), cols,
+          wp, bp, eps, y.data_ptr(), mean.data_ptr(), rstd.data_ptr())
     return LayerNorm(y, mean, rstd)
 
 
@@ -413,12 +413,10 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
         db = torch.empty(cols, dtype=x.dtype, device=x.device)
         n = lib.qat_layer_norm_backward_workspace_bytes(rows, cols)
         ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-    st = lib.qat_layer_norm_backward(
-        _ptr(dy), _ptr(x), _dt(x), rows, cols, wp, _ptr(mean), _ptr(rstd),
-        dx.data_ptr() if want_dx else None, dw.data_ptr() if want_dw else None,
-        db.data_ptr() if want_dw else None, ws.data_ptr() if n else None, n, _here(x))
-    if st:
-        _lib.check("qat_layer_norm_backward", st)
+    _call("qat_layer_norm_backward", x.device, lib.qat_layer_norm_backward, _ptr(dy), _ptr(x), _dt(x),
+          rows, cols, wp, _ptr(mean), _ptr(rstd), dx.data_ptr() if want_dx else None,
+          dw.data_ptr() if want_dw else None, db.data_ptr() if want_dw else None,
+          ws.data_ptr() if n else None, n)
     return dx, dw, db
 
 

@@ -121,3 +121,46 @@ def test_ste_second_derivative(monkeypatch):
     assert torch.equal(dx.detach(), 3 * m * x.detach() ** 2)
     (ddx,) = torch.autograd.grad(dx.sum(), x)
     assert torch.equal(ddx, 6 * m * x.detach())
+
+
+# --- the current device ----------------------------------------------------------
+@pytest.mark.parametrize("current,guarded", [(None, False), (1, True)])
+def test_calls_launch_on_the_tensors_device(monkeypatch, current, guarded):
+    """A launch goes to the current device, so tensors of another one make theirs
+    current for the call (host tensors, whose device has no index, stand for them)."""
+    from fake_quant_numerics_gb300 import layers
+
+    entered, seen = [], []
+
+    class Guard:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            entered.append(self.device)
+
+        def __exit__(self, *args):
+            entered.pop()
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith("workspace_bytes"):
+                return lambda *a: 64
+            return lambda *a: seen.append((name, bool(entered))) or 0
+
+    monkeypatch.setattr(layers._lib, "lib", lambda: Lib())
+    monkeypatch.setattr(layers, "_ptr", lambda t: t.data_ptr())
+    monkeypatch.setattr(layers, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(layers, "_current_device", lambda: current, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    x, w, wd = torch.zeros(3, 64), torch.zeros(32, 64), torch.zeros(64, 32)
+    w4, down = fq.weight4(CODES, SCALE, 32, 64, "row"), fq.weight4(CODES, torch.ones(64), 64, 32, "row")
+    fq.linear4(x, w4)
+    fq.gated_ffn4(x, w4, w4, down)
+    r = fq.gated_ffn(x, w, w, wd, save=True)
+    fq.gated_ffn_backward(x, x, w, w, wd, r)
+    n = fq.layer_norm(x)
+    fq.layer_norm_backward(x, x, None, n.mean, n.rstd)
+    assert not entered
+    names = ["linear4", "gated_ffn4", "gated_ffn", "gated_ffn_backward", "layer_norm", "layer_norm_backward"]
+    assert seen == [("qat_" + name, guarded) for name in names]
