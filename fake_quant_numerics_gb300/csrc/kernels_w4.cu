@@ -772,6 +772,9 @@ qat_status launch_gated4(const void* x, qat_dtype dt, int64_t tokens, const qat_
   char* h = base + planes_bytes(tokens, dim, 3);
   char* h_planes = h + r256((size_t)tokens * hidden * 4);
   bool launched = false;
+  // no hidden values: the second product is an empty sum, the first has no rows to launch
+  if (hidden == 0)
+    return product(h, QAT_F32, tokens, &down, 1, 0, Y4{y, dt, 0, 0, 0}, h_planes, &launched, s);
   if (fast_ok(*gate_up, tokens) && fast_ok(down, tokens)) {
     // h straight as the second product's planes
     const int terms = dt == QAT_BF16 ? 2 : 3;

@@ -1,0 +1,28 @@
+"""GPU tests of the layer operators at the edges of their ranges: empty sizes, time-outs
+in the middle of a call, the tile shapes of the large products.  Bounds as in
+layer_reference.py."""
+import numpy as np
+import pytest
+import torch
+
+import fake_quant_numerics_gb300 as fq
+import layer_reference as ref
+from test_gpu_layers import DTYPES, quantized, rnd
+
+pytestmark = pytest.mark.gpu
+
+
+def empty_weight(rows, cols):
+    return fq.weight4(torch.empty(0, dtype=torch.uint8, device="cuda"), torch.ones(rows, device="cuda"), rows, cols,
+                      "row")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,dim,hidden", [(3, 64, 0), (3, 0, 64), (3, 31, 0), (0, 64, 32), (600, 64, 0), (2, 0, 0)])
+def test_gated_ffn4_empty_sizes(dtype, tokens, dim, hidden):
+    """An empty sum is zero (act(0) * 0 too), no tokens are no output."""
+    up = quantized(hidden, dim, "row", 0, "symmetric") if hidden and dim else empty_weight(hidden, dim)
+    down = quantized(dim, hidden, "row", 0, "symmetric") if hidden and dim else empty_weight(dim, hidden)
+    x = rnd(1, tokens, dim, dtype=dtype)
+    y = fq.gated_ffn4(x, up, up, down)
+    assert y.dtype == dtype and torch.equal(y, torch.zeros(tokens, dim, dtype=dtype, device="cuda"))
