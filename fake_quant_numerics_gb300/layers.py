@@ -369,6 +369,9 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     y = torch.empty_like(x)
     mean = torch.empty(lead, dtype=f32, device=dev)
     rstd = torch.empty(lead, dtype=f32, device=dev)
+    if cols == 0:  # the call is a no-op, and the mean of no elements 0 / 0
+        mean.fill_(float("nan"))
+        rstd.fill_(float("nan"))
     _call("qat_layer_norm", dev, _lib.lib().qat_layer_norm, _ptr(x), _dt(x), _leading(x, shape), cols,
           wp, bp, eps, y.data_ptr(), mean.data_ptr(), rstd.data_ptr())
     return LayerNorm(y, mean, rstd)

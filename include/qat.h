@@ -545,7 +545,8 @@ qat_status qat_gated_ffn_backward(const void* dy, const void* x, qat_dtype dtype
  * bias.  x, y: dtype[rows, cols]; weight, bias (nullable: 1 and 0):
  * dtype[cols]; mean, rstd (nullable): float[rows].  The deviations are summed
  * around the mean, not from sum x^2.  eps finite and >= 0
- * (QAT_ERR_INVALID_ARGUMENT).  rows * cols == 0 is a no-op.  One launch.
+ * (QAT_ERR_INVALID_ARGUMENT).  rows * cols == 0 is a no-op (mean and rstd are
+ * left as they are).  One launch.
  */
 qat_status qat_layer_norm(const void* x, qat_dtype dtype, int64_t rows, int64_t cols,
                           const void* weight, const void* bias, float eps, void* y, float* mean,

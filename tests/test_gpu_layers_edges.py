@@ -26,3 +26,17 @@ def test_gated_ffn4_empty_sizes(dtype, tokens, dim, hidden):
     x = rnd(1, tokens, dim, dtype=dtype)
     y = fq.gated_ffn4(x, up, up, down)
     assert y.dtype == dtype and torch.equal(y, torch.zeros(tokens, dim, dtype=dtype, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_layer_norm_of_empty_rows(dtype):
+    """The mean of no elements is 0 / 0, and so is what follows from it; memory that
+    was freed before must not show through."""
+    for _ in range(3):
+        torch.full((4096,), 7.0, device="cuda")
+    x = torch.empty(5, 3, 0, dtype=dtype, device="cuda")
+    r = fq.layer_norm(x)
+    assert r.y.shape == x.shape and r.mean.shape == r.rstd.shape == (5, 3)
+    assert torch.isnan(r.mean).all() and torch.isnan(r.rstd).all()
+    dx, dw, db = fq.layer_norm_backward(x, x, None, r.mean, r.rstd)
+    assert dx.shape == x.shape and dw.shape == db.shape == (0,)

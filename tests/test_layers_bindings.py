@@ -164,3 +164,15 @@ def test_calls_launch_on_the_tensors_device(monkeypatch, current, guarded):
     assert not entered
     names = ["linear4", "gated_ffn4", "gated_ffn", "gated_ffn_backward", "layer_norm", "layer_norm_backward"]
     assert seen == [("qat_" + name, guarded) for name in names]
+
+
+def test_layer_norm_of_empty_rows_has_no_statistics(monkeypatch):
+    """The library's call is a no-op for rows without elements: the binding gives
+    their mean, 0 / 0, not the memory it allocated."""
+    from fake_quant_numerics_gb300 import layers
+
+    monkeypatch.setattr(layers, "_call", lambda *a: None)
+    monkeypatch.setattr(layers, "_ptr", lambda t: t.data_ptr())
+    monkeypatch.setattr(torch, "empty", lambda *s, **kw: torch.ones(*s, **kw))
+    r = fq.layer_norm(torch.zeros(4, 0))
+    assert torch.isnan(r.mean).all() and torch.isnan(r.rstd).all() and r.mean.shape == (4,)
