@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
               tc::tmem_ld32(acc + kOut + c, r);
               tc::tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) su[c + i] += __uint_as_float(r[i]);
+              for (int i = 0; i < 32; ++i) su[c + i] += ok ? __uint_as_float(r[i]) : kBad;
             }
           }
           if (un + 1 < u1) sum_read();
@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             v[i] = ok ? __uint_as_float(r[i]) : kBad;
-            u[i] = EPI == kDenseGated ? __uint_as_float(q[i]) : 0.0f;
+            u[i] = EPI != kDenseGated ? 0.0f : ok ? __uint_as_float(q[i]) : kBad;
           }
           if (CG == 1 && p.split > 1) {
 #pragma unroll

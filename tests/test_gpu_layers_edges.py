@@ -40,3 +40,44 @@ def test_layer_norm_of_empty_rows(dtype):
     assert torch.isnan(r.mean).all() and torch.isnan(r.rstd).all()
     dx, dw, db = fq.layer_norm_backward(x, x, None, r.mean, r.rstd)
     assert dx.shape == x.shape and dw.shape == db.shape == (0,)
+
+
+# --- bounded waits ---------------------------------------------------------------
+class Timed:
+    """One forward call of the gated block through the C ABI, with a limit on the
+    polls of its device waits."""
+
+    def __init__(self, tokens, dim, hidden, dtype):
+        self.x, self.sizes = rnd(1, tokens, dim, dtype=dtype), (tokens, dim, hidden)
+        self.w = [rnd(s, hidden, dim, dtype=dtype, scale=0.1) for s in (2, 3)]
+        self.wd = rnd(4, dim, hidden, dtype=dtype, scale=0.1)
+        n = fq.qat_gated_ffn_workspace_bytes(0 if dtype == torch.float32 else 1, *self.sizes)
+        self.ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+
+    def run(self, limit):
+        """(flags, h, g, u, y)"""
+        tokens, dim, hidden = self.sizes
+        h, y = self.x.new_zeros(tokens, hidden), torch.zeros_like(self.x)
+        g, u = (torch.zeros(tokens, hidden, device="cuda") for _ in range(2))
+        flags, lib = torch.zeros(1, dtype=torch.int32, device="cuda"), fq.load()
+        try:
+            lib.qat_debug_set_wait_limit(limit)
+            fq.qat_gated_ffn(self.x, tokens, dim, hidden, *self.w, self.wd, "silu", h, g, u, y, flags, self.ws)
+            torch.cuda.synchronize()
+        finally:
+            lib.qat_debug_set_wait_limit(-1)
+        return int(flags.item()), h, g, u, y
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,dim,hidden", [(70, 1024, 256), (200, 128, 128), (2600, 256, 2048)])
+def test_wait_that_runs_out_leaves_no_stale_output(dtype, tokens, dim, hidden):
+    """With no polls allowed nothing is computed: every output is NaN, both
+    pre-activations among them."""
+    call = Timed(tokens, dim, hidden, dtype)
+    flags, *outs = call.run(0)
+    assert flags & 16                                   # QAT_FLAG_DEVICE_TIMEOUT
+    for name, t in zip(("h", "gate_pre", "up_pre", "y"), outs):
+        assert torch.isnan(t).all(), name
+    flags, *again = call.run(-1)
+    assert flags == 0 and all(torch.isfinite(t).all() for t in again)
