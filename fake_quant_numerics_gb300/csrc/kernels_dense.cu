@@ -61,6 +61,7 @@ __host__ __device__ constexpr uint32_t dense_smem(int epi) {
          kFinishWarps * (epi == kDenseGatedBwd ? kSideBytes : kTurnBytes);
 }
 constexpr int kDenseThreads = 64 + 32 * kFinishWarps;
+constexpr uint32_t kDrainPolls = 1u << 16;  // of a wait for what is in flight at the block's end
 
 struct DenseArgs {
   CUtensorMap a[2], b[2];
@@ -447,14 +448,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
           }
         }
       }
-      if (!ok) {  // copies in flight land before the block ends
-        volatile int none = 0;
-        if (leader)
-          for (int64_t i = issued > stages ? issued - stages : 0; i < issued; ++i)
-            tc::bar_wait(full((int)(i % stages)), (uint32_t)(i / stages) & 1, &none, 1u << 16);
-        else  // they are counted in the other CTA: a millisecond is ample
-          for (int i = 0; i < 1024; ++i) __nanosleep(1000);
-      }
+      // The last copies land before the block ends, also where other warps gave up
+      // on them (a pair's are counted in its leader, see the block's end).
+      volatile int none = 0;
+      if (leader)
+        for (int64_t i = issued > stages ? issued - stages : 0; i < issued; ++i)
+          if (!tc::bar_wait(full((int)(i % stages)), (uint32_t)(i / stages) & 1, &none, kDrainPolls))
+            abort_flag = 1;
     }
   } else if (warp == 1) {
     if (leader && lane == 0) {
@@ -495,11 +495,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
           }
         }
       }
-      if (!ok) {  // MMAs in flight end before tensor memory is freed
-        volatile int none = 0;
-        tc::mma_commit<CG>(drain);
-        tc::bar_wait(drain, 0, &none, 1u << 16);
-      }
+      // The last MMAs end before tensor memory is freed, also where the finishing
+      // warps gave up on them.
+      volatile int none = 0;
+      tc::mma_commit<CG>(drain);
+      if (!tc::bar_wait(drain, 0, &none, kDrainPolls)) abort_flag = 1;
     }
   } else {
     const int quad = warp & 3;
@@ -789,7 +789,20 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
       finish4<T, EPI>(p, w.prob, w.m0 + r, w.n0 + c, vs, us);
     }
   }
+  if (CG == 2) {
+    volatile int none = 0;
+    if (leader && threadIdx.x == 0 && abort_flag)
+      tc::st_cluster(tc::map_rank(tc::smem(const_cast<int*>(&abort_flag)), 1), 1);
+    // the MMAs' end has been signalled here too
+    if (!leader && threadIdx.x == 0) tc::bar_wait(drain, 0, &none, kDrainPolls);
+    __syncwarp();
+  }
   if (CG == 2 || p.split > 1) tc::cluster_sync();  // peers have read this CTA's memory
+  // The leader has seen the pair's copies land unless one of the two gave up; then
+  // those it did not wait for have a millisecond, which is ample, before the CTA they
+  // write to and the one that counts them may end.
+  if (CG == 2 && threadIdx.x == 0 && abort_flag)
+    for (int i = 0; i < 1024; ++i) __nanosleep(1000);
   if (threadIdx.x == 0 && abort_flag && p.flags) atomicOr(p.flags, QAT_FLAG_DEVICE_TIMEOUT);
   if (warp == 1) tc::tmem_free<CG>(tmem, kTmemCols);
 }

@@ -81,3 +81,28 @@ def test_wait_that_runs_out_leaves_no_stale_output(dtype, tokens, dim, hidden):
         assert torch.isnan(t).all(), name
     flags, *again = call.run(-1)
     assert flags == 0 and all(torch.isfinite(t).all() for t in again)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,dim,hidden", [(200, 128, 128), (1500, 192, 256)])
+def test_wait_that_runs_out_in_the_middle(dtype, tokens, dim, hidden):
+    """A limit that some waits pass and others may not: an output is either right or
+    NaN, and without a flag all are right.  The block waits for the copies and
+    products it has in flight before it ends, whichever warp gave up."""
+    right_or_nan(dtype, tokens, dim, hidden)
+
+
+def right_or_nan(dtype, tokens, dim, hidden):
+    call = Timed(tokens, dim, hidden, dtype)
+    flags, *whole = call.run(-1)
+    assert flags == 0
+    for limit in (1, 2, 3, 5, 9, 17, 40, 100):
+        flags, *outs = call.run(limit)
+        missing = 0
+        for name, t, w in zip(("h", "gate_pre", "up_pre", "y"), outs, whole):
+            nan = torch.isnan(t)
+            missing += int(nan.sum())
+            assert torch.equal(torch.where(nan, w, t), w), (limit, name)
+        assert bool(flags & 16) or not missing, limit
+    flags, *again = call.run(-1)
+    assert flags == 0 and all(torch.equal(a, w) for a, w in zip(again, whole))
