@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
       const int64_t col = w.n0 + c_first;
       if (EPI == kDenseGatedBwd && (CG == 2 || p.split == 1)) side_load(row - lane, col);
       // where k is split: this row of the CTA's sums, in the stage buffers (every
-      // stage has been multiplied by then)
+      // stage has been multiplied by then, unless a wait ran out)
       float* sums = reinterpret_cast<float*>(raw + (base - tc::smem(raw))) +
                     (quad * 32 + lane) * kJoinPitch + c_first;
       if constexpr (U::kParts) {
@@ -766,6 +766,14 @@ __global__ void __launch_bounds__(kDenseThreads, 1) k_dense(const __grid_constan
   }
   __syncthreads();
   if (CG == 1 && p.split > 1) {
+    // A finishing warp that gave up left its NaN in the stage buffers while copies
+    // could still land there: once more, now that none is in flight.
+    if (!ok && warp >= 2) {
+      float* row = reinterpret_cast<float*>(raw + (base - tc::smem(raw))) +
+                   ((warp & 3) * 32 + lane) * kJoinPitch;
+      constexpr float kBad = __builtin_nanf("");
+      for (int c = 0; c < kAccCols; c += 4) put4(row + c, kBad, kBad, kBad, kBad);
+    }
     tc::cluster_sync();
     // the cluster's CTAs finish the tile together, four columns of a row a
     // thread, adding the k slices in rank order with every slice's load in flight

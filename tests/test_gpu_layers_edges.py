@@ -106,3 +106,11 @@ def right_or_nan(dtype, tokens, dim, hidden):
         assert bool(flags & 16) or not missing, limit
     flags, *again = call.run(-1)
     assert flags == 0 and all(torch.equal(a, w) for a, w in zip(again, whole))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,dim,hidden", [(70, 1024, 256), (128, 2048, 640), (40, 384, 4096)])
+def test_wait_that_runs_out_in_the_middle_of_split_sums(dtype, tokens, dim, hidden):
+    """The CTAs of a cluster leave their sums where the copies land: no copy that is
+    still in flight may put its data in the place of a NaN."""
+    right_or_nan(dtype, tokens, dim, hidden)
