@@ -468,10 +468,9 @@ __global__ void __launch_bounds__(256)
 // every 32nd part, their sums added in order.
 template <typename T>
 __global__ void __launch_bounds__(1024)
-    k_norm_cols_join(const float* __restrict__ ws, int parts, int64_t cols, void* __restrict__ dw,
-                     void* __restrict__ db) {
+    k_norm_cols_join(const float* ws, int parts, int64_t cols, void* dw, void* db) {
   __shared__ float sums[2][32][33];
-  pdl_wait();
+  pdl_wait();  // the partials are the previous kernel's
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float sw = 0.0f, sb = 0.0f;

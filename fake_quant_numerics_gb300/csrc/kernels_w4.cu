@@ -72,11 +72,11 @@ __device__ __forceinline__ void w4_row_generic(const void* x, int64_t t0, int nt
 }
 
 template <typename T, bool DOUBLE, int NW>
-__global__ void __launch_bounds__(128) k_w4_generic(const void* __restrict__ x, int64_t tokens,
-                                                    W4 wa, W4 wb, int64_t rows, int64_t cols,
-                                                    int act, void* __restrict__ y, int y_bf16) {
+__global__ void __launch_bounds__(128) k_w4_generic(const void* x, int64_t tokens, W4 wa, W4 wb,
+                                                    int64_t rows, int64_t cols, int act, void* y,
+                                                    int y_bf16) {
   pdl_trigger();
-  pdl_wait();
+  pdl_wait();  // x may be the previous kernel's output
   const int lane = threadIdx.x & 31;
   const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (n >= rows) return;
@@ -161,6 +161,15 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t w, uint32_t bias) {
 }
 // 136 + zp as a bf16 pair (exact)
 __device__ __forceinline__ uint32_t w4_bias(int zp) { return (uint32_t)(0x4308 + zp) * 0x10001u; }
+// 8 bf16 of x, coherently, and free to move among the products (a C++ load is not:
+// 32 fp32 tokens by [14336, 4096] take 132 us in place of 93)
+__device__ __forceinline__ uint4 ld_x(const uint4* p) {
+  uint4 v;
+  asm("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "l"(__cvta_generic_to_global(p)));
+  return v;
+}
 // what a lane past the end of a row takes for x
 __device__ const uint4 kZeros[4] = {};
 
@@ -405,7 +414,11 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) k_w4(const __grid_constant__
 #pragma unroll
   for (int d = 0; d < D; ++d)
     if (d < work) fetch(d);
-  pdl_wait();  // x may be the previous kernel's output; the weights are not
+  // x may be the previous kernel's output; the weights, which come through the
+  // read-only path, are not.  No load of x moves above this: its address is known here.
+  pdl_wait();
+#pragma unroll
+  for (int q = 0; q < NT; ++q) asm volatile("" : "+l"(xp[q])::"memory");
   int kb = start;
   for (int it = 0; it < work; it += D) {
 #pragma unroll
@@ -453,7 +466,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) k_w4(const __grid_constant__
 #pragma unroll
           for (int q = 0; q < NT; ++q)
 #pragma unroll
-            for (int m = 0; m < kTerms; ++m) b[q][m] = x_pairs<TERMS != 0>(__ldg(xs[q][m] + j));
+            for (int m = 0; m < kTerms; ++m) b[q][m] = x_pairs<TERMS != 0>(ld_x(xs[q][m] + j));
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint32_t a[2][4];
@@ -496,9 +509,8 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) k_w4(const __grid_constant__
 
 // x [tokens, cols] as planes (cols a multiple of 8): a thread takes 8 elements.
 template <typename T>
-__global__ void __launch_bounds__(256) k_w4_planes(const void* __restrict__ x, int64_t total,
-                                                   int terms, int64_t plane,
-                                                   __nv_bfloat16* __restrict__ out) {
+__global__ void __launch_bounds__(256) k_w4_planes(const void* x, int64_t total, int terms,
+                                                   int64_t plane, __nv_bfloat16* out) {
   pdl_trigger();
   pdl_wait();
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
