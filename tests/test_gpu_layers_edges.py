@@ -114,3 +114,41 @@ def test_wait_that_runs_out_in_the_middle_of_split_sums(dtype, tokens, dim, hidd
     """The CTAs of a cluster leave their sums where the copies land: no copy that is
     still in flight may put its data in the place of a NaN."""
     right_or_nan(dtype, tokens, dim, hidden)
+
+
+# --- the large tiles -----------------------------------------------------------------
+def sample(n, side, seed):
+    """Indices on both sides of every tile edge and some between them."""
+    at = {0, n - 1} | {i + d for i in range(side, n, side) for d in (-1, 0)}
+    at |= set(np.random.default_rng(seed).integers(0, n, 48).tolist())
+    return sorted(at)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,dim,hidden", [
+    (5000, 1032, 1104), (5000, 1031, 1101),   # y, dx: tiles of 224 columns; gated, dh: of 256
+    (4100, 2048, 1104), (4100, 2047, 1101),   # y, dx: tiles of 256 columns
+    (192, 4096, 2304), (150, 4095, 2301),     # weight gradients: 256 columns, two of them at once
+    (192, 2048, 2560), (150, 2049, 2563),     # weight gradients: 224 columns
+])
+def test_ffn_tiles_of_cta_pairs(dtype, tokens, dim, hidden):
+    """Products large enough for pairs of CTAs with more than one tile each, in whole
+    vectors and off them, on a sample of rows (of y and dx) and of hidden values (of
+    the weights' gradients) with every tile edge in it."""
+    x, dy = rnd(1, tokens, dim, dtype=dtype), rnd(5, tokens, dim, dtype=dtype)
+    wg, wu = (rnd(s, hidden, dim, dtype=dtype, scale=2 * dim ** -0.5) for s in (2, 3))
+    wd = rnd(4, dim, hidden, dtype=dtype, scale=hidden ** -0.5)
+    r = fq.gated_ffn(x, wg, wu, wd, save=True)
+    dx, dwg, dwu, dwd = fq.gated_ffn_backward(dy, x, wg, wu, wd, r)
+    full = [ref.f64(t) for t in (x, wg, wu, wd, dy)]
+    x64, wg64, wu64, wd64, dy64 = full
+    rows = sample(tokens, 128, 1)
+    want = ref.ffn(x64[rows], wg64, wu64, wd64, dy64[rows], "silu", dtype)
+    for name, t in (("y", r.y), ("dx", dx)):
+        v, e = want[name]
+        ref.within(t[rows], v, e + 1e-37, f"{name} {dtype}")
+    cols = sample(hidden, 16, 2)
+    want = ref.ffn(x64, wg64[cols], wu64[cols], wd64[:, cols], dy64, "silu", dtype)
+    for name, t in (("dw_gate", dwg[cols]), ("dw_up", dwu[cols]), ("dw_down", dwd[:, cols])):
+        v, e = want[name]
+        ref.within(t, v, e + 1e-37, f"{name} {dtype}")
