@@ -10,6 +10,8 @@ using namespace qat;
 namespace {
 
 constexpr int64_t kMaxElems = INT64_C(1) << 50;
+// four rows a block of the 4-bit kernel for any shape: what gridDim.x holds
+constexpr int64_t kMaxRows4 = INT64_C(4) * INT32_MAX;
 
 bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool dtype_ok(qat_dtype d) { return d == QAT_F32 || d == QAT_BF16; }
@@ -25,7 +27,7 @@ qat_status check_w4(const qat_weight4* w) {
   if (w->layout != QAT_PER_TENSOR && w->layout != QAT_PER_ROW && w->layout != QAT_PER_GROUP &&
       w->layout != QAT_W4_DOUBLE)
     return QAT_ERR_UNSUPPORTED;
-  if (!fits(w->rows, w->cols)) return QAT_ERR_INVALID_ARGUMENT;
+  if (!fits(w->rows, w->cols) || w->rows > kMaxRows4) return QAT_ERR_INVALID_ARGUMENT;
   if (w->layout == QAT_PER_GROUP && (w->group <= 0 || w->cols % w->group))
     return QAT_ERR_INVALID_ARGUMENT;
   if (w->layout == QAT_W4_DOUBLE && w->zero_points) return QAT_ERR_INVALID_ARGUMENT;

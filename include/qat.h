@@ -447,7 +447,7 @@ qat_status qat_fake_quant_fp8_noalloc(const void* x, qat_dtype dtype, int64_t n,
  *     qat_quant4_double writes them for the flat weight; w = q * (qscale / 255
  *     * super).  scales holds the uint8 qscales, zero_points is NULL.
  * codes 16-byte aligned, the other arrays to their element.  rows * cols up
- * to 2^50.
+ * to 2^50, rows below 2^33 - 3.
  */
 #define QAT_W4_DOUBLE 16
 typedef struct {

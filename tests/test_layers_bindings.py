@@ -176,3 +176,25 @@ def test_layer_norm_of_empty_rows_has_no_statistics(monkeypatch):
     monkeypatch.setattr(torch, "empty", lambda *s, **kw: torch.ones(*s, **kw))
     r = fq.layer_norm(torch.zeros(4, 0))
     assert torch.isnan(r.mean).all() and torch.isnan(r.rstd).all() and r.mean.shape == (4,)
+
+
+def test_more_weight_rows_than_a_grid_holds_are_refused():
+    """The kernel for any shape takes four rows a block: past 2^33 - 4 rows the number
+    of blocks does not fit a launch, and past 2^34 it would wrap to a few."""
+    import ctypes
+
+    from fake_quant_numerics_gb300 import build
+
+    build.build()
+    lib = L.load(build_if_missing=False)
+    at = ctypes.c_void_p(0x10000)
+
+    def call(rows):
+        w = L.Weight4Struct(0x10000, 0x10000, None, None, rows, 1, 0, L.PER_TENSOR)
+        # (no tokens, no workspace: stops at the first check that fails)
+        return (lib.qat_linear4(at, L.F32, 1, ctypes.byref(w), at, None, 0, None),
+                lib.qat_linear4(at, L.F32, 0, ctypes.byref(w), at, None, 0, None))
+
+    assert call((1 << 33) - 4) == (L.QAT_ERR_WORKSPACE, L.QAT_OK)
+    for rows in ((1 << 33) - 3, 1 << 34, (1 << 34) + 8):
+        assert call(rows) == (L.QAT_ERR_INVALID_ARGUMENT,) * 2
