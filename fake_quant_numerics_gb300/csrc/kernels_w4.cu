@@ -161,9 +161,13 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t w, uint32_t bias) {
 }
 // 136 + zp as a bf16 pair (exact)
 __device__ __forceinline__ uint32_t w4_bias(int zp) { return (uint32_t)(0x4308 + zp) * 0x10001u; }
-// 8 bf16 of x, coherently, and free to move among the products (a C++ load is not:
-// 32 fp32 tokens by [14336, 4096] take 132 us in place of 93)
+// 8 bf16 of x.  PLANES: what a kernel of this call may have written, by a coherent
+// load that is free to move among the products (a C++ load is not: 32 fp32 tokens by
+// [14336, 4096] take 132 us in place of 95); else the caller's rows, which nobody
+// writes meanwhile (32 bf16 tokens: 50 us in place of 52).
+template <bool PLANES>
 __device__ __forceinline__ uint4 ld_x(const uint4* p) {
+  if (!PLANES) return __ldg(p);
   uint4 v;
   asm("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
@@ -414,11 +418,14 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) k_w4(const __grid_constant__
 #pragma unroll
   for (int d = 0; d < D; ++d)
     if (d < work) fetch(d);
-  // x may be the previous kernel's output; the weights, which come through the
-  // read-only path, are not.  No load of x moves above this: its address is known here.
+  // Planes may be the previous kernel's output; the weights, which come through the
+  // read-only path, are not.  No load of a plane moves above this: its address is
+  // known here.
   pdl_wait();
+  if (TERMS) {
 #pragma unroll
-  for (int q = 0; q < NT; ++q) asm volatile("" : "+l"(xp[q])::"memory");
+    for (int q = 0; q < NT; ++q) asm volatile("" : "+l"(xp[q])::"memory");
+  }
   int kb = start;
   for (int it = 0; it < work; it += D) {
 #pragma unroll
@@ -466,7 +473,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) k_w4(const __grid_constant__
 #pragma unroll
           for (int q = 0; q < NT; ++q)
 #pragma unroll
-            for (int m = 0; m < kTerms; ++m) b[q][m] = x_pairs<TERMS != 0>(ld_x(xs[q][m] + j));
+            for (int m = 0; m < kTerms; ++m) b[q][m] = x_pairs<TERMS != 0>(ld_x<TERMS != 0>(xs[q][m] + j));
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint32_t a[2][4];
