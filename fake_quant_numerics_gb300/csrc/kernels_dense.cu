@@ -22,15 +22,16 @@
 // the others from whatever follows in the stage; they end in sums of rows that do
 // not exist.
 //
-// Measured at 4096 x 4096 x 14336 (tokens, dim, hidden; repeated calls, power
-// capped): the gated product 590 us (1631 TFLOP/s), the one back 340 (1415, its
-// tiles fill 3.4 waves of 76 pairs), dh 344 (1398, the epilogue reads and writes
-// 12 bytes an element), dx 655 (1469), the three weight gradients 937 (1540);
-// cuBLAS runs plain products at 1708 under the same cap.  fp32 at 2048 x 4096 x
-// 14336: 265 TFLOP/s forward, 236 backward, six bf16 products each.  With one
-// token the weights are read at 4.3 TB/s forward and for dx (128 rows of A in
-// every stage: 3.8; tiles of 96 columns, for fuller waves, moved nothing there and
-// cost 16% at 16 x 1024 x 4096).
+// Measured at 4096 x 4096 x 14336 (tokens, dim, hidden; calls repeated for a second
+// each, power capped): forward 946 us, keeping g and u 980 (1472 TFLOP/s); backward
+// 2019 (1429), of which dw_down 326 (1478) and, by differences, dh 377 (1276, the
+// epilogue reads and writes 12 bytes an element), dx 678 (1419, its tiles fill 3.4
+// waves of 76 pairs) and the other two weight gradients 639 (1506).  cuBLAS, the same
+// way, runs plain products of these shapes at 1738 and 1798.  fp32 at 2048 x 4096 x
+// 14336: 247 TFLOP/s forward, 236 backward, six bf16 products each.  With one token
+// the weights are read at 4.3 TB/s forward and for dx (128 rows of A in every stage:
+// 3.8; tiles of 96 columns, for fuller waves, moved nothing there and cost 16% at 16 x
+// 1024 x 4096).
 
 #include "qat_dense.h"
 #include "qat_layer.cuh"

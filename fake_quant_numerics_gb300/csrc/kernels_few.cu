@@ -10,11 +10,23 @@
 // multiply-adds suffice: 16 tokens cost three quarters of their rate at the copy
 // bandwidth.  a is staged in shared memory; sums are binary32.
 //
-// Measured at dim 4096, hidden 14336 (us, here / on the tensor cores): forward of
-// 1 token 123 / 654 (reading the weights takes 104), 16 tokens 228 / 654, 32
-// tokens 442 / 655, 64 tokens 866 / 658; backward of 1 token 403 / 896, 16 tokens
-// 603 / 877, 32 tokens 924 / 879, 64 tokens 1595 / 885.  From 16 tokens on the
-// multiply-adds bound it.
+// Measured (GPU time of a call in us with a cold L2, here / on the tensor cores):
+//
+//   dim x hidden     tokens  forward      backward
+//   4096 x 14336     16      232 / 657    674 / 955
+//                    17      433 / 658    958 / 955
+//                    32      448 / 658    1011 / 956
+//   1024 x 4096      16      54 / 79      110 / 130
+//                    32      75 / 79      124 / 130
+//   510 x 1363       16      44 / 42      81 / 71
+//                    32      53 / 42      77 / 73
+//
+// One token by 4096 x 14336 takes 123 us forward (reading the weights takes 104).  From
+// 16 tokens on the multiply-adds bound it.  One limit for both passes and all layers:
+// past 16 tokens the backward pass of a large layer loses up to 6% by it, and a layer
+// whose weights are a few MB, where launches are all that counts, up to 27% of one
+// pass; the forward pass of a large layer gains a third to two thirds.
+
 #include "qat_few.h"
 #include "qat_layer.cuh"
 #include "qat_tc.cuh"

@@ -11,7 +11,10 @@
 //
 // Roundings: h is rounded to the layer's type, as the tensor cores take it, and
 // dg and du likewise; g and u are kept in binary32 for the backward pass (a bf16
-// copy would double the error of dg).
+// copy would double the error of dg).  A bf16 layer's outputs are then 0.0023 to
+// 0.0025 of their norm off, where results that are rounded only once are 0.0017 off;
+// two bf16 parts each of h, dg and du would close that, for a third more products
+// forward and five sixths more backward.
 #include "qat_dense.h"
 #include "qat_few.h"
 #include "qat_layer.h"

@@ -151,7 +151,8 @@ struct W4Args {
   int dbl, act, out, y_terms, split;
 };
 
-// two codes of a word (bits 0-3 and 16-19 after the shift) as bf16 q - zp
+// two codes of a word (bits 0-3 and 16-19 after the shift) as bf16 q - zp: the bits of
+// an integer under a fixed exponent are a float (the conversion of arXiv 2211.10017)
 __device__ __forceinline__ uint32_t w4_pair(uint32_t w, uint32_t bias) {
   uint32_t v;
   // (w & 0x000f000f) ^ 0x43084308: bf16 128 + (q + 8)

@@ -10,8 +10,8 @@
 
 namespace qat {
 
-// fp32 layers of this many tokens or fewer take these kernels (measured on both
-// sides in kernels_few.cu)
+// fp32 layers of this many tokens or fewer take these kernels (both sides' times, and
+// where the limit loses, in kernels_few.cu)
 constexpr int64_t kFewTokens = 32;
 
 // h[t, f] = act(x wg^T) * (x wu^T); g and u kept where gp is set

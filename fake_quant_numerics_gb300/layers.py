@@ -191,8 +191,10 @@ def linear4(x: torch.Tensor, weight: Weight4) -> torch.Tensor:
 
 def gated_ffn4(x: torch.Tensor, gate: Weight4, up: Weight4, down: Weight4,
                activation="silu") -> torch.Tensor:
-    """The gated feed-forward block from 4-bit codes: (act(x gate^T) * (x up^T)) down^T,
-    the hidden values kept in float32."""
+    """The gated feed-forward block from 4-bit codes: (act(x gate^T) * (x up^T)) down^T.
+    The hidden values are computed in float32; the second product takes all their 24
+    bits for a float32 x and, unless a weight's shape is off the fast kernel's, 16 of
+    them for a bfloat16 x."""
     shape = x.shape
     if not shape or shape[-1] != gate.cols or down.cols != gate.rows:
         raise _mismatch("gated_ffn4")
