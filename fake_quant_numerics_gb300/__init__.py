@@ -7,7 +7,9 @@ units may also be columns, and calibration takes a clip factor and binary16
 scales; block-scaled floating-point formats (MX with E8M0 scales, NVFP4
 with E4M3 scales under an FP32 tensor scale).  Layer operators use those
 weights: products with 4-bit codes, the gated feed-forward block and layer
-norm, forward and backward.
+norm, forward and backward; attention operators serve a layer from a quantized
+key-value cache: norms of queries and keys with the position rotation (forward and
+backward), cache writes and reads, and the attention of single tokens over it.
 """
 from ._lib import QatError, load  # noqa: F401
 from .api import (DoubleQuantized4Bit, FakeQuantBlock, FakeQuantFp8, FakeQuantInt,  # noqa: F401
@@ -27,3 +29,9 @@ from .layers import (GatedFfn, GatedFfnFunction, LayerNorm, LayerNormFunction, W
                      linear4, qat_gated_ffn, qat_gated_ffn_backward,
                      qat_gated_ffn4, qat_gated_ffn4_workspace_bytes, qat_gated_ffn_workspace_bytes, qat_layer_norm, qat_layer_norm_backward,
                      qat_layer_norm_backward_workspace_bytes, qat_linear4, qat_linear4_workspace_bytes, weight4, weight4_double)
+from .attention import (HeadNormRope, HeadNormRopeFunction, KeysValues, KvAttention, KVCache,  # noqa: F401
+                        head_norm_rope, head_norm_rope_backward, kv_attention, kv_cache, kv_read, kv_write,
+                        qat_head_norm_rope, qat_head_norm_rope_backward,
+                        qat_head_norm_rope_backward_workspace_bytes, qat_kv_attention,
+                        qat_kv_attention_workspace_bytes, qat_kv_read, qat_kv_write, rope_frequencies,
+                        rope_turns)

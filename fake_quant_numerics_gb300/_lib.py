@@ -32,6 +32,8 @@ PER_TENSOR, PER_ROW, PER_GROUP, PER_COLUMN = 0, 1, 2, 3
 E4M3, E5M2 = 0, 1
 W4_DOUBLE = 16
 SILU, GELU, RELU = 0, 1, 2
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+CACHE_BF16, CACHE_INT8, CACHE_INT4, CACHE_E4M3, CACHE_E5M2 = 0, 1, 2, 3, 4
 
 _lib = None
 
@@ -58,6 +60,18 @@ class Weight4Struct(ctypes.Structure):
                 ("zero_points", ctypes.c_void_p), ("super_scales", ctypes.c_void_p),
                 ("rows", _i64), ("cols", _i64), ("group", _i64), ("layout", _int)]
 
+
+class KvCacheStruct(ctypes.Structure):
+    """qat_kv_cache (include/qat.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("k_zero_points", ctypes.c_void_p),
+                ("v_zero_points", ctypes.c_void_p), ("pages", _i64), ("heads", _i64), ("page_size", _i64),
+                ("head_dim", _i64), ("format", _int)]
+
+
+_kv = ctypes.c_void_p  # the address of a KvCacheStruct
+_f32 = ctypes.c_float
+_rope = [_int] + [_i64] * 8 + [_vp, _vp, _i64, _int, _f32, _int, _vp, _vp, _f32]  # dtype ... eps
 
 _w4 = ctypes.c_void_p  # the address of a Weight4Struct (a pointer type would wrap it on every call)
 
@@ -98,6 +112,15 @@ PROTOTYPES = {
     "qat_layer_norm_backward_workspace_bytes": ([_i64, _i64], _sz),
     "qat_layer_norm_backward": ([_vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                  _sz, _vp], _int),
+    "qat_head_norm_rope": ([_vp, _vp] + _rope + [_vp, _vp, _vp], _int),
+    "qat_head_norm_rope_backward_workspace_bytes": ([_i64], _sz),
+    "qat_head_norm_rope_backward": ([_vp] * 4 + _rope + [_vp] * 5 + [_sz, _vp], _int),
+    "qat_kv_row_bytes": ([_int, _i64], _sz),
+    "qat_kv_write": ([_kv, _vp, _vp, _int, _i64, _i64, _i64, _i64, _i64, _vp, _vp], _int),
+    "qat_kv_read": ([_kv, _vp, _i64, _vp, _vp, _int, _vp], _int),
+    "qat_kv_attention_workspace_bytes": ([_kv, _i64], _sz),
+    "qat_kv_attention": ([_vp, _int, _i64, _i64, _i64, _i64, _kv, _vp, _i64, _i64, _vp, _f32, _vp, _vp, _vp, _sz,
+                          _vp], _int),
     "qat_kernel_launch_count": ([], ctypes.c_uint64),
     "qat_debug_set_wait_limit": ([_i64], None),
 }

@@ -22,12 +22,13 @@ SOURCES = ["qat_abi.cu", "kernels_tensor.cu", "kernels_fused.cu", "kernels_fp8.c
            "kernels_misc.cu", "kernels_optim.cu", "kernels_cols.cu", "kernels_pct.cu", "kernels_block.cu", "kernels_onchip.cu",
            "kernels_unaligned.cu", "qat_noalloc.cu",
            "qat_layer_abi.cu", "kernels_w4.cu", "kernels_norm.cu", "kernels_ffn.cu",
-           "kernels_dense.cu", "kernels_few.cu"]
+           "kernels_dense.cu", "kernels_few.cu",
+           "qat_attention_abi.cu", "kernels_rope.cu", "kernels_kvcache.cu", "kernels_kvattn.cu"]
 # sources compiled a second time with QAT_SR=1: their stochastic-rounding
 # kernels and *_sr launchers (object <name>_sr.o)
 SR_SOURCES = ["kernels_tensor.cu", "kernels_fused.cu", "kernels_fp8.cu", "kernels_cols.cu"]
 HEADERS = ["qat_device.cuh", "qat_launch.h", "qat_sr.h", "qat_layer.h", "qat_layer.cuh",
-           "qat_dense.h", "qat_few.h", "qat_tc.cuh"]
+           "qat_dense.h", "qat_few.h", "qat_tc.cuh", "qat_attention.h", "qat_kv.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-fmad=false",
            "-prec-div=true", "-prec-sqrt=true", "-ftz=false", "-I", INCLUDE, "-I", CSRC]

@@ -569,6 +569,146 @@ qat_status qat_layer_norm_backward(const void* dy, const void* x, qat_dtype dtyp
                                    const float* rstd, void* dx, void* dweight, void* dbias,
                                    void* workspace, size_t workspace_bytes, qat_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Attention operators: the other half of a layer that is served from codes.
+ * The conventions of the layer operators hold.
+ */
+
+/*
+ * RMS norm of each head of queries and keys with the position rotation in the
+ * same pass.  Per head x of head_dim elements:
+ *   z = x / sqrt(sum x^2 / head_dim + eps), p = z * weight   (norm = 0: p = x)
+ *   pairs (a, b) of the first rotary_dim elements turn by the token's angle,
+ *     a' = amplitude (a cos - b sin), b' = amplitude (b cos + a sin);
+ *   the other elements pass as they are.
+ * QAT_ROPE_HALF pairs (j, j + rotary_dim / 2), QAT_ROPE_INTERLEAVED (2j, 2j + 1).
+ * Pair j of a token at position t turns by t * turns[j] modulo 2^64, in units of
+ * 2^-64 of a full turn: exact whatever the position (turns[j] is the frequency
+ * over 2 pi, times 2^64).
+ *   q, k: dtype[tokens, heads, head_dim] with the given strides in elements (the
+ *     last one is 1); k may be NULL with k_heads 0.  q_out, k_out: contiguous.
+ *   q_weight, k_weight (nullable: 1): dtype[head_dim]; NULL without norm.
+ *   positions: int64[tokens] (any, negative ones too); turns: uint64[rotary_dim / 2].
+ * head_dim 1 .. 512; rotary_dim even, 0 .. head_dim; eps finite and >= 0;
+ * amplitude finite.  One launch.
+ */
+typedef enum { QAT_ROPE_HALF = 0, QAT_ROPE_INTERLEAVED = 1 } qat_rope_layout;
+
+qat_status qat_head_norm_rope(const void* q, const void* k, qat_dtype dtype, int64_t tokens,
+                              int64_t q_heads, int64_t k_heads, int64_t head_dim,
+                              int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                              int64_t k_head_stride, const int64_t* positions, const uint64_t* turns,
+                              int64_t rotary_dim, qat_rope_layout layout, float amplitude, int norm,
+                              const void* q_weight, const void* k_weight, float eps, void* q_out,
+                              void* k_out, qat_stream_t stream);
+
+/*
+ * Its backward pass from dq_out, dk_out (contiguous) and the forward call's
+ * arguments: with g the gradient turned back (the transposed rotation, amplitude
+ * included), dweight = sum over tokens and heads of g z, and dx = (g weight -
+ * z mean(g weight z)) / sqrt(sum x^2 / head_dim + eps); dx = g without norm.  dq,
+ * dk contiguous; dq, dk, dq_weight, dk_weight are each nullable (weights' with
+ * norm only); weight gradients are summed in a fixed order (the same bits every
+ * call) and are zeros for no tokens or heads.  workspace:
+ * qat_head_norm_rope_backward_workspace_bytes(head_dim) bytes, 16-byte aligned,
+ * when a weight's gradient is asked for.  One launch, two with weight gradients.
+ */
+size_t qat_head_norm_rope_backward_workspace_bytes(int64_t head_dim);
+qat_status qat_head_norm_rope_backward(
+    const void* dq_out, const void* dk_out, const void* q, const void* k, qat_dtype dtype,
+    int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t head_dim, int64_t q_token_stride,
+    int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride, const int64_t* positions,
+    const uint64_t* turns, int64_t rotary_dim, qat_rope_layout layout, float amplitude, int norm,
+    const void* q_weight, const void* k_weight, float eps, void* dq, void* dk, void* dq_weight,
+    void* dk_weight, void* workspace, size_t workspace_bytes, qat_stream_t stream);
+
+/*
+ * A paged cache of keys and values in one of the library's formats.  A position's
+ * slot is page * page_size + offset; its key of one head is a row of head_dim
+ * codes with a scale of its own:
+ *   QAT_CACHE_INT8, QAT_CACHE_INT4: codes, scale and zero point as
+ *     qat_fake_quant_int gives them per row (bits 8 or 4; affine where the cache
+ *     has zero points, held in 8 bits), value (q - zp) * scale;
+ *   QAT_CACHE_E4M3, QAT_CACHE_E5M2: qat_fake_quant_fp8 of the row, value c * scale;
+ *   QAT_CACHE_BF16: the row in bf16; no scales.
+ * A row of zeros has scale 0.  A row with a NaN or an infinity, or whose range
+ * overflows, has scale NaN and code 0: it reads back as NaN (in bf16 as it is).
+ *   k, v: [pages, heads, page_size, row bytes], row bytes = qat_kv_row_bytes
+ *     (whole 16-byte vectors; 4-bit codes two per byte, the even element high;
+ *     padding bytes are 0), 16-byte aligned;
+ *   k_scales, v_scales: float[pages, heads, page_size];
+ *   k_zero_points, v_zero_points (both or neither, integer formats): int8, alike.
+ * head_dim: a multiple of 8 up to 256; page_size: a multiple of 16; pages *
+ * page_size below 2^31; heads up to 65535.
+ */
+typedef enum {
+  QAT_CACHE_BF16 = 0,
+  QAT_CACHE_INT8 = 1,
+  QAT_CACHE_INT4 = 2,
+  QAT_CACHE_E4M3 = 3,
+  QAT_CACHE_E5M2 = 4
+} qat_cache_format;
+
+typedef struct {
+  void *k, *v;
+  float *k_scales, *v_scales;
+  int8_t *k_zero_points, *v_zero_points;
+  int64_t pages, heads, page_size, head_dim;
+  int format;
+} qat_kv_cache;
+
+/* Bytes of a row; 0 for an unknown format or head_dim. */
+size_t qat_kv_row_bytes(int format, int64_t head_dim);
+
+/*
+ * Quantizes the keys and values of `tokens` positions into the cache: k, v are
+ * dtype[tokens, heads, head_dim] with the given strides in elements (the last one
+ * is 1); slots: int64[tokens].  Tokens whose slot lies outside [0, pages *
+ * page_size) are not written; where a slot is given twice it is unspecified which
+ * token's codes and parameters it holds afterwards.  One launch.
+ */
+qat_status qat_kv_write(const qat_kv_cache* cache, const void* k, const void* v, qat_dtype dtype,
+                        int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                        int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,
+                        qat_stream_t stream);
+
+/*
+ * The values of `tokens` cached positions: k, v are dtype[tokens, heads,
+ * head_dim], contiguous and 16-byte aligned, rounded once.  A slot outside [0,
+ * pages * page_size) gives zeros.  One launch.
+ */
+qat_status qat_kv_read(const qat_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k,
+                       void* v, qat_dtype dtype, qat_stream_t stream);
+
+/*
+ * Attention of one new token of each sequence over its cached positions:
+ *   y[b, h] = sum_t p_t v_t,  p = softmax_t(scale * q[b, h] . k_t),  t < lengths[b],
+ * with head h reading the cache's head h / (q_heads / cache heads).
+ *   q: dtype[batch, q_heads, head_dim] with the given strides in elements (the last
+ *     one is 1); y: dtype[batch, q_heads, head_dim], contiguous;
+ *   lse (nullable): float[batch, q_heads], log sum_t exp(scale * q . k_t);
+ *   table: int32[batch, table_cols] with table_stride elements from row to row:
+ *     position t of sequence b lies in page table[b, t / page_size];
+ *   lengths: int32[batch].
+ * Nothing behind a sequence's length is read, nor are table entries behind its
+ * last page.  A length <= 0 gives y = 0 and lse = -inf.  A length that the table's
+ * row cannot hold, or a page outside [0, pages), makes that sequence's outputs NaN.
+ * The codes' products with q are exact and summed in binary32, as are those with
+ * the softmax's weights, which keep 16 bits for a bf16 y and 24 for a float one.
+ * q_heads a multiple of the cache's heads (QAT_ERR_DIMENSION_MISMATCH); scale
+ * finite; batch up to 65535, batch * q_heads and table_cols below 2^31.  workspace:
+ * qat_kv_attention_workspace_bytes(cache, q_heads) bytes, 16-byte aligned: partial
+ * results of sequences that are split, a fixed amount.  The same bits every call.
+ * Two launches.
+ */
+size_t qat_kv_attention_workspace_bytes(const qat_kv_cache* cache, int64_t q_heads);
+qat_status qat_kv_attention(const void* q, qat_dtype dtype, int64_t batch, int64_t q_heads,
+                            int64_t q_batch_stride, int64_t q_head_stride, const qat_kv_cache* cache,
+                            const int32_t* table, int64_t table_cols, int64_t table_stride,
+                            const int32_t* lengths, float scale, void* y, float* lse,
+                            void* workspace, size_t workspace_bytes, qat_stream_t stream);
+
 /* Number of kernels this library has launched in this process (diagnostic). */
 uint64_t qat_kernel_launch_count(void);
 
