@@ -273,7 +273,7 @@ class KVCache:
             if t.dtype != kind:
                 raise TypeError("scales are float32, zero points int8")
         for t in (k, v, k_scale, v_scale, k_zero_point, v_zero_point):
-            if t is not None and (not t.is_contiguous() or (t.dim() == 4 and t.data_ptr() % 16)):
+            if t is not None and (not t.is_contiguous() or t.data_ptr() % 16):
                 raise ValueError("the cache's tensors are contiguous and 16-byte aligned (they are written in place)")
         _on_device(k.device, v, k_scale, v_scale, k_zero_point, v_zero_point)
         self.k, self.v, self.format, self.head_dim = k, v, format, head_dim
@@ -395,7 +395,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, len
 
     scale defaults to head_dim^-0.5.  A length of 0 gives zeros (lse -inf).  Lengths
     that the table cannot hold and pages outside the cache make the sequence's outputs
-    NaN; nothing behind a sequence's length is read."""
+    NaN; what lies behind a sequence's length has no effect."""
     what = "kv_attention"
     if q.dim() != 3 or q.shape[2] != cache.head_dim or q.shape[1] % cache.heads:
         raise _mismatch(what)

@@ -28,7 +28,9 @@ SOURCES = ["qat_abi.cu", "kernels_tensor.cu", "kernels_fused.cu", "kernels_fp8.c
 # kernels and *_sr launchers (object <name>_sr.o)
 SR_SOURCES = ["kernels_tensor.cu", "kernels_fused.cu", "kernels_fp8.cu", "kernels_cols.cu"]
 HEADERS = ["qat_device.cuh", "qat_launch.h", "qat_sr.h", "qat_layer.h", "qat_layer.cuh",
-           "qat_dense.h", "qat_few.h", "qat_tc.cuh", "qat_attention.h", "qat_kv.cuh"]
+           "qat_dense.h", "qat_few.h", "qat_tc.cuh", "qat_attention.h", "qat_kv.cuh", "qat_kvsplit.h"]
+# the attention's split kernel is compiled once for each cache format
+KV_FORMATS = range(5)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-fmad=false",
            "-prec-div=true", "-prec-sqrt=true", "-ftz=false", "-I", INCLUDE, "-I", CSRC]
@@ -56,6 +58,7 @@ def build(verbose: bool = False, extra_flags=()) -> str:
     jobs, objs = [], []
     units = [(src, src.replace(".cu", ".o"), []) for src in SOURCES]
     units += [(src, src.replace(".cu", "_sr.o"), ["-DQAT_SR=1"]) for src in SR_SOURCES]
+    units += [("kernels_kvsplit.cu", f"kernels_kvsplit_{f}.o", [f"-DQAT_KV_FORMAT={f}"]) for f in KV_FORMATS]
     # the longest translation units first, so the parallel build ends sooner
     units.sort(key=lambda u: u[0] != "kernels_fused.cu")
     for src, oname, defs in units:

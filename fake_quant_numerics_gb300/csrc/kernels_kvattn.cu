@@ -1,122 +1,119 @@
-// kernels_kvattn.cu -- attention of one new token of each sequence over a paged,
-// quantized key-value cache.
-//
-//   y = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q . k_t - m),  t < length
-//
-// One block per sequence and query head; its warps take positions in turn, each
-// with a running maximum and sum, and are joined at the end.  A lane holds eight
-// elements of the head.
+// kernels_kvattn.cu -- attention of one new token of each sequence over a paged
+// cache: the split kernel of the cache's format, and the join of what it cut.
 #include <cmath>
 
-#include "qat_attention.h"
 #include "qat_kv.cuh"
+#include "qat_kvsplit.h"
 #include "qat_layer.cuh"
 
 namespace qat {
 namespace {
 
-constexpr int kWarps = 4;
-
-struct CacheView {
-  const char *k, *v;
-  const float *ks, *vs;
-  const int8_t *kz, *vz;
-  int64_t pages;
-  int heads, page_size, d, row_bytes;
-};
-
-template <int F>
-__device__ __forceinline__ void row8(const char* codes, const float* scales, const int8_t* zps,
-                                     int64_t row, int row_bytes, int lane, bool on, float* x) {
-  uint32_t w[4] = {};
-  constexpr int UB = kv_unit_bytes(F) / 2;
-  const char* p = codes + row * row_bytes + lane * UB;
-  if (on) {
-#pragma unroll
-    for (int i = 0; i < UB / 4; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
-  }
-  const float scale = F == QAT_CACHE_BF16 ? 1.0f : scales[row];
-  kv_decode<F, 8>(w, scale, kv_is_int(F) && zps ? zps[row] : 0, x);
-  if (!on) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-  }
-}
-
-template <typename T, int F>
-__global__ void __launch_bounds__(32 * kWarps) k_kv_attn(CacheView c, KvAttnArgs a) {
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][256];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t b = blockIdx.y;
-  const int h = blockIdx.x, kvh = h / (int)(a.q_heads / c.heads);
-  const int64_t length = a.lengths[b];
-  const bool on = 8 * lane < c.d;
-  float q[8], o[8] = {}, m = -INFINITY, l = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    q[e] = on ? ld_elem<T>(a.q, b * a.q_batch_stride + h * a.q_head_stride + 8 * lane + e) : 0.0f;
-  bool bad = length > a.table_cols * c.page_size;
-  for (int64_t t = warp; t < length && !bad; t += kWarps) {
-    const int page = a.table[b * a.table_stride + t / c.page_size];
-    if (page < 0 || page >= c.pages) {
-      bad = true;
-      break;
-    }
-    const int64_t row = ((int64_t)page * c.heads + kvh) * c.page_size + t % c.page_size;
-    float k[8], v[8], s = 0.0f;
-    row8<F>(c.k, c.ks, c.kz, row, c.row_bytes, lane, on, k);
-    row8<F>(c.v, c.vs, c.vz, row, c.row_bytes, lane, on, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s = __fmaf_rn(q[e], k[e], s);
-    for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(kFull, s, i);
-    s *= a.scale;
-    const float top = fmaxf(m, s);
-    const float was = m == top ? 1.0f : expf(m - top), p = s == top ? 1.0f : expf(s - top);
-    m = top;
-    l = __fmaf_rn(l, was, p);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = __fmaf_rn(o[e], was, __fmul_rn(p, v[e]));
-  }
-  if (lane == 0) s_m[warp] = m, s_l[warp] = bad ? NAN : l;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) s_o[warp][8 * lane + e] = o[e];
-  __syncthreads();
-  float top = -INFINITY, sum = 0.0f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-  for (int w = 0; w < kWarps; ++w)
-    if (s_m[w] > -INFINITY || s_l[w] != 0.0f) sum += s_l[w] * expf(s_m[w] - top);
-  for (int e = threadIdx.x; e < c.d; e += 32 * kWarps) {
-    float y = 0.0f;
-    for (int w = 0; w < kWarps; ++w)
-      if (s_m[w] > -INFINITY || s_l[w] != 0.0f) y += s_o[w][e] * expf(s_m[w] - top);
-    if (sum != 0.0f) y /= sum;
-    st_elem<T>(a.y, (b * a.q_heads + h) * c.d + e, y);
-  }
-  if (a.lse && threadIdx.x == 0) a.lse[b * a.q_heads + h] = sum == 0.0f ? -INFINITY : top + logf(sum);
-}
+// One block for each block of the split kernel: where that one's last piece was cut
+// off by the end of its run, the parts - its second slot, then the first slots of
+// the blocks behind it - are added in that order.  A warp takes a head and every
+// eighth... part; four warps a head.
+constexpr int kJoinWarps = 32;
 
 template <typename T>
-qat_status launch_any(const qat_kv_cache& c, const KvAttnArgs& a, cudaStream_t s) {
-  const CacheView v = {(const char*)c.k, (const char*)c.v, c.k_scales, c.v_scales, c.k_zero_points,
-                       c.v_zero_points, c.pages, (int)c.heads, (int)c.page_size, (int)c.head_dim,
-                       (int)kv_row_bytes(c.format, c.head_dim)};
-  auto k = k_kv_attn<T, QAT_CACHE_BF16>;
-  if (c.format == QAT_CACHE_INT8) k = k_kv_attn<T, QAT_CACHE_INT8>;
-  if (c.format == QAT_CACHE_INT4) k = k_kv_attn<T, QAT_CACHE_INT4>;
-  if (c.format == QAT_CACHE_E4M3) k = k_kv_attn<T, QAT_CACHE_E4M3>;
-  if (c.format == QAT_CACHE_E5M2) k = k_kv_attn<T, QAT_CACHE_E5M2>;
-  k<<<dim3((unsigned)a.q_heads, (unsigned)a.batch), 32 * kWarps, 0, s>>>(v, a);
-  count_launch(1);
-  return launch_status();
+__global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join(SplitWs ws, KvAttnArgs a, int kv_heads,
+                                                             int d, int group, int tiles, int tile) {
+  extern __shared__ float share[];  // [kJoinWarps][d], then the warps' sums
+  pdl_wait();
+  const int4 cut = ws.cut[blockIdx.x];
+  if (cut.z == 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int kvh = cut.y / tiles, h0 = kvh * group + (cut.y - kvh * tiles) * tile;
+  const int heads = min(tile, (kvh + 1) * group - h0);
+  auto slot = [&](int part) {
+    return ((int64_t)(blockIdx.x + part) * 2 + (part == 0)) * tile;
+  };
+  float* const sums = share + kJoinWarps * d;
+  for (int base = 0; base < heads; base += 8) {
+    const int h = base + (warp & 7), first = warp >> 3;
+    float top = -INFINITY, sum = 0.0f;
+    if (h < heads) {
+      for (int p = lane; p < cut.z; p += 32) top = fmaxf(top, ws.ml[slot(p) + h].x);
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      float y[8] = {};
+#pragma unroll 4
+      for (int p = first; p < cut.z; p += kJoinWarps / 8) {
+        const float2 ml = ws.ml[slot(p) + h];
+        const float f = ml.x == top ? 1.0f : exp2f(ml.x - top);
+        sum = __fmaf_rn(f, ml.y, sum);
+        const float* from = ws.o + (slot(p) + h) * d;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (4 * (lane + 32 * i) < d) {
+            const float4 v = *reinterpret_cast<const float4*>(from + 4 * (lane + 32 * i));
+            y[4 * i] = __fmaf_rn(f, v.x, y[4 * i]);
+            y[4 * i + 1] = __fmaf_rn(f, v.y, y[4 * i + 1]);
+            y[4 * i + 2] = __fmaf_rn(f, v.z, y[4 * i + 2]);
+            y[4 * i + 3] = __fmaf_rn(f, v.w, y[4 * i + 3]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = 4 * (lane + 32 * (i / 4)) + i % 4;
+        if (e < d) share[warp * d + e] = y[i];
+      }
+      if (lane == 0) sums[warp] = sum;
+    }
+    __syncthreads();
+    if (h < heads && first == 0) {
+      sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; w += 8) sum += sums[(warp & 7) + w];
+      const int64_t row = (int64_t)cut.x * a.q_heads + h0 + h;
+      for (int e = lane; e < d; e += 32) {
+        float y = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; w += 8) y += share[((warp & 7) + w) * d + e];
+        st_elem<T>(a.y, row * d + e, sum == 0.0f ? 0.0f : __fdiv_rn(y, sum));
+      }
+      if (lane == 0 && a.lse)
+        a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+    }
+    __syncthreads();
+  }
 }
+
+constexpr size_t kCutBytes = kSplitBlocks * sizeof(int4);
+size_t ml_bytes(int tile) { return (size_t)kSplitBlocks * 2 * tile * sizeof(float2); }
 
 }  // namespace
 
-size_t kv_attn_ws_bytes(int64_t, int64_t, int64_t) { return 16; }
+size_t kv_attn_ws_bytes(int64_t q_heads, int64_t kv_heads, int64_t d) {
+  const int tile = head_tiles(q_heads, kv_heads, d, false).tile;  // (the larger of both types)
+  return kCutBytes + ml_bytes(tile) + (size_t)kSplitBlocks * 2 * tile * (size_t)d * 4;
+}
 
-qat_status launch_kv_attn(const qat_kv_cache& c, const KvAttnArgs& a, qat_dtype dt, void*,
+qat_status launch_kv_attn(const qat_kv_cache& c, const KvAttnArgs& a, qat_dtype dt, void* ws,
                           cudaStream_t s) {
-  return dt == QAT_F32 ? launch_any<F32>(c, a, s) : launch_any<BF16>(c, a, s);
+  const KvCacheView v = {(const char*)c.k, (const char*)c.v, c.k_scales, c.v_scales, c.k_zero_points,
+                         c.v_zero_points, c.pages, (int)c.heads, (int)c.page_size, (int)c.head_dim,
+                         (int)kv_row_bytes(c.format, c.head_dim)};
+  const HeadTiles t = head_tiles(a.q_heads, c.heads, c.head_dim, dt == QAT_F32);
+  char* p = static_cast<char*>(ws);
+  const SplitWs w = {reinterpret_cast<int4*>(p), reinterpret_cast<float2*>(p + kCutBytes),
+                     reinterpret_cast<float*>(p + kCutBytes + ml_bytes(t.tile))};
+  int grid = 0;
+  qat_status st;
+  switch (c.format) {
+    case QAT_CACHE_INT8: st = launch_kv_split<QAT_CACHE_INT8>(v, a, dt, w, &grid, s); break;
+    case QAT_CACHE_INT4: st = launch_kv_split<QAT_CACHE_INT4>(v, a, dt, w, &grid, s); break;
+    case QAT_CACHE_E4M3: st = launch_kv_split<QAT_CACHE_E4M3>(v, a, dt, w, &grid, s); break;
+    case QAT_CACHE_E5M2: st = launch_kv_split<QAT_CACHE_E5M2>(v, a, dt, w, &grid, s); break;
+    default: st = launch_kv_split<QAT_CACHE_BF16>(v, a, dt, w, &grid, s);
+  }
+  if (st) return st;
+  const auto k = dt == QAT_F32 ? k_kv_join<F32> : k_kv_join<BF16>;
+  const size_t smem = (size_t)kJoinWarps * (c.head_dim + 1) * 4;
+  if (launch_kernel(k, dim3(grid), dim3(32 * kJoinWarps), smem, s, true, w, a, (int)c.heads,
+                    (int)c.head_dim, t.group, t.tiles, t.tile) != cudaSuccess)
+    return QAT_ERR_CUDA;
+  count_launch(1);
+  return QAT_OK;
 }
 
 }  // namespace qat

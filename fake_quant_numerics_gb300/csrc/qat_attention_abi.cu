@@ -75,7 +75,8 @@ qat_status check_cache(const qat_kv_cache* c) {
   if (c->pages == 0) return QAT_OK;
   if (!c->k || !c->v || (f != QAT_CACHE_BF16 && (!c->k_scales || !c->v_scales)))
     return QAT_ERR_INVALID_ARGUMENT;
-  if (!on(c->k, 16) || !on(c->v, 16) || !on(c->k_scales, 4) || !on(c->v_scales, 4))
+  if (!on(c->k, 16) || !on(c->v, 16) || !on(c->k_scales, 16) || !on(c->v_scales, 16) ||
+      !on(c->k_zero_points, 16) || !on(c->v_zero_points, 16))
     return QAT_ERR_MISALIGNED;
   return QAT_OK;
 }

@@ -636,9 +636,10 @@ qat_status qat_head_norm_rope_backward(
  * overflows, has scale NaN and code 0: it reads back as NaN (in bf16 as it is).
  *   k, v: [pages, heads, page_size, row bytes], row bytes = qat_kv_row_bytes
  *     (whole 16-byte vectors; 4-bit codes two per byte, the even element high;
- *     padding bytes are 0), 16-byte aligned;
+ *     padding bytes are 0; FP8 codes are finite);
  *   k_scales, v_scales: float[pages, heads, page_size];
- *   k_zero_points, v_zero_points (both or neither, integer formats): int8, alike.
+ *   k_zero_points, v_zero_points (both or neither, integer formats): int8, alike;
+ *   all 16-byte aligned.
  * head_dim: a multiple of 8 up to 256; page_size: a multiple of 16; pages *
  * page_size below 2^31; heads up to 65535.
  */
@@ -691,9 +692,10 @@ qat_status qat_kv_read(const qat_kv_cache* cache, const int64_t* slots, int64_t 
  *   table: int32[batch, table_cols] with table_stride elements from row to row:
  *     position t of sequence b lies in page table[b, t / page_size];
  *   lengths: int32[batch].
- * Nothing behind a sequence's length is read, nor are table entries behind its
- * last page.  A length <= 0 gives y = 0 and lse = -inf.  A length that the table's
- * row cannot hold, or a page outside [0, pages), makes that sequence's outputs NaN.
+ * What lies behind a sequence's length has no effect, whatever it is, and table
+ * entries behind its last page are not read.  A length <= 0 gives y = 0 and lse =
+ * -inf.  A length that the table's row cannot hold or that is above 2^31 - 1025, or a
+ * page outside [0, pages), makes that sequence's outputs NaN.
  * The codes' products with q are exact and summed in binary32, as are those with
  * the softmax's weights, which keep 16 bits for a bf16 y and 24 for a float one.
  * q_heads a multiple of the cache's heads (QAT_ERR_DIMENSION_MISMATCH); scale
