@@ -9,73 +9,62 @@
 namespace qat {
 namespace {
 
-// One block for each block of the split kernel: where that one's last piece was cut
-// off by the end of its run, the parts - its second slot, then the first slots of
-// the blocks behind it - are added in that order.  A warp takes a head and every
-// eighth... part; four warps a head.
-constexpr int kJoinWarps = 32;
+// For each block of the split kernel (x) whose end cut a sequence off, a query head of
+// it (y): the parts - the block's second slot, then the first slots of the blocks
+// behind it - are added in that order within each of four warps, every fourth one a
+// warp's, and then over the warps.
+constexpr int kJoinWarps = 4;
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join(SplitWs ws, KvAttnArgs a, int kv_heads,
-                                                             int d, int group, int tiles, int tile) {
-  extern __shared__ float share[];  // [kJoinWarps][d], then the warps' sums
+__global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join(SplitWs ws, KvAttnArgs a, int d,
+                                                             int group, int tiles, int tile) {
+  __shared__ __align__(16) float share[kJoinWarps][256];
+  __shared__ float sums[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
   pdl_wait();
   const int4 cut = ws.cut[blockIdx.x];
-  if (cut.z == 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int kvh = cut.y / tiles, h0 = kvh * group + (cut.y - kvh * tiles) * tile;
-  const int heads = min(tile, (kvh + 1) * group - h0);
+  if (cut.z == 0 || h >= min(tile, (kvh + 1) * group - h0)) return;
   auto slot = [&](int part) {
-    return ((int64_t)(blockIdx.x + part) * 2 + (part == 0)) * tile;
+    return ((int64_t)(blockIdx.x + part) * 2 + (part == 0)) * tile + h;
   };
-  float* const sums = share + kJoinWarps * d;
-  for (int base = 0; base < heads; base += 8) {
-    const int h = base + (warp & 7), first = warp >> 3;
-    float top = -INFINITY, sum = 0.0f;
-    if (h < heads) {
-      for (int p = lane; p < cut.z; p += 32) top = fmaxf(top, ws.ml[slot(p) + h].x);
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-      float y[8] = {};
+  float top = -INFINITY, sum = 0.0f, y[8] = {};
+  for (int p = lane; p < cut.z; p += 32) top = fmaxf(top, ws.ml[slot(p)].x);
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
 #pragma unroll 4
-      for (int p = first; p < cut.z; p += kJoinWarps / 8) {
-        const float2 ml = ws.ml[slot(p) + h];
-        const float f = ml.x == top ? 1.0f : exp2f(ml.x - top);
-        sum = __fmaf_rn(f, ml.y, sum);
-        const float* from = ws.o + (slot(p) + h) * d;
+  for (int p = warp; p < cut.z; p += kJoinWarps) {
+    const float2 ml = ws.ml[slot(p)];
+    const float f = ml.x == top ? 1.0f : exp2f(ml.x - top);
+    sum = __fmaf_rn(f, ml.y, sum);
+    const float* from = ws.o + slot(p) * d;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (4 * (lane + 32 * i) < d) {
-            const float4 v = *reinterpret_cast<const float4*>(from + 4 * (lane + 32 * i));
-            y[4 * i] = __fmaf_rn(f, v.x, y[4 * i]);
-            y[4 * i + 1] = __fmaf_rn(f, v.y, y[4 * i + 1]);
-            y[4 * i + 2] = __fmaf_rn(f, v.z, y[4 * i + 2]);
-            y[4 * i + 3] = __fmaf_rn(f, v.w, y[4 * i + 3]);
-          }
+    for (int i = 0; i < 2; ++i)
+      if (4 * (lane + 32 * i) < d) {
+        const float4 v = *reinterpret_cast<const float4*>(from + 4 * (lane + 32 * i));
+        y[4 * i] = __fmaf_rn(f, v.x, y[4 * i]);
+        y[4 * i + 1] = __fmaf_rn(f, v.y, y[4 * i + 1]);
+        y[4 * i + 2] = __fmaf_rn(f, v.z, y[4 * i + 2]);
+        y[4 * i + 3] = __fmaf_rn(f, v.w, y[4 * i + 3]);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = 4 * (lane + 32 * (i / 4)) + i % 4;
-        if (e < d) share[warp * d + e] = y[i];
-      }
-      if (lane == 0) sums[warp] = sum;
-    }
-    __syncthreads();
-    if (h < heads && first == 0) {
-      sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kJoinWarps; w += 8) sum += sums[(warp & 7) + w];
-      const int64_t row = (int64_t)cut.x * a.q_heads + h0 + h;
-      for (int e = lane; e < d; e += 32) {
-        float y = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; w += 8) y += share[((warp & 7) + w) * d + e];
-        st_elem<T>(a.y, row * d + e, sum == 0.0f ? 0.0f : __fdiv_rn(y, sum));
-      }
-      if (lane == 0 && a.lse)
-        a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
-    }
-    __syncthreads();
   }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    *reinterpret_cast<float4*>(&share[warp][4 * (lane + 32 * i)]) =
+        make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+  if (lane == 0) sums[warp] = sum;
+  __syncthreads();
+  sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) sum += sums[w];
+  const int64_t row = (int64_t)cut.x * a.q_heads + h0 + h;
+  for (int e = threadIdx.x; e < d; e += 32 * kJoinWarps) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) v += share[w][e];
+    st_elem<T>(a.y, row * d + e, sum == 0.0f ? 0.0f : __fdiv_rn(v, sum));
+  }
+  if (threadIdx.x == 0 && a.lse)
+    a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
 constexpr size_t kCutBytes = kSplitBlocks * sizeof(int4);
@@ -108,9 +97,8 @@ qat_status launch_kv_attn(const qat_kv_cache& c, const KvAttnArgs& a, qat_dtype 
   }
   if (st) return st;
   const auto k = dt == QAT_F32 ? k_kv_join<F32> : k_kv_join<BF16>;
-  const size_t smem = (size_t)kJoinWarps * (c.head_dim + 1) * 4;
-  if (launch_kernel(k, dim3(grid), dim3(32 * kJoinWarps), smem, s, true, w, a, (int)c.heads,
-                    (int)c.head_dim, t.group, t.tiles, t.tile) != cudaSuccess)
+  if (launch_kernel(k, dim3(grid, t.tile), dim3(32 * kJoinWarps), 0, s, true, w, a, (int)c.head_dim,
+                    t.group, t.tiles, t.tile) != cudaSuccess)
     return QAT_ERR_CUDA;
   count_launch(1);
   return QAT_OK;

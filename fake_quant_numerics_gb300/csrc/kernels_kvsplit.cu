@@ -6,20 +6,25 @@
 //
 // The floor is reading the codes once.  The query heads of a cache head share a
 // read: they are the eight columns of m16n8k16 products whose rows are positions
-// (scores) or head elements (values), both operands' codes exact in bf16.
+// (scores) or head elements (values).  Codes are exact in fp16, which takes fewer
+// operations to reach than bf16 (a code is the low bits of a number of exponent 10;
+// FP8 converts), so quantized rows are multiplied in fp16: queries and weights are
+// first scaled by powers of two, so that their largest values lie near the top of its
+// range and what falls below it is 2^-38 of them.  bf16 rows are multiplied in bf16.
 //
-// Work is cut evenly whatever the lengths: the blocks of kBlockKeys positions of
-// every (sequence, head group), in one row, are dealt to the resident blocks in
-// equal runs.  A run that starts or ends inside a sequence leaves a partial result
-// (maximum, sum, weighted values), joined in order by k_kv_join.
+// Work is cut evenly whatever the lengths: the tiles of 16 positions of every
+// (sequence, head group), in one row, are dealt to the resident warps in equal runs.
+// A run that starts or ends inside a sequence leaves a part (maximum, sum, weighted
+// values): a block joins what its warps, whose runs follow each other, hold of the same
+// sequence, and k_kv_join the rest.  Until then warps share nothing, so that the start
+// and the end of a piece, a few latencies each, pass behind the others' work; what they
+// cost a warp counts as kPieceTiles tiles when the runs are cut.
 //
-// A warp takes every fourth tile of its block's run, with a maximum, a sum and
-// weighted values of its own, joined over the block's warps where a sequence's
-// piece ends.  Each lane copies exactly the codes that it multiplies (cp.async into
-// slots of its own), so that only scales are exchanged between lanes: rows of the
-// product are positions lane / 4 (+ 8) for keys, and the lane's share of a key is
-// every fourth 16-byte run; of a value every eighth.  Which head element a product's
-// k index stands for is free, so the codes' own order is taken for both operands.
+// Each lane copies exactly the codes that it multiplies (cp.async into slots of its
+// own), so that only scales are exchanged between lanes: rows of a product are
+// positions lane / 4 (+ 8) for keys, and the lane's share of a key is every fourth
+// 16-byte run; of a value every eighth.  Which head element a product's k index
+// stands for is free, so the codes' own order is taken for both operands.
 #include <cmath>
 
 #include "qat_kv.cuh"
@@ -30,8 +35,9 @@ namespace qat {
 namespace {
 
 constexpr int kFormat = QAT_KV_FORMAT;
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kPieceTiles = 4;  // what a piece costs beside its tiles, in tiles
+constexpr int kLeastRun = 2;    // tiles of a run at least
 constexpr float kSlack = 8.0f;  // scores may exceed the running maximum by 2^8 before it moves
 
 // ---------------------------------------------------------------------------
@@ -40,9 +46,18 @@ constexpr float kSlack = 8.0f;  // scores may exceed the running maximum by 2^8 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
-// `bytes` (4, 8 or 16) from global to shared memory, or zeros
+// 4, 8 or 16 bytes from global to shared memory
 template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool on) {
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
+                 : "memory");
+}
+// the same, or zeros
+template <int BYTES>
+__device__ __forceinline__ void copy_async_if(uint32_t dst, const void* src, bool on) {
   const int n = on ? BYTES : 0;
   if constexpr (BYTES == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
@@ -57,12 +72,36 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+template <bool HALF>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  if constexpr (HALF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The next 16-bit parts of two numbers, packed; they keep the remainders.
+template <bool HALF>
+__device__ __forceinline__ uint32_t take_pair(float& x, float& y) {
+  if constexpr (HALF) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&r));
+    x -= v.x, y -= v.y;
+    return r;
+  } else {
+    const uint32_t r = pack_bf16x2(x, y);
+    x -= __uint_as_float(r << 16);
+    y -= __uint_as_float(r & 0xffff0000u);
+    return r;
+  }
 }
 // an 8 x 8 matrix of 16-bit elements, transposed over the warp
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -90,49 +129,69 @@ __device__ __forceinline__ void load_run(const char* p, uint32_t (&w)[BYTES / 4]
 }
 
 // ---------------------------------------------------------------------------
-// codes: the pairs of bf16 that a 32-bit word holds, in the order of its bits
+// codes: the pairs of fp16 (or bf16) that a 32-bit word holds, in the order in which
+// they are cheapest to reach
 // ---------------------------------------------------------------------------
 template <int F>
 struct Word {
+  static constexpr bool kHalf = F != QAT_CACHE_BF16;
+  static constexpr bool kFp8 = F == QAT_CACHE_E4M3 || F == QAT_CACHE_E5M2;
   static constexpr int CODES = F == QAT_CACHE_INT4 ? 8 : F == QAT_CACHE_BF16 ? 2 : 4;
   static constexpr int PAIRS = CODES / 2;
-  // the elements of pair i: `lo` in the low half, HALF elements on the one in the high
-  static constexpr int HALF = CODES / 2;
-  __host__ __device__ static constexpr int lo(int i) { return F == QAT_CACHE_INT4 ? i ^ 1 : i; }
+  // Keys: the places of pair i's halves in the word.  Integer codes lie 16 bits apart.
+  __host__ __device__ static constexpr int lo(int i) {
+    return kFp8 ? 2 * i : F == QAT_CACHE_INT4 ? i ^ 1 : i;
+  }
+  __host__ __device__ static constexpr int hi(int i) { return kFp8 ? 2 * i + 1 : lo(i) + PAIRS; }
+  // Values: words of two positions are first brought together, one half (0, 1) of each
+  // at a time, so that a pair is the same element of both.
+  static constexpr uint32_t kLower = kFp8 ? 0x5140 : 0x5410, kUpper = kFp8 ? 0x7362 : 0x7632;
+  // element c of the word among the pairs of both halves
+  __host__ __device__ static constexpr int rank(int c) {
+    return F == QAT_CACHE_INT4 ? c ^ 1 : c;
+  }
 
   __device__ __forceinline__ static void decode(uint32_t w, uint32_t (&out)[PAIRS]) {
     if constexpr (F == QAT_CACHE_BF16) {
       out[0] = w;
     } else if constexpr (F == QAT_CACHE_INT4) {
-      // 128 + (q + 8) in bf16, less 136
+      // a low nibble is 1024 + (q + 8), less 1032; a high one 1024 + 16 (q + 8), by 1/16, less 72
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        out[i] = sub2(((w >> (4 * i)) & 0x000f000fu) ^ 0x43084308u, 0x43084308u);
+      for (int i = 0; i < 4; i += 2) {
+        const uint32_t x = w >> (4 * i);
+        out[i] = sub2(pick(x, 0x000f000fu, 0x64086408u), 0x64086408u);
+        out[i + 1] = fma2(pick(x, 0x00f000f0u, 0x64806480u), 0x2c002c00u, 0xd480d480u);
+      }
     } else if constexpr (F == QAT_CACHE_INT8) {
-      // 128 + the low seven bits, less 128 or, where the sign is set, 256
+      // 1024 + (q + 128), less 1152
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        out[i] = sub2(pick(w >> (8 * i), 0x00ff00ffu, 0x64806480u), 0x64806480u);
+    } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t x = w >> (8 * i);
-        out[i] = sub2((x & 0x007f007fu) | 0x43004300u, (x & 0x00800080u) | 0x43004300u);
+        const uint16_t x = (uint16_t)(w >> (16 * i));
+        if (F == QAT_CACHE_E4M3)
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(out[i]) : "h"(x));
+        else
+          asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(out[i]) : "h"(x));
       }
-    } else {
-      // the code's exponent and fraction at bf16's place, times 2^(127 - bias); codes
-      // are finite, as the cache's rows are written
-      constexpr int SH = F == QAT_CACHE_E4M3 ? 4 : 3;
-      constexpr uint32_t M = F == QAT_CACHE_E4M3 ? 0x07f007f0u : 0x0fe00fe0u;
-      constexpr uint32_t UP = F == QAT_CACHE_E4M3 ? 0x7b807b80u : 0x77807780u;  // 2^120, 2^112
-      out[0] = mul2(((w << (8 - SH)) & M) | ((w << 8) & 0x80008000u), UP);
-      out[1] = mul2(((w >> SH) & M) | (w & 0x80008000u), UP);
     }
+  }
+  // (w & mask) ^ bits in one operation
+  __device__ __forceinline__ static uint32_t pick(uint32_t w, uint32_t mask, uint32_t bits) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
+    return r;
   }
   __device__ __forceinline__ static uint32_t sub2(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
   }
-  __device__ __forceinline__ static uint32_t mul2(uint32_t a, uint32_t b) {
+  __device__ __forceinline__ static uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
   }
 };
@@ -141,7 +200,6 @@ struct Word {
 // shapes: DP the head dimension the products take (64, 128, 256; elements behind
 // head_dim are zeros), HT tiles of eight query heads
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ int smaller_of(int a, int b) { return a < b ? a : b; }
 constexpr int smaller(int a, int b) { return a < b ? a : b; }
 constexpr int larger(int a, int b) { return a > b ? a : b; }
 
@@ -150,72 +208,119 @@ struct Shape {
   using W = Word<F>;
   static constexpr bool kF32 = T::BYTES == 4;
   static constexpr int ROW = DP / W::CODES * 4;  // bytes of a row of DP codes
-  // a lane's share of a key: NK runs of CK bytes, every fourth one; of a value NV of
-  // CV bytes, every eighth
+  // a lane's share of a key: NK runs of CK bytes (EK codes), every fourth one; of a
+  // value NV of CV bytes (EV codes), every eighth
   static constexpr int CK = smaller(16, ROW / 4), NK = ROW / 4 / CK, EK = CK / 4 * W::CODES;
   static constexpr int CV = smaller(16, ROW / 8), NV = ROW / 8 / CV, EV = CV / 4 * W::CODES;
   static constexpr int TILE = 32 * ROW;  // 16 keys and values
-  static constexpr int PARAMS = kFormat == QAT_CACHE_BF16 ? 0 : 160;  // 16 scales each, 16 zero points each
+  // 16 scales and 16 zero points of both
+  static constexpr int PARAMS = F == QAT_CACHE_BF16 ? 0 : 160;
   static constexpr int NT = smaller(2, larger(1, 4096 / TILE));  // tiles a step
-  static constexpr int STAGES = TILE > 8192 ? 2 : TILE > 4096 ? 3 : 4;
+  static constexpr int STAGES = TILE > 4096 ? 2 : 3;
   static constexpr int STAGE = NT * (TILE + PARAMS);
-  static constexpr int RING = kWarps * STAGES * STAGE;
-  static constexpr int KEYS = kWarps * NT * 16;  // a block's step
   static constexpr int H = 8 * HT, KS = DP / 16, MT = DP / 16;
-  static constexpr int QP = kF32 ? 3 : 1, PP = kF32 ? 3 : 2;  // bf16 parts of q and of the weights
-  static constexpr int OPAD = DP + 4;
-  static constexpr int JOIN = kWarps * H * OPAD * 4;  // (reuses the ring)
-  static constexpr int QRAW = H * (DP + 1) * 4;       // (likewise)
-  static constexpr int BODY = larger(larger(RING, JOIN), QRAW);
+  static constexpr int QP = kF32 ? 3 : 1, PP = kF32 ? 3 : 2;  // 16-bit parts of q and of the weights
   static constexpr int QFRAG = kF32 ? QP * KS * 32 * 8 : 0;
-  static constexpr int ML = kWarps * H * 3 * 4;
-  static constexpr int SMEM = (BODY + 15) / 16 * 16 + QFRAG + ML;
+  // A warp's ring and queries, then the part it starts with (its run began inside a
+  // sequence); the part it ends with takes the ring's place.
+  static constexpr int PART = H * DP * 4;
+  static constexpr int RING = larger(STAGES * STAGE + QFRAG, PART), WARP = RING + PART;
+  // Registers hold twelve warps of up to 168, eight of up to 255.
+  static constexpr int WARPS =
+      smaller(224 * 1024 / WARP, DP * HT <= 128 && !kF32 ? 12 : 8);
+  static constexpr int THREADS = 32 * WARPS, SMEM = WARPS * WARP;
 
-  // The head element of half `hi` of pair p of lane t's share of a key.
-  __device__ __forceinline__ static int key_elem(int p, int hi, int t) {
-    const int word = p / W::PAIRS, i = p % W::PAIRS, run = word / (CK / 4);
-    return (4 * run + t) * EK + (word % (CK / 4)) * W::CODES + W::lo(i) + hi * W::HALF;
+  // Pair p of a run of a key: the place of its halves in the run.
+  __host__ __device__ static constexpr int key_place(int p, int hi) {
+    return p / W::PAIRS * W::CODES + (hi ? W::hi(p % W::PAIRS) : W::lo(p % W::PAIRS));
   }
-  // The place of head element e in the order of the value products' rows: eight
-  // lanes side by side, pairs in the order in which they are decoded.
-  __device__ __forceinline__ static int value_place(int e) {
-    const int chunk = e / EV, g = chunk % 8, run = chunk / 8, in = e % EV;
-    const int word = run * (CV / 4) + in / W::CODES, c = in % W::CODES;
-    const int half = c / W::HALF, i = W::lo(c % W::HALF);  // (lo is its own inverse)
-    return ((word * 2 + half) * W::PAIRS + i) * 8 + g;
+  // Element e of run j of a value: its place among the rows of the products (even
+  // and odd ones are rows g and g + 8 of a tile).
+  __host__ __device__ static constexpr int value_place(int j, int e) {
+    return (j * (CV / 4) + e / W::CODES) * W::CODES + W::rank(e % W::CODES);
   }
 };
 
-struct Piece {  // blocks [from, to) of `blocks` of sequence b's head group hg
-  int b, hg, from, to, blocks;
-};
+// Eight consecutive elements of q or y.
+template <typename T>
+__device__ __forceinline__ void load8(const void* x, int64_t at, bool vec, float* v) {
+  if (!vec) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = ld_elem<T>(x, at + e);
+  } else if constexpr (T::BYTES == 2) {
+    const uint4 r = *reinterpret_cast<const uint4*>(static_cast<const char*>(x) + 2 * at);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = __uint_as_float(w[e] << 16);
+      v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const char*>(x) + 4 * at);
+    const float4 a = p[0], b = p[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(void* x, int64_t at, bool vec, const float* v) {
+  if (!vec) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) st_elem<T>(x, at + e, v[e]);
+  } else if constexpr (T::BYTES == 2) {
+    *reinterpret_cast<uint4*>(static_cast<char*>(x) + 2 * at) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                   pack_bf16x2(v[6], v[7]));
+  } else {
+    float4* p = reinterpret_cast<float4*>(static_cast<char*>(x) + 4 * at);
+    p[0] = make_float4(v[0], v[1], v[2], v[3]);
+    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
 
-template <typename T, int F, int DP, int HT>
-__global__ void __launch_bounds__(kThreads, DP * HT <= 128 && T::BYTES == 2 ? 3 : 2)
-    k_kv_split(KvCacheView c, KvAttnArgs a, int group, int tiles, SplitWs ws) {
+// The exponent of the power of two at or below x (0 for 0 and what is not finite).
+__device__ __forceinline__ int exponent_of(float x) {
+  const int e = (int)(__float_as_uint(x) >> 23 & 255u);
+  return e == 0 || e == 255 ? 0 : e - 127;
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// EXACT: rows of exactly DP codes.
+template <typename T, int F, int DP, int HT, bool EXACT>
+__global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
+    k_kv_split(KvCacheView c, KvAttnArgs a, int group, int tiles, bool q_vec, bool y_vec,
+               SplitWs ws) {
   using S = Shape<T, F, DP, HT>;
   using W = typename S::W;
+  constexpr int WARPS = S::WARPS, H = S::H;
+  constexpr bool HALF = W::kHalf;
   extern __shared__ __align__(16) char smem[];
-  __shared__ int64_t s_sum[kWarps + 1];
-  __shared__ int s_at[3];
+  __shared__ int64_t s_sum[WARPS], s_off[WARPS];
+  __shared__ int s_b[WARPS];
+  __shared__ int4 s_part[2 * WARPS];     // sequence, head group, tiles from .. to (none: to = 0)
+  __shared__ float2 s_ml[2 * WARPS][H];  // maximum and sum
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t4 = lane & 3;
+  const int d = EXACT ? DP : c.d, row_bytes = EXACT ? S::ROW : c.row_bytes;
   pdl_trigger();
 
-  // --- this block's run of the work ---------------------------------------------
-  // (a position's number plus a block's step fits 31 bits)
+  // --- this warp's run of the work --------------------------------------------------
+  // (a position's number plus a step fits 31 bits)
   const int64_t capacity = min(a.table_cols * c.page_size, (int64_t)kKvMaxLength);
   const int hgs = c.heads * tiles;
   auto length_of = [&](int b) -> int {  // 0 where there is nothing to read
     const int n = __ldg(a.lengths + b);
     return n <= 0 || n > capacity ? 0 : n;
   };
-  auto blocks_of = [&](int b) { return (length_of(b) + S::KEYS - 1) / S::KEYS; };
+  // what a head group of sequence b counts for: its tiles and the cost of a piece
+  auto cost_of = [&](int b) -> int64_t {
+    const int n = length_of(b);
+    return n ? (n + 15) / 16 + kPieceTiles : 0;
+  };
   const int batch = (int)a.batch;
-  const int each = (batch + kThreads - 1) / kThreads;
-  const int b_lo = smaller_of(threadIdx.x * each, batch), b_hi = smaller_of(b_lo + each, batch);
+  const int each = (batch + S::THREADS - 1) / S::THREADS;
+  const int b_lo = min((int)threadIdx.x * each, batch), b_hi = min(b_lo + each, batch);
   int64_t own = 0;
-  for (int b = b_lo; b < b_hi; ++b) own += blocks_of(b);
+  for (int b = b_lo; b < b_hi; ++b) own += cost_of(b);
   int64_t before = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -223,466 +328,571 @@ __global__ void __launch_bounds__(kThreads, DP * HT <= 128 && T::BYTES == 2 ? 3 
     if (lane >= o) before += v;
   }
   if (lane == 31) s_sum[warp] = before;
-  if (threadIdx.x == 0) s_at[0] = -1;
   __syncthreads();
   int64_t total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += s_sum[w];
     total += s_sum[w];
   }
-  before -= own;
-  total *= hgs;
-  // equal runs for as many blocks as there is work for; the others have none
-  const int64_t runs = max((int64_t)1, min((int64_t)gridDim.x, total));
-  const bool idle = blockIdx.x >= runs || total == 0;
-  const int64_t first = idle ? 0 : total * blockIdx.x / runs;
-  const int64_t end = idle ? 0 : total * (blockIdx.x + 1) / runs;
-  if (first < end && before * hgs <= first && first < (before + own) * hgs) {
-    int b = b_lo;
-    int64_t at = before * hgs;
-    while (first >= at + (int64_t)blocks_of(b) * hgs) at += (int64_t)blocks_of(b++) * hgs;
-    const int n = blocks_of(b);
-    s_at[0] = b;
-    s_at[1] = (int)((first - at) / n);
-    s_at[2] = (int)((first - at) % n);
+  before = (before - own) * hgs, own *= hgs, total *= hgs;
+  // Equal runs for as many warps as there is work for, on as many blocks as possible.
+  const int64_t runs = max((int64_t)1, min((int64_t)gridDim.x * WARPS, total / kLeastRun));
+  const int per = (int)((runs + gridDim.x - 1) / gridDim.x);  // of a block
+  auto run_start = [&](int64_t r) { return total * min(r, runs) / runs; };
+  for (int w = 0; w < per; ++w) {
+    const int64_t first = run_start((int64_t)blockIdx.x * per + w);
+    if (before <= first && first < before + own) {
+      int b = b_lo;
+      int64_t at = before;
+      while (first >= at + cost_of(b) * hgs) at += cost_of(b++) * hgs;
+      s_b[w] = b;
+      s_off[w] = first - at;
+    }
   }
+  if (threadIdx.x < 2 * WARPS) s_part[threadIdx.x] = make_int4(0, 0, 0, 0);
+  __syncthreads();
+  const int64_t run = (int64_t)blockIdx.x * per + warp;
   // sequences that have nothing to read
   const int64_t y_row = a.q_heads * c.d;
-  for (int b = blockIdx.x; b < batch; b += gridDim.x) {
-    if (length_of(b)) continue;
+  for (int64_t b = (int64_t)blockIdx.x * WARPS + warp; b < batch; b += (int64_t)gridDim.x * WARPS) {
+    if (length_of((int)b)) continue;
     const bool none = __ldg(a.lengths + b) <= 0;
-    for (int64_t i = threadIdx.x; i < y_row; i += kThreads)
-      st_elem<T>(a.y, b * y_row + i, none ? 0.0f : NAN);
+    for (int64_t i = lane; i < y_row; i += 32) st_elem<T>(a.y, b * y_row + i, none ? 0.0f : NAN);
     if (a.lse)
-      for (int64_t i = threadIdx.x; i < a.q_heads; i += kThreads)
+      for (int64_t i = lane; i < a.q_heads; i += 32)
         a.lse[b * a.q_heads + i] = none ? -INFINITY : NAN;
   }
-  __syncthreads();
-  int4 cut = make_int4(0, 0, 0, 0);
-  int64_t left = end - first;
-  Piece pc = {s_at[0], s_at[1], s_at[2], 0, 0};
+  int64_t left = 0, skip = 0;  // tiles of the run; of its first piece before it
+  int b = 0, hg = 0;
+  if (warp < per && run < runs && total > 0) {
+    left = run_start(run + 1) - run_start(run);
+    b = s_b[warp];
+    hg = (int)(s_off[warp] / cost_of(b));
+    skip = s_off[warp] - hg * cost_of(b);
+  }
 
-  const uint32_t ring = smem_at(smem) + warp * (S::STAGES * S::STAGE);
-  char* const ring_p = smem + warp * (S::STAGES * S::STAGE);
-  uint2* const qfrag = reinterpret_cast<uint2*>(smem + (S::BODY + 15) / 16 * 16);
-  float* const ml = reinterpret_cast<float*>(smem + (S::BODY + 15) / 16 * 16 + S::QFRAG);
+  char* const ring_p = smem + warp * S::WARP;
+  const uint32_t ring = smem_at(ring_p);
+  uint2* const qfrag = reinterpret_cast<uint2*>(ring_p + S::STAGES * S::STAGE);
   const int tiles_page = c.page_size / 16;
   const float to_log2 = a.scale * kLog2e;
+  const bool zeros = kv_is_int(F) && c.kz;
+  // where the lane's share of a tile starts
+  const uint32_t k_lane = g * row_bytes + t4 * S::CK, v_lane = 2 * t4 * row_bytes + g * S::CV;
 
   while (left > 0) {
-    const int length = length_of(pc.b);
-    pc.blocks = (length + S::KEYS - 1) / S::KEYS;
-    pc.to = (int)min((int64_t)pc.blocks, pc.from + left);
-    left -= pc.to - pc.from;
-    const int kvh = pc.hg / tiles, h0 = kvh * group + (pc.hg - kvh * tiles) * S::H;
-    const int heads = min(S::H, (kvh + 1) * group - h0);
-    const int steps = pc.to - pc.from;
+    const int length = length_of(b), n_tiles = (length + 15) / 16;
+    const int64_t cost = n_tiles + kPieceTiles, take = min(cost - skip, left);
+    const int from = (int)max((int64_t)0, skip - kPieceTiles);
+    const int to = (int)max((int64_t)0, skip + take - kPieceTiles);
+    left -= take;
+    if (to > from) {
+      const int kvh = hg / tiles, h0 = kvh * group + (hg - kvh * tiles) * S::H;
+      const int heads = min(S::H, (kvh + 1) * group - h0);
+      const int steps = (to - from + S::NT - 1) / S::NT;
 
-    // --- the queries as products take them ----------------------------------------
-    float* const raw = reinterpret_cast<float*>(smem);
-    for (int i = threadIdx.x; i < S::H * DP; i += kThreads) {
-      const int h = i / DP, e = i % DP;
-      raw[h * (DP + 1) + e] =
-          h < heads && e < c.d
-              ? ld_elem<T>(a.q, pc.b * a.q_batch_stride + (h0 + h) * a.q_head_stride + e)
-              : 0.0f;
-    }
-    __syncthreads();
-    uint32_t qr[S::kF32 ? 1 : HT][S::kF32 ? 1 : S::KS][2];
-    float qsum[HT][2];  // of heads 2 t4, 2 t4 + 1
-#pragma unroll
-    for (int ht = 0; ht < HT; ++ht) {
-      float sum = 0.0f;
-#pragma unroll
-      for (int ks = 0; ks < S::KS; ++ks) {
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = raw[(8 * ht + g) * (DP + 1) + S::key_elem(2 * ks + i / 2, i % 2, t4)];
-          sum += v[i];
+      // --- copies: the lane's share of tile after tile ------------------------------
+      // Lane l knows the place (in tiles of 16 rows) of the l-th of the 32 tiles from
+      // the last look-up on: -1 a page that does not exist, -2 behind the piece.
+      int64_t place = -2;
+      bool bad = false;
+      auto look_up = [&](int first) {
+        const int tile = first + lane;
+        place = -2;
+        if (tile < to) {
+          const int col = tile / tiles_page;
+          const int page = __ldg(a.table + (int64_t)b * a.table_stride + col);
+          place = page < 0 || page >= c.pages
+                      ? -1
+                      : ((int64_t)page * c.heads + kvh) * tiles_page + (tile - col * tiles_page);
         }
-        if constexpr (!S::kF32) {
-          qr[ht][ks][0] = pack_bf16x2(v[0], v[1]);
-          qr[ht][ks][1] = pack_bf16x2(v[2], v[3]);
-        } else if (ks % kWarps == warp) {
+      };
+      auto issue = [&](int step, uint32_t stage) {
+        if (step < steps) {
+          if ((step * S::NT) % 32 == 0) look_up(from + step * S::NT);
 #pragma unroll
-          for (int p = 0; p < 3; ++p) {
-            uint2 f;
-            const float x0 = take_bf16(v[0]), x1 = take_bf16(v[1]);
-            const float x2 = take_bf16(v[2]), x3 = take_bf16(v[3]);
-            f.x = __float_as_uint(x0) >> 16 | (__float_as_uint(x1) & 0xffff0000u);
-            f.y = __float_as_uint(x2) >> 16 | (__float_as_uint(x3) & 0xffff0000u);
-            qfrag[(p * S::KS + ks) * 32 + lane] = f;
+          for (int t = 0; t < S::NT; ++t) {
+            const int64_t at = __shfl_sync(kFull, place, (step * S::NT + t) % 32);
+            if (at == -1) bad = true;
+            if (at < 0) continue;
+            const uint32_t slot = ring + stage + t * (S::TILE + S::PARAMS);
+            const char* kp = c.k + at * (16 * row_bytes) + k_lane;
+            const char* vp = c.v + at * (16 * row_bytes) + v_lane;
+            const int left_rows = length - (from + step * S::NT + t) * 16;
+            if (EXACT && left_rows >= 16) {
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int j = 0; j < S::NK; ++j)
+                  copy_async<S::CK>(slot + (r * S::NK + j) * 32 * S::CK + lane * S::CK,
+                                    kp + 8 * r * S::ROW + 4 * j * S::CK);
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j < S::NV; ++j)
+                  copy_async<S::CV>(
+                      slot + S::TILE / 2 + (r * S::NV + j) * 32 * S::CV + lane * S::CV,
+                      vp + ((r & 1) + 8 * (r >> 1)) * S::ROW + 8 * j * S::CV);
+            } else {
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int j = 0; j < S::NK; ++j)
+                  copy_async_if<S::CK>(slot + (r * S::NK + j) * 32 * S::CK + lane * S::CK,
+                                       kp + 8 * r * row_bytes + 4 * j * S::CK,
+                                       g + 8 * r < left_rows && (4 * j + t4) * S::CK < row_bytes);
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j < S::NV; ++j) {
+                  const int row = (r & 1) + 8 * (r >> 1);
+                  copy_async_if<S::CV>(
+                      slot + S::TILE / 2 + (r * S::NV + j) * 32 * S::CV + lane * S::CV,
+                      vp + row * row_bytes + 8 * j * S::CV,
+                      2 * t4 + row < left_rows && (8 * j + g) * S::CV < row_bytes);
+                }
+            }
+            if constexpr (F != QAT_CACHE_BF16) {
+              // 16 scales of keys, of values, then the zero points: runs of 16 bytes
+              if (lane < (zeros ? 10 : 8)) {
+                const char* src = lane < 4 ? reinterpret_cast<const char*>(c.ks) + at * 64 + lane * 16
+                                  : lane < 8
+                                      ? reinterpret_cast<const char*>(c.vs) + at * 64 + lane * 16 - 64
+                                      : reinterpret_cast<const char*>(lane == 8 ? c.kz : c.vz) + at * 16;
+                copy_async<16>(slot + S::TILE + lane * 16, src);
+              }
+            }
           }
         }
-      }
-      sum += __shfl_xor_sync(kFull, sum, 1);
-      sum += __shfl_xor_sync(kFull, sum, 2);
-      qsum[ht][0] = __shfl_sync(kFull, sum, 8 * t4);
-      qsum[ht][1] = __shfl_sync(kFull, sum, 8 * t4 + 4);
-    }
-    __syncthreads();
+        copy_commit();
+      };
+#pragma unroll
+      for (int i = 0; i < S::STAGES - 1; ++i) issue(i, i * S::STAGE);
 
-    // --- copies: the lane's share of tile after tile --------------------------------
-    // The warp's tiles of this piece in order; lane l knows the place (in tiles of 16
-    // rows) of the l-th of the 32 from `known` on: -1 a page that does not exist, -2
-    // behind the sequence.
-    const int n_tiles = (length + 15) / 16;
-    int64_t place = -2;
-    bool bad = false;
-    auto look_up = [&](int from) {
-      const int e = from + lane;
-      const int tile = ((pc.from + e / S::NT) * kWarps + warp) * S::NT + e % S::NT;
-      place = -2;
-      if (e < steps * S::NT && tile < n_tiles) {
-        const int col = tile / tiles_page;
-        const int page = __ldg(a.table + pc.b * a.table_stride + col);
-        place = page < 0 || page >= c.pages
-                    ? -1
-                    : ((int64_t)page * c.heads + kvh) * tiles_page + (tile - col * tiles_page);
+      // --- the queries as products take them ------------------------------------------
+      uint32_t qr[S::kF32 ? 1 : HT][S::kF32 ? 1 : S::KS][2];
+      // of heads 2 t4, 2 t4 + 1: the sum of the scaled query, and the factor of its scores
+      float qsum[HT][2], qscale[HT][2];
+#pragma unroll
+      for (int ht = 0; ht < HT; ++ht) {
+        float v[S::NK][S::EK], sum = 0.0f, top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < S::NK; ++j)
+#pragma unroll
+          for (int e = 0; e < S::EK; e += 8) {
+            const int at = (4 * j + t4) * S::EK + e;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][e + i] = 0.0f;
+            if (8 * ht + g < heads && at < d)
+              load8<T>(a.q, (int64_t)b * a.q_batch_stride + (h0 + 8 * ht + g) * a.q_head_stride + at,
+                       q_vec, v[j] + e);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[j][e + i]));
+          }
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+        // fp16: the largest element between 2^13 and 2^14 (or, below 2^-100, as near as that)
+        const int up = HALF ? 13 - max(exponent_of(top), -87) : 0;
+#pragma unroll
+        for (int j = 0; j < S::NK; ++j) {
+#pragma unroll
+          for (int e = 0; e < S::EK; ++e) {
+            if constexpr (HALF) v[j][e] *= power_of_two(up);
+            sum += v[j][e];
+          }
+#pragma unroll
+          for (int k = 0; k < S::EK / 4; ++k) {
+            const int ks = j * (S::EK / 4) + k;
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = v[j][S::key_place(2 * k + i / 2, i % 2)];
+            if constexpr (!S::kF32) {
+              qr[ht][ks][0] = take_pair<HALF>(x[0], x[1]);
+              qr[ht][ks][1] = take_pair<HALF>(x[2], x[3]);
+            } else {
+#pragma unroll
+              for (int p = 0; p < 3; ++p) {
+                uint2 y;
+                y.x = take_pair<HALF>(x[0], x[1]);
+                y.y = take_pair<HALF>(x[2], x[3]);
+                qfrag[(p * S::KS + ks) * 32 + lane] = y;
+              }
+            }
+          }
+        }
+        sum += __shfl_xor_sync(kFull, sum, 1);
+        sum += __shfl_xor_sync(kFull, sum, 2);
+        const float factor = to_log2 * power_of_two(-up);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          qsum[ht][i] = __shfl_sync(kFull, sum, 8 * t4 + 4 * i);
+          qscale[ht][i] = __shfl_sync(kFull, factor, 8 * t4 + 4 * i);
+        }
       }
-    };
-    auto issue = [&](int step) {
-      if (step < steps) {
-        if ((step * S::NT) % 32 == 0) look_up(step * S::NT);
+
+      // m: the maximum that weights refer to; limit: where it moves; base: m, but 0 before
+      // the first score.  Weighted values are summed times `unit`, a power of two that
+      // keeps p vs unit within 2^15 (p <= 2^8) for scales up to v_limit.
+      float m[HT][2], limit[HT][2], base[HT][2], l[HT][2], zsum[HT][2], o[HT][S::MT][4];
+      float unit = 1.0f, v_limit = -1.0f;
+#pragma unroll
+      for (int ht = 0; ht < HT; ++ht) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          m[ht][i] = limit[ht][i] = -INFINITY, base[ht][i] = l[ht][i] = zsum[ht][i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < S::MT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[ht][i][j] = 0.0f;
+      }
+
+      uint32_t stage = 0, ahead = (S::STAGES - 1) * S::STAGE;
+      for (int step = 0; step < steps; ++step) {
+        copy_wait<S::STAGES - 2>();
+        __syncwarp();  // scales of other lanes' copies; and the slot of the step before is free
+        issue(step + S::STAGES - 1, ahead);
+        ahead = ahead == (S::STAGES - 1) * S::STAGE ? 0 : ahead + S::STAGE;
+        const char* const stage_p = ring_p + stage;
+        stage = stage == (S::STAGES - 1) * S::STAGE ? 0 : stage + S::STAGE;
 #pragma unroll
         for (int t = 0; t < S::NT; ++t) {
-          const int64_t at = __shfl_sync(kFull, place, (step * S::NT + t) % 32);
-          if (at == -1) bad = true;
-          if (at < 0) continue;
-          const int key0 = (((pc.from + step) * kWarps + warp) * S::NT + t) * 16;
-          const uint32_t slot = ring + (step % S::STAGES) * S::STAGE + t * (S::TILE + S::PARAMS);
-          const char* kp = c.k + at * 16 * c.row_bytes;
-          const char* vp = c.v + at * 16 * c.row_bytes;
+          const int tile = from + step * S::NT + t;
+          if (S::NT > 1 && tile >= to) break;
+          const char* const slot = stage_p + t * (S::TILE + S::PARAMS);
+          // scores of positions g, g + 8 (rows) and heads 2 t4, 2 t4 + 1 (columns)
+          float s[HT][4];
+          {
+            float acc[S::QP][HT][4];
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
+            for (int p = 0; p < S::QP; ++p)
+#pragma unroll
+              for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[p][ht][i] = 0.0f;
 #pragma unroll
             for (int j = 0; j < S::NK; ++j) {
-              const int off = (4 * j + t4) * S::CK;
-              copy_async<S::CK>(slot + ((r * S::NK + j) * 32 + lane) * S::CK,
-                                kp + (g + 8 * r) * c.row_bytes + off,
-                                key0 + g + 8 * r < length && off < c.row_bytes);
+              uint32_t w[2][S::CK / 4];
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                load_run<S::CK>(slot + (r * S::NK + j) * 32 * S::CK + lane * S::CK, w[r]);
+              uint32_t pr[2][S::CK / 4 * W::PAIRS];
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int i = 0; i < S::CK / 4; ++i) {
+                  uint32_t x[W::PAIRS];
+                  W::decode(w[r][i], x);
+#pragma unroll
+                  for (int k = 0; k < W::PAIRS; ++k) pr[r][i * W::PAIRS + k] = x[k];
+                }
+#pragma unroll
+              for (int k = 0; k < S::EK / 4; ++k) {
+                const int ks = j * (S::EK / 4) + k;
+                const uint32_t fa[4] = {pr[0][2 * k], pr[1][2 * k], pr[0][2 * k + 1],
+                                        pr[1][2 * k + 1]};
+                if constexpr (S::kF32) {
+#pragma unroll
+                  for (int p = 0; p < 3; ++p) {
+                    const uint2 f = qfrag[(p * S::KS + ks) * 32 + lane];
+                    mma<HALF>(acc[p][0], fa, f.x, f.y);
+                  }
+                } else {
+#pragma unroll
+                  for (int ht = 0; ht < HT; ++ht) mma<HALF>(acc[0][ht], fa, qr[ht][ks][0], qr[ht][ks][1]);
+                }
+              }
             }
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int j = 0; j < S::NV; ++j) {
-              const int row = 2 * t4 + (r & 1) + 8 * (r >> 1), off = (8 * j + g) * S::CV;
-              copy_async<S::CV>(slot + S::TILE / 2 + ((r * S::NV + j) * 32 + lane) * S::CV,
-                                vp + row * c.row_bytes + off,
-                                key0 + row < length && off < c.row_bytes);
-            }
-          if constexpr (F != QAT_CACHE_BF16) {
-            // 16 scales of keys, of values, then the zero points: runs of 16 bytes
-            const char* src = reinterpret_cast<const char*>(lane < 4 ? c.ks : c.vs) + at * 64 +
-                              (lane & 3) * 16;
-            if (lane >= 8)
-              src = reinterpret_cast<const char*>(lane == 8 ? c.kz : c.vz) + at * 16;
-            if (lane < (kv_is_int(F) && c.kz ? 10 : 8))
-              copy_async<16>(slot + S::TILE + lane * 16, src, true);
-          }
-        }
-      }
-      copy_commit();
-    };
-
-    float m[HT][2], l[HT][2], zsum[HT][2], o[HT][S::MT][4];
-#pragma unroll
-    for (int ht = 0; ht < HT; ++ht) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) m[ht][i] = -INFINITY, l[ht][i] = 0.0f, zsum[ht][i] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < S::MT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[ht][i][j] = 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < S::STAGES - 1; ++i) issue(i);
-
-    for (int step = 0; step < steps; ++step) {
-      copy_wait<S::STAGES - 2>();
-      __syncwarp();  // scales of other lanes' copies; and the slot of the step before is free
-      issue(step + S::STAGES - 1);
-      const char* const stage = ring_p + (step % S::STAGES) * S::STAGE;
-#pragma unroll
-      for (int t = 0; t < S::NT; ++t) {
-        const int key0 = (((pc.from + step) * kWarps + warp) * S::NT + t) * 16;
-        if (key0 >= length) break;
-        const char* const slot = stage + t * (S::TILE + S::PARAMS);
-        // scores of positions g, g + 8 (rows) and heads 2 t4, 2 t4 + 1 (columns)
-        float s[HT][4];
-        {
-          float acc[S::QP][HT][4];
-#pragma unroll
-          for (int p = 0; p < S::QP; ++p)
 #pragma unroll
             for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) acc[p][ht][i] = 0.0f;
-#pragma unroll
-          for (int j = 0; j < S::NK; ++j) {
-            uint32_t w[2][S::CK / 4];
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-              load_run<S::CK>(slot + ((r * S::NK + j) * 32 + lane) * S::CK, w[r]);
-            uint32_t pr[2][S::CK / 4 * W::PAIRS];
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-              for (int i = 0; i < S::CK / 4; ++i) {
-                uint32_t d[W::PAIRS];
-                W::decode(w[r][i], d);
-#pragma unroll
-                for (int k = 0; k < W::PAIRS; ++k) pr[r][i * W::PAIRS + k] = d[k];
+              for (int i = 0; i < 4; ++i) {
+                s[ht][i] = acc[0][ht][i];
+                if constexpr (S::kF32) s[ht][i] += acc[1][ht][i] + acc[2][ht][i];
               }
-#pragma unroll
-            for (int k = 0; k < S::EK / 4; ++k) {
-              const int ks = j * (S::EK / 4) + k;
-              const uint32_t fa[4] = {pr[0][2 * k], pr[1][2 * k], pr[0][2 * k + 1], pr[1][2 * k + 1]};
-              if constexpr (S::kF32) {
-#pragma unroll
-                for (int p = 0; p < 3; ++p) {
-                  const uint2 f = qfrag[(p * S::KS + ks) * 32 + lane];
-                  mma(acc[p][0], fa, f.x, f.y);
-                }
-              } else {
-#pragma unroll
-                for (int ht = 0; ht < HT; ++ht) mma(acc[0][ht], fa, qr[ht][ks][0], qr[ht][ks][1]);
-              }
-            }
           }
-#pragma unroll
-          for (int ht = 0; ht < HT; ++ht)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              s[ht][i] = acc[0][ht][i];
-              if constexpr (S::kF32) s[ht][i] += acc[1][ht][i] + acc[2][ht][i];
-            }
-        }
-        float vs[2] = {1.0f, 1.0f}, vz[2] = {0.0f, 0.0f};
-        {
-          float ks[2] = {1.0f, 1.0f}, kz[2] = {0.0f, 0.0f};
+          float vs[2] = {1.0f, 1.0f}, vz[2] = {0.0f, 0.0f}, kz[2] = {0.0f, 0.0f};
+          float ks[2] = {1.0f, 1.0f};
           if constexpr (F != QAT_CACHE_BF16) {
             const float* sc = reinterpret_cast<const float*>(slot + S::TILE);
             ks[0] = sc[g], ks[1] = sc[g + 8], vs[0] = sc[16 + g], vs[1] = sc[24 + g];
-            if (kv_is_int(F) && c.kz) {
+            if (zeros) {
               const int8_t* z = reinterpret_cast<const int8_t*>(slot + S::TILE + 128);
               kz[0] = z[g], kz[1] = z[g + 8], vz[0] = z[16 + g], vz[1] = z[24 + g];
             }
           }
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float f = ks[r] * to_log2;
+          for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 float& x = s[ht][2 * r + i];
-                x = f * __fmaf_rn(-kz[r], qsum[ht][i], x);
+                if constexpr (kv_is_int(F)) x = __fmaf_rn(-kz[r], qsum[ht][i], x);
+                x *= F == QAT_CACHE_BF16 ? qscale[ht][i] : qscale[ht][i] * ks[r];
               }
-          }
-          if (key0 + 16 > length) {  // rows behind the sequence
+          if (tile * 16 + 16 > length) {  // rows behind the sequence
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              if (key0 + g + 8 * r >= length) {
+              if (tile * 16 + g + 8 * r >= length) {
                 vs[r] = vz[r] = 0.0f;
 #pragma unroll
                 for (int ht = 0; ht < HT; ++ht) s[ht][2 * r] = s[ht][2 * r + 1] = -INFINITY;
               }
           }
-        }
-        // the running maximum moves only where a score is far above it
-        bool above = false;
-#pragma unroll
-        for (int ht = 0; ht < HT; ++ht)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            above = above || fmaxf(s[ht][i], s[ht][2 + i]) > m[ht][i] + kSlack;
-        if (__any_sync(kFull, above)) {
+          // the maximum and the unit move only where a score or a scale is far above them
+          bool above = HALF && fmaxf(fabsf(vs[0]), fabsf(vs[1])) > v_limit;
 #pragma unroll
           for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float top = fmaxf(s[ht][i], s[ht][2 + i]);
+            for (int i = 0; i < 2; ++i)
+              above = above || fmaxf(s[ht][i], s[ht][2 + i]) > limit[ht][i];
+          if (__any_sync(kFull, above)) {
+            float shrink = 1.0f;
+            if constexpr (HALF) {
+              float top = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
 #pragma unroll
-              for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-              top = fmaxf(top, m[ht][i]);
-              const float was = m[ht][i] == top ? 1.0f : exp2_fast(m[ht][i] - top);
-              m[ht][i] = top;
-              l[ht][i] *= was;
-              zsum[ht][i] *= was;
-#pragma unroll
-              for (int j = 0; j < S::MT; ++j) o[ht][j][i] *= was, o[ht][j][2 + i] *= was;
+              for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+              if (top > v_limit) {  // to between 16 and 32
+                const int e = top < 0x1p-100f ? -100 : exponent_of(top);
+                const int by = 4 - e - exponent_of(unit);
+                if (v_limit >= 0.0f) shrink = power_of_two(max(by, -126));
+                unit = power_of_two(4 - e);
+                v_limit = power_of_two(min(e + 3, 127));
+              }
             }
-        }
-        // weights, as the second operand of the value products
-        uint32_t wb[HT][S::PP][2];
 #pragma unroll
-        for (int ht = 0; ht < HT; ++ht) {
-          float w[4];
+            for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float base = m[ht][i & 1] == -INFINITY ? 0.0f : m[ht][i & 1];
-            const float p = exp2_fast(s[ht][i] - base);
-            l[ht][i & 1] += p;
-            w[i] = p * vs[i >> 1];
-            zsum[ht][i & 1] = __fmaf_rn(w[i], vz[i >> 1], zsum[ht][i & 1]);
+              for (int i = 0; i < 2; ++i) {
+                float top = fmaxf(s[ht][i], s[ht][2 + i]);
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+                top = fmaxf(top, m[ht][i]);
+                const float was = m[ht][i] == top ? 1.0f : exp2_fast(m[ht][i] - top);
+                m[ht][i] = top;
+                limit[ht][i] = top + kSlack;
+                base[ht][i] = top == -INFINITY ? 0.0f : top;
+                l[ht][i] *= was;
+                const float both = was * shrink;
+                zsum[ht][i] *= both;
+#pragma unroll
+                for (int j = 0; j < S::MT; ++j) o[ht][j][i] *= both, o[ht][j][2 + i] *= both;
+              }
           }
+          if constexpr (HALF) vs[0] *= unit, vs[1] *= unit;
+          // weights, as the second operand of the value products
+          uint32_t wb[HT][S::PP][2];
 #pragma unroll
-          for (int p = 0; p < S::PP; ++p)
+          for (int ht = 0; ht < HT; ++ht) {
+            float w[4];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const uint32_t two = pack_bf16x2(w[2 * r], w[2 * r + 1]);
-              wb[ht][p][r] = transpose8(two);
-              w[2 * r] -= __uint_as_float(two << 16);
-              w[2 * r + 1] -= __uint_as_float(two & 0xffff0000u);
-            }
-        }
-        // weighted values: rows are head elements, k the positions
-#pragma unroll
-        for (int j = 0; j < S::NV; ++j) {
-          uint32_t v[4][S::CV / 4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            load_run<S::CV>(slot + S::TILE / 2 + ((r * S::NV + j) * 32 + lane) * S::CV, v[r]);
-#pragma unroll
-          for (int i = 0; i < S::CV / 4; ++i) {
-            uint32_t pr[2][2 * W::PAIRS];  // positions 2 t4, + 1; and those + 8
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t d[W::PAIRS];
-              W::decode(__byte_perm(v[2 * k][i], v[2 * k + 1][i], 0x5410), d);
-#pragma unroll
-              for (int q = 0; q < W::PAIRS; ++q) pr[k][q] = d[q];
-              W::decode(__byte_perm(v[2 * k][i], v[2 * k + 1][i], 0x7632), d);
-#pragma unroll
-              for (int q = 0; q < W::PAIRS; ++q) pr[k][W::PAIRS + q] = d[q];
+            for (int i = 0; i < 4; ++i) {
+              const float p = exp2_fast(s[ht][i] - base[ht][i & 1]);
+              l[ht][i & 1] += p;
+              w[i] = p;
+              if constexpr (F != QAT_CACHE_BF16) w[i] *= vs[i >> 1];
+              if constexpr (kv_is_int(F))
+                zsum[ht][i & 1] = __fmaf_rn(w[i], vz[i >> 1], zsum[ht][i & 1]);
             }
 #pragma unroll
-            for (int q = 0; q < W::PAIRS; ++q) {
-              const int mt = (j * (S::CV / 4) + i) * W::PAIRS + q;
-              const uint32_t fa[4] = {pr[0][2 * q], pr[0][2 * q + 1], pr[1][2 * q], pr[1][2 * q + 1]};
+            for (int p = 0; p < S::PP; ++p)
 #pragma unroll
-              for (int ht = 0; ht < HT; ++ht) {
-                if constexpr (S::kF32) {
-                  // (sums of many tiles on the tensor cores would drift: 16 positions only)
-                  float part[4] = {};
+              for (int r = 0; r < 2; ++r) {
+                wb[ht][p][r] = transpose8(take_pair<HALF>(w[2 * r], w[2 * r + 1]));
+              }
+          }
+          // weighted values: rows are head elements, k the positions
 #pragma unroll
-                  for (int p = S::PP - 1; p >= 0; --p) mma(part, fa, wb[ht][p][0], wb[ht][p][1]);
+          for (int j = 0; j < S::NV; ++j) {
+            uint32_t v[4][S::CV / 4];
 #pragma unroll
-                  for (int x = 0; x < 4; ++x) o[ht][mt][x] += part[x];
-                } else {
+            for (int r = 0; r < 4; ++r)
+              load_run<S::CV>(slot + S::TILE / 2 + (r * S::NV + j) * 32 * S::CV + lane * S::CV, v[r]);
 #pragma unroll
-                  for (int p = 0; p < S::PP; ++p) mma(o[ht][mt], fa, wb[ht][p][0], wb[ht][p][1]);
+            for (int i = 0; i < S::CV / 4; ++i) {
+              uint32_t pr[2][2 * W::PAIRS];  // positions 2 t4, + 1; and those + 8
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                uint32_t x[W::PAIRS];
+                W::decode(__byte_perm(v[2 * k][i], v[2 * k + 1][i], W::kLower), x);
+#pragma unroll
+                for (int q = 0; q < W::PAIRS; ++q) pr[k][q] = x[q];
+                W::decode(__byte_perm(v[2 * k][i], v[2 * k + 1][i], W::kUpper), x);
+#pragma unroll
+                for (int q = 0; q < W::PAIRS; ++q) pr[k][W::PAIRS + q] = x[q];
+              }
+#pragma unroll
+              for (int q = 0; q < W::PAIRS; ++q) {
+                const int mt = (j * (S::CV / 4) + i) * W::PAIRS + q;
+                const uint32_t fa[4] = {pr[0][2 * q], pr[0][2 * q + 1], pr[1][2 * q],
+                                        pr[1][2 * q + 1]};
+#pragma unroll
+                for (int ht = 0; ht < HT; ++ht) {
+                  if constexpr (S::kF32) {
+                    // (sums of many tiles on the tensor cores would drift: 16 positions only)
+                    float part[4] = {};
+#pragma unroll
+                    for (int p = S::PP - 1; p >= 0; --p) mma<HALF>(part, fa, wb[ht][p][0], wb[ht][p][1]);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[ht][mt][x] += part[x];
+                  } else {
+#pragma unroll
+                    for (int p = 0; p < S::PP; ++p) mma<HALF>(o[ht][mt], fa, wb[ht][p][0], wb[ht][p][1]);
+                  }
                 }
               }
             }
           }
         }
       }
-    }
-    copy_wait<0>();
+      copy_wait<0>();
+      __syncwarp();  // (the next piece's copies write where other lanes read scales)
 
-    // --- the block's warps joined ------------------------------------------------------
+      // --- the piece's result -----------------------------------------------------------
+      const bool whole = from == 0 && to == n_tiles;
+      const int which = 2 * warp + (from == 0);
+      float* const part = reinterpret_cast<float*>(ring_p + (from == 0 ? 0 : S::RING));
+      if (!whole && lane == 0) s_part[which] = make_int4(b, hg, from, to);
 #pragma unroll
-    for (int ht = 0; ht < HT; ++ht)
+      for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i) {
+          float sum = bad ? NAN : l[ht][i], z = zsum[ht][i];
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          l[ht][i] += __shfl_xor_sync(kFull, l[ht][i], d);
-          zsum[ht][i] += __shfl_xor_sync(kFull, zsum[ht][i], d);
+          for (int x = 4; x < 32; x <<= 1) {
+            sum += __shfl_xor_sync(kFull, sum, x);
+            if constexpr (kv_is_int(F)) z += __shfl_xor_sync(kFull, z, x);
+          }
+          const int h = 8 * ht + 2 * t4 + i;
+          if (h >= heads) continue;
+          const float by = __frcp_rn(unit) * (!whole ? 1.0f : sum == 0.0f ? 0.0f : __frcp_rn(sum));
+          const int64_t y_at = ((int64_t)b * a.q_heads + h0 + h) * d;
+#pragma unroll
+          for (int j = 0; j < S::NV; ++j)
+#pragma unroll
+            for (int e = 0; e < S::EV; e += 8) {
+              const int at = (8 * j + g) * S::EV + e;
+              if (!EXACT && at >= d) continue;
+              float y[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                constexpr auto pl = &S::value_place;
+                const int p = pl(j, e + x);
+                y[x] = (o[ht][p / 2][i + 2 * (p % 2)] - z) * by;
+              }
+              if (whole)
+                store8<T>(a.y, y_at + at, y_vec, y);
+              else
+                store8<F32>(part, h * d + at, true, y);
+            }
+          if (g == 0) {
+            if (!whole)
+              s_ml[which][h] = make_float2(m[ht][i], sum);
+            else if (a.lse)
+              a.lse[(int64_t)b * a.q_heads + h0 + h] =
+                  sum == 0.0f ? -INFINITY : (m[ht][i] + log2f(sum)) * 0.69314718055994531f;
+          }
         }
-    __syncthreads();  // every warp is done with its ring
-    float* const part = reinterpret_cast<float*>(smem);
-#pragma unroll
-    for (int ht = 0; ht < HT; ++ht)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int h = 8 * ht + 2 * t4 + i;
-        float* row = part + (warp * S::H + h) * S::OPAD;
-#pragma unroll
-        for (int j = 0; j < S::MT; ++j) {
-          row[2 * j * 8 + g] = o[ht][j][i];
-          row[(2 * j + 1) * 8 + g] = o[ht][j][2 + i];
-        }
-        if (g == 0) {
-          ml[(warp * S::H + h) * 3] = m[ht][i];
-          ml[(warp * S::H + h) * 3 + 1] = bad ? NAN : l[ht][i];
-          ml[(warp * S::H + h) * 3 + 2] = zsum[ht][i];
-        }
-      }
-    __syncthreads();
-    const bool whole = pc.from == 0 && pc.to == pc.blocks;
-    const int64_t at = ((int64_t)blockIdx.x * 2 + (pc.from == 0)) * S::H;
-    for (int i = threadIdx.x; i < heads * c.d; i += kThreads) {
-      const int h = i / c.d, e = i - h * c.d;
-      float top = -INFINITY, sum = 0.0f, y = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[(w * S::H + h) * 3]);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float* r = ml + (w * S::H + h) * 3;
-        const float f = r[0] == top ? 1.0f : exp2_fast(r[0] - top);
-        sum = __fmaf_rn(f, r[1], sum);
-        y = __fmaf_rn(f, part[(w * S::H + h) * S::OPAD + S::value_place(e)] - r[2], y);
+    }
+    // --- the next piece -------------------------------------------------------------------
+    skip = 0;
+    if (left > 0 && ++hg == hgs) {
+      hg = 0;
+      do ++b;
+      while (cost_of(b) == 0);
+    }
+  }
+  __syncthreads();
+
+  // --- parts of one sequence that the block's warps hold, one after the other, joined ------
+  int4 cut = make_int4(0, 0, 0, 0);
+  for (int first = 0; first < 2 * per;) {
+    const int4 p0 = s_part[first];
+    if (p0.w == 0) {
+      ++first;
+      continue;
+    }
+    int last = first, to = p0.w;  // parts first .. last are neighbours
+    for (int i = first + 1; i < 2 * per; ++i) {
+      const int4 p = s_part[i];
+      if (p.w == 0) continue;
+      if (p.x != p0.x || p.y != p0.y || p.z != to) break;
+      last = i, to = p.w;
+    }
+    const int length = length_of(p0.x), n_tiles = (length + 15) / 16;
+    const int kvh = p0.y / tiles, h0 = kvh * group + (p0.y - kvh * tiles) * H;
+    const int heads = min(H, (kvh + 1) * group - h0);
+    const bool whole = p0.z == 0 && to == n_tiles;
+    const int64_t slot = ((int64_t)blockIdx.x * 2 + (p0.z == 0)) * H;
+    for (int i = threadIdx.x; i < heads * (d / 4); i += S::THREADS) {
+      const int h = i / (d / 4), e = (i - h * (d / 4)) * 4;
+      float top = -INFINITY, sum = 0.0f, y[4] = {};
+      for (int k = first; k <= last; ++k)
+        if (s_part[k].w) top = fmaxf(top, s_ml[k][h].x);
+      for (int k = first; k <= last; ++k) {
+        if (s_part[k].w == 0) continue;
+        const float2 ml = s_ml[k][h];
+        const float f = ml.x == top ? 1.0f : exp2_fast(ml.x - top);
+        sum = __fmaf_rn(f, ml.y, sum);
+        const float4 v = *reinterpret_cast<const float4*>(
+            smem + (k / 2) * S::WARP + (k % 2 ? 0 : S::RING) + (h * d + e) * 4);
+        y[0] = __fmaf_rn(f, v.x, y[0]), y[1] = __fmaf_rn(f, v.y, y[1]);
+        y[2] = __fmaf_rn(f, v.z, y[2]), y[3] = __fmaf_rn(f, v.w, y[3]);
       }
       if (whole) {
-        st_elem<T>(a.y, ((int64_t)pc.b * a.q_heads + h0 + h) * c.d + e,
-                   sum == 0.0f ? 0.0f : __fdiv_rn(y, sum));
+        const int64_t row = (int64_t)p0.x * a.q_heads + h0 + h;
+        const float by = sum == 0.0f ? 0.0f : __frcp_rn(sum);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) st_elem<T>(a.y, row * d + e + x, y[x] * by);
         if (e == 0 && a.lse)
-          a.lse[(int64_t)pc.b * a.q_heads + h0 + h] =
-              sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+          a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
       } else {
-        ws.o[(at + h) * c.d + e] = y;
-        if (e == 0) ws.ml[at + h] = make_float2(top, sum);
+        *reinterpret_cast<float4*>(ws.o + (slot + h) * d + e) = make_float4(y[0], y[1], y[2], y[3]);
+        if (e == 0) ws.ml[slot + h] = make_float2(top, sum);
       }
     }
-    if (!whole && pc.from == 0) {
-      // cut off by the run's end: the blocks behind this one hold the rest
-      const int64_t rest = pc.blocks - pc.to;
-      const int64_t last = end + rest - 1;  // its last block's place in the row
-      int n = 1;
-      while (total * (blockIdx.x + n + 1) / runs <= last) ++n;
-      cut = make_int4(pc.b, pc.hg, n + 1, 0);
+    if (p0.z == 0 && to < n_tiles) {
+      // cut off by the end of the block's last run: the blocks behind it hold the rest
+      const int64_t at = run_start((int64_t)(blockIdx.x + 1) * per) + (n_tiles - to) - 1;
+      int n = 1;  // (`at`: the place of its last tile in the row)
+      while (run_start((int64_t)(blockIdx.x + n + 1) * per) <= at) ++n;
+      cut = make_int4(p0.x, p0.y, n + 1, 0);
     }
-    __syncthreads();
-    // --- the next piece -----------------------------------------------------------------
-    if (left > 0) {
-      pc.from = 0;
-      if (++pc.hg == hgs) {
-        pc.hg = 0;
-        do ++pc.b;
-        while (blocks_of(pc.b) == 0);
-      }
-    }
+    first = last + 1;
   }
   if (threadIdx.x == 0) ws.cut[blockIdx.x] = cut;
 }
 
-template <typename T, int F, int DP, int HT>
+template <typename T, int F, int DP, int HT, bool EXACT>
 qat_status go(const KvCacheView& c, const KvAttnArgs& a, const SplitWs& ws, int* grid,
               cudaStream_t s) {
   using S = Shape<T, F, DP, HT>;
-  static_assert(S::SMEM <= 227 * 1024, "shared memory");
-  const auto k = k_kv_split<T, F, DP, HT>;
+  static_assert(S::WARPS >= 2, "shared memory");
+  const auto k = k_kv_split<T, F, DP, HT, EXACT>;
   if (S::SMEM > 48 * 1024 &&
       cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) != cudaSuccess) {
     (void)cudaGetLastError();
     return QAT_ERR_CUDA;
   }
   const HeadTiles t = head_tiles(a.q_heads, c.heads, c.d, S::kF32);
-  int per = 227 * 1024 / (S::SMEM + 2048);
-  if (per > 3) per = 3;
-  if (DP * HT > 128 || S::kF32) per = per < 2 ? per : 2;
-  *grid = device_info().sms * per;
-  if (*grid > kSplitBlocks) *grid = kSplitBlocks;
-  if (launch_kernel(k, dim3(*grid), dim3(kThreads), S::SMEM, s, false, c, a, t.group, t.tiles, ws) !=
-      cudaSuccess)
+  const int sms = device_info().sms;
+  *grid = sms < kSplitBlocks ? sms : kSplitBlocks;
+  const auto vec = [](const void* p, int64_t s0, int64_t s1) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && s0 * T::BYTES % 16 == 0 &&
+           s1 * T::BYTES % 16 == 0;
+  };
+  if (launch_kernel(k, dim3(*grid), dim3(S::THREADS), S::SMEM, s, false, c, a, t.group, t.tiles,
+                    vec(a.q, a.q_batch_stride, a.q_head_stride), vec(a.y, 8, 8), ws) != cudaSuccess)
     return QAT_ERR_CUDA;
   count_launch(1);
   return QAT_OK;
+}
+template <typename T, int F, int DP, int HT>
+qat_status go_any(const KvCacheView& c, const KvAttnArgs& a, const SplitWs& ws, int* grid,
+                  cudaStream_t s) {
+  return c.d == DP ? go<T, F, DP, HT, true>(c, a, ws, grid, s)
+                   : go<T, F, DP, HT, false>(c, a, ws, grid, s);
 }
 
 }  // namespace
@@ -692,14 +902,16 @@ qat_status launch_kv_split(const KvCacheView& c, const KvAttnArgs& a, qat_dtype 
                            int* grid, cudaStream_t s) {
   const bool wide = head_tiles(a.q_heads, c.heads, c.d, dt == QAT_F32).tile == 16;
   if (dt == QAT_F32) {
-    if (c.d <= 64) return go<F32, F, 64, 1>(c, a, ws, grid, s);
-    if (c.d <= 128) return go<F32, F, 128, 1>(c, a, ws, grid, s);
-    return go<F32, F, 256, 1>(c, a, ws, grid, s);
+    if (c.d <= 64) return go_any<F32, F, 64, 1>(c, a, ws, grid, s);
+    if (c.d <= 128) return go_any<F32, F, 128, 1>(c, a, ws, grid, s);
+    return go_any<F32, F, 256, 1>(c, a, ws, grid, s);
   }
-  if (c.d <= 64) return wide ? go<BF16, F, 64, 2>(c, a, ws, grid, s) : go<BF16, F, 64, 1>(c, a, ws, grid, s);
+  if (c.d <= 64)
+    return wide ? go_any<BF16, F, 64, 2>(c, a, ws, grid, s) : go_any<BF16, F, 64, 1>(c, a, ws, grid, s);
   if (c.d <= 128)
-    return wide ? go<BF16, F, 128, 2>(c, a, ws, grid, s) : go<BF16, F, 128, 1>(c, a, ws, grid, s);
-  return go<BF16, F, 256, 1>(c, a, ws, grid, s);
+    return wide ? go_any<BF16, F, 128, 2>(c, a, ws, grid, s)
+                : go_any<BF16, F, 128, 1>(c, a, ws, grid, s);
+  return go_any<BF16, F, 256, 1>(c, a, ws, grid, s);
 }
 template qat_status launch_kv_split<kFormat>(const KvCacheView&, const KvAttnArgs&, qat_dtype,
                                              const SplitWs&, int*, cudaStream_t);

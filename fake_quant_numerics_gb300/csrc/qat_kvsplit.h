@@ -5,8 +5,9 @@
 
 namespace qat {
 
-// Blocks of the split kernel at most; each leaves up to two partial results.
-constexpr int kSplitBlocks = 608;
+// Blocks of the split kernel at most, one on each SM; a block leaves up to two parts
+// of sequences that it shares with its neighbours.
+constexpr int kSplitBlocks = 160;
 
 // The longest sequence.
 constexpr int kKvMaxLength = INT32_MAX - 1024;
@@ -19,9 +20,10 @@ struct KvCacheView {
   int heads, page_size, d, row_bytes;
 };
 
-// Workspace: one int4 a block - sequence, group of heads, number of parts that
-// its last, unfinished piece was cut into (0: none) -, then for each block and
-// slot [heads] maximum and sum, then [heads][d] sums of weighted values.
+// Workspace: one int4 a block - sequence, group of heads, number of parts of the
+// sequence that its end cuts off (0: none) -, then for each block and slot [heads]
+// maximum and sum, then [heads][d] sums of weighted values.  Slot 0 holds a sequence
+// that began in an earlier block, slot 1 the one cut off.
 struct SplitWs {
   int4* cut;
   float2* ml;
