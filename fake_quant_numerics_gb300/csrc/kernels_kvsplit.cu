@@ -20,11 +20,12 @@
 // and the end of a piece, a few latencies each, pass behind the others' work; what they
 // cost a warp counts as kPieceTiles tiles when the runs are cut.
 //
-// Each lane copies exactly the codes that it multiplies (cp.async into slots of its
-// own), so that only scales are exchanged between lanes: rows of a product are
-// positions lane / 4 (+ 8) for keys, and the lane's share of a key is every fourth
-// 16-byte run; of a value every eighth.  Which head element a product's k index
-// stands for is free, so the codes' own order is taken for both operands.
+// Tiles come by cp.async, each warp's own ring, 512 consecutive bytes an operation
+// (copies of 64 bytes of eight rows took nearly twice the bytes from L2), to places
+// that are swizzled so that both products' operands are read without conflicts.  Rows
+// of a product are positions lane / 4 (+ 8) for keys, and the lane's share of a key is
+// every fourth 16-byte run; of a value every eighth.  Which head element a product's k
+// index stands for is free, so the codes' own order is taken for both operands.
 #include <cmath>
 
 #include "qat_kv.cuh"
@@ -46,26 +47,9 @@ constexpr float kSlack = 8.0f;  // scores may exceed the running maximum by 2^8 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
-// 4, 8 or 16 bytes from global to shared memory
-template <int BYTES>
+// 16 bytes from global to shared memory
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
-                 : "memory");
-}
-// the same, or zeros
-template <int BYTES>
-__device__ __forceinline__ void copy_async_if(uint32_t dst, const void* src, bool on) {
-  const int n = on ? BYTES : 0;
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES),
-                 "r"(n)
-                 : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -75,14 +59,12 @@ __device__ __forceinline__ void copy_wait() {
 template <bool HALF>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (HALF)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -213,22 +195,36 @@ struct Shape {
   static constexpr int CK = smaller(16, ROW / 4), NK = ROW / 4 / CK, EK = CK / 4 * W::CODES;
   static constexpr int CV = smaller(16, ROW / 8), NV = ROW / 8 / CV, EV = CV / 4 * W::CODES;
   static constexpr int TILE = 32 * ROW;  // 16 keys and values
+  static constexpr int UNITS = ROW / 16, LOADS = ROW / 32;  // 16-byte units a row; of a tile's half, a lane
   // 16 scales and 16 zero points of both
   static constexpr int PARAMS = F == QAT_CACHE_BF16 ? 0 : 160;
-  static constexpr int NT = smaller(2, larger(1, 4096 / TILE));  // tiles a step
-  static constexpr int STAGES = TILE > 4096 ? 2 : 3;
-  static constexpr int STAGE = NT * (TILE + PARAMS);
+  // Keys of a tile and, a step later, its values, each with their scales and zero points.
+  static constexpr int HALF_STAGE = (TILE + PARAMS) / 2;
+  static constexpr int STAGES = smaller(6, larger(2, 13 * 1024 / (TILE + PARAMS)));
   static constexpr int H = 8 * HT, KS = DP / 16, MT = DP / 16;
   static constexpr int QP = kF32 ? 3 : 1, PP = kF32 ? 3 : 2;  // 16-bit parts of q and of the weights
   static constexpr int QFRAG = kF32 ? QP * KS * 32 * 8 : 0;
   // A warp's ring and queries, then the part it starts with (its run began inside a
   // sequence); the part it ends with takes the ring's place.
   static constexpr int PART = H * DP * 4;
-  static constexpr int RING = larger(STAGES * STAGE + QFRAG, PART), WARP = RING + PART;
+  static constexpr int RING = larger(2 * STAGES * HALF_STAGE + QFRAG, PART), WARP = RING + PART;
   // Registers hold twelve warps of up to 168, eight of up to 255.
   static constexpr int WARPS =
       smaller(224 * 1024 / WARP, DP * HT <= 128 && !kF32 ? 12 : 8);
   static constexpr int THREADS = 32 * WARPS, SMEM = WARPS * WARP;
+
+  // Where a unit of a row lies in a tile's half.  Reads of keys (rows lane / 4, four
+  // units side by side) and of values (rows 2 (lane % 4), eight runs side by side) then
+  // meet every bank once.  mix() is linear: mix(r + s) = mix(r) ^ mix(s) without carries.
+  __host__ __device__ static constexpr int mix(int r) {
+    return UNITS >= 8 ? (r & 6) ^ 4 * (r & 1) : UNITS == 4 ? (r >> 1) & 2 : 0;
+  }
+  __host__ __device__ static constexpr int row_place(int r) {
+    return UNITS >= 8 ? r : UNITS == 4 ? r ^ ((r >> 1) & 1) : r ^ ((r >> 2) & 1);
+  }
+  __host__ __device__ static constexpr int place(int r, int byte) {
+    return (row_place(r) * UNITS + ((byte / 16) ^ mix(r))) * 16 + byte % 16;
+  }
 
   // Pair p of a run of a key: the place of its halves in the run.
   __host__ __device__ static constexpr int key_place(int p, int hi) {
@@ -372,14 +368,25 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
     skip = s_off[warp] - hg * cost_of(b);
   }
 
-  char* const ring_p = smem + warp * S::WARP;
+  char* const ring_p = smem + warp * S::WARP;  // keys' slots, then values'
   const uint32_t ring = smem_at(ring_p);
-  uint2* const qfrag = reinterpret_cast<uint2*>(ring_p + S::STAGES * S::STAGE);
+  constexpr uint32_t kRingEnd = S::STAGES * S::HALF_STAGE;
+  uint2* const qfrag = reinterpret_cast<uint2*>(ring_p + 2 * kRingEnd);
   const int tiles_page = c.page_size / 16;
   const float to_log2 = a.scale * kLog2e;
   const bool zeros = kv_is_int(F) && c.kz;
-  // where the lane's share of a tile starts
-  const uint32_t k_lane = g * row_bytes + t4 * S::CK, v_lane = 2 * t4 * row_bytes + g * S::CV;
+  // Places of the lane's units as they are copied, and of its shares as they are read:
+  // of keys in row g, of values in rows 2 t4 and 2 t4 + 1.
+  const int units = row_bytes / 16;
+  const int c_row = EXACT ? lane / S::UNITS : lane / units;
+  const int c_unit = EXACT ? lane % S::UNITS : lane - c_row * units;
+  const int c_place = S::place(c_row, c_unit * 16), k_place = S::place(g, t4 * S::CK);
+  const int v_places[2] = {S::place(2 * t4, g * S::CV), S::place(2 * t4 + 1, g * S::CV)};
+  if (!EXACT) {  // elements behind head_dim stay zeros (never NaN, whose product with 0 is NaN)
+    for (int i = lane * 16; i < 2 * (int)kRingEnd; i += 512)
+      *reinterpret_cast<uint4*>(ring_p + i) = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+  }
 
   while (left > 0) {
     const int length = length_of(b), n_tiles = (length + 15) / 16;
@@ -390,85 +397,74 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
     if (to > from) {
       const int kvh = hg / tiles, h0 = kvh * group + (hg - kvh * tiles) * S::H;
       const int heads = min(S::H, (kvh + 1) * group - h0);
-      const int steps = (to - from + S::NT - 1) / S::NT;
+      const int steps = to - from;
 
-      // --- copies: the lane's share of tile after tile ------------------------------
+      // --- copies, tile after tile ----------------------------------------------------
       // Lane l knows the place (in tiles of 16 rows) of the l-th of the 32 tiles from
       // the last look-up on: -1 a page that does not exist, -2 behind the piece.
-      int64_t place = -2;
+      int64_t place = -2, v_at = -2;  // (v_at: of the tile whose values come next)
       bool bad = false;
-      auto look_up = [&](int first) {
-        const int tile = first + lane;
-        place = -2;
-        if (tile < to) {
-          const int col = tile / tiles_page;
-          const int page = __ldg(a.table + (int64_t)b * a.table_stride + col);
-          place = page < 0 || page >= c.pages
-                      ? -1
-                      : ((int64_t)page * c.heads + kvh) * tiles_page + (tile - col * tiles_page);
+      // 16 rows, their scales and zero points.  Where rows lie behind the sequence the
+      // last unit before them is read in their stead: they have no weight.
+      auto copy = [&](uint32_t slot, const char* codes, const float* scales, const int8_t* zps,
+                      int64_t at, int step) {
+        const char* src = codes + at * (16 * row_bytes);
+        const int last = min(16, length - (from + step) * 16) * row_bytes - 16;
+        if constexpr (EXACT) {
+#pragma unroll
+          for (int i = 0; i < S::LOADS; ++i)
+            copy_async(slot + 512 * i + (c_place ^ S::mix(i * 32 / S::UNITS) * 16),
+                           src + min(lane * 16 + 512 * i, last));
+        } else {
+          int r = c_row, u = c_unit;
+          for (int i = lane; i < 16 * units; i += 32) {
+            copy_async(slot + S::place(r, u * 16), src + min(i * 16, last));
+            r += 32 / units, u += 32 % units;
+            if (u >= units) u -= units, ++r;
+          }
+        }
+        if constexpr (F != QAT_CACHE_BF16) {
+          if (lane < (zeros ? 5 : 4)) {
+            src = reinterpret_cast<const char*>(scales) + at * 64 + lane * 16;
+            if (lane == 4) src = reinterpret_cast<const char*>(zps) + at * 16;
+            copy_async(slot + S::TILE / 2 + lane * 16, src);
+          }
         }
       };
-      auto issue = [&](int step, uint32_t stage) {
-        if (step < steps) {
-          if ((step * S::NT) % 32 == 0) look_up(from + step * S::NT);
-#pragma unroll
-          for (int t = 0; t < S::NT; ++t) {
-            const int64_t at = __shfl_sync(kFull, place, (step * S::NT + t) % 32);
-            if (at == -1) bad = true;
-            if (at < 0) continue;
-            const uint32_t slot = ring + stage + t * (S::TILE + S::PARAMS);
-            const char* kp = c.k + at * (16 * row_bytes) + k_lane;
-            const char* vp = c.v + at * (16 * row_bytes) + v_lane;
-            const int left_rows = length - (from + step * S::NT + t) * 16;
-            if (EXACT && left_rows >= 16) {
-#pragma unroll
-              for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int j = 0; j < S::NK; ++j)
-                  copy_async<S::CK>(slot + (r * S::NK + j) * 32 * S::CK + lane * S::CK,
-                                    kp + 8 * r * S::ROW + 4 * j * S::CK);
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int j = 0; j < S::NV; ++j)
-                  copy_async<S::CV>(
-                      slot + S::TILE / 2 + (r * S::NV + j) * 32 * S::CV + lane * S::CV,
-                      vp + ((r & 1) + 8 * (r >> 1)) * S::ROW + 8 * j * S::CV);
-            } else {
-#pragma unroll
-              for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int j = 0; j < S::NK; ++j)
-                  copy_async_if<S::CK>(slot + (r * S::NK + j) * 32 * S::CK + lane * S::CK,
-                                       kp + 8 * r * row_bytes + 4 * j * S::CK,
-                                       g + 8 * r < left_rows && (4 * j + t4) * S::CK < row_bytes);
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int j = 0; j < S::NV; ++j) {
-                  const int row = (r & 1) + 8 * (r >> 1);
-                  copy_async_if<S::CV>(
-                      slot + S::TILE / 2 + (r * S::NV + j) * 32 * S::CV + lane * S::CV,
-                      vp + row * row_bytes + 8 * j * S::CV,
-                      2 * t4 + row < left_rows && (8 * j + g) * S::CV < row_bytes);
-                }
-            }
-            if constexpr (F != QAT_CACHE_BF16) {
-              // 16 scales of keys, of values, then the zero points: runs of 16 bytes
-              if (lane < (zeros ? 10 : 8)) {
-                const char* src = lane < 4 ? reinterpret_cast<const char*>(c.ks) + at * 64 + lane * 16
-                                  : lane < 8
-                                      ? reinterpret_cast<const char*>(c.vs) + at * 64 + lane * 16 - 64
-                                      : reinterpret_cast<const char*>(lane == 8 ? c.kz : c.vz) + at * 16;
-                copy_async<16>(slot + S::TILE + lane * 16, src);
-              }
+      // keys of tile `step` + 1 and values of tile `step`
+      auto issue = [&](int step, uint32_t k_slot, uint32_t v_slot) {
+        if (v_at >= 0) copy(ring + kRingEnd + v_slot, c.v, c.vs, c.vz, v_at, step);
+        v_at = -2;
+        if (++step < steps) {
+          if (step % 32 == 0) {
+            const int tile = from + step + lane;
+            place = -2;
+            if (tile < to) {
+              const int col = tile / tiles_page;
+              const int page = __ldg(a.table + (int64_t)b * a.table_stride + col);
+              place = page < 0 || page >= c.pages
+                          ? -1
+                          : ((int64_t)page * c.heads + kvh) * tiles_page + (tile - col * tiles_page);
             }
           }
+          v_at = __shfl_sync(kFull, place, step % 32);
+          if (v_at >= 0)
+            copy(ring + k_slot, c.k, c.ks, c.kz, v_at, step);
+          else
+            bad = true;
         }
         copy_commit();
       };
+      uint32_t k_next = 0, v_next = 0;  // slots that are filled next
+      auto advance = [&](uint32_t& at) {
+        at = at == kRingEnd - S::HALF_STAGE ? 0 : at + S::HALF_STAGE;
+      };
 #pragma unroll
-      for (int i = 0; i < S::STAGES - 1; ++i) issue(i, i * S::STAGE);
+      for (int i = -1; i < S::STAGES - 1; ++i) {
+        issue(i, k_next, v_next);
+        advance(k_next);
+        if (i >= 0) advance(v_next);
+      }
 
       // --- the queries as products take them ------------------------------------------
       uint32_t qr[S::kF32 ? 1 : HT][S::kF32 ? 1 : S::KS][2];
@@ -547,204 +543,226 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
           for (int j = 0; j < 4; ++j) o[ht][i][j] = 0.0f;
       }
 
-      uint32_t stage = 0, ahead = (S::STAGES - 1) * S::STAGE;
-      for (int step = 0; step < steps; ++step) {
-        copy_wait<S::STAGES - 2>();
-        __syncwarp();  // scales of other lanes' copies; and the slot of the step before is free
-        issue(step + S::STAGES - 1, ahead);
-        ahead = ahead == (S::STAGES - 1) * S::STAGE ? 0 : ahead + S::STAGE;
-        const char* const stage_p = ring_p + stage;
-        stage = stage == (S::STAGES - 1) * S::STAGE ? 0 : stage + S::STAGE;
+      // Scores of a tile: positions g, g + 8 (rows) and heads 2 t4, 2 t4 + 1 (columns).
+      float s[HT][4];
+      auto scores = [&](const char* slot) {
+        // (two sums: a product waits for the one before the last)
+        float acc[S::kF32 ? 3 : 2][HT][4];
 #pragma unroll
-        for (int t = 0; t < S::NT; ++t) {
-          const int tile = from + step * S::NT + t;
-          if (S::NT > 1 && tile >= to) break;
-          const char* const slot = stage_p + t * (S::TILE + S::PARAMS);
-          // scores of positions g, g + 8 (rows) and heads 2 t4, 2 t4 + 1 (columns)
-          float s[HT][4];
-          {
-            float acc[S::QP][HT][4];
-#pragma unroll
-            for (int p = 0; p < S::QP; ++p)
-#pragma unroll
-              for (int ht = 0; ht < HT; ++ht)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[p][ht][i] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < S::NK; ++j) {
-              uint32_t w[2][S::CK / 4];
-#pragma unroll
-              for (int r = 0; r < 2; ++r)
-                load_run<S::CK>(slot + (r * S::NK + j) * 32 * S::CK + lane * S::CK, w[r]);
-              uint32_t pr[2][S::CK / 4 * W::PAIRS];
-#pragma unroll
-              for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int i = 0; i < S::CK / 4; ++i) {
-                  uint32_t x[W::PAIRS];
-                  W::decode(w[r][i], x);
-#pragma unroll
-                  for (int k = 0; k < W::PAIRS; ++k) pr[r][i * W::PAIRS + k] = x[k];
-                }
-#pragma unroll
-              for (int k = 0; k < S::EK / 4; ++k) {
-                const int ks = j * (S::EK / 4) + k;
-                const uint32_t fa[4] = {pr[0][2 * k], pr[1][2 * k], pr[0][2 * k + 1],
-                                        pr[1][2 * k + 1]};
-                if constexpr (S::kF32) {
-#pragma unroll
-                  for (int p = 0; p < 3; ++p) {
-                    const uint2 f = qfrag[(p * S::KS + ks) * 32 + lane];
-                    mma<HALF>(acc[p][0], fa, f.x, f.y);
-                  }
-                } else {
-#pragma unroll
-                  for (int ht = 0; ht < HT; ++ht) mma<HALF>(acc[0][ht], fa, qr[ht][ks][0], qr[ht][ks][1]);
-                }
-              }
-            }
-#pragma unroll
-            for (int ht = 0; ht < HT; ++ht)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                s[ht][i] = acc[0][ht][i];
-                if constexpr (S::kF32) s[ht][i] += acc[1][ht][i] + acc[2][ht][i];
-              }
-          }
-          float vs[2] = {1.0f, 1.0f}, vz[2] = {0.0f, 0.0f}, kz[2] = {0.0f, 0.0f};
-          float ks[2] = {1.0f, 1.0f};
-          if constexpr (F != QAT_CACHE_BF16) {
-            const float* sc = reinterpret_cast<const float*>(slot + S::TILE);
-            ks[0] = sc[g], ks[1] = sc[g + 8], vs[0] = sc[16 + g], vs[1] = sc[24 + g];
-            if (zeros) {
-              const int8_t* z = reinterpret_cast<const int8_t*>(slot + S::TILE + 128);
-              kz[0] = z[g], kz[1] = z[g + 8], vz[0] = z[16 + g], vz[1] = z[24 + g];
-            }
-          }
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int ht = 0; ht < HT; ++ht)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                float& x = s[ht][2 * r + i];
-                if constexpr (kv_is_int(F)) x = __fmaf_rn(-kz[r], qsum[ht][i], x);
-                x *= F == QAT_CACHE_BF16 ? qscale[ht][i] : qscale[ht][i] * ks[r];
-              }
-          if (tile * 16 + 16 > length) {  // rows behind the sequence
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-              if (tile * 16 + g + 8 * r >= length) {
-                vs[r] = vz[r] = 0.0f;
-#pragma unroll
-                for (int ht = 0; ht < HT; ++ht) s[ht][2 * r] = s[ht][2 * r + 1] = -INFINITY;
-              }
-          }
-          // the maximum and the unit move only where a score or a scale is far above them
-          bool above = HALF && fmaxf(fabsf(vs[0]), fabsf(vs[1])) > v_limit;
+        for (int p = 0; p < (S::kF32 ? 3 : 2); ++p)
 #pragma unroll
           for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              above = above || fmaxf(s[ht][i], s[ht][2 + i]) > limit[ht][i];
-          if (__any_sync(kFull, above)) {
-            float shrink = 1.0f;
-            if constexpr (HALF) {
-              float top = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
+            for (int i = 0; i < 4; ++i) acc[p][ht][i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < S::NK; ++j) {
+          uint32_t w[2][S::CK / 4];
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            load_run<S::CK>(slot + 8 * r * S::ROW + (k_place ^ (j & 1) * 64) + j / 2 * 128, w[r]);
+          uint32_t pr[2][S::CK / 4 * W::PAIRS];
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < S::CK / 4; ++i) {
+              uint32_t x[W::PAIRS];
+              W::decode(w[r][i], x);
+#pragma unroll
+              for (int k = 0; k < W::PAIRS; ++k) pr[r][i * W::PAIRS + k] = x[k];
+            }
+#pragma unroll
+          for (int k = 0; k < S::EK / 4; ++k) {
+            const int ks = j * (S::EK / 4) + k;
+            const uint32_t fa[4] = {pr[0][2 * k], pr[1][2 * k], pr[0][2 * k + 1], pr[1][2 * k + 1]};
+            if constexpr (S::kF32) {
+#pragma unroll
+              for (int p = 0; p < 3; ++p) {
+                const uint2 f = qfrag[(p * S::KS + ks) * 32 + lane];
+                mma<HALF>(acc[p][0], fa, f.x, f.y);
+              }
+            } else {
+#pragma unroll
+              for (int ht = 0; ht < HT; ++ht)
+                mma<HALF>(acc[ks % 2][ht], fa, qr[ht][ks][0], qr[ht][ks][1]);
+            }
+          }
+        }
+#pragma unroll
+        for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[ht][i] = acc[0][ht][i] + acc[1][ht][i];
+            if constexpr (S::kF32) s[ht][i] += acc[2][ht][i];
+          }
+      };
+      // The tile's weights, as the second operand of the value products.
+      uint32_t wb[HT][S::PP][2];
+      float ks[2] = {1.0f, 1.0f}, kz[2] = {0.0f, 0.0f};
+      auto key_params = [&](const char* slot) {
+        if constexpr (F != QAT_CACHE_BF16) {
+          const float* sc = reinterpret_cast<const float*>(slot + S::TILE / 2);
+          ks[0] = sc[g], ks[1] = sc[g + 8];
+          if (zeros) {
+            const int8_t* z = reinterpret_cast<const int8_t*>(slot + S::TILE / 2 + 64);
+            kz[0] = z[g], kz[1] = z[g + 8];
+          }
+        }
+      };
+      auto weigh = [&](int tile, const char* v_slot) {
+        float vs[2] = {1.0f, 1.0f}, vz[2] = {0.0f, 0.0f};
+        if constexpr (F != QAT_CACHE_BF16) {
+          const float* sc = reinterpret_cast<const float*>(v_slot + S::TILE / 2);
+          vs[0] = sc[g], vs[1] = sc[g + 8];
+          if (zeros) {
+            const int8_t* z = reinterpret_cast<const int8_t*>(v_slot + S::TILE / 2 + 64);
+            vz[0] = z[g], vz[1] = z[g + 8];
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float& x = s[ht][2 * r + i];
+              if constexpr (kv_is_int(F)) x = __fmaf_rn(-kz[r], qsum[ht][i], x);
+              x *= F == QAT_CACHE_BF16 ? qscale[ht][i] : qscale[ht][i] * ks[r];
+            }
+        if (tile * 16 + 16 > length) {  // rows behind the sequence
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (tile * 16 + g + 8 * r >= length) {
+              vs[r] = vz[r] = 0.0f;
+#pragma unroll
+              for (int ht = 0; ht < HT; ++ht) s[ht][2 * r] = s[ht][2 * r + 1] = -INFINITY;
+            }
+        }
+        // the maximum and the unit move only where a score or a scale is far above them
+        bool above = HALF && fmaxf(fabsf(vs[0]), fabsf(vs[1])) > v_limit;
+#pragma unroll
+        for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            above = above || fmaxf(s[ht][i], s[ht][2 + i]) > limit[ht][i];
+        if (__any_sync(kFull, above)) {
+          float shrink = 1.0f;
+          if constexpr (HALF) {
+            float top = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+            if (top > v_limit) {  // to between 16 and 32
+              const int e = top < 0x1p-100f ? -100 : exponent_of(top);
+              const int by = 4 - e - exponent_of(unit);
+              if (v_limit >= 0.0f) shrink = power_of_two(max(by, -126));
+              unit = power_of_two(4 - e);
+              v_limit = power_of_two(min(e + 3, 127));
+            }
+          }
+#pragma unroll
+          for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float top = fmaxf(s[ht][i], s[ht][2 + i]);
 #pragma unroll
               for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
-              if (top > v_limit) {  // to between 16 and 32
-                const int e = top < 0x1p-100f ? -100 : exponent_of(top);
-                const int by = 4 - e - exponent_of(unit);
-                if (v_limit >= 0.0f) shrink = power_of_two(max(by, -126));
-                unit = power_of_two(4 - e);
-                v_limit = power_of_two(min(e + 3, 127));
-              }
+              top = fmaxf(top, m[ht][i]);
+              const float was = m[ht][i] == top ? 1.0f : exp2_fast(m[ht][i] - top);
+              m[ht][i] = top;
+              limit[ht][i] = top + kSlack;
+              base[ht][i] = top == -INFINITY ? 0.0f : top;
+              l[ht][i] *= was;
+              const float both = was * shrink;
+              zsum[ht][i] *= both;
+#pragma unroll
+              for (int j = 0; j < S::MT; ++j) o[ht][j][i] *= both, o[ht][j][2 + i] *= both;
+            }
+        }
+        if constexpr (HALF) vs[0] *= unit, vs[1] *= unit;
+#pragma unroll
+        for (int ht = 0; ht < HT; ++ht) {
+          float w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p = exp2_fast(s[ht][i] - base[ht][i & 1]);
+            l[ht][i & 1] += p;
+            w[i] = p;
+            if constexpr (F != QAT_CACHE_BF16) w[i] *= vs[i >> 1];
+            if constexpr (kv_is_int(F))
+              zsum[ht][i & 1] = __fmaf_rn(w[i], vz[i >> 1], zsum[ht][i & 1]);
+          }
+#pragma unroll
+          for (int p = 0; p < S::PP; ++p)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              wb[ht][p][r] = transpose8(take_pair<HALF>(w[2 * r], w[2 * r + 1]));
+        }
+      };
+      // Weighted values: rows are head elements, k the positions.
+      auto values = [&](const char* slot) {
+#pragma unroll
+        for (int j = 0; j < S::NV; ++j) {
+          uint32_t v[4][S::CV / 4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            load_run<S::CV>(slot + (r >> 1) * 8 * S::ROW + v_places[r & 1] + 128 * j, v[r]);
+#pragma unroll
+          for (int i = 0; i < S::CV / 4; ++i) {
+            uint32_t pr[2][2 * W::PAIRS];  // positions 2 t4, + 1; and those + 8
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t x[W::PAIRS];
+              W::decode(__byte_perm(v[2 * k][i], v[2 * k + 1][i], W::kLower), x);
+#pragma unroll
+              for (int q = 0; q < W::PAIRS; ++q) pr[k][q] = x[q];
+              W::decode(__byte_perm(v[2 * k][i], v[2 * k + 1][i], W::kUpper), x);
+#pragma unroll
+              for (int q = 0; q < W::PAIRS; ++q) pr[k][W::PAIRS + q] = x[q];
             }
 #pragma unroll
-            for (int ht = 0; ht < HT; ++ht)
+            for (int q = 0; q < W::PAIRS; ++q) {
+              const int mt = (j * (S::CV / 4) + i) * W::PAIRS + q;
+              const uint32_t fa[4] = {pr[0][2 * q], pr[0][2 * q + 1], pr[1][2 * q], pr[1][2 * q + 1]};
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                float top = fmaxf(s[ht][i], s[ht][2 + i]);
+              for (int ht = 0; ht < HT; ++ht) {
+                if constexpr (S::kF32) {
+                  // (sums of many tiles on the tensor cores would drift: 16 positions only)
+                  float part[4] = {};
 #pragma unroll
-                for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
-                top = fmaxf(top, m[ht][i]);
-                const float was = m[ht][i] == top ? 1.0f : exp2_fast(m[ht][i] - top);
-                m[ht][i] = top;
-                limit[ht][i] = top + kSlack;
-                base[ht][i] = top == -INFINITY ? 0.0f : top;
-                l[ht][i] *= was;
-                const float both = was * shrink;
-                zsum[ht][i] *= both;
+                  for (int p = S::PP - 1; p >= 0; --p) mma<HALF>(part, fa, wb[ht][p][0], wb[ht][p][1]);
 #pragma unroll
-                for (int j = 0; j < S::MT; ++j) o[ht][j][i] *= both, o[ht][j][2 + i] *= both;
-              }
-          }
-          if constexpr (HALF) vs[0] *= unit, vs[1] *= unit;
-          // weights, as the second operand of the value products
-          uint32_t wb[HT][S::PP][2];
+                  for (int x = 0; x < 4; ++x) o[ht][mt][x] += part[x];
+                } else {
 #pragma unroll
-          for (int ht = 0; ht < HT; ++ht) {
-            float w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float p = exp2_fast(s[ht][i] - base[ht][i & 1]);
-              l[ht][i & 1] += p;
-              w[i] = p;
-              if constexpr (F != QAT_CACHE_BF16) w[i] *= vs[i >> 1];
-              if constexpr (kv_is_int(F))
-                zsum[ht][i & 1] = __fmaf_rn(w[i], vz[i >> 1], zsum[ht][i & 1]);
-            }
-#pragma unroll
-            for (int p = 0; p < S::PP; ++p)
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                wb[ht][p][r] = transpose8(take_pair<HALF>(w[2 * r], w[2 * r + 1]));
-              }
-          }
-          // weighted values: rows are head elements, k the positions
-#pragma unroll
-          for (int j = 0; j < S::NV; ++j) {
-            uint32_t v[4][S::CV / 4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              load_run<S::CV>(slot + S::TILE / 2 + (r * S::NV + j) * 32 * S::CV + lane * S::CV, v[r]);
-#pragma unroll
-            for (int i = 0; i < S::CV / 4; ++i) {
-              uint32_t pr[2][2 * W::PAIRS];  // positions 2 t4, + 1; and those + 8
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                uint32_t x[W::PAIRS];
-                W::decode(__byte_perm(v[2 * k][i], v[2 * k + 1][i], W::kLower), x);
-#pragma unroll
-                for (int q = 0; q < W::PAIRS; ++q) pr[k][q] = x[q];
-                W::decode(__byte_perm(v[2 * k][i], v[2 * k + 1][i], W::kUpper), x);
-#pragma unroll
-                for (int q = 0; q < W::PAIRS; ++q) pr[k][W::PAIRS + q] = x[q];
-              }
-#pragma unroll
-              for (int q = 0; q < W::PAIRS; ++q) {
-                const int mt = (j * (S::CV / 4) + i) * W::PAIRS + q;
-                const uint32_t fa[4] = {pr[0][2 * q], pr[0][2 * q + 1], pr[1][2 * q],
-                                        pr[1][2 * q + 1]};
-#pragma unroll
-                for (int ht = 0; ht < HT; ++ht) {
-                  if constexpr (S::kF32) {
-                    // (sums of many tiles on the tensor cores would drift: 16 positions only)
-                    float part[4] = {};
-#pragma unroll
-                    for (int p = S::PP - 1; p >= 0; --p) mma<HALF>(part, fa, wb[ht][p][0], wb[ht][p][1]);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) o[ht][mt][x] += part[x];
-                  } else {
-#pragma unroll
-                    for (int p = 0; p < S::PP; ++p) mma<HALF>(o[ht][mt], fa, wb[ht][p][0], wb[ht][p][1]);
-                  }
+                  for (int p = 0; p < S::PP; ++p) mma<HALF>(o[ht][mt], fa, wb[ht][p][0], wb[ht][p][1]);
                 }
               }
             }
           }
         }
+      };
+
+      // A tile's scores are computed beside the weighted values of the tile before: one
+      // chain of products alone would leave the warp waiting.
+      uint32_t k_at = 0, v_slot = 0;
+      copy_wait<S::STAGES - 1>();
+      __syncwarp();  // (scales are other lanes' copies)
+      scores(ring_p);
+      key_params(ring_p);
+      advance(k_at);
+      for (int step = 0; step < steps; ++step) {
+        copy_wait<S::STAGES - 2>();
+        __syncwarp();  // also: the slots of the step before are free
+        weigh(from + step, ring_p + kRingEnd + v_slot);
+        issue(step + S::STAGES - 1, k_next, v_next);
+        advance(k_next);
+        advance(v_next);
+        if (step + 1 < steps) {
+          scores(ring_p + k_at);
+          key_params(ring_p + k_at);
+        }
+        values(ring_p + kRingEnd + v_slot);
+        advance(k_at);
+        advance(v_slot);
       }
       copy_wait<0>();
       __syncwarp();  // (the next piece's copies write where other lanes read scales)
