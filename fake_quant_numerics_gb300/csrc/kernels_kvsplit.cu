@@ -202,7 +202,9 @@ struct Shape {
   static constexpr int HALF_STAGE = (TILE + PARAMS) / 2;
   static constexpr int STAGES = smaller(6, larger(2, 13 * 1024 / (TILE + PARAMS)));
   static constexpr int H = 8 * HT, KS = DP / 16, MT = DP / 16;
-  static constexpr int QP = kF32 ? 3 : 1, PP = kF32 ? 3 : 2;  // 16-bit parts of q and of the weights
+  // 16-bit parts of q and of the weights.  One of fp16 holds a weight to 2^-12, an eighth
+  // of what a bf16 output's own rounding is off; bf16 takes two for that.
+  static constexpr int QP = kF32 ? 3 : 1, PP = kF32 ? 3 : F == QAT_CACHE_BF16 ? 2 : 1;
   static constexpr int QFRAG = kF32 ? QP * KS * 32 * 8 : 0;
   // A warp's ring and queries, then the part it starts with (its run began inside a
   // sequence); the part it ends with takes the ring's place.
@@ -382,6 +384,11 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
   const int c_unit = EXACT ? lane % S::UNITS : lane - c_row * units;
   const int c_place = S::place(c_row, c_unit * 16), k_place = S::place(g, t4 * S::CK);
   const int v_places[2] = {S::place(2 * t4, g * S::CV), S::place(2 * t4 + 1, g * S::CV)};
+  // 16 scales a tile, then the zero points: lanes 0 to 3 and 4 take 16 bytes each
+  const char* const k_params =
+      lane == 4 ? reinterpret_cast<const char*>(c.kz) : reinterpret_cast<const char*>(c.ks) + lane * 16;
+  const char* const v_params =
+      lane == 4 ? reinterpret_cast<const char*>(c.vz) : reinterpret_cast<const char*>(c.vs) + lane * 16;
   if (!EXACT) {  // elements behind head_dim stay zeros (never NaN, whose product with 0 is NaN)
     for (int i = lane * 16; i < 2 * (int)kRingEnd; i += 512)
       *reinterpret_cast<uint4*>(ring_p + i) = make_uint4(0, 0, 0, 0);
@@ -406,17 +413,18 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
       bool bad = false;
       // 16 rows, their scales and zero points.  Where rows lie behind the sequence the
       // last unit before them is read in their stead: they have no weight.
-      auto copy = [&](uint32_t slot, const char* codes, const float* scales, const int8_t* zps,
-                      int64_t at, int step) {
+      auto copy = [&](uint32_t slot, const char* codes, const char* params, int64_t at, int step) {
         const char* src = codes + at * (16 * row_bytes);
-        const int last = min(16, length - (from + step) * 16) * row_bytes - 16;
-        if constexpr (EXACT) {
+        const int rows = length - (from + step) * 16;
+        if (EXACT && rows >= 16) {
+          src += lane * 16;
 #pragma unroll
           for (int i = 0; i < S::LOADS; ++i)
-            copy_async(slot + 512 * i + (c_place ^ S::mix(i * 32 / S::UNITS) * 16),
-                           src + min(lane * 16 + 512 * i, last));
+            copy_async(slot + 512 * i + (c_place ^ S::mix(i * 32 / S::UNITS) * 16), src + 512 * i);
         } else {
+          const int last = min(16, rows) * row_bytes - 16;
           int r = c_row, u = c_unit;
+#pragma unroll 1
           for (int i = lane; i < 16 * units; i += 32) {
             copy_async(slot + S::place(r, u * 16), src + min(i * 16, last));
             r += 32 / units, u += 32 % units;
@@ -424,16 +432,13 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
           }
         }
         if constexpr (F != QAT_CACHE_BF16) {
-          if (lane < (zeros ? 5 : 4)) {
-            src = reinterpret_cast<const char*>(scales) + at * 64 + lane * 16;
-            if (lane == 4) src = reinterpret_cast<const char*>(zps) + at * 16;
-            copy_async(slot + S::TILE / 2 + lane * 16, src);
-          }
+          if (lane < (zeros ? 5 : 4))
+            copy_async(slot + S::TILE / 2 + lane * 16, params + at * (lane == 4 ? 16 : 64));
         }
       };
       // keys of tile `step` + 1 and values of tile `step`
       auto issue = [&](int step, uint32_t k_slot, uint32_t v_slot) {
-        if (v_at >= 0) copy(ring + kRingEnd + v_slot, c.v, c.vs, c.vz, v_at, step);
+        if (v_at >= 0) copy(ring + kRingEnd + v_slot, c.v, v_params, v_at, step);
         v_at = -2;
         if (++step < steps) {
           if (step % 32 == 0) {
@@ -449,22 +454,18 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
           }
           v_at = __shfl_sync(kFull, place, step % 32);
           if (v_at >= 0)
-            copy(ring + k_slot, c.k, c.ks, c.kz, v_at, step);
+            copy(ring + k_slot, c.k, k_params, v_at, step);
           else
             bad = true;
         }
         copy_commit();
       };
-      uint32_t k_next = 0, v_next = 0;  // slots that are filled next
-      auto advance = [&](uint32_t& at) {
-        at = at == kRingEnd - S::HALF_STAGE ? 0 : at + S::HALF_STAGE;
+      auto after = [&](uint32_t slot) {
+        return slot == kRingEnd - S::HALF_STAGE ? 0 : slot + S::HALF_STAGE;
       };
 #pragma unroll
-      for (int i = -1; i < S::STAGES - 1; ++i) {
-        issue(i, k_next, v_next);
-        advance(k_next);
-        if (i >= 0) advance(v_next);
-      }
+      for (int i = -1; i < S::STAGES - 1; ++i)
+        issue(i, (i + 1) * S::HALF_STAGE, max(i, 0) * S::HALF_STAGE);
 
       // --- the queries as products take them ------------------------------------------
       uint32_t qr[S::kF32 ? 1 : HT][S::kF32 ? 1 : S::KS][2];
@@ -743,26 +744,22 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
 
       // A tile's scores are computed beside the weighted values of the tile before: one
       // chain of products alone would leave the warp waiting.
-      uint32_t k_at = 0, v_slot = 0;
+      uint32_t prev = kRingEnd - S::HALF_STAGE, slot = 0, next = after(0);  // of this step
       copy_wait<S::STAGES - 1>();
       __syncwarp();  // (scales are other lanes' copies)
       scores(ring_p);
       key_params(ring_p);
-      advance(k_at);
       for (int step = 0; step < steps; ++step) {
         copy_wait<S::STAGES - 2>();
-        __syncwarp();  // also: the slots of the step before are free
-        weigh(from + step, ring_p + kRingEnd + v_slot);
-        issue(step + S::STAGES - 1, k_next, v_next);
-        advance(k_next);
-        advance(v_next);
+        __syncwarp();  // also: this step's keys and the values of the step before are done with
+        weigh(from + step, ring_p + kRingEnd + slot);
+        issue(step + S::STAGES - 1, slot, prev);
         if (step + 1 < steps) {
-          scores(ring_p + k_at);
-          key_params(ring_p + k_at);
+          scores(ring_p + next);
+          key_params(ring_p + next);
         }
-        values(ring_p + kRingEnd + v_slot);
-        advance(k_at);
-        advance(v_slot);
+        values(ring_p + kRingEnd + slot);
+        prev = slot, slot = next, next = after(next);
       }
       copy_wait<0>();
       __syncwarp();  // (the next piece's copies write where other lanes read scales)

@@ -696,8 +696,10 @@ qat_status qat_kv_read(const qat_kv_cache* cache, const int64_t* slots, int64_t 
  * entries behind its last page are not read.  A length <= 0 gives y = 0 and lse =
  * -inf.  A length that the table's row cannot hold or that is above 2^31 - 1025, or a
  * page outside [0, pages), makes that sequence's outputs NaN.
- * The codes' products with q are exact and summed in binary32, as are those with
- * the softmax's weights, which keep 16 bits for a bf16 y and 24 for a float one.
+ * The codes' products with q and with the softmax's weights are summed in binary32.
+ * q keeps all its bits down to 2^-38 of its head's largest element (of a bf16 cache,
+ * all).  Under a bf16 y a weight is rounded once to the 11 bits of fp16 (two bf16 parts
+ * for a bf16 cache); under a float one it keeps 24.
  * q_heads a multiple of the cache's heads (QAT_ERR_DIMENSION_MISMATCH); scale
  * finite; batch up to 65535, batch * q_heads and table_cols below 2^31.  workspace:
  * qat_kv_attention_workspace_bytes(cache, q_heads) bytes, 16-byte aligned: partial
