@@ -257,8 +257,8 @@ class KVCache:
             raise TypeError(f"a cache in {format} holds {dtype}")
         if k.shape[2] < 16 or k.shape[2] % 16:
             raise ValueError(f"page size {k.shape[2]} must be a multiple of 16")
-        if not 1 <= k.shape[1] <= 65535 or k.shape[0] * k.shape[2] >= 1 << 31:
-            raise ValueError("a cache has 1 to 65535 heads and less than 2^31 positions")
+        if not 1 <= k.shape[1] <= 32767 or k.shape[0] * k.shape[2] >= 1 << 31:
+            raise ValueError("a cache has 1 to 32767 heads and less than 2^31 positions")
         if (k_scale is None) != (format == "bf16") or (v_scale is None) != (format == "bf16"):
             raise ValueError("quantized rows have scales, bf16 rows none")
         if (k_zero_point is None) != (v_zero_point is None) or (k_zero_point is not None

@@ -36,200 +36,293 @@ int kv_lanes(int units) {
   return lanes;
 }
 
+// (an index that is not known would put the parameters into local memory)
+template <typename A>
+__device__ __forceinline__ A one(A const (&two)[2], int which) {
+  return which ? two[1] : two[0];
+}
 // The row of a slot and head: [page][head][offset].
 __device__ __forceinline__ int64_t kv_row(const KvPlace& p, int64_t slot, int head) {
   const int page = (int)slot / p.page_size;  // slots fit 31 bits
   return ((int64_t)page * p.heads + head) * p.page_size + ((int)slot - page * p.page_size);
 }
 
-// Half `i` of a lane's unit: 8 elements from a run's start.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const void* x, int64_t at, float* v) {
-  if constexpr (!VEC) {
+// A lane's 16 elements of a row, as they lie in memory; elements behind the row's end
+// are zeros.  How they are loaded: one by one, 16 bytes at a time, or 32 (bf16).
+enum { kSingle = 0, kVec16 = 1, kVec32 = 2 };
+template <typename T>
+struct Unit {
+  V32 v[T::BYTES / 2];
+  template <int HOW>
+  __device__ __forceinline__ void load(const void* x, int64_t at, int left) {
+    const char* p = static_cast<const char*>(x) + at * T::BYTES;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = ld_elem<T>(x, at + e);
-  } else if constexpr (T::BYTES == 2) {
-    const uint4 r = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(x) + at * 2));
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    for (int i = 0; i < T::BYTES / 2; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      v[e] = __uint_as_float(w[e / 2] << 16);
-      v[e + 1] = __uint_as_float(w[e / 2] & 0xffff0000u);
-    }
-  } else {
+      for (int j = 0; j < 8; ++j) v[i].w[j] = 0u;
+    if constexpr (HOW == kVec32) {
+      if (left > 0) v[0] = ld_v32(p);
+    } else if constexpr (HOW == kVec16) {
+      constexpr int E = 16 / T::BYTES;  // elements a load
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float4 r =
-          __ldg(reinterpret_cast<const float4*>(static_cast<const char*>(x) + at * 4) + j);
-      v[4 * j] = r.x, v[4 * j + 1] = r.y, v[4 * j + 2] = r.z, v[4 * j + 3] = r.w;
-    }
-  }
-}
-
-template <typename T, int F, bool AFFINE, bool VEC>
-__global__ void __launch_bounds__(kKvThreads) k_kv_write(KvRows x, KvPlace p, int64_t rows,
-                                                         const int64_t* slots, int lanes) {
-  const int lane = threadIdx.x & (lanes - 1);
-  const int64_t row = ((int64_t)blockIdx.x * kKvThreads + threadIdx.x) / lanes;
-  int64_t slot = -1, token = 0;
-  int which = 0, head = 0;
-  if (row < rows) {
-    token = row / (2 * p.heads);
-    const int r = (int)(row - token * 2 * p.heads);
-    which = r >= p.heads;
-    head = r - which * p.heads;
-    slot = __ldg(slots + token);
-  }
-  const bool on = slot >= 0 && slot < p.slots;
-  float v[16];
-  const int e0 = 16 * lane;
-  const int64_t from = token * x.token_stride[which] + head * x.head_stride[which] + e0;
-  const void* src = which ? x.v : x.k;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] = 0.0f;
-  if (on && e0 < p.d) load8<T, VEC>(src, from, v);
-  if (on && e0 + 8 < p.d) load8<T, VEC>(src, from + 8, v + 8);
-  const int64_t to = on ? kv_row(p, slot, head) : 0;
-  uint32_t w[8];
-  if constexpr (F == QAT_CACHE_BF16) {
-#pragma unroll
-    for (int e = 0; e < 16; e += 2) w[e / 2] = pack_bf16x2(v[e], v[e + 1]);
-  } else {
-    constexpr int BITS = F == QAT_CACHE_INT4 ? 4 : 8;
-    constexpr int qmin = QRange<BITS, AFFINE>::qmin, qmax = QRange<BITS, AFFINE>::qmax;
-    // Extremes over the finite elements and zero, and whether all are finite.
-    float lo = 0.0f, hi = 0.0f;
-    int bad = 0;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      bad |= (__float_as_uint(v[e]) & 0x7f800000u) == 0x7f800000u;
-      if (AFFINE) lo = fminf(lo, v[e]);
-      hi = fmaxf(hi, AFFINE ? v[e] : fabsf(v[e]));
-    }
-    for (int o = lanes >> 1; o; o >>= 1) {
-      if (AFFINE) lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
-      bad |= __shfl_xor_sync(kFull, bad, o);
-    }
-    float scale, zp = 0.0f;
-    if constexpr (kv_is_int(F)) {
-      scale = __fdiv_rn(AFFINE ? __fsub_rn(hi, lo) : hi, (float)(AFFINE ? qmax - qmin : qmax));
+      for (int i = 0; i < 16 / E; ++i)
+        if (i * E < left) {
+          const uint4 r = __ldg(reinterpret_cast<const uint4*>(p) + i);
+          uint32_t* w = v[i / 2].w + 4 * (i % 2);
+          w[0] = r.x, w[1] = r.y, w[2] = r.z, w[3] = r.w;
+        }
     } else {
-      scale = __fdiv_rn(hi, F == QAT_CACHE_E4M3 ? 448.0f : 57344.0f);
-    }
-    if (bad || isinf(scale)) scale = __uint_as_float(0x7fc00000u);
-    const bool usable = scale > 0.0f;
-    if (AFFINE && usable)
-      zp = fminf(fmaxf(rintf(__fsub_rn((float)qmin, __fdiv_rn(lo, scale))), (float)qmin),
-                 (float)qmax);
-    const bool fast = quot_scale_ok(scale);
-    const float rcp = fast ? __frcp_rn(scale) : 0.0f;
-    float q[16];
-#pragma unroll
-    for (int e = 0; e < 16; e += 2) {
-      if (fast) {
-        quotient_rn2(v[e], v[e + 1], rcp, -scale, q[e], q[e + 1]);
-      } else {
-        q[e] = usable ? __fdiv_rn(v[e], scale) : 0.0f;
-        q[e + 1] = usable ? __fdiv_rn(v[e + 1], scale) : 0.0f;
-      }
-    }
-    if constexpr (kv_is_int(F)) {
-      uint32_t c[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const float k = fminf(fmaxf(__fadd_rn(rintf(q[e]), zp), (float)qmin), (float)qmax);
-        // (a row's padding is code 0, whatever its zero point)
-        c[e] = e0 + e < p.d && usable ? (uint32_t)(int)k : 0u;
+        if (e >= left) break;
+        const uint32_t b = load_elem_bits<T>(x, at + e);
+        if (T::BYTES == 4)
+          v[e / 8].w[e % 8] = b;
+        else
+          v[0].w[e / 2] |= e & 1 ? b & 0xffff0000u : b >> 16;
       }
-#pragma unroll
-      for (int j = 0; j < 16 / (32 / BITS); ++j) {
-        uint32_t word = 0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          if (BITS == 8)
-            word |= (c[4 * j + b] & 255u) << (8 * b);
-          else
-            word |= ((c[8 * j + 2 * b] & 15u) << 4 | (c[8 * j + 2 * b + 1] & 15u)) << (8 * b);
-        }
-        w[j] = word;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = usable ? fp8_pair<F>(q[4 * j], q[4 * j + 1]) | fp8_pair<F>(q[4 * j + 2], q[4 * j + 3]) << 16 : 0u;
-    }
-    if (on && lane == 0) {
-      p.scales[which][to] = scale;
-      if (AFFINE) p.zps[which][to] = (int8_t)zp;
     }
   }
-  constexpr int UB = kv_unit_bytes(F);
-  char* dst = static_cast<char*>(p.codes[which]) + to * p.row_bytes + lane * UB;
-  const int left = p.row_bytes - lane * UB;
-  if (!on || left <= 0) return;
-  if constexpr (UB == 8) {
-    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-  } else {
-    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-    if (UB == 32 && left > 16)
-      *reinterpret_cast<uint4*>(dst + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+  __device__ __forceinline__ float get(int e) const {
+    return elem<T>(v[T::BYTES == 4 ? e / 8 : 0], T::BYTES == 4 ? e % 8 : e);
+  }
+  // max |x|, NaN where one is; and the extremes beside zero
+  __device__ __forceinline__ float top() const {
+    if constexpr (T::BYTES == 2) {
+      uint32_t m = 0u;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = bf16x2_max_nan(m, v[0].w[k] & 0x7fff7fffu);
+      return fmax_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    } else {
+      float m = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) m = fmax3_nan(m, fabsf(get(e)), fabsf(get(e + 1)));
+      return m;
+    }
+  }
+  __device__ __forceinline__ void range(float& lo, float& hi) const {
+    if constexpr (T::BYTES == 2) {
+      uint32_t a = 0u, b = 0u;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(v[0].w[k]));
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(v[0].w[k]));
+      }
+      lo = fmin3_nan(0.0f, __uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+      hi = fmax3_nan(0.0f, __uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+    } else {
+      lo = hi = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        lo = fmin3_nan(lo, get(e), get(e + 1));
+        hi = fmax3_nan(hi, get(e), get(e + 1));
+      }
+    }
+  }
+};
+
+// Blocks (x: tokens, y: runs of U rows of the token's keys, then values), a group of
+// lanes a token; the U rows are loaded together.
+template <typename T, int F, bool AFFINE, int HOW, int U>
+__global__ void __launch_bounds__(kKvThreads) k_kv_write(KvRows x, KvPlace p, int64_t tokens,
+                                                         const int64_t* slots, int lanes) {
+  const int lane = threadIdx.x & (lanes - 1);
+  const int64_t token = (int64_t)blockIdx.x * (kKvThreads / lanes) + threadIdx.x / lanes;
+  int64_t slot = token < tokens ? __ldg(slots + token) : -1;
+  if (slot >= p.slots) slot = -1;
+  const int left = p.d - 16 * lane;  // elements from this lane's on
+  Unit<T> unit[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int row = blockIdx.y * U + i;
+    const int which = row >= p.heads, head = row - (which ? p.heads : 0);
+    unit[i].template load<HOW>(
+        which ? x.v : x.k, token * one(x.token_stride, which) + head * one(x.head_stride, which) + 16 * lane,
+        slot >= 0 && row < 2 * p.heads ? left : 0);
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int row = blockIdx.y * U + i;
+    const int which = row >= p.heads, head = row - (which ? p.heads : 0);
+    const bool on = slot >= 0 && row < 2 * p.heads;
+    const int64_t to = on ? kv_row(p, slot, head) : 0;
+    const Unit<T>& u = unit[i];
+    uint32_t w[8];
+    if constexpr (F == QAT_CACHE_BF16) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) w[e / 2] = pack_bf16x2(u.get(e), u.get(e + 1));
+    } else {
+      constexpr int BITS = F == QAT_CACHE_INT4 ? 4 : 8;
+      constexpr int qmin = QRange<BITS, AFFINE>::qmin, qmax = QRange<BITS, AFFINE>::qmax;
+      float lo = 0.0f, hi;
+      if constexpr (AFFINE)
+        u.range(lo, hi);
+      else
+        hi = u.top();
+      for (int o = lanes >> 1; o; o >>= 1) {
+        if (AFFINE) {
+          const float other = __shfl_xor_sync(kFull, lo, o);
+          lo = fmin3_nan(lo, lo, other);
+        }
+        hi = fmax_nan(hi, __shfl_xor_sync(kFull, hi, o));
+      }
+      // (a NaN or an infinity in the row is one here, and the scale not finite)
+      float scale, zp = 0.0f;
+      if constexpr (kv_is_int(F))
+        scale = __fdiv_rn(AFFINE ? __fsub_rn(hi, lo) : hi, (float)(AFFINE ? qmax - qmin : qmax));
+      else
+        scale = __fdiv_rn(hi, F == QAT_CACHE_E4M3 ? 448.0f : 57344.0f);
+      if (!(scale < __uint_as_float(0x7f800000u))) scale = __uint_as_float(0x7fc00000u);
+      const bool usable = scale > 0.0f;
+      if (AFFINE && usable)
+        zp = fminf(fmaxf(rintf(__fsub_rn((float)qmin, __fdiv_rn(lo, scale))), (float)qmin),
+                   (float)qmax);
+      float q[16];
+      if (quot_scale_ok(scale)) {
+        const float rcp = __frcp_rn(scale);
+#pragma unroll
+        for (int e = 0; e < 16; e += 2)
+          quotient_rn2(u.get(e), u.get(e + 1), rcp, -scale, q[e], q[e + 1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) q[e] = usable ? __fdiv_rn(u.get(e), scale) : 0.0f;
+      }
+      if constexpr (kv_is_int(F)) {
+        // rint by the magic constant (|q| stays below 2^9), then the zero point.  Packing
+        // saturates, which is an affine code's clamp; a symmetric one's quotient can pass
+        // qmax only where the scale is subnormal.
+        const uint32_t bias = kRintMagicBits - (uint32_t)(int)zp;
+        const bool clamp = !AFFINE && scale < 0x1p-126f;
+#pragma unroll
+        for (int j = 0; j < BITS / 2; ++j) w[j] = 0u;
+#pragma unroll
+        for (int e = 14; e >= 0; e -= 2) {
+          float a, b;
+          add2(q[e], q[e + 1], kRintMagic, kRintMagic, a, b);
+          int qa = (int)(__float_as_uint(a) - bias), qb = (int)(__float_as_uint(b) - bias);
+          if (clamp) qa = min(max(qa, qmin), qmax), qb = min(max(qb, qmin), qmax);
+          if (BITS == 8)
+            w[e / 4] = pack_s8x2(qb, qa, w[e / 4]);
+          else
+            w[e / 8] = pack_s4x2(qa, qb, w[e / 8]);
+        }
+        // a row's padding, and a row without a scale, is code 0 whatever its zero point
+        const int codes = usable ? left : 0;
+#pragma unroll
+        for (int j = 0; j < BITS / 2; ++j) {
+          const int n = (codes - j * 32 / BITS) * BITS;  // bits of the word in use
+          if (n < 32) w[j] = n <= 0 ? 0u : w[j] & (0xffffffffu >> (32 - n));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = usable ? fp8_pair<F>(q[4 * j], q[4 * j + 1]) | fp8_pair<F>(q[4 * j + 2], q[4 * j + 3]) << 16
+                        : 0u;
+      }
+      if (on && lane == 0) {
+        one(p.scales, which)[to] = scale;
+        if (AFFINE) one(p.zps, which)[to] = (int8_t)zp;
+      }
+    }
+    constexpr int UB = kv_unit_bytes(F);
+    char* dst = static_cast<char*>(one(p.codes, which)) + to * p.row_bytes + lane * UB;
+    const int bytes = on ? p.row_bytes - lane * UB : 0;
+    if (bytes <= 0) continue;
+    if constexpr (UB == 8) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    } else {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (UB == 32 && bytes > 16)
+        *reinterpret_cast<uint4*>(dst + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
   }
 }
 
-template <typename T, int F>
-__global__ void __launch_bounds__(kKvThreads) k_kv_read(KvPlace p, int64_t rows,
+// The same walk the other way.  WIDE: rows start on 32 bytes and hold whole units.
+template <typename T, int F, bool WIDE, int U>
+__global__ void __launch_bounds__(kKvThreads) k_kv_read(KvPlace p, int64_t tokens,
                                                         const int64_t* slots, int lanes, void* k,
                                                         void* v) {
   const int lane = threadIdx.x & (lanes - 1);
-  const int64_t row = ((int64_t)blockIdx.x * kKvThreads + threadIdx.x) / lanes;
-  const int e0 = 16 * lane;
-  if (row >= rows || e0 >= p.d) return;
-  const int64_t token = row / (2 * p.heads);
-  const int r = (int)(row - token * 2 * p.heads);
-  const int which = r >= p.heads, head = r - which * p.heads;
+  const int64_t token = (int64_t)blockIdx.x * (kKvThreads / lanes) + threadIdx.x / lanes;
+  const int left = p.d - 16 * lane;
+  if (token >= tokens || left <= 0) return;
   const int64_t slot = __ldg(slots + token);
-  const bool two = e0 + 8 < p.d;
-  float x[16];
+  const bool there = slot >= 0 && slot < p.slots;
+  constexpr int UB = kv_unit_bytes(F);
+  uint32_t w[U][UB / 4];
+  float scale[U];
+  int zp[U];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) x[e] = 0.0f;
-  if (slot >= 0 && slot < p.slots) {
-    constexpr int UB = kv_unit_bytes(F);
+  for (int i = 0; i < U; ++i) {
+    const int row = blockIdx.y * U + i;
+    const int which = row >= p.heads, head = row - (which ? p.heads : 0);
+#pragma unroll
+    for (int j = 0; j < UB / 4; ++j) w[i][j] = 0u;
+    scale[i] = 0.0f, zp[i] = 0;
+    if (!there || row >= 2 * p.heads) continue;
     const int64_t from = kv_row(p, slot, head);
-    const char* src = static_cast<const char*>(p.codes[which]) + from * p.row_bytes + lane * UB;
-    uint32_t w[8] = {};
+    const char* src = static_cast<const char*>(one(p.codes, which)) + from * p.row_bytes + lane * UB;
     if constexpr (UB == 8) {
       const uint2 a = *reinterpret_cast<const uint2*>(src);
-      w[0] = a.x, w[1] = a.y;
+      w[i][0] = a.x, w[i][1] = a.y;
     } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(src);
-      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-      if (UB == 32 && two) {
-        const uint4 b = *reinterpret_cast<const uint4*>(src + 16);
-        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-      }
-    }
-    const float scale = F == QAT_CACHE_BF16 ? 1.0f : p.scales[which][from];
-    const int zp = kv_is_int(F) && p.zps[which] ? p.zps[which][from] : 0;
-    kv_decode<F, 16>(w, scale, zp, x);
-  }
-  char* dst = static_cast<char*>(which ? v : k) +
-              ((token * p.heads + head) * p.d + e0) * (int64_t)T::BYTES;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    if (j && !two) break;
-    if constexpr (T::BYTES == 2) {
-      uint4 o;
-      o.x = pack_bf16x2(x[8 * j], x[8 * j + 1]), o.y = pack_bf16x2(x[8 * j + 2], x[8 * j + 3]);
-      o.z = pack_bf16x2(x[8 * j + 4], x[8 * j + 5]), o.w = pack_bf16x2(x[8 * j + 6], x[8 * j + 7]);
-      reinterpret_cast<uint4*>(dst)[j] = o;
+      for (int j = 0; j < UB / 16; ++j)
+        if (j == 0 || left > 8) {
+          const uint4 a = *reinterpret_cast<const uint4*>(src + 16 * j);
+          w[i][4 * j] = a.x, w[i][4 * j + 1] = a.y, w[i][4 * j + 2] = a.z, w[i][4 * j + 3] = a.w;
+        }
+    }
+    if constexpr (F != QAT_CACHE_BF16) scale[i] = one(p.scales, which)[from];
+    if constexpr (kv_is_int(F))
+      if (one(p.zps, which)) zp[i] = one(p.zps, which)[from];
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int row = blockIdx.y * U + i;
+    if (row >= 2 * p.heads) break;
+    const int which = row >= p.heads, head = row - (which ? p.heads : 0);
+    float x[16];
+    kv_decode<F>(w[i], scale[i], zp[i], x);
+    uint32_t o[4 * T::BYTES];
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      if (T::BYTES == 2)
+        o[e / 2] = pack_bf16x2(x[e], x[e + 1]);
+      else
+        o[e] = __float_as_uint(x[e]), o[e + 1] = __float_as_uint(x[e + 1]);
+    }
+    char* dst = static_cast<char*>(which ? v : k) +
+                ((token * p.heads + head) * p.d + 16 * lane) * (int64_t)T::BYTES;
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int j = 0; j < T::BYTES / 2; ++j) {
+        V32 y;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y.w[e] = o[8 * j + e];
+        st_v32(dst + 32 * j, y);
+      }
     } else {
-      reinterpret_cast<float4*>(dst)[2 * j] =
-          make_float4(x[8 * j], x[8 * j + 1], x[8 * j + 2], x[8 * j + 3]);
-      reinterpret_cast<float4*>(dst)[2 * j + 1] =
-          make_float4(x[8 * j + 4], x[8 * j + 5], x[8 * j + 6], x[8 * j + 7]);
+#pragma unroll
+      for (int j = 0; j < T::BYTES; ++j)
+        if (j * 16 / T::BYTES < left)
+          reinterpret_cast<uint4*>(dst)[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
     }
   }
+}
+
+// Rows a group takes at a time: four once that leaves every SM full (read: 134 MB of
+// int8 rows with four 63 us, one 111), one for fewer, which then run side by side.
+bool many_rows(int64_t rows, int lanes) {
+  return rows * lanes >= (int64_t)device_info().sms * 2048 * 8;
+}
+// A grid for runs of U rows of each token; false where it does not fit.
+bool kv_grid(const KvPlace& p, int64_t tokens, int lanes, int u, dim3* grid) {
+  const int64_t x = (tokens + kKvThreads / lanes - 1) / (kKvThreads / lanes);
+  const int64_t y = (2 * (int64_t)p.heads + u - 1) / u;
+  *grid = dim3((unsigned)x, (unsigned)y);
+  return x <= INT32_MAX && y <= 65535;
 }
 
 template <typename T, int F, bool AFFINE>
@@ -237,15 +330,23 @@ qat_status write_rows(const qat_kv_cache& c, const KvRows& x, int64_t tokens, co
                       cudaStream_t s) {
   const KvPlace p = place_of(c);
   const int lanes = kv_lanes(p.units);
-  const int64_t rows = tokens * 2 * p.heads;
-  const int64_t blocks = (rows * lanes + kKvThreads - 1) / kKvThreads;
-  if (blocks > INT32_MAX) return QAT_ERR_INVALID_ARGUMENT;
-  bool vec = true;
-  for (const void* q : {x.k, x.v}) vec = vec && reinterpret_cast<uintptr_t>(q) % 16 == 0;
-  for (int i = 0; i < 2; ++i)
-    vec = vec && x.token_stride[i] * T::BYTES % 16 == 0 && x.head_stride[i] * T::BYTES % 16 == 0;
-  auto k = vec ? k_kv_write<T, F, AFFINE, true> : k_kv_write<T, F, AFFINE, false>;
-  k<<<(unsigned)blocks, kKvThreads, 0, s>>>(x, p, rows, slots, lanes);
+  const auto on = [&](int64_t bytes) {
+    bool fits = true;
+    for (const void* q : {x.k, x.v}) fits = fits && reinterpret_cast<uintptr_t>(q) % bytes == 0;
+    for (int i = 0; i < 2; ++i)
+      fits = fits && x.token_stride[i] * T::BYTES % bytes == 0 && x.head_stride[i] * T::BYTES % bytes == 0;
+    return fits;
+  };
+  constexpr int MOST = T::BYTES == 2 ? kVec32 : kVec16, U = T::BYTES == 2 ? 4 : 2;
+  const bool vec = on(16), wide = T::BYTES == 4 ? vec : on(32) && p.d % 16 == 0;
+  const bool many = wide && many_rows(tokens * 2 * p.heads, lanes);
+  dim3 grid;
+  if (!kv_grid(p, tokens, lanes, many ? U : 1, &grid)) return QAT_ERR_INVALID_ARGUMENT;
+  auto k = many   ? k_kv_write<T, F, AFFINE, MOST, U>
+           : wide ? k_kv_write<T, F, AFFINE, MOST, 1>
+           : vec  ? k_kv_write<T, F, AFFINE, kVec16, 1>
+                  : k_kv_write<T, F, AFFINE, kSingle, 1>;
+  k<<<grid, kKvThreads, 0, s>>>(x, p, tokens, slots, lanes);
   count_launch(1);
   return launch_status();
 }
@@ -267,22 +368,34 @@ qat_status write_any(const qat_kv_cache& c, const KvRows& x, int64_t tokens, con
   }
 }
 
+template <typename T, int F>
+qat_status read_rows(const qat_kv_cache& c, const int64_t* slots, int64_t tokens, void* k, void* v,
+                     cudaStream_t s) {
+  const KvPlace p = place_of(c);
+  const int lanes = kv_lanes((p.d + 15) / 16);
+  const bool wide = p.d % 16 == 0 && reinterpret_cast<uintptr_t>(k) % 32 == 0 &&
+                    reinterpret_cast<uintptr_t>(v) % 32 == 0;
+  const bool many = wide && many_rows(tokens * 2 * p.heads, lanes);
+  dim3 grid;
+  if (!kv_grid(p, tokens, lanes, many ? 4 : 1, &grid)) return QAT_ERR_INVALID_ARGUMENT;
+  auto kernel = many   ? k_kv_read<T, F, true, 4>
+                : wide ? k_kv_read<T, F, true, 1>
+                       : k_kv_read<T, F, false, 1>;
+  kernel<<<grid, kKvThreads, 0, s>>>(p, tokens, slots, lanes, k, v);
+  count_launch(1);
+  return launch_status();
+}
+
 template <typename T>
 qat_status read_any(const qat_kv_cache& c, const int64_t* slots, int64_t tokens, void* k, void* v,
                     cudaStream_t s) {
-  const KvPlace p = place_of(c);
-  const int lanes = kv_lanes(p.units);
-  const int64_t rows = tokens * 2 * p.heads;
-  const int64_t blocks = (rows * lanes + kKvThreads - 1) / kKvThreads;
-  if (blocks > INT32_MAX) return QAT_ERR_INVALID_ARGUMENT;
-  auto kernel = k_kv_read<T, QAT_CACHE_BF16>;
-  if (c.format == QAT_CACHE_INT8) kernel = k_kv_read<T, QAT_CACHE_INT8>;
-  if (c.format == QAT_CACHE_INT4) kernel = k_kv_read<T, QAT_CACHE_INT4>;
-  if (c.format == QAT_CACHE_E4M3) kernel = k_kv_read<T, QAT_CACHE_E4M3>;
-  if (c.format == QAT_CACHE_E5M2) kernel = k_kv_read<T, QAT_CACHE_E5M2>;
-  kernel<<<(unsigned)blocks, kKvThreads, 0, s>>>(p, rows, slots, lanes, k, v);
-  count_launch(1);
-  return launch_status();
+  switch (c.format) {
+    case QAT_CACHE_INT8: return read_rows<T, QAT_CACHE_INT8>(c, slots, tokens, k, v, s);
+    case QAT_CACHE_INT4: return read_rows<T, QAT_CACHE_INT4>(c, slots, tokens, k, v, s);
+    case QAT_CACHE_E4M3: return read_rows<T, QAT_CACHE_E4M3>(c, slots, tokens, k, v, s);
+    case QAT_CACHE_E5M2: return read_rows<T, QAT_CACHE_E5M2>(c, slots, tokens, k, v, s);
+    default: return read_rows<T, QAT_CACHE_BF16>(c, slots, tokens, k, v, s);
+  }
 }
 
 }  // namespace

@@ -11,7 +11,8 @@
 // Bound by reading and writing the heads.  A group of lanes holds a head in
 // registers: each lane the two runs of V elements whose pairs it turns, so that
 // norm, weight and rotation need one pass and one reduction over the group.  A
-// group walks over several heads of a token, which share its angles.
+// group walks over several heads of a token, which share its angles and weights, with
+// the next head's loads in flight; arithmetic is on pairs of binary32 numbers.
 #include "qat_attention.h"
 #include "qat_layer.cuh"
 
@@ -75,20 +76,22 @@ struct Run {
   }
 };
 
-// Cosine and sine of a 2^-64 fraction of a turn: the quarter by its two top bits,
-// the rest (|r| <= an eighth of a turn) by the library's function of half turns.
+// Cosine and sine of a 2^-64 fraction of a turn: the quarter by its two top bits, the
+// rest (|x| <= pi / 4) by the Taylor series, whose next terms are below 2^-25.
 __device__ __forceinline__ void turn_cos_sin(uint64_t t, float m, float& c, float& s) {
-  const uint64_t quarter = (t + (UINT64_C(1) << 61)) >> 62;
-  const int32_t r = (int32_t)((int64_t)(t - (quarter << 62)) >> 32);
-  float sr, cr;
-  sincospif((float)r * 0x1p-31f, &sr, &cr);
-  const int n = (int)quarter & 3;
+  const uint32_t top = (uint32_t)(t >> 32) + 0x20000000u;  // (an eighth of a turn on)
+  const int n = (int)(top >> 30);
+  const int32_t r = (int32_t)(top & 0x3fffffffu) - 0x20000000;
+  const float x = __fmul_rn((float)r, 1.4629180792671596e-9f);  // 2 pi / 2^32
+  const float q = __fmul_rn(x, x);
+  float sr = __fmaf_rn(q, 1.0f / 362880, -1.0f / 5040), cr = __fmaf_rn(q, 1.0f / 40320, -1.0f / 720);
+  sr = __fmaf_rn(q, sr, 1.0f / 120), cr = __fmaf_rn(q, cr, 1.0f / 24);
+  sr = __fmaf_rn(q, sr, -1.0f / 6), cr = __fmaf_rn(q, cr, -0.5f);
+  sr = __fmaf_rn(__fmul_rn(q, x), sr, x), cr = __fmaf_rn(q, cr, 1.0f);
   c = (n & 1) ? sr : cr;
   s = (n & 1) ? cr : sr;
-  if (n == 1 || n == 2) c = -c;
-  if (n >= 2) s = -s;
-  c = __fmul_rn(c, m);
-  s = __fmul_rn(s, m);
+  c = __fmul_rn(c, n == 1 || n == 2 ? -m : m);
+  s = __fmul_rn(s, n >= 2 ? -m : m);
 }
 
 // Where the runs A and B of unit u start.  Units of turned pairs come first; a
@@ -105,143 +108,192 @@ __device__ __forceinline__ void unit_runs(int u, int rotary, int& a, int& b) {
   }
 }
 
-// The lane's V pairs turned in place: v holds run A, then run B.
-template <int V, bool INTER>
-__device__ __forceinline__ void turn_pairs(float (&v)[2 * V], const float (&c)[V],
-                                           const float (&s)[V], bool back) {
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const int p = INTER ? 2 * e : e, q = INTER ? 2 * e + 1 : V + e;
-    const float se = back ? -s[e] : s[e];
-    const float a = v[p], b = v[q];
-    v[p] = __fmaf_rn(a, c[e], -__fmul_rn(b, se));
-    v[q] = __fmaf_rn(b, c[e], __fmul_rn(a, se));
-  }
-}
-
 __device__ __forceinline__ float group_sum(float v, int lanes) {
   for (int o = lanes >> 1; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
 }
 
-// A lane's units of one head, u = lane + lanes * p.
+// r = a b + c and r = a b over N elements, two at a time.
+template <int N>
+__device__ __forceinline__ void vfma(const float (&a)[N], const float (&b)[N], const float (&c)[N],
+                                     float (&r)[N]) {
+#pragma unroll
+  for (int e = 0; e + 1 < N; e += 2) fma2(a[e], a[e + 1], b[e], b[e + 1], c[e], c[e + 1], r[e], r[e + 1]);
+  if (N & 1) r[N - 1] = __fmaf_rn(a[N - 1], b[N - 1], c[N - 1]);
+}
+template <int N>
+__device__ __forceinline__ void vmul(const float (&a)[N], const float (&b)[N], float (&r)[N]) {
+#pragma unroll
+  for (int e = 0; e + 1 < N; e += 2) mul2(a[e], a[e + 1], b[e], b[e + 1], r[e], r[e + 1]);
+  if (N & 1) r[N - 1] = __fmul_rn(a[N - 1], b[N - 1]);
+}
+template <int N>
+__device__ __forceinline__ void vmul(const float (&a)[N], float b, float (&r)[N]) {
+#pragma unroll
+  for (int e = 0; e + 1 < N; e += 2) mul2(a[e], a[e + 1], b, b, r[e], r[e + 1]);
+  if (N & 1) r[N - 1] = __fmul_rn(a[N - 1], b);
+}
+template <int N>
+__device__ __forceinline__ float vsum(const float (&a)[N]) {
+  float s = 0.0f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) s += a[e];
+  return s;
+}
+
+// A lane's units of one head, u = lane + lanes * p: where they lie, and whether their
+// pairs are turned.
 template <int V, int NP, bool INTER>
 struct Units {
   int a[NP], b[NP];
-  bool has_a[NP], has_b[NP];
+  bool has_a[NP], has_b[NP], turned[NP];
   __device__ __forceinline__ Units(int lane, int lanes, int d, int rotary) {
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-      unit_runs<V, INTER>(lane + lanes * p, rotary, a[p], b[p]);
+      const int u = lane + lanes * p;
+      unit_runs<V, INTER>(u, rotary, a[p], b[p]);
+      turned[p] = u < rotary / (2 * V);
       has_a[p] = a[p] < d;
       has_b[p] = has_a[p] && b[p] < d;
     }
   }
 };
 
-template <typename T, int V, int NP>
-__device__ __forceinline__ void load_weight(const void* w, const int (&a)[NP], const int (&b)[NP],
-                                            const bool (&ha)[NP], const bool (&hb)[NP],
-                                            float (&wt)[NP][2 * V]) {
-#pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    Run<T, V> ra, rb;
+// The first and second elements of a unit's V pairs, from its runs and back.
+template <typename T, int V, bool INTER>
+struct Pairs {
+  Run<T, V> ra, rb;
+  __device__ __forceinline__ void load(const void* base, int64_t at, int a, int b, bool ha, bool hb) {
     ra.zero(), rb.zero();
-    if (w && ha[p]) ra.load(w, a[p]);
-    if (w && hb[p]) rb.load(w, b[p]);
+    if (ha) ra.load(base, at + a);
+    if (hb) rb.load(base, at + b);
+  }
+  __device__ __forceinline__ void get(float (&x)[V], float (&y)[V]) const {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      wt[p][e] = w ? ra.get(e) : 1.0f;
-      wt[p][V + e] = w ? rb.get(e) : 1.0f;
+      if (INTER) {
+        x[e] = 2 * e < V ? ra.get(2 * e) : rb.get(2 * e - V);
+        y[e] = 2 * e + 1 < V ? ra.get(2 * e + 1) : rb.get(2 * e + 1 - V);
+      } else {
+        x[e] = ra.get(e), y[e] = rb.get(e);
+      }
+    }
+  }
+  __device__ __forceinline__ void put(const float (&x)[V], const float (&y)[V]) {
+    float v[2 * V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      v[INTER ? 2 * e : e] = x[e];
+      v[INTER ? 2 * e + 1 : V + e] = y[e];
+    }
+    ra.set(v), rb.set(v + V);
+  }
+  __device__ __forceinline__ void store(void* base, int64_t at, int a, int b, bool ha, bool hb) const {
+    if (ha) ra.store(base, at + a);
+    if (hb) rb.store(base, at + b);
+  }
+};
+
+template <typename T, int V, int NP, bool INTER>
+__device__ __forceinline__ void load_weight(const void* w, const Units<V, NP, INTER>& un,
+                                            float (&wa)[NP][V], float (&wb)[NP][V]) {
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    if (w) {
+      Pairs<T, V, INTER> x;
+      x.load(w, 0, un.a[p], un.b[p], un.has_a[p], un.has_b[p]);
+      x.get(wa[p], wb[p]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) wa[p][e] = wb[p][e] = 1.0f;
     }
   }
 }
 
-template <int V, int NP, bool INTER>
+template <int V, int NP>
 __device__ __forceinline__ void load_angles(const RopeArgs& r, int64_t token, int lane, int lanes,
                                             float (&c)[NP][V], float (&s)[NP][V]) {
   const uint64_t pos = (uint64_t)__ldg(r.positions + token);
 #pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    const int u = lane + lanes * p;
+  for (int p = 0; p < NP; ++p)
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const int j = u * V + e;
+      const int j = (lane + lanes * p) * V + e;
       c[p][e] = 1.0f, s[p][e] = 0.0f;
       if (j < r.rotary / 2) turn_cos_sin(pos * __ldg(r.turns + j), r.amplitude, c[p][e], s[p][e]);
     }
-  }
+}
+
+__device__ __forceinline__ float rstd_of(const RopeArgs& r, float sum) {
+  return rsqrtf(__fmaf_rn(sum, r.inv_d, r.eps));
 }
 
 constexpr int kRopeThreads = 256;
 
-// `per` heads of one token a group; items are the query heads' runs, then the
-// keys'.  All lanes of a warp take the same number of steps (shuffles).
-template <typename T, int V, int NP, int U, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) k_rope_fwd(RopeArgs r, int lanes, int per) {
+// Blocks (x: tokens, y: runs of `per` heads, the queries' first), a group a token.
+// All lanes of a warp take the same number of steps (shuffles).
+template <typename T, int V, int NP, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads, V == 8 ? 3 : 2) k_rope_fwd(RopeArgs r, int lanes, int per, int runs0) {
+  using P = Pairs<T, V, INTER>;
   const int lane = threadIdx.x & (lanes - 1);
-  const int64_t item = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) / lanes;
-  const int runs0 = (r.heads[0] + per - 1) / per, runs1 = (r.heads[1] + per - 1) / per;
-  const int64_t items0 = r.tokens * runs0;
-  const bool there = item < items0 + r.tokens * runs1;
-  const int which = item >= items0;
-  const int runs = which ? runs1 : runs0;
-  const int64_t at = item - (which ? items0 : 0);
-  const int64_t token = there ? at / runs : 0;
-  const int h0 = there ? (int)(at - token * runs) * per : 0;
-  const int heads = there ? r.heads[which] : 0;
-  const void* x = r.x[which];
+  const int64_t token = (int64_t)blockIdx.x * (kRopeThreads / lanes) + threadIdx.x / lanes;
+  const int which = (int)blockIdx.y >= runs0;
+  const int h0 = ((int)blockIdx.y - (which ? runs0 : 0)) * per;
+  const int n = token < r.tokens ? min(per, r.heads[which] - h0) : 0;
+  const int steps = min(per, r.heads[which] - h0);
   const int64_t hs = r.head_stride[which];
-  const int64_t xt = token * r.token_stride[which];
-  const int64_t yt = (token * r.heads[which]) * r.d;
-
+  const int64_t xt = n ? token * r.token_stride[which] + h0 * hs : 0;
+  const int64_t yt = (token * r.heads[which] + h0) * r.d;
   const Units<V, NP, INTER> un(lane, lanes, r.d, r.rotary);
-  float w[NP][2 * V], c[NP][V], s[NP][V];
-  load_weight<T, V, NP>(r.w[which], un.a, un.b, un.has_a, un.has_b, w);
-  load_angles<V, NP, INTER>(r, token, lane, lanes, c, s);
-  for (int h = 0; h < per; h += U) {
-    Run<T, V> ra[U][NP], rb[U][NP];
+
+  P next[NP];
+  auto fetch = [&](int h) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const bool on = h + i < per && h0 + h + i < heads;
+    for (int p = 0; p < NP; ++p)
+      next[p].load(r.x[which], xt + h * hs, un.a[p], un.b[p], h < n && un.has_a[p], h < n && un.has_b[p]);
+  };
+  fetch(0);
+  // a' = (a wa c - b wb s) rstd, b' = (b wb c + a wa s) rstd
+  float ac[NP][V], bs[NP][V], bc[NP][V], as[NP][V];
+  {
+    float wa[NP][V], wb[NP][V], c[NP][V], s[NP][V];
+    load_weight<T, V, NP, INTER>(r.w[which], un, wa, wb);
+    load_angles<V, NP>(r, n ? token : 0, lane, lanes, c, s);
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        ra[i][p].zero(), rb[i][p].zero();
-        const int64_t o = xt + (h0 + h + i) * hs;
-        if (on && un.has_a[p]) ra[i][p].load(x, o + un.a[p]);
-        if (on && un.has_b[p]) rb[i][p].load(x, o + un.b[p]);
-      }
+    for (int p = 0; p < NP; ++p) {
+      vmul(wa[p], c[p], ac[p]);
+      vmul(wb[p], s[p], bs[p]);
+      vmul(bs[p], -1.0f, bs[p]);
+      vmul(wb[p], c[p], bc[p]);
+      vmul(wa[p], s[p], as[p]);
     }
+  }
+  for (int h = 0; h < steps; ++h) {
+    P now[NP];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const bool on = h + i < per && h0 + h + i < heads;
-      float rstd = 1.0f;
-      if (r.norm) {
-        float sum = 0.0f;
+    for (int p = 0; p < NP; ++p) now[p] = next[p];
+    if (h + 1 < steps) fetch(h + 1);
+    float a[NP][V], b[NP][V], sq[V] = {};
 #pragma unroll
-        for (int p = 0; p < NP; ++p)
+    for (int p = 0; p < NP; ++p) {
+      now[p].get(a[p], b[p]);
+      if (r.norm) vfma(a[p], a[p], sq, sq), vfma(b[p], b[p], sq, sq);
+    }
+    const float rstd = r.norm ? rstd_of(r, group_sum(vsum(sq), lanes)) : 1.0f;
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            sum = __fmaf_rn(ra[i][p].get(e), ra[i][p].get(e), sum);
-            sum = __fmaf_rn(rb[i][p].get(e), rb[i][p].get(e), sum);
-          }
-        sum = group_sum(sum, lanes);
-        rstd = __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)r.d), r.eps)));
+    for (int p = 0; p < NP; ++p) {
+      float x[V], y[V];
+      vmul(a[p], ac[p], x);
+      vmul(b[p], bc[p], y);
+      if (un.turned[p]) {  // (0 times what is not finite would not pass the others as they are)
+        vfma(b[p], bs[p], x, x);
+        vfma(a[p], as[p], y, y);
       }
-      const int64_t o = yt + (int64_t)(h0 + h + i) * r.d;
-#pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        float v[2 * V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          v[e] = __fmul_rn(__fmul_rn(ra[i][p].get(e), rstd), w[p][e]);
-          v[V + e] = __fmul_rn(__fmul_rn(rb[i][p].get(e), rstd), w[p][V + e]);
-        }
-        turn_pairs<V, INTER>(v, c[p], s[p], false);
-        Run<T, V> out;
-        if (on && un.has_a[p]) out.set(v), out.store(r.y[which], o + un.a[p]);
-        if (on && un.has_b[p]) out.set(v + V), out.store(r.y[which], o + un.b[p]);
-      }
+      vmul(x, rstd, x);
+      vmul(y, rstd, y);
+      now[p].put(x, y);
+      now[p].store(r.y[which], yt + (int64_t)h * r.d, un.a[p], un.b[p], h < n && un.has_a[p],
+                   h < n && un.has_b[p]);
     }
   }
 }
@@ -249,8 +301,9 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_fwd(RopeArgs r, int lanes
 // The same walk with the gradients; each lane keeps its elements' share of dweight,
 // and a block's shares are added over its groups in shared memory, in order.
 template <typename T, int V, int NP, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) k_rope_bwd(RopeArgs r, int lanes, int per,
+__global__ void __launch_bounds__(kRopeThreads, V == 8 && T::BYTES == 2 ? 2 : 1) k_rope_bwd(RopeArgs r, int lanes, int per,
                                                            float* parts) {
+  using P = Pairs<T, V, INTER>;
   __shared__ float share[kRopeThreads * 2 * V * NP];
   pdl_trigger();
   const int lane = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes;
@@ -261,64 +314,82 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_bwd(RopeArgs r, int lanes
     const bool sums = r.dw[which] != nullptr;
     const int runs = (heads + per - 1) / per;
     const int64_t items = r.y[which] || sums ? r.tokens * runs : 0;
-    const void *x = r.x[which], *g = r.g[which];
-    float w[NP][2 * V], acc[NP][2 * V] = {};
-    load_weight<T, V, NP>(r.w[which], un.a, un.b, un.has_a, un.has_b, w);
+    float wa[NP][V], wb[NP][V], da[NP][V] = {}, db[NP][V] = {};
+    load_weight<T, V, NP, INTER>(r.w[which], un, wa, wb);
     // (whole blocks step together: the shuffles need every lane)
     for (int64_t base = (int64_t)blockIdx.x * groups; base < items;
          base += (int64_t)gridDim.x * groups) {
-      const int64_t item = base + group;
-      const bool there = item < items;
-      const int64_t token = there ? item / runs : 0;
-      const int h0 = there ? (int)(item - token * runs) * per : 0;
-      float c[NP][V], s[NP][V];
-      load_angles<V, NP, INTER>(r, token, lane, lanes, c, s);
-      for (int h = 0; h < per; ++h) {
-        const bool on = there && h0 + h < heads;
-        Run<T, V> xa[NP], xb[NP], ga[NP], gb[NP];
-        const int64_t xo = token * r.token_stride[which] + (h0 + h) * r.head_stride[which];
-        const int64_t go = (token * heads + h0 + h) * r.d;
+      const int64_t item = base + group, token = item < items ? item / runs : 0;
+      const int h0 = item < items ? (int)(item - token * runs) * per : 0;
+      const int n = item < items ? min(per, heads - h0) : 0;
+      const int64_t xt = token * r.token_stride[which] + h0 * r.head_stride[which];
+      const int64_t gt = (token * heads + h0) * r.d;
+      P next_x[NP], next_g[NP];
+      auto fetch = [&](int h) {
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          xa[p].zero(), xb[p].zero(), ga[p].zero(), gb[p].zero();
-          if (on && un.has_a[p]) xa[p].load(x, xo + un.a[p]), ga[p].load(g, go + un.a[p]);
-          if (on && un.has_b[p]) xb[p].load(x, xo + un.b[p]), gb[p].load(g, go + un.b[p]);
+          const bool ha = h < n && un.has_a[p], hb = h < n && un.has_b[p];
+          next_x[p].load(r.x[which], xt + h * r.head_stride[which], un.a[p], un.b[p], ha, hb);
+          next_g[p].load(r.g[which], gt + (int64_t)h * r.d, un.a[p], un.b[p], ha, hb);
         }
-        float v[NP][2 * V], sum = 0.0f, dot = 0.0f;
+      };
+      fetch(0);
+      float c[NP][V], s[NP][V];
+      load_angles<V, NP>(r, token, lane, lanes, c, s);
+      for (int h = 0; h < per; ++h) {
+        P now[NP];
+        float a[NP][V], b[NP][V], ga[NP][V], gb[NP][V], sq[V] = {}, gx[V] = {};
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
+          next_x[p].get(a[p], b[p]);
+          now[p] = next_g[p];
+        }
+        if (h + 1 < per) fetch(h + 1);
 #pragma unroll
-          for (int e = 0; e < V; ++e) v[p][e] = ga[p].get(e), v[p][V + e] = gb[p].get(e);
-          turn_pairs<V, INTER>(v[p], c[p], s[p], true);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float a = xa[p].get(e), b = xb[p].get(e);
-            sum = __fmaf_rn(b, b, __fmaf_rn(a, a, sum));
-            dot = __fmaf_rn(__fmul_rn(v[p][e], w[p][e]), a, dot);
-            dot = __fmaf_rn(__fmul_rn(v[p][V + e], w[p][V + e]), b, dot);
+        for (int p = 0; p < NP; ++p) {
+          float x[V], y[V], t[V];
+          now[p].get(x, y);
+          vmul(x, c[p], ga[p]);
+          vmul(y, c[p], gb[p]);
+          if (un.turned[p]) {
+            vfma(y, s[p], ga[p], ga[p]);
+            vmul(s[p], -1.0f, t);
+            vfma(x, t, gb[p], gb[p]);
+          }
+          if (r.norm) {
+            vfma(a[p], a[p], sq, sq), vfma(b[p], b[p], sq, sq);
+            vmul(ga[p], wa[p], t), vfma(t, a[p], gx, gx);
+            vmul(gb[p], wb[p], t), vfma(t, b[p], gx, gx);
           }
         }
         float rstd = 1.0f, mean = 0.0f;
         if (r.norm) {
-          sum = group_sum(sum, lanes);
-          dot = group_sum(dot, lanes);
-          rstd = __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)r.d), r.eps)));
-          mean = __fdiv_rn(__fmul_rn(dot, rstd), (float)r.d);  // of g'w z
+          rstd = rstd_of(r, group_sum(vsum(sq), lanes));
+          mean = -(group_sum(vsum(gx), lanes) * rstd) * r.inv_d;  // of g'w z
         }
+        // dw += g' z; dx = (g'w - z mean) rstd
+        auto finish = [&](const float (&g)[V], const float (&w)[V], float (&x)[V], float (&dw)[V]) {
+          float t[V], u[V];
+          vmul(x, rstd, x);
+          vfma(g, x, dw, dw);
+          vmul(g, w, t);
+          vmul(x, mean, u);
+#pragma unroll
+          for (int e = 0; e < V; ++e) u[e] += t[e];
+          vmul(u, rstd, x);
+        };
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          float dx[2 * V];
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float za = __fmul_rn(xa[p].get(e), rstd), zb = __fmul_rn(xb[p].get(e), rstd);
-            acc[p][e] = __fmaf_rn(v[p][e], za, acc[p][e]);
-            acc[p][V + e] = __fmaf_rn(v[p][V + e], zb, acc[p][V + e]);
-            dx[e] = __fmul_rn(rstd, __fmaf_rn(-mean, za, __fmul_rn(v[p][e], w[p][e])));
-            dx[V + e] = __fmul_rn(rstd, __fmaf_rn(-mean, zb, __fmul_rn(v[p][V + e], w[p][V + e])));
+          if (r.norm) {
+            finish(ga[p], wa[p], a[p], da[p]);
+            finish(gb[p], wb[p], b[p], db[p]);
+            now[p].put(a[p], b[p]);
+          } else {
+            now[p].put(ga[p], gb[p]);
           }
-          Run<T, V> out;
-          if (on && r.y[which] && un.has_a[p]) out.set(dx), out.store(r.y[which], go + un.a[p]);
-          if (on && r.y[which] && un.has_b[p]) out.set(dx + V), out.store(r.y[which], go + un.b[p]);
+          if (r.y[which])
+            now[p].store(r.y[which], gt + (int64_t)h * r.d, un.a[p], un.b[p], h < n && un.has_a[p],
+                         h < n && un.has_b[p]);
         }
       }
     }
@@ -327,7 +398,10 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_bwd(RopeArgs r, int lanes
 #pragma unroll
     for (int p = 0; p < NP; ++p)
 #pragma unroll
-      for (int e = 0; e < 2 * V; ++e) mine[p * 2 * V + e] = acc[p][e];
+      for (int e = 0; e < V; ++e) {
+        mine[p * 2 * V + (INTER ? 2 * e : e)] = da[p][e];
+        mine[p * 2 * V + (INTER ? 2 * e + 1 : V + e)] = db[p][e];
+      }
     __syncthreads();
     for (int i = threadIdx.x; i < lanes * NP * 2 * V; i += kRopeThreads) {
       const int ln = i / (NP * 2 * V), p = i / (2 * V) % NP, e = i % (2 * V);
@@ -336,7 +410,8 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_bwd(RopeArgs r, int lanes
       const int at = e < V ? a + e : b + e - V;
       if (at >= r.d || a >= r.d) continue;
       float total = 0.0f;
-      for (int k = 0; k < groups; ++k) total += share[((size_t)k * lanes + ln) * NP * 2 * V + i % (NP * 2 * V)];
+      for (int k = 0; k < groups; ++k)
+        total += share[((size_t)k * lanes + ln) * NP * 2 * V + i % (NP * 2 * V)];
       parts[((int64_t)blockIdx.x * 2 + which) * r.d + at] = total;
     }
     __syncthreads();
@@ -351,8 +426,10 @@ __global__ void __launch_bounds__(1024) k_rope_join(const float* parts, int n, i
   pdl_wait();
   const int col = blockIdx.x * 32 + threadIdx.x;
   float sum = 0.0f;
-  if (col < 2 * d)
+  if (col < 2 * d) {
+#pragma unroll 4
     for (int i = threadIdx.y; i < n; i += 32) sum += parts[(int64_t)i * 2 * d + col];
+  }
   part[threadIdx.y][threadIdx.x] = sum;
   __syncthreads();
   if (threadIdx.y || col >= 2 * d) return;
@@ -390,22 +467,21 @@ int group_lanes(int d, int v) {
   return lanes;
 }
 
-template <typename T, int V, int NP, int U>
+template <typename T, int V, int NP>
 qat_status fwd(const RopeArgs& r, cudaStream_t s) {
-  const int lanes = group_lanes(r.d, V);
+  const int lanes = group_lanes(r.d, V), groups = kRopeThreads / lanes;
   // Heads a group takes (they share a token's angles and weights): as many as
   // leave two waves of full SMs.
   const int64_t rows = r.tokens * (r.heads[0] + r.heads[1]);
-  const int64_t want = (int64_t)device_info().sms * 4096 / lanes;
+  const int64_t want = (int64_t)device_info().sms * 2048 / lanes;
   int per = 1;
   while (per < 8 && rows / (2 * per) >= want) per *= 2;
-  const int64_t items = r.tokens * ((r.heads[0] + per - 1) / per + (r.heads[1] + per - 1) / per);
-  const int64_t blocks = (items * lanes + kRopeThreads - 1) / kRopeThreads;
-  if (blocks > INT32_MAX) return QAT_ERR_INVALID_ARGUMENT;
-  auto k = r.interleaved ? k_rope_fwd<T, V, NP, U, true> : k_rope_fwd<T, V, NP, U, false>;
-  RopeArgs a = r;
-  if (launch_kernel(k, dim3((unsigned)blocks), dim3(kRopeThreads), 0, s, false, a, lanes, per) !=
-      cudaSuccess)
+  const int runs0 = (r.heads[0] + per - 1) / per, runs1 = (r.heads[1] + per - 1) / per;
+  const int64_t blocks = (r.tokens + groups - 1) / groups;
+  if (blocks > INT32_MAX || runs0 + runs1 > 65535) return QAT_ERR_INVALID_ARGUMENT;
+  auto k = r.interleaved ? k_rope_fwd<T, V, NP, true> : k_rope_fwd<T, V, NP, false>;
+  if (launch_kernel(k, dim3((unsigned)blocks, runs0 + runs1), dim3(kRopeThreads), 0, s, false, r, lanes,
+                    per, runs0) != cudaSuccess)
     return QAT_ERR_CUDA;
   count_launch(1);
   return QAT_OK;
@@ -419,12 +495,12 @@ qat_status bwd(const RopeArgs& r, float* ws, cudaStream_t s) {
   int per = 1;
   while (per < 8 && r.tokens * most / (2 * per) >= (int64_t)kRopeParts * groups) per *= 2;
   const int64_t blocks = (r.tokens * ((most + per - 1) / per) + groups - 1) / groups;
-  const int grid = (int)(blocks < kRopeParts ? blocks : kRopeParts);
+  const int64_t most_blocks = 2 * device_info().sms < kRopeParts ? 2 * device_info().sms : kRopeParts;
+  const int grid = (int)(blocks < most_blocks ? blocks : most_blocks);
   const bool sums = r.dw[0] || r.dw[1];
-  RopeArgs a = r;
   if (grid > 0) {
     auto k = r.interleaved ? k_rope_bwd<T, V, NP, true> : k_rope_bwd<T, V, NP, false>;
-    if (launch_kernel(k, dim3(grid), dim3(kRopeThreads), 0, s, false, a, lanes, per, ws) !=
+    if (launch_kernel(k, dim3(grid), dim3(kRopeThreads), 0, s, false, r, lanes, per, ws) !=
         cudaSuccess)
       return QAT_ERR_CUDA;
     count_launch(1);
@@ -441,10 +517,10 @@ qat_status bwd(const RopeArgs& r, float* ws, cudaStream_t s) {
 template <typename T>
 qat_status fwd_any(const RopeArgs& r, cudaStream_t s) {
   switch (run_width<T>(r)) {
-    case 8: return fwd<T, 8, 1, 2>(r, s);
-    case 4: return fwd<T, 4, 2, 1>(r, s);
-    case 2: return fwd<T, 2, 4, 1>(r, s);
-    default: return fwd<T, 1, 8, 1>(r, s);
+    case 8: return fwd<T, 8, 1>(r, s);
+    case 4: return fwd<T, 4, 2>(r, s);
+    case 2: return fwd<T, 2, 4>(r, s);
+    default: return fwd<T, 1, 8>(r, s);
   }
 }
 template <typename T>

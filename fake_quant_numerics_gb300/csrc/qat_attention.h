@@ -20,11 +20,11 @@ struct RopeArgs {
   const uint64_t* turns;
   int64_t tokens;
   int d, rotary, norm, interleaved;
-  float amplitude, eps;
+  float amplitude, eps, inv_d;
 };
-// Blocks of the backward pass, one row of partial weight gradients each:
+// Blocks of the backward pass at most, one row of partial weight gradients each:
 // float[kRopeParts][2][d] in the workspace.
-constexpr int kRopeParts = 608;
+constexpr int kRopeParts = 320;
 qat_status launch_rope_fwd(const RopeArgs& a, qat_dtype dt, cudaStream_t s);
 qat_status launch_rope_bwd(const RopeArgs& a, qat_dtype dt, float* ws, cudaStream_t s);
 

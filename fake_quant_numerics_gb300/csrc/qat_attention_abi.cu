@@ -34,8 +34,7 @@ qat_status check_rope(const RopeSizes& z, qat_dtype dtype, int layout, float amp
   if (z.head_dim < 1 || z.head_dim > 512 || z.rotary_dim < 0 || z.rotary_dim > z.head_dim ||
       z.rotary_dim % 2)
     return QAT_ERR_INVALID_ARGUMENT;
-  if (z.q_heads < 0 || z.k_heads < 0 || z.q_heads > INT32_MAX / 1024 ||
-      z.k_heads > INT32_MAX / 1024 || !fits(z.tokens, (z.q_heads + z.k_heads) * z.head_dim))
+  if (z.q_heads < 0 || z.k_heads < 0 || z.q_heads > 32767 || z.k_heads > 32767 || !fits(z.tokens, (z.q_heads + z.k_heads) * z.head_dim))
     return QAT_ERR_INVALID_ARGUMENT;
   if (!stride_ok(z.q_ts, z.tokens) || !stride_ok(z.k_ts, z.tokens) ||
       !stride_ok(z.q_hs, z.q_heads) || !stride_ok(z.k_hs, z.k_heads))
@@ -57,6 +56,7 @@ RopeArgs rope_args(const RopeSizes& z, const void* q, const void* k, const int64
   a.positions = positions, a.turns = turns, a.tokens = z.tokens;
   a.d = (int)z.head_dim, a.rotary = (int)z.rotary_dim, a.norm = norm != 0;
   a.interleaved = layout == QAT_ROPE_INTERLEAVED, a.amplitude = amplitude, a.eps = eps;
+  a.inv_d = 1.0f / (float)z.head_dim;
   return a;
 }
 
@@ -67,7 +67,7 @@ qat_status check_cache(const qat_kv_cache* c) {
   if (c->head_dim < 8 || c->head_dim > 256 || c->head_dim % 8) return QAT_ERR_UNSUPPORTED;
   if (c->page_size < 16 || c->page_size % 16 || c->page_size > INT32_MAX)
     return QAT_ERR_INVALID_ARGUMENT;
-  if (c->pages < 0 || c->pages > INT32_MAX / c->page_size || c->heads < 1 || c->heads > 65535)
+  if (c->pages < 0 || c->pages > INT32_MAX / c->page_size || c->heads < 1 || c->heads > 32767)
     return QAT_ERR_INVALID_ARGUMENT;
   const bool ints = f == QAT_CACHE_INT8 || f == QAT_CACHE_INT4;
   if (!c->k_zero_points != !c->v_zero_points || (c->k_zero_points && !ints))

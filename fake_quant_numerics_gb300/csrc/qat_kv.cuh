@@ -34,29 +34,39 @@ __device__ __forceinline__ float2 fp8_values(uint32_t pair) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// The values of E codes (E = 8 or 16): (q - zp) * scale, c * scale, or the bf16.
-template <int F, int E>
+// The values of 16 codes: (q - zp) * scale, c * scale, or the bf16.  An integer code
+// comes as the low byte of a float of 2^23 (its sign bit turned), from which the same
+// number for the zero point is taken: exact.
+template <int F>
 __device__ __forceinline__ void kv_decode(const uint32_t* w, float scale, int zp, float* v) {
+  if constexpr (F == QAT_CACHE_BF16) {
 #pragma unroll
-  for (int i = 0; i < E; i += 2) {
-    if (F == QAT_CACHE_BF16) {
+    for (int i = 0; i < 16; i += 2) {
       v[i] = __uint_as_float(w[i / 2] << 16);
       v[i + 1] = __uint_as_float(w[i / 2] & 0xffff0000u);
-    } else if (F == QAT_CACHE_INT8) {
-      const int32_t a = (int32_t)(w[i / 4] << (24 - 8 * (i % 4))) >> 24;
-      const int32_t b = (int32_t)(w[i / 4] << (16 - 8 * (i % 4))) >> 24;
-      v[i] = __fmul_rn((float)(a - zp), scale);
-      v[i + 1] = __fmul_rn((float)(b - zp), scale);
-    } else if (F == QAT_CACHE_INT4) {
-      const int byte = 8 * ((i / 2) % 4);  // the even element in the high nibble
-      const int32_t a = (int32_t)(w[i / 8] << (24 - byte)) >> 28;
-      const int32_t b = (int32_t)(w[i / 8] << (28 - byte)) >> 28;
-      v[i] = __fmul_rn((float)(a - zp), scale);
-      v[i + 1] = __fmul_rn((float)(b - zp), scale);
-    } else {
+    }
+  } else if constexpr (kv_is_int(F)) {
+    const float base = 8388608.0f + (float)(zp + (F == QAT_CACHE_INT8 ? 128 : 8));
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      uint32_t a, b;
+      if (F == QAT_CACHE_INT8) {
+        const uint32_t x = w[i / 4] ^ 0x80808080u;
+        a = __byte_perm(x, 0x4b000000u, 0x7550 + i % 4);
+        b = __byte_perm(x, 0x4b000000u, 0x7551 + i % 4);
+      } else {  // the even element in the high nibble
+        const uint32_t x = w[i / 8] ^ 0x88888888u;
+        a = __byte_perm((x >> 4) & 0x0f0f0f0fu, 0x4b000000u, 0x7550 + i / 2 % 4);
+        b = __byte_perm(x & 0x0f0f0f0fu, 0x4b000000u, 0x7550 + i / 2 % 4);
+      }
+      sub2(__uint_as_float(a), __uint_as_float(b), base, base, v[i], v[i + 1]);
+      mul2(v[i], v[i + 1], scale, scale, v[i], v[i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
       const float2 c = fp8_values<F>((w[i / 4] >> (8 * (i % 4))) & 0xffffu);
-      v[i] = __fmul_rn(c.x, scale);
-      v[i + 1] = __fmul_rn(c.y, scale);
+      mul2(c.x, c.y, scale, scale, v[i], v[i + 1]);
     }
   }
 }

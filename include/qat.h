@@ -590,8 +590,8 @@ qat_status qat_layer_norm_backward(const void* dy, const void* x, qat_dtype dtyp
  *     last one is 1); k may be NULL with k_heads 0.  q_out, k_out: contiguous.
  *   q_weight, k_weight (nullable: 1): dtype[head_dim]; NULL without norm.
  *   positions: int64[tokens] (any, negative ones too); turns: uint64[rotary_dim / 2].
- * head_dim 1 .. 512; rotary_dim even, 0 .. head_dim; eps finite and >= 0;
- * amplitude finite.  One launch.
+ * head_dim 1 .. 512; rotary_dim even, 0 .. head_dim; q_heads and k_heads up to
+ * 32767; eps finite and >= 0; amplitude finite.  One launch.
  */
 typedef enum { QAT_ROPE_HALF = 0, QAT_ROPE_INTERLEAVED = 1 } qat_rope_layout;
 
@@ -641,7 +641,7 @@ qat_status qat_head_norm_rope_backward(
  *   k_zero_points, v_zero_points (both or neither, integer formats): int8, alike;
  *   all 16-byte aligned.
  * head_dim: a multiple of 8 up to 256; page_size: a multiple of 16; pages *
- * page_size below 2^31; heads up to 65535.
+ * page_size below 2^31; heads up to 32767.
  */
 typedef enum {
   QAT_CACHE_BF16 = 0,

@@ -78,7 +78,7 @@ def cache(**kw):
 BAD_CACHES = [
     (dict(format=5), UNS), (dict(format=-1), UNS), (dict(head_dim=60), UNS), (dict(head_dim=0), UNS),
     (dict(head_dim=264), UNS), (dict(page_size=8), INV), (dict(page_size=24), INV), (dict(page_size=0), INV),
-    (dict(pages=-1), INV), (dict(pages=1 << 27), INV), (dict(heads=0), INV), (dict(heads=65536), INV),
+    (dict(pages=-1), INV), (dict(pages=1 << 27), INV), (dict(heads=0), INV), (dict(heads=32768), INV),
     (dict(kz=0x10000), INV), (dict(kz=0x10000, vz=0x10000, format=L.CACHE_E4M3), INV), (dict(k=None), INV),
     (dict(vs=None), INV), (dict(v=0x10008), MIS), (dict(ks=0x10008), MIS), (dict(kz=0x10004, vz=0x10000), MIS),
 ]

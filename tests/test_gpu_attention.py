@@ -232,6 +232,32 @@ def test_kv_write_and_read(qat, form, scheme, d, heads, page, dtype):
             assert not got[gone].any()
 
 
+@pytest.mark.parametrize("form,scheme,dtype", [("int8", "symmetric", BF16), ("int4", "affine", F32),
+                                               ("e4m3", "symmetric", BF16), ("bf16", "symmetric", F32)])
+def test_kv_many_tokens_are_each_as_alone(qat, form, scheme, dtype):
+    """A long prompt, whose rows are taken several at a time, gives what short calls give."""
+    t, heads, d = 27000, 7, 128  # (14 rows a token: no whole number of fours)
+    pages = -(-t // 64)
+    slots = torch.randperm(pages * 64, generator=torch.Generator().manual_seed(1))[:t].cuda()
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k, v = (torch.randn(t, heads, d, generator=g, device="cuda").to(dtype) for _ in range(2))
+    k[77, 3] = 0
+    k[78, 2, 5] = float("nan")
+    once, parts = (qat.kv_cache(pages, heads, 64, d, form, scheme) for _ in range(2))
+    qat.kv_write(once, k, v, slots)
+    for a in range(0, t, 999):
+        qat.kv_write(parts, k[a:a + 999], v[a:a + 999], slots[a:a + 999])
+    for name in ("k", "v", "k_scale", "v_scale", "k_zero_point", "v_zero_point"):
+        x, y = getattr(once, name), getattr(parts, name)
+        assert x is None or torch.equal(x.view(torch.uint8), y.view(torch.uint8)), name
+    slots[5] = -1
+    r = qat.kv_read(once, slots, dtype)
+    for a in range(0, t, 999):
+        p = qat.kv_read(once, slots[a:a + 999], dtype)
+        for x, y in zip(r, p):
+            assert torch.equal(x[a:a + 999].view(torch.uint8), y.view(torch.uint8))
+
+
 @pytest.mark.parametrize("form,scheme", FORMS[:4])
 def test_kv_rows_are_the_fake_quant_view(qat, form, scheme):
     """A cached row reads back as the per-row fake-quant view of the same row."""
