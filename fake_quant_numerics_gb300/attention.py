@@ -104,30 +104,40 @@ def _heads(t: torch.Tensor) -> torch.Tensor:
     return t if t.stride(2) == 1 or t.shape[2] <= 1 else t.contiguous()
 
 
+_I64 = torch.int64
+
+
 def _rope_inputs(what, q, k, positions, turns, q_weight, k_weight, norm, layout):
-    """q and k as [tokens, heads, head_dim], then their strides, sizes and weights."""
-    if q.dim() < 2 or turns.dim() != 1 or positions.numel() != q.shape[:-2].numel():
+    """q and k as [tokens, heads, head_dim], then positions, turns and the weights, each
+    as the kernels read it."""
+    shape, dev, dtype = q.shape, q.device, q.dtype
+    if len(shape) < 2 or turns.dim() != 1 or positions.numel() != (shape[0] if len(shape) == 3
+                                                                  else shape[:-2].numel()):
         raise _mismatch(what)
-    if k is not None and (k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]):
-        raise _mismatch(what)
-    if positions.dtype != torch.int64 or turns.dtype != torch.int64:
+    d = shape[-1]
+    if positions.dtype is not _I64 or turns.dtype is not _I64:
         raise TypeError("positions and turns are int64")
     if layout not in _LAYOUT:
         raise ValueError(f"layout must be 'half' or 'interleaved', not {layout!r}")
-    d = q.shape[-1]
-    if not norm and (q_weight is not None or k_weight is not None):
-        raise ValueError("weights belong to the norm")
-    if k is None and k_weight is not None:
-        raise ValueError("k_weight without k")
-    if q.device != positions.device or q.device != turns.device:
-        _on_device(q.device, positions, turns)
+    if positions.device != dev or turns.device != dev:
+        _on_device(dev, positions, turns)
     if k is not None:
-        _of_type(q, k)
-    wq = None if q_weight is None else _vector(what, q, q_weight, d)
-    wk = None if k_weight is None else _vector(what, q, k_weight, d)
-    q = _heads(q)
-    k = None if k is None else _heads(k)
-    return q, k, positions.contiguous(), turns.contiguous(), wq, wk
+        ks = k.shape
+        if len(ks) != len(shape) or ks[-1] != d or ks[:-2] != shape[:-2]:
+            raise _mismatch(what)
+        if k.dtype is not dtype or k.device != dev:
+            _of_type(q, k)
+        k = _heads(k)
+    elif k_weight is not None:
+        raise ValueError("k_weight without k")
+    if q_weight is not None or k_weight is not None:
+        if not norm:
+            raise ValueError("weights belong to the norm")
+        if q_weight is not None:
+            q_weight = _vector(what, q, q_weight, d)
+        if k_weight is not None:
+            k_weight = _vector(what, q, k_weight, d)
+    return _heads(q), k, positions.contiguous(), turns.contiguous(), q_weight, k_weight
 
 
 def head_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, turns: torch.Tensor,
@@ -240,7 +250,7 @@ class KVCache:
     offset."""
 
     __slots__ = ("k", "v", "format", "head_dim", "k_scale", "v_scale", "k_zero_point", "v_zero_point", "pages",
-                 "heads", "page_size", "device", "struct", "address")
+                 "heads", "page_size", "device", "struct", "address", "workspace")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, format: str, head_dim: int,
                  k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
@@ -285,6 +295,7 @@ class KVCache:
             k, v, k_scale, v_scale, k_zero_point, v_zero_point)), self.pages, self.heads, self.page_size, head_dim,
             _CACHE[format])
         self.address = ctypes.addressof(self.struct)
+        self.workspace = {}  # bytes that kv_attention needs, by the number of query heads
 
 
 def _row_elements(format: str, head_dim: int) -> int:
@@ -341,17 +352,20 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     in a padded batch) are not written.  Slots must differ: where one is given twice
     it is unspecified which token's codes and scales it holds."""
     what = "kv_write"
-    if k.dim() < 2 or k.shape != v.shape or k.shape[-2] != cache.heads or k.shape[-1] != cache.head_dim:
+    shape, dev = k.shape, cache.device
+    if len(shape) < 2 or v.shape != shape or shape[-2] != cache.heads or shape[-1] != cache.head_dim:
         raise _mismatch(what)
-    if slots.numel() != k.shape[:-2].numel():
+    tokens = shape[0] if len(shape) == 3 else shape[:-2].numel()
+    if slots.numel() != tokens:
         raise _mismatch(what)
-    _of_type(k, v)
-    _on_device(cache.device, k, slots)
-    slots = _slots(slots)
-    k, v = _heads(k), _heads(v)
+    if v.dtype is not k.dtype or v.device != k.device:
+        _of_type(k, v)
+    if k.device != dev or slots.device != dev:
+        _on_device(dev, k, slots)
+    slots, k, v = _slots(slots), _heads(k), _heads(v)
     ks, vs = k.stride(), v.stride()
-    _call("qat_kv_write", k.device, _lib.lib().qat_kv_write, cache.address, _ptr(k), v.data_ptr(), _dt(k),
-          k.shape[0], ks[0], ks[1], vs[0], vs[1], slots.data_ptr())
+    _call("qat_kv_write", dev, _lib.lib().qat_kv_write, cache.address, _ptr(k), v.data_ptr(), _dt(k), tokens,
+          ks[0], ks[1], vs[0], vs[1], slots.data_ptr())
 
 
 def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> KeysValues:
@@ -411,13 +425,14 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, len
         block_table = block_table.contiguous()
     lengths = lengths.contiguous()
     q = _heads(q)
+    lib, qs, qp = _lib.lib(), q.stride(), _ptr(q)
     y = torch.empty((batch, heads, d), dtype=q.dtype, device=dev)
     lse = torch.empty((batch, heads), dtype=torch.float32, device=dev) if want_lse else None
     if batch == 0 or heads == 0:
-        _ptr(q)
         return KvAttention(y, lse)
-    lib, qs, qp = _lib.lib(), q.stride(), _ptr(q)
-    n = lib.qat_kv_attention_workspace_bytes(cache.address, heads)
+    n = cache.workspace.get(heads)
+    if n is None:
+        n = cache.workspace[heads] = lib.qat_kv_attention_workspace_bytes(cache.address, heads)
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
     _call("qat_kv_attention", dev, lib.qat_kv_attention, qp, _dt(q), batch, heads, qs[0], qs[1], cache.address,
           block_table.data_ptr(), block_table.shape[1], block_table.stride(0), lengths.data_ptr(),

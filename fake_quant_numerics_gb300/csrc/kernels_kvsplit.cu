@@ -26,6 +26,7 @@
 // of a product are positions lane / 4 (+ 8) for keys, and the lane's share of a key is
 // every fourth 16-byte run; of a value every eighth.  Which head element a product's k
 // index stands for is free, so the codes' own order is taken for both operands.
+#include <atomic>
 #include <cmath>
 
 #include "qat_kv.cuh"
@@ -885,10 +886,17 @@ qat_status go(const KvCacheView& c, const KvAttnArgs& a, const SplitWs& ws, int*
   using S = Shape<T, F, DP, HT>;
   static_assert(S::WARPS >= 2, "shared memory");
   const auto k = k_kv_split<T, F, DP, HT, EXACT>;
-  if (S::SMEM > 48 * 1024 &&
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return QAT_ERR_CUDA;
+  // (once for each device: the attribute stays)
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 63;
+  const uint64_t bit = uint64_t{1} << dev;
+  if (!(done.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return QAT_ERR_CUDA;
+    }
+    if (dev < 63) done.fetch_or(bit, std::memory_order_acq_rel);
   }
   const HeadTiles t = head_tiles(a.q_heads, c.heads, c.d, S::kF32);
   const int sms = device_info().sms;

@@ -25,8 +25,7 @@ template <typename T, int V>
 struct Run {
   static constexpr int BYTES = V * T::BYTES, W = (BYTES + 3) / 4;
   uint32_t w[W];
-  __device__ __forceinline__ void load(const void* base, int64_t i) {
-    const char* p = static_cast<const char*>(base) + i * T::BYTES;
+  __device__ __forceinline__ void load(const char* p) {
     if constexpr (BYTES >= 16) {
 #pragma unroll
       for (int j = 0; j < BYTES / 16; ++j) {
@@ -59,8 +58,7 @@ struct Run {
       for (int e = 0; e < V; e += 2) w[e >> 1] = pack_bf16x2(v[e], e + 1 < V ? v[e + 1] : 0.0f);
     }
   }
-  __device__ __forceinline__ void store(void* base, int64_t i) const {
-    char* p = static_cast<char*>(base) + i * T::BYTES;
+  __device__ __forceinline__ void store(char* p) const {
     if constexpr (BYTES >= 16) {
 #pragma unroll
       for (int j = 0; j < BYTES / 16; ++j)
@@ -134,16 +132,28 @@ __device__ __forceinline__ void vmul(const float (&a)[N], float b, float (&r)[N]
   if (N & 1) r[N - 1] = __fmul_rn(a[N - 1], b);
 }
 template <int N>
-__device__ __forceinline__ float vsum(const float (&a)[N]) {
-  float s = 0.0f;
+__device__ __forceinline__ void vfma(const float (&a)[N], float b, const float (&c)[N], float (&r)[N]) {
 #pragma unroll
-  for (int e = 0; e < N; ++e) s += a[e];
-  return s;
+  for (int e = 0; e + 1 < N; e += 2) fma2(a[e], a[e + 1], b, b, c[e], c[e + 1], r[e], r[e + 1]);
+  if (N & 1) r[N - 1] = __fmaf_rn(a[N - 1], b, c[N - 1]);
+}
+template <int N>
+__device__ __forceinline__ float vsum(const float (&a)[N]) {
+  if constexpr (N == 1) {
+    return a[0];
+  } else if constexpr (N == 2) {
+    return a[0] + a[1];
+  } else {
+    float x = a[0], y = a[1];
+#pragma unroll
+    for (int e = 2; e < N; e += 2) add2(x, y, a[e], a[e + 1], x, y);
+    return x + y;
+  }
 }
 
-// A lane's units of one head, u = lane + lanes * p: where they lie, and whether their
-// pairs are turned.
-template <int V, int NP, bool INTER>
+// A lane's units of one head, u = lane + lanes * p: the bytes where their runs lie,
+// and whether their pairs are turned.
+template <typename T, int V, int NP, bool INTER>
 struct Units {
   int a[NP], b[NP];
   bool has_a[NP], has_b[NP], turned[NP];
@@ -155,6 +165,7 @@ struct Units {
       turned[p] = u < rotary / (2 * V);
       has_a[p] = a[p] < d;
       has_b[p] = has_a[p] && b[p] < d;
+      a[p] *= T::BYTES, b[p] *= T::BYTES;
     }
   }
 };
@@ -163,10 +174,11 @@ struct Units {
 template <typename T, int V, bool INTER>
 struct Pairs {
   Run<T, V> ra, rb;
-  __device__ __forceinline__ void load(const void* base, int64_t at, int a, int b, bool ha, bool hb) {
+  // from a head at p: the runs at bytes a and b of it, where there are any
+  __device__ __forceinline__ void load(const char* p, int a, int b, bool ha, bool hb) {
     ra.zero(), rb.zero();
-    if (ha) ra.load(base, at + a);
-    if (hb) rb.load(base, at + b);
+    if (ha) ra.load(p + a);
+    if (hb) rb.load(p + b);
   }
   __device__ __forceinline__ void get(float (&x)[V], float (&y)[V]) const {
 #pragma unroll
@@ -188,20 +200,20 @@ struct Pairs {
     }
     ra.set(v), rb.set(v + V);
   }
-  __device__ __forceinline__ void store(void* base, int64_t at, int a, int b, bool ha, bool hb) const {
-    if (ha) ra.store(base, at + a);
-    if (hb) rb.store(base, at + b);
+  __device__ __forceinline__ void store(char* p, int a, int b, bool ha, bool hb) const {
+    if (ha) ra.store(p + a);
+    if (hb) rb.store(p + b);
   }
 };
 
 template <typename T, int V, int NP, bool INTER>
-__device__ __forceinline__ void load_weight(const void* w, const Units<V, NP, INTER>& un,
+__device__ __forceinline__ void load_weight(const void* w, const Units<T, V, NP, INTER>& un,
                                             float (&wa)[NP][V], float (&wb)[NP][V]) {
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     if (w) {
       Pairs<T, V, INTER> x;
-      x.load(w, 0, un.a[p], un.b[p], un.has_a[p], un.has_b[p]);
+      x.load(static_cast<const char*>(w), un.a[p], un.b[p], un.has_a[p], un.has_b[p]);
       x.get(wa[p], wb[p]);
     } else {
 #pragma unroll
@@ -233,32 +245,34 @@ constexpr int kRopeThreads = 256;
 // Blocks (x: tokens, y: runs of `per` heads, the queries' first), a group a token.
 // All lanes of a warp take the same number of steps (shuffles).
 template <typename T, int V, int NP, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, V == 8 ? 3 : 2) k_rope_fwd(RopeArgs r, int lanes, int per, int runs0) {
+__global__ void __launch_bounds__(kRopeThreads, V == 8 && T::BYTES == 2 ? 3 : 2) k_rope_fwd(RopeArgs r, int lanes, int per, int runs0) {
   using P = Pairs<T, V, INTER>;
   const int lane = threadIdx.x & (lanes - 1);
   const int64_t token = (int64_t)blockIdx.x * (kRopeThreads / lanes) + threadIdx.x / lanes;
   const int which = (int)blockIdx.y >= runs0;
   const int h0 = ((int)blockIdx.y - (which ? runs0 : 0)) * per;
-  const int n = token < r.tokens ? min(per, r.heads[which] - h0) : 0;
   const int steps = min(per, r.heads[which] - h0);
-  const int64_t hs = r.head_stride[which];
-  const int64_t xt = n ? token * r.token_stride[which] + h0 * hs : 0;
-  const int64_t yt = (token * r.heads[which] + h0) * r.d;
-  const Units<V, NP, INTER> un(lane, lanes, r.d, r.rotary);
+  const bool on = token < r.tokens;
+  const Units<T, V, NP, INTER> un(lane, lanes, r.d, r.rotary);
+  const int64_t x_step = r.head_stride[which] * T::BYTES, y_step = (int64_t)r.d * T::BYTES;
+  const char* x = static_cast<const char*>(r.x[which]) +
+                  (on ? token * r.token_stride[which] * T::BYTES + h0 * x_step : 0);
+  char* y = static_cast<char*>(r.y[which]) + (on ? (token * r.heads[which] + h0) * y_step : 0);
 
   P next[NP];
-  auto fetch = [&](int h) {
+  auto fetch = [&]() {
 #pragma unroll
     for (int p = 0; p < NP; ++p)
-      next[p].load(r.x[which], xt + h * hs, un.a[p], un.b[p], h < n && un.has_a[p], h < n && un.has_b[p]);
+      next[p].load(x, un.a[p], un.b[p], on && un.has_a[p], on && un.has_b[p]);
+    x += x_step;
   };
-  fetch(0);
+  fetch();
   // a' = (a wa c - b wb s) rstd, b' = (b wb c + a wa s) rstd
   float ac[NP][V], bs[NP][V], bc[NP][V], as[NP][V];
   {
     float wa[NP][V], wb[NP][V], c[NP][V], s[NP][V];
     load_weight<T, V, NP, INTER>(r.w[which], un, wa, wb);
-    load_angles<V, NP>(r, n ? token : 0, lane, lanes, c, s);
+    load_angles<V, NP>(r, on ? token : 0, lane, lanes, c, s);
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
       vmul(wa[p], c[p], ac[p]);
@@ -272,7 +286,7 @@ __global__ void __launch_bounds__(kRopeThreads, V == 8 ? 3 : 2) k_rope_fwd(RopeA
     P now[NP];
 #pragma unroll
     for (int p = 0; p < NP; ++p) now[p] = next[p];
-    if (h + 1 < steps) fetch(h + 1);
+    if (h + 1 < steps) fetch();
     float a[NP][V], b[NP][V], sq[V] = {};
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
@@ -282,19 +296,19 @@ __global__ void __launch_bounds__(kRopeThreads, V == 8 ? 3 : 2) k_rope_fwd(RopeA
     const float rstd = r.norm ? rstd_of(r, group_sum(vsum(sq), lanes)) : 1.0f;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-      float x[V], y[V];
-      vmul(a[p], ac[p], x);
-      vmul(b[p], bc[p], y);
+      float u[V], v[V];
+      vmul(a[p], ac[p], u);
+      vmul(b[p], bc[p], v);
       if (un.turned[p]) {  // (0 times what is not finite would not pass the others as they are)
-        vfma(b[p], bs[p], x, x);
-        vfma(a[p], as[p], y, y);
+        vfma(b[p], bs[p], u, u);
+        vfma(a[p], as[p], v, v);
       }
-      vmul(x, rstd, x);
-      vmul(y, rstd, y);
-      now[p].put(x, y);
-      now[p].store(r.y[which], yt + (int64_t)h * r.d, un.a[p], un.b[p], h < n && un.has_a[p],
-                   h < n && un.has_b[p]);
+      vmul(u, rstd, u);
+      vmul(v, rstd, v);
+      now[p].put(u, v);
+      now[p].store(y, un.a[p], un.b[p], on && un.has_a[p], on && un.has_b[p]);
     }
+    y += y_step;
   }
 }
 
@@ -308,7 +322,7 @@ __global__ void __launch_bounds__(kRopeThreads, V == 8 && T::BYTES == 2 ? 2 : 1)
   pdl_trigger();
   const int lane = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes;
   const int groups = kRopeThreads / lanes;
-  const Units<V, NP, INTER> un(lane, lanes, r.d, r.rotary);
+  const Units<T, V, NP, INTER> un(lane, lanes, r.d, r.rotary);
   for (int which = 0; which < 2; ++which) {
     const int heads = r.heads[which];
     const bool sums = r.dw[which] != nullptr;
@@ -322,18 +336,21 @@ __global__ void __launch_bounds__(kRopeThreads, V == 8 && T::BYTES == 2 ? 2 : 1)
       const int64_t item = base + group, token = item < items ? item / runs : 0;
       const int h0 = item < items ? (int)(item - token * runs) * per : 0;
       const int n = item < items ? min(per, heads - h0) : 0;
-      const int64_t xt = token * r.token_stride[which] + h0 * r.head_stride[which];
-      const int64_t gt = (token * heads + h0) * r.d;
+      const int64_t x_step = r.head_stride[which] * T::BYTES, g_step = (int64_t)r.d * T::BYTES;
+      const char* x = static_cast<const char*>(r.x[which]) +
+                      token * r.token_stride[which] * T::BYTES + h0 * x_step;
+      const char* g = static_cast<const char*>(r.g[which]) + (token * heads + h0) * g_step;
+      char* y = r.y[which] ? static_cast<char*>(r.y[which]) + (token * heads + h0) * g_step : nullptr;
       P next_x[NP], next_g[NP];
-      auto fetch = [&](int h) {
+      auto fetch = [&](bool on) {
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          const bool ha = h < n && un.has_a[p], hb = h < n && un.has_b[p];
-          next_x[p].load(r.x[which], xt + h * r.head_stride[which], un.a[p], un.b[p], ha, hb);
-          next_g[p].load(r.g[which], gt + (int64_t)h * r.d, un.a[p], un.b[p], ha, hb);
+          next_x[p].load(x, un.a[p], un.b[p], on && un.has_a[p], on && un.has_b[p]);
+          next_g[p].load(g, un.a[p], un.b[p], on && un.has_a[p], on && un.has_b[p]);
         }
+        x += x_step, g += g_step;
       };
-      fetch(0);
+      fetch(n > 0);
       float c[NP][V], s[NP][V];
       load_angles<V, NP>(r, token, lane, lanes, c, s);
       for (int h = 0; h < per; ++h) {
@@ -344,17 +361,17 @@ __global__ void __launch_bounds__(kRopeThreads, V == 8 && T::BYTES == 2 ? 2 : 1)
           next_x[p].get(a[p], b[p]);
           now[p] = next_g[p];
         }
-        if (h + 1 < per) fetch(h + 1);
+        if (h + 1 < per) fetch(h + 1 < n);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          float x[V], y[V], t[V];
-          now[p].get(x, y);
-          vmul(x, c[p], ga[p]);
-          vmul(y, c[p], gb[p]);
+          float u[V], v[V], t[V];
+          now[p].get(u, v);
+          vmul(u, c[p], ga[p]);
+          vmul(v, c[p], gb[p]);
           if (un.turned[p]) {
-            vfma(y, s[p], ga[p], ga[p]);
-            vmul(s[p], -1.0f, t);
-            vfma(x, t, gb[p], gb[p]);
+            vfma(v, s[p], ga[p], ga[p]);
+            vmul(u, -1.0f, t);
+            vfma(t, s[p], gb[p], gb[p]);
           }
           if (r.norm) {
             vfma(a[p], a[p], sq, sq), vfma(b[p], b[p], sq, sq);
@@ -368,15 +385,13 @@ __global__ void __launch_bounds__(kRopeThreads, V == 8 && T::BYTES == 2 ? 2 : 1)
           mean = -(group_sum(vsum(gx), lanes) * rstd) * r.inv_d;  // of g'w z
         }
         // dw += g' z; dx = (g'w - z mean) rstd
-        auto finish = [&](const float (&g)[V], const float (&w)[V], float (&x)[V], float (&dw)[V]) {
-          float t[V], u[V];
-          vmul(x, rstd, x);
-          vfma(g, x, dw, dw);
-          vmul(g, w, t);
-          vmul(x, mean, u);
-#pragma unroll
-          for (int e = 0; e < V; ++e) u[e] += t[e];
-          vmul(u, rstd, x);
+        auto finish = [&](const float (&gr)[V], const float (&w)[V], float (&z)[V], float (&dw)[V]) {
+          float t[V];
+          vmul(z, rstd, z);
+          vfma(gr, z, dw, dw);
+          vmul(gr, w, t);
+          vfma(z, mean, t, t);
+          vmul(t, rstd, z);
         };
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
@@ -387,10 +402,10 @@ __global__ void __launch_bounds__(kRopeThreads, V == 8 && T::BYTES == 2 ? 2 : 1)
           } else {
             now[p].put(ga[p], gb[p]);
           }
-          if (r.y[which])
-            now[p].store(r.y[which], gt + (int64_t)h * r.d, un.a[p], un.b[p], h < n && un.has_a[p],
-                         h < n && un.has_b[p]);
+          const bool on = h < n && y;
+          now[p].store(y, un.a[p], un.b[p], on && un.has_a[p], on && un.has_b[p]);
         }
+        y += y ? g_step : 0;
       }
     }
     if (!sums) continue;  // (the same for the whole grid)
