@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_read(KvPlace p, int64_t token
 // Rows a group takes at a time: four once that leaves every SM full (read: 134 MB of
 // int8 rows with four 63 us, one 111), one for fewer, which then run side by side.
 bool many_rows(int64_t rows, int lanes) {
-  return rows * lanes >= (int64_t)device_info().sms * 2048 * 8;
+  return rows * lanes >= (int64_t)device_info().sms * 2048 * 4;
 }
 // A grid for runs of U rows of each token; false where it does not fit.
 bool kv_grid(const KvPlace& p, int64_t tokens, int lanes, int u, dim3* grid) {

@@ -48,9 +48,12 @@ constexpr float kSlack = 8.0f;  // scores may exceed the running maximum by 2^8 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
-// 16 bytes from global to shared memory
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes from global to shared memory, where `on`
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool on) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.u32 p, %2, 0; @p cp.async.cg.shared.global [%0], [%1], 16; }" ::"r"(dst),
+      "l"(src), "r"((uint32_t)on)
+      : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -94,10 +97,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
+// x *= f in x's own register: the branch that rescales the sums must not leave them
+// in others, from which every pass of the loop would move them back
+__device__ __forceinline__ void scale_in_place(float& x, float f) {
+  asm volatile("mul.rn.f32 %0, %0, %1;" : "+f"(x) : "f"(f));
+}
 template <int BYTES>
 __device__ __forceinline__ void load_run(const char* p, uint32_t (&w)[BYTES / 4]) {
   if constexpr (BYTES == 16) {
@@ -304,7 +312,8 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
 
   // --- this warp's run of the work --------------------------------------------------
   // (a position's number plus a step fits 31 bits)
-  const int64_t capacity = min(a.table_cols * c.page_size, (int64_t)kKvMaxLength);
+  const int64_t capacity =
+      c.pages > 0 ? min(a.table_cols * c.page_size, (int64_t)kKvMaxLength) : 0;
   const int hgs = c.heads * tiles;
   auto length_of = [&](int b) -> int {  // 0 where there is nothing to read
     const int n = __ldg(a.lengths + b);
@@ -390,6 +399,8 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
       lane == 4 ? reinterpret_cast<const char*>(c.kz) : reinterpret_cast<const char*>(c.ks) + lane * 16;
   const char* const v_params =
       lane == 4 ? reinterpret_cast<const char*>(c.vz) : reinterpret_cast<const char*>(c.vs) + lane * 16;
+  const int p_step = lane == 4 ? 16 : 64, p_lanes = zeros ? 5 : 4;
+  const int r_step = 32 / units, u_step = 32 - r_step * units;  // from one of a lane's units to its next
   if (!EXACT) {  // elements behind head_dim stay zeros (never NaN, whose product with 0 is NaN)
     for (int i = lane * 16; i < 2 * (int)kRingEnd; i += 512)
       *reinterpret_cast<uint4*>(ring_p + i) = make_uint4(0, 0, 0, 0);
@@ -408,56 +419,48 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
       const int steps = to - from;
 
       // --- copies, tile after tile ----------------------------------------------------
-      // Lane l knows the place (in tiles of 16 rows) of the l-th of the 32 tiles from
-      // the last look-up on: -1 a page that does not exist, -2 behind the piece.
-      int64_t place = -2, v_at = -2;  // (v_at: of the tile whose values come next)
+      // The page of the next tile of keys, its offset there (in tiles), and the place in
+      // the cache (in tiles of 16 rows) of the tile whose values come next.
+      int rem = from % tiles_page;
+      const int32_t* entry = a.table + (int64_t)b * a.table_stride + from / tiles_page;
+      int page = __ldg(entry);
+      int64_t v_at = 0;
       bool bad = false;
       // 16 rows, their scales and zero points.  Where rows lie behind the sequence the
       // last unit before them is read in their stead: they have no weight.
-      auto copy = [&](uint32_t slot, const char* codes, const char* params, int64_t at, int step) {
+      auto copy = [&](uint32_t slot, const char* codes, const char* params, int64_t at, int step,
+                      bool on) {
         const char* src = codes + at * (16 * row_bytes);
-        const int rows = length - (from + step) * 16;
-        if (EXACT && rows >= 16) {
-          src += lane * 16;
+        const int last = min(16, length - (from + step) * 16) * row_bytes - 16;
+        if constexpr (EXACT) {
 #pragma unroll
           for (int i = 0; i < S::LOADS; ++i)
-            copy_async(slot + 512 * i + (c_place ^ S::mix(i * 32 / S::UNITS) * 16), src + 512 * i);
+            copy_async(slot + 512 * i + (c_place ^ S::mix(i * 32 / S::UNITS) * 16),
+                       src + min(lane * 16 + 512 * i, last), on);
         } else {
-          const int last = min(16, rows) * row_bytes - 16;
           int r = c_row, u = c_unit;
 #pragma unroll 1
           for (int i = lane; i < 16 * units; i += 32) {
-            copy_async(slot + S::place(r, u * 16), src + min(i * 16, last));
-            r += 32 / units, u += 32 % units;
+            copy_async(slot + S::place(r, u * 16), src + min(i * 16, last), on);
+            r += r_step, u += u_step;
             if (u >= units) u -= units, ++r;
           }
         }
-        if constexpr (F != QAT_CACHE_BF16) {
-          if (lane < (zeros ? 5 : 4))
-            copy_async(slot + S::TILE / 2 + lane * 16, params + at * (lane == 4 ? 16 : 64));
-        }
+        if constexpr (F != QAT_CACHE_BF16)
+          copy_async(slot + S::TILE / 2 + lane * 16, params + at * p_step, on && lane < p_lanes);
       };
       // keys of tile `step` + 1 and values of tile `step`
       auto issue = [&](int step, uint32_t k_slot, uint32_t v_slot) {
-        if (v_at >= 0) copy(ring + kRingEnd + v_slot, c.v, v_params, v_at, step);
-        v_at = -2;
-        if (++step < steps) {
-          if (step % 32 == 0) {
-            const int tile = from + step + lane;
-            place = -2;
-            if (tile < to) {
-              const int col = tile / tiles_page;
-              const int page = __ldg(a.table + (int64_t)b * a.table_stride + col);
-              place = page < 0 || page >= c.pages
-                          ? -1
-                          : ((int64_t)page * c.heads + kvh) * tiles_page + (tile - col * tiles_page);
-            }
-          }
-          v_at = __shfl_sync(kFull, place, step % 32);
-          if (v_at >= 0)
-            copy(ring + k_slot, c.k, k_params, v_at, step);
-          else
-            bad = true;
+        copy(ring + kRingEnd + v_slot, c.v, v_params, v_at, step, step >= 0 && step < steps);
+        ++step;
+        const bool on = step < steps;
+        const bool there = page >= 0 && page < c.pages;
+        bad = bad || (on && !there);
+        v_at = ((int64_t)(there ? page : 0) * c.heads + kvh) * tiles_page + rem;
+        copy(ring + k_slot, c.k, k_params, v_at, step, on && there);
+        if (++rem == tiles_page) {
+          rem = 0, ++entry;
+          if (step + 1 < steps) page = __ldg(entry);
         }
         copy_commit();
       };
@@ -676,7 +679,7 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
               const float both = was * shrink;
               zsum[ht][i] *= both;
 #pragma unroll
-              for (int j = 0; j < S::MT; ++j) o[ht][j][i] *= both, o[ht][j][2 + i] *= both;
+              for (int j = 0; j < S::MT; ++j) scale_in_place(o[ht][j][i], both), scale_in_place(o[ht][j][2 + i], both);
             }
         }
         if constexpr (HALF) vs[0] *= unit, vs[1] *= unit;
