@@ -48,30 +48,36 @@ constexpr float kSlack = 8.0f;  // scores may exceed the running maximum by 2^8 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
-// 16 bytes from global to shared memory, where `on`
+// 16 bytes from global to shared memory, or zeros
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool on) {
-  asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %2, 0; @p cp.async.cg.shared.global [%0], [%1], 16; }" ::"r"(dst),
-      "l"(src), "r"((uint32_t)on)
-      : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-template <bool HALF>
+// (FIRST: with no sum before it)
+template <bool HALF, bool FIRST = false>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (HALF)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+#define QAT_MMA(TYPE)                                                                              \
+  if constexpr (FIRST)                                                                             \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                                    \
+        ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"                 \
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])                                           \
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));                \
+  else                                                                                             \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                                    \
+        ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"                     \
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])                                           \
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1))
+  if constexpr (HALF) {
+    QAT_MMA("f16");
+  } else {
+    QAT_MMA("bf16");
+  }
+#undef QAT_MMA
 }
 // The next 16-bit parts of two numbers, packed; they keep the remainders.
 template <bool HALF>
@@ -106,17 +112,29 @@ __device__ __forceinline__ float exp2_fast(float x) {
 __device__ __forceinline__ void scale_in_place(float& x, float f) {
   asm volatile("mul.rn.f32 %0, %0, %1;" : "+f"(x) : "f"(f));
 }
+// Loads from shared memory (as one instruction each: vectors that the compiler takes
+// apart it does not always put together again).
 template <int BYTES>
-__device__ __forceinline__ void load_run(const char* p, uint32_t (&w)[BYTES / 4]) {
-  if constexpr (BYTES == 16) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-  } else if constexpr (BYTES == 8) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    w[0] = v.x, w[1] = v.y;
-  } else {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
-  }
+__device__ __forceinline__ void load_run(uint32_t at, uint32_t (&w)[BYTES / 4]) {
+  if constexpr (BYTES == 16)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(at)
+                 : "memory");
+  else if constexpr (BYTES == 8)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ float load_f32(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float load_s8(uint32_t at) {
+  int v;
+  asm volatile("ld.shared.s8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return (float)v;
 }
 
 // ---------------------------------------------------------------------------
@@ -420,54 +438,57 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
 
       // --- copies, tile after tile ----------------------------------------------------
       // The page of the next tile of keys, its offset there (in tiles), and the place in
-      // the cache (in tiles of 16 rows) of the tile whose values come next.
+      // the cache (in tiles of 16 rows: 31 bits) of the tile whose values come next.
       int rem = from % tiles_page;
       const int32_t* entry = a.table + (int64_t)b * a.table_stride + from / tiles_page;
       int page = __ldg(entry);
-      int64_t v_at = 0;
+      uint32_t v_at = 0;
       bool bad = false;
-      // 16 rows, their scales and zero points.  Where rows lie behind the sequence the
-      // last unit before them is read in their stead: they have no weight.
-      auto copy = [&](uint32_t slot, const char* codes, const char* params, int64_t at, int step,
+      // 16 rows, their scales and zero points; zeros in place of the rows from `rows` on.
+      auto copy = [&](uint32_t slot, const char* codes, const char* params, uint32_t at, int rows,
                       bool on) {
-        const char* src = codes + at * (16 * row_bytes);
-        const int last = min(16, length - (from + step) * 16) * row_bytes - 16;
+        const char* src = codes + (uint64_t)at * (uint32_t)(16 * row_bytes);
+        const int left = on ? rows - c_row : 0;
         if constexpr (EXACT) {
 #pragma unroll
           for (int i = 0; i < S::LOADS; ++i)
-            copy_async(slot + 512 * i + (c_place ^ S::mix(i * 32 / S::UNITS) * 16),
-                       src + min(lane * 16 + 512 * i, last), on);
+            copy_async(slot + 512 * i + (c_place ^ S::mix(i * 32 / S::UNITS) * 16), src + 512 * i,
+                       left > i * 32 / S::UNITS);
         } else {
-          int r = c_row, u = c_unit;
+          int r = 0, u = c_unit;
 #pragma unroll 1
-          for (int i = lane; i < 16 * units; i += 32) {
-            copy_async(slot + S::place(r, u * 16), src + min(i * 16, last), on);
+          for (int i = 0; lane + i < 16 * units; i += 32) {
+            copy_async(slot + S::place(c_row + r, u * 16), src + i * 16, left > r);
             r += r_step, u += u_step;
             if (u >= units) u -= units, ++r;
           }
         }
         if constexpr (F != QAT_CACHE_BF16)
-          copy_async(slot + S::TILE / 2 + lane * 16, params + at * p_step, on && lane < p_lanes);
+          if (lane < p_lanes)
+            copy_async(slot + S::TILE / 2 + lane * 16, params + (uint64_t)at * (uint32_t)p_step, on);
       };
+      const char* const k_codes = c.k + lane * 16;
+      const char* const v_codes = c.v + lane * 16;
+      int rows_ahead = length - from * 16 + 16;  // of the tile whose values come next
       // keys of tile `step` + 1 and values of tile `step`
       auto issue = [&](int step, uint32_t k_slot, uint32_t v_slot) {
-        copy(ring + kRingEnd + v_slot, c.v, v_params, v_at, step, step >= 0 && step < steps);
-        ++step;
-        const bool on = step < steps;
-        const bool there = page >= 0 && page < c.pages;
+        copy(ring + kRingEnd + v_slot, v_codes, v_params, v_at, rows_ahead, step >= 0 && step < steps);
+        rows_ahead -= 16;
+        const bool on = step + 1 < steps;
+        const bool there = (uint32_t)page < (uint32_t)c.pages;
         bad = bad || (on && !there);
-        v_at = ((int64_t)(there ? page : 0) * c.heads + kvh) * tiles_page + rem;
-        copy(ring + k_slot, c.k, k_params, v_at, step, on && there);
+        v_at = ((uint32_t)(there ? page : 0) * (uint32_t)c.heads + kvh) * tiles_page + rem;
+        copy(ring + k_slot, k_codes, k_params, v_at, rows_ahead, on && there);
         if (++rem == tiles_page) {
           rem = 0, ++entry;
-          if (step + 1 < steps) page = __ldg(entry);
+          if (step + 2 < steps) page = __ldg(entry);
         }
         copy_commit();
       };
       auto after = [&](uint32_t slot) {
         return slot == kRingEnd - S::HALF_STAGE ? 0 : slot + S::HALF_STAGE;
       };
-#pragma unroll
+#pragma unroll 1
       for (int i = -1; i < S::STAGES - 1; ++i)
         issue(i, (i + 1) * S::HALF_STAGE, max(i, 0) * S::HALF_STAGE);
 
@@ -550,15 +571,9 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
 
       // Scores of a tile: positions g, g + 8 (rows) and heads 2 t4, 2 t4 + 1 (columns).
       float s[HT][4];
-      auto scores = [&](const char* slot) {
+      auto scores = [&](uint32_t slot) {
         // (two sums: a product waits for the one before the last)
         float acc[S::kF32 ? 3 : 2][HT][4];
-#pragma unroll
-        for (int p = 0; p < (S::kF32 ? 3 : 2); ++p)
-#pragma unroll
-          for (int ht = 0; ht < HT; ++ht)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[p][ht][i] = 0.0f;
 #pragma unroll
         for (int j = 0; j < S::NK; ++j) {
           uint32_t w[2][S::CK / 4];
@@ -583,12 +598,19 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
 #pragma unroll
               for (int p = 0; p < 3; ++p) {
                 const uint2 f = qfrag[(p * S::KS + ks) * 32 + lane];
-                mma<HALF>(acc[p][0], fa, f.x, f.y);
+                if (ks == 0)
+                  mma<HALF, true>(acc[p][0], fa, f.x, f.y);
+                else
+                  mma<HALF>(acc[p][0], fa, f.x, f.y);
               }
             } else {
 #pragma unroll
-              for (int ht = 0; ht < HT; ++ht)
-                mma<HALF>(acc[ks % 2][ht], fa, qr[ht][ks][0], qr[ht][ks][1]);
+              for (int ht = 0; ht < HT; ++ht) {
+                if (ks < 2)
+                  mma<HALF, true>(acc[ks % 2][ht], fa, qr[ht][ks][0], qr[ht][ks][1]);
+                else
+                  mma<HALF>(acc[ks % 2][ht], fa, qr[ht][ks][0], qr[ht][ks][1]);
+              }
             }
           }
         }
@@ -603,25 +625,19 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
       // The tile's weights, as the second operand of the value products.
       uint32_t wb[HT][S::PP][2];
       float ks[2] = {1.0f, 1.0f}, kz[2] = {0.0f, 0.0f};
-      auto key_params = [&](const char* slot) {
+      auto key_params = [&](uint32_t slot) {
         if constexpr (F != QAT_CACHE_BF16) {
-          const float* sc = reinterpret_cast<const float*>(slot + S::TILE / 2);
-          ks[0] = sc[g], ks[1] = sc[g + 8];
-          if (zeros) {
-            const int8_t* z = reinterpret_cast<const int8_t*>(slot + S::TILE / 2 + 64);
-            kz[0] = z[g], kz[1] = z[g + 8];
-          }
+          const uint32_t at = slot + S::TILE / 2;
+          ks[0] = load_f32(at + 4 * g), ks[1] = load_f32(at + 4 * g + 32);
+          if (zeros) kz[0] = load_s8(at + 64 + g), kz[1] = load_s8(at + 72 + g);
         }
       };
-      auto weigh = [&](int tile, const char* v_slot) {
+      auto weigh = [&](int tile, uint32_t v_slot) {
         float vs[2] = {1.0f, 1.0f}, vz[2] = {0.0f, 0.0f};
         if constexpr (F != QAT_CACHE_BF16) {
-          const float* sc = reinterpret_cast<const float*>(v_slot + S::TILE / 2);
-          vs[0] = sc[g], vs[1] = sc[g + 8];
-          if (zeros) {
-            const int8_t* z = reinterpret_cast<const int8_t*>(v_slot + S::TILE / 2 + 64);
-            vz[0] = z[g], vz[1] = z[g + 8];
-          }
+          const uint32_t at = v_slot + S::TILE / 2;
+          vs[0] = load_f32(at + 4 * g), vs[1] = load_f32(at + 4 * g + 32);
+          if (zeros) vz[0] = load_s8(at + 64 + g), vz[1] = load_s8(at + 72 + g);
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r)
@@ -703,7 +719,7 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
         }
       };
       // Weighted values: rows are head elements, k the positions.
-      auto values = [&](const char* slot) {
+      auto values = [&](uint32_t slot) {
 #pragma unroll
         for (int j = 0; j < S::NV; ++j) {
           uint32_t v[4][S::CV / 4];
@@ -731,9 +747,10 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
               for (int ht = 0; ht < HT; ++ht) {
                 if constexpr (S::kF32) {
                   // (sums of many tiles on the tensor cores would drift: 16 positions only)
-                  float part[4] = {};
-#pragma unroll
-                  for (int p = S::PP - 1; p >= 0; --p) mma<HALF>(part, fa, wb[ht][p][0], wb[ht][p][1]);
+                  float part[4];
+                  mma<HALF, true>(part, fa, wb[ht][2][0], wb[ht][2][1]);
+                  mma<HALF>(part, fa, wb[ht][1][0], wb[ht][1][1]);
+                  mma<HALF>(part, fa, wb[ht][0][0], wb[ht][0][1]);
 #pragma unroll
                   for (int x = 0; x < 4; ++x) o[ht][mt][x] += part[x];
                 } else {
@@ -751,18 +768,18 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
       uint32_t prev = kRingEnd - S::HALF_STAGE, slot = 0, next = after(0);  // of this step
       copy_wait<S::STAGES - 1>();
       __syncwarp();  // (scales are other lanes' copies)
-      scores(ring_p);
-      key_params(ring_p);
+      scores(ring);
+      key_params(ring);
       for (int step = 0; step < steps; ++step) {
         copy_wait<S::STAGES - 2>();
         __syncwarp();  // also: this step's keys and the values of the step before are done with
-        weigh(from + step, ring_p + kRingEnd + slot);
+        weigh(from + step, ring + kRingEnd + slot);
         issue(step + S::STAGES - 1, slot, prev);
         if (step + 1 < steps) {
-          scores(ring_p + next);
-          key_params(ring_p + next);
+          scores(ring + next);
+          key_params(ring + next);
         }
-        values(ring_p + kRingEnd + slot);
+        values(ring + kRingEnd + slot);
         prev = slot, slot = next, next = after(next);
       }
       copy_wait<0>();

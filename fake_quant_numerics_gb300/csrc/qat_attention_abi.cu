@@ -69,6 +69,8 @@ qat_status check_cache(const qat_kv_cache* c) {
     return QAT_ERR_INVALID_ARGUMENT;
   if (c->pages < 0 || c->pages > INT32_MAX / c->page_size || c->heads < 1 || c->heads > 32767)
     return QAT_ERR_INVALID_ARGUMENT;
+  // (tiles of 16 rows are counted in 31 bits; their bytes would fill more than any memory)
+  if (c->pages * (c->page_size / 16) > INT32_MAX / c->heads) return QAT_ERR_INVALID_ARGUMENT;
   const bool ints = f == QAT_CACHE_INT8 || f == QAT_CACHE_INT4;
   if (!c->k_zero_points != !c->v_zero_points || (c->k_zero_points && !ints))
     return QAT_ERR_INVALID_ARGUMENT;

@@ -641,7 +641,7 @@ qat_status qat_head_norm_rope_backward(
  *   k_zero_points, v_zero_points (both or neither, integer formats): int8, alike;
  *   all 16-byte aligned.
  * head_dim: a multiple of 8 up to 256; page_size: a multiple of 16; pages *
- * page_size below 2^31; heads up to 32767.
+ * page_size below 2^31 and pages * page_size * heads below 2^35; heads up to 32767.
  */
 typedef enum {
   QAT_CACHE_BF16 = 0,
