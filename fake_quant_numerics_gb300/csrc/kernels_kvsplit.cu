@@ -319,10 +319,13 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
   constexpr int WARPS = S::WARPS, H = S::H;
   constexpr bool HALF = W::kHalf;
   extern __shared__ __align__(16) char smem[];
-  __shared__ int64_t s_sum[WARPS], s_off[WARPS];
+  __shared__ int64_t s_sum[WARPS], s_first[WARPS], s_off[WARPS];
   __shared__ int s_b[WARPS];
-  __shared__ int4 s_part[2 * WARPS];     // sequence, head group, tiles from .. to (none: to = 0)
-  __shared__ float2 s_ml[2 * WARPS][H];  // maximum and sum
+  // Parts: sequence, head group, tiles from .. to (none: to = 0); maximum and sum, then
+  // the factor in its chain; of the chain that starts with it, maximum and sum.
+  static_assert(2 * WARPS <= 32, "a lane for each part");
+  __shared__ int4 s_part[2 * WARPS];
+  __shared__ float2 s_ml[2 * WARPS][H], s_chain[2 * WARPS][H];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   const int d = EXACT ? DP : c.d, row_bytes = EXACT ? S::ROW : c.row_bytes;
@@ -366,19 +369,22 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
   const int64_t runs = max((int64_t)1, min((int64_t)gridDim.x * WARPS, total / kLeastRun));
   const int per = (int)((runs + gridDim.x - 1) / gridDim.x);  // of a block
   auto run_start = [&](int64_t r) { return total * min(r, runs) / runs; };
-  for (int w = 0; w < per; ++w) {
-    const int64_t first = run_start((int64_t)blockIdx.x * per + w);
-    if (before <= first && first < before + own) {
+  const int64_t run = (int64_t)blockIdx.x * per + warp;
+  const int64_t first = run_start(run);
+  if (lane == 0) s_first[warp] = first;
+  __syncthreads();
+  if (own > 0)
+    for (int w = 0; w < per; ++w) {
+      const int64_t f = s_first[w];
+      if (f < before || f >= before + own) continue;
       int b = b_lo;
       int64_t at = before;
-      while (first >= at + cost_of(b) * hgs) at += cost_of(b++) * hgs;
+      while (f >= at + cost_of(b) * hgs) at += cost_of(b++) * hgs;
       s_b[w] = b;
-      s_off[w] = first - at;
+      s_off[w] = f - at;
     }
-  }
   if (threadIdx.x < 2 * WARPS) s_part[threadIdx.x] = make_int4(0, 0, 0, 0);
   __syncthreads();
-  const int64_t run = (int64_t)blockIdx.x * per + warp;
   // sequences that have nothing to read
   const int64_t y_row = a.q_heads * c.d;
   for (int64_t b = (int64_t)blockIdx.x * WARPS + warp; b < batch; b += (int64_t)gridDim.x * WARPS) {
@@ -392,7 +398,7 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
   int64_t left = 0, skip = 0;  // tiles of the run; of its first piece before it
   int b = 0, hg = 0;
   if (warp < per && run < runs && total > 0) {
-    left = run_start(run + 1) - run_start(run);
+    left = run_start(run + 1) - first;
     b = s_b[warp];
     hg = (int)(s_off[warp] / cost_of(b));
     skip = s_off[warp] - hg * cost_of(b);
@@ -842,60 +848,76 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
   __syncthreads();
 
   // --- parts of one sequence that the block's warps hold, one after the other, joined ------
+  // Lane k looks at part k.  A chain is a row of neighbours: the same sequence and group,
+  // each beginning where the one before it ends.
+  const int4 mine = lane < 2 * per ? s_part[lane] : make_int4(0, 0, 0, 0);
+  const uint32_t valid = __ballot_sync(kFull, mine.w > 0);
+  const uint32_t before_me = valid & ((1u << lane) - 1u);
+  const int prev = before_me ? 31 - __clz(before_me) : 0;
+  // (every lane takes part in each exchange: none may hang on the outcome of another)
+  const int prev_b = __shfl_sync(kFull, mine.x, prev), prev_g = __shfl_sync(kFull, mine.y, prev);
+  const int prev_to = __shfl_sync(kFull, mine.w, prev);
+  const bool follows = before_me && prev_b == mine.x && prev_g == mine.y && prev_to == mine.z;
+  const uint32_t starts = __ballot_sync(kFull, mine.w > 0 && !follows);
+  auto chain_of = [&](uint32_t rest) {  // its parts; `rest`: the starts from it on
+    const uint32_t after = rest & (rest - 1);
+    return valid & ~((rest & -rest) - 1u) & (after ? (after & -after) - 1u : kFull);
+  };
+  for (int h = warp; h < H; h += WARPS)
+    for (uint32_t rest = starts; rest; rest &= rest - 1) {
+      const bool in = chain_of(rest) >> lane & 1u;
+      const float2 x = in ? s_ml[lane][h] : make_float2(-INFINITY, 0.0f);
+      float top = x.x;
+      for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
+      const float f = x.x == top ? 1.0f : exp2_fast(x.x - top);
+      float sum = in ? f * x.y : 0.0f;
+      for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(kFull, sum, i);
+      if (in) s_ml[lane][h].x = f;
+      if (lane == 0) s_chain[__ffs(rest) - 1][h] = make_float2(top, sum);
+    }
+  __syncthreads();
   int4 cut = make_int4(0, 0, 0, 0);
-  for (int first = 0; first < 2 * per;) {
-    const int4 p0 = s_part[first];
-    if (p0.w == 0) {
-      ++first;
-      continue;
-    }
-    int last = first, to = p0.w;  // parts first .. last are neighbours
-    for (int i = first + 1; i < 2 * per; ++i) {
-      const int4 p = s_part[i];
-      if (p.w == 0) continue;
-      if (p.x != p0.x || p.y != p0.y || p.z != to) break;
-      last = i, to = p.w;
-    }
-    const int length = length_of(p0.x), n_tiles = (length + 15) / 16;
-    const int kvh = p0.y / tiles, h0 = kvh * group + (p0.y - kvh * tiles) * H;
+  for (uint32_t rest = starts; rest; rest &= rest - 1) {
+    const uint32_t chain = chain_of(rest);
+    const int head = __ffs(rest) - 1, tail = 31 - __clz(chain);
+    const int pb = __shfl_sync(kFull, mine.x, head), pg = __shfl_sync(kFull, mine.y, head);
+    const int from = __shfl_sync(kFull, mine.z, head), to = __shfl_sync(kFull, mine.w, tail);
+    const int n_tiles = (length_of(pb) + 15) / 16;
+    const int kvh = pg / tiles, h0 = kvh * group + (pg - kvh * tiles) * H;
     const int heads = min(H, (kvh + 1) * group - h0);
-    const bool whole = p0.z == 0 && to == n_tiles;
-    const int64_t slot = ((int64_t)blockIdx.x * 2 + (p0.z == 0)) * H;
+    const bool whole = from == 0 && to == n_tiles;
+    const int64_t slot = ((int64_t)blockIdx.x * 2 + (from == 0)) * H;
     for (int i = threadIdx.x; i < heads * (d / 4); i += S::THREADS) {
       const int h = i / (d / 4), e = (i - h * (d / 4)) * 4;
-      float top = -INFINITY, sum = 0.0f, y[4] = {};
-      for (int k = first; k <= last; ++k)
-        if (s_part[k].w) top = fmaxf(top, s_ml[k][h].x);
-      for (int k = first; k <= last; ++k) {
-        if (s_part[k].w == 0) continue;
-        const float2 ml = s_ml[k][h];
-        const float f = ml.x == top ? 1.0f : exp2_fast(ml.x - top);
-        sum = __fmaf_rn(f, ml.y, sum);
+      float y[4] = {};
+      for (uint32_t m = chain; m; m &= m - 1) {
+        const int k = __ffs(m) - 1;
+        const float f = s_ml[k][h].x;
         const float4 v = *reinterpret_cast<const float4*>(
             smem + (k / 2) * S::WARP + (k % 2 ? 0 : S::RING) + (h * d + e) * 4);
         y[0] = __fmaf_rn(f, v.x, y[0]), y[1] = __fmaf_rn(f, v.y, y[1]);
         y[2] = __fmaf_rn(f, v.z, y[2]), y[3] = __fmaf_rn(f, v.w, y[3]);
       }
+      const float2 t = s_chain[head][h];
       if (whole) {
-        const int64_t row = (int64_t)p0.x * a.q_heads + h0 + h;
-        const float by = sum == 0.0f ? 0.0f : __frcp_rn(sum);
+        const int64_t row = (int64_t)pb * a.q_heads + h0 + h;
+        const float by = t.y == 0.0f ? 0.0f : __frcp_rn(t.y);
 #pragma unroll
         for (int x = 0; x < 4; ++x) st_elem<T>(a.y, row * d + e + x, y[x] * by);
         if (e == 0 && a.lse)
-          a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+          a.lse[row] = t.y == 0.0f ? -INFINITY : (t.x + log2f(t.y)) * 0.69314718055994531f;
       } else {
         *reinterpret_cast<float4*>(ws.o + (slot + h) * d + e) = make_float4(y[0], y[1], y[2], y[3]);
-        if (e == 0) ws.ml[slot + h] = make_float2(top, sum);
+        if (e == 0) ws.ml[slot + h] = t;
       }
     }
-    if (p0.z == 0 && to < n_tiles) {
-      // cut off by the end of the block's last run: the blocks behind it hold the rest
-      const int64_t at = run_start((int64_t)(blockIdx.x + 1) * per) + (n_tiles - to) - 1;
-      int n = 1;  // (`at`: the place of its last tile in the row)
-      while (run_start((int64_t)(blockIdx.x + n + 1) * per) <= at) ++n;
-      cut = make_int4(p0.x, p0.y, n + 1, 0);
+    if (from == 0 && to < n_tiles && threadIdx.x == 0) {
+      // cut off by the end of the block's last run: the blocks behind it hold the rest.  The
+      // run of a place x in the row is the last that starts at or before it.
+      const int64_t x = run_start((int64_t)(blockIdx.x + 1) * per) + (n_tiles - to) - 1;
+      const int64_t r = ((x + 1) * runs - 1) / total;
+      cut = make_int4(pb, pg, (int)(r / per) - (int)blockIdx.x + 1, 0);
     }
-    first = last + 1;
   }
   if (threadIdx.x == 0) ws.cut[blockIdx.x] = cut;
 }
