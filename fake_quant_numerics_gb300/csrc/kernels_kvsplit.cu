@@ -38,7 +38,9 @@ namespace {
 
 constexpr int kFormat = QAT_KV_FORMAT;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kPieceTiles = 4;  // what a piece costs beside its tiles, in tiles
+// What a piece costs beside its tiles, in tiles (64 sequences of up to 8192 positions
+// in 4-bit codes: 74 us with 2, 60 with 4, 57 with 8, 58 with 14).
+constexpr int kPieceTiles = 8;
 constexpr int kLeastRun = 2;    // tiles of a run at least
 constexpr float kSlack = 8.0f;  // scores may exceed the running maximum by 2^8 before it moves
 

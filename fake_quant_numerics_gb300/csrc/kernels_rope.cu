@@ -312,27 +312,30 @@ __global__ void __launch_bounds__(kRopeThreads, V == 8 && T::BYTES == 2 ? 3 : 2)
   }
 }
 
-// The same walk with the gradients; each lane keeps its elements' share of dweight,
-// and a block's shares are added over its groups in shared memory, in order.
+// The same walk with the gradients, the first `blocks0` blocks over the queries, the
+// others over the keys; each lane keeps its elements' share of dweight, and a block's
+// shares are added over its groups in shared memory, in order.
 template <typename T, int V, int NP, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, V == 8 && T::BYTES == 2 ? 2 : 1) k_rope_bwd(RopeArgs r, int lanes, int per,
-                                                           float* parts) {
+__global__ void __launch_bounds__(kRopeThreads, V == 8 && T::BYTES == 2 ? 2 : 1)
+    k_rope_bwd(RopeArgs r, int lanes, int per, int blocks0, float* parts) {
   using P = Pairs<T, V, INTER>;
   __shared__ float share[kRopeThreads * 2 * V * NP];
   pdl_trigger();
   const int lane = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes;
   const int groups = kRopeThreads / lanes;
   const Units<T, V, NP, INTER> un(lane, lanes, r.d, r.rotary);
-  for (int which = 0; which < 2; ++which) {
+  const int which = (int)blockIdx.x >= blocks0;
+  const int64_t block = blockIdx.x - (which ? blocks0 : 0);
+  const int64_t blocks = which ? gridDim.x - blocks0 : blocks0;
+  {
     const int heads = r.heads[which];
     const bool sums = r.dw[which] != nullptr;
     const int runs = (heads + per - 1) / per;
-    const int64_t items = r.y[which] || sums ? r.tokens * runs : 0;
+    const int64_t items = r.tokens * runs;
     float wa[NP][V], wb[NP][V], da[NP][V] = {}, db[NP][V] = {};
     load_weight<T, V, NP, INTER>(r.w[which], un, wa, wb);
     // (whole blocks step together: the shuffles need every lane)
-    for (int64_t base = (int64_t)blockIdx.x * groups; base < items;
-         base += (int64_t)gridDim.x * groups) {
+    for (int64_t base = block * groups; base < items; base += blocks * groups) {
       const int64_t item = base + group, token = item < items ? item / runs : 0;
       const int h0 = item < items ? (int)(item - token * runs) * per : 0;
       const int n = item < items ? min(per, heads - h0) : 0;
@@ -408,7 +411,7 @@ __global__ void __launch_bounds__(kRopeThreads, V == 8 && T::BYTES == 2 ? 2 : 1)
         y += y ? g_step : 0;
       }
     }
-    if (!sums) continue;  // (the same for the whole grid)
+    if (!sums) return;
     float* mine = share + (size_t)threadIdx.x * 2 * V * NP;
 #pragma unroll
     for (int p = 0; p < NP; ++p)
@@ -427,32 +430,35 @@ __global__ void __launch_bounds__(kRopeThreads, V == 8 && T::BYTES == 2 ? 2 : 1)
       float total = 0.0f;
       for (int k = 0; k < groups; ++k)
         total += share[((size_t)k * lanes + ln) * NP * 2 * V + i % (NP * 2 * V)];
-      parts[((int64_t)blockIdx.x * 2 + which) * r.d + at] = total;
+      parts[(int64_t)blockIdx.x * r.d + at] = total;
     }
-    __syncthreads();
   }
 }
 
-// dweight from the blocks' shares: 32 columns a block, 32 rows at a time, in order.
+// dweight from the blocks' shares: 32 columns of the queries' (y = 0) or the keys' a
+// block, 32 rows at a time, in order.
 template <typename T>
-__global__ void __launch_bounds__(1024) k_rope_join(const float* parts, int n, int d, void* dwq,
-                                                    void* dwk) {
+__global__ void __launch_bounds__(1024) k_rope_join(const float* parts, int blocks0, int blocks, int d,
+                                                    void* dwq, void* dwk) {
   __shared__ float part[32][33];
-  pdl_wait();
   const int col = blockIdx.x * 32 + threadIdx.x;
+  void* const dw = blockIdx.y ? dwk : dwq;
+  if (!dw) return;
+  const int end = blockIdx.y ? blocks : blocks0;
   float sum = 0.0f;
-  if (col < 2 * d) {
+  pdl_wait();
+  if (col < d) {
 #pragma unroll 4
-    for (int i = threadIdx.y; i < n; i += 32) sum += parts[(int64_t)i * 2 * d + col];
+    for (int i = (blockIdx.y ? blocks0 : 0) + threadIdx.y; i < end; i += 32)
+      sum += parts[(int64_t)i * d + col];
   }
   part[threadIdx.y][threadIdx.x] = sum;
   __syncthreads();
-  if (threadIdx.y || col >= 2 * d) return;
+  if (threadIdx.y || col >= d) return;
   sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < 32; ++i) sum += part[i][threadIdx.x];
-  void* dw = col < d ? dwq : dwk;
-  if (dw) st_elem<T>(dw, col < d ? col : col - d, sum);
+  st_elem<T>(dw, col, sum);
 }
 
 // The widest run that fits every run's start: elements of a vector of at most 16
@@ -505,24 +511,31 @@ qat_status fwd(const RopeArgs& r, cudaStream_t s) {
 template <typename T, int V, int NP>
 qat_status bwd(const RopeArgs& r, float* ws, cudaStream_t s) {
   const int lanes = group_lanes(r.d, V), groups = kRopeThreads / lanes;
-  int64_t most = 0;
-  for (int i = 0; i < 2; ++i) most = r.heads[i] > most ? r.heads[i] : most;
+  const int64_t most = 2 * device_info().sms < kRopeParts ? 2 * device_info().sms : kRopeParts;
+  const int64_t all = r.heads[0] + r.heads[1];
   int per = 1;
-  while (per < 8 && r.tokens * most / (2 * per) >= (int64_t)kRopeParts * groups) per *= 2;
-  const int64_t blocks = (r.tokens * ((most + per - 1) / per) + groups - 1) / groups;
-  const int64_t most_blocks = 2 * device_info().sms < kRopeParts ? 2 * device_info().sms : kRopeParts;
-  const int grid = (int)(blocks < most_blocks ? blocks : most_blocks);
-  const bool sums = r.dw[0] || r.dw[1];
+  while (per < 8 && r.tokens * all / (2 * per) >= most * groups) per *= 2;
+  // Blocks of both in proportion to their heads.
+  int64_t need[2];
+  for (int i = 0; i < 2; ++i)
+    need[i] = (r.tokens * ((r.heads[i] + per - 1) / per) + groups - 1) / groups;
+  if (need[0] + need[1] > most) {
+    const int64_t q = (most * r.heads[0] + all / 2) / all;
+    const int64_t floor0 = r.heads[0] ? 1 : 0, ceil0 = r.heads[1] ? most - 1 : most;
+    need[0] = q < floor0 ? floor0 : q > ceil0 ? ceil0 : q;
+    need[1] = most - need[0];
+  }
+  const int grid = (int)(need[0] + need[1]), blocks0 = (int)need[0];
   if (grid > 0) {
     auto k = r.interleaved ? k_rope_bwd<T, V, NP, true> : k_rope_bwd<T, V, NP, false>;
-    if (launch_kernel(k, dim3(grid), dim3(kRopeThreads), 0, s, false, r, lanes, per, ws) !=
+    if (launch_kernel(k, dim3(grid), dim3(kRopeThreads), 0, s, false, r, lanes, per, blocks0, ws) !=
         cudaSuccess)
       return QAT_ERR_CUDA;
     count_launch(1);
   }
-  if (sums) {
-    if (launch_kernel(k_rope_join<T>, dim3((2 * r.d + 31) / 32), dim3(32, 32), 0, s, grid > 0,
-                      (const float*)ws, grid, r.d, r.dw[0], r.dw[1]) != cudaSuccess)
+  if (r.dw[0] || r.dw[1]) {
+    if (launch_kernel(k_rope_join<T>, dim3((r.d + 31) / 32, 2), dim3(32, 32), 0, s, grid > 0,
+                      (const float*)ws, blocks0, grid, r.d, r.dw[0], r.dw[1]) != cudaSuccess)
       return QAT_ERR_CUDA;
     count_launch(1);
   }

@@ -23,7 +23,7 @@ struct RopeArgs {
   float amplitude, eps, inv_d;
 };
 // Blocks of the backward pass at most, one row of partial weight gradients each:
-// float[kRopeParts][2][d] in the workspace.
+// float[kRopeParts][d] in the workspace.
 constexpr int kRopeParts = 320;
 qat_status launch_rope_fwd(const RopeArgs& a, qat_dtype dt, cudaStream_t s);
 qat_status launch_rope_bwd(const RopeArgs& a, qat_dtype dt, float* ws, cudaStream_t s);

@@ -115,7 +115,7 @@ qat_status qat_head_norm_rope(const void* q, const void* k, qat_dtype dtype, int
 
 size_t qat_head_norm_rope_backward_workspace_bytes(int64_t head_dim) {
   if (head_dim < 1 || head_dim > 512) return 0;
-  return (size_t)kRopeParts * 2 * (size_t)head_dim * 4;
+  return (size_t)kRopeParts * (size_t)head_dim * 4;
 }
 
 qat_status qat_head_norm_rope_backward(
