@@ -409,7 +409,8 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, len
 
     scale defaults to head_dim^-0.5.  A length of 0 gives zeros (lse -inf).  Lengths
     that the table cannot hold and pages outside the cache make the sequence's outputs
-    NaN; what lies behind a sequence's length has no effect."""
+    NaN; what lies behind a sequence's length has no effect.  For serving: the result
+    has no gradient."""
     what = "kv_attention"
     if q.dim() != 3 or q.shape[2] != cache.head_dim or q.shape[1] % cache.heads:
         raise _mismatch(what)

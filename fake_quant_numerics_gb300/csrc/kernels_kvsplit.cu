@@ -81,20 +81,24 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
   }
 #undef QAT_MMA
 }
-// The next 16-bit parts of two numbers, packed; they keep the remainders.
-template <bool HALF>
+// The next 16-bit parts of two numbers, packed; they keep the remainders.  bf16 parts
+// before the LAST are cut off, so that none overflows.
+template <bool HALF, bool LAST>
 __device__ __forceinline__ uint32_t take_pair(float& x, float& y) {
   if constexpr (HALF) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
-    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&r));
-    x -= v.x, y -= v.y;
+    if constexpr (!LAST) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&r));
+      x -= v.x, y -= v.y;
+    }
     return r;
+  } else if constexpr (LAST) {
+    return pack_bf16x2(x, y);
   } else {
-    const uint32_t r = pack_bf16x2(x, y);
-    x -= __uint_as_float(r << 16);
-    y -= __uint_as_float(r & 0xffff0000u);
-    return r;
+    const uint32_t u = __float_as_uint(x), v = __float_as_uint(y) & 0xffff0000u;
+    x -= __uint_as_float(u & 0xffff0000u), y -= __uint_as_float(v);
+    return u >> 16 | v;
   }
 }
 // an 8 x 8 matrix of 16-bit elements, transposed over the warp
@@ -370,7 +374,8 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
   // Equal runs for as many warps as there is work for, on as many blocks as possible.
   const int64_t runs = max((int64_t)1, min((int64_t)gridDim.x * WARPS, total / kLeastRun));
   const int per = (int)((runs + gridDim.x - 1) / gridDim.x);  // of a block
-  auto run_start = [&](int64_t r) { return total * min(r, runs) / runs; };
+  const int64_t run_least = total / runs, run_more = total - run_least * runs;  // (one more tile)
+  auto run_start = [&](int64_t r) { return r < runs ? run_least * r + min(r, run_more) : total; };
   const int64_t run = (int64_t)blockIdx.x * per + warp;
   const int64_t first = run_start(run);
   if (lane == 0) s_first[warp] = first;
@@ -538,14 +543,14 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = v[j][S::key_place(2 * k + i / 2, i % 2)];
             if constexpr (!S::kF32) {
-              qr[ht][ks][0] = take_pair<HALF>(x[0], x[1]);
-              qr[ht][ks][1] = take_pair<HALF>(x[2], x[3]);
+              qr[ht][ks][0] = take_pair<HALF, true>(x[0], x[1]);
+              qr[ht][ks][1] = take_pair<HALF, true>(x[2], x[3]);
             } else {
 #pragma unroll
               for (int p = 0; p < 3; ++p) {
                 uint2 y;
-                y.x = take_pair<HALF>(x[0], x[1]);
-                y.y = take_pair<HALF>(x[2], x[3]);
+                y.x = p < 2 ? take_pair<HALF, false>(x[0], x[1]) : take_pair<HALF, true>(x[0], x[1]);
+                y.y = p < 2 ? take_pair<HALF, false>(x[2], x[3]) : take_pair<HALF, true>(x[2], x[3]);
                 qfrag[(p * S::KS + ks) * 32 + lane] = y;
               }
             }
@@ -723,7 +728,8 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
           for (int p = 0; p < S::PP; ++p)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              wb[ht][p][r] = transpose8(take_pair<HALF>(w[2 * r], w[2 * r + 1]));
+              wb[ht][p][r] = transpose8(p + 1 < S::PP ? take_pair<HALF, false>(w[2 * r], w[2 * r + 1])
+                                                      : take_pair<HALF, true>(w[2 * r], w[2 * r + 1]));
         }
       };
       // Weighted values: rows are head elements, k the positions.
@@ -914,10 +920,11 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
       }
     }
     if (from == 0 && to < n_tiles && threadIdx.x == 0) {
-      // cut off by the end of the block's last run: the blocks behind it hold the rest.  The
-      // run of a place x in the row is the last that starts at or before it.
+      // cut off by the end of the block's last run: the blocks behind it hold the rest, up
+      // to the run of its last tile's place x
       const int64_t x = run_start((int64_t)(blockIdx.x + 1) * per) + (n_tiles - to) - 1;
-      const int64_t r = ((x + 1) * runs - 1) / total;
+      const int64_t longer = run_more * (run_least + 1);
+      const int64_t r = x < longer ? x / (run_least + 1) : run_more + (x - longer) / run_least;
       cut = make_int4(pb, pg, (int)(r / per) - (int)blockIdx.x + 1, 0);
     }
   }
