@@ -542,32 +542,48 @@ qat_status bwd(const RopeArgs& r, float* ws, cudaStream_t s) {
   return QAT_OK;
 }
 
-template <typename T>
-qat_status fwd_any(const RopeArgs& r, cudaStream_t s) {
-  switch (run_width<T>(r)) {
-    case 8: return fwd<T, 8, 1>(r, s);
-    case 4: return fwd<T, 4, 2>(r, s);
-    case 2: return fwd<T, 2, 4>(r, s);
-    default: return fwd<T, 1, 8>(r, s);
+// Units a lane of a head holds where 32 lanes are too few: kernels for as few as there
+// are (the others' steps would be empty).
+template <typename T, typename F>
+qat_status by_width(const RopeArgs& r, F f) {
+  const int v = run_width<T>(r), units = (r.d + 2 * v - 1) / (2 * v);
+  switch (v) {
+    case 8: return f.template operator()<8, 1>();
+    case 4: return units <= 32 ? f.template operator()<4, 1>() : f.template operator()<4, 2>();
+    case 2: return units <= 32 ? f.template operator()<2, 1>() : f.template operator()<2, 4>();
+    default:
+      return units <= 32   ? f.template operator()<1, 1>()
+             : units <= 64 ? f.template operator()<1, 2>()
+                           : f.template operator()<1, 8>();
   }
 }
 template <typename T>
-qat_status bwd_any(const RopeArgs& r, float* ws, cudaStream_t s) {
-  switch (run_width<T>(r)) {
-    case 8: return bwd<T, 8, 1>(r, ws, s);
-    case 4: return bwd<T, 4, 2>(r, ws, s);
-    case 2: return bwd<T, 2, 4>(r, ws, s);
-    default: return bwd<T, 1, 8>(r, ws, s);
+struct Fwd {
+  const RopeArgs& r;
+  cudaStream_t s;
+  template <int V, int NP>
+  qat_status operator()() const {
+    return fwd<T, V, NP>(r, s);
   }
-}
+};
+template <typename T>
+struct Bwd {
+  const RopeArgs& r;
+  float* ws;
+  cudaStream_t s;
+  template <int V, int NP>
+  qat_status operator()() const {
+    return bwd<T, V, NP>(r, ws, s);
+  }
+};
 
 }  // namespace
 
 qat_status launch_rope_fwd(const RopeArgs& a, qat_dtype dt, cudaStream_t s) {
-  return dt == QAT_F32 ? fwd_any<F32>(a, s) : fwd_any<BF16>(a, s);
+  return dt == QAT_F32 ? by_width<F32>(a, Fwd<F32>{a, s}) : by_width<BF16>(a, Fwd<BF16>{a, s});
 }
 qat_status launch_rope_bwd(const RopeArgs& a, qat_dtype dt, float* ws, cudaStream_t s) {
-  return dt == QAT_F32 ? bwd_any<F32>(a, ws, s) : bwd_any<BF16>(a, ws, s);
+  return dt == QAT_F32 ? by_width<F32>(a, Bwd<F32>{a, ws, s}) : by_width<BF16>(a, Bwd<BF16>{a, ws, s});
 }
 
 }  // namespace qat

@@ -37,6 +37,10 @@ ROPE = [
     (6, 3, 0, 64, 64, "half", False, 1.5, 9, F32),            # no keys
     (2, 1, 1, 1, 0, "half", True, 1.0, 0, F32),
     (70, 7, 7, 80, 40, "interleaved", True, 1.25, 4096, F32),
+    (5, 3, 2, 127, 62, "half", True, 1.0, 77, BF16),          # two single elements a lane
+    (5, 3, 2, 512, 24, "interleaved", True, 1.0, 77, BF16),   # two runs of four a lane
+    (5, 3, 2, 500, 20, "half", True, 1.25, 77, F32),          # four runs of two a lane
+    (2000, 9, 3, 64, 64, "half", True, 1.0, 50, BF16),        # more heads than the blocks hold at once
 ]
 
 
@@ -533,3 +537,18 @@ def test_captured_backward(qat):
     torch.cuda.synchronize()
     dq, _, dw, _ = qat.head_norm_rope_backward(c, None, q.detach(), None, positions, turns, w.detach())
     assert torch.equal(got[0], dq) and torch.equal(got[1], dw)
+
+
+def test_example_serves_from_every_cache(qat):
+    """The example's layer runs, and its outputs are numbers of the layer's shape."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "qat_attention_layer.py")
+    spec = importlib.util.spec_from_file_location("qat_attention_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    want, off = example.main(steps=20, dim=256)
+    assert want.shape == (20, 3, 256) and torch.isfinite(want).all()
+    assert set(off) == {"int8", "e4m3", "int4"} and all(math.isfinite(v) for v in off.values())
