@@ -42,7 +42,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // in 4-bit codes: 74 us with 2, 60 with 4, 57 with 8, 58 with 14).
 constexpr int kPieceTiles = 8;
 constexpr int kLeastRun = 2;    // tiles of a run at least
-constexpr float kSlack = 8.0f;  // scores may exceed the running maximum by 2^8 before it moves
+constexpr float kSlack = 4.0f;  // scores may exceed the running maximum by 2^4 before it moves
 
 // ---------------------------------------------------------------------------
 // instructions
@@ -568,7 +568,8 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
 
       // m: the maximum that weights refer to; limit: where it moves; base: m, but 0 before
       // the first score.  Weighted values are summed times `unit`, a power of two that
-      // keeps p vs unit within 2^15 (p <= 2^8) for scales up to v_limit.
+      // keeps p vs unit within 2^15 (p <= 2^4) for scales up to v_limit, and the largest
+      // scale above 2^8 (what p vs loses below fp16's last bit is 2^-33 of that scale).
       float m[HT][2], limit[HT][2], base[HT][2], l[HT][2], zsum[HT][2], o[HT][S::MT][4];
       float unit = 1.0f, v_limit = -1.0f;
 #pragma unroll
@@ -684,11 +685,11 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
             float top = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
-            if (top > v_limit) {  // to between 16 and 32
+            if (top > v_limit) {  // to between 2^8 and 2^9
               const int e = top < 0x1p-100f ? -100 : exponent_of(top);
-              const int by = 4 - e - exponent_of(unit);
+              const int by = 8 - e - exponent_of(unit);
               if (v_limit >= 0.0f) shrink = power_of_two(max(by, -126));
-              unit = power_of_two(4 - e);
+              unit = power_of_two(8 - e);
               v_limit = power_of_two(min(e + 3, 127));
             }
           }

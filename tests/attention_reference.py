@@ -209,6 +209,12 @@ def attention(q, cache, table, lengths, scale, dtype):
             # weights, and their products with values, below the normal range of binary32 may
             # be lost: each less than 2^-126 times 1 + |v| (the sum of weights is at least 1)
             err = err + n * 2.0 ** -126 * (1 + np.abs(v).max(0))
+            if cache.format != "bf16":
+                # fp16's last bit (half of 2^-24) where a weight times its scale is a number of up
+                # to 2^8 times the largest scale or more: 2^-33 of that scale, a code each
+                vs = np.abs(f64(cache.v_scale)[pages, h // group, t % cache.page_size])
+                code = np.abs(v) / np.where(vs > 0, vs, 1.0)[:, None]
+                err = err + 2.0 ** -33 * vs.max() * (code + extra_codes(cache, pages, h // group, t)[:, None]).sum(0)
             ey[b, h] = err + step(dtype) * (np.abs(y[b, h]) + err)
             elv[b, h] = (w * rel).sum() + es.max() + (8 * math.sqrt(n) + 16) * U + 4 * U * abs(lse[b, h])
     return y, ey, lse, elv
@@ -227,3 +233,9 @@ def extra_values(cache, pages, head, t):
         return np.zeros(len(t))
     return np.abs(f64(cache.v_zero_point)[pages, head, t % cache.page_size]
                   * f64(cache.v_scale)[pages, head, t % cache.page_size])
+
+
+def extra_codes(cache, pages, head, t):
+    if cache.v_zero_point is None:
+        return np.zeros(len(t))
+    return np.abs(f64(cache.v_zero_point)[pages, head, t % cache.page_size])

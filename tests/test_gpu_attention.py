@@ -367,6 +367,79 @@ def test_kv_attention_lengths(qat, lengths):
     check_attention(qat, 11, lengths, 4, 2, 64, 64, "int8", "symmetric", BF16)
 
 
+@pytest.mark.parametrize("heads,kv_heads,d,form,scheme", [(16, 1, 128, "int4", "affine"), (12, 1, 96, "e4m3", "symmetric"),
+                                                          (11, 1, 128, "bf16", "symmetric"), (20, 2, 40, "int8", "affine")])
+def test_kv_attention_wide_groups(qat, heads, kv_heads, d, form, scheme):
+    check_attention(qat, 21, [90, 0, 333, 16], heads, kv_heads, d, 32, form, scheme, BF16)
+
+
+@pytest.mark.parametrize("form,scheme", FORMS[:6])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("order", ["up", "down", "mixed"])
+def test_kv_attention_of_values_far_apart(qat, form, scheme, dtype, order):
+    """Values whose scales differ by 2^60, growing, falling and mixed; tiny ones, and rows of
+    zeros."""
+    n, d = 400, 64
+    cache = qat.kv_cache(30, 2, 16, d, form, scheme)
+    table = torch.randperm(30, generator=torch.Generator().manual_seed(0)).int()[:25].view(1, 25)
+    e = torch.linspace(-30, 30, n)
+    e = {"up": e, "down": e.flip(0), "mixed": e[torch.randperm(n, generator=torch.Generator().manual_seed(1))]}[order]
+    k, v = randn(1, n, 2, d), randn(2, n, 2, d) * (2.0 ** e).cuda()[:, None, None]
+    v[50:60] = 0
+    v[70] = 1e-40
+    v[:, 1] *= 2.0 ** -90
+    t = torch.arange(n)
+    slots = table[0].long()[t // 16] * 16 + t % 16
+    qat.kv_write(cache, k, v, slots.cuda())
+    q = randn(3, 1, 4, d, dtype=dtype)
+    r = qat.kv_attention(q, cache, table.cuda(), torch.tensor([n], dtype=torch.int32).cuda())
+    y, ey, _, _ = ref.attention(f64(q), cache, table.numpy(), [n], d ** -0.5, dtype)
+    within(r.y, y, ey, "y")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("form", ["int8", "bf16"])
+def test_kv_attention_of_large_and_small_queries(qat, form, dtype):
+    """Query heads of very different sizes share a read of the cache."""
+    q = randn(4, 2, 4, 64, dtype=dtype)
+    q = q * torch.tensor([1e-30, 1.0, 1e-4, 30.0]).cuda().to(dtype)[None, :, None]
+    q[1, 0] = 0
+    check_attention(qat, 4, [100, 33], 4, 1, 64, 16, form, "symmetric", dtype, None, q)
+
+
+def test_kv_attention_on_two_streams_at_once(qat):
+    """Calls that overlap on the GPU have workspaces of their own."""
+    lengths = [3000, 1, 2500]
+    cache, table, q, r = check_attention(qat, 12, lengths, 8, 2, 128, 16, "int8", "symmetric", BF16)
+    n, tab = torch.tensor(lengths, dtype=torch.int32).cuda(), table.cuda()
+    q2 = (q.float() * -0.5).to(BF16)
+    r2 = qat.kv_attention(q2, cache, tab, n).y
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    out = []
+    for _ in range(20):
+        for s, x in zip(streams, (q, q2)):
+            with torch.cuda.stream(s):
+                out.append(qat.kv_attention(x, cache, tab, n).y)
+    torch.cuda.synchronize()
+    for i, y in enumerate(out):
+        assert torch.equal(y, r2 if i % 2 else r.y)
+
+
+def test_kv_write_of_a_slot_twice_spares_the_others(qat):
+    cache = qat.kv_cache(4, 2, 16, 64, "int8")
+    k, v = randn(0, 40, 2, 64), randn(1, 40, 2, 64)
+    slots = torch.arange(40).cuda()
+    qat.kv_write(cache, k, v, slots)
+    want = qat.kv_read(cache, slots, F32)
+    slots[7] = 8
+    qat.kv_write(cache, k, v, slots)
+    got = qat.kv_read(cache, torch.arange(40).cuda(), F32)
+    keep = [i for i in range(40) if i not in (7, 8)]
+    assert torch.equal(got.k[keep], want.k[keep]) and torch.equal(got.v[keep], want.v[keep])
+    assert torch.equal(got.k[7], want.k[7])  # (as the first call left it)
+
+
 def test_kv_attention_sharp_and_flat_scores(qat):
     """Scores far apart (one weight takes all), equal scores, a negative scale, scale 0."""
     lengths = [300, 40]
