@@ -20,7 +20,7 @@ from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._lib import (AFFINE, CACHE_BF16, CACHE_E4M3, CACHE_E5M2, CACHE_INT4, CACHE_INT8, ROPE_HALF, ROPE_INTERLEAVED)
-from .api import _SCHEME, _dt, _nbytes, _p, _s
+from .api import _DT, _SCHEME, _dt, _nbytes, _p, _s
 from .layers import _call, _mismatch, _of_type, _on_device, _ptr, _vector
 
 _LAYOUT = {"half": ROPE_HALF, "interleaved": ROPE_INTERLEAVED}
@@ -104,7 +104,7 @@ def _heads(t: torch.Tensor) -> torch.Tensor:
     return t if t.stride(2) == 1 or t.shape[2] <= 1 else t.contiguous()
 
 
-_I64 = torch.int64
+_I64, _I32 = torch.int64, torch.int32
 
 
 def _rope_inputs(what, q, k, positions, turns, q_weight, k_weight, norm, layout):
@@ -151,20 +151,21 @@ def head_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.
     frequencies (:func:`rope_turns`; their number is half the rotated dimensions).
     norm=False rotates only.  amplitude scales the rotated part.  q and k may be
     views of one projection's output: only the last dimension has to be dense."""
-    what = "head_norm_rope"
     shape, k_shape = q.shape, None if k is None else k.shape
-    q, k, positions, turns, wq, wk = _rope_inputs(what, q, k, positions, turns, q_weight, k_weight, norm, layout)
-    tokens, hq, d = q.shape
-    dev, hk, ks, kp, yk, ykp = q.device, 0, (0, 0), None, None, None
-    yq = torch.empty(shape, dtype=q.dtype, device=dev)
+    q, k, positions, turns, wq, wk = _rope_inputs("head_norm_rope", q, k, positions, turns, q_weight, k_weight, norm,
+                                                  layout)
+    dev, dtype, qs = q.device, q.dtype, q.stride()
+    qp, dt = _ptr(q), _dt(q)
+    yq = torch.empty(shape, dtype=dtype, device=dev)
+    yk = kp = ykp = None
+    hk = ks0 = ks1 = 0
     if k is not None:
-        hk, ks, kp = k.shape[1], k.stride(), _ptr(k)
-        yk = torch.empty(k_shape, dtype=q.dtype, device=dev)
+        hk, (ks0, ks1, _), kp = k.shape[1], k.stride(), k.data_ptr()
+        yk = torch.empty(k_shape, dtype=dtype, device=dev)
         ykp = yk.data_ptr()
-    qs = q.stride()
-    _call("qat_head_norm_rope", dev, _lib.lib().qat_head_norm_rope, _ptr(q), kp, _dt(q), tokens, hq, hk, d,
-          qs[0], qs[1], ks[0], ks[1], positions.data_ptr(), turns.data_ptr(), 2 * turns.numel(), _LAYOUT[layout],
-          amplitude, 1 if norm else 0, None if wq is None else wq.data_ptr(),
+    _call("qat_head_norm_rope", dev, _lib.lib().qat_head_norm_rope, qp, kp, dt, q.shape[0], q.shape[1], hk,
+          shape[-1], qs[0], qs[1], ks0, ks1, positions.data_ptr(), turns.data_ptr(), 2 * turns.numel(),
+          _LAYOUT[layout], amplitude, 1 if norm else 0, None if wq is None else wq.data_ptr(),
           None if wk is None else wk.data_ptr(), eps, yq.data_ptr(), ykp)
     return HeadNormRope(yq, yk)
 
@@ -180,33 +181,44 @@ def head_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor]
     shape, k_shape = q.shape, None if k is None else k.shape
     if dq_out.shape != shape or (k is None) != (dk_out is None) or (k is not None and dk_out.shape != k_shape):
         raise _mismatch(what)
-    _of_type(q, dq_out, dk_out)
+    dtype, dev = q.dtype, q.device
+    if dq_out.dtype is not dtype or dq_out.device != dev:
+        _of_type(q, dq_out)
+    if dk_out is not None and (dk_out.dtype is not dtype or dk_out.device != dev):
+        _of_type(q, dk_out)
     q, k, positions, turns, wq, wk = _rope_inputs(what, q, k, positions, turns, q_weight, k_weight, norm, layout)
     dq_out = dq_out.contiguous()
-    dk_out = None if dk_out is None else dk_out.contiguous()
-    tokens, hq, d = q.shape
-    dev, dt, hk, ks, kp, gkp = q.device, q.dtype, 0, (0, 0), None, None
-    dq = torch.empty(shape, dtype=dt, device=dev) if want_dx else None
-    dk = dwq = dwk = ws = None
+    qs, d, gp, dt = q.stride(), shape[-1], _ptr(dq_out), _dt(q)
+    dq = dk = dwq = dwk = ws = kp = gkp = dqp = dkp = wqp = wkp = dwqp = dwkp = wsp = None
+    hk = ks0 = ks1 = n = 0
+    if want_dx:
+        dq = torch.empty(shape, dtype=dtype, device=dev)
+        dqp = dq.data_ptr()
     if k is not None:
-        hk, ks, kp, gkp = k.shape[1], k.stride(), _ptr(k), dk_out.data_ptr()
-        dk = torch.empty(k_shape, dtype=dt, device=dev) if want_dx else None
-    lib, n, qs = _lib.lib(), 0, q.stride()
-    if want_dw and wq is not None:
-        dwq = torch.empty(d, dtype=dt, device=dev)
-    if want_dw and wk is not None:
-        dwk = torch.empty(d, dtype=dt, device=dev)
+        dk_out = dk_out.contiguous()
+        hk, (ks0, ks1, _), kp, gkp = k.shape[1], k.stride(), k.data_ptr(), dk_out.data_ptr()
+        if want_dx:
+            dk = torch.empty(k_shape, dtype=dtype, device=dev)
+            dkp = dk.data_ptr()
+    if wq is not None:
+        wqp = wq.data_ptr()
+        if want_dw:
+            dwq = torch.empty(d, dtype=dtype, device=dev)
+            dwqp = dwq.data_ptr()
+    if wk is not None:
+        wkp = wk.data_ptr()
+        if want_dw:
+            dwk = torch.empty(d, dtype=dtype, device=dev)
+            dwkp = dwk.data_ptr()
+    lib = _lib.lib()
     if dwq is not None or dwk is not None:
         n = lib.qat_head_norm_rope_backward_workspace_bytes(d)
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
-
-    def at(t):
-        return None if t is None else t.data_ptr()
-
-    _call("qat_head_norm_rope_backward", dev, lib.qat_head_norm_rope_backward, _ptr(dq_out), gkp, _ptr(q), kp,
-          _dt(q), tokens, hq, hk, d, qs[0], qs[1], ks[0], ks[1], positions.data_ptr(), turns.data_ptr(),
-          2 * turns.numel(), _LAYOUT[layout], amplitude, 1 if norm else 0, at(wq), at(wk), eps, at(dq), at(dk),
-          at(dwq), at(dwk), at(ws), n)
+        wsp = ws.data_ptr()
+    _call("qat_head_norm_rope_backward", dev, lib.qat_head_norm_rope_backward, gp, gkp, q.data_ptr(), kp, dt,
+          q.shape[0], q.shape[1], hk, d, qs[0], qs[1], ks0, ks1, positions.data_ptr(), turns.data_ptr(),
+          2 * turns.numel(), _LAYOUT[layout], amplitude, 1 if norm else 0, wqp, wkp, eps, dqp, dkp, dwqp, dwkp,
+          wsp, n)
     return dq, dk, dwq, dwk
 
 
@@ -341,7 +353,7 @@ def qat_kv_read(cache: KVCache, slots, tokens, k, v, stream=None):
 
 
 def _slots(slots: torch.Tensor) -> torch.Tensor:
-    if slots.dtype != torch.int64:
+    if slots.dtype is not _I64:
         raise TypeError("slots are int64")
     return slots.contiguous()
 
@@ -371,13 +383,17 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
 def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> KeysValues:
     """The cached keys and values at `slots` (int64, any shape) as [..., heads, head_dim]
     in float32 or bfloat16; zeros for a slot outside the cache."""
-    _on_device(cache.device, slots)
-    shape = slots.shape + (cache.heads, cache.head_dim)
-    slots = _slots(slots)
-    k = torch.empty(shape, dtype=dtype, device=cache.device)
-    v = torch.empty(shape, dtype=dtype, device=cache.device)
-    _call("qat_kv_read", cache.device, _lib.lib().qat_kv_read, cache.address, _ptr(slots), slots.numel(),
-          k.data_ptr(), v.data_ptr(), _dt(k))
+    dev = cache.device
+    if slots.device != dev:
+        _on_device(dev, slots)
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    shape, slots = (*slots.shape, cache.heads, cache.head_dim), _slots(slots)
+    sp = _ptr(slots)
+    k = torch.empty(shape, dtype=dtype, device=dev)
+    v = torch.empty(shape, dtype=dtype, device=dev)
+    _call("qat_kv_read", dev, _lib.lib().qat_kv_read, cache.address, sp, slots.numel(), k.data_ptr(), v.data_ptr(),
+          _DT[dtype])
     return KeysValues(k, v)
 
 
@@ -411,32 +427,36 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, len
     that the table cannot hold and pages outside the cache make the sequence's outputs
     NaN; what lies behind a sequence's length has no effect.  For serving: the result
     has no gradient."""
-    what = "kv_attention"
-    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.shape[1] % cache.heads:
-        raise _mismatch(what)
-    batch, heads, d = q.shape
-    if block_table.dim() != 2 or block_table.shape[0] != batch or lengths.shape != (batch,):
-        raise _mismatch(what)
-    if block_table.dtype != torch.int32 or lengths.dtype != torch.int32:
+    shape, table_shape, dev = q.shape, block_table.shape, q.device
+    if len(shape) != 3 or shape[2] != cache.head_dim or shape[1] % cache.heads:
+        raise _mismatch("kv_attention")
+    batch, heads, d = shape
+    if len(table_shape) != 2 or table_shape[0] != batch or lengths.dim() != 1 or lengths.shape[0] != batch:
+        raise _mismatch("kv_attention")
+    if block_table.dtype is not _I32 or lengths.dtype is not _I32:
         raise TypeError("block_table and lengths are int32")
-    dev = q.device
     if cache.device != dev or block_table.device != dev or lengths.device != dev:
         _on_device(dev, cache, block_table, lengths)
-    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+    ts = block_table.stride()
+    if ts[1] != 1 and table_shape[1] > 1:
         block_table = block_table.contiguous()
+        ts = block_table.stride()
     lengths = lengths.contiguous()
-    q = _heads(q)
-    lib, qs, qp = _lib.lib(), q.stride(), _ptr(q)
-    y = torch.empty((batch, heads, d), dtype=q.dtype, device=dev)
+    qs = q.stride()
+    if qs[2] != 1:
+        q = q.contiguous()
+        qs = q.stride()
+    qp, dt = _ptr(q), _dt(q)
+    y = torch.empty(shape, dtype=q.dtype, device=dev)
     lse = torch.empty((batch, heads), dtype=torch.float32, device=dev) if want_lse else None
     if batch == 0 or heads == 0:
         return KvAttention(y, lse)
+    lib = _lib.lib()
     n = cache.workspace.get(heads)
     if n is None:
         n = cache.workspace[heads] = lib.qat_kv_attention_workspace_bytes(cache.address, heads)
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    _call("qat_kv_attention", dev, lib.qat_kv_attention, qp, _dt(q), batch, heads, qs[0], qs[1], cache.address,
-          block_table.data_ptr(), block_table.shape[1], block_table.stride(0), lengths.data_ptr(),
-          d ** -0.5 if scale is None else scale, y.data_ptr(), lse.data_ptr() if want_lse else None, ws.data_ptr(),
-          n)
+    _call("qat_kv_attention", dev, lib.qat_kv_attention, qp, dt, batch, heads, qs[0], qs[1], cache.address,
+          block_table.data_ptr(), table_shape[1], ts[0], lengths.data_ptr(), d ** -0.5 if scale is None else scale,
+          y.data_ptr(), lse.data_ptr() if want_lse else None, ws.data_ptr(), n)
     return KvAttention(y, lse)
