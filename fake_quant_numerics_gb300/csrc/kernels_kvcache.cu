@@ -41,10 +41,22 @@ template <typename A>
 __device__ __forceinline__ A one(A const (&two)[2], int which) {
   return which ? two[1] : two[0];
 }
-// The row of a slot and head: [page][head][offset].
-__device__ __forceinline__ int64_t kv_row(const KvPlace& p, int64_t slot, int head) {
-  const int page = (int)slot / p.page_size;  // slots fit 31 bits
-  return ((int64_t)page * p.heads + head) * p.page_size + ((int)slot - page * p.page_size);
+// Where a token's rows lie, [page][head][offset]: head 0's, and the slot's validity.
+struct KvToken {
+  int64_t row;
+  bool on;
+};
+__device__ __forceinline__ KvToken kv_token(const KvPlace& p, int64_t slot) {
+  const bool on = slot >= 0 && slot < p.slots;
+  const uint32_t at = on ? (uint32_t)slot : 0u, page = at / (uint32_t)p.page_size;  // (31 bits)
+  return {(int64_t)page * p.heads * p.page_size + (at - page * p.page_size), on};
+}
+// x / n for a constant n: as the division rounds it, by its reciprocal and two remainders
+// where nothing of them is lost.
+template <int N>
+__device__ __forceinline__ float over(float x) {
+  constexpr float n = (float)N, r = 1.0f / n;
+  return x >= 0x1p-80f && x <= 0x1p100f ? quotient_rn(x, r, -n) : __fdiv_rn(x, n);
 }
 
 // A lane's 16 elements of a row, as they lie in memory; elements behind the row's end
@@ -128,8 +140,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_write(KvRows x, KvPlace p, in
                                                          const int64_t* slots, int lanes) {
   const int lane = threadIdx.x & (lanes - 1);
   const int64_t token = (int64_t)blockIdx.x * (kKvThreads / lanes) + threadIdx.x / lanes;
-  int64_t slot = token < tokens ? __ldg(slots + token) : -1;
-  if (slot >= p.slots) slot = -1;
+  const KvToken at = kv_token(p, token < tokens ? __ldg(slots + token) : -1);
   const int left = p.d - 16 * lane;  // elements from this lane's on
   Unit<T> unit[U];
 #pragma unroll
@@ -138,14 +149,14 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_write(KvRows x, KvPlace p, in
     const int which = row >= p.heads, head = row - (which ? p.heads : 0);
     unit[i].template load<HOW>(
         which ? x.v : x.k, token * one(x.token_stride, which) + head * one(x.head_stride, which) + 16 * lane,
-        slot >= 0 && row < 2 * p.heads ? left : 0);
+        at.on && row < 2 * p.heads ? left : 0);
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const int row = blockIdx.y * U + i;
     const int which = row >= p.heads, head = row - (which ? p.heads : 0);
-    const bool on = slot >= 0 && row < 2 * p.heads;
-    const int64_t to = on ? kv_row(p, slot, head) : 0;
+    const bool on = at.on && row < 2 * p.heads;
+    const int64_t to = at.row + (int64_t)head * p.page_size;
     const Unit<T>& u = unit[i];
     uint32_t w[8];
     if constexpr (F == QAT_CACHE_BF16) {
@@ -169,17 +180,19 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_write(KvRows x, KvPlace p, in
       // (a NaN or an infinity in the row is one here, and the scale not finite)
       float scale, zp = 0.0f;
       if constexpr (kv_is_int(F))
-        scale = __fdiv_rn(AFFINE ? __fsub_rn(hi, lo) : hi, (float)(AFFINE ? qmax - qmin : qmax));
+        scale = over<AFFINE ? qmax - qmin : qmax>(AFFINE ? __fsub_rn(hi, lo) : hi);
       else
-        scale = __fdiv_rn(hi, F == QAT_CACHE_E4M3 ? 448.0f : 57344.0f);
+        scale = over<F == QAT_CACHE_E4M3 ? 448 : 57344>(hi);
       if (!(scale < __uint_as_float(0x7f800000u))) scale = __uint_as_float(0x7fc00000u);
       const bool usable = scale > 0.0f;
-      if (AFFINE && usable)
-        zp = fminf(fmaxf(rintf(__fsub_rn((float)qmin, __fdiv_rn(lo, scale))), (float)qmin),
-                   (float)qmax);
+      const bool fast = quot_scale_ok(scale);
+      const float rcp = fast ? __frcp_rn(scale) : 0.0f;
+      if (AFFINE && usable) {
+        const float z = fast ? quotient_rn(lo, rcp, -scale) : __fdiv_rn(lo, scale);
+        zp = fminf(fmaxf(rintf(__fsub_rn((float)qmin, z)), (float)qmin), (float)qmax);
+      }
       float q[16];
-      if (quot_scale_ok(scale)) {
-        const float rcp = __frcp_rn(scale);
+      if (fast) {
 #pragma unroll
         for (int e = 0; e < 16; e += 2)
           quotient_rn2(u.get(e), u.get(e + 1), rcp, -scale, q[e], q[e + 1]);
@@ -247,8 +260,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_read(KvPlace p, int64_t token
   const int64_t token = (int64_t)blockIdx.x * (kKvThreads / lanes) + threadIdx.x / lanes;
   const int left = p.d - 16 * lane;
   if (token >= tokens || left <= 0) return;
-  const int64_t slot = __ldg(slots + token);
-  const bool there = slot >= 0 && slot < p.slots;
+  const KvToken at = kv_token(p, __ldg(slots + token));
   constexpr int UB = kv_unit_bytes(F);
   uint32_t w[U][UB / 4];
   float scale[U];
@@ -260,8 +272,8 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_read(KvPlace p, int64_t token
 #pragma unroll
     for (int j = 0; j < UB / 4; ++j) w[i][j] = 0u;
     scale[i] = 0.0f, zp[i] = 0;
-    if (!there || row >= 2 * p.heads) continue;
-    const int64_t from = kv_row(p, slot, head);
+    if (!at.on || row >= 2 * p.heads) continue;
+    const int64_t from = at.row + (int64_t)head * p.page_size;
     const char* src = static_cast<const char*>(one(p.codes, which)) + from * p.row_bytes + lane * UB;
     if constexpr (UB == 8) {
       const uint2 a = *reinterpret_cast<const uint2*>(src);

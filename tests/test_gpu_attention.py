@@ -262,6 +262,25 @@ def test_kv_many_tokens_are_each_as_alone(qat, form, scheme, dtype):
             assert torch.equal(x[a:a + 999].view(torch.uint8), y.view(torch.uint8))
 
 
+@pytest.mark.parametrize("form,scheme", FORMS[:6])
+def test_kv_scales_of_every_size(qat, form, scheme):
+    """Scales, zero points and codes are the rounded quotients bit for bit from subnormal
+    rows to those near overflow (the division by a constant takes its reciprocal and two
+    remainders only where nothing of them is lost)."""
+    n, d = 1 << 16, 8
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(n, 1, d, generator=g) * 2.0 ** (torch.rand(n, 1, 1, generator=g) * 266 - 142)
+    x[:4096] = x[:4096].to(BF16).float()
+    cache = qat.kv_cache(n // 64, 1, 64, d, form, scheme)
+    qat.kv_write(cache, x.cuda(), x.flip(0).cuda(), torch.arange(n).cuda())
+    for name, y in (("k", x), ("v", x.flip(0))):
+        q, scale, zp = ref.quantized(f64(y)[:, 0], form, scheme)
+        np.testing.assert_array_equal(f64(getattr(cache, name + "_scale")).reshape(-1), scale)
+        np.testing.assert_array_equal(ref.codes_of(cache, name).reshape(n, d), q)
+        if scheme == "affine":
+            np.testing.assert_array_equal(f64(getattr(cache, name + "_zero_point")).reshape(-1), zp)
+
+
 @pytest.mark.parametrize("form,scheme", FORMS[:4])
 def test_kv_rows_are_the_fake_quant_view(qat, form, scheme):
     """A cached row reads back as the per-row fake-quant view of the same row."""
