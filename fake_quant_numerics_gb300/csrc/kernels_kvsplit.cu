@@ -30,7 +30,7 @@
 // Twelve warps an SM (168 registers, 17 KB of ring each, two tiles and more in flight)
 // walk through tiles at 0.7 to 1 us each.  Measured (both launches, in a graph): 64
 // sequences of up to 8192 positions, 32 heads over 8 of 128 in affine 4-bit codes, 58 us
-// (3.3 TB/s; about 330 instructions a tile, 52% of the issue slots); two of 131072 in
+// (3.3 TB/s; about 380 instructions a tile, 52% of the issue slots); two of 131072 in
 // E4M3 98 us (5.6 TB/s, 83% of the copy bandwidth); 32 of up to 2048, 16 heads of 64 in
 // bf16, 22 us; one of 700 in int8 10.6 us, of which 8 are the latencies of lengths, table,
 // codes and the two joins.

@@ -426,6 +426,46 @@ def test_kv_attention_of_large_and_small_queries(qat, form, dtype):
     check_attention(qat, 4, [100, 33], 4, 1, 64, 16, form, "symmetric", dtype, None, q)
 
 
+def test_kv_attention_of_many_sequences(qat):
+    """More sequences than a block has threads, some empty: each as in a small batch."""
+    g = torch.Generator().manual_seed(5)
+    lengths = torch.randint(0, 70, (1100,), generator=g).tolist()
+    lengths[500], lengths[1099] = 3000, 0
+    cache, table = filled(qat, 31, lengths, 2, 64, 16, "int8", "symmetric")
+    q, n = randn(7, 1100, 4, 64, dtype=BF16), torch.tensor(lengths, dtype=torch.int32)
+    r = qat.kv_attention(q, cache, table.cuda(), n.cuda(), want_lse=True)
+    for part in (slice(0, 8), slice(496, 504), slice(1092, 1100)):
+        y, ey, lse, el = ref.attention(f64(q[part]), cache, table[part].numpy(), lengths[part], 0.125, BF16)
+        within(r.y[part], y, ey, "y")
+        full = np.isfinite(lse)
+        within(r.lse[part].cpu()[full], lse[full], el[full], "lse")
+    empty = [i for i, x in enumerate(lengths) if x == 0]
+    assert not r.y[empty].any() and torch.isinf(r.lse[empty]).all()
+    assert torch.isfinite(r.y).all()
+
+
+@pytest.mark.parametrize("form,pages,d", [("bf16", 70000, 256), ("int8", 140000, 256)])
+def test_cache_offsets_past_32_bits(qat, form, pages, d):
+    """Slots whose rows lie more than 2^32 bytes into the cache: what a small cache gives."""
+    heads, page, n = 8, 16, 200
+    k, v, q = (randn(i, n, heads, d, dtype=BF16) for i in range(3))
+    q = q[:1].repeat(1, 2, 1)[:, :2 * heads].contiguous()
+    lengths = torch.tensor([n], dtype=torch.int32).cuda()
+    t = torch.arange(n)
+    out = []
+    for total, first in ((16, 0), (pages, pages - 13)):
+        cache = qat.kv_cache(total, heads, page, d, form)
+        table = torch.arange(first, first + 13, dtype=torch.int32).flip(0).view(1, 13)
+        slots = (table[0].long()[t // page] * page + t % page).cuda()
+        qat.kv_write(cache, k, v, slots)
+        r = qat.kv_read(cache, slots)
+        out.append((r.k, r.v, qat.kv_attention(q, cache, table.cuda(), lengths).y))
+        assert cache.k.numel() * cache.k.element_size() > 1 << 32 or total == 16
+        del cache
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+
+
 def test_kv_attention_on_two_streams_at_once(qat):
     """Calls that overlap on the GPU have workspaces of their own."""
     lengths = [3000, 1, 2500]
