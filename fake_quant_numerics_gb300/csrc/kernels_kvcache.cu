@@ -6,8 +6,8 @@
 // directions are bound by their bytes.  A group of lanes holds a row in registers,
 // 16 elements a lane, so the statistics, the codes and the store take one read.
 // Measured: 65536 int8 positions x 8 heads of 128 to bf16 61 us (6.6 TB/s); 16384 tokens
-// of bf16 to affine 4-bit codes 24 us (3.6 TB/s, bound by the instructions of the exact
-// quotients) and back 14.
+// of bf16 to affine 4-bit codes 22 us (3.9 TB/s, bound by the instructions of the exact
+// quotients) and back 14; blocks of 256 threads in place of 128 2.4 us more.
 #include "qat_attention.h"
 #include "qat_kv.cuh"
 #include "qat_layer.cuh"
@@ -15,7 +15,7 @@
 namespace qat {
 namespace {
 
-constexpr int kKvThreads = 256;
+constexpr int kKvThreads = 128;
 
 struct KvPlace {
   void *codes[2];
@@ -329,8 +329,8 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_read(KvPlace p, int64_t token
 
 // Rows a group takes at a time: four (two of fp32) once that leaves every SM full, so
 // that their loads are in flight together; one for fewer, which then run side by side
-// (write and read of 16384 tokens x 8 heads as affine int4: 47 us with one row, 43 with
-// four; 16 tokens 3.6 us with one).
+// (write and read of 16384 tokens x 8 heads as affine int4: 41 us with one row, 36 with
+// four; 16 tokens 3.5 us with one).
 bool many_rows(int64_t rows, int lanes) {
   return rows * lanes >= (int64_t)device_info().sms * 2048 * 4;
 }
