@@ -512,9 +512,10 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
       auto after = [&](uint32_t slot) {
         return slot == kRingEnd - S::HALF_STAGE ? 0 : slot + S::HALF_STAGE;
       };
+      // (no slot has two copies under way: before the first tile the last slot gets zeros)
 #pragma unroll 1
       for (int i = -1; i < S::STAGES - 1; ++i)
-        issue(i, (i + 1) * S::HALF_STAGE, max(i, 0) * S::HALF_STAGE);
+        issue(i, (i + 1) * S::HALF_STAGE, (i < 0 ? S::STAGES - 1 : i) * S::HALF_STAGE);
 
       // --- the queries as products take them ------------------------------------------
       uint32_t qr[S::kF32 ? 1 : HT][S::kF32 ? 1 : S::KS][2];

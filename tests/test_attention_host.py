@@ -265,3 +265,44 @@ def test_rope_turns_are_exact():
         assert off <= 1 + 4 * abs(exact) * Decimal(2) ** -53 + (1 << 12 if abs(x) > math.tau else 0), x
     c, s = ref.angles([3, -3], [1 << 62], 1.0)
     assert abs(c[0, 0]) < 1e-15 and abs(s[0, 0] + 1) < 1e-15 and abs(s[1, 0] - 1) < 1e-15
+
+
+@pytest.mark.parametrize("current,guarded", [(None, False), (1, True)])
+def test_calls_launch_on_the_tensors_device(monkeypatch, current, guarded):
+    """A launch goes to the current device, so tensors of another one make theirs
+    current for the call (host tensors, whose device has no index, stand for them)."""
+    from fake_quant_numerics_gb300 import attention, layers
+
+    entered, seen = [], []
+
+    class Guard:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            entered.append(self.device)
+
+        def __exit__(self, *args):
+            entered.pop()
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith("workspace_bytes"):
+                return lambda *a: 64
+            return lambda *a: seen.append((name, bool(entered))) or 0
+
+    monkeypatch.setattr(layers._lib, "lib", lambda: Lib())
+    monkeypatch.setattr(attention, "_ptr", lambda t: t.data_ptr())
+    monkeypatch.setattr(layers, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(layers, "_current_device", lambda: current, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    q, w, p = torch.zeros(3, 4, 64), torch.ones(64), torch.arange(3)
+    turns, c = fq.rope_turns(fq.rope_frequencies(64)), fq.kv_cache(3, 2, 16, 64, device="cpu")
+    fq.head_norm_rope(q, q, p, turns, w, w)
+    fq.head_norm_rope_backward(q, q, q, q, p, turns, w, w)
+    fq.kv_write(c, q[:, :2], q[:, 2:], p)
+    fq.kv_read(c, p)
+    fq.kv_attention(q, c, torch.zeros(3, 1, dtype=torch.int32), torch.ones(3, dtype=torch.int32))
+    assert not entered
+    names = ["head_norm_rope", "head_norm_rope_backward", "kv_write", "kv_read", "kv_attention"]
+    assert seen == [("qat_" + name, guarded) for name in names]
