@@ -245,9 +245,8 @@ struct Shape {
   static constexpr int HALF_STAGE = (TILE + PARAMS) / 2;
   static constexpr int STAGES = smaller(6, larger(2, 13 * 1024 / (TILE + PARAMS)));
   static constexpr int H = 8 * HT, KS = DP / 16, MT = DP / 16;
-  // 16-bit parts of q and of the weights.  One of fp16 holds a weight to 2^-12, an eighth
-  // of what a bf16 output's own rounding is off; bf16 takes two for that.
-  static constexpr int QP = kF32 ? 3 : 1, PP = kF32 ? 3 : F == QAT_CACHE_BF16 ? 2 : 1;
+  // 16-bit parts of q and of the weights
+  static constexpr int QP = kF32 ? 3 : 1, PP = kF32 ? 3 : 2;
   static constexpr int QFRAG = kF32 ? QP * KS * 32 * 8 : 0;
   // A warp's ring and queries, then the part it starts with (its run began inside a
   // sequence); the part it ends with takes the ring's place.

@@ -698,8 +698,8 @@ qat_status qat_kv_read(const qat_kv_cache* cache, const int64_t* slots, int64_t 
  * page outside [0, pages), makes that sequence's outputs NaN.
  * The codes' products with q and with the softmax's weights are summed in binary32.
  * q keeps all its bits down to 2^-38 of its head's largest element (of a bf16 cache,
- * all).  Under a bf16 y a weight is rounded once to the 11 bits of fp16 (two bf16 parts
- * for a bf16 cache); under a float one it keeps 24.  Weights times value scales are
+ * all).  Under a bf16 y a weight goes as two parts, of fp16 (22 bits) or for a bf16 cache
+ * of bf16 (16 bits); under a float one it keeps 24 bits.  Weights times value scales are
  * held down to 2^-33 of the largest value scale (of a bf16 cache, all).
  * q_heads a multiple of the cache's heads (QAT_ERR_DIMENSION_MISMATCH); scale
  * finite; batch up to 65535, batch * q_heads and table_cols below 2^31.  workspace:

@@ -201,9 +201,8 @@ def attention(q, cache, table, lengths, scale, dtype):
             y[b, h] = w @ v
             lse[b, h] = top + math.log(e.sum())
             # weights: their exponent's error, the hardware exponential (2^-21) and, under a bf16
-            # output, their rounding to the 11 bits of fp16 (half a step: 2^-12 of the weight)
-            # or to two bf16 parts
-            rel = 2 * es + 2.0 ** -21 + 8 * U * np.abs(s - top) + (2.0 ** -12 if dtype == torch.bfloat16 else 8 * U)
+            # output, their two 16-bit parts
+            rel = 2 * es + 2.0 ** -21 + 8 * U * np.abs(s - top) + (2.0 ** -16 if dtype == torch.bfloat16 else 8 * U)
             size = np.abs(v) + np.abs(y[b, h]) + extra_values(cache, pages, h // group, t)[:, None]
             err = (w * rel) @ size + (8 * math.sqrt(n) + 16) * U * (w @ size)
             # weights, and their products with values, below the normal range of binary32 may
