@@ -29,9 +29,9 @@
 //
 // Twelve warps an SM (168 registers, 17 KB of ring each, two tiles and more in flight)
 // walk through tiles at 0.7 to 1 us each.  Measured (both launches, in a graph): 64
-// sequences of up to 8192 positions, 32 heads over 8 of 128 in affine 4-bit codes, 58 us
-// (3.3 TB/s; about 380 instructions a tile, 52% of the issue slots); two of 131072 in
-// E4M3 98 us (5.6 TB/s, 83% of the copy bandwidth); 32 of up to 2048, 16 heads of 64 in
+// sequences of up to 8192 positions, 32 heads over 8 of 128 in affine 4-bit codes, 63 us
+// (3.1 TB/s; about 400 instructions a tile, 51% of the issue slots); two of 131072 in
+// E4M3 100 us (5.5 TB/s, 82% of the copy bandwidth); 32 of up to 2048, 16 heads of 64 in
 // bf16, 22 us; one of 700 in int8 10.6 us, of which 8 are the latencies of lengths, table,
 // codes and the two joins.
 #include <atomic>
@@ -47,7 +47,7 @@ namespace {
 constexpr int kFormat = QAT_KV_FORMAT;
 constexpr float kLog2e = 1.4426950408889634f;
 // What a piece costs beside its tiles, in tiles (64 sequences of up to 8192 positions
-// in 4-bit codes: 74 us with 2, 60 with 4, 57 with 8, 58 with 14).
+// in 4-bit codes, with one part a weight: 74 us with 2, 60 with 4, 57 with 8, 58 with 14).
 constexpr int kPieceTiles = 8;
 // Tiles of a run at least (one sequence of 700 positions: 10.5 us with 1 or 2, 11.3 with
 // 4, 12.6 with 8; a run's first tiles may be a piece's cost).
@@ -245,15 +245,17 @@ struct Shape {
   static constexpr int HALF_STAGE = (TILE + PARAMS) / 2;
   static constexpr int STAGES = smaller(6, larger(2, 13 * 1024 / (TILE + PARAMS)));
   static constexpr int H = 8 * HT, KS = DP / 16, MT = DP / 16;
-  // 16-bit parts of q and of the weights
+  // 16-bit parts of q and of the weights (one of fp16 a weight: 58 us in place of 63 for the
+  // 4-bit batch, but a sequence's elements off by up to 2^-12 all alike)
   static constexpr int QP = kF32 ? 3 : 1, PP = kF32 ? 3 : 2;
   static constexpr int QFRAG = kF32 ? QP * KS * 32 * 8 : 0;
   // A warp's ring and queries, then the part it starts with (its run began inside a
   // sequence); the part it ends with takes the ring's place.
   static constexpr int PART = H * DP * 4;
   static constexpr int RING = larger(2 * STAGES * HALF_STAGE + QFRAG, PART), WARP = RING + PART;
-  // Registers hold twelve warps of up to 168, eight of up to 255 (thirteen spill: 71 us
-  // against 58 for the 4-bit batch; fourteen for short heads, 23.3 against 22.2).
+  // Registers hold twelve warps of up to 168, eight of up to 255 (with one part a weight
+  // thirteen spill: 71 us against 58 for the 4-bit batch; fourteen for short heads, 23.3
+  // against 22.2).
   static constexpr int WARPS =
       smaller(224 * 1024 / WARP, DP * HT <= 128 && !kF32 ? 12 : 8);
   static constexpr int THREADS = 32 * WARPS, SMEM = WARPS * WARP;
