@@ -387,7 +387,9 @@ __global__ void __launch_bounds__(kRopeThreads, V == 8 && T::BYTES == 2 ? 2 : 1)
         }
         float rstd = 1.0f, mean = 0.0f;
         if (r.norm) {
+          // (a step without a head: zeros, whose norm without an epsilon is not a number)
           rstd = rstd_of(r, group_sum(vsum(sq), lanes));
+          if (h >= n) rstd = 0.0f;
           mean = -(group_sum(vsum(gx), lanes) * rstd) * r.inv_d;  // of g'w z
         }
         // dw += g' z; dx = (g'w - z mean) rstd
