@@ -44,3 +44,79 @@ def test_head_norm_rope_backward_without_epsilon(qat, tokens, hq, hk, d, layout,
         want = ref.rope(f64(x), f64(w), f64(g), c, s, layout, 0.0, True, 1.0, dtype)
         within(dx, *want["dx"], "dx")
         within(dw, *want["dw"], "dw")
+
+
+# --- several heads a group -----------------------------------------------------------
+# Once the heads fill the GPU twice, a group takes 2, 4 or 8 of a token's (the launchers'
+# rule: forward from 2 sms 2048 / lanes heads, backward from 2 * 304 * 256 / lanes), the
+# last group of the queries, and of the keys, what is left of them.
+WALKS = [
+    # tokens, query heads, key heads, head_dim, rotary, layout, norm, type; heads a group on 152 SMs
+    (600, 31, 9, 128, 128, "half", True, BF16),           # 1, backward 2
+    (1100, 31, 9, 128, 64, "half", True, BF16),           # 1, 4
+    (2100, 31, 9, 128, 128, "interleaved", True, BF16),   # 2, 8
+    (4100, 31, 9, 128, 128, "half", True, BF16),          # 4, 8
+    (8200, 31, 9, 128, 128, "interleaved", False, BF16),  # 8, 8
+    (8200, 9, 3, 128, 128, "half", True, F32),            # 2, 8
+    (8200, 21, 0, 128, 32, "interleaved", True, F32),     # 4, 8 (no keys)
+    (8100, 7, 3, 40, 10, "half", True, F32),              # 8, 8 (single elements)
+    (8100, 7, 7, 80, 20, "interleaved", True, BF16),      # 8, 8 (runs of two)
+    (13000, 9, 3, 72, 72, "half", True, BF16),            # 8, 8 (runs of four)
+]
+
+
+@pytest.mark.parametrize("case", WALKS, ids=lambda c: "-".join(map(str, c[:6])))
+def test_head_norm_rope_several_heads_a_group(qat, case):
+    """A large call gives each token what a call of few tokens gives it, which is the
+    formula's; weight gradients are the formula's sums."""
+    t, hq, hk, d, rot, layout, norm, dtype = case
+    row = randn(0, t, (hq + 2 * hk) * d + 8, dtype=dtype)  # (queries, keys and values side by side)
+    q = row[:, :hq * d].view(t, hq, d)
+    k = row[:, hq * d:(hq + hk) * d].view(t, hk, d) if hk else None
+    gq, gk = randn(1, t, hq, d, dtype=dtype), randn(2, t, hk, d, dtype=dtype) if hk else None
+    wq = wk = None
+    if norm:
+        wq, wk = ((1 + randn(3 + i, d, scale=0.3)).to(dtype) for i in range(2))
+        wk = wk if hk else None
+    positions, turns = torch.arange(900, 900 + t).cuda(), qat.rope_turns(qat.rope_frequencies(rot), "cuda")
+    kw = dict(eps=1e-5, norm=norm, layout=layout, amplitude=1.25)
+    y = qat.head_norm_rope(q, k, positions, turns, wq, wk, **kw)
+    dq, dk, dwq, dwk = qat.head_norm_rope_backward(gq, gk, q, k, positions, turns, wq, wk, **kw)
+
+    def few(x, a):
+        return None if x is None else x[a:a + 64]
+
+    for a in range(0, t, 64):
+        args = few(q, a), few(k, a), positions[a:a + 64], turns, wq, wk
+        y1 = qat.head_norm_rope(*args, **kw)
+        g1 = qat.head_norm_rope_backward(few(gq, a), few(gk, a), *args, **kw)
+        for got, want in ((y.q, y1.q), (y.k, y1.k), (dq, g1[0]), (dk, g1[1])):
+            assert got is None and want is None or torch.equal(got[a:a + 64], want)
+    some = torch.tensor([0, 1, t // 2, t - 2, t - 1])
+    c, s = ref.angles(positions[some].tolist(), turns.tolist(), 1.25)
+    for x, w, g, got, dx in ((q, wq, gq, y.q, dq), (k, wk, gk, y.k, dk)):
+        if x is not None:
+            want = ref.rope(f64(x[some]), None if w is None else f64(w), f64(g[some]), c, s, layout, 1e-5, norm, 1.25,
+                            dtype)
+            within(got[some], *want["y"], "y")
+            within(dx[some], *want["dx"], "dx")
+    # dw = sum g' z in 64 bits (the angle's integer product wraps as the definition does)
+    a = (positions[:, None] * turns[None]).double() * (2 * math.pi * 2.0 ** -64)
+    c, s = a.cos()[:, None] * 1.25, a.sin()[:, None] * 1.25
+    i = torch.arange(rot // 2).cuda()
+    at, bt = (i, i + rot // 2) if layout == "half" else (2 * i, 2 * i + 1)
+    for x, w, g, dw in ((q, wq, gq, dwq), (k, wk, gk, dwk)):
+        if w is None:
+            assert dw is None
+            continue
+        x, g = x.double(), g.double()
+        z = x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-5)
+        gb, both = g.clone(), g.abs()
+        gb[..., at], gb[..., bt] = g[..., at] * c + g[..., bt] * s, g[..., bt] * c - g[..., at] * s
+        both[..., at] = both[..., bt] = g[..., at].abs() + g[..., bt].abs()
+        # ref.rope's bound: the sum, z's norm, and the turned gradient's angle
+        rel = (8 * math.sqrt(d) + 6) * U
+        err = (8 * math.sqrt(x.shape[0] * x.shape[1] + 16) * U + rel + 4 * U) * (gb * z).abs().sum((0, 1)) \
+            + (6 * 1.25 + 4 * 1.25) * U * (both * z.abs()).sum((0, 1))
+        want = (gb * z).sum((0, 1))
+        within(dw, f64(want), f64(err + ref.step(dtype) * (want.abs() + err)), "dw")
