@@ -91,9 +91,19 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
   }
 #undef QAT_MMA
 }
-// The next 16-bit parts of two numbers, packed; they keep the remainders.  bf16 parts
-// before the LAST are cut off, so that none overflows.
-template <bool HALF, bool LAST>
+// The number one binary32 step nearer to 0, cut off to its upper half (0 stays): never the
+// number itself, so that a remainder is left, of its sign.
+template <bool SIGNED>
+__device__ __forceinline__ uint32_t upper_below(float x) {
+  const uint32_t u = __float_as_uint(x);
+  if constexpr (!SIGNED) return (max(u, 1u) - 1u) & 0xffff0000u;
+  return ((max(u & 0x7fffffffu, 1u) - 1u) & 0x7fff0000u) | (u & 0x80000000u);
+}
+// The next 16-bit parts of two numbers, packed; they keep the remainders.  bf16 parts before
+// the LAST are cut off, so that none overflows, and none is 0 unless the number is (or lies
+// below 2^-110): 0 times an infinity of the cache's would make NaN of what is infinite.
+// SIGNED: numbers that may be negative.
+template <bool HALF, bool LAST, bool SIGNED>
 __device__ __forceinline__ uint32_t take_pair(float& x, float& y) {
   if constexpr (HALF) {
     uint32_t r;
@@ -106,8 +116,8 @@ __device__ __forceinline__ uint32_t take_pair(float& x, float& y) {
   } else if constexpr (LAST) {
     return pack_bf16x2(x, y);
   } else {
-    const uint32_t u = __float_as_uint(x), v = __float_as_uint(y) & 0xffff0000u;
-    x -= __uint_as_float(u & 0xffff0000u), y -= __uint_as_float(v);
+    const uint32_t u = upper_below<SIGNED>(x), v = upper_below<SIGNED>(y);
+    x -= __uint_as_float(u), y -= __uint_as_float(v);
     return u >> 16 | v;
   }
 }
@@ -556,14 +566,16 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = v[j][S::key_place(2 * k + i / 2, i % 2)];
             if constexpr (!S::kF32) {
-              qr[ht][ks][0] = take_pair<HALF, true>(x[0], x[1]);
-              qr[ht][ks][1] = take_pair<HALF, true>(x[2], x[3]);
+              qr[ht][ks][0] = take_pair<HALF, true, true>(x[0], x[1]);
+              qr[ht][ks][1] = take_pair<HALF, true, true>(x[2], x[3]);
             } else {
 #pragma unroll
               for (int p = 0; p < 3; ++p) {
                 uint2 y;
-                y.x = p < 2 ? take_pair<HALF, false>(x[0], x[1]) : take_pair<HALF, true>(x[0], x[1]);
-                y.y = p < 2 ? take_pair<HALF, false>(x[2], x[3]) : take_pair<HALF, true>(x[2], x[3]);
+                y.x = p < 2 ? take_pair<HALF, false, true>(x[0], x[1])
+                            : take_pair<HALF, true, true>(x[0], x[1]);
+                y.y = p < 2 ? take_pair<HALF, false, true>(x[2], x[3])
+                            : take_pair<HALF, true, true>(x[2], x[3]);
                 qfrag[(p * S::KS + ks) * 32 + lane] = y;
               }
             }
@@ -742,8 +754,8 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
           for (int p = 0; p < S::PP; ++p)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              wb[ht][p][r] = transpose8(p + 1 < S::PP ? take_pair<HALF, false>(w[2 * r], w[2 * r + 1])
-                                                      : take_pair<HALF, true>(w[2 * r], w[2 * r + 1]));
+              wb[ht][p][r] = transpose8(p + 1 < S::PP ? take_pair<HALF, false, false>(w[2 * r], w[2 * r + 1])
+                                                      : take_pair<HALF, true, false>(w[2 * r], w[2 * r + 1]));
         }
       };
       // Weighted values: rows are head elements, k the positions.

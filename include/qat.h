@@ -701,6 +701,10 @@ qat_status qat_kv_read(const qat_kv_cache* cache, const int64_t* slots, int64_t 
  * all).  Under a bf16 y a weight goes as two parts, of fp16 (22 bits) or for a bf16 cache
  * of bf16 (16 bits); under a float one it keeps 24 bits.  Weights times value scales are
  * held down to 2^-33 of the largest value scale (of a bf16 cache, all).
+ * An infinity in a bf16 cache is one in the formula: a key whose score is -inf has weight
+ * 0, an infinite value makes that element of y infinite, and inf - inf or 0 inf NaN
+ * (weights and elements of q below 2^-110 may count as 0 there).  A sequence whose scores
+ * are all -inf gives what an empty one gives.
  * q_heads a multiple of the cache's heads (QAT_ERR_DIMENSION_MISMATCH); scale
  * finite; batch up to 65535, batch * q_heads and table_cols below 2^31.  workspace:
  * qat_kv_attention_workspace_bytes(cache, q_heads) bytes, 16-byte aligned: partial

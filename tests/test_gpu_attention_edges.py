@@ -120,3 +120,90 @@ def test_head_norm_rope_several_heads_a_group(qat, case):
             + (6 * 1.25 + 4 * 1.25) * U * (both * z.abs()).sum((0, 1))
         want = (gb * z).sum((0, 1))
         within(dw, f64(want), f64(err + ref.step(dtype) * (want.abs() + err)), "dw")
+
+
+# --- infinities in a bf16 cache --------------------------------------------------------
+def bf16_sequences(qat, seed, lengths, kv_heads, d, page):
+    """A bf16 cache that holds the sequences on scattered pages, and their table."""
+    need = [-(-n // page) for n in lengths]
+    order = torch.randperm(sum(need), generator=torch.Generator().manual_seed(seed)).int()
+    table = torch.full((len(lengths), max(need)), -1, dtype=torch.int32)
+    cache, at = qat.kv_cache(sum(need), kv_heads, page, d, "bf16"), 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    cache.k.copy_(randn(seed, *cache.k.shape, dtype=BF16))
+    cache.v.copy_(randn(seed + 1, *cache.v.shape, dtype=BF16))
+    return cache, table
+
+
+def queries(kind, seed, *shape):
+    """bf16 queries; fp32 ones of 24 bits, and of the 8 or 16 that one or two bf16 parts hold."""
+    q = randn(seed, *shape)
+    if kind == "bf16":
+        return q.to(BF16)
+    if kind == "fp32 of 8 bits":
+        return q.to(BF16).float()
+    return (q.to(BF16).float() * 1.0078125).contiguous() if kind == "fp32 of 16 bits" else q
+
+
+KINDS = ["bf16", "fp32", "fp32 of 8 bits", "fp32 of 16 bits"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 72, 256])
+def test_kv_attention_infinite_values(qat, kind, d):
+    """An infinite value makes its element of its key head's outputs infinite, two of both
+    signs NaN; the other elements keep their bits."""
+    lengths, page = [1, 40, 300, 6000], 16
+    cache, table = bf16_sequences(qat, 3, lengths, 2, d, page)
+    q, n, tab = queries(kind, 9, 4, 4, d), torch.tensor(lengths, dtype=torch.int32).cuda(), table.cuda()
+    want = qat.kv_attention(q, cache, tab, n).y.clone()
+    inf = float("inf")
+    # sequence, position, element, value
+    for b, t, e, x in ((0, 0, 3, inf), (0, 0, 5, -inf), (1, 39, 0, inf), (1, 7, d - 1, -inf), (2, 0, 8, inf),
+                       (2, 299, 9, -inf), (3, 3000, 17, inf), (3, 3001, 17, inf), (3, 5999, 40, -inf)):
+        cache.v[int(table[b, t // page]), 1, t % page, e] = x
+        want[b, 2:, e] = x
+    for b, t, u, e in ((1, 3, 20, 11), (2, 10, 11, 12), (3, 1, 5000, 13)):
+        cache.v[int(table[b, t // page]), 1, t % page, e] = inf
+        cache.v[int(table[b, u // page]), 1, u % page, e] = -inf
+        want[b, 2:, e] = float("nan")
+    got = qat.kv_attention(q, cache, tab, n).y
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(got, 0.0, inf, -inf), torch.nan_to_num(want, 0.0, inf, -inf))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 72, 256])
+def test_kv_attention_infinite_keys(qat, kind, d):
+    """A key whose score is -inf has weight 0: the outputs are those of the sequence without
+    it.  One whose score is inf makes NaN, as inf - inf does."""
+    lengths, page, e = [2, 40, 300, 6000], 16, 5
+    dtype = BF16 if kind == "bf16" else F32
+    cache, table = bf16_sequences(qat, 5, lengths, 2, d, page)
+    q, tab = queries(kind, 9, 4, 4, d), table.cuda()
+    q[:, 0, e], q[:, 1, e], q[:, 2, e], q[:, 3, e] = 1.5, -1.5, q[:, 2, e].abs() + q[0, 0, 0].abs(), -2.0
+    if kind == "fp32 of 8 bits":
+        q = q.to(BF16).float()
+    without = qat.kv_cache(cache.pages, 2, page, d, "bf16")
+    without.k.copy_(cache.k), without.v.copy_(cache.v)
+    for b, t, x in ((0, 0, math.inf), (1, 39, -math.inf), (2, 0, math.inf), (3, 4000, -math.inf)):
+        n = lengths[b]
+        # heads 0, 1 read key head 0, which keeps its keys
+        cache.k[int(table[b, t // page]), 1, t % page, e] = x
+        for c in (without.k, without.v):  # the last position takes the place of position t
+            last = c[int(table[b, (n - 1) // page]), :, (n - 1) % page].clone()
+            c[int(table[b, t // page]), :, t % page] = last
+    n = torch.tensor(lengths, dtype=torch.int32)
+    r = qat.kv_attention(q, cache, tab, n.cuda(), want_lse=True)
+    y, ey, lse, el = ref.attention(f64(q), without, table.numpy(), (n - 1).tolist(), d ** -0.5, dtype)
+    for b, up in ((0, True), (1, False), (2, True), (3, False)):
+        good, bad = (3, 2) if up else (2, 3)  # (q's sign times the infinity's)
+        within(r.y[b, good], y[b, good], ey[b, good], "y")
+        within(r.lse[b, good], lse[b, good], el[b, good], "lse")
+        assert torch.isnan(r.y[b, bad]).all() and not torch.isnan(r.y[b, :2]).any()
+    # nothing but such keys
+    cache.k[int(table[0, 0]), 1, :2, e] = math.inf
+    r = qat.kv_attention(q, cache, tab, n.cuda(), want_lse=True)
+    assert not r.y[0, 3].any() and r.lse[0, 3] == -math.inf
