@@ -255,9 +255,10 @@ struct Shape {
   static constexpr int HALF_STAGE = (TILE + PARAMS) / 2;
   static constexpr int STAGES = smaller(6, larger(2, 13 * 1024 / (TILE + PARAMS)));
   static constexpr int H = 8 * HT, KS = DP / 16, MT = DP / 16;
-  // 16-bit parts of q and of the weights (one of fp16 a weight: 58 us in place of 63 for the
-  // 4-bit batch, but a sequence's elements off by up to 2^-12 all alike)
-  static constexpr int QP = kF32 ? 3 : 1, PP = kF32 ? 3 : 2;
+  // 16-bit parts of q and of the weights: two of fp16 hold 22 bits of a weight (one: 58 us in
+  // place of 63 for the 4-bit batch, but a sequence's elements off by up to 2^-12 all alike),
+  // three of bf16 all 24.
+  static constexpr int QP = kF32 ? 3 : 1, PP = kF32 || F == QAT_CACHE_BF16 ? 3 : 2;
   static constexpr int QFRAG = kF32 ? QP * KS * 32 * 8 : 0;
   // A warp's ring and queries, then the part it starts with (its run began inside a
   // sequence); the part it ends with takes the ring's place.

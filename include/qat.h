@@ -698,9 +698,9 @@ qat_status qat_kv_read(const qat_kv_cache* cache, const int64_t* slots, int64_t 
  * page outside [0, pages), makes that sequence's outputs NaN.
  * The codes' products with q and with the softmax's weights are summed in binary32.
  * q keeps all its bits down to 2^-38 of its head's largest element (of a bf16 cache,
- * all).  Under a bf16 y a weight goes as two parts, of fp16 (22 bits) or for a bf16 cache
- * of bf16 (16 bits); under a float one it keeps 24 bits.  Weights times value scales are
- * held down to 2^-33 of the largest value scale (of a bf16 cache, all).
+ * all).  A softmax weight keeps 24 bits, under a bf16 y over a quantized cache 22 (two
+ * parts of fp16).  Weights times value scales are held down to 2^-33 of the largest value
+ * scale (of a bf16 cache, all).
  * An infinity in a bf16 cache is one in the formula: a key whose score is -inf has weight
  * 0, an infinite value makes that element of y infinite, and inf - inf or 0 inf NaN
  * (weights and elements of q below 2^-110 may count as 0 there).  A sequence whose scores

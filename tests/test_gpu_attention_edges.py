@@ -207,3 +207,30 @@ def test_kv_attention_infinite_keys(qat, kind, d):
     cache.k[int(table[0, 0]), 1, :2, e] = math.inf
     r = qat.kv_attention(q, cache, tab, n.cuda(), want_lse=True)
     assert not r.y[0, 3].any() and r.lse[0, 3] == -math.inf
+
+
+def test_kv_attention_weights_of_bf16_rows(qat):
+    """Weighted values that cancel to 2^-16 of their size show a weight's last bits under a
+    bf16 output too.  Queries of one element make scores exact products: a weight is off by
+    the rounding of score * log2 e (3 U of up to 2) and of the hardware exponential (2^-22),
+    its sum by 3 U; the nine products of a sum by 2 U each.  That is below 40 U of the
+    values' size; weights of 16 bits were off by up to 2^-17 of it."""
+    batch, heads, d, page = 32, 3, 64, 16
+    cache = qat.kv_cache(batch, heads, page, d, "bf16")
+    g = torch.Generator().manual_seed(7)
+    q = torch.zeros(batch, heads, d)
+    q[..., 9] = 1.0
+    k0 = (torch.rand(batch, heads, 3, generator=g) * 2 - 1).to(BF16).double()
+    w = torch.softmax(k0, -1)[..., None]
+    v = torch.zeros(batch, heads, 3, d, dtype=torch.float64)
+    v[:, :, 0] = (1 + torch.rand(batch, heads, d, generator=g)).to(BF16).double()
+    v[:, :, 1] = (-v[:, :, 0] * w[:, :, 0] / w[:, :, 1]).to(BF16).double()
+    v[:, :, 2] = (-(v[:, :, :2] * w[:, :, :2]).sum(2) / w[:, :, 2]).to(BF16).double()
+    want, size = (v * w).sum(2), (v.abs() * w).sum(2)
+    cache.k[:, :, :3, 9] = k0.to(BF16).cuda()
+    cache.v[:, :, :3] = v.to(BF16).cuda()
+    table = torch.arange(batch, dtype=torch.int32).view(batch, 1).cuda()
+    n = torch.full((batch,), 3, dtype=torch.int32).cuda()
+    for dtype in (BF16, F32):
+        y = qat.kv_attention(q.to(dtype).cuda(), cache, table, n, 1.0).y
+        within(y, f64(want), f64(40 * U * size + ref.step(dtype) * (want.abs() + 40 * U * size)), "y")
