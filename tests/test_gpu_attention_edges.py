@@ -234,3 +234,32 @@ def test_kv_attention_weights_of_bf16_rows(qat):
     for dtype in (BF16, F32):
         y = qat.kv_attention(q.to(dtype).cuda(), cache, table, n, 1.0).y
         within(y, f64(want), f64(40 * U * size + ref.step(dtype) * (want.abs() + 40 * U * size)), "y")
+
+
+# --- long runs -------------------------------------------------------------------------
+@pytest.mark.parametrize("form", ["int8", "int4", "e4m3", "bf16"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_kv_attention_sums_of_long_runs(qat, form, dtype):
+    """More sequences of 2^20 positions than warps, so that one warp adds up tens of thousands
+    of tiles.  Values are positive: each of N = n / 16 additions rounds by at most U of the
+    sum so far, of either sign, U sqrt(N) / 3 in all and 8 sqrt(N) U far above it.  (The
+    sequences share their pages.  Queries of one element make scores exact: 10 U a weight.)"""
+    n, d, page, batch = 1 << 20, 64, 1 << 13, 2000
+    g = torch.Generator(device="cuda").manual_seed(3)
+    cache = qat.kv_cache(n // page, 1, page, d, form)
+    k = torch.rand(n, 1, d, generator=g, device="cuda") * 2 - 1
+    v = torch.rand(n, 1, d, generator=g, device="cuda") + 0.5
+    slots = torch.arange(n, device="cuda")
+    qat.kv_write(cache, k, v, slots)
+    r = qat.kv_read(cache, slots, F32)
+    q = torch.zeros(1, 1, d, device="cuda")
+    q[..., 9] = 2.0
+    s = r.k[:, 0].double() @ q[0, 0].double()
+    want, lse = torch.softmax(s, 0) @ r.v[:, 0].double(), torch.logsumexp(s, 0)
+    table = torch.arange(n // page, dtype=torch.int32, device="cuda").view(1, -1).expand(batch, -1)
+    got = qat.kv_attention(q.to(dtype).expand(batch, 1, d), cache, table,
+                           torch.full((batch,), n, dtype=torch.int32, device="cuda"), 1.0, want_lse=True)
+    err = (8 * math.sqrt(n / 16) + 40) * U * want.abs()
+    for i in (0, 1, 777, batch - 1):
+        within(got.y[i, 0], f64(want), f64(err + ref.step(dtype) * (want.abs() + err)), "y")
+        assert abs(float(got.lse[i, 0]) - float(lse)) <= (8 * math.sqrt(n / 16) + 40) * U + 4 * U * float(lse)
