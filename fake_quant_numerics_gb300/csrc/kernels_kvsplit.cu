@@ -8,9 +8,10 @@
 // read: they are the eight columns of m16n8k16 products whose rows are positions
 // (scores) or head elements (values).  Codes are exact in fp16, which takes fewer
 // operations to reach than bf16 (a code is the low bits of a number of exponent 10;
-// FP8 converts), so quantized rows are multiplied in fp16: queries and weights are
-// first scaled by powers of two, so that their largest values lie near the top of its
-// range and what falls below it is 2^-38 of them.  bf16 rows are multiplied in bf16.
+// FP8 converts), so quantized rows are multiplied in fp16: queries and weights (with
+// their value's scale) are first scaled by powers of two, so that a head's largest lie near
+// the top of its range; what falls below it is 2^-38 of the largest element of q and 2^-33
+// of the largest weight.  bf16 rows are multiplied in bf16.
 //
 // Work is cut evenly whatever the lengths: the tiles of 16 positions of every
 // (sequence, head group), in one row, are dealt to the resident warps in equal runs.
@@ -593,16 +594,18 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
       }
 
       // m: the maximum that weights refer to; limit: where it moves; base: m, but 0 before
-      // the first score.  Weighted values are summed times `unit`, a power of two that
-      // keeps p vs unit within 2^15 (p <= 2^4) for scales up to v_limit, and the largest
-      // scale above 2^8 (what p vs loses below fp16's last bit is 2^-33 of that scale).
+      // the first score.  Weighted values of codes are summed times `unit`, a head's power of
+      // two that keeps p vs unit within 2^15 and `most`, which the largest p vs has reached,
+      // between 2^8 and 2^9: what p vs loses below fp16's last bit is 2^-33 of the largest, and
+      // rows of small weights count for what they add, whatever their scale.
       float m[HT][2], limit[HT][2], base[HT][2], l[HT][2], zsum[HT][2], o[HT][S::MT][4];
-      float unit = 1.0f, v_limit = -1.0f;
+      float unit[HT][2], most[HT][2];
 #pragma unroll
       for (int ht = 0; ht < HT; ++ht) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          m[ht][i] = limit[ht][i] = -INFINITY, base[ht][i] = l[ht][i] = zsum[ht][i] = 0.0f;
+          m[ht][i] = limit[ht][i] = -INFINITY, base[ht][i] = l[ht][i] = zsum[ht][i] = 0.0f,
+          unit[ht][i] = HALF ? 0x1p108f : 1.0f, most[ht][i] = 0.0f;
 #pragma unroll
         for (int i = 0; i < S::MT; ++i)
 #pragma unroll
@@ -698,27 +701,28 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
               for (int ht = 0; ht < HT; ++ht) s[ht][2 * r] = s[ht][2 * r + 1] = -INFINITY;
             }
         }
-        // the maximum and the unit move only where a score or a scale is far above them
-        bool above = HALF && fmaxf(fabsf(vs[0]), fabsf(vs[1])) > v_limit;
+        float p[HT][4], w[HT][4];
+        auto weights = [&] {
 #pragma unroll
-        for (int ht = 0; ht < HT; ++ht)
+          for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            above = above || fmaxf(s[ht][i], s[ht][2 + i]) > limit[ht][i];
-        if (__any_sync(kFull, above)) {
-          float shrink = 1.0f;
-          if constexpr (HALF) {
-            float top = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
-            if (top > v_limit) {  // to between 2^8 and 2^9
-              const int e = top < 0x1p-100f ? -100 : exponent_of(top);
-              const int by = 8 - e - exponent_of(unit);
-              if (v_limit >= 0.0f) shrink = power_of_two(max(by, -126));
-              unit = power_of_two(8 - e);
-              v_limit = power_of_two(min(e + 3, 127));
+            for (int i = 0; i < 4; ++i) {
+              w[ht][i] = p[ht][i] = exp2_fast(s[ht][i] - base[ht][i & 1]);
+              if constexpr (HALF) w[ht][i] = p[ht][i] * unit[ht][i & 1] * vs[i >> 1];
             }
-          }
+        };
+        weights();
+        // the maximum and the unit move only where a score or a weighted scale is far above them
+        bool above = false;
+#pragma unroll
+        for (int ht = 0; ht < HT; ++ht) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) above = above || fmaxf(s[ht][i], s[ht][2 + i]) > limit[ht][i];
+          if constexpr (HALF)
+            above = above || fmaxf(fmaxf(fabsf(w[ht][0]), fabsf(w[ht][1])),
+                                   fmaxf(fabsf(w[ht][2]), fabsf(w[ht][3]))) > 0x1p15f;
+        }
+        if (__any_sync(kFull, above)) {
 #pragma unroll
           for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
@@ -732,31 +736,39 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
               limit[ht][i] = top + kSlack;
               base[ht][i] = top == -INFINITY ? 0.0f : top;
               l[ht][i] *= was;
-              const float both = was * shrink;
+              float both = was;
+              if constexpr (HALF) {
+                // (Below 2^-100 as near to 2^8 as that.  The unit grows by more than 1 / was only
+                // beside sums of 0, and falls by more than 2^126 from sums that no longer count.)
+                float here = fmaxf(fabsf(exp2_fast(s[ht][i] - base[ht][i]) * vs[0]),
+                                   fabsf(exp2_fast(s[ht][2 + i] - base[ht][i]) * vs[1]));
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) here = fmaxf(here, __shfl_xor_sync(kFull, here, x));
+                most[ht][i] = fmaxf(fmaxf(here, most[ht][i] * was), 0x1p-100f);
+                const int old = exponent_of(unit[ht][i]), now = 8 - exponent_of(most[ht][i]);
+                unit[ht][i] = power_of_two(now);
+                both *= power_of_two(min(max(now - old, -126), 127));
+              }
               zsum[ht][i] *= both;
 #pragma unroll
               for (int j = 0; j < S::MT; ++j) scale_in_place(o[ht][j][i], both), scale_in_place(o[ht][j][2 + i], both);
             }
+          weights();
         }
-        if constexpr (HALF) vs[0] *= unit, vs[1] *= unit;
 #pragma unroll
         for (int ht = 0; ht < HT; ++ht) {
-          float w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float p = exp2_fast(s[ht][i] - base[ht][i & 1]);
-            l[ht][i & 1] += p;
-            w[i] = p;
-            if constexpr (F != QAT_CACHE_BF16) w[i] *= vs[i >> 1];
+            l[ht][i & 1] += p[ht][i];
             if constexpr (kv_is_int(F))
-              zsum[ht][i & 1] = __fmaf_rn(w[i], vz[i >> 1], zsum[ht][i & 1]);
+              zsum[ht][i & 1] = __fmaf_rn(w[ht][i], vz[i >> 1], zsum[ht][i & 1]);
           }
 #pragma unroll
-          for (int p = 0; p < S::PP; ++p)
+          for (int k = 0; k < S::PP; ++k)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              wb[ht][p][r] = transpose8(p + 1 < S::PP ? take_pair<HALF, false, false>(w[2 * r], w[2 * r + 1])
-                                                      : take_pair<HALF, true, false>(w[2 * r], w[2 * r + 1]));
+              wb[ht][k][r] = transpose8(k + 1 < S::PP ? take_pair<HALF, false, false>(w[ht][2 * r], w[ht][2 * r + 1])
+                                                      : take_pair<HALF, true, false>(w[ht][2 * r], w[ht][2 * r + 1]));
         }
       };
       // Weighted values: rows are head elements, k the positions.
@@ -839,7 +851,7 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
           }
           const int h = 8 * ht + 2 * t4 + i;
           if (h >= heads) continue;
-          const float by = __frcp_rn(unit) * (!whole ? 1.0f : sum == 0.0f ? 0.0f : __frcp_rn(sum));
+          const float by = __frcp_rn(unit[ht][i]) * (!whole ? 1.0f : sum == 0.0f ? 0.0f : __frcp_rn(sum));
           const int64_t y_at = ((int64_t)b * a.q_heads + h0 + h) * d;
 #pragma unroll
           for (int j = 0; j < S::NV; ++j)

@@ -263,3 +263,79 @@ def test_kv_attention_sums_of_long_runs(qat, form, dtype):
     for i in (0, 1, 777, batch - 1):
         within(got.y[i, 0], f64(want), f64(err + ref.step(dtype) * (want.abs() + err)), "y")
         assert abs(float(got.lse[i, 0]) - float(lse)) <= (8 * math.sqrt(n / 16) + 40) * U + 4 * U * float(lse)
+
+
+# --- value scales under unequal weights --------------------------------------------------
+FORMS = [("int8", "symmetric"), ("int8", "affine"), ("int4", "symmetric"), ("int4", "affine"), ("e4m3", "symmetric"),
+         ("e5m2", "symmetric"), ("bf16", "symmetric")]
+
+
+def unequal(kind, n, g):
+    """Scores [n, 2] of two heads that share a key head (nats), and exponents of the values' sizes."""
+    s, e = torch.rand(n, 2, generator=g) * 6 - 3, torch.zeros(n)
+    if kind.startswith("far"):    # one row, far larger than the others, that no head attends to
+        _, at, e_far = kind.split()
+        s[int(at) % n], e[int(at) % n] = -1000.0, float(e_far)
+    elif kind == "two heads":     # one head attends to small values, the other to large ones
+        e[::2] = -40
+        s[::2, 1] -= 200
+        s[1::2, 0] -= 200
+    elif kind == "fall":          # large values first, whose weights fade
+        e = torch.linspace(60, -60, n)
+        s = torch.linspace(-20, 20, n)[:, None].repeat(1, 2)
+    elif kind == "records":       # scores that keep growing over rows of zeros
+        e[16:] = -math.inf
+        s = torch.linspace(0, 40, n)[:, None] * torch.tensor([1.0, 0.7])
+    else:
+        s, e = torch.rand(n, 2, generator=g) * 60 - 30, torch.rand(n, generator=g) * 80 - 40
+    return s, e
+
+
+@pytest.mark.parametrize("form,scheme", FORMS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind", ["far 0 24", "far 200 40", "far -1 80", "far 17 -80", "two heads", "fall", "records",
+                                  "random"])
+def test_kv_attention_scales_under_unequal_weights(qat, form, scheme, dtype, kind):
+    """What fp16 parts of a weight times its value's scale lose is 2^-33 of the largest such
+    product of the head: rows that it does not attend to, and other heads, cost it nothing.
+
+    Each head's queries have one element, a power of two, so that products with the codes are
+    exact; a score is off by 4 U of itself (its scale, log2 e and the two products).  Moving
+    the maximum rounds what is summed by 6 U (exponential and product); it moves by 2^4 or for
+    a product 2^6 times the largest."""
+    n, d, page = 1000, 64, 16
+    g = torch.Generator().manual_seed(len(kind))
+    s, e = unequal(kind, n, g)
+    cache = qat.kv_cache(-(-n // page), 1, page, d, form, scheme)
+    table = torch.randperm(cache.pages, generator=g).int().view(1, -1)
+    t = torch.arange(n)
+    pages = table[0].long()[t // page]
+    k = torch.zeros(n, 1, d)
+    k[:, 0, :2] = s / 4
+    v = torch.randn(n, 1, d, generator=g) * (2.0 ** e)[:, None, None]
+    qat.kv_write(cache, k.cuda(), v.cuda(), (pages * page + t % page).cuda())
+    q = torch.zeros(1, 2, d)
+    q[0, 0, 0] = q[0, 1, 1] = 4.0
+    r = qat.kv_attention(q.to(dtype).cuda(), cache, table.cuda(), torch.tensor([n], dtype=torch.int32).cuda(), 1.0,
+                         want_lse=True)
+    at = pages, 0, t % page
+    kv, vv, codes = ref.values_of(cache, "k")[at], ref.values_of(cache, "v")[at], np.abs(ref.codes_of(cache, "v")[at])
+    vs = np.zeros(n) if form == "bf16" else np.abs(f64(cache.v_scale)[at])
+    zp = ref.extra_codes(cache, pages.numpy(), 0, t.numpy())[:, None]
+    zv = ref.extra_values(cache, pages.numpy(), 0, t.numpy())[:, None]
+    bits = 1.45 * f64(s.max(0).values - s.min(0).values).sum()  # (of both heads' scores)
+    moves = 4 + bits / 4 + float(e[e > -math.inf].max() - e[e > -math.inf].min()) / 6
+    for h in range(2):
+        x = kv[:, h] * 4
+        w = np.exp(x - x.max())
+        total = w.sum()
+        w /= total
+        want = w @ vv
+        # (the part's bits: 8 U, or 2^-22 under a bf16 output)
+        rel = (8 * np.abs(x) + 8 * np.abs(x - x.max()) + 16 + 6 * moves) * U
+        size = np.abs(vv) + np.abs(want) + zv
+        err = (w * rel) @ size + (8 * math.sqrt(n) + 16) * U * (w @ size) + n * 2.0 ** -126 * (1 + np.abs(vv).max(0))
+        err = err + 2.0 ** -33 * (w * vs).max() * (codes + zp).sum(0)
+        within(r.y[0, h], want, err + ref.step(dtype) * (np.abs(want) + err), "y")
+        lse = x.max() + math.log(total)
+        assert abs(float(r.lse[0, h]) - lse) <= (w * rel).sum() + (8 * math.sqrt(n) + 16) * U + 4 * U * abs(lse)
