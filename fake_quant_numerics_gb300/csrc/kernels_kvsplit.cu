@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           m[ht][i] = limit[ht][i] = -INFINITY, base[ht][i] = l[ht][i] = zsum[ht][i] = 0.0f,
-          unit[ht][i] = HALF ? 0x1p108f : 1.0f, most[ht][i] = 0.0f;
+          unit[ht][i] = HALF ? 0x1p123f : 1.0f, most[ht][i] = 0.0f;
 #pragma unroll
         for (int i = 0; i < S::MT; ++i)
 #pragma unroll
@@ -738,13 +738,14 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
               l[ht][i] *= was;
               float both = was;
               if constexpr (HALF) {
-                // (Below 2^-100 as near to 2^8 as that.  The unit grows by more than 1 / was only
+                // (Below 2^-115 as near to 2^8 as that: the unit times p stays finite, and what is
+                // lost lies below the smallest number.  The unit grows by more than 1 / was only
                 // beside sums of 0, and falls by more than 2^126 from sums that no longer count.)
                 float here = fmaxf(fabsf(exp2_fast(s[ht][i] - base[ht][i]) * vs[0]),
                                    fabsf(exp2_fast(s[ht][2 + i] - base[ht][i]) * vs[1]));
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) here = fmaxf(here, __shfl_xor_sync(kFull, here, x));
-                most[ht][i] = fmaxf(fmaxf(here, most[ht][i] * was), 0x1p-100f);
+                most[ht][i] = fmaxf(fmaxf(here, most[ht][i] * was), 0x1p-115f);
                 const int old = exponent_of(unit[ht][i]), now = 8 - exponent_of(most[ht][i]);
                 unit[ht][i] = power_of_two(now);
                 both *= power_of_two(min(max(now - old, -126), 127));
@@ -851,7 +852,7 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
           }
           const int h = 8 * ht + 2 * t4 + i;
           if (h >= heads) continue;
-          const float by = __frcp_rn(unit[ht][i]) * (!whole ? 1.0f : sum == 0.0f ? 0.0f : __frcp_rn(sum));
+          const float by = !whole ? 1.0f : sum == 0.0f ? 0.0f : __frcp_rn(sum), down = __frcp_rn(unit[ht][i]);
           const int64_t y_at = ((int64_t)b * a.q_heads + h0 + h) * d;
 #pragma unroll
           for (int j = 0; j < S::NV; ++j)
@@ -864,7 +865,7 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
               for (int x = 0; x < 8; ++x) {
                 constexpr auto pl = &S::value_place;
                 const int p = pl(j, e + x);
-                y[x] = (o[ht][p / 2][i + 2 * (p % 2)] - z) * by;
+                y[x] = (o[ht][p / 2][i + 2 * (p % 2)] - z) * by * down;
               }
               if (whole)
                 store8<T>(a.y, y_at + at, y_vec, y);

@@ -700,8 +700,8 @@ qat_status qat_kv_read(const qat_kv_cache* cache, const int64_t* slots, int64_t 
  * q keeps all its bits down to 2^-38 of its head's largest element (of a bf16 cache,
  * all).  A softmax weight keeps 24 bits, under a bf16 y over a quantized cache 22 (two
  * parts of fp16).  Weights times value scales are held down to 2^-33 of the head's largest
- * such product (of a bf16 cache, all).  A value times 16 lengths[b] has to be a binary32
- * number, as the sums of weighted values are.
+ * such product, or 2^-148 (of a bf16 cache, all).  A value times 16 lengths[b] has to be a
+ * binary32 number, as the sums of weighted values are.
  * An infinity in a bf16 cache is one in the formula: a key whose score is -inf has weight
  * 0, an infinite value makes that element of y infinite, and inf - inf or 0 inf NaN
  * (weights and elements of q below 2^-110 may count as 0 there).  A sequence whose scores

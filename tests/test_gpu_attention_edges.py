@@ -276,6 +276,8 @@ def unequal(kind, n, g):
     if kind.startswith("far"):    # one row, far larger than the others, that no head attends to
         _, at, e_far = kind.split()
         s[int(at) % n], e[int(at) % n] = -1000.0, float(e_far)
+    elif kind == "tiny":          # all of them near the end of binary32's range
+        e[:] = -112
     elif kind == "two heads":     # one head attends to small values, the other to large ones
         e[::2] = -40
         s[::2, 1] -= 200
@@ -294,7 +296,7 @@ def unequal(kind, n, g):
 @pytest.mark.parametrize("form,scheme", FORMS)
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("kind", ["far 0 24", "far 200 40", "far -1 80", "far 17 -80", "two heads", "fall", "records",
-                                  "random"])
+                                  "random", "tiny"])
 def test_kv_attention_scales_under_unequal_weights(qat, form, scheme, dtype, kind):
     """What fp16 parts of a weight times its value's scale lose is 2^-33 of the largest such
     product of the head: rows that it does not attend to, and other heads, cost it nothing.
@@ -334,7 +336,7 @@ def test_kv_attention_scales_under_unequal_weights(qat, form, scheme, dtype, kin
         # (the part's bits: 8 U, or 2^-22 under a bf16 output)
         rel = (8 * np.abs(x) + 8 * np.abs(x - x.max()) + 16 + 6 * moves) * U
         size = np.abs(vv) + np.abs(want) + zv
-        err = (w * rel) @ size + (8 * math.sqrt(n) + 16) * U * (w @ size) + n * 2.0 ** -126 * (1 + np.abs(vv).max(0))
+        err = (w * rel) @ size + (8 * math.sqrt(n) + 16) * U * (w @ size) + n * (2.0 ** -126 * np.abs(vv).max(0) + 2.0 ** -148)
         err = err + 2.0 ** -33 * (w * vs).max() * (codes + zp).sum(0)
         within(r.y[0, h], want, err + ref.step(dtype) * (np.abs(want) + err), "y")
         lse = x.max() + math.log(total)
