@@ -341,3 +341,82 @@ def test_kv_attention_scales_under_unequal_weights(qat, form, scheme, dtype, kin
         within(r.y[0, h], want, err + ref.step(dtype) * (np.abs(want) + err), "y")
         lse = x.max() + math.log(total)
         assert abs(float(r.lse[0, h]) - lse) <= (w * rel).sum() + (8 * math.sqrt(n) + 16) * U + 4 * U * abs(lse)
+
+
+# --- every kernel of the attention -------------------------------------------------------
+@pytest.mark.parametrize("form,scheme", [f for f in FORMS if f != ("int8", "symmetric") and f != ("int4", "symmetric")])
+@pytest.mark.parametrize("d", [16, 64, 104, 128, 232, 256])
+def test_kv_attention_every_kernel(qat, form, scheme, d):
+    """Both output types, whole and partial head sizes, groups of one to eight and of more
+    query heads, in sequences within a block and across blocks."""
+    page, lengths = 32, [5, 0, 800, 33]
+    g = torch.Generator().manual_seed(d)
+    need = [-(-n // page) for n in lengths]
+    order = torch.randperm(sum(need) + 1, generator=g).int()
+    table, at = torch.full((4, max(need)), -1, dtype=torch.int32), 0
+    cache = qat.kv_cache(sum(need) + 1, 2, page, d, form, scheme)
+    for b, n in enumerate(lengths):
+        table[b, :need[b]] = order[at:at + need[b]]
+        at += need[b]
+        if n:
+            t = torch.arange(n)
+            slots = table[b].long()[t // page] * page + t % page
+            qat.kv_write(cache, randn(b, n, 2, d, dtype=BF16), randn(9 + b, n, 2, d, dtype=BF16), slots.cuda())
+    n = torch.tensor(lengths, dtype=torch.int32).cuda()
+    for dtype in (BF16, F32):
+        for heads in (2, 6, 22):
+            q = randn(heads, 4, heads, d, dtype=dtype)
+            r = qat.kv_attention(q, cache, table.cuda(), n, want_lse=True)
+            y, ey, lse, el = ref.attention(f64(q), cache, table.numpy(), lengths, d ** -0.5, dtype)
+            within(r.y, y, ey, "y")
+            full = [0, 2, 3]
+            within(r.lse[full], lse[full], el[full], "lse")
+            assert not r.y[1].any() and (r.lse[1] == -math.inf).all()
+
+
+# --- the calls that mirror the C entry points ----------------------------------------------
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attention_calls_with_the_users_own_buffers(qat, dtype):
+    """The qat_* calls, into outputs and workspaces that the caller has, on a stream of the
+    caller's: what the named functions give; the workspace that a call needs is checked."""
+    t, hq, hk, d, page = 50, 6, 2, 64, 16
+    row = randn(0, t, (hq + 2 * hk) * d, dtype=dtype).view(t, hq + 2 * hk, d)
+    q, k, v = row[:, :hq], row[:, hq:hq + hk], row[:, hq + hk:]
+    wq, wk = ((1 + randn(1 + i, d, scale=0.3)).to(dtype) for i in range(2))
+    positions, turns = torch.arange(t).cuda(), qat.rope_turns(qat.rope_frequencies(32), "cuda")
+    gq, gk = randn(5, t, hq, d, dtype=dtype), randn(6, t, hk, d, dtype=dtype)
+    want = qat.head_norm_rope(q, k, positions, turns, wq, wk, 1e-5, True, "interleaved", 1.25)
+    grads = qat.head_norm_rope_backward(gq, gk, q, k, positions, turns, wq, wk, 1e-5, True, "interleaved", 1.25)
+    cache, same = (qat.kv_cache(-(-t // page), hk, page, d, "int8", "affine") for _ in range(2))
+    slots = torch.arange(t).cuda()
+    qat.kv_write(same, want.k, v, slots)
+    rows = qat.kv_read(same, slots, dtype)
+    table = torch.arange(cache.pages, dtype=torch.int32).view(1, -1).cuda().expand(3, -1).contiguous()
+    n = torch.tensor([t, 7, 0], dtype=torch.int32).cuda()
+    attended = qat.kv_attention(want.q[:3], same, table, n, 0.2, want_lse=True)
+    torch.cuda.synchronize()
+
+    s = torch.cuda.Stream()
+    yq, yk, dq, dk = (torch.empty(t, h, d, dtype=dtype, device="cuda") for h in (hq, hk, hq, hk))
+    dwq, dwk = (torch.empty(d, dtype=dtype, device="cuda") for _ in range(2))
+    rk, rv = torch.empty_like(yk), torch.empty_like(yk)
+    y, lse = torch.empty(3, hq, d, dtype=dtype, device="cuda"), torch.empty(3, hq, device="cuda")
+    rope = t, hq, hk, d, q.stride()[:2], k.stride()[:2], positions, turns, 32, "interleaved", 1.25, True, wq, wk, 1e-5
+    ws = torch.empty(qat.qat_head_norm_rope_backward_workspace_bytes(d), dtype=torch.uint8, device="cuda")
+    ws_attn = torch.empty(qat.qat_kv_attention_workspace_bytes(cache, hq), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    qat.qat_head_norm_rope(q, k, *rope, yq, yk, s)
+    qat.qat_head_norm_rope_backward(gq, gk, q, k, *rope, dq, dk, dwq, dwk, ws, s)
+    qat.qat_kv_write(cache, yk, v, t, yk.stride()[:2], v.stride()[:2], slots, s)
+    qat.qat_kv_read(cache, slots, t, rk, rv, s)
+    attn = yq, 3, hq, yq.stride()[:2], cache, table, table.shape[1], table.stride(0), n, 0.2, y, lse
+    qat.qat_kv_attention(*attn, ws_attn, s)
+    s.synchronize()
+    for a, b in ((yq, want.q), (yk, want.k), (dq, grads[0]), (dk, grads[1]), (dwq, grads[2]), (dwk, grads[3]),
+                 (cache.k, same.k), (cache.v_scale, same.v_scale), (rk, rows.k), (rv, rows.v), (y, attended.y),
+                 (lse, attended.lse)):
+        assert torch.equal(a, b)
+    with pytest.raises(qat.QatError):
+        qat.qat_kv_attention(*attn, ws_attn[:-16], s)
+    with pytest.raises(qat.QatError):
+        qat.qat_head_norm_rope_backward(gq, gk, q, k, *rope, dq, dk, dwq, dwk, ws[:-16], s)
