@@ -420,3 +420,50 @@ def test_attention_calls_with_the_users_own_buffers(qat, dtype):
         qat.qat_kv_attention(*attn, ws_attn[:-16], s)
     with pytest.raises(qat.QatError):
         qat.qat_head_norm_rope_backward(gq, gk, q, k, *rope, dq, dk, dwq, dwk, ws[:-16], s)
+
+
+# --- the largest calls -------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_kv_attention_longest_sequence(qat, dtype):
+    """2^31 - 1025 positions (of pages that repeat) are the most a sequence may have: one more
+    is NaN, and the sequence beside it is as alone.  A warp adds up 74 000 tiles."""
+    n, d, page = (1 << 31) - 1025, 16, 1 << 20
+    cache = qat.kv_cache(1, 1, page, d, "int8")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = torch.rand(page, 1, d, generator=g, device="cuda") * 2 - 1, torch.rand(page, 1, d, generator=g, device="cuda")
+    v[page - 1025:] += 3  # (what the last page's end leaves out would show)
+    slots = torch.arange(page, device="cuda")
+    qat.kv_write(cache, k, v, slots)
+    r = qat.kv_read(cache, slots, F32)
+    q = torch.zeros(3, 1, d, device="cuda")
+    q[..., 9] = 2.0
+    table = torch.zeros(1, 2048, dtype=torch.int32, device="cuda").expand(3, -1)
+    got = qat.kv_attention(q.to(dtype), cache, table, torch.tensor([5, n, n + 1], dtype=torch.int32, device="cuda"), 1.0,
+                           want_lse=True)
+    times = torch.full((page,), 2048.0, device="cuda", dtype=torch.float64)
+    times[n % page:] -= 1
+    s = r.k[:, 0].double() @ q[0, 0].double()
+    w = times * s.exp()
+    for b, w in ((0, s[:5].exp()), (1, w)):
+        want, lse, steps = (w @ r.v[:len(w), 0].double()) / w.sum(), float(w.sum().log()), 8 * math.sqrt(80000)
+        err = (steps + 40) * U * want.abs()
+        within(got.y[b, 0], f64(want), f64(err + ref.step(dtype) * (want.abs() + err)), "y")
+        assert abs(float(got.lse[b, 0]) - lse) <= (steps + 40) * U + 4 * U * lse
+    assert torch.isnan(got.y[2]).all() and torch.isnan(got.lse[2]).all()
+
+
+def test_kv_attention_largest_batch(qat):
+    """65535 sequences, every other one empty, and one more is refused."""
+    batch, d = 65535, 16
+    cache = qat.kv_cache(64, 2, 16, d, "bf16")
+    cache.k.copy_(randn(0, *cache.k.shape, dtype=BF16)), cache.v.copy_(randn(1, *cache.v.shape, dtype=BF16))
+    q = randn(2, 64, 4, d, dtype=BF16).repeat(1024, 1, 1)
+    table = torch.arange(64, dtype=torch.int32, device="cuda").view(64, 1).repeat(1024, 1)
+    n = (torch.arange(64, dtype=torch.int32, device="cuda") % 17).repeat(1024)
+    n[1::2] = 0
+    few = qat.kv_attention(q[:64], cache, table[:64], n[:64], want_lse=True)
+    got = qat.kv_attention(q[:batch], cache, table[:batch], n[:batch], want_lse=True)
+    want = few.y.repeat(1024, 1, 1)[:batch], few.lse.repeat(1024, 1)[:batch]
+    assert torch.equal(got.y, want[0]) and torch.equal(got.lse, want[1])
+    with pytest.raises(qat.QatError):
+        qat.kv_attention(q, cache, table, n)
