@@ -29,12 +29,12 @@
 // index stands for is free, so the codes' own order is taken for both operands.
 //
 // Twelve warps an SM (168 registers, 17 KB of ring each, two tiles and more in flight)
-// walk through tiles at 0.7 to 1 us each.  Measured (both launches, in a graph): 64
-// sequences of up to 8192 positions, 32 heads over 8 of 128 in affine 4-bit codes, 63 us
-// (3.1 TB/s; about 400 instructions a tile, 51% of the issue slots); two of 131072 in
-// E4M3 100 us (5.5 TB/s, 82% of the copy bandwidth); 32 of up to 2048, 16 heads of 64 in
-// bf16, 22 us; one of 700 in int8 10.6 us, of which 8 are the latencies of lengths, table,
-// codes and the two joins.
+// walk through tiles at 0.8 to 1.1 us each.  Measured (both launches, in a graph): 64
+// sequences of up to 8192 positions, 32 heads over 8 of 128 in affine 4-bit codes, 68 us
+// (2.9 TB/s; 486 instructions a tile with the pieces' starts and ends, 53% of the issue
+// slots); two of 131072 in E4M3 103 us (5.4 TB/s, 79% of the copy bandwidth); 32 of up to
+// 2048, 16 heads of 64 in bf16, 23 us; one of 700 in int8 10.9 us, of which 8 are the
+// latencies of lengths, table, codes and the two joins.
 #include <atomic>
 #include <cmath>
 
@@ -48,10 +48,11 @@ namespace {
 constexpr int kFormat = QAT_KV_FORMAT;
 constexpr float kLog2e = 1.4426950408889634f;
 // What a piece costs beside its tiles, in tiles (64 sequences of up to 8192 positions
-// in 4-bit codes, with one part a weight: 74 us with 2, 60 with 4, 57 with 8, 58 with 14).
+// in 4-bit codes: 68.5 us with 4, 68.1 with 6, 67.7 with 8, 67.3 with 11, 68.5 with 14; two
+// of 131072 in E4M3 100.5 to 102.5, the fewest with 11).
 constexpr int kPieceTiles = 8;
-// Tiles of a run at least (one sequence of 700 positions: 10.5 us with 1 or 2, 11.3 with
-// 4, 12.6 with 8; a run's first tiles may be a piece's cost).
+// Tiles of a run at least (one sequence of 700 positions: 10.9 us with 1 or 2, 11.7 with
+// 4; a run's first tiles may be a piece's cost).
 constexpr int kLeastRun = 2;
 constexpr float kSlack = 4.0f;  // scores may exceed the running maximum by 2^4 before it moves
 
@@ -256,18 +257,18 @@ struct Shape {
   static constexpr int HALF_STAGE = (TILE + PARAMS) / 2;
   static constexpr int STAGES = smaller(6, larger(2, 13 * 1024 / (TILE + PARAMS)));
   static constexpr int H = 8 * HT, KS = DP / 16, MT = DP / 16;
-  // 16-bit parts of q and of the weights: two of fp16 hold 22 bits of a weight (one: 58 us in
-  // place of 63 for the 4-bit batch, but a sequence's elements off by up to 2^-12 all alike),
-  // three of bf16 all 24.
+  // 16-bit parts of q and of the weights: two of fp16 hold 22 bits of a weight (one took five
+  // us less for the 4-bit batch, but left a sequence's elements off by up to 2^-12 all alike),
+  // three of bf16 all 24 (two: no less time, 16 bits).
   static constexpr int QP = kF32 ? 3 : 1, PP = kF32 || F == QAT_CACHE_BF16 ? 3 : 2;
   static constexpr int QFRAG = kF32 ? QP * KS * 32 * 8 : 0;
   // A warp's ring and queries, then the part it starts with (its run began inside a
   // sequence); the part it ends with takes the ring's place.
   static constexpr int PART = H * DP * 4;
   static constexpr int RING = larger(2 * STAGES * HALF_STAGE + QFRAG, PART), WARP = RING + PART;
-  // Registers hold twelve warps of up to 168, eight of up to 255 (with one part a weight
-  // thirteen spill: 71 us against 58 for the 4-bit batch; fourteen for short heads, 23.3
-  // against 22.2).
+  // Registers hold twelve warps of up to 168, eight of up to 255 (64 sequences in 4-bit codes:
+  // 70.6 us with eleven, 67.7 with twelve, 82.7 with thirteen, which spill; 32 sequences of
+  // short heads in bf16: 21.5, 22.8, 24.5).
   static constexpr int WARPS =
       smaller(224 * 1024 / WARP, DP * HT <= 128 && !kF32 ? 12 : 8);
   static constexpr int THREADS = 32 * WARPS, SMEM = WARPS * WARP;
@@ -752,7 +753,8 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
               }
               zsum[ht][i] *= both;
 #pragma unroll
-              for (int j = 0; j < S::MT; ++j) scale_in_place(o[ht][j][i], both), scale_in_place(o[ht][j][2 + i], both);
+              for (int j = 0; j < S::MT; ++j)
+                scale_in_place(o[ht][j][i], both), scale_in_place(o[ht][j][2 + i], both);
             }
           weights();
         }
@@ -768,8 +770,9 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
           for (int k = 0; k < S::PP; ++k)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              wb[ht][k][r] = transpose8(k + 1 < S::PP ? take_pair<HALF, false, false>(w[ht][2 * r], w[ht][2 * r + 1])
-                                                      : take_pair<HALF, true, false>(w[ht][2 * r], w[ht][2 * r + 1]));
+              wb[ht][k][r] =
+                  transpose8(k + 1 < S::PP ? take_pair<HALF, false, false>(w[ht][2 * r], w[ht][2 * r + 1])
+                                           : take_pair<HALF, true, false>(w[ht][2 * r], w[ht][2 * r + 1]));
         }
       };
       // Weighted values: rows are head elements, k the positions.
@@ -800,7 +803,8 @@ __global__ void __launch_bounds__(Shape<T, F, DP, HT>::THREADS, 1)
 #pragma unroll
               for (int ht = 0; ht < HT; ++ht) {
                 // 16 positions only: the tensor cores cut their sums off toward zero, a loss that
-                // grows with the run (2^-7 of the result after 2^20 positions)
+                // grows with the run (2^-7 of the result after 2^20 positions; the additions take
+                // 3 us of the 4-bit batch's 68)
                 float part[4];
                 mma<HALF, true>(part, fa, wb[ht][S::PP - 1][0], wb[ht][S::PP - 1][1]);
 #pragma unroll

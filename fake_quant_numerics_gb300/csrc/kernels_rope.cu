@@ -248,7 +248,8 @@ constexpr int kRopeThreads = 256;
 // Blocks (x: tokens, y: runs of `per` heads, the queries' first), a group a token.
 // All lanes of a warp take the same number of steps (shuffles).
 template <typename T, int V, int NP, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, V == 8 && T::BYTES == 2 ? 3 : 2) k_rope_fwd(RopeArgs r, int lanes, int per, int runs0) {
+__global__ void __launch_bounds__(kRopeThreads, V == 8 && T::BYTES == 2 ? 3 : 2)
+    k_rope_fwd(RopeArgs r, int lanes, int per, int runs0) {
   using P = Pairs<T, V, INTER>;
   const int lane = threadIdx.x & (lanes - 1);
   const int64_t token = (int64_t)blockIdx.x * (kRopeThreads / lanes) + threadIdx.x / lanes;

@@ -34,7 +34,8 @@ qat_status check_rope(const RopeSizes& z, qat_dtype dtype, int layout, float amp
   if (z.head_dim < 1 || z.head_dim > 512 || z.rotary_dim < 0 || z.rotary_dim > z.head_dim ||
       z.rotary_dim % 2)
     return QAT_ERR_INVALID_ARGUMENT;
-  if (z.q_heads < 0 || z.k_heads < 0 || z.q_heads > 32767 || z.k_heads > 32767 || !fits(z.tokens, (z.q_heads + z.k_heads) * z.head_dim))
+  if (z.q_heads < 0 || z.k_heads < 0 || z.q_heads > 32767 || z.k_heads > 32767 ||
+      !fits(z.tokens, (z.q_heads + z.k_heads) * z.head_dim))
     return QAT_ERR_INVALID_ARGUMENT;
   if (!stride_ok(z.q_ts, z.tokens) || !stride_ok(z.k_ts, z.tokens) ||
       !stride_ok(z.q_hs, z.q_heads) || !stride_ok(z.k_hs, z.k_heads))

@@ -591,7 +591,8 @@ qat_status qat_layer_norm_backward(const void* dy, const void* x, qat_dtype dtyp
  *   q_weight, k_weight (nullable: 1): dtype[head_dim]; NULL without norm.
  *   positions: int64[tokens] (any, negative ones too); turns: uint64[rotary_dim / 2].
  * head_dim 1 .. 512; rotary_dim even, 0 .. head_dim; q_heads and k_heads up to
- * 32767; eps finite and >= 0; amplitude finite.  One launch.
+ * 32767; eps finite and >= 0 (with 0 a head of zeros has no norm: NaN); amplitude
+ * finite.  Squares are summed in binary32, whose range sum x^2 has to keep.  One launch.
  */
 typedef enum { QAT_ROPE_HALF = 0, QAT_ROPE_INTERLEAVED = 1 } qat_rope_layout;
 
