@@ -467,3 +467,46 @@ def test_kv_attention_largest_batch(qat):
     assert torch.equal(got.y, want[0]) and torch.equal(got.lse, want[1])
     with pytest.raises(qat.QatError):
         qat.kv_attention(q, cache, table, n)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attention_operators_of_most_heads(qat, dtype):
+    """32767 heads are each as one of a few; so are 100000 query heads of one cache head."""
+    heads, few, d, t = 32767, 31, 8, 3
+    q, k, v = (randn(i, t, few, d, dtype=dtype).repeat(1, 1057, 1) for i in range(3))
+    assert q.shape[1] == heads
+    positions, turns = torch.arange(5, 5 + t).cuda(), qat.rope_turns(qat.rope_frequencies(4), "cuda")
+    w = torch.ones(d, dtype=dtype, device="cuda")
+    r = qat.head_norm_rope(q, k, positions, turns, w, w)
+    dq, dk, _, dw = qat.head_norm_rope_backward(v, v, q, k, positions, turns, w, w)
+    cache, small = (qat.kv_cache(1, h, 16, d, "int8", "affine") for h in (heads, few))
+    slots = torch.arange(t).cuda()
+    qat.kv_write(cache, k, v, slots)
+    rows = qat.kv_read(cache, slots, dtype)
+    table, n = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.tensor([t], dtype=torch.int32, device="cuda")
+    y = qat.kv_attention(q[:1], cache, table, n).y
+    q1, k1, v1 = (x[:, :few].contiguous() for x in (q, k, v))
+    r1 = qat.head_norm_rope(q1, k1, positions, turns, w, w)
+    g1 = qat.head_norm_rope_backward(v1, v1, q1, k1, positions, turns, w, w)
+    qat.kv_write(small, k1, v1, slots)
+    rows1 = qat.kv_read(small, slots, dtype)
+    y1 = qat.kv_attention(q1[:1], small, table, n).y
+    for got, want in ((r.q, r1.q), (r.k, r1.k), (dq, g1[0]), (dk, g1[1]), (rows.k, rows1.k), (rows.v, rows1.v), (y, y1)):
+        assert torch.equal(got, want.repeat(1, 1057, 1))
+    # the gradient of the keys' weight: 1057 times the few heads' sum, of products of up to 6 in size
+    c, s = ref.angles(positions.tolist(), turns.tolist(), 1.0)
+    one = ref.rope(f64(k1), np.ones(d), f64(v1), c, s, "half", 1e-6, True, 1.0, F32)["dw"]
+    size = np.abs(one[0]) * 1057
+    err = (8 * math.sqrt(heads * t) + 40) * U * 1057 * few * t * 6 + 1057 * one[1]
+    within(dw, one[0] * 1057, err + ref.step(dtype) * (size + err), "dw")
+    # one cache head
+    lone = qat.kv_cache(4, 1, 16, 64, "int8")
+    slots = torch.arange(50).cuda()
+    qat.kv_write(lone, randn(4, 50, 1, 64, dtype=dtype), randn(5, 50, 1, 64, dtype=dtype), slots)
+    q = randn(6, 1, 10, 64, dtype=dtype)
+    table, n = torch.arange(4, dtype=torch.int32).view(1, 4).cuda(), torch.tensor([50], dtype=torch.int32, device="cuda")
+    got = qat.kv_attention(q.repeat(1, 10000, 1), lone, table, n).y.view(10000, 10, 64)
+    y, ey, _, _ = ref.attention(f64(q), lone, table.cpu().numpy(), [50], 0.125, dtype)
+    for i in (0, 1, 4999, 9999):
+        within(got[i], y[0], ey[0], "y")
+    assert (got - got[:1]).abs().max() <= 2 * float(ey.max())
