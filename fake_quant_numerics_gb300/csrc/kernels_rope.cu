@@ -78,7 +78,8 @@ struct Run {
 };
 
 // Cosine and sine of a 2^-64 fraction of a turn: the quarter by its two top bits, the
-// rest (|x| <= pi / 4) by the Taylor series, whose next terms are below 2^-25.
+// rest (|x| <= pi / 4) by the Taylor series, whose next terms are below 2^-25: within 6 U of m,
+// U = 2^-24, with the roundings of the angle and of the steps.
 __device__ __forceinline__ void turn_cos_sin(uint64_t t, float m, float& c, float& s) {
   const uint32_t top = (uint32_t)(t >> 32) + 0x20000000u;  // (an eighth of a turn on)
   const int n = (int)(top >> 30);

@@ -510,3 +510,25 @@ def test_attention_operators_of_most_heads(qat, dtype):
     for i in (0, 1, 4999, 9999):
         within(got[i], y[0], ey[0], "y")
     assert (got - got[:1]).abs().max() <= 2 * float(ey.max())
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_head_norm_rope_cosines_and_sines(qat, layout):
+    """The pair (1, 0) turns to (cos, sin).  The reduced angle x, at most pi / 4, is off by 3 U
+    of itself (its integer, the constant and their product) and by 2^-32 of a turn: 1.7 U of
+    either.  The cosine's series leaves out less than 0.5 U, and rounds in its last step (U),
+    the one before (0.6 U) and the square (0.3 U); the sine's rounds by less; the amplitude's
+    product by U: 5.1 U, and 6 U is the bound that the rotation's tests take."""
+    t, d = 4001, 64
+    g = torch.Generator().manual_seed(5)
+    positions = torch.cat([torch.arange(2000), torch.randint(-(1 << 62), 1 << 62, (2001,), generator=g)]).cuda()
+    turns = qat.rope_turns(qat.rope_frequencies(d), "cuda")
+    q = torch.zeros(t, 1, d, device="cuda")
+    i = torch.arange(d // 2)
+    a, b = (i, i + d // 2) if layout == "half" else (2 * i, 2 * i + 1)
+    q[..., a] = 1.0
+    for amplitude in (1.0, 0.75):
+        y = qat.head_norm_rope(q, None, positions, turns, norm=False, layout=layout, amplitude=amplitude).q[:, 0]
+        c, s = ref.angles(positions.tolist(), turns.tolist(), amplitude)
+        within(y[:, a], c, 6 * U * amplitude + np.zeros_like(c), "cos")
+        within(y[:, b], s, 6 * U * amplitude + np.zeros_like(s), "sin")
